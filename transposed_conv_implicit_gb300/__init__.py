@@ -19,6 +19,8 @@ from . import _lib
 from ._lib import (CONV_ERR_CUDA, CONV_ERR_DEVICE_TIMEOUT, CONV_ERR_INVALID_VALUE,
                    CONV_ERR_MISALIGNED, CONV_ERR_NOT_SUPPORTED, CONV_ERR_WORKSPACE_TOO_SMALL,
                    CONV_OK, CONV_STATUS_BYTES, ExtensionMissing)
+from .attention import (cross_attention_bwd, cross_attention_fwd, cross_attention_workspace_size,
+                        qk_norm_rope_bwd, qk_norm_rope_fwd, qk_norm_rope_workspace_size)
 
 __all__ = [
     "conv2d_fwd", "conv2d_fwd_packed", "conv2d_pack_filter", "conv2d_packed_filter_bytes",
@@ -27,6 +29,8 @@ __all__ = [
     "conv_transposed_pack_filter", "conv_transposed_packed_filter_bytes",
     "conv_transposed_workspace_size", "conv_check_device_status", "conv_status_string",
     "ConvError", "ExtensionMissing", "new_workspace", "dtype_name", "library_path",
+    "cross_attention_fwd", "cross_attention_bwd", "cross_attention_workspace_size",
+    "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_workspace_size",
 ]
 
 

@@ -41,6 +41,8 @@ EXPORTS = (
     "conv_testing_cache_stats", "conv_streamk_workspace_size",
     "conv_transposed_packed_filter_bytes_dilated", "conv_transposed_workspace_size_dilated",
     "conv_transposed_pack_filter_dilated",
+    "cross_attention_workspace_size", "cross_attention_fwd", "cross_attention_bwd",
+    "qk_norm_rope_fwd", "qk_norm_rope_workspace_size", "qk_norm_rope_bwd",
 )
 
 
@@ -98,6 +100,20 @@ def _declare(lib):
     lib.conv_testing_reload_tuning.restype = None
     lib.conv_testing_cache_stats.argtypes = [ctypes.POINTER(U64), ctypes.POINTER(U64)]
     lib.conv_testing_cache_stats.restype = None
+    # The attention entry points take their argument structs as packed bytes.
+    B = ctypes.c_char_p
+    lib.cross_attention_workspace_size.argtypes = [B, I]
+    lib.cross_attention_workspace_size.restype = Z
+    lib.cross_attention_fwd.argtypes = [B, P, Z, P]
+    lib.cross_attention_fwd.restype = I
+    lib.cross_attention_bwd.argtypes = [B, P, Z, P]
+    lib.cross_attention_bwd.restype = I
+    lib.qk_norm_rope_fwd.argtypes = [B, P]
+    lib.qk_norm_rope_fwd.restype = I
+    lib.qk_norm_rope_workspace_size.argtypes = [I]
+    lib.qk_norm_rope_workspace_size.restype = Z
+    lib.qk_norm_rope_bwd.argtypes = [B, P, Z, P]
+    lib.qk_norm_rope_bwd.restype = I
     return lib
 
 

@@ -2060,6 +2060,25 @@ void* noalloc_scratch_ptr(conv_status_t* st) {
 
 }  // namespace
 
+// What the attention entry points share with the convolutions' (attn_internal.h).
+namespace convgb300 {
+
+PFN_cuTensorMapEncodeTiled_v12000 tiled_map_encoder() {
+  const DriverFns* fns = driver_fns();
+  return fns ? fns->tiled : nullptr;
+}
+
+int attn_sm_count() { return device_sm_count(); }
+
+long long wait_limit_cycles() {
+  const unsigned long long tmo = g_timeout_ns.load(std::memory_order_relaxed);
+  return ns_to_cycles(tmo ? tmo : kDefaultTimeoutNs);
+}
+
+int wait_fault_mode() { return g_fault_mode.load(std::memory_order_relaxed); }
+
+}  // namespace convgb300
+
 // =================================================================== C ABI
 extern "C" {
 
