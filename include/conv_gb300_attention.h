@@ -86,8 +86,9 @@ typedef struct {
 
 /* Workspace bytes of a call on the current device (the status region
  * included): packed mask bits, partial results of work split along the keys
- * (forward) or the queries (backward), row sums (backward).  Of `args` only
- * the sizes, the dtype, whether mask is NULL and its strides are read. */
+ * (forward) or the queries (backward), row sums (backward).  With `backward`
+ * they serve both passes.  Of `args` only the sizes, the dtype, whether mask
+ * is NULL and its strides are read. */
 size_t cross_attention_workspace_size(const cross_attention_args_t* args, int backward);
 
 conv_status_t cross_attention_fwd(const cross_attention_args_t* args, void* workspace,

@@ -110,6 +110,24 @@ def test_forward_and_gradients(size, kind, dtype):
     _check(dtype, *size, kind, seed=sum(size))
 
 
+LONG = [  # many tiles for each thread block, cut in the middle of rows
+    (2, 1021, 523, 12, 4, 80, "none", "bf16"),
+    (2, 1021, 523, 12, 4, 80, "rows", "f16"),
+    (2, 1021, 523, 12, 12, 80, "keys", "bf16"),
+    (5, 700, 900, 8, 4, 128, "lengths", "bf16"),
+    (2, 1024, 512, 12, 12, 128, "heads", "f16"),
+    (1, 2048, 2000, 16, 16, 128, "none", "bf16"),
+    (2, 3000, 1100, 8, 2, 40, "rows", "f16"),
+    (16, 1024, 77, 8, 8, 40, "lengths", "bf16"),
+    (1, 100, 9000, 4, 4, 64, "lengths", "bf16"),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "x".join(map(str, c)))
+def test_long(case):
+    _check(case[7], *case[:7], seed=3)
+
+
 TOKENS = [  # b, lq, lk, h, hkv, d: few queries over many keys
     (1, 1, 5000, 8, 8, 64),
     (3, 1, 4097, 32, 8, 128),

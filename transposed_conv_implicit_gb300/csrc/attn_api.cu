@@ -15,9 +15,6 @@
 namespace convgb300 {
 
 
-cudaError_t launch_attn_simple_fwd(const AttnShape& a, cudaStream_t stream);
-cudaError_t launch_attn_simple_bwd(const AttnShape& a, cudaStream_t stream);
-
 namespace {
 
 constexpr int kMaxHeadDim = 128;
@@ -45,8 +42,6 @@ conv_status_t check_sizes(const cross_attention_args_t& a) {
       a.head_dim <= 0 || a.heads % a.kv_heads != 0)
     return CONV_ERR_INVALID_VALUE;
   if (a.head_dim % 8 != 0 || a.head_dim > kMaxHeadDim) return CONV_ERR_NOT_SUPPORTED;
-  // Heads and batches share a launch's grid.
-  if (static_cast<long long>(a.batch) * a.heads > 65535) return CONV_ERR_NOT_SUPPORTED;
   return CONV_OK;
 }
 
@@ -69,17 +64,261 @@ MaskShape mask_shape(const cross_attention_args_t& a) {
 
 size_t round_up(size_t v, size_t to) { return (v + to - 1) / to * to; }
 
-struct Layout {
-  MaskShape mask;
-  size_t mask_at, total;
+// ------------------------------------------------------------------ forward plan
+// How the rows of one key head are cut into row tiles, and which schedule
+// runs them (attn_fwd.cu).
+struct FwdPlan {
+  int tile_heads, tile_tokens, token_tiles, row_tiles;
+  int kv_box;
+  bool split;
+  int grid;
+  long long items;       // pairs: launch items
+  size_t part_bytes;     // split: partial rows and their statistics
 };
 
-Layout layout(const cross_attention_args_t& a) {
+FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
+  FwdPlan f{};
+  const int group = a.heads / a.kv_heads;
+  const int token_tiles = (a.q_len + kAttnRows - 1) / kAttnRows;
+  f.token_tiles = std::max(1, token_tiles);
+  f.tile_heads = 1;
+  f.tile_tokens = std::min(kAttnRows, std::max(1, a.q_len));
+  long long row_tiles = static_cast<long long>(group) * f.token_tiles;
+  // The query heads of a key head side by side, where that makes fewer tiles.
+  if (may_pack && group > 1 && group <= kAttnRows) {
+    const int tokens = kAttnRows / group;
+    const int packed = (a.q_len + tokens - 1) / tokens;
+    if (packed < row_tiles) {
+      f.tile_heads = group;
+      f.tile_tokens = std::min(tokens, std::max(1, a.q_len));
+      row_tiles = std::max(1, packed);
+    }
+  }
+  f.row_tiles = static_cast<int>(row_tiles);
+  f.kv_box = std::min(kAttnRows, std::max(16, (a.kv_len + 15) / 16 * 16));
+  const long long nt = std::max(1, (a.kv_len + f.kv_box - 1) / f.kv_box);
+  const long long heads = static_cast<long long>(a.batch) * a.kv_heads;
+  f.items = heads * ((row_tiles + 1) / 2);
+  // Pairs take whole rounds of items; split shares steps out evenly.  A
+  // pair's step covers two row tiles on a whole SM.
+  const long long rounds = (f.items + sms - 1) / sms;
+  const double pairs_cost = static_cast<double>(rounds) * nt;
+  const double split_cost = static_cast<double>(heads) * row_tiles * nt / (2.0 * sms) * 1.25;
+  f.split = split_cost < pairs_cost;
+  const long long steps = heads * row_tiles * nt;
+  f.grid = static_cast<int>(f.split ? std::min<long long>(steps, 2ll * sms)
+                                    : std::min<long long>(f.items, sms));
+  if (f.split && nt > 1)
+    f.part_bytes = static_cast<size_t>(2) * f.grid * kAttnRows * (128 + 2) * sizeof(float);
+  return f;
+}
+
+// ------------------------------------------------------------------ backward plan
+struct BwdPlan {
+  int q_tiles, item_steps, kv_tiles;
+  int q_grid, kv_grid;     // CTAs of the dq and the dk, dv kernel
+  bool norms;              // fp16: ds is scaled by the rows' norms
+  size_t stat_bytes, norm_bytes, part_q_bytes, part_kv_bytes;
+};
+
+BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
+  BwdPlan p{};
+  p.q_tiles = (a.q_len + kAttnRows - 1) / kAttnRows;
+  p.item_steps = a.heads / a.kv_heads * p.q_tiles;
+  p.kv_tiles = (a.kv_len + kAttnRows - 1) / kAttnRows;
+  const long long heads = static_cast<long long>(a.batch) * a.kv_heads;
+  const long long nt = std::max(1, (a.kv_len + f.kv_box - 1) / f.kv_box);
+  p.q_grid = static_cast<int>(std::min<long long>(heads * f.row_tiles * nt, sms));
+  p.kv_grid = static_cast<int>(std::min<long long>(heads * p.kv_tiles * p.item_steps, sms));
+  p.norms = a.dtype == CONV_DTYPE_F16;
+  p.stat_bytes = static_cast<size_t>(a.batch) * a.heads * p.q_tiles * 256 * sizeof(float);
+  p.norm_bytes = 2 * kAttnNormBlocks * sizeof(float);  // (of one size for both types)
+  const size_t tile = static_cast<size_t>(kAttnRows) * 128 * sizeof(float);
+  p.part_q_bytes = nt > 1 ? 2 * tile * p.q_grid : 0;
+  p.part_kv_bytes = p.item_steps > 1 ? 4 * tile * p.kv_grid : 0;
+  return p;
+}
+
+struct Layout {
+  MaskShape mask;
+  size_t mask_at, part_at, stat_at, norm_at, part_q_at, part_kv_at, total;
+};
+
+Layout layout(const cross_attention_args_t& a, bool backward, const FwdPlan& f, const BwdPlan& g) {
   Layout l{};
   l.mask = mask_shape(a);
   l.mask_at = CONV_STATUS_BYTES;
-  l.total = round_up(l.mask_at + l.mask.bytes, 256);
+  l.part_at = round_up(l.mask_at + l.mask.bytes, 256);
+  if (!backward) {
+    l.total = round_up(l.part_at + f.part_bytes, 256);
+    return l;
+  }
+  l.stat_at = l.part_at;
+  l.norm_at = round_up(l.stat_at + g.stat_bytes, 256);
+  l.part_q_at = round_up(l.norm_at + g.norm_bytes, 256);
+  l.part_kv_at = round_up(l.part_q_at + g.part_q_bytes, 256);
+  l.total = round_up(l.part_kv_at + g.part_kv_bytes, 256);
   return l;
+}
+
+// {D, heads, tokens, batch} of a tensor with strides s (0: one entry, or a
+// broadcast), rows of 64 elements, 128-byte swizzle.
+conv_status_t encode_map(CUtensorMap* map, const void* base, const AttnShape& a, int heads,
+                         int tokens, const long long s[3], int box_heads, int box_tokens) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tiled_map_encoder();
+  if (!encode) return CONV_ERR_CUDA;
+  const long long any = 16 * ((a.head_dim + 7) / 8);  // stride of a single entry: unused
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.head_dim),
+                        static_cast<cuuint64_t>(s[2] ? heads : 1),
+                        static_cast<cuuint64_t>(s[1] ? tokens : 1),
+                        static_cast<cuuint64_t>(s[0] ? a.batch : 1)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(s[2] ? 2 * s[2] : any),
+                           static_cast<cuuint64_t>(s[1] ? 2 * s[1] : any),
+                           static_cast<cuuint64_t>(s[0] ? 2 * s[0] : any)};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens),
+                       1};
+  cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = encode(
+      map,
+      a.dtype == CONV_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      4, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CONV_OK : CONV_ERR_CUDA;
+}
+
+conv_status_t run_fwd(const AttnShape& s, const FwdPlan& f, char* ws, const Layout& l,
+                      cudaStream_t stream) {
+  AttnFwdParams p{};
+  p.a = s;
+  p.tile_heads = f.tile_heads;
+  p.tile_tokens = f.tile_tokens;
+  p.token_tiles = f.token_tiles;
+  p.row_tiles = f.row_tiles;
+  p.kv_box = f.kv_box;
+  p.items = f.items;
+  p.item_rows = static_cast<long long>(s.kv_heads) * f.row_tiles;
+  p.scale_log2 = s.scale * 1.44269504088896341f;
+  conv_status_t st = encode_map(&p.map_q, s.q, s, s.heads, s.q_len, s.qs, f.tile_heads, f.tile_tokens);
+  if (st == CONV_OK) st = encode_map(&p.map_k, s.k, s, s.kv_heads, s.kv_len, s.ks, 1, f.kv_box);
+  if (st == CONV_OK) st = encode_map(&p.map_v, s.v, s, s.kv_heads, s.kv_len, s.vs, 1, f.kv_box);
+  if (st == CONV_OK)
+    st = encode_map(&p.map_out, s.out_w, s, s.heads, s.q_len, s.os, f.tile_heads, f.tile_tokens);
+  if (st != CONV_OK) return st;
+  p.q_mul[0] = s.qs[2] != 0;
+  p.q_mul[1] = s.qs[0] != 0;
+  p.k_mul[0] = s.ks[2] != 0;
+  p.k_mul[1] = s.ks[0] != 0;
+  p.v_mul[0] = s.vs[2] != 0;
+  p.v_mul[1] = s.vs[0] != 0;
+  // Shared memory: queries, the key/value ring, output staging, barriers.
+  const bool wide = s.head_dim > 64;
+  const uint32_t q_tile = wide ? 32768 : 16384, kv_tile = f.kv_box * (wide ? 256 : 128);
+  const uint32_t ring = f.split ? (wide ? 65536 : 81920) : (wide ? 131072 : 98304);
+  const int groups = f.split ? 1 : 2;
+  p.q_stages = f.split || wide ? 1 : 2;
+  p.stages = std::min<uint32_t>(8, ring / kv_tile);
+  p.off_q = 0;
+  p.off_kv = p.off_q + groups * p.q_stages * q_tile;
+  p.off_out = p.off_kv + p.stages * kv_tile;
+  p.off_bar = p.off_out + groups * 16384;
+  const size_t smem = p.off_bar + attn_fwd_bar_bytes();
+  if (f.split) {
+    p.part_out = reinterpret_cast<float*>(ws + l.part_at);
+    p.part_stat = p.part_out + static_cast<size_t>(2) * f.grid * kAttnRows * 128;
+  }
+  p.status = reinterpret_cast<unsigned int*>(ws);
+  p.timeout_cycles = wait_limit_cycles();
+  p.fault_mode = wait_fault_mode();
+  return launch_attn_fwd(p, f.split, f.grid, smem, stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+}
+
+conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, char* ws,
+                      const Layout& l, cudaStream_t stream) {
+  AttnBwdParams p{};
+  p.a = s;
+  p.tile_heads = f.tile_heads;
+  p.tile_tokens = f.tile_tokens;
+  p.token_tiles = f.token_tiles;
+  p.row_tiles = f.row_tiles;
+  p.kv_box = f.kv_box;
+  p.q_tiles = g.q_tiles;
+  p.q_box = std::min(kAttnRows, std::max(16, (s.q_len + 15) / 16 * 16));
+  p.item_steps = g.item_steps;
+  p.item_rows = static_cast<long long>(s.kv_heads) * f.row_tiles;
+  p.scale_log2 = s.scale * 1.44269504088896341f;
+  p.p_shift = g.norms ? 15.f : 0.f;
+  p.p_unscale = g.norms ? 1.f / 32768.f : 1.f;
+  p.stats = reinterpret_cast<float*>(ws + l.stat_at);
+  p.norms = g.norms ? reinterpret_cast<float*>(ws + l.norm_at) : nullptr;
+  p.part_q = reinterpret_cast<float*>(ws + l.part_q_at);
+  p.part_kv = reinterpret_cast<float*>(ws + l.part_kv_at);
+  p.status = reinterpret_cast<unsigned int*>(ws);
+  p.timeout_cycles = wait_limit_cycles();
+  p.fault_mode = wait_fault_mode();
+  const bool queries = s.q_len > 0, keys = s.kv_len > 0;
+  const bool wide = s.head_dim > 64;
+  const uint32_t block = wide ? 32768 : 16384;  // 128 rows
+  if (queries && keys) {
+    // Row statistics.
+    const long long rows = static_cast<long long>(s.batch) * s.heads * g.q_tiles * kAttnRows;
+    p.row_blocks = static_cast<int>(std::min<long long>(kAttnNormBlocks, (rows + 63) / 64));
+    const long long values = static_cast<long long>(s.batch) * s.kv_heads * s.kv_len;
+    p.value_blocks =
+        g.norms ? static_cast<int>(std::min<long long>(kAttnNormBlocks, (values + 63) / 64)) : 0;
+    if (launch_attn_rows(p, stream) != cudaSuccess) return CONV_ERR_CUDA;
+    // dq.
+    conv_status_t st =
+        encode_map(&p.map_q, s.q, s, s.heads, s.q_len, s.qs, f.tile_heads, f.tile_tokens);
+    if (st == CONV_OK)
+      st = encode_map(&p.map_do, s.dout, s, s.heads, s.q_len, s.dos, f.tile_heads, f.tile_tokens);
+    if (st == CONV_OK) st = encode_map(&p.map_k, s.k, s, s.kv_heads, s.kv_len, s.ks, 1, f.kv_box);
+    if (st == CONV_OK) st = encode_map(&p.map_v, s.v, s, s.kv_heads, s.kv_len, s.vs, 1, f.kv_box);
+    if (st != CONV_OK) return st;
+    p.q_mul[0] = s.qs[2] != 0;
+    p.q_mul[1] = s.qs[0] != 0;
+    p.do_mul[0] = s.dos[2] != 0;
+    p.do_mul[1] = s.dos[0] != 0;
+    p.k_mul[0] = s.ks[2] != 0;
+    p.k_mul[1] = s.ks[0] != 0;
+    p.v_mul[0] = s.vs[2] != 0;
+    p.v_mul[1] = s.vs[0] != 0;
+    const uint32_t kv_tile = f.kv_box * (wide ? 256 : 128);
+    p.x_stages = wide ? 3 : 4;
+    p.y_stages = wide ? 2 : 4;
+    p.off_a = 0;
+    p.off_x = 2 * block;
+    p.off_y = p.off_x + p.x_stages * kv_tile;
+    p.off_bar = p.off_y + p.y_stages * kv_tile;
+    if (launch_attn_dq(p, g.q_grid, p.off_bar + attn_bwd_bar_bytes(), stream) != cudaSuccess)
+      return CONV_ERR_CUDA;
+    // dk, dv: the queries in tiles of 128 tokens of one head.
+    st = encode_map(&p.map_q, s.q, s, s.heads, s.q_len, s.qs, 1, p.q_box);
+    if (st == CONV_OK) st = encode_map(&p.map_do, s.dout, s, s.heads, s.q_len, s.dos, 1, p.q_box);
+    if (st != CONV_OK) return st;
+    p.x_stages = wide && s.mask_bits ? 2 : 3;
+    p.y_stages = 2;
+    p.off_y = p.off_x + p.x_stages * block;
+    p.off_stat = p.off_y + p.y_stages * block;
+    p.off_mask = p.off_stat + 2048;
+    p.off_bar = p.off_mask + (s.mask_bits ? 4096 : 0);
+    if (launch_attn_dkv(p, g.kv_grid, p.off_bar + attn_bwd_bar_bytes(), stream) != cudaSuccess)
+      return CONV_ERR_CUDA;
+  } else if (queries) {
+    AttnShape z = s;  // no keys: dq is zero
+    z.out_w = s.dq;
+    z.lse = nullptr;
+    for (int i = 0; i < 3; ++i) z.os[i] = s.dqs[i];
+    return launch_attn_no_keys(z, stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+  }
+  // Tiles that were cut between CTAs, and keys without queries.
+  const long long heads = static_cast<long long>(s.batch) * s.kv_heads;
+  const long long q_blocks = queries && s.kv_len > f.kv_box ? heads * f.row_tiles : 0;
+  const bool kv_join = g.item_steps != 1 || s.kv_lengths;
+  const long long kv_blocks = kv_join ? heads * g.kv_tiles : 0;
+  return launch_attn_bwd_join(p, g.q_grid, g.kv_grid, q_blocks, kv_blocks, stream) == cudaSuccess
+             ? CONV_OK
+             : CONV_ERR_CUDA;
 }
 
 conv_status_t check_args(const cross_attention_args_t& a, bool backward, AttnShape* s) {
@@ -146,7 +385,13 @@ conv_status_t run(const cross_attention_args_t* args, bool backward, void* works
   if (st != CONV_OK) return st;
   if (!workspace) return CONV_ERR_INVALID_VALUE;
   if (off16(workspace)) return CONV_ERR_MISALIGNED;
-  const Layout l = layout(a);
+  const int sms = attn_sm_count();
+  if (sms <= 0) return CONV_ERR_CUDA;
+  // (Tensors broadcast over heads have no head axis to load side by side.)
+  const bool may_pack = s.qs[2] != 0 && (!backward || s.dos[2] != 0);
+  const FwdPlan f = plan_fwd(a, sms, may_pack);
+  const BwdPlan g = backward ? plan_bwd(a, f, sms) : BwdPlan{};
+  const Layout l = layout(a, backward, f, g);
   if (workspace_bytes < l.total) return CONV_ERR_WORKSPACE_TOO_SMALL;
   if (a.batch == 0 || (!backward && a.q_len == 0)) return CONV_OK;
   char* ws = static_cast<char*>(workspace);
@@ -161,9 +406,9 @@ conv_status_t run(const cross_attention_args_t* args, bool backward, void* works
                          a.kv_len, l.mask.words, bits, stream) != cudaSuccess)
       return CONV_ERR_CUDA;
   }
-  const cudaError_t e =
-      backward ? launch_attn_simple_bwd(s, stream) : launch_attn_simple_fwd(s, stream);
-  return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+  if (backward) return run_bwd(s, f, g, ws, l, stream);
+  if (a.kv_len > 0) return run_fwd(s, f, ws, l, stream);
+  return launch_attn_no_keys(s, stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 
 }  // namespace
@@ -175,7 +420,17 @@ extern "C" {
 size_t cross_attention_workspace_size(const cross_attention_args_t* args, int backward) {
   using namespace convgb300;
   if (!args || check_sizes(*args) != CONV_OK) return 0;
-  return layout(*args).total;
+  const int sms = attn_sm_count();
+  if (sms <= 0) return 0;
+  // Whichever way the queries turn out to be strided.
+  size_t total = 0;
+  for (int packed = 0; packed < 2; ++packed) {
+    const FwdPlan f = plan_fwd(*args, sms, packed != 0);
+    const BwdPlan g = plan_bwd(*args, f, sms);
+    total = std::max(total, layout(*args, false, f, g).total);
+    if (backward) total = std::max(total, layout(*args, true, f, g).total);
+  }
+  return total;
 }
 
 conv_status_t cross_attention_fwd(const cross_attention_args_t* args, void* workspace,

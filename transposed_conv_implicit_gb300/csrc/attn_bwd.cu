@@ -1,0 +1,1314 @@
+// Cross attention backward on the tensor cores.
+//
+//   p_ij = exp(s_ij - lse_i),  dv_j = sum_i p_ij do_i,  dp_ij = do_i . v_j
+//   ds_ij = p_ij (dp_ij - delta_i),  delta_i = do_i . o_i
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+//
+// Three kernels, none with atomics, so that every sum has a fixed order:
+//  - rows: delta and the statistics of every query (bound by reading do, o);
+//  - dq: a row tile of 128 (token, head) rows stays, key tiles stream by.
+//    S = q k^T and dp = do v^T (lanes = queries) land in TMEM, ds replaces S
+//    there and is the A operand of dq += ds k: three products per tile;
+//  - dk, dv: 128 keys stay, query tiles stream by, over all query heads that
+//    share the key head.  S^T = k q^T and dp^T = v do^T (lanes = keys), so
+//    that p^T and ds^T are A operands in TMEM where they are made: dv += p^T
+//    do, dk += ds^T q: four products per tile.
+// The scores are multiplied twice (seven products where five would do): the
+// price of dq and dk, dv each summing in registers of their own CTA, without
+// adding fp32 partial sums of dq through L2 once per key tile.
+//
+// Each kernel's (tile, step) sequence is cut into equal shares, one per SM;
+// the tiles that a share boundary cuts go through fp32 partial sums, which a
+// last kernel adds in order.  Rows that take no part are cleared in shared
+// memory before a product sums over them.
+//
+// p and ds are rounded to the inputs' type.  In fp16 both are scaled by
+// powers of two first: p <= 1 by 2^15, and ds by the largest power that
+// |ds| <= 2 max|do| max|v| allows, so that neither leaves fp16's range; the
+// results are scaled back in fp32.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "attn_common.cuh"
+#include "attn_internal.h"
+#include "attn_params.h"
+
+namespace convgb300 {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr int kMaxRing = 8;
+constexpr int kNormBlocks = kAttnNormBlocks;
+
+// ------------------------------------------------------------------ rows
+template <typename T>
+__device__ __forceinline__ float2 widen2(uint32_t v);
+template <>
+__device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <>
+__device__ __forceinline__ float2 widen2<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+template <typename T>
+__device__ __forceinline__ float dot8(uint4 x, uint4 y) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = widen2<T>(a[i]), v = widen2<T>(b[i]);
+    s = fmaf(u.x, v.x, s);
+    s = fmaf(u.y, v.y, s);
+  }
+  return s;
+}
+
+// stats[b][h][token tile][2][128]: lse in log2 units (+inf for queries without
+// keys and past the end, which makes p zero) and delta.  With norms: the
+// largest |do| row of each block, then (kNormBlocks blocks on) |v| row, both
+// squared; rows that take no part are left out.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnBwdParams p) {
+  __shared__ float most[8];
+  const AttnShape& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // Power-of-two lanes per row, 16 bytes each.
+  const int words = a.head_dim >> 3;
+  int width = 1;
+  while (width < words) width <<= 1;
+  const int at = lane & (width - 1), slot = lane / width, slots = 32 / width;
+  const long long padded = static_cast<long long>(p.q_tiles) * kAttnRows;
+  float norm = 0.f;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const bool values = blockIdx.x >= static_cast<unsigned>(p.row_blocks);
+  const int block = values ? blockIdx.x - p.row_blocks : blockIdx.x;
+  const int blocks = values ? gridDim.x - p.row_blocks : p.row_blocks;
+  const int heads = values ? a.kv_heads : a.heads;
+  const long long length = values ? a.kv_len : padded;
+  const long long rows = length * heads * a.batch;  // tokens outermost within a batch
+  const long long step = static_cast<long long>(blocks) * 8 * slots;
+  for (long long row0 = (static_cast<long long>(block) * 8 + warp) * slots; row0 < rows;
+       row0 += step) {
+    const long long row = row0 + slot;
+    const long long bt = row / heads;
+    const int h = static_cast<int>(row - bt * heads);
+    const int b = static_cast<int>(bt / length);
+    const long long t = bt - b * length;
+    const bool in = row < rows;
+    float dot = 0.f, sq = 0.f;
+    if (values) {
+      if (in && at < words && t < valid_keys(a, b)) {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + b * a.vs[0] +
+                                                        t * a.vs[1] + h * a.vs[2] + at * 8);
+        sq = dot8<T>(v, v);
+      }
+    } else if (in && at < words && t < a.q_len) {
+      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + b * a.dos[0] +
+                                                      t * a.dos[1] + h * a.dos[2] + at * 8);
+      const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + b * a.os[0] +
+                                                      t * a.os[1] + h * a.os[2] + at * 8);
+      dot = dot8<T>(x, y);
+      if (p.norms) sq = dot8<T>(x, x);
+    }
+    for (int o = width >> 1; o; o >>= 1) {
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+      sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+    }
+    if (!values && in && at == 0) {
+      float lse2 = INFINITY;
+      if (t < a.q_len) {
+        const float lse = a.lse[(static_cast<long long>(b) * a.heads + h) * a.q_len + t];
+        if (lse != -INFINITY) lse2 = lse * kLog2e;
+      }
+      if (lse2 == INFINITY) dot = sq = 0.f;
+      const long long tile = (static_cast<long long>(b) * a.heads + h) * p.q_tiles + (t >> 7);
+      p.stats[tile * 256 + (t & 127)] = lse2;
+      p.stats[tile * 256 + 128 + (t & 127)] = dot;
+    }
+    if (in && at == 0 && sq < INFINITY) norm = fmaxf(norm, sq);  // (NaN compares false)
+  }
+  if (!p.norms) return;
+  for (int o = 16; o; o >>= 1) norm = fmaxf(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
+  if (lane == 0) most[warp] = norm;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) norm = fmaxf(norm, most[i]);
+    p.norms[(values ? kNormBlocks : 0) + block] = norm;
+  }
+}
+
+// The power of two that ds is scaled by: |ds| 2^k <= 2^15.  One warp.
+__device__ __forceinline__ float ds_scale(const AttnBwdParams& p, int lane) {
+  if (!p.norms) return 1.f;
+  float x = 0.f, y = 0.f;
+  for (int i = lane; i < p.row_blocks; i += 32) x = fmaxf(x, p.norms[i]);
+  for (int i = lane; i < p.value_blocks; i += 32) y = fmaxf(y, p.norms[kNormBlocks + i]);
+  for (int o = 16; o; o >>= 1) {
+    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+    y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
+  }
+  // 2 |do| |v| < 2^(1 + ceil exponents); both norms in fp16's range, so k is
+  // within +-60.
+  const float bound = 2.f * sqrtf(x) * sqrtf(y);
+  if (!(bound > 0.f)) return 1.f;
+  int e;
+  frexpf(bound, &e);  // bound < 2^e
+  return ldexpf(1.f, max(-60, min(60, 14 - e)));
+}
+
+struct Bars {
+  uint64_t a_full[2], a_empty[2];                 // q, do (dq kernel); k, v (dk, dv kernel)
+  uint64_t x_full[kMaxRing], x_empty[kMaxRing];   // k ring; q ring
+  uint64_t y_full[kMaxRing], y_empty[kMaxRing];   // v ring; do ring
+  uint64_t st_full[2], st_empty[2];               // dk, dv: the queries' statistics
+  uint64_t s_full[2], dp_full, dp_free, p_full, acc_done, acc_free;
+  // dq: by step parity.  The step after next cannot arrive before the
+  // products have waited for this one, so no wait sees a phase go by.
+  uint64_t ds_full[2];
+  uint64_t drain;
+  SplitStart start;
+  float ds_scale;
+  uint32_t any[2][4][4];  // dq, by step parity: keys that a row of the quarter attends
+  uint32_t tmem;
+  int abort_flag;
+};
+
+static_assert(sizeof(Bars) <= 1024, "shared-memory plan of the dk, dv kernel");
+
+constexpr int kBwdThreads = 320;  // 8 softmax warps, products, loads
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+
+__device__ __forceinline__ void clear_rows(uint8_t* tile, uint32_t block_bytes, int blocks, int r0,
+                                           int limit, uint32_t keep, int lane) {
+  const int r = r0 + lane;
+  if (r < limit && !((keep >> lane) & 1u)) {
+    uint4* q = reinterpret_cast<uint4*>(tile) + r * 8;
+    for (int c = 0; c < blocks; ++c)
+      for (int i = 0; i < 8; ++i) q[c * (block_bytes >> 4) + i] = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Writes 32 fp32 columns of a row, scaled: rounded to T.
+template <typename T>
+__device__ __forceinline__ void store_cols(T* dst, const uint32_t* v, int n, float f) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    if (i < n) {
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[j] = round2<T>(__uint_as_float(v[i + 2 * j]) * f, __uint_as_float(v[i + 2 * j + 1]) * f);
+      *reinterpret_cast<uint4*>(dst + i) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+__device__ __forceinline__ void store_cols_f32(float* dst, const uint32_t* v, int n) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+    if (i < n) *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
+// ------------------------------------------------------------------ dq
+template <typename T, int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_dq_kernel(const __grid_constant__ AttnBwdParams p) {
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kBlocks = DP / 64;
+  constexpr uint32_t kATile = 128u * 128u * kBlocks;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + p.off_bar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars.abort_flag;
+  unsigned int* status = p.status;
+  const long long limit = p.timeout_cycles;
+  const uint32_t kv_block = static_cast<uint32_t>(p.kv_box) * 128u;
+  const uint32_t kv_tile = kv_block * kBlocks;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.a_full[i]), 1);
+      mbar_init(smem_u32(&bars.a_empty[i]), 1);
+      mbar_init(smem_u32(&bars.s_full[i]), 1);
+      mbar_init(smem_u32(&bars.ds_full[i]), 8);
+    }
+    for (int i = 0; i < p.x_stages; ++i) {
+      mbar_init(smem_u32(&bars.x_full[i]), 1);
+      mbar_init(smem_u32(&bars.x_empty[i]), 1);
+    }
+    for (int i = 0; i < p.y_stages; ++i) {
+      mbar_init(smem_u32(&bars.y_full[i]), 1);
+      mbar_init(smem_u32(&bars.y_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&bars.dp_full), 1);
+    mbar_init(smem_u32(&bars.dp_free), 8);
+    mbar_init(smem_u32(&bars.acc_done), 1);
+    mbar_init(smem_u32(&bars.acc_free), 8);
+    mbar_init(smem_u32(&bars.drain), 1);
+    bars.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars.tmem), 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&p.map_q);
+    tma_prefetch_desc(&p.map_do);
+    tma_prefetch_desc(&p.map_k);
+    tma_prefetch_desc(&p.map_v);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (warp == 0) {
+    const SplitStart st = split_rows(p, lane);
+    const float f = ds_scale(p, lane);
+    if (lane == 0) {
+      bars.start = st;
+      bars.ds_scale = f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  const SplitStart start = bars.start;
+  // TMEM columns: S (two buffers; ds over them), dp, dq.
+  const uint32_t t_dp = tmem + 256, t_acc = tmem + 384;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int code) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag, status,
+                                                     code, limit));
+  };
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    const uint32_t a_bytes = static_cast<uint32_t>(p.tile_heads * p.tile_tokens) * 128u * kBlocks;
+    bool ok = true;
+    int xs = 0, ys = 0;
+    uint32_t xph = 0, yph = 0, aph = 0;
+    long long nx = 0, ny = 0, na = 0;
+    for (Walk<true, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
+      int token, head;
+      w.place(0, &token, &head);
+      for (int i = 0; ok && i < 2; ++i) {
+        ok = wait(&bars.a_empty[i], aph ^ 1u, kAttnProducerTimeout);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&bars.a_full[i]);
+        mbar_arrive_expect_tx_if(lead, bar, a_bytes);
+        const CUtensorMap* map = i ? &p.map_do : &p.map_q;
+        const int* mul = i ? p.do_mul : p.q_mul;
+        for (int c = 0; c < kBlocks; ++c)
+          tma_load_4d_if(lead, smem_u32(smem + p.off_a) + i * kATile + c * 16384u, map, bar, c * 64,
+                         head * mul[0], token, w.b * mul[1]);
+        if (i == 1) ++na;
+      }
+      aph ^= 1u;
+      for (int t = w.t0; ok && t < w.t1; ++t) {
+        ok = wait(&bars.x_empty[xs], xph ^ 1u, kAttnProducerTimeout);
+        if (!ok) break;
+        if (!(p.fault_mode == 1 && blockIdx.x == 0 && nx == 0)) {
+          mbar_arrive_expect_tx_if(lead, smem_u32(&bars.x_full[xs]), kv_tile);
+          for (int c = 0; c < kBlocks; ++c)
+            tma_load_4d_if(lead, smem_u32(smem + p.off_x) + xs * kv_tile + c * kv_block, &p.map_k,
+                           smem_u32(&bars.x_full[xs]), c * 64, w.hk * p.k_mul[0], t * p.kv_box,
+                           w.b * p.k_mul[1]);
+        }
+        ++nx;
+        if (++xs == p.x_stages) {
+          xs = 0;
+          xph ^= 1u;
+        }
+        ok = wait(&bars.y_empty[ys], yph ^ 1u, kAttnProducerTimeout);
+        if (!ok) break;
+        mbar_arrive_expect_tx_if(lead, smem_u32(&bars.y_full[ys]), kv_tile);
+        for (int c = 0; c < kBlocks; ++c)
+          tma_load_4d_if(lead, smem_u32(smem + p.off_y) + ys * kv_tile + c * kv_block, &p.map_v,
+                         smem_u32(&bars.y_full[ys]), c * 64, w.hk * p.v_mul[0], t * p.kv_box,
+                         w.b * p.v_mul[1]);
+        ++ny;
+        if (++ys == p.y_stages) {
+          ys = 0;
+          yph ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      // Let every copy still in flight land before the CTA exits.
+      for (long long q = nx - p.x_stages; q < nx; ++q)
+        if (q >= 0)
+          mbar_wait_drain(smem_u32(&bars.x_full[q % p.x_stages]),
+                          static_cast<uint32_t>((q / p.x_stages) & 1), limit / 8 + 1);
+      for (long long q = ny - p.y_stages; q < ny; ++q)
+        if (q >= 0)
+          mbar_wait_drain(smem_u32(&bars.y_full[q % p.y_stages]),
+                          static_cast<uint32_t>((q / p.y_stages) & 1), limit / 8 + 1);
+      if (na > 0)
+        for (int i = 0; i < 2; ++i)
+          mbar_wait_drain(smem_u32(&bars.a_full[i]), static_cast<uint32_t>((na - 1) & 1),
+                          limit / 8 + 1);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    const int k_steps = (p.a.head_dim + 15) >> 4;
+    const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
+    const uint32_t idesc_acc = attn_idesc(kBf16, k_steps * 16, false, true);
+    const uint64_t desc_k = desc_mn(kv_block);
+    const uint32_t a_lo = smem_u32(smem + p.off_a) >> 4, x_lo = smem_u32(smem + p.off_x) >> 4,
+                   y_lo = smem_u32(smem + p.off_y) >> 4;
+    const uint32_t tile_lo = kv_tile >> 4, block_lo = kv_block >> 4;
+    bool ok = true;
+    int xs = 0, ys = 0;
+    uint32_t xph = 0, yph = 0, aph = 0, count = 0, items = 0;
+    // A (128 rows) times a key/value tile, over the head dimension.
+    auto rows_by_keys = [&](uint32_t d, uint32_t a, uint32_t b, int cols) {
+      const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
+      for (int k = 0; k < k_steps; ++k)
+        mma_f16_warp(d, kDescK | (a + (k >> 2) * 1024u + (k & 3) * 2u),
+                     kDescK | (b + (k >> 2) * block_lo + (k & 3) * 2u), id, k != 0);
+    };
+    Walk<true, AttnBwdParams> w(p, start);
+    bool live = w.live;
+    int t = w.t0, cols = 0, k_stage = 0;
+    if (live) {
+      cols = w.tile_cols(t);
+      ok = wait(&bars.a_full[0], 0, kAttnMmaTimeout) && wait(&bars.x_full[0], 0, kAttnMmaTimeout);
+      if (ok) {
+        tc_fence_after();
+        rows_by_keys(tmem, a_lo, x_lo, cols);
+        mma_commit_warp(smem_u32(&bars.s_full[0]));
+        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
+        if (++xs == p.x_stages) {
+          xs = 0;
+          xph ^= 1u;
+        }
+        ok = wait(&bars.a_full[1], 0, kAttnMmaTimeout) && wait(&bars.y_full[0], 0, kAttnMmaTimeout);
+      }
+      if (ok) {
+        tc_fence_after();
+        rows_by_keys(t_dp, a_lo + (kATile >> 4), y_lo, cols);
+        mma_commit_warp(smem_u32(&bars.dp_full));
+        mma_commit_warp(smem_u32(&bars.y_empty[0]));
+        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
+        if (++ys == p.y_stages) {
+          ys = 0;
+          yph ^= 1u;
+        }
+      }
+    }
+    while (ok && live) {
+      const bool first = t == w.t0, last = t + 1 == w.t1;
+      const int keys = w.tile_keys(t), this_cols = cols, this_k = k_stage;
+      bool more = true;
+      if (last) {
+        w.next();
+        more = w.live;
+        t = w.t0;
+        aph ^= 1u;
+      } else {
+        ++t;
+      }
+      if (more) {
+        // The next step's S runs beside this step's exponentials ...
+        cols = w.tile_cols(t);
+        if (last) ok = wait(&bars.a_full[0], aph, kAttnMmaTimeout);
+        ok = ok && wait(&bars.x_full[xs], xph, kAttnMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        k_stage = xs;
+        rows_by_keys(tmem + ((count + 1) & 1u) * 128, a_lo, x_lo + xs * tile_lo, cols);
+        mma_commit_warp(smem_u32(&bars.s_full[(count + 1) & 1u]));
+        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
+        if (++xs == p.x_stages) {
+          xs = 0;
+          xph ^= 1u;
+        }
+        // ... and its dp as soon as this step's has been read.
+        ok = wait(&bars.dp_free, count & 1u, kAttnMmaTimeout);
+        if (ok && last) ok = wait(&bars.a_full[1], aph, kAttnMmaTimeout);
+        ok = ok && wait(&bars.y_full[ys], yph, kAttnMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        rows_by_keys(t_dp, a_lo + (kATile >> 4), y_lo + ys * tile_lo, cols);
+        mma_commit_warp(smem_u32(&bars.dp_full));
+        mma_commit_warp(smem_u32(&bars.y_empty[ys]));
+        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
+        if (++ys == p.y_stages) {
+          ys = 0;
+          yph ^= 1u;
+        }
+      }
+      ok = wait(&bars.ds_full[count & 1u], (count >> 1) & 1u, kAttnMmaTimeout);
+      if (ok && first) {
+        if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
+        ++items;
+      }
+      if (!ok) break;
+      const bool masked = p.a.mask_bits != nullptr;
+      if (masked || (keys < this_cols && p.a.kv_lengths)) {
+        for (int r0 = 0; r0 < this_cols; r0 += 32) {
+          uint32_t used = keys - r0 >= 32 ? 0xFFFFFFFFu : keys > r0 ? (1u << (keys - r0)) - 1u : 0u;
+          if (masked)
+            for (int i = 0, any = 0; i < 4; ++i) {
+              any |= bars.any[count & 1u][i][r0 >> 5];
+              if (i == 3) used &= any;
+            }
+          clear_rows(smem + p.off_x + this_k * kv_tile, kv_block, kBlocks, r0, this_cols, used, lane);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+      }
+      tc_fence_after();
+      const uint32_t ds = tmem + (count & 1u) * 128;
+      for (int k = 0; k < (this_cols >> 4); ++k)
+        mma_f16_ts_warp(t_acc, ds + (k >> 2) * 64 + (k & 3) * 8,
+                        desc_k | (x_lo + this_k * tile_lo + k * 128u), idesc_acc, !(first && k == 0));
+      mma_commit_warp(smem_u32(&bars.x_empty[this_k]));
+      if (last) mma_commit_warp(smem_u32(&bars.acc_done));
+      ++count;
+      live = more;
+    }
+    if (!ok) {
+      mma_commit_warp(smem_u32(&bars.drain));
+      mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ p and ds
+    // Two warps share a quarter of the lanes; each takes half of the keys.
+    const int half = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
+    const float c2 = p.scale_log2, sc = bars.ds_scale;
+    const int d = p.a.head_dim;
+    uint32_t count = 0, items = 0;
+    bool ok = true;
+    for (Walk<true, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
+      int token, head;
+      w.place(0, &token, &head);
+      bool row_ok = true;
+      if (p.tile_heads > 1) {
+        const int dt = r / p.tile_heads;
+        row_ok = dt < p.tile_tokens;
+        token += dt;
+        head += r - dt * p.tile_heads;
+      } else {
+        token += r;
+      }
+      row_ok = row_ok && token < p.a.q_len;
+      float lse2 = INFINITY, delta = 0.f;
+      const uint32_t* bits = nullptr;
+      if (row_ok) {
+        const float* st = p.stats +
+                          ((static_cast<long long>(w.b) * p.a.heads + head) * p.q_tiles + (token >> 7)) * 256;
+        lse2 = st[token & 127];
+        delta = st[128 + (token & 127)];
+        if (p.a.mask_bits)
+          bits = p.a.mask_bits +
+                 (w.b * p.a.mask_b + head * p.a.mask_h + token * p.a.mask_q) * p.a.mask_words;
+      }
+      const uint64_t c22 = pack2(c2, c2), l2 = pack2(-lse2, -lse2), sc2 = pack2(sc, sc),
+                     dl2 = pack2(-delta * sc, -delta * sc);
+      for (int t = w.t0; t < w.t1; ++t) {
+        const int keys = w.tile_keys(t), cols = w.tile_cols(t);
+        uint32_t word[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (p.a.mask_bits) {
+          uint2 q = make_uint2(0, 0);
+          if (bits) q = *reinterpret_cast<const uint2*>(bits + (t * p.kv_box >> 5) + half * 2);
+          word[0] = q.x;
+          word[1] = q.y;
+        }
+        const uint32_t buf = count & 1u;
+        ok = wait(&bars.s_full[buf], (count >> 1) & 1u, kAttnSoftmaxTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ts = tmem + buf * 128 + half * 64 + lane_field;
+        const uint32_t td = t_dp + half * 64 + lane_field;
+        const int mine = cols - half * 64;  // columns of this half
+        uint32_t s[64];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (c * 32 < mine) tmem_ld_x32(ts + c * 32, s + c * 32);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c * 32 < mine) {
+            tmem_wait_ld_x32(s + c * 32);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x, y;
+              unpack2(fma2(pack2(__uint_as_float(s[c * 32 + 2 * i]),
+                                 __uint_as_float(s[c * 32 + 2 * i + 1])), c22, l2), x, y);
+              s[c * 32 + 2 * i] = __float_as_uint(exp2_approx(x));
+              s[c * 32 + 2 * i + 1] = __float_as_uint(exp2_approx(y));
+            }
+          }
+        }
+        ok = wait(&bars.dp_full, count & 1u, kAttnSoftmaxTimeout);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c * 32 < mine) {
+            uint32_t dp[32], h[16];
+            tmem_ld_x32(td + c * 32, dp);
+            tmem_wait_ld_x32(dp);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x, y;
+              unpack2(mul2(fma2(pack2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), sc2,
+                                dl2),
+                           pack2(__uint_as_float(s[c * 32 + 2 * i]),
+                                 __uint_as_float(s[c * 32 + 2 * i + 1]))), x, y);
+              dp[2 * i] = __float_as_uint(x);
+              dp[2 * i + 1] = __float_as_uint(y);
+            }
+            uint32_t on = word[c];
+            const int rest = keys - half * 64 - c * 32;
+            if (rest < 32) on &= rest <= 0 ? 0u : (1u << rest) - 1u;
+            if (on != 0xFFFFFFFFu) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((on >> i) & 1u)) dp[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              h[i] = round2<T>(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
+            tmem_st_x16(ts + c * 16, h);
+          }
+        }
+        if (p.a.mask_bits) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, word[i]);
+            if (lane == 0) bars.any[buf][quarter][half * 2 + i] = any;
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&bars.dp_free));
+          mbar_arrive(smem_u32(&bars.ds_full[buf]));
+        }
+        ++count;
+      }
+      if (!ok) break;
+      ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      ++items;
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = w.t0 == 0 && w.t1 == w.nt;
+      const long long slot = 2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+      const float f = p.a.scale / sc;
+#pragma unroll
+      for (int c = 0; c < DP / 2; c += 32) {
+        const int col = half * (DP / 2) + c;
+        uint32_t v[32];
+        tmem_ld_x32(t_acc + col + lane_field, v);
+        tmem_wait_ld_x32(v);
+        if (row_ok && col < d) {
+          if (whole)
+            store_cols(static_cast<T*>(p.a.dq) + w.b * p.a.dqs[0] + token * p.a.dqs[1] +
+                           head * p.a.dqs[2] + col,
+                       v, d - col, f);
+          else
+            store_cols_f32(p.part_q + (slot * kAttnRows + r) * 128 + col, v, d - col);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.acc_free));
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dk, dv
+// Key tiles of 128 of each batch's valid keys; an item is one key tile of one
+// key head, its steps the query tiles of the heads that share it.
+__device__ __forceinline__ long long key_steps(const AttnBwdParams& p, int b) {
+  return static_cast<long long>((valid_keys(p.a, b) + kAttnRows - 1) / kAttnRows) * p.a.kv_heads *
+         p.item_steps;
+}
+__device__ __forceinline__ long long key_steps_uniform(const AttnBwdParams& p) {
+  return p.a.kv_lengths ? -1 : key_steps(p, 0);
+}
+
+struct KeyWalk {
+  const AttnBwdParams& p;
+  long long left;  // steps after this item
+  int b, hk, tile, n;
+  int i0, i1;      // steps [i0, i1) of item_steps
+  bool live;
+  __device__ KeyWalk(const AttnBwdParams& params, const SplitStart& st) : p(params) {
+    left = st.left;
+    live = left > 0;
+    b = st.b;
+    if (!live) return;
+    n = valid_keys(p.a, b);
+    const long long item = st.rest / p.item_steps;
+    const int tiles = (n + kAttnRows - 1) / kAttnRows;
+    hk = static_cast<int>(item / tiles);
+    tile = static_cast<int>(item - static_cast<long long>(hk) * tiles);
+    take(static_cast<int>(st.rest - item * p.item_steps));
+  }
+  __device__ void take(int from) {
+    i0 = from;
+    i1 = static_cast<int>(min(static_cast<long long>(p.item_steps), from + left));
+    left -= i1 - i0;
+  }
+  __device__ void next() {
+    live = left > 0;
+    if (!live) return;
+    if (++tile * kAttnRows >= n) {
+      tile = 0;
+      if (++hk == p.a.kv_heads) {
+        hk = 0;
+        do n = valid_keys(p.a, ++b);
+        while (n == 0);
+      }
+    }
+    take(0);
+  }
+  __device__ int head(int i) const { return hk * p.a.group + i / p.q_tiles; }
+  __device__ int q_tile(int i) const { return i % p.q_tiles; }
+  __device__ int cols(int i) const {
+    return (min(kAttnRows, p.a.q_len - q_tile(i) * kAttnRows) + 15) & ~15;
+  }
+  __device__ int keys() const { return min(kAttnRows, n - tile * kAttnRows); }
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_dkv_kernel(const __grid_constant__ AttnBwdParams p) {
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kBlocks = DP / 64;
+  constexpr uint32_t kTile = 128u * 128u * kBlocks;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + p.off_bar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars.abort_flag;
+  unsigned int* status = p.status;
+  const long long limit = p.timeout_cycles;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.a_full[i]), 1);
+      mbar_init(smem_u32(&bars.a_empty[i]), 1);
+    }
+    for (int i = 0; i < p.x_stages; ++i) {
+      mbar_init(smem_u32(&bars.x_full[i]), 1);
+      mbar_init(smem_u32(&bars.x_empty[i]), 1);
+    }
+    for (int i = 0; i < p.y_stages; ++i) {
+      mbar_init(smem_u32(&bars.y_full[i]), 1);
+      mbar_init(smem_u32(&bars.y_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.st_full[i]), 1);
+      mbar_init(smem_u32(&bars.st_empty[i]), 8);
+    }
+    mbar_init(smem_u32(&bars.s_full[0]), 1);
+    mbar_init(smem_u32(&bars.dp_full), 1);
+    mbar_init(smem_u32(&bars.p_full), 8);
+    mbar_init(smem_u32(&bars.ds_full[0]), 8);
+    mbar_init(smem_u32(&bars.acc_done), 1);
+    mbar_init(smem_u32(&bars.acc_free), 8);
+    mbar_init(smem_u32(&bars.drain), 1);
+    bars.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars.tmem), 512);
+    tmem_relinquish();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&p.map_q);
+    tma_prefetch_desc(&p.map_do);
+    tma_prefetch_desc(&p.map_k);
+    tma_prefetch_desc(&p.map_v);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (warp == 0) {
+    const SplitStart st = split_start(p.a.batch, key_steps_uniform(p), lane,
+                                      [&](int b) { return key_steps(p, b); });
+    const float f = ds_scale(p, lane);
+    if (lane == 0) {
+      bars.start = st;
+      bars.ds_scale = f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  const SplitStart start = bars.start;
+  // TMEM columns: S^T (p^T over it), dp^T (ds^T over it), dv, dk.
+  const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int code) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag, status,
+                                                     code, limit));
+  };
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    const uint32_t kv_bytes = static_cast<uint32_t>(p.kv_box) * 128u * kBlocks;
+    const uint32_t q_bytes = static_cast<uint32_t>(p.q_box) * 128u * kBlocks;
+    bool ok = true;
+    int xs = 0, ys = 0;
+    uint32_t xph = 0, yph = 0, aph = 0;
+    long long nx = 0, ny = 0, na = 0, nst = 0;
+    for (KeyWalk w(p, start); ok && w.live; w.next()) {
+      for (int i = 0; ok && i < 2; ++i) {
+        ok = wait(&bars.a_empty[i], aph ^ 1u, kAttnProducerTimeout);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&bars.a_full[i]);
+        mbar_arrive_expect_tx_if(lead, bar, kv_bytes);
+        const CUtensorMap* map = i ? &p.map_v : &p.map_k;
+        const int* mul = i ? p.v_mul : p.k_mul;
+        for (int c = 0; c < kBlocks; ++c)
+          tma_load_4d_if(lead, smem_u32(smem + p.off_a) + i * kTile + c * 16384u, map, bar, c * 64,
+                         w.hk * mul[0], w.tile * kAttnRows, w.b * mul[1]);
+        if (i == 1) ++na;
+      }
+      aph ^= 1u;
+      for (int i = w.i0; ok && i < w.i1; ++i) {
+        const int h = w.head(i), qt = w.q_tile(i);
+        ok = wait(&bars.x_empty[xs], xph ^ 1u, kAttnProducerTimeout);
+        if (!ok) break;
+        uint32_t bar = smem_u32(&bars.x_full[xs]);
+        if (!(p.fault_mode == 1 && blockIdx.x == 0 && nx == 0)) {
+          mbar_arrive_expect_tx_if(lead, bar, q_bytes);
+          for (int c = 0; c < kBlocks; ++c)
+            tma_load_4d_if(lead, smem_u32(smem + p.off_x) + xs * kTile + c * 16384u, &p.map_q, bar,
+                           c * 64, h * p.q_mul[0], qt * kAttnRows, w.b * p.q_mul[1]);
+        }
+        const uint32_t ss = static_cast<uint32_t>(nx & 1);
+        ok = wait(&bars.st_empty[ss], static_cast<uint32_t>((nx >> 1) & 1) ^ 1u, kAttnProducerTimeout);
+        if (ok) {
+          const uint32_t sbar = smem_u32(&bars.st_full[ss]);
+          mbar_arrive_expect_tx_if(lead, sbar, 1024u);
+          if (lead)
+            bulk_load(smem_u32(smem + p.off_stat) + ss * 1024u,
+                      p.stats + ((static_cast<long long>(w.b) * p.a.heads + h) * p.q_tiles + qt) * 256,
+                      1024u, sbar);
+          __syncwarp();
+          ++nst;
+        }
+        ++nx;
+        if (!ok) break;
+        if (++xs == p.x_stages) {
+          xs = 0;
+          xph ^= 1u;
+        }
+        ok = wait(&bars.y_empty[ys], yph ^ 1u, kAttnProducerTimeout);
+        if (!ok) break;
+        bar = smem_u32(&bars.y_full[ys]);
+        mbar_arrive_expect_tx_if(lead, bar, q_bytes);
+        for (int c = 0; c < kBlocks; ++c)
+          tma_load_4d_if(lead, smem_u32(smem + p.off_y) + ys * kTile + c * 16384u, &p.map_do, bar,
+                         c * 64, h * p.do_mul[0], qt * kAttnRows, w.b * p.do_mul[1]);
+        ++ny;
+        if (++ys == p.y_stages) {
+          ys = 0;
+          yph ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      for (long long q = nx - p.x_stages; q < nx; ++q)
+        if (q >= 0)
+          mbar_wait_drain(smem_u32(&bars.x_full[q % p.x_stages]),
+                          static_cast<uint32_t>((q / p.x_stages) & 1), limit / 8 + 1);
+      for (long long q = ny - p.y_stages; q < ny; ++q)
+        if (q >= 0)
+          mbar_wait_drain(smem_u32(&bars.y_full[q % p.y_stages]),
+                          static_cast<uint32_t>((q / p.y_stages) & 1), limit / 8 + 1);
+      for (long long q = nst - 2; q < nst; ++q)
+        if (q >= 0)
+          mbar_wait_drain(smem_u32(&bars.st_full[q & 1]), static_cast<uint32_t>((q >> 1) & 1),
+                          limit / 8 + 1);
+      if (na > 0)
+        for (int i = 0; i < 2; ++i)
+          mbar_wait_drain(smem_u32(&bars.a_full[i]), static_cast<uint32_t>((na - 1) & 1),
+                          limit / 8 + 1);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ products
+    const int k_steps = (p.a.head_dim + 15) >> 4;
+    const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
+    const uint32_t idesc_acc = attn_idesc(kBf16, k_steps * 16, false, true);
+    const uint64_t desc_b = desc_mn(16384);
+    const uint32_t a_lo = smem_u32(smem + p.off_a) >> 4, x_lo = smem_u32(smem + p.off_x) >> 4,
+                   y_lo = smem_u32(smem + p.off_y) >> 4;
+    constexpr uint32_t kTileLo = kTile >> 4;
+    const bool masked = p.a.mask_bits != nullptr;
+    bool ok = true;
+    int xs = 0, ys = 0;
+    uint32_t xph = 0, yph = 0, aph = 0, count = 0, items = 0;
+    auto keys_by_rows = [&](uint32_t d, uint32_t a, uint32_t b, int cols) {
+      const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
+      for (int k = 0; k < k_steps; ++k) {
+        const uint32_t at = (k >> 2) * 1024u + (k & 3) * 2u;
+        mma_f16_warp(d, kDescK | (a + at), kDescK | (b + at), id, k != 0);
+      }
+    };
+    // A (in TMEM, halves of 64 columns) times a query tile, over its rows.
+    auto accumulate = [&](uint32_t acc, uint32_t a, uint32_t b, int cols, bool fresh) {
+      for (int k = 0; k < (cols >> 4); ++k)
+        mma_f16_ts_warp(acc, a + (k >> 2) * 64 + (k & 3) * 8, desc_b | (b + k * 128u), idesc_acc,
+                        !(fresh && k == 0));
+    };
+    // Queries without keys are cleared: nothing they hold meets a zero of p or ds.
+    auto clear = [&](uint8_t* tile, int stat_stage) {
+      const float* st = reinterpret_cast<const float*>(smem + p.off_stat + stat_stage * 1024);
+      for (int r0 = 0; r0 < kAttnRows; r0 += 32) {
+        const uint32_t used = __ballot_sync(0xFFFFFFFFu, st[r0 + lane] != INFINITY);
+        clear_rows(tile, 16384, kBlocks, r0, kAttnRows, used, lane);
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+    };
+    KeyWalk w(p, start);
+    bool live = w.live;
+    int i = w.i0, cols = 0, x_now = 0, y_now = 0;
+    bool new_item = true;
+    // S^T of the step (i of w), then its dp^T.
+    auto step_s = [&](uint32_t step) {
+      cols = w.cols(i);
+      if (new_item) ok = wait(&bars.a_full[0], aph, kAttnMmaTimeout);
+      ok = ok && wait(&bars.x_full[xs], xph, kAttnMmaTimeout);
+      if (!ok) return;
+      tc_fence_after();
+      x_now = xs;
+      if (masked) {
+        ok = wait(&bars.st_full[step & 1u], (step >> 1) & 1u, kAttnMmaTimeout);
+        if (!ok) return;
+        clear(smem + p.off_x + xs * kTile, step & 1u);
+      }
+      keys_by_rows(t_s, a_lo, x_lo + xs * kTileLo, cols);
+      mma_commit_warp(smem_u32(&bars.s_full[0]));
+      if (i + 1 == w.i1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
+      if (++xs == p.x_stages) {
+        xs = 0;
+        xph ^= 1u;
+      }
+    };
+    auto step_dp = [&](uint32_t step) {
+      if (new_item) ok = wait(&bars.a_full[1], aph, kAttnMmaTimeout);
+      ok = ok && wait(&bars.y_full[ys], yph, kAttnMmaTimeout);
+      if (!ok) return;
+      tc_fence_after();
+      y_now = ys;
+      if (masked) clear(smem + p.off_y + ys * kTile, step & 1u);
+      keys_by_rows(t_dp, a_lo + kTileLo, y_lo + ys * kTileLo, cols);
+      mma_commit_warp(smem_u32(&bars.dp_full));
+      if (i + 1 == w.i1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
+      if (++ys == p.y_stages) {
+        ys = 0;
+        yph ^= 1u;
+      }
+    };
+    if (live) {
+      step_s(0);
+      if (ok) step_dp(0);
+    }
+    while (ok && live) {
+      const bool first = i == w.i0, last = i + 1 == w.i1;
+      const int this_cols = cols, this_x = x_now, this_y = y_now;
+      ok = wait(&bars.p_full, count & 1u, kAttnMmaTimeout);
+      if (ok && first) {
+        if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
+        ++items;
+      }
+      if (!ok) break;
+      tc_fence_after();
+      accumulate(t_dv, t_s, y_lo + this_y * kTileLo, this_cols, first);
+      mma_commit_warp(smem_u32(&bars.y_empty[this_y]));
+      bool more = true;
+      new_item = false;
+      if (last) {
+        w.next();
+        more = w.live;
+        i = w.i0;
+        new_item = true;
+        aph ^= 1u;
+      } else {
+        ++i;
+      }
+      if (more) step_s(count + 1);
+      if (!ok) break;
+      ok = wait(&bars.ds_full[0], count & 1u, kAttnMmaTimeout);
+      if (!ok) break;
+      tc_fence_after();
+      accumulate(t_dk, t_dp, x_lo + this_x * kTileLo, this_cols, first);
+      mma_commit_warp(smem_u32(&bars.x_empty[this_x]));
+      if (last) mma_commit_warp(smem_u32(&bars.acc_done));
+      if (more) step_dp(count + 1);
+      ++count;
+      live = more;
+    }
+    if (!ok) {
+      mma_commit_warp(smem_u32(&bars.drain));
+      mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ p and ds
+    // One thread per key and half of the queries.
+    const int half = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
+    const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
+    const uint64_t c22 = pack2(c2, c2), sc2 = pack2(sc, sc);
+    const float up = p.p_shift;
+    const int d = p.a.head_dim;
+    const uint32_t ts = t_s + half * 64 + lane_field, td = t_dp + half * 64 + lane_field;
+    uint32_t* mask_tile = reinterpret_cast<uint32_t*>(smem + p.off_mask);
+    uint32_t count = 0, items = 0;
+    bool ok = true;
+    for (KeyWalk w(p, start); ok && w.live; w.next()) {
+      const bool key_ok = r < w.keys();
+      const bool keys_whole = w.keys() == kAttnRows;
+      bool told = false;  // of a failed wait, at a barrier
+      for (int i = w.i0; i < w.i1; ++i) {
+        const int cols = w.cols(i), mine = cols - half * 64;
+        uint32_t on[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (p.a.mask_bits) {
+          // The tile's mask words, [query][4 words of 32 keys]: every warp reads
+          // its word of 64 queries, one bit per lane.
+          const int h = w.head(i), t0 = w.q_tile(i) * kAttnRows;
+          uint32_t* buf = mask_tile + (count & 1u) * 512;
+          const int row = threadIdx.x >> 1, pair = threadIdx.x & 1;
+          uint2 q = make_uint2(0, 0);
+          if (t0 + row < p.a.q_len)
+            q = *reinterpret_cast<const uint2*>(
+                p.a.mask_bits +
+                (w.b * p.a.mask_b + h * p.a.mask_h + (t0 + row) * p.a.mask_q) * p.a.mask_words +
+                w.tile * 4 + pair * 2);
+          *reinterpret_cast<uint2*>(buf + row * 4 + pair * 2) = q;
+          ok = barrier_all(1, 256, ok);
+          told = !ok;
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            on[c] = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              on[c] |= ((buf[(half * 64 + c * 32 + j) * 4 + quarter] >> lane) & 1u) << j;
+          }
+        }
+        if (!key_ok) on[0] = on[1] = 0;
+        const bool select = p.a.mask_bits || !keys_whole;
+        const uint32_t ss = count & 1u;
+        ok = wait(&bars.st_full[ss], (count >> 1) & 1u, kAttnSoftmaxTimeout) &&
+             wait(&bars.s_full[0], count & 1u, kAttnSoftmaxTimeout);
+        if (!p.a.mask_bits && !ok) break;
+        const float* st = reinterpret_cast<const float*>(smem + p.off_stat + ss * 1024) + half * 64;
+        uint32_t s[64];
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (c * 32 < mine) tmem_ld_x32(ts + c * 32, s + c * 32);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (c * 32 < mine) {
+              tmem_wait_ld_x32(s + c * 32);
+              uint32_t h[16];
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(st + c * 32 + j);
+                float x[4];
+                unpack2(fma2(pack2(__uint_as_float(s[c * 32 + j]), __uint_as_float(s[c * 32 + j + 1])),
+                             c22, pack2(up - l.x, up - l.y)), x[0], x[1]);
+                unpack2(fma2(pack2(__uint_as_float(s[c * 32 + j + 2]), __uint_as_float(s[c * 32 + j + 3])),
+                             c22, pack2(up - l.z, up - l.w)), x[2], x[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[c * 32 + j + k] = __float_as_uint(exp2_approx(x[k]));
+              }
+              if (select) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((on[c] >> j) & 1u)) s[c * 32 + j] = 0u;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                h[j] = round2<T>(__uint_as_float(s[c * 32 + 2 * j]), __uint_as_float(s[c * 32 + 2 * j + 1]));
+              tmem_st_x16(ts + c * 16, h);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.p_full));
+          ok = wait(&bars.dp_full, count & 1u, kAttnSoftmaxTimeout);
+        }
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (c * 32 < mine) {
+              uint32_t dp[32], h[16];
+              tmem_ld_x32(td + c * 32, dp);
+              tmem_wait_ld_x32(dp);
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(st + 128 + c * 32 + j);
+                float x[4];
+                unpack2(mul2(fma2(pack2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1])), sc2,
+                                  pack2(-l.x * sc, -l.y * sc)),
+                             pack2(__uint_as_float(s[c * 32 + j]), __uint_as_float(s[c * 32 + j + 1]))),
+                        x[0], x[1]);
+                unpack2(mul2(fma2(pack2(__uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3])), sc2,
+                                  pack2(-l.z * sc, -l.w * sc)),
+                             pack2(__uint_as_float(s[c * 32 + j + 2]), __uint_as_float(s[c * 32 + j + 3]))),
+                        x[2], x[3]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dp[j + k] = __float_as_uint(x[k]);
+              }
+              if (select) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((on[c] >> j) & 1u)) dp[j] = 0u;
+              }
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                h[j] = round2<T>(__uint_as_float(dp[2 * j]), __uint_as_float(dp[2 * j + 1]));
+              tmem_st_x16(td + c * 16, h);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&bars.ds_full[0]));
+            mbar_arrive(smem_u32(&bars.st_empty[ss]));
+          }
+        }
+        ++count;
+        // (With a mask the warps meet at the next barrier, where a failed one
+        // tells the others.)
+        if (!ok && !p.a.mask_bits) break;
+      }
+      if (p.a.mask_bits && !told) ok = barrier_all(1, 256, ok);
+      if (!ok) break;
+      ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      ++items;
+      if (!ok) break;
+      tc_fence_after();
+      // Half 0 takes dv, half 1 dk.
+      const bool whole = w.i0 == 0 && w.i1 == p.item_steps;
+      const long long slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
+      const float f = half ? p.a.scale / bars.ds_scale : p.p_unscale;
+      const int j = w.tile * kAttnRows + r;
+      T* dst = half ? static_cast<T*>(p.a.dk) + w.b * p.a.dks[0] + j * p.a.dks[1] + w.hk * p.a.dks[2]
+                    : static_cast<T*>(p.a.dv) + w.b * p.a.dvs[0] + j * p.a.dvs[1] + w.hk * p.a.dvs[2];
+#pragma unroll
+      for (int c = 0; c < DP; c += 32) {
+        uint32_t v[32];
+        tmem_ld_x32((half ? t_dk : t_dv) + c + lane_field, v);
+        tmem_wait_ld_x32(v);
+        if (c < d) {
+          if (whole) {
+            if (j < p.a.kv_len) store_cols(dst + c, v, d - c, f);
+          } else {
+            store_cols_f32(p.part_kv + ((slot * 2 + half) * kAttnRows + r) * 128 + c, v, d - c);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.acc_free));
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ joins
+// Adds the shares of tiles that the launches before cut, in order, and clears
+// the gradients of keys past each request's length.  One block per tile: the
+// row tiles of dq first, then the key tiles of dk and dv.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    attn_bwd_join_kernel(const __grid_constant__ AttnBwdParams p, int q_ctas, int kv_ctas,
+                         long long q_blocks) {
+  __shared__ long long sums[2][32];
+  __shared__ float factor;
+  const AttnShape& a = p.a;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = lane * 4;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (warp == 0) {
+    const float f = ds_scale(p, lane);
+    if (lane == 0) factor = a.scale / f;
+  }
+  __syncthreads();
+  long long before, total;
+  if (blockIdx.x < q_blocks) {
+    const int b = static_cast<int>(blockIdx.x / p.item_rows);
+    const int item = static_cast<int>(blockIdx.x - b * p.item_rows);
+    split_prefix(a.batch, row_steps_uniform(p), b, sums, [&](int i) { return row_steps(p, i); },
+                 &before, &total);
+    const int nt = key_tiles(valid_keys(a, b), p.kv_box);
+    const long long s0 = before + static_cast<long long>(item) * nt;
+    const int c0 = share_of(total, q_ctas, s0), c1 = share_of(total, q_ctas, s0 + nt - 1);
+    if (c0 == c1) return;
+    const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
+    int token0, head0, rows;
+    if (p.tile_heads > 1) {
+      token0 = rt * p.tile_tokens;
+      head0 = hk * a.group;
+      rows = min(p.tile_tokens, a.q_len - token0) * p.tile_heads;
+    } else {
+      const int hg = rt / p.token_tiles;
+      token0 = (rt - hg * p.token_tiles) * kAttnRows;
+      head0 = hk * a.group + hg;
+      rows = min(kAttnRows, a.q_len - token0);
+    }
+    for (int r = warp; r < rows; r += 8) {
+      if (d0 >= a.head_dim) break;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = c0; c <= c1; ++c) {
+        if (share_begin(total, q_ctas, c) == share_begin(total, q_ctas, c + 1)) continue;
+        const float4 v = *reinterpret_cast<const float4*>(
+            p.part_q + ((2ll * c + (c == c0 ? 1 : 0)) * kAttnRows + r) * 128 + d0);
+        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+      }
+      const int dt = p.tile_heads > 1 ? r / p.tile_heads : r;
+      const int token = token0 + dt, head = p.tile_heads > 1 ? head0 + r - dt * p.tile_heads : head0;
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.dq) + b * a.dqs[0] + token * a.dqs[1] +
+                                head * a.dqs[2] + d0) =
+          make_uint2(round2<T>(acc.x * factor, acc.y * factor), round2<T>(acc.z * factor, acc.w * factor));
+    }
+    return;
+  }
+  const int all_tiles = (a.kv_len + kAttnRows - 1) / kAttnRows;
+  const long long at = blockIdx.x - q_blocks;
+  const long long bh = at / all_tiles;
+  const int tile = static_cast<int>(at - bh * all_tiles);
+  const int b = static_cast<int>(bh / a.kv_heads), hk = static_cast<int>(bh - static_cast<long long>(b) * a.kv_heads);
+  const int n = p.item_steps > 0 ? valid_keys(a, b) : 0, tiles = (n + kAttnRows - 1) / kAttnRows;
+  const int rows = min(kAttnRows, a.kv_len - tile * kAttnRows);
+  int c0 = 0, c1 = -1;
+  if (tile < tiles) {
+    split_prefix(a.batch, key_steps_uniform(p), b, sums, [&](int i) { return key_steps(p, i); },
+                 &before, &total);
+    const long long s0 = before + (static_cast<long long>(hk) * tiles + tile) * p.item_steps;
+    c0 = share_of(total, kv_ctas, s0);
+    c1 = share_of(total, kv_ctas, s0 + p.item_steps - 1);
+    if (c0 == c1) return;
+  }
+  for (int i = warp; i < 2 * rows; i += 8) {
+    if (d0 >= a.head_dim) break;
+    const int half = i & 1, r = i >> 1, j = tile * kAttnRows + r;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      if (share_begin(total, kv_ctas, c) == share_begin(total, kv_ctas, c + 1)) continue;
+      const float4 v = *reinterpret_cast<const float4*>(
+          p.part_kv + (((2ll * c + (c == c0 ? 1 : 0)) * 2 + half) * kAttnRows + r) * 128 + d0);
+      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    }
+    const float f = half ? factor : p.p_unscale;
+    T* dst = half ? static_cast<T*>(a.dk) + b * a.dks[0] + j * a.dks[1] + hk * a.dks[2]
+                  : static_cast<T*>(a.dv) + b * a.dvs[0] + j * a.dvs[1] + hk * a.dvs[2];
+    *reinterpret_cast<uint2*>(dst + d0) =
+        make_uint2(round2<T>(acc.x * f, acc.y * f), round2<T>(acc.z * f, acc.w * f));
+  }
+}
+
+constexpr int kMaxDevices = 64;
+
+template <typename K>
+cudaError_t raise_smem(K kernel, std::atomic<size_t>* configured, size_t smem) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (configured[dev].load(std::memory_order_relaxed) < smem) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    configured[dev].store(smem, std::memory_order_relaxed);
+  }
+  return cudaSuccess;
+}
+
+template <typename T, int DP>
+cudaError_t launch_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
+  static std::atomic<size_t> configured[kMaxDevices];
+  cudaError_t e = raise_smem(attn_dq_kernel<T, DP>, configured, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_dq_kernel<T, DP>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+}
+
+template <typename T, int DP>
+cudaError_t launch_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
+  static std::atomic<size_t> configured[kMaxDevices];
+  cudaError_t e = raise_smem(attn_dkv_kernel<T, DP>, configured, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_dkv_kernel<T, DP>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+}
+
+}  // namespace
+
+size_t attn_bwd_bar_bytes() { return sizeof(Bars); }
+
+cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t stream) {
+  const dim3 grid(p.row_blocks + p.value_blocks);
+  return p.a.dtype == 0
+             ? launch_pdl(attn_rows_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, p)
+             : launch_pdl(attn_rows_kernel<__half>, grid, dim3(256), 0, stream, p);
+}
+
+cudaError_t launch_attn_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
+  const bool wide = p.a.head_dim > 64;
+  if (p.a.dtype == 0)
+    return wide ? launch_dq<__nv_bfloat16, 128>(p, grid, smem, stream)
+                : launch_dq<__nv_bfloat16, 64>(p, grid, smem, stream);
+  return wide ? launch_dq<__half, 128>(p, grid, smem, stream)
+              : launch_dq<__half, 64>(p, grid, smem, stream);
+}
+
+cudaError_t launch_attn_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
+  const bool wide = p.a.head_dim > 64;
+  if (p.a.dtype == 0)
+    return wide ? launch_dkv<__nv_bfloat16, 128>(p, grid, smem, stream)
+                : launch_dkv<__nv_bfloat16, 64>(p, grid, smem, stream);
+  return wide ? launch_dkv<__half, 128>(p, grid, smem, stream)
+              : launch_dkv<__half, 64>(p, grid, smem, stream);
+}
+
+cudaError_t launch_attn_bwd_join(const AttnBwdParams& p, int q_ctas, int kv_ctas,
+                                 long long q_blocks, long long kv_blocks, cudaStream_t stream) {
+  if (q_blocks + kv_blocks == 0) return cudaSuccess;
+  const dim3 grid(static_cast<unsigned>(q_blocks + kv_blocks));
+  return p.a.dtype == 0 ? launch_pdl(attn_bwd_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
+                                     p, q_ctas, kv_ctas, q_blocks)
+                        : launch_pdl(attn_bwd_join_kernel<__half>, grid, dim3(256), 0, stream, p,
+                                     q_ctas, kv_ctas, q_blocks);
+}
+
+}  // namespace convgb300

@@ -1,0 +1,235 @@
+// Device code shared by the attention kernels: rounding, barriers, and the
+// ways a call's work is cut between CTAs.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "attn_params.h"
+#include "attn_ptx.cuh"
+
+namespace convgb300 {
+
+template <typename T>
+__device__ __forceinline__ uint32_t round2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t round2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// bar.sync over `count` threads that also ANDs a predicate across them.
+__device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool v) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(count)
+      : "memory");
+  return out != 0;
+}
+
+__device__ __forceinline__ int valid_keys(const AttnShape& a, int b) {
+  return a.kv_lengths ? max(0, min(a.kv_lengths[b], a.kv_len)) : a.kv_len;
+}
+
+// Key tiles of a row with n keys; a row without keys takes one, fully masked.
+__device__ __forceinline__ int key_tiles(int n, int box) { return n > box ? (n + box - 1) / box : 1; }
+
+// A split launch's shares: CTA c takes steps [total * c / ctas, total * (c + 1) / ctas).
+__device__ __forceinline__ long long share_begin(long long total, int ctas, int c) {
+  return total * c / ctas;
+}
+// The CTA whose share holds step s.
+__device__ __forceinline__ int share_of(long long total, int ctas, long long s) {
+  return static_cast<int>(((s + 1) * ctas - 1) / total);
+}
+
+// Where a CTA's share begins.
+struct SplitStart {
+  long long left;  // steps of this CTA
+  long long rest;  // steps of batch b before the share
+  int b;
+};
+
+// One warp: this CTA's share of the steps of all batches, steps(b) each, or
+// `uniform` each when that is not negative.  (Each lane sums some batches.)
+template <typename F>
+__device__ SplitStart split_start(int batch, long long uniform, int lane, F steps) {
+  SplitStart st{};
+  long long total = 0;
+  if (uniform >= 0) {
+    total = uniform * batch;
+  } else {
+    for (int b = lane; b < batch; b += 32) total += steps(b);
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  }
+  const long long lo = share_begin(total, gridDim.x, blockIdx.x);
+  st.left = share_begin(total, gridDim.x, blockIdx.x + 1) - lo;
+  st.rest = lo;
+  if (st.left == 0) return st;
+  if (uniform >= 0) {
+    st.b = static_cast<int>(lo / uniform);
+    st.rest -= st.b * uniform;
+    return st;
+  }
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    const int b = b0 + lane;
+    const long long mine = b < batch ? steps(b) : 0ll;
+    long long upto = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > st.rest);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      st.b = b0 + at;
+      st.rest -= __shfl_sync(0xFFFFFFFFu, upto - mine, at);
+      return st;
+    }
+    st.rest -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return st;
+}
+
+// Block-wide: steps of all batches and of those before b.  `sums`: 2 x warps.
+template <typename F>
+__device__ void split_prefix(int batch, long long uniform, int b, long long (*sums)[32], F steps,
+                             long long* before, long long* total) {
+  if (uniform >= 0) {
+    *before = uniform * b;
+    *total = uniform * batch;
+    return;
+  }
+  long long t = 0, u = 0;
+  for (int i = threadIdx.x; i < batch; i += blockDim.x) {
+    const long long v = steps(i);
+    t += v;
+    if (i < b) u += v;
+  }
+  for (int o = 16; o; o >>= 1) {
+    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    sums[0][threadIdx.x >> 5] = t;
+    sums[1][threadIdx.x >> 5] = u;
+  }
+  __syncthreads();
+  *total = *before = 0;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) {
+    *total += sums[0][i];
+    *before += sums[1][i];
+  }
+}
+
+// Row tiles (forward, dq): a batch has item_rows items of its key tiles each.
+template <typename P>
+__device__ __forceinline__ long long row_steps(const P& p, int b) {
+  return key_tiles(valid_keys(p.a, b), p.kv_box) * p.item_rows;
+}
+template <typename P>
+__device__ __forceinline__ long long row_steps_uniform(const P& p) {
+  return p.a.kv_lengths ? -1 : key_tiles(p.a.kv_len, p.kv_box) * p.item_rows;
+}
+template <typename P>
+__device__ SplitStart split_rows(const P& p, int lane) {
+  return split_start(p.a.batch, row_steps_uniform(p), lane, [&](int b) { return row_steps(p, b); });
+}
+
+// Walks a CTA's work: every role walks the same sequence.
+template <bool kSplit, typename P>
+struct Walk {
+  const P& p;
+  long long pos;       // pairs: item index; split: steps left after this item
+  int b, hk, row_tile; // row_tile: the first of the item's row tiles
+  int tiles_here;      // row tiles of the item
+  int n;               // valid keys
+  int t0, t1, nt;      // key tiles [t0, t1) of nt
+  bool live;
+
+  __device__ Walk(const P& params, const SplitStart& st) : p(params) {
+    if constexpr (kSplit) {
+      b = st.b;
+      pos = st.left;
+      live = pos > 0;
+      if (live) {
+        const int per = key_tiles(valid_keys(p.a, b), p.kv_box);
+        const int item = static_cast<int>(st.rest / per);
+        set_split(item, static_cast<int>(st.rest - static_cast<long long>(item) * per));
+      }
+    } else {
+      pos = blockIdx.x;
+      set_pair();
+    }
+  }
+  __device__ void set_split(int item, int tile) {
+    n = valid_keys(p.a, b);
+    nt = key_tiles(n, p.kv_box);
+    hk = item / p.row_tiles;
+    row_tile = item - hk * p.row_tiles;
+    tiles_here = 1;
+    t0 = tile;
+    t1 = static_cast<int>(min(static_cast<long long>(nt), tile + pos));
+    pos -= t1 - t0;
+  }
+  __device__ void set_pair() {
+    if constexpr (kSplit) return;
+    else live = pos < p.items;
+    if (!live) return;
+    const int pairs = (p.row_tiles + 1) >> 1;
+    const long long bh = pos / pairs;
+    row_tile = 2 * static_cast<int>(pos - bh * pairs);
+    b = static_cast<int>(bh / p.a.kv_heads);
+    hk = static_cast<int>(bh - static_cast<long long>(b) * p.a.kv_heads);
+    tiles_here = min(2, p.row_tiles - row_tile);
+    n = valid_keys(p.a, b);
+    nt = key_tiles(n, p.kv_box);
+    t0 = 0;
+    t1 = nt;
+  }
+  __device__ void next() {
+    if (kSplit) {
+      live = pos > 0;
+      if (!live) return;
+      int item = hk * p.row_tiles + row_tile + 1;
+      if (item == p.item_rows) {
+        item = 0;
+        ++b;
+      }
+      set_split(item, 0);
+    } else {
+      pos += gridDim.x;
+      set_pair();
+    }
+  }
+  // First token and head of row tile `row_tile + g`.
+  __device__ void place(int g, int* token, int* head) const {
+    const int rt = row_tile + g;
+    if (p.tile_heads > 1) {
+      *token = rt * p.tile_tokens;
+      *head = hk * p.a.group;
+    } else {
+      const int hg = rt / p.token_tiles;
+      *token = (rt - hg * p.token_tiles) * kAttnRows;
+      *head = hk * p.a.group + hg;
+    }
+  }
+  // Keys of tile t that are valid, and the columns multiplied for them.
+  __device__ int tile_keys(int t) const { return max(0, min(p.kv_box, n - t * p.kv_box)); }
+  __device__ int tile_cols(int t) const { return max(16, (tile_keys(t) + 15) & ~15); }
+};
+
+}  // namespace convgb300

@@ -1,0 +1,723 @@
+// Cross attention forward on the tensor cores.
+//
+//   s = scale q k^T,  p = exp(s - max),  out = (p v) / sum p
+//
+// in one pass over the keys with the running maximum and sum of each row.  A
+// softmax group of four warps owns a row tile of 128 (token, head) rows, one
+// thread per row: S (fp32, 128 TMEM lanes x keys) comes from one tcgen05.mma
+// over the head dimension, the thread reads its row, and writes P (16-bit)
+// over it, which the second tcgen05.mma takes straight from TMEM as its A
+// operand against V, whose rows run along N in shared memory.  The output
+// accumulates in TMEM; it is rescaled only when a row's maximum grows by more
+// than a factor of 2^8 (P stays within 2^8 and the sum in fp32, so nothing is
+// lost meanwhile), which after the first tiles hardly happens.
+//
+// Two schedules:
+//  - pairs: a persistent CTA per SM takes two row tiles of one key head at a
+//    time; each key/value tile is loaded once for both, and while one group
+//    does its exponentials the tensor core multiplies for the other.
+//  - split: two CTAs per SM, one row tile each; the sequence of (row tile, key
+//    tile) steps of the whole call is cut into equal shares, so that few rows
+//    over many keys still fill the GPU and ragged lengths balance.  A row tile
+//    cut between CTAs goes through fp32 partial rows in the workspace, which
+//    a second kernel joins in order.  Query heads that share a key head sit
+//    side by side in a row tile when that makes fewer tiles.
+//
+// P is rounded to the inputs' type (the product's operand type), the sum is
+// taken of the unrounded fp32 values; O is rounded once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "attn_internal.h"
+#include "attn_params.h"
+#include "attn_common.cuh"
+
+namespace convgb300 {
+
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kRescaleLog2 = 8.f;
+
+template <typename T, int DP, int G>
+struct Layout {
+  static constexpr bool kSplit = G == 1;
+  static constexpr int kBlocks = DP / 64;
+  static constexpr int kMmaWarp = 4 * G, kLoadWarp = 4 * G + 1;
+  static constexpr uint32_t kQTile = 128u * 128u * kBlocks;
+  static constexpr uint32_t kTmemCols = G == 2 ? 512 : 256;
+};
+
+constexpr int kMaxStages = 8;
+
+struct Bars {
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
+  uint64_t q_full[2][2], q_empty[2][2];  // [group][stage]
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t drain;
+  SplitStart start;
+  uint32_t any[2][4][4];  // [group][warp]: keys of the tile that a row of the warp attends
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <typename T, int DP, int G>
+__global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
+    attn_fwd_kernel(const __grid_constant__ AttnFwdParams p) {
+  using L = Layout<T, DP, G>;
+  constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bars = *reinterpret_cast<Bars*>(smem + p.off_bar);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &bars.abort_flag;
+  unsigned int* status = p.status;
+  const long long limit = p.timeout_cycles;
+  const uint32_t kv_block = static_cast<uint32_t>(p.kv_box) * 128u;  // 64 columns of a key tile
+  const uint32_t kv_tile = kv_block * L::kBlocks;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&bars.kv_full[s]), 1);
+      mbar_init(smem_u32(&bars.kv_empty[s]), 1);
+    }
+    for (int g = 0; g < G; ++g) {
+      for (int s = 0; s < p.q_stages; ++s) {
+        mbar_init(smem_u32(&bars.q_full[g][s]), 1);
+        mbar_init(smem_u32(&bars.q_empty[g][s]), 1);
+      }
+      mbar_init(smem_u32(&bars.s_full[g]), 1);
+      mbar_init(smem_u32(&bars.p_full[g]), 4);
+      mbar_init(smem_u32(&bars.o_done[g]), 1);
+      mbar_init(smem_u32(&bars.o_free[g]), 4);
+    }
+    mbar_init(smem_u32(&bars.drain), 1);
+    bars.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == L::kMmaWarp) {
+    tmem_alloc(smem_u32(&bars.tmem), L::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == L::kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&p.map_q);
+    tma_prefetch_desc(&p.map_k);
+    tma_prefetch_desc(&p.map_v);
+    tma_prefetch_desc(&p.map_out);
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (L::kSplit && warp == 0) {
+    const SplitStart st = split_rows(p, lane);
+    if (lane == 0) bars.start = st;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  const SplitStart start = L::kSplit ? bars.start : SplitStart{};
+
+  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int code) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag, status,
+                                                     code, limit));
+  };
+
+  if (warp == L::kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    const uint32_t q_bytes =
+        static_cast<uint32_t>(p.tile_heads * p.tile_tokens) * 128u * L::kBlocks;
+    bool ok = true;
+    int stage = 0, qs = 0;
+    uint32_t phase = 0, q_phase = 0;
+    long long issued = 0;
+    long long q_issued[2] = {0, 0};
+    for (Walk<L::kSplit, AttnFwdParams> w(p, start); ok && w.live; w.next()) {
+      // Both groups' stages move together.  A group without a row tile in
+      // this item has its stage's phase completed for it (group 1 first, so
+      // that its wait precedes everything that ends the phase).
+      for (int g = G - 1; ok && g >= 0; --g) {
+        if (!wait(&bars.q_empty[g][qs], q_phase ^ 1u, kAttnProducerTimeout)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = smem_u32(&bars.q_full[g][qs]);
+        ++q_issued[g];
+        if (g >= w.tiles_here) {
+          if (lead) mbar_arrive(bar);
+          continue;
+        }
+        int token, head;
+        w.place(g, &token, &head);
+        mbar_arrive_expect_tx_if(lead, bar, q_bytes);
+#pragma unroll
+        for (int c = 0; c < L::kBlocks; ++c)
+          tma_load_4d_if(lead,
+                         smem_u32(smem + p.off_q) + (g * p.q_stages + qs) * L::kQTile + c * 16384u,
+                         &p.map_q, bar, c * 64, head * p.q_mul[0], token, w.b * p.q_mul[1]);
+      }
+      if (++qs == p.q_stages) {
+        qs = 0;
+        q_phase ^= 1u;
+      }
+      for (int t = w.t0; ok && t < w.t1; ++t) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!wait(&bars.kv_empty[stage], phase ^ 1u, kAttnProducerTimeout)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = smem_u32(&bars.kv_full[stage]);
+          const CUtensorMap* map = kv ? &p.map_v : &p.map_k;
+          const int* mul = kv ? p.v_mul : p.k_mul;
+          // (fault_mode 1, a test hook: CTA 0 leaves its first key tile un-armed.)
+          if (!(p.fault_mode == 1 && blockIdx.x == 0 && issued == 0)) {
+            mbar_arrive_expect_tx_if(lead, bar, kv_tile);
+#pragma unroll
+            for (int c = 0; c < L::kBlocks; ++c)
+              tma_load_4d_if(lead, smem_u32(smem + p.off_kv) + stage * kv_tile + c * kv_block, map,
+                             bar, c * 64, w.hk * mul[0], t * p.kv_box, w.b * mul[1]);
+          }
+          ++issued;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    if (!ok) {
+      // Let every copy still in flight land before the CTA exits.
+      for (long long q = issued - p.stages; q < issued; ++q)
+        if (q >= 0)
+          mbar_wait_drain(smem_u32(&bars.kv_full[q % p.stages]),
+                          static_cast<uint32_t>((q / p.stages) & 1), limit / 8 + 1);
+      for (int g = 0; g < G; ++g)
+        for (long long q = q_issued[g] - p.q_stages; q < q_issued[g]; ++q)
+          if (q >= 0)
+            mbar_wait_drain(smem_u32(&bars.q_full[g][q % p.q_stages]),
+                            static_cast<uint32_t>((q / p.q_stages) & 1), limit / 8 + 1);
+    }
+    __syncwarp();
+  } else if (warp == L::kMmaWarp) {
+    // ------------------------------------------------------------ products
+    // The converged warp walks the MMAs; one elected lane issues each.
+    const int k_steps = (p.a.head_dim + 15) >> 4;
+    const uint32_t n_out = static_cast<uint32_t>(k_steps) * 16u;
+    const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
+    const uint32_t idesc_o = attn_idesc(kBf16, n_out, false, true);
+    const uint64_t desc_v = desc_mn(kv_block);
+    const uint32_t q_lo = smem_u32(smem + p.off_q) >> 4, kv_lo = smem_u32(smem + p.off_kv) >> 4;
+    const uint32_t kv_tile_lo = kv_tile >> 4, kv_block_lo = kv_block >> 4;
+    bool ok = true;
+    int stage = 0, qs = 0;
+    uint32_t phase = 0, q_phase = 0, tile_parity[2] = {0, 0}, item_count[2] = {0, 0};
+    auto advance = [&]() {
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    // S of group g for the item and key stage given.
+    auto scores = [&](int g, int q_stage, int k_stage, int cols) {
+      const uint32_t a = q_lo + ((g * p.q_stages + q_stage) * L::kQTile >> 4);
+      const uint32_t b = kv_lo + k_stage * kv_tile_lo;
+      const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
+      for (int k = 0; k < k_steps; ++k)
+        mma_f16_warp(tmem + g * 128, kDescK | (a + (k >> 2) * 1024u + (k & 3) * 2u),
+                     kDescK | (b + (k >> 2) * kv_block_lo + (k & 3) * 2u), id, k != 0);
+      mma_commit_warp(smem_u32(&bars.s_full[g]));
+    };
+    Walk<L::kSplit, AttnFwdParams> w(p, start);
+    int t = w.t0;
+    bool live = w.live;
+    int cols = 0;
+    if (live) {
+      cols = w.tile_cols(t);
+      ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+      for (int g = 0; ok && g < w.tiles_here; ++g) {
+        ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        scores(g, qs, stage, cols);
+        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+      }
+      if (ok) mma_commit_warp(smem_u32(&bars.kv_empty[stage]));
+      advance();
+    }
+    while (ok && live) {
+      // This step's values, then the next step's keys.
+      const int v_stage = stage;
+      const bool first = t == w.t0;
+      const int here = w.tiles_here, keys = w.tile_keys(t);
+      ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+      if (!ok) break;
+      advance();
+      // Group 1 absent: its query stage is free as it stands.
+      if (t + 1 == w.t1 && here < G) mma_commit_warp(smem_u32(&bars.q_empty[1][qs]));
+      bool more = true, next_item = false;
+      int next_qs = qs;
+      uint32_t next_qphase = q_phase;
+      if (t + 1 == w.t1) {
+        w.next();
+        more = w.live;
+        next_item = true;
+        t = w.t0;
+        if (++next_qs == p.q_stages) {
+          next_qs = 0;
+          next_qphase ^= 1u;
+        }
+      } else {
+        ++t;
+      }
+      const int k_stage = stage;
+      int next_cols = 0;
+      if (more) {
+        next_cols = w.tile_cols(t);
+        ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+        if (!ok) break;
+        advance();
+      }
+      // Values that no row of the CTA takes part with are cleared, so that
+      // nothing they hold meets a zero of P: keys past the request's length
+      // (past the tensor's end the load has filled zeros), and masked keys.
+      const bool masked = p.a.mask_bits != nullptr;
+      if (masked)
+        for (int g = 0; ok && g < here; ++g)
+          ok = wait(&bars.p_full[g], tile_parity[g], kAttnMmaTimeout);
+      if (!ok) break;
+      if (masked || (keys < cols && p.a.kv_lengths)) {
+        uint4* row0 = reinterpret_cast<uint4*>(smem + p.off_kv + v_stage * kv_tile);
+        for (int r0 = 0; r0 < cols; r0 += 32) {
+          uint32_t used = keys - r0 >= 32 ? 0xFFFFFFFFu : keys > r0 ? (1u << (keys - r0)) - 1u : 0u;
+          if (masked) {
+            uint32_t any = 0;
+            for (int g = 0; g < here; ++g)
+              for (int i = 0; i < 4; ++i) any |= bars.any[g][i][r0 >> 5];
+            used &= any;
+          }
+          const int r = r0 + lane;
+          if (r < cols && !((used >> lane) & 1u))
+#pragma unroll
+            for (int c = 0; c < L::kBlocks; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                row0[c * (kv_block >> 4) + r * 8 + i] = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+      }
+      for (int g = 0; ok && g < G; ++g) {
+        if (g < here) {
+          if (!masked) ok = wait(&bars.p_full[g], tile_parity[g], kAttnMmaTimeout);
+          tile_parity[g] ^= 1u;
+          if (ok && first) {
+            if (item_count[g] > 0)
+              ok = wait(&bars.o_free[g], (item_count[g] - 1) & 1u, kAttnMmaTimeout);
+            ++item_count[g];
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t o = tmem + G * 128 + g * DP;
+          const uint32_t b = kv_lo + v_stage * kv_tile_lo;
+          for (int k = 0; k < (cols >> 4); ++k)
+            mma_f16_ts_warp(o, tmem + g * 128 + k * 8, desc_v | (b + k * 128u), idesc_o,
+                            !(first && k == 0));
+          mma_commit_warp(smem_u32(&bars.o_done[g]));
+        }
+        if (more && g < w.tiles_here) {
+          if (next_item) {
+            ok = wait(&bars.q_full[g][next_qs], next_qphase, kAttnMmaTimeout);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          scores(g, next_qs, k_stage, next_cols);
+          if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][next_qs]));
+        }
+      }
+      if (!ok) break;
+      mma_commit_warp(smem_u32(&bars.kv_empty[v_stage]));
+      if (more) mma_commit_warp(smem_u32(&bars.kv_empty[k_stage]));
+      qs = next_qs;
+      q_phase = next_qphase;
+      cols = next_cols;
+      live = more;
+    }
+    if (!ok) {
+      // Every MMA already issued must finish before TMEM is released.
+      mma_commit_warp(smem_u32(&bars.drain));
+      mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int g = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + g * 128 + lane_field;
+    const uint32_t to = tmem + G * 128 + g * DP + lane_field;
+    const uint32_t bar_id = 1 + g;
+    const float c2 = p.scale_log2;
+    const int d = p.a.head_dim;
+    uint8_t* stage_out = smem + p.off_out + g * 16384;
+    uint32_t tiles = 0;  // S tiles seen: barrier parity
+    bool ok = true;
+    for (Walk<L::kSplit, AttnFwdParams> w(p, start); ok && w.live; w.next()) {
+      if (g >= w.tiles_here) continue;
+      int token, head;
+      w.place(g, &token, &head);
+      bool row_ok = true;
+      if (p.tile_heads > 1) {
+        const int dt = r / p.tile_heads;
+        row_ok = dt < p.tile_tokens;
+        token += dt;
+        head += r - dt * p.tile_heads;
+      } else {
+        token += r;
+      }
+      row_ok = row_ok && token < p.a.q_len;
+      const bool warp_ok = __any_sync(0xFFFFFFFFu, row_ok);
+      const uint32_t* bits = nullptr;
+      if (p.a.mask_bits && row_ok)
+        bits = p.a.mask_bits +
+               (w.b * p.a.mask_b + head * p.a.mask_h + token * p.a.mask_q) * p.a.mask_words;
+      float m = -INFINITY, mc = 0.f, l = 0.f;
+      for (int t = w.t0; t < w.t1; ++t) {
+        const int keys = w.tile_keys(t), cols = w.tile_cols(t);
+        uint32_t word[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (p.a.mask_bits) {
+          // A tile of kv_box keys starts inside a row of whole 128-key words
+          // only when it is the row's single tile (kv_box < 128).
+          uint4 q = make_uint4(0, 0, 0, 0);
+          if (bits) q = *reinterpret_cast<const uint4*>(bits + (t * p.kv_box >> 5));
+          word[0] = q.x; word[1] = q.y; word[2] = q.z; word[3] = q.w;
+        }
+        ok = wait(&bars.s_full[g], tiles & 1u, kAttnSoftmaxTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        if (p.a.mask_bits) {
+          // (After the wait: the products have read the tile before's by then.)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, word[i]);
+            if (lane == 0) bars.any[g][quarter][i] = any;
+          }
+        }
+        if (warp_ok) {
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c * 32 < cols) tmem_ld_x32(ts + c * 32, s + c * 32);
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c * 32 < cols) {
+              tmem_wait_ld_x32(s + c * 32);
+              uint32_t on = word[c];
+              const int rest = keys - c * 32;
+              if (rest < 32) on &= rest <= 0 ? 0u : (1u << rest) - 1u;
+              if (on != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((on >> i) & 1u)) s[c * 32 + i] = 0xFF800000u;  // -infinity
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[c * 32 + i]));
+            }
+          }
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          if (t == w.t0) {
+            m = mx;
+            mc = m == -INFINITY ? 0.f : m * c2;
+          } else {
+            const bool grown = (mx - m) * c2 > kRescaleLog2;  // (false for -inf - -inf = NaN)
+            if (__any_sync(0xFFFFFFFFu, grown)) {
+              float f = 1.f;
+              if (grown) {
+                const float next = mx * c2;
+                f = m == -INFINITY ? 0.f : exp2_approx(mc - next);
+                m = mx;
+                mc = next;
+                l *= f;
+              }
+              // The product of the tile before has to be done.
+              ok = wait(&bars.o_done[g], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < d; c += 32) {
+                uint32_t o[32];
+                tmem_ld_x32(to + c, o);
+                tmem_wait_ld_x32(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_x32(to + c, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          const uint64_t c22 = pack2(c2, c2), mc2 = pack2(-mc, -mc);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c * 32 < cols) {
+              uint32_t h[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(s[c * 32 + 2 * i]),
+                                   __uint_as_float(s[c * 32 + 2 * i + 1])),
+                             c22, mc2),
+                        x, y);
+                x = exp2_approx(x);
+                y = exp2_approx(y);
+                sum[i & 1] = add2(sum[i & 1], pack2(x, y));
+                h[i] = round2<T>(x, y);
+              }
+              tmem_st_x16(ts + c * 16, h);
+            }
+          }
+          float x, y;
+          unpack2(add2(sum[0], sum[1]), x, y);
+          l += x + y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[g]));
+        ++tiles;
+      }
+      if (ok) ok = wait(&bars.o_done[g], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
+      // The staging buffer's last store has been read; every warp agrees that
+      // the item is complete.
+      if (quarter == 0 && lane == 0) bulk_wait_read_all();
+      ok = barrier_all(bar_id, 128, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = !L::kSplit || (w.t0 == 0 && w.t1 == w.nt);
+      if (!whole) {
+        // A share of the row's keys: unnormalised, with its maximum and sum.
+        const long long slot = 2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+        if (warp_ok) {
+          float* dst = p.part_out + (slot * kAttnRows + r) * 128;
+#pragma unroll 1
+          for (int c = 0; c < d; c += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(to + c, o);
+            tmem_wait_ld_x32(o);
+            if (row_ok)
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                if (c + i < d)
+                  *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+          if (row_ok)
+            *reinterpret_cast<float2*>(p.part_stat + (slot * kAttnRows + r) * 2) =
+                make_float2(m == -INFINITY ? -INFINITY : mc, l);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.o_free[g]));
+        continue;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (p.a.lse && row_ok)
+        p.a.lse[(static_cast<long long>(w.b) * p.a.heads + head) * p.a.q_len + token] =
+            l == 0.f ? -INFINITY : fmaf(mc, kLn2, logf(l));
+      int token0, head0;
+      w.place(g, &token0, &head0);
+#pragma unroll 1
+      for (int blk = 0; blk < L::kBlocks; ++blk) {
+        if (blk * 64 >= d) break;
+        if (blk > 0) {
+          if (quarter == 0 && lane == 0) bulk_wait_read_all();
+          named_barrier(bar_id, 128);
+        }
+        if (warp_ok) {
+          uint32_t o[64];
+          tmem_ld_x32(to + blk * 64, o);
+          tmem_ld_x32(to + blk * 64 + 32, o + 32);
+          tmem_wait_ld_x32(o);
+          tmem_wait_ld_x32(o + 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              h[j] = round2<T>(__uint_as_float(o[i * 8 + 2 * j]) * inv,
+                               __uint_as_float(o[i * 8 + 2 * j + 1]) * inv);
+            // 16-byte words of a row sit at their index XOR the row's low bits (128-byte swizzle).
+            *reinterpret_cast<uint4*>(stage_out + r * 128 + ((i ^ (r & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        fence_proxy_async_shared();
+        if (blk == L::kBlocks - 1 || (blk + 1) * 64 >= d) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.o_free[g]));
+        }
+        named_barrier(bar_id, 128);
+        if (quarter == 0 && lane == 0) {
+          tma_store_4d(&p.map_out, smem_u32(stage_out), blk * 64, head0, token0, w.b);
+          bulk_commit_group();
+        }
+      }
+    }
+    // Shared memory stays until the last store has read it.
+    if (quarter == 0 && lane == 0) bulk_wait_read_all();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+}
+
+// Joins the shares of row tiles that a split launch cut, in order: one warp
+// per row, weights 2^(m_f - max m) over the shares' maxima.
+template <typename T>
+__global__ void __launch_bounds__(128)
+    attn_join_kernel(const __grid_constant__ AttnFwdParams p, int ctas) {
+  __shared__ long long sums[2][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const AttnShape& a = p.a;
+  const int b = static_cast<int>(blockIdx.x / p.item_rows);
+  const int item = static_cast<int>(blockIdx.x - b * p.item_rows);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  long long before, total;
+  split_prefix(a.batch, row_steps_uniform(p), b, sums, [&](int i) { return row_steps(p, i); },
+               &before, &total);
+  const int nt = key_tiles(valid_keys(a, b), p.kv_box);
+  const long long s0 = before + static_cast<long long>(item) * nt;
+  const int c0 = share_of(total, ctas, s0), c1 = share_of(total, ctas, s0 + nt - 1);
+  if (c0 == c1) return;  // written whole
+  const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
+  int token0, head0, rows;
+  if (p.tile_heads > 1) {
+    token0 = rt * p.tile_tokens;
+    head0 = hk * a.group;
+    rows = min(p.tile_tokens, a.q_len - token0) * p.tile_heads;
+  } else {
+    const int hg = rt / p.token_tiles;
+    token0 = (rt - hg * p.token_tiles) * kAttnRows;
+    head0 = hk * a.group + hg;
+    rows = min(kAttnRows, a.q_len - token0);
+  }
+  const int d0 = lane * 4;
+  for (int r = warp; r < rows; r += 4) {
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      if (share_begin(total, ctas, c) == share_begin(total, ctas, c + 1)) continue;  // no steps
+      const long long slot = 2ll * c + (c == c0 ? 1 : 0);
+      m = fmaxf(m, p.part_stat[(slot * kAttnRows + r) * 2]);
+    }
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+      if (share_begin(total, ctas, c) == share_begin(total, ctas, c + 1)) continue;
+      const long long row = (2ll * c + (c == c0 ? 1 : 0)) * kAttnRows + r;
+      const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
+      // A share whose pairs are all left out holds zeros.
+      const float f = st.x == -INFINITY && st.y == 0.f ? 0.f : exp2_approx(st.x - m);
+      l = fmaf(f, st.y, l);
+      if (d0 < a.head_dim) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_out + row * 128 + d0);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+    }
+    const int dt = p.tile_heads > 1 ? r / p.tile_heads : r;
+    const int token = token0 + dt, head = p.tile_heads > 1 ? head0 + r - dt * p.tile_heads : head0;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (d0 < a.head_dim) {
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<T*>(a.out_w) + b * a.os[0] +
+                                            token * a.os[1] + head * a.os[2] + d0);
+      *dst = make_uint2(round2<T>(acc.x * inv, acc.y * inv), round2<T>(acc.z * inv, acc.w * inv));
+    }
+    if (a.lse && lane == 0)
+      a.lse[(static_cast<long long>(b) * a.heads + head) * a.q_len + token] =
+          l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));
+  }
+}
+
+// Outputs of a call without keys.
+__global__ void __launch_bounds__(256) attn_no_keys_kernel(const AttnShape a) {
+  const long long rows = static_cast<long long>(a.batch) * a.q_len * a.heads;
+  const int words = a.head_dim / 8;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * words;
+       i += step) {
+    const long long row = i / words;
+    const int h = static_cast<int>(row % a.heads);
+    const long long bt = row / a.heads;
+    const long long b = bt / a.q_len, t = bt - b * a.q_len;
+    *reinterpret_cast<uint4*>(static_cast<__half*>(a.out_w) + b * a.os[0] + t * a.os[1] +
+                              h * a.os[2] + (i - row * words) * 8) = make_uint4(0, 0, 0, 0);
+    if (a.lse && i == row * words) a.lse[(b * a.heads + h) * a.q_len + t] = -INFINITY;
+  }
+}
+
+constexpr int kMaxDevices = 64;
+
+template <typename T, int DP, int G>
+cudaError_t launch_one(const AttnFwdParams& p, int grid, size_t smem, cudaStream_t stream) {
+  // The shared-memory limit is a per-device attribute: raise it once per
+  // device to the largest size asked for so far.
+  static std::atomic<size_t> configured[kMaxDevices];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (configured[dev].load(std::memory_order_relaxed) < smem) {
+    err = cudaFuncSetAttribute(attn_fwd_kernel<T, DP, G>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    configured[dev].store(smem, std::memory_order_relaxed);
+  }
+  return launch_pdl(attn_fwd_kernel<T, DP, G>, dim3(grid), dim3(G * 128 + 64), smem, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_type(const AttnFwdParams& p, bool split, int grid, size_t smem,
+                        cudaStream_t stream) {
+  const bool wide = p.a.head_dim > 64;
+  cudaError_t err;
+  if (!split)
+    return wide ? launch_one<T, 128, 2>(p, grid, smem, stream)
+                : launch_one<T, 64, 2>(p, grid, smem, stream);
+  err = wide ? launch_one<T, 128, 1>(p, grid, smem, stream)
+             : launch_one<T, 64, 1>(p, grid, smem, stream);
+  // Rows of one key tile are never cut.
+  if (err != cudaSuccess || p.a.kv_len <= p.kv_box) return err;
+  return launch_pdl(attn_join_kernel<T>, dim3(static_cast<unsigned>(p.item_rows * p.a.batch)),
+                    dim3(128), 0, stream, p, grid);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_no_keys(const AttnShape& a, cudaStream_t stream) {
+  const long long words = static_cast<long long>(a.batch) * a.q_len * a.heads * (a.head_dim / 8);
+  const int grid = static_cast<int>(words / 256 < 2048 ? words / 256 + 1 : 2048);
+  return launch_pdl(attn_no_keys_kernel, dim3(grid), dim3(256), 0, stream, a);
+}
+
+size_t attn_fwd_bar_bytes() { return sizeof(Bars); }
+
+cudaError_t launch_attn_fwd(const AttnFwdParams& p, bool split, int grid, size_t smem,
+                            cudaStream_t stream) {
+  return p.a.dtype == 0 ? launch_type<__nv_bfloat16>(p, split, grid, smem, stream)
+                        : launch_type<__half>(p, split, grid, smem, stream);
+}
+
+}  // namespace convgb300

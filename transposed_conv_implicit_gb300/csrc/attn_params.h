@@ -27,6 +27,85 @@ struct AttnShape {
   long long mask_b, mask_h, mask_q;
 };
 
+constexpr int kAttnRows = 128;  // rows of one MMA: TMEM lanes
+
+// Device status bits, as the convolutions' (1 producer, 2 MMA, 4 the rest).
+constexpr unsigned int kAttnProducerTimeout = 1u;
+constexpr unsigned int kAttnMmaTimeout = 2u;
+constexpr unsigned int kAttnSoftmaxTimeout = 4u;
+
+// Forward launch.  A row tile is up to 128 (token, head) rows of one key
+// head: 128 tokens of one head, or (packed) tile_tokens tokens of all its
+// query heads.
+struct AttnFwdParams {  // aligned like CUtensorMap
+  CUtensorMap map_q;    // {D, heads, tokens, batch}, box {64, tile_heads, tile_tokens, 1}
+  CUtensorMap map_k;    // {D, kv_heads, tokens, batch}, box {64, 1, kv_box, 1}
+  CUtensorMap map_v;
+  CUtensorMap map_out;  // as map_q
+  AttnShape a;
+  int q_mul[2], k_mul[2], v_mul[2];  // {head, batch} coordinate factors: 0 for broadcasts
+  int tile_heads, tile_tokens;
+  int token_tiles;      // tiles along the tokens
+  int row_tiles;        // row tiles of one key head
+  int kv_box;           // keys per tile (multiple of 16, <= 128)
+  int stages;           // key/value ring
+  int q_stages;
+  uint32_t off_q, off_kv, off_out, off_bar;  // shared-memory offsets
+  float scale_log2;     // scale * log2(e)
+  // One item per CTA step: two row tiles (pairs), or ranges of the sequence
+  // of (item, key tile) steps, cut evenly between the CTAs (split).
+  long long items;
+  long long item_rows;  // kv_heads * row_tiles: items of one batch (split)
+  float* part_out;      // split: [2 * grid][128][128] unnormalised rows
+  float* part_stat;     // split: [2 * grid][128][2]: maximum (log2 units), sum
+  unsigned int* status;
+  long long timeout_cycles;
+  int fault_mode;       // test hook: 1 = CTA 0 leaves its first key tile un-armed
+};
+
+size_t attn_fwd_bar_bytes();
+cudaError_t launch_attn_fwd(const AttnFwdParams& p, bool split, int grid, size_t smem,
+                            cudaStream_t stream);
+
+// Backward launches (attn_bwd.cu).  The dq kernel's row tiles are as the
+// forward pass's; the dk, dv kernel takes tiles of 128 tokens of one head.
+constexpr int kAttnNormBlocks = 2048;  // most blocks of each part of the rows kernel
+
+struct AttnBwdParams {  // aligned like CUtensorMap
+  CUtensorMap map_q, map_do;  // {D, heads, tokens, batch}, box by kernel
+  CUtensorMap map_k, map_v;   // {D, kv_heads, tokens, batch}, box {64, 1, kv_box, 1}
+  AttnShape a;
+  int q_mul[2], do_mul[2], k_mul[2], v_mul[2];
+  int tile_heads, tile_tokens, token_tiles, row_tiles;
+  int kv_box;           // keys per tile (multiple of 16, <= 128)
+  int q_box;            // dk, dv: tokens per box
+  int q_tiles;          // tiles of 128 tokens
+  int item_steps;       // dk, dv: group * q_tiles
+  long long item_rows;
+  int x_stages, y_stages;
+  uint32_t off_a, off_x, off_y, off_stat, off_mask, off_bar;
+  float scale_log2;
+  float p_shift, p_unscale;  // fp16: p is held times 2^p_shift; 2^-p_shift
+  float* stats;         // [batch][heads][q_tiles][2][128]
+  float* norms;         // fp16: row norms' maxima by block, else null
+  int row_blocks, value_blocks;  // blocks of the rows kernel
+  float* part_q;        // [2 * CTAs][128][128]
+  float* part_kv;       // [2 * CTAs][2][128][128]
+  unsigned int* status;
+  long long timeout_cycles;
+  int fault_mode;
+};
+
+size_t attn_bwd_bar_bytes();
+cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t stream);
+cudaError_t launch_attn_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_attn_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream);
+cudaError_t launch_attn_bwd_join(const AttnBwdParams& p, int q_ctas, int kv_ctas,
+                                 long long q_blocks, long long kv_blocks, cudaStream_t stream);
+
+// Without keys: zeros to out (batch, q_len, heads rows) and -inf to lse.
+cudaError_t launch_attn_no_keys(const AttnShape& a, cudaStream_t stream);
+
 // Packs the byte mask into AttnShape::mask_bits (batches x heads x queries
 // rows, extents after broadcasting).
 cudaError_t launch_mask_pack(const unsigned char* mask, const long long stride[4], int batches,
