@@ -208,16 +208,6 @@ conv_status_t channel_block(int c_in, int elt, int* bk, uint32_t* row_bytes) {
   return CONV_OK;
 }
 
-FastDiv make_fast_div(uint32_t d) {
-  FastDiv f{};
-  f.d = d;
-  uint32_t s = 0;
-  while ((1ull << s) < d) ++s;
-  f.shift = s;
-  f.mul = static_cast<uint32_t>((((1ull << 32) * ((1ull << s) - d)) / d + 1) & 0xFFFFFFFFull);
-  return f;
-}
-
 // Forward convs whose channel rows a TMA box cannot address (C_in * elt not
 // a multiple of 16 bytes, or under 32) use the gather A loader.  Its
 // contraction layout: per filter row r one run of S taps x C_in channels

@@ -61,12 +61,6 @@ struct TileInfo {
   int kblocks;  // k-blocks in this tile's contraction
 };
 
-// x / f.d for 0 <= x < 2^31 (see FastDiv).
-__device__ __forceinline__ int fast_div(int x, const FastDiv& f) {
-  const uint32_t u = static_cast<uint32_t>(x);
-  return static_cast<int>((static_cast<uint64_t>(__umulhi(u, f.mul)) + u) >> f.shift);
-}
-
 __device__ __forceinline__ TileInfo decode_tile(const ConvKernelParams& p, int t) {
   if (p.window) {  // one C_out tile; m0 carries the tile index
     TileInfo ti;

@@ -41,6 +41,24 @@ struct FastDiv {
   uint32_t d, mul, shift;
 };
 
+inline FastDiv make_fast_div(uint32_t d) {
+  FastDiv f{};
+  f.d = d;
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  f.shift = s;
+  f.mul = static_cast<uint32_t>((((1ull << 32) * ((1ull << s) - d)) / d + 1) & 0xFFFFFFFFull);
+  return f;
+}
+
+#ifdef __CUDACC__
+// x / f.d for 0 <= x < 2^31 (see FastDiv).
+__device__ __forceinline__ int fast_div(int x, const FastDiv& f) {
+  const uint32_t u = static_cast<uint32_t>(x);
+  return static_cast<int>((static_cast<uint64_t>(__umulhi(u, f.mul)) + u) >> f.shift);
+}
+#endif
+
 struct ConvKernelParams {  // aligned like CUtensorMap (64 B or more)
   CUtensorMap map_a[kMaxPhases];  // im2col maps over the NHWC input, one per phase
   CUtensorMap map_b;              // tiled map over the packed filter [phase][C_out][K]

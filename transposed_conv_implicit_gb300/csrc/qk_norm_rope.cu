@@ -23,7 +23,8 @@
 
 #include "../../include/conv_gb300_attention.h"
 #include "attn_internal.h"
-#include "ptx.cuh"
+#include "conv_params.h"
+#include "attn_ptx.cuh"
 
 namespace convgb300 {
 
@@ -31,8 +32,10 @@ namespace {
 
 constexpr int kThreadsQn = 256;
 constexpr int kWarpsQn = kThreadsQn / 32;
-constexpr int kUnroll = 4;          // rows in flight per lane
-constexpr int kMaxBlocksQn = 8;     // per SM: 2048 resident threads
+// Rows in flight per lane: the backward pass holds two tensors and their
+// product for each.
+constexpr int kUnrollFwd = 4, kUnrollBwd = 2;
+constexpr int kBlocksFwd = 3, kBlocksBwd = 3;  // thread blocks per SM (launch bounds)
 
 struct QnTensor {
   const void* x;
@@ -45,12 +48,12 @@ struct QnTensor {
   int weight_f32;
   int length, heads;
   int blocks;      // thread blocks that share this tensor's rows
-  int slots_heads; // heads side by side in a warp (many heads: the slots; else all heads)
   int units_per_token;
-  long long tokens;  // batch * length
-  long long units;
+  int rows;          // batch * length * heads
+  int many, units;
+  FastDiv div_upt, div_length, div_heads;
   long long position_stride;
-  long long xs[3], ds[3], ys[3];  // batch, token, head
+  uint32_t xs[3], ds[3], ys[3];  // batch, token, head; in 8 elements
 };
 
 struct QnParams {
@@ -85,117 +88,162 @@ struct Pair<__half> {
   }
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const void* base, long long off, float (&v)[V]) {
-  const T* p = static_cast<const T*>(base) + off;
+// V elements of a row as loaded, and as fp32 pairs.
+template <int V>
+struct Raw {
   uint32_t w[V / 2];
-  if (V == 8) {
+};
+template <int V>
+struct Pairs {
+  uint64_t v[V / 2];
+};
+
+template <int V>
+__device__ __forceinline__ Raw<V> load_raw(const uint16_t* p) {
+  Raw<V> r;
+  if constexpr (V == 8) {
     const uint4 u = *reinterpret_cast<const uint4*>(p);
-    w[0] = u.x; w[1] = u.y; w[V / 2 - 2] = u.z; w[V / 2 - 1] = u.w;
+    r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
   } else {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
-    w[0] = u.x; w[1] = u.y;
+    r.w[0] = u.x; r.w[1] = u.y;
   }
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    const float2 f = Pair<T>::load(w[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
+  return r;
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void store_row(void* base, long long off, const float (&v)[V]) {
-  T* p = static_cast<T*>(base) + off;
+__device__ __forceinline__ Pairs<V> widen(const Raw<V>& r) {
+  Pairs<V> o;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const float2 f = Pair<T>::load(r.w[i]);
+    o.v[i] = pack2(f.x, f.y);
+  }
+  return o;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_row(uint16_t* p, const Pairs<V>& v) {
   uint32_t w[V / 2];
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) w[i] = Pair<T>::store(v[2 * i], v[2 * i + 1]);
-  if (V == 8)
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[V / 2 - 2], w[V / 2 - 1]);
+  for (int i = 0; i < V / 2; ++i) {
+    float x, y;
+    unpack2(v.v[i], x, y);
+    w[i] = Pair<T>::store(x, y);
+  }
+  if constexpr (V == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   else
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-// Sum over the `lanes` lanes of a row (lane `at` of it), given to all of
-// them.  Rows need not fill a power of two: lanes past the end add nothing.
-__device__ __forceinline__ float row_sum(float v, int lanes, int at, int first) {
+// The pairs' other members: the lane's own words the other way round
+// (adjacent), or those of lane `other`.  Every lane of the warp takes part.
+template <typename T, int V, bool kAdjacent>
+__device__ __forceinline__ Pairs<V> partners(const Raw<V>& r, const Pairs<V>& own, int other) {
+  if constexpr (kAdjacent) {
+    Pairs<V> q;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      float x, y;
+      unpack2(own.v[i], x, y);
+      q.v[i] = pack2(y, x);
+    }
+    return q;
+  } else {
+    Raw<V> q;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) q.w[i] = __shfl_sync(0xFFFFFFFFu, r.w[i], other);
+    return widen<T, V>(q);
+  }
+}
+
+// Sums over the `lanes` lanes of a row (lane `at` of it), given to all of
+// them, for kUnroll rows at once.  Rows need not fill a power of two: lanes
+// past the end add nothing.
+template <int kUnroll>
+__device__ __forceinline__ void row_sums(float (&v)[kUnroll], int lanes, int at, int first) {
+  if ((lanes & (lanes - 1)) == 0) {
+    for (int step = lanes >> 1; step > 0; step >>= 1)
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) v[u] += __shfl_xor_sync(0xFFFFFFFFu, v[u], step);
+    return;
+  }
   int step = 16;
   while (step >= lanes) step >>= 1;
   for (; step > 0; step >>= 1) {
-    const float o = __shfl_down_sync(0xFFFFFFFFu, v, step);
-    if (at + step < lanes && at < step) v += o;
+    const bool adds = at + step < lanes && at < step;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const float o = __shfl_down_sync(0xFFFFFFFFu, v[u], step);
+      if (adds) v[u] += o;
+    }
   }
-  return __shfl_sync(0xFFFFFFFFu, v, first);
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) v[u] = __shfl_sync(0xFFFFFFFFu, v[u], first);
 }
 
-// The lane's angles: cos[] and sin[] of its V/2 pairs (adjacent), or of its V
-// elements, the second half's sine negated (halves), so that
-//   turned = x * c - partner * s.
-template <int V>
-__device__ __forceinline__ void load_angles(const QnParams& p, const QnTensor& t, long long token,
-                                            int e0, float (&c)[V], float (&s)[V]) {
-  const long long b = token / t.length;
-  const int l = static_cast<int>(token - b * t.length);
+// 1/sqrt(x): the hardware's approximation and one Newton step.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  return r * fmaf(-0.5f * x * r, r, 1.5f);
+}
+
+// The lane's angles for a token: each of its elements x turns into
+//   x * c - partner * s
+// (the sine of a pair's second member is negated).  Lanes that are not
+// rotated have c = 1, s = 0.
+template <int V, bool kAdjacent>
+__device__ __forceinline__ void load_angles(const QnParams& p, const QnTensor& t, int b, int l,
+                                            int e0, bool rotated, Pairs<V>& c, Pairs<V>& s) {
+  if (!rotated) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      c.v[i] = pack2(1.f, 1.f);
+      s.v[i] = 0;
+    }
+    return;
+  }
   int pos = t.positions ? t.positions[b * t.position_stride + l] : l;
   pos = max(0, min(pos, p.table_rows - 1));
   const int half = p.rot >> 1;
-  const long long row = static_cast<long long>(pos) * half;
-  if (p.adjacent) {
+  const uint64_t row = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * static_cast<uint32_t>(half);
+  if constexpr (kAdjacent) {
     const float4 fc = *reinterpret_cast<const float4*>(p.cos + row + (e0 >> 1));
     const float4 fs = *reinterpret_cast<const float4*>(p.sin + row + (e0 >> 1));
     const float cc[4] = {fc.x, fc.y, fc.z, fc.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      c[i] = cc[(i >> 1) & 3];
-      s[i] = (i & 1) ? -ss[(i >> 1) & 3] : ss[(i >> 1) & 3];
+    for (int i = 0; i < V / 2; ++i) {
+      c.v[i] = pack2(cc[i & 3], cc[i & 3]);
+      s.v[i] = pack2(ss[i & 3], -ss[i & 3]);
     }
-    return;
-  }
-  const bool second = e0 >= half;
-  const long long at = row + (second ? e0 - half : e0);
-#pragma unroll
-  for (int i = 0; i < V; i += 4) {
-    const float4 fc = *reinterpret_cast<const float4*>(p.cos + at + i);
-    const float4 fs = *reinterpret_cast<const float4*>(p.sin + at + i);
-    c[i] = fc.x; c[i + 1] = fc.y; c[i + 2] = fc.z; c[i + 3] = fc.w;
-    s[i] = fs.x; s[i + 1] = fs.y; s[i + 2] = fs.z; s[i + 3] = fs.w;
-  }
-  if (second) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = -s[i];
-  }
-}
-
-// v turned by the angles (sign +1) or back (-1).  Every lane of the warp
-// takes part: the pair's other member comes from lane `other`.
-template <int V>
-__device__ __forceinline__ void turn(const QnParams& p, bool rotated, int other, float sign,
-                                     const float (&c)[V], const float (&s)[V], float (&v)[V]) {
-  float q[V];
-  if (p.adjacent) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) q[i] = v[i ^ 1];
   } else {
+    const bool second = e0 >= half;
+    const uint64_t at = row + (second ? e0 - half : e0);
+    const float sign = second ? -1.f : 1.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) q[i] = __shfl_sync(0xFFFFFFFFu, v[i], other);
-  }
-  if (rotated) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = v[i] * c[i] - sign * (q[i] * s[i]);
+    for (int i = 0; i < V; i += 4) {
+      const float4 fc = *reinterpret_cast<const float4*>(p.cos + at + i);
+      const float4 fs = *reinterpret_cast<const float4*>(p.sin + at + i);
+      c.v[i / 2] = pack2(fc.x, fc.y);
+      c.v[i / 2 + 1] = pack2(fc.z, fc.w);
+      s.v[i / 2] = pack2(fs.x * sign, fs.y * sign);
+      s.v[i / 2 + 1] = pack2(fs.z * sign, fs.w * sign);
+    }
   }
 }
 
-// kMany: at least as many heads as row slots in a warp; the unit's rows are
-// heads of one token.  Otherwise a warp's slots take all heads of several
-// tokens.
-template <typename T, int V, bool kBackward>
-__global__ void __launch_bounds__(kThreadsQn)
-    qk_norm_rope_kernel(const __grid_constant__ QnParams p) {
-  __shared__ float red[kWarpsQn][256];
+__device__ __forceinline__ uint64_t offset8(uint32_t i, uint32_t stride8) {
+  return static_cast<uint64_t>(i) * stride8;
+}
+
+// kMany: a unit's rows are heads of one token, which share its angles.
+// Otherwise they are consecutive (token, head) rows, each with its own.
+template <typename T, int V, bool kAdjacent, bool kBackward, bool kMany>
+__device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, int block,
+                                          const float (*weight)[256], float (*red)[256]) {
+  constexpr int kUnroll = kBackward ? kUnrollBwd : kUnrollFwd;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool is_k = blockIdx.x >= static_cast<unsigned>(p.t[0].blocks);
-  const QnTensor& t = p.t[is_k ? 1 : 0];
-  const int block = is_k ? blockIdx.x - p.t[0].blocks : blockIdx.x;
   const int slot = lane / p.lanes;
   const int at = lane - slot * p.lanes;
   const int first = slot * p.lanes;
@@ -203,118 +251,193 @@ __global__ void __launch_bounds__(kThreadsQn)
   const int e0 = at * V;
   const int half = p.rot >> 1;
   const bool rotated = live && e0 < p.rot;
-  const int other = rotated ? first + (e0 >= half ? at - half / V : at + half / V) : lane;
-  const bool many = t.heads >= p.slots;
-  grid_dependency_wait();
+  const int other = rotated && !kAdjacent ? first + (e0 >= half ? at - half / V : at + half / V) : lane;
+  const uint16_t* px = static_cast<const uint16_t*>(t.x) + e0;
+  const uint16_t* pg = static_cast<const uint16_t*>(t.dy) + e0;
+  uint16_t* py = static_cast<uint16_t*>(t.y) + e0;
+  const uint64_t* w0 = reinterpret_cast<const uint64_t*>(weight[0] + e0);
+  const uint64_t* w1 = reinterpret_cast<const uint64_t*>(weight[1] + e0);
+  Pairs<V> dw;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) dw.v[i] = 0;
 
-  float w[V];
+  // The angles of a token; forward, with the weights in them.
+  auto angles = [&](int b, int l, Pairs<V>& c, Pairs<V>& s) {
+    load_angles<V, kAdjacent>(p, t, b, l, e0, rotated, c, s);
+    if constexpr (!kBackward) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) w[i] = 0.f;
-  if (live) {
-    if (t.weight_f32) {
-      const float* wp = static_cast<const float*>(t.weight) + e0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) w[i] = wp[i];
-    } else {
-      load_row<T, V>(t.weight, e0, w);
+      for (int i = 0; i < V / 2; ++i) {
+        c.v[i] = mul2(c.v[i], w0[i]);
+        s.v[i] = mul2(s.v[i], w1[i]);
+      }
     }
-  }
-  float dw[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) dw[i] = 0.f;
-
-  const long long step = static_cast<long long>(t.blocks) * kWarpsQn;
-  for (long long unit = static_cast<long long>(block) * kWarpsQn + warp; unit < t.units;
-       unit += step) {
-    float x[kUnroll][V], g[kUnroll][V], c[V], s[V];
-    long long token[kUnroll];
-    int head[kUnroll];
+  };
+  const uint64_t head_step = offset8(p.slots, t.ys[2]);  // to the next row's head (kMany)
+  const int step = t.blocks * kWarpsQn;
+  for (int unit = block * kWarpsQn + warp; unit < t.units; unit += step) {
+    Raw<V> x[kUnroll], g[kUnroll];
+    Pairs<V> c, s;
+    int b[kUnroll], l[kUnroll];
+    uint64_t oy[kMany ? 1 : kUnroll];
     bool ok[kUnroll];
-    // Which rows: fixed token and heads slot, slot + slots, ..., or all heads
-    // of tokens token0 + slot / heads, ...
-    if (many) {
-      const long long tk = unit / t.units_per_token;
-      const int h0 = static_cast<int>(unit - tk * t.units_per_token) * p.slots * kUnroll + slot;
+    if constexpr (kMany) {
+      const int token = fast_div(unit, t.div_upt);
+      const int h0 = (unit - token * t.units_per_token) * p.slots * kUnroll + slot;
+      b[0] = fast_div(token, t.div_length);
+      l[0] = token - b[0] * t.length;
+      uint64_t ox = offset8(b[0], t.xs[0]) + offset8(l[0], t.xs[1]) + offset8(h0, t.xs[2]);
+      uint64_t og = offset8(b[0], t.ds[0]) + offset8(l[0], t.ds[1]) + offset8(h0, t.ds[2]);
+      oy[0] = offset8(b[0], t.ys[0]) + offset8(l[0], t.ys[1]) + offset8(h0, t.ys[2]);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        token[u] = tk;
-        head[u] = h0 + u * p.slots;
-        ok[u] = live && head[u] < t.heads;
+        ok[u] = live && h0 + u * p.slots < t.heads;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) x[u].w[i] = g[u].w[i] = 0u;
+        if (ok[u]) {
+          x[u] = load_raw<V>(px + ox * 8);
+          if constexpr (kBackward) g[u] = load_raw<V>(pg + og * 8);
+        }
+        ox += offset8(p.slots, t.xs[2]);
+        og += offset8(p.slots, t.ds[2]);
+      }
+      angles(b[0], l[0], c, s);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int row = (unit * kUnroll + u) * p.slots + slot;
+        const int token = fast_div(row, t.div_heads);
+        const int head = row - token * t.heads;
+        b[u] = fast_div(token, t.div_length);
+        l[u] = token - b[u] * t.length;
+        ok[u] = live && row < t.rows;
+        oy[u] = offset8(b[u], t.ys[0]) + offset8(l[u], t.ys[1]) + offset8(head, t.ys[2]);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) x[u].w[i] = g[u].w[i] = 0u;
+        if (ok[u]) {
+          x[u] = load_raw<V>(px + (offset8(b[u], t.xs[0]) + offset8(l[u], t.xs[1]) +
+                                   offset8(head, t.xs[2])) * 8);
+          if constexpr (kBackward)
+            g[u] = load_raw<V>(pg + (offset8(b[u], t.ds[0]) + offset8(l[u], t.ds[1]) +
+                                     offset8(head, t.ds[2])) * 8);
+        } else {
+          b[u] = l[u] = 0;
+        }
+      }
+    }
+    float r[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const Pairs<V> v = widen<T, V>(x[u]);
+      uint64_t sq = mul2(v.v[0], v.v[0]);
+#pragma unroll
+      for (int i = 1; i < V / 2; ++i) sq = fma2(v.v[i], v.v[i], sq);
+      float lo, hi;
+      unpack2(sq, lo, hi);
+      r[u] = lo + hi;
+    }
+    row_sums(r, p.lanes, at, first);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) r[u] = inverse_root(fmaf(r[u], p.inv_d, p.eps));
+    if constexpr (!kBackward) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if constexpr (!kMany) angles(b[u], l[u], c, s);
+        Pairs<V> v = widen<T, V>(x[u]);
+        const Pairs<V> q = partners<T, V, kAdjacent>(x[u], v, other);
+        const uint64_t rr = pack2(r[u], r[u]), mr = pack2(-r[u], -r[u]);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i)
+          v.v[i] = fma2(mul2(q.v[i], s.v[i]), mr, mul2(mul2(v.v[i], c.v[i]), rr));
+        if (ok[u]) store_row<T, V>(py + (kMany ? oy[0] + u * head_step : oy[u]) * 8, v);
       }
     } else {
-      const int side = slot / t.heads;            // which of the warp's tokens
-      const int tokens = p.slots / t.heads;       // tokens side by side
+      float dot[kUnroll];
+      Pairs<V> gw[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        token[u] = (unit * kUnroll + u) * tokens + side;
-        head[u] = slot - side * t.heads;
-        ok[u] = live && side < tokens && token[u] < t.tokens;
-      }
-    }
-    long long off_y[kUnroll];
+        if constexpr (!kMany) angles(b[u], l[u], c, s);
+        const Pairs<V> own = widen<T, V>(g[u]);
+        const Pairs<V> q = partners<T, V, kAdjacent>(g[u], own, other);
+        const Pairs<V> v = widen<T, V>(x[u]);
+        const uint64_t rr = pack2(r[u], r[u]);
+        uint64_t sum = 0;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      off_y[u] = 0;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[u][i] = 0.f;
-        g[u][i] = 0.f;
-      }
-      if (ok[u]) {
-        const long long b = token[u] / t.length, l = token[u] - b * t.length;
-        off_y[u] = b * t.ys[0] + l * t.ys[1] + head[u] * t.ys[2] + e0;
-        load_row<T, V>(t.x, b * t.xs[0] + l * t.xs[1] + head[u] * t.xs[2] + e0, x[u]);
-        if (kBackward)
-          load_row<T, V>(t.dy, b * t.ds[0] + l * t.ds[1] + head[u] * t.ds[2] + e0, g[u]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (rotated && ok[u] && (u == 0 || !many)) load_angles<V>(p, t, token[u], e0, c, s);
-      float sq = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) sq = fmaf(x[u][i], x[u][i], sq);
-      sq = row_sum(sq, p.lanes, at, first);
-      const float r = 1.0f / sqrtf(fmaf(sq, p.inv_d, p.eps));
-      if (!kBackward) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[u][i] = x[u][i] * r * w[i];
-        turn<V>(p, rotated, other, 1.f, c, s, x[u]);
-        if (ok[u]) store_row<T, V>(t.y, off_y[u], x[u]);
-      } else {
-        turn<V>(p, rotated, other, -1.f, c, s, g[u]);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          x[u][i] *= r;                                // the normed row
-          if (ok[u]) dw[i] = fmaf(g[u][i], x[u][i], dw[i]);
-          g[u][i] *= w[i];
-          dot = fmaf(g[u][i], x[u][i], dot);
+        for (int i = 0; i < V / 2; ++i) {
+          const uint64_t back = fma2(q.v[i], s.v[i], mul2(own.v[i], c.v[i]));  // turned back
+          const uint64_t xhat = mul2(v.v[i], rr);                             // the normed row
+          dw.v[i] = fma2(back, xhat, dw.v[i]);  // (rows left out hold zeros)
+          gw[u].v[i] = mul2(back, w0[i]);
+          sum = fma2(gw[u].v[i], xhat, sum);
         }
-        dot = row_sum(dot, p.lanes, at, first) * p.inv_d;
+        float lo, hi;
+        unpack2(sum, lo, hi);
+        dot[u] = lo + hi;
+      }
+      row_sums(dot, p.lanes, at, first);
 #pragma unroll
-        for (int i = 0; i < V; ++i) g[u][i] = r * (g[u][i] - x[u][i] * dot);
-        if (ok[u]) store_row<T, V>(t.y, off_y[u], g[u]);
+      for (int u = 0; u < kUnroll; ++u) {
+        Pairs<V> v = widen<T, V>(x[u]);
+        const float f = -dot[u] * p.inv_d * r[u];
+        const uint64_t rr = pack2(r[u], r[u]), ff = pack2(f, f);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) v.v[i] = mul2(rr, fma2(v.v[i], ff, gw[u].v[i]));
+        if (ok[u]) store_row<T, V>(py + (kMany ? oy[0] + u * head_step : oy[u]) * 8, v);
       }
     }
   }
-  grid_launch_dependents();
-  if (!kBackward) return;
-  // The block's share of dw: slots of a warp, then warps, in order.
-  for (int sl = 0; sl < p.slots; ++sl) {
-    if (slot == sl) {
+  if constexpr (kBackward) {
+    // The block's share of dw: slots of a warp, then warps, in order.
+    for (int sl = 0; sl < p.slots; ++sl) {
+      if (slot == sl) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) red[warp][e0 + i] = dw[i] + (sl ? red[warp][e0 + i] : 0.f);
+        for (int i = 0; i < V / 2; ++i) {
+          float x, y;
+          unpack2(dw.v[i], x, y);
+          red[warp][e0 + 2 * i] = x + (sl ? red[warp][e0 + 2 * i] : 0.f);
+          red[warp][e0 + 2 * i + 1] = y + (sl ? red[warp][e0 + 2 * i + 1] : 0.f);
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
+    __syncthreads();
+    for (int d = threadIdx.x; d < p.head_dim; d += kThreadsQn) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarpsQn; ++i) sum += red[i][d];
+      t.partial[static_cast<long long>(block) * p.head_dim + d] = sum;
+    }
+  }
+}
+
+template <typename T, int V, bool kAdjacent, bool kBackward>
+__global__ void __launch_bounds__(kThreadsQn, kBackward ? kBlocksBwd : kBlocksFwd)
+    qk_norm_rope_kernel(const __grid_constant__ QnParams p) {
+  __shared__ __align__(16) float weight[2][256];
+  __shared__ float red[kBackward ? kWarpsQn : 1][256];
+  const bool is_k = blockIdx.x >= static_cast<unsigned>(p.t[0].blocks);
+  const QnTensor& t = p.t[is_k ? 1 : 0];
+  const int block = is_k ? blockIdx.x - p.t[0].blocks : blockIdx.x;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // The weights, and those of each element's partner.
+  for (int e = threadIdx.x; e < 256; e += kThreadsQn) {
+    int far = e;
+    if (e < p.rot) far = kAdjacent ? e ^ 1 : e < (p.rot >> 1) ? e + (p.rot >> 1) : e - (p.rot >> 1);
+    float w[2] = {0.f, 0.f};
+    if (e < p.head_dim) {
+      w[0] = t.weight_f32 ? static_cast<const float*>(t.weight)[e]
+                          : Pair<T>::load(static_cast<const uint16_t*>(t.weight)[e]).x;
+      w[1] = t.weight_f32 ? static_cast<const float*>(t.weight)[far]
+                          : Pair<T>::load(static_cast<const uint16_t*>(t.weight)[far]).x;
+    }
+    weight[0][e] = w[0];
+    weight[1][e] = w[1];
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < p.head_dim; d += kThreadsQn) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kWarpsQn; ++i) sum += red[i][d];
-    t.partial[static_cast<long long>(block) * p.head_dim + d] = sum;
-  }
+  if (t.many)
+    norm_rows<T, V, kAdjacent, kBackward, true>(p, t, block, weight, red);
+  else
+    norm_rows<T, V, kAdjacent, kBackward, false>(p, t, block, weight, red);
 }
 
 // dw = the blocks' shares, summed in a fixed order: one thread block per
@@ -357,12 +480,15 @@ bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) !
 
 // Fills one tensor's strides, with those of dimensions of extent 1 cleared.
 conv_status_t take_strides(const long long in[3], int batch, int length, int heads, bool output,
-                           long long out[3]) {
+                           uint32_t out[3]) {
   const int extent[3] = {batch, length, heads};
   for (int i = 0; i < 3; ++i) {
-    out[i] = extent[i] > 1 ? in[i] : 0;
-    if (extent[i] > 1 && output && in[i] == 0) return CONV_ERR_INVALID_VALUE;
-    if (out[i] % 8 != 0) return CONV_ERR_MISALIGNED;
+    out[i] = 0;
+    if (extent[i] <= 1) continue;
+    if (in[i] < 0 || (output && in[i] == 0)) return CONV_ERR_INVALID_VALUE;
+    if (in[i] % 8 != 0) return CONV_ERR_MISALIGNED;
+    if (in[i] / 8 > 0xFFFFFFFFll) return CONV_ERR_NOT_SUPPORTED;
+    out[i] = static_cast<uint32_t>(in[i] / 8);
   }
   return CONV_OK;
 }
@@ -400,23 +526,24 @@ conv_status_t take_tensor(const qk_norm_rope_args_t& a, const qk_norm_rope_tenso
   t->dweight = in.dweight;
   t->length = in.length;
   t->heads = in.heads;
-  t->tokens = static_cast<long long>(a.batch) * in.length;
+  const long long tokens = static_cast<long long>(a.batch) * in.length;
+  if (tokens * in.heads > 0x7FFF0000ll) return CONV_ERR_NOT_SUPPORTED;  // rows count in 31 bits
+  t->rows = static_cast<int>(tokens * in.heads);
   return CONV_OK;
 }
 
-template <typename T, int V, bool kBackward>
-cudaError_t launch_qn(const QnParams& p, int grid, cudaStream_t stream) {
-  return launch_pdl(qk_norm_rope_kernel<T, V, kBackward>, dim3(grid), dim3(kThreadsQn), 0, stream,
-                    p);
+template <typename T, bool kBackward>
+cudaError_t launch_qn(const QnParams& p, int v, int grid, cudaStream_t stream) {
+  const dim3 g(grid), b(kThreadsQn);
+  if (p.adjacent) return launch_pdl(qk_norm_rope_kernel<T, 8, true, kBackward>, g, b, 0, stream, p);
+  if (v == 8) return launch_pdl(qk_norm_rope_kernel<T, 8, false, kBackward>, g, b, 0, stream, p);
+  return launch_pdl(qk_norm_rope_kernel<T, 4, false, kBackward>, g, b, 0, stream, p);
 }
 
 template <bool kBackward>
 cudaError_t launch_qn_dtype(int dtype, int v, const QnParams& p, int grid, cudaStream_t stream) {
-  if (dtype == CONV_DTYPE_BF16)
-    return v == 8 ? launch_qn<__nv_bfloat16, 8, kBackward>(p, grid, stream)
-                  : launch_qn<__nv_bfloat16, 4, kBackward>(p, grid, stream);
-  return v == 8 ? launch_qn<__half, 8, kBackward>(p, grid, stream)
-                : launch_qn<__half, 4, kBackward>(p, grid, stream);
+  return dtype == CONV_DTYPE_BF16 ? launch_qn<__nv_bfloat16, kBackward>(p, v, grid, stream)
+                                  : launch_qn<__half, kBackward>(p, v, grid, stream);
 }
 
 conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, void* workspace,
@@ -460,24 +587,27 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
   p.inv_d = 1.0f / static_cast<float>(a.head_dim);
   long long units = 0;
   for (QnTensor& t : p.t) {
-    if (!t.x || t.tokens == 0) continue;
-    if (t.heads >= p.slots) {
-      t.units_per_token = (t.heads + p.slots * kUnroll - 1) / (p.slots * kUnroll);
-      t.units = t.tokens * t.units_per_token;
-    } else {
-      const long long rows = static_cast<long long>(p.slots / t.heads) * kUnroll;
-      t.units = (t.tokens + rows - 1) / rows;
-    }
+    if (!t.x || t.rows == 0) continue;
+    // One token to a unit where its heads fill most of the unit's rows (the
+    // angles are then read once for all of them); else rows back to back.
+    const int unit_rows = p.slots * (backward ? kUnrollBwd : kUnrollFwd);
+    t.units_per_token = (t.heads + unit_rows - 1) / unit_rows;
+    t.many = 4 * t.heads >= 3 * t.units_per_token * unit_rows;
+    t.units = t.many ? t.rows / t.heads * t.units_per_token : (t.rows + unit_rows - 1) / unit_rows;
+    t.div_heads = make_fast_div(static_cast<uint32_t>(t.heads));
+    t.div_upt = make_fast_div(static_cast<uint32_t>(t.units_per_token));
+    t.div_length = make_fast_div(static_cast<uint32_t>(t.length));
     units += t.units;
   }
   // The grid fills the SMs once; the two tensors share the blocks in
   // proportion to their units.
-  const long long most = static_cast<long long>(sms) * kMaxBlocksQn;
+  const long long most = static_cast<long long>(sms) * (backward ? kBlocksBwd : kBlocksFwd);
   int grid = 0;
   for (QnTensor& t : p.t) {
     if (t.units == 0) continue;
     const long long want = (t.units + kWarpsQn - 1) / kWarpsQn;
-    long long share = units <= most * kWarpsQn ? want : std::max(1ll, (most - 1) * t.units / units);
+    const long long share =
+        units <= most * kWarpsQn ? want : std::max(1ll, (most - 1) * t.units / units);
     t.blocks = static_cast<int>(std::min(want, share));
     grid += t.blocks;
   }
@@ -506,7 +636,7 @@ size_t qk_norm_rope_workspace_size(int head_dim) {
   if (head_dim <= 0 || sms <= 0) return 0;
   // One row of partial sums per thread block.
   return CONV_STATUS_BYTES +
-         static_cast<size_t>(sms) * convgb300::kMaxBlocksQn * head_dim * sizeof(float);
+         static_cast<size_t>(sms) * convgb300::kBlocksBwd * head_dim * sizeof(float);
 }
 
 conv_status_t qk_norm_rope_fwd(const qk_norm_rope_args_t* args, void* stream) {
