@@ -1239,23 +1239,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-constexpr int kMaxDevices = 64;
-
-template <typename K>
-cudaError_t raise_smem(K kernel, std::atomic<size_t>* configured, size_t smem) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (configured[dev].load(std::memory_order_relaxed) < smem) {
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-    configured[dev].store(smem, std::memory_order_relaxed);
-  }
-  return cudaSuccess;
-}
-
 template <typename T, int DP>
 cudaError_t launch_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
   static std::atomic<size_t> configured[kMaxDevices];

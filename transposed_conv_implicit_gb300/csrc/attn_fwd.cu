@@ -668,23 +668,11 @@ __global__ void __launch_bounds__(256) attn_no_keys_kernel(const AttnShape a) {
   }
 }
 
-constexpr int kMaxDevices = 64;
-
 template <typename T, int DP, int G>
 cudaError_t launch_one(const AttnFwdParams& p, int grid, size_t smem, cudaStream_t stream) {
-  // The shared-memory limit is a per-device attribute: raise it once per
-  // device to the largest size asked for so far.
   static std::atomic<size_t> configured[kMaxDevices];
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  const cudaError_t err = raise_smem(attn_fwd_kernel<T, DP, G>, configured, smem);
   if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (configured[dev].load(std::memory_order_relaxed) < smem) {
-    err = cudaFuncSetAttribute(attn_fwd_kernel<T, DP, G>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-    configured[dev].store(smem, std::memory_order_relaxed);
-  }
   return launch_pdl(attn_fwd_kernel<T, DP, G>, dim3(grid), dim3(G * 128 + 64), smem, stream, p);
 }
 

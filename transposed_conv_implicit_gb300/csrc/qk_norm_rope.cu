@@ -18,6 +18,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -30,12 +31,12 @@ namespace convgb300 {
 
 namespace {
 
-constexpr int kThreadsQn = 256;
+constexpr int kThreadsQn = 128;
 constexpr int kWarpsQn = kThreadsQn / 32;
-// Rows in flight per lane: the backward pass holds two tensors and their
-// product for each.
-constexpr int kUnrollFwd = 4, kUnrollBwd = 2;
-constexpr int kBlocksFwd = 3, kBlocksBwd = 3;  // thread blocks per SM (launch bounds)
+// Rows in flight per lane, and thread blocks per SM (the register budget):
+// the backward pass holds two tensors and a product for each row.
+constexpr int kRowsFwd = 4, kRowsBwd = 2;
+constexpr int kBlocksFwd = 4, kBlocksBwd = 3;
 
 struct QnTensor {
   const void* x;
@@ -48,10 +49,12 @@ struct QnTensor {
   int weight_f32;
   int length, heads;
   int blocks;      // thread blocks that share this tensor's rows
-  int units_per_token;
   int rows;          // batch * length * heads
-  int many, units;
-  FastDiv div_upt, div_length, div_heads;
+  int many;          // steps take heads of one token (else rows back to back)
+  int parts;         // many: steps of one token
+  int run;           // steps that a warp takes at once: of one token, or one
+  int units;         // runs
+  FastDiv div_runs, div_length, div_heads;  // div_runs: runs of a token
   long long position_stride;
   uint32_t xs[3], ds[3], ys[3];  // batch, token, head; in 8 elements
 };
@@ -60,7 +63,9 @@ struct QnParams {
   QnTensor t[2];
   const float* cos;
   const float* sin;
-  int head_dim, rot, lanes, slots;  // lanes per row, rows side by side in a warp
+  int head_dim, rot;
+  int lanes, slots;   // lanes per row, rows side by side in a warp
+  int rot_lanes;      // lanes that hold rotated elements
   int table_rows, adjacent;
   float eps, inv_d;
 };
@@ -98,19 +103,6 @@ struct Pairs {
   uint64_t v[V / 2];
 };
 
-template <int V>
-__device__ __forceinline__ Raw<V> load_raw(const uint16_t* p) {
-  Raw<V> r;
-  if constexpr (V == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    r.w[0] = u.x; r.w[1] = u.y;
-  }
-  return r;
-}
-
 template <typename T, int V>
 __device__ __forceinline__ Pairs<V> widen(const Raw<V>& r) {
   Pairs<V> o;
@@ -137,36 +129,48 @@ __device__ __forceinline__ void store_row(uint16_t* p, const Pairs<V>& v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-// The pairs' other members: the lane's own words the other way round
-// (adjacent), or those of lane `other`.  Every lane of the warp takes part.
-template <typename T, int V, bool kAdjacent>
-__device__ __forceinline__ Pairs<V> partners(const Raw<V>& r, const Pairs<V>& own, int other) {
-  if constexpr (kAdjacent) {
-    Pairs<V> q;
+// Each pair's members the other way round.
+template <int V>
+__device__ __forceinline__ Pairs<V> swapped(const Pairs<V>& own) {
+  Pairs<V> q;
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      float x, y;
-      unpack2(own.v[i], x, y);
-      q.v[i] = pack2(y, x);
-    }
-    return q;
-  } else {
-    Raw<V> q;
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) q.w[i] = __shfl_sync(0xFFFFFFFFu, r.w[i], other);
-    return widen<T, V>(q);
+  for (int i = 0; i < V / 2; ++i) {
+    float x, y;
+    unpack2(own.v[i], x, y);
+    q.v[i] = pack2(y, x);
   }
+  return q;
+}
+
+template <int V>
+__device__ __forceinline__ Raw<V> load_raw(const uint16_t* p) {
+  Raw<V> r;
+  if constexpr (V == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = u.x; r.w[1] = u.y;
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ Raw<V> no_raw() {
+  Raw<V> r;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) r.w[i] = 0u;
+  return r;
 }
 
 // Sums over the `lanes` lanes of a row (lane `at` of it), given to all of
-// them, for kUnroll rows at once.  Rows need not fill a power of two: lanes
-// past the end add nothing.
-template <int kUnroll>
-__device__ __forceinline__ void row_sums(float (&v)[kUnroll], int lanes, int at, int first) {
+// them, for R rows at once.  Rows need not fill a power of two:
+// lanes past the end add nothing.
+template <int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], int lanes, int at, int first) {
   if ((lanes & (lanes - 1)) == 0) {
     for (int step = lanes >> 1; step > 0; step >>= 1)
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) v[u] += __shfl_xor_sync(0xFFFFFFFFu, v[u], step);
+      for (int u = 0; u < R; ++u) v[u] += __shfl_xor_sync(0xFFFFFFFFu, v[u], step);
     return;
   }
   int step = 16;
@@ -174,13 +178,13 @@ __device__ __forceinline__ void row_sums(float (&v)[kUnroll], int lanes, int at,
   for (; step > 0; step >>= 1) {
     const bool adds = at + step < lanes && at < step;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < R; ++u) {
       const float o = __shfl_down_sync(0xFFFFFFFFu, v[u], step);
       if (adds) v[u] += o;
     }
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) v[u] = __shfl_sync(0xFFFFFFFFu, v[u], first);
+  for (int u = 0; u < R; ++u) v[u] = __shfl_sync(0xFFFFFFFFu, v[u], first);
 }
 
 // 1/sqrt(x): the hardware's approximation and one Newton step.
@@ -189,212 +193,347 @@ __device__ __forceinline__ float inverse_root(float x) {
   return r * fmaf(-0.5f * x * r, r, 1.5f);
 }
 
-// The lane's angles for a token: each of its elements x turns into
-//   x * c - partner * s
-// (the sine of a pair's second member is negated).  Lanes that are not
-// rotated have c = 1, s = 0.
-template <int V, bool kAdjacent>
-__device__ __forceinline__ void load_angles(const QnParams& p, const QnTensor& t, int b, int l,
-                                            int e0, bool rotated, Pairs<V>& c, Pairs<V>& s) {
-  if (!rotated) {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      c.v[i] = pack2(1.f, 1.f);
-      s.v[i] = 0;
-    }
-    return;
-  }
-  int pos = t.positions ? t.positions[b * t.position_stride + l] : l;
-  pos = max(0, min(pos, p.table_rows - 1));
-  const int half = p.rot >> 1;
-  const uint64_t row = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * static_cast<uint32_t>(half);
-  if constexpr (kAdjacent) {
-    const float4 fc = *reinterpret_cast<const float4*>(p.cos + row + (e0 >> 1));
-    const float4 fs = *reinterpret_cast<const float4*>(p.sin + row + (e0 >> 1));
-    const float cc[4] = {fc.x, fc.y, fc.z, fc.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      c.v[i] = pack2(cc[i & 3], cc[i & 3]);
-      s.v[i] = pack2(ss[i & 3], -ss[i & 3]);
-    }
-  } else {
-    const bool second = e0 >= half;
-    const uint64_t at = row + (second ? e0 - half : e0);
-    const float sign = second ? -1.f : 1.f;
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 fc = *reinterpret_cast<const float4*>(p.cos + at + i);
-      const float4 fs = *reinterpret_cast<const float4*>(p.sin + at + i);
-      c.v[i / 2] = pack2(fc.x, fc.y);
-      c.v[i / 2 + 1] = pack2(fc.z, fc.w);
-      s.v[i / 2] = pack2(fs.x * sign, fs.y * sign);
-      s.v[i / 2 + 1] = pack2(fs.z * sign, fs.w * sign);
-    }
-  }
-}
-
 __device__ __forceinline__ uint64_t offset8(uint32_t i, uint32_t stride8) {
   return static_cast<uint64_t>(i) * stride8;
 }
 
-// kMany: a unit's rows are heads of one token, which share its angles.
-// Otherwise they are consecutive (token, head) rows, each with its own.
-template <typename T, int V, bool kAdjacent, bool kBackward, bool kMany>
-__device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, int block,
-                                          const float (*weight)[256], float (*red)[256]) {
-  constexpr int kUnroll = kBackward ? kUnrollBwd : kUnrollFwd;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slot = lane / p.lanes;
-  const int at = lane - slot * p.lanes;
-  const int first = slot * p.lanes;
-  const bool live = slot < p.slots;
-  const int e0 = at * V;
-  const int half = p.rot >> 1;
-  const bool rotated = live && e0 < p.rot;
-  const int other = rotated && !kAdjacent ? first + (e0 >= half ? at - half / V : at + half / V) : lane;
-  const uint16_t* px = static_cast<const uint16_t*>(t.x) + e0;
-  const uint16_t* pg = static_cast<const uint16_t*>(t.dy) + e0;
-  uint16_t* py = static_cast<uint16_t*>(t.y) + e0;
-  const uint64_t* w0 = reinterpret_cast<const uint64_t*>(weight[0] + e0);
-  const uint64_t* w1 = reinterpret_cast<const uint64_t*>(weight[1] + e0);
-  Pairs<V> dw;
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) dw.v[i] = 0;
+// What a lane holds of a row: V elements at ea and V at eb (which may be
+// missing).  Rotated halves: the two members of V pairs; else words some
+// lanes apart, so that each access of a warp is contiguous.
+struct LaneAt {
+  int ea, eb;
+  bool rot_a, rot_b, has_b;
+};
 
-  // The angles of a token; forward, with the weights in them.
-  auto angles = [&](int b, int l, Pairs<V>& c, Pairs<V>& s) {
-    load_angles<V, kAdjacent>(p, t, b, l, e0, rotated, c, s);
-    if constexpr (!kBackward) {
+template <int V, bool kAdjacent>
+__device__ __forceinline__ LaneAt lane_at(const QnParams& p, int at) {
+  LaneAt o;
+  if (!kAdjacent && at < p.rot_lanes) {
+    o.ea = at * V;
+    o.eb = (p.rot >> 1) + at * V;
+    o.rot_a = o.rot_b = o.has_b = true;
+    return o;
+  }
+  const int from = kAdjacent ? 0 : p.rot, lane = kAdjacent ? at : at - p.rot_lanes;
+  o.ea = from + lane * V;
+  o.eb = o.ea + (kAdjacent ? p.lanes : p.lanes - p.rot_lanes) * V;
+  o.has_b = o.eb < p.head_dim;
+  o.rot_a = kAdjacent && o.ea < p.rot;
+  o.rot_b = kAdjacent && o.eb < p.rot;
+  return o;
+}
+
+// A lane's angles for a position, so that x -> x c + q s with q the pair's
+// other member: the other word's element (halves), or the word's neighbour
+// (adjacent).  The rotation: s = -sin for first members, +sin for second
+// ones; `back` turns the other way.
+template <int V>
+struct Angles {
+  Pairs<V> ca, sa, cb, sb;
+};
+
+template <int V, bool kAdjacent, bool kBack>
+__device__ __forceinline__ void load_angles(const QnParams& p, int pos, const LaneAt& at,
+                                            Angles<V>& o) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    o.ca.v[i] = o.cb.v[i] = pack2(1.f, 1.f);
+    o.sa.v[i] = o.sb.v[i] = 0;
+  }
+  if (!at.rot_a) return;
+  pos = max(0, min(pos, p.table_rows - 1));
+  const uint64_t row =
+      static_cast<uint64_t>(static_cast<uint32_t>(pos)) * static_cast<uint32_t>(p.rot >> 1);
+  constexpr float f = kBack ? 1.f : -1.f;  // of a first member's sine
+  if constexpr (kAdjacent) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int e = w ? at.eb : at.ea;
+      if (w && !at.rot_b) break;
+      const float4 fc = *reinterpret_cast<const float4*>(p.cos + row + (e >> 1));
+      const float4 fs = *reinterpret_cast<const float4*>(p.sin + row + (e >> 1));
+      const float cc[4] = {fc.x, fc.y, fc.z, fc.w}, ss[4] = {fs.x, fs.y, fs.z, fs.w};
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) {
-        c.v[i] = mul2(c.v[i], w0[i]);
-        s.v[i] = mul2(s.v[i], w1[i]);
+        (w ? o.cb : o.ca).v[i] = pack2(cc[i & 3], cc[i & 3]);
+        (w ? o.sb : o.sa).v[i] = pack2(f * ss[i & 3], -f * ss[i & 3]);
       }
     }
-  };
-  const uint64_t head_step = offset8(p.slots, t.ys[2]);  // to the next row's head (kMany)
-  const int step = t.blocks * kWarpsQn;
-  for (int unit = block * kWarpsQn + warp; unit < t.units; unit += step) {
-    Raw<V> x[kUnroll], g[kUnroll];
-    Pairs<V> c, s;
-    int b[kUnroll], l[kUnroll];
-    uint64_t oy[kMany ? 1 : kUnroll];
-    bool ok[kUnroll];
-    if constexpr (kMany) {
-      const int token = fast_div(unit, t.div_upt);
-      const int h0 = (unit - token * t.units_per_token) * p.slots * kUnroll + slot;
-      b[0] = fast_div(token, t.div_length);
-      l[0] = token - b[0] * t.length;
-      uint64_t ox = offset8(b[0], t.xs[0]) + offset8(l[0], t.xs[1]) + offset8(h0, t.xs[2]);
-      uint64_t og = offset8(b[0], t.ds[0]) + offset8(l[0], t.ds[1]) + offset8(h0, t.ds[2]);
-      oy[0] = offset8(b[0], t.ys[0]) + offset8(l[0], t.ys[1]) + offset8(h0, t.ys[2]);
+  } else {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        ok[u] = live && h0 + u * p.slots < t.heads;
+    for (int i = 0; i < V; i += 4) {
+      const float4 fc = *reinterpret_cast<const float4*>(p.cos + row + at.ea + i);
+      const float4 fs = *reinterpret_cast<const float4*>(p.sin + row + at.ea + i);
+      o.ca.v[i / 2] = o.cb.v[i / 2] = pack2(fc.x, fc.y);
+      o.ca.v[i / 2 + 1] = o.cb.v[i / 2 + 1] = pack2(fc.z, fc.w);
+      o.sa.v[i / 2] = pack2(f * fs.x, f * fs.y);
+      o.sa.v[i / 2 + 1] = pack2(f * fs.z, f * fs.w);
+      o.sb.v[i / 2] = pack2(-f * fs.x, -f * fs.y);
+      o.sb.v[i / 2 + 1] = pack2(-f * fs.z, -f * fs.w);
+    }
+  }
+}
+
+template <int V>
+__device__ __forceinline__ Pairs<V> weights(const float* weight, int e, bool ok) {
+  Pairs<V> w;
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) x[u].w[i] = g[u].w[i] = 0u;
-        if (ok[u]) {
-          x[u] = load_raw<V>(px + ox * 8);
-          if constexpr (kBackward) g[u] = load_raw<V>(pg + og * 8);
+  for (int i = 0; i < V / 2; ++i)
+    w.v[i] = ok ? *reinterpret_cast<const uint64_t*>(weight + e + 2 * i) : 0ull;
+  return w;
+}
+
+// Forward, the weights go into the angles: q is the other member before its
+// own weight.
+template <int V, bool kAdjacent>
+__device__ __forceinline__ void weigh(const float* weight, const LaneAt& la, Angles<V>& an) {
+  const Pairs<V> wa = weights<V>(weight, la.ea, true), wb = weights<V>(weight, la.eb, la.has_b);
+  const Pairs<V> fa = kAdjacent ? swapped<V>(wa) : wb, fb = kAdjacent ? swapped<V>(wb) : wa;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    an.ca.v[i] = mul2(an.ca.v[i], wa.v[i]);
+    an.sa.v[i] = mul2(an.sa.v[i], fa.v[i]);
+    an.cb.v[i] = mul2(an.cb.v[i], wb.v[i]);
+    an.sb.v[i] = mul2(an.sb.v[i], fb.v[i]);
+  }
+}
+
+template <int V>
+struct Loaded {
+  Raw<V> xa, xb, ga, gb;
+};
+
+template <int V, bool kBackward>
+__device__ __forceinline__ Loaded<V> load_row(const uint16_t* x, const uint16_t* g, const LaneAt& la,
+                                              bool ok) {
+  Loaded<V> o;
+  o.xa = o.xb = o.ga = o.gb = no_raw<V>();
+  if (ok) {
+    o.xa = load_raw<V>(x + la.ea);
+    if (la.has_b) o.xb = load_raw<V>(x + la.eb);
+    if constexpr (kBackward) {
+      o.ga = load_raw<V>(g + la.ea);
+      if (la.has_b) o.gb = load_raw<V>(g + la.eb);
+    }
+  }
+  return o;
+}
+
+// A row's sum of squares, this lane's part.
+template <typename T, int V>
+__device__ __forceinline__ float square_sum(const Loaded<V>& x) {
+  const Pairs<V> va = widen<T, V>(x.xa), vb = widen<T, V>(x.xb);
+  uint64_t sq = mul2(va.v[0], va.v[0]);
+#pragma unroll
+  for (int i = 1; i < V / 2; ++i) sq = fma2(va.v[i], va.v[i], sq);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) sq = fma2(vb.v[i], vb.v[i], sq);
+  float lo, hi;
+  unpack2(sq, lo, hi);
+  return lo + hi;
+}
+
+template <typename T, int V, bool kAdjacent>
+__device__ __forceinline__ void forward_row(const Loaded<V>& x, float r, const Angles<V>& an,
+                                            uint16_t* y, const LaneAt& la) {
+  const Pairs<V> va = widen<T, V>(x.xa), vb = widen<T, V>(x.xb);
+  const Pairs<V> qa = kAdjacent ? swapped<V>(va) : vb, qb = kAdjacent ? swapped<V>(vb) : va;
+  const uint64_t rr = pack2(r, r);
+  Pairs<V> ya, yb;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    ya.v[i] = mul2(rr, fma2(qa.v[i], an.sa.v[i], mul2(va.v[i], an.ca.v[i])));
+    yb.v[i] = mul2(rr, fma2(qb.v[i], an.sb.v[i], mul2(vb.v[i], an.cb.v[i])));
+  }
+  store_row<T, V>(y + la.ea, ya);
+  if (la.has_b) store_row<T, V>(y + la.eb, yb);
+}
+
+// Turns dy back and weighs it (fa, fb), adds the row's share of dw, and
+// returns this lane's part of the dot product with the normed row.
+template <typename T, int V, bool kAdjacent>
+__device__ __forceinline__ float turn_back(const Loaded<V>& x, float r, const Angles<V>& an,
+                                           const float* weight, const LaneAt& la, Pairs<V>& fa,
+                                           Pairs<V>& fb, Pairs<V>& dwa, Pairs<V>& dwb) {
+  const Pairs<V> da = widen<T, V>(x.ga), db = widen<T, V>(x.gb);
+  const Pairs<V> qa = kAdjacent ? swapped<V>(da) : db, qb = kAdjacent ? swapped<V>(db) : da;
+  const Pairs<V> va = widen<T, V>(x.xa), vb = widen<T, V>(x.xb);
+  const Pairs<V> wa = weights<V>(weight, la.ea, true), wb = weights<V>(weight, la.eb, la.has_b);
+  const uint64_t rr = pack2(r, r);
+  uint64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const uint64_t ta = fma2(qa.v[i], an.sa.v[i], mul2(da.v[i], an.ca.v[i]));
+    const uint64_t tb = fma2(qb.v[i], an.sb.v[i], mul2(db.v[i], an.cb.v[i]));
+    const uint64_t ha = mul2(va.v[i], rr), hb = mul2(vb.v[i], rr);
+    dwa.v[i] = fma2(ta, ha, dwa.v[i]);  // (rows left out hold zeros)
+    dwb.v[i] = fma2(tb, hb, dwb.v[i]);
+    fa.v[i] = mul2(ta, wa.v[i]);
+    fb.v[i] = mul2(tb, wb.v[i]);
+    sum = fma2(fa.v[i], ha, sum);
+    sum = fma2(fb.v[i], hb, sum);
+  }
+  float lo, hi;
+  unpack2(sum, lo, hi);
+  return lo + hi;
+}
+
+// dx = r f - x r^3 mean(f x): `dot` is mean(f x r).
+template <typename T, int V>
+__device__ __forceinline__ void backward_row(const Loaded<V>& x, float r, float dot,
+                                             const Pairs<V>& fa, const Pairs<V>& fb, uint16_t* y,
+                                             const LaneAt& la) {
+  Pairs<V> va = widen<T, V>(x.xa), vb = widen<T, V>(x.xb);
+  const float f = -dot * r * r;
+  const uint64_t rr = pack2(r, r), ff = pack2(f, f);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    va.v[i] = fma2(va.v[i], ff, mul2(rr, fa.v[i]));
+    vb.v[i] = fma2(vb.v[i], ff, mul2(rr, fb.v[i]));
+  }
+  store_row<T, V>(y + la.ea, va);
+  if (la.has_b) store_row<T, V>(y + la.eb, vb);
+}
+
+// A step's rows and where they go.
+template <int V, int R>
+struct Rows {
+  Loaded<V> x[R];
+  bool ok[R];
+  uint16_t* y[R];
+};
+
+// One step; `angles(u)` gives those of row u.
+template <typename T, int V, int R, bool kAdjacent, bool kBackward, typename F>
+__device__ __forceinline__ void norm_step(const QnParams& p, const Rows<V, R>& s, const float* weight,
+                                          const LaneAt& la, int at, int first, Pairs<V>& dwa,
+                                          Pairs<V>& dwb, F angles) {
+  float r[R];
+#pragma unroll
+  for (int u = 0; u < R; ++u) r[u] = square_sum<T, V>(s.x[u]);
+  row_sums<R>(r, p.lanes, at, first);
+#pragma unroll
+  for (int u = 0; u < R; ++u) r[u] = inverse_root(fmaf(r[u], p.inv_d, p.eps));
+  if constexpr (!kBackward) {
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      const Angles<V>& an = angles(u);
+      if (s.ok[u]) forward_row<T, V, kAdjacent>(s.x[u], r[u], an, s.y[u], la);
+    }
+  } else {
+    float dot[R];
+    Pairs<V> fa[R], fb[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+      dot[u] = turn_back<T, V, kAdjacent>(s.x[u], r[u], angles(u), weight, la, fa[u], fb[u], dwa, dwb);
+    row_sums<R>(dot, p.lanes, at, first);
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+      if (s.ok[u]) backward_row<T, V>(s.x[u], r[u], dot[u] * p.inv_d, fa[u], fb[u], s.y[u], la);
+  }
+}
+
+// kMany: a step's rows are heads of one token, and the steps of a run share
+// its angles.  Otherwise they are consecutive (token, head) rows, each with
+// its own.
+template <typename T, int V, bool kAdjacent, bool kBackward, bool kMany>
+__device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, int block,
+                                          const float* weight, float* red) {
+  constexpr int R = kBackward ? kRowsBwd : kRowsFwd;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot = lane / p.lanes;
+  const int at = lane - slot * p.lanes, first = slot * p.lanes;
+  const bool live = slot < p.slots;
+  const LaneAt la = lane_at<V, kAdjacent>(p, live ? at : 0);
+  Pairs<V> dwa, dwb;
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) dwa.v[i] = dwb.v[i] = 0;
+  const uint16_t* px = static_cast<const uint16_t*>(t.x);
+  const uint16_t* pg = static_cast<const uint16_t*>(t.dy);
+  uint16_t* py = static_cast<uint16_t*>(t.y);
+  const int stride = t.blocks * kWarpsQn;
+  Angles<V> an;
+  if constexpr (kMany) {
+    auto position = [&](int unit, int* b, int* l) {
+      const int token = fast_div(unit, t.div_runs);
+      *b = fast_div(token, t.div_length);
+      *l = token - *b * t.length;
+      return t.positions ? t.positions[*b * t.position_stride + *l] : *l;
+    };
+    int unit = block * kWarpsQn + warp, b = 0, l = 0, pos = 0;
+    if (unit < t.units) pos = position(unit, &b, &l);
+    const uint64_t sx = offset8(t.xs[2], 8), sg = offset8(t.ds[2], 8), sy = offset8(t.ys[2], 8);
+    while (unit < t.units) {
+      const int run = unit - fast_div(unit, t.div_runs) * static_cast<int>(t.div_runs.d);
+      int head = run * t.run * p.slots * R + slot;
+      const uint16_t* x0 = px + (offset8(b, t.xs[0]) + offset8(l, t.xs[1])) * 8 + head * sx;
+      const uint16_t* g0 = pg + (offset8(b, t.ds[0]) + offset8(l, t.ds[1])) * 8 + head * sg;
+      uint16_t* y0 = py + (offset8(b, t.ys[0]) + offset8(l, t.ys[1])) * 8 + head * sy;
+      const int this_pos = pos;
+      const int heads = live ? min(t.heads, (run + 1) * t.run * p.slots * R) : 0;
+      unit += stride;
+      if (unit < t.units) pos = position(unit, &b, &l);  // (read one run ahead)
+      bool fresh = true;
+      for (int i = 0; i < t.run; ++i) {
+        Rows<V, R> s;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          s.ok[u] = head + u * p.slots < heads;
+          s.x[u] = load_row<V, kBackward>(x0 + u * p.slots * sx, g0 + u * p.slots * sg, la, s.ok[u]);
+          s.y[u] = y0 + u * p.slots * sy;
         }
-        ox += offset8(p.slots, t.xs[2]);
-        og += offset8(p.slots, t.ds[2]);
-      }
-      angles(b[0], l[0], c, s);
-    } else {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int row = (unit * kUnroll + u) * p.slots + slot;
-        const int token = fast_div(row, t.div_heads);
-        const int head = row - token * t.heads;
-        b[u] = fast_div(token, t.div_length);
-        l[u] = token - b[u] * t.length;
-        ok[u] = live && row < t.rows;
-        oy[u] = offset8(b[u], t.ys[0]) + offset8(l[u], t.ys[1]) + offset8(head, t.ys[2]);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) x[u].w[i] = g[u].w[i] = 0u;
-        if (ok[u]) {
-          x[u] = load_raw<V>(px + (offset8(b[u], t.xs[0]) + offset8(l[u], t.xs[1]) +
-                                   offset8(head, t.xs[2])) * 8);
-          if constexpr (kBackward)
-            g[u] = load_raw<V>(pg + (offset8(b[u], t.ds[0]) + offset8(l[u], t.ds[1]) +
-                                     offset8(head, t.ds[2])) * 8);
-        } else {
-          b[u] = l[u] = 0;
+        if (fresh) {
+          load_angles<V, kAdjacent, kBackward>(p, this_pos, la, an);
+          if constexpr (!kBackward) weigh<V, kAdjacent>(weight, la, an);
+          fresh = false;
         }
+        norm_step<T, V, R, kAdjacent, kBackward>(p, s, weight, la, at, first, dwa, dwb,
+                                                 [&](int) -> const Angles<V>& { return an; });
+        head += p.slots * R;
+        x0 += p.slots * R * sx;
+        g0 += p.slots * R * sg;
+        y0 += p.slots * R * sy;
       }
     }
-    float r[kUnroll];
+  } else {
+    for (int unit = block * kWarpsQn + warp; unit < t.units; unit += stride) {
+      Rows<V, R> s;
+      int pos[R];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const Pairs<V> v = widen<T, V>(x[u]);
-      uint64_t sq = mul2(v.v[0], v.v[0]);
-#pragma unroll
-      for (int i = 1; i < V / 2; ++i) sq = fma2(v.v[i], v.v[i], sq);
-      float lo, hi;
-      unpack2(sq, lo, hi);
-      r[u] = lo + hi;
-    }
-    row_sums(r, p.lanes, at, first);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) r[u] = inverse_root(fmaf(r[u], p.inv_d, p.eps));
-    if constexpr (!kBackward) {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if constexpr (!kMany) angles(b[u], l[u], c, s);
-        Pairs<V> v = widen<T, V>(x[u]);
-        const Pairs<V> q = partners<T, V, kAdjacent>(x[u], v, other);
-        const uint64_t rr = pack2(r[u], r[u]), mr = pack2(-r[u], -r[u]);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-          v.v[i] = fma2(mul2(q.v[i], s.v[i]), mr, mul2(mul2(v.v[i], c.v[i]), rr));
-        if (ok[u]) store_row<T, V>(py + (kMany ? oy[0] + u * head_step : oy[u]) * 8, v);
+      for (int u = 0; u < R; ++u) {
+        const int row = (unit * R + u) * p.slots + slot;
+        s.ok[u] = live && row < t.rows;
+        const int token = fast_div(row, t.div_heads), head = row - token * t.heads;
+        const int b = fast_div(token, t.div_length), l = token - b * t.length;
+        s.x[u] = load_row<V, kBackward>(
+            px + (offset8(b, t.xs[0]) + offset8(l, t.xs[1]) + offset8(head, t.xs[2])) * 8,
+            pg + (offset8(b, t.ds[0]) + offset8(l, t.ds[1]) + offset8(head, t.ds[2])) * 8, la, s.ok[u]);
+        s.y[u] = py + (offset8(b, t.ys[0]) + offset8(l, t.ys[1]) + offset8(head, t.ys[2])) * 8;
+        pos[u] = !s.ok[u] ? 0 : t.positions ? t.positions[b * t.position_stride + l] : l;
       }
-    } else {
-      float dot[kUnroll];
-      Pairs<V> gw[kUnroll];
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if constexpr (!kMany) angles(b[u], l[u], c, s);
-        const Pairs<V> own = widen<T, V>(g[u]);
-        const Pairs<V> q = partners<T, V, kAdjacent>(g[u], own, other);
-        const Pairs<V> v = widen<T, V>(x[u]);
-        const uint64_t rr = pack2(r[u], r[u]);
-        uint64_t sum = 0;
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          const uint64_t back = fma2(q.v[i], s.v[i], mul2(own.v[i], c.v[i]));  // turned back
-          const uint64_t xhat = mul2(v.v[i], rr);                             // the normed row
-          dw.v[i] = fma2(back, xhat, dw.v[i]);  // (rows left out hold zeros)
-          gw[u].v[i] = mul2(back, w0[i]);
-          sum = fma2(gw[u].v[i], xhat, sum);
-        }
-        float lo, hi;
-        unpack2(sum, lo, hi);
-        dot[u] = lo + hi;
-      }
-      row_sums(dot, p.lanes, at, first);
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        Pairs<V> v = widen<T, V>(x[u]);
-        const float f = -dot[u] * p.inv_d * r[u];
-        const uint64_t rr = pack2(r[u], r[u]), ff = pack2(f, f);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) v.v[i] = mul2(rr, fma2(v.v[i], ff, gw[u].v[i]));
-        if (ok[u]) store_row<T, V>(py + (kMany ? oy[0] + u * head_step : oy[u]) * 8, v);
-      }
+      norm_step<T, V, R, kAdjacent, kBackward>(
+          p, s, weight, la, at, first, dwa, dwb, [&](int u) -> const Angles<V>& {
+            load_angles<V, kAdjacent, kBackward>(p, pos[u], la, an);
+            if (!kBackward) weigh<V, kAdjacent>(weight, la, an);
+            return an;
+          });
     }
   }
   if constexpr (kBackward) {
     // The block's share of dw: slots of a warp, then warps, in order.
+    float* mine = red + warp * 256;
     for (int sl = 0; sl < p.slots; ++sl) {
       if (slot == sl) {
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
           float x, y;
-          unpack2(dw.v[i], x, y);
-          red[warp][e0 + 2 * i] = x + (sl ? red[warp][e0 + 2 * i] : 0.f);
-          red[warp][e0 + 2 * i + 1] = y + (sl ? red[warp][e0 + 2 * i + 1] : 0.f);
+          unpack2(dwa.v[i], x, y);
+          mine[la.ea + 2 * i] = x + (sl ? mine[la.ea + 2 * i] : 0.f);
+          mine[la.ea + 2 * i + 1] = y + (sl ? mine[la.ea + 2 * i + 1] : 0.f);
+          if (!la.has_b) continue;
+          unpack2(dwb.v[i], x, y);
+          mine[la.eb + 2 * i] = x + (sl ? mine[la.eb + 2 * i] : 0.f);
+          mine[la.eb + 2 * i + 1] = y + (sl ? mine[la.eb + 2 * i + 1] : 0.f);
         }
       }
       __syncwarp();
@@ -403,7 +542,7 @@ __device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, 
     for (int d = threadIdx.x; d < p.head_dim; d += kThreadsQn) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarpsQn; ++i) sum += red[i][d];
+      for (int i = 0; i < kWarpsQn; ++i) sum += red[i * 256 + d];
       t.partial[static_cast<long long>(block) * p.head_dim + d] = sum;
     }
   }
@@ -412,27 +551,16 @@ __device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, 
 template <typename T, int V, bool kAdjacent, bool kBackward>
 __global__ void __launch_bounds__(kThreadsQn, kBackward ? kBlocksBwd : kBlocksFwd)
     qk_norm_rope_kernel(const __grid_constant__ QnParams p) {
-  __shared__ __align__(16) float weight[2][256];
-  __shared__ float red[kBackward ? kWarpsQn : 1][256];
+  __shared__ __align__(16) float weight[256];
+  __shared__ float red[kBackward ? kWarpsQn * 256 : 1];
   const bool is_k = blockIdx.x >= static_cast<unsigned>(p.t[0].blocks);
   const QnTensor& t = p.t[is_k ? 1 : 0];
   const int block = is_k ? blockIdx.x - p.t[0].blocks : blockIdx.x;
   grid_dependency_wait();
   grid_launch_dependents();
-  // The weights, and those of each element's partner.
-  for (int e = threadIdx.x; e < 256; e += kThreadsQn) {
-    int far = e;
-    if (e < p.rot) far = kAdjacent ? e ^ 1 : e < (p.rot >> 1) ? e + (p.rot >> 1) : e - (p.rot >> 1);
-    float w[2] = {0.f, 0.f};
-    if (e < p.head_dim) {
-      w[0] = t.weight_f32 ? static_cast<const float*>(t.weight)[e]
-                          : Pair<T>::load(static_cast<const uint16_t*>(t.weight)[e]).x;
-      w[1] = t.weight_f32 ? static_cast<const float*>(t.weight)[far]
-                          : Pair<T>::load(static_cast<const uint16_t*>(t.weight)[far]).x;
-    }
-    weight[0][e] = w[0];
-    weight[1][e] = w[1];
-  }
+  for (int e = threadIdx.x; e < p.head_dim; e += kThreadsQn)
+    weight[e] = t.weight_f32 ? static_cast<const float*>(t.weight)[e]
+                             : Pair<T>::load(static_cast<const uint16_t*>(t.weight)[e]).x;
   __syncthreads();
   if (t.many)
     norm_rows<T, V, kAdjacent, kBackward, true>(p, t, block, weight, red);
@@ -560,9 +688,12 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
     if (misaligned(a.cos) || misaligned(a.sin)) return CONV_ERR_MISALIGNED;
   }
   // Halves that split a 16-byte word (rot_dim an odd multiple of 8) take
-  // 8-byte words, so that a pair's members sit in whole words of two lanes.
+  // 8-byte words, so that a pair's members sit in whole words.
   const int v = !a.adjacent_pairs && a.rot_dim % 16 != 0 ? 4 : 8;
-  if (a.head_dim / v > 32) return CONV_ERR_NOT_SUPPORTED;
+  const int rot_lanes = (a.rot_dim + 2 * v - 1) / (2 * v);
+  const int lanes = a.adjacent_pairs ? (a.head_dim + 15) / 16
+                                     : rot_lanes + (a.head_dim - a.rot_dim + 2 * v - 1) / (2 * v);
+  if (lanes > 32) return CONV_ERR_NOT_SUPPORTED;
   QnParams p{};
   conv_status_t st = take_tensor(a, a.q, backward, &p.t[0]);
   if (st == CONV_OK) st = take_tensor(a, a.k, backward, &p.t[1]);
@@ -579,7 +710,8 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
   p.sin = a.sin;
   p.head_dim = a.head_dim;
   p.rot = a.rot_dim;
-  p.lanes = a.head_dim / v;
+  p.lanes = lanes;
+  p.rot_lanes = rot_lanes;
   p.slots = 32 / p.lanes;
   p.table_rows = a.table_rows;
   p.adjacent = a.adjacent_pairs != 0;
@@ -588,14 +720,19 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
   long long units = 0;
   for (QnTensor& t : p.t) {
     if (!t.x || t.rows == 0) continue;
-    // One token to a unit where its heads fill most of the unit's rows (the
+    // Steps of one token's heads where these fill most of their rows (the
     // angles are then read once for all of them); else rows back to back.
-    const int unit_rows = p.slots * (backward ? kUnrollBwd : kUnrollFwd);
-    t.units_per_token = (t.heads + unit_rows - 1) / unit_rows;
-    t.many = 4 * t.heads >= 3 * t.units_per_token * unit_rows;
-    t.units = t.many ? t.rows / t.heads * t.units_per_token : (t.rows + unit_rows - 1) / unit_rows;
+    const int step_rows = p.slots * (backward ? kRowsBwd : kRowsFwd);
+    t.parts = (t.heads + step_rows - 1) / step_rows;
+    t.many = 4 * t.heads >= 3 * t.parts * step_rows;
+    const int tokens = t.rows / t.heads;
+    // A warp takes all of a token's steps when there are tokens enough.
+    const int warps = sms * (backward ? kBlocksBwd : kBlocksFwd) * kWarpsQn;
+    t.run = t.many && tokens >= warps ? t.parts : 1;
+    const int runs = t.many ? (t.parts + t.run - 1) / t.run : 1;
+    t.units = t.many ? tokens * runs : (t.rows + step_rows - 1) / step_rows;
+    t.div_runs = make_fast_div(static_cast<uint32_t>(runs));
     t.div_heads = make_fast_div(static_cast<uint32_t>(t.heads));
-    t.div_upt = make_fast_div(static_cast<uint32_t>(t.units_per_token));
     t.div_length = make_fast_div(static_cast<uint32_t>(t.length));
     units += t.units;
   }
