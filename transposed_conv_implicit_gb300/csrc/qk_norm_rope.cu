@@ -36,7 +36,8 @@ constexpr int kWarpsQn = kThreadsQn / 32;
 // Rows in flight per lane, and thread blocks per SM (the register budget):
 // the backward pass holds two tensors and a product for each row.
 constexpr int kRowsFwd = 4, kRowsBwd = 2;
-constexpr int kBlocksFwd = 4, kBlocksBwd = 3;
+constexpr int kStagesBwd = 2;  // steps of the backward pass's ring
+constexpr int kBlocksFwd = 4, kBlocksBwd = 4;
 
 struct QnTensor {
   const void* x;
@@ -159,6 +160,32 @@ __device__ __forceinline__ Raw<V> no_raw() {
   Raw<V> r;
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) r.w[i] = 0u;
+  return r;
+}
+
+// One word of a lane's own ring slot: global -> shared without registers;
+// zeros when the row is left out.
+template <int kBytes>
+__device__ __forceinline__ void ring_load(uint32_t dst, const void* src, bool ok) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+                 "r"(ok ? kBytes : 0)
+                 : "memory");
+}
+template <int V>
+__device__ __forceinline__ Raw<V> ring_read(uint32_t src) {
+  Raw<V> r;
+  if constexpr (V == 8)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                 : "r"(src)
+                 : "memory");
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(src) : "memory");
   return r;
 }
 
@@ -303,18 +330,13 @@ struct Loaded {
   Raw<V> xa, xb, ga, gb;
 };
 
-template <int V, bool kBackward>
-__device__ __forceinline__ Loaded<V> load_row(const uint16_t* x, const uint16_t* g, const LaneAt& la,
-                                              bool ok) {
+template <int V>
+__device__ __forceinline__ Loaded<V> load_row(const uint16_t* x, const LaneAt& la, bool ok) {
   Loaded<V> o;
-  o.xa = o.xb = o.ga = o.gb = no_raw<V>();
+  o.xa = o.xb = no_raw<V>();
   if (ok) {
     o.xa = load_raw<V>(x + la.ea);
     if (la.has_b) o.xb = load_raw<V>(x + la.eb);
-    if constexpr (kBackward) {
-      o.ga = load_raw<V>(g + la.ea);
-      if (la.has_b) o.gb = load_raw<V>(g + la.eb);
-    }
   }
   return o;
 }
@@ -404,52 +426,34 @@ struct Rows {
 };
 
 // One step; `angles(u)` gives those of row u.
-template <typename T, int V, int R, bool kAdjacent, bool kBackward, typename F>
-__device__ __forceinline__ void norm_step(const QnParams& p, const Rows<V, R>& s, const float* weight,
-                                          const LaneAt& la, int at, int first, Pairs<V>& dwa,
-                                          Pairs<V>& dwb, F angles) {
+template <typename T, int V, int R, bool kAdjacent, typename F>
+__device__ __forceinline__ void norm_step(const QnParams& p, const Rows<V, R>& s, const LaneAt& la, int at, int first, F angles) {
   float r[R];
 #pragma unroll
   for (int u = 0; u < R; ++u) r[u] = square_sum<T, V>(s.x[u]);
   row_sums<R>(r, p.lanes, at, first);
 #pragma unroll
   for (int u = 0; u < R; ++u) r[u] = inverse_root(fmaf(r[u], p.inv_d, p.eps));
-  if constexpr (!kBackward) {
 #pragma unroll
-    for (int u = 0; u < R; ++u) {
-      const Angles<V>& an = angles(u);
-      if (s.ok[u]) forward_row<T, V, kAdjacent>(s.x[u], r[u], an, s.y[u], la);
-    }
-  } else {
-    float dot[R];
-    Pairs<V> fa[R], fb[R];
-#pragma unroll
-    for (int u = 0; u < R; ++u)
-      dot[u] = turn_back<T, V, kAdjacent>(s.x[u], r[u], angles(u), weight, la, fa[u], fb[u], dwa, dwb);
-    row_sums<R>(dot, p.lanes, at, first);
-#pragma unroll
-    for (int u = 0; u < R; ++u)
-      if (s.ok[u]) backward_row<T, V>(s.x[u], r[u], dot[u] * p.inv_d, fa[u], fb[u], s.y[u], la);
+  for (int u = 0; u < R; ++u) {
+    const Angles<V>& an = angles(u);
+    if (s.ok[u]) forward_row<T, V, kAdjacent>(s.x[u], r[u], an, s.y[u], la);
   }
 }
 
 // kMany: a step's rows are heads of one token, and the steps of a run share
 // its angles.  Otherwise they are consecutive (token, head) rows, each with
 // its own.
-template <typename T, int V, bool kAdjacent, bool kBackward, bool kMany>
+template <typename T, int V, bool kAdjacent, bool kMany>
 __device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, int block,
-                                          const float* weight, float* red) {
-  constexpr int R = kBackward ? kRowsBwd : kRowsFwd;
+                                          const float* weight) {
+  constexpr int R = kRowsFwd;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slot = lane / p.lanes;
   const int at = lane - slot * p.lanes, first = slot * p.lanes;
   const bool live = slot < p.slots;
   const LaneAt la = lane_at<V, kAdjacent>(p, live ? at : 0);
-  Pairs<V> dwa, dwb;
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) dwa.v[i] = dwb.v[i] = 0;
   const uint16_t* px = static_cast<const uint16_t*>(t.x);
-  const uint16_t* pg = static_cast<const uint16_t*>(t.dy);
   uint16_t* py = static_cast<uint16_t*>(t.y);
   const int stride = t.blocks * kWarpsQn;
   Angles<V> an;
@@ -462,12 +466,11 @@ __device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, 
     };
     int unit = block * kWarpsQn + warp, b = 0, l = 0, pos = 0;
     if (unit < t.units) pos = position(unit, &b, &l);
-    const uint64_t sx = offset8(t.xs[2], 8), sg = offset8(t.ds[2], 8), sy = offset8(t.ys[2], 8);
+    const uint64_t sx = offset8(t.xs[2], 8), sy = offset8(t.ys[2], 8);
     while (unit < t.units) {
       const int run = unit - fast_div(unit, t.div_runs) * static_cast<int>(t.div_runs.d);
       int head = run * t.run * p.slots * R + slot;
       const uint16_t* x0 = px + (offset8(b, t.xs[0]) + offset8(l, t.xs[1])) * 8 + head * sx;
-      const uint16_t* g0 = pg + (offset8(b, t.ds[0]) + offset8(l, t.ds[1])) * 8 + head * sg;
       uint16_t* y0 = py + (offset8(b, t.ys[0]) + offset8(l, t.ys[1])) * 8 + head * sy;
       const int this_pos = pos;
       const int heads = live ? min(t.heads, (run + 1) * t.run * p.slots * R) : 0;
@@ -479,19 +482,18 @@ __device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, 
 #pragma unroll
         for (int u = 0; u < R; ++u) {
           s.ok[u] = head + u * p.slots < heads;
-          s.x[u] = load_row<V, kBackward>(x0 + u * p.slots * sx, g0 + u * p.slots * sg, la, s.ok[u]);
+          s.x[u] = load_row<V>(x0 + u * p.slots * sx, la, s.ok[u]);
           s.y[u] = y0 + u * p.slots * sy;
         }
         if (fresh) {
-          load_angles<V, kAdjacent, kBackward>(p, this_pos, la, an);
-          if constexpr (!kBackward) weigh<V, kAdjacent>(weight, la, an);
+          load_angles<V, kAdjacent, false>(p, this_pos, la, an);
+          weigh<V, kAdjacent>(weight, la, an);
           fresh = false;
         }
-        norm_step<T, V, R, kAdjacent, kBackward>(p, s, weight, la, at, first, dwa, dwb,
-                                                 [&](int) -> const Angles<V>& { return an; });
+        norm_step<T, V, R, kAdjacent>(p, s, la, at, first,
+                                      [&](int) -> const Angles<V>& { return an; });
         head += p.slots * R;
         x0 += p.slots * R * sx;
-        g0 += p.slots * R * sg;
         y0 += p.slots * R * sy;
       }
     }
@@ -505,54 +507,197 @@ __device__ __forceinline__ void norm_rows(const QnParams& p, const QnTensor& t, 
         s.ok[u] = live && row < t.rows;
         const int token = fast_div(row, t.div_heads), head = row - token * t.heads;
         const int b = fast_div(token, t.div_length), l = token - b * t.length;
-        s.x[u] = load_row<V, kBackward>(
-            px + (offset8(b, t.xs[0]) + offset8(l, t.xs[1]) + offset8(head, t.xs[2])) * 8,
-            pg + (offset8(b, t.ds[0]) + offset8(l, t.ds[1]) + offset8(head, t.ds[2])) * 8, la, s.ok[u]);
+        s.x[u] = load_row<V>(
+            px + (offset8(b, t.xs[0]) + offset8(l, t.xs[1]) + offset8(head, t.xs[2])) * 8, la, s.ok[u]);
         s.y[u] = py + (offset8(b, t.ys[0]) + offset8(l, t.ys[1]) + offset8(head, t.ys[2])) * 8;
         pos[u] = !s.ok[u] ? 0 : t.positions ? t.positions[b * t.position_stride + l] : l;
       }
-      norm_step<T, V, R, kAdjacent, kBackward>(
-          p, s, weight, la, at, first, dwa, dwb, [&](int u) -> const Angles<V>& {
-            load_angles<V, kAdjacent, kBackward>(p, pos[u], la, an);
-            if (!kBackward) weigh<V, kAdjacent>(weight, la, an);
+      norm_step<T, V, R, kAdjacent>(
+          p, s, la, at, first, [&](int u) -> const Angles<V>& {
+            load_angles<V, kAdjacent, false>(p, pos[u], la, an);
+            weigh<V, kAdjacent>(weight, la, an);
             return an;
           });
     }
   }
-  if constexpr (kBackward) {
-    // The block's share of dw: slots of a warp, then warps, in order.
-    float* mine = red + warp * 256;
-    for (int sl = 0; sl < p.slots; ++sl) {
-      if (slot == sl) {
+}
+
+// Backward: the rows come through a ring of kStages steps in shared memory,
+// each lane's words in slots of its own (no barriers), with where the row's
+// result goes and its position beside them; kStages - 1 steps are in flight.
+template <typename T, int V, bool kAdjacent, bool kMany>
+__device__ __forceinline__ void norm_rows_back(const QnParams& p, const QnTensor& t, int block,
+                                               const float* weight, float* red, uint32_t ring) {
+  constexpr int R = kRowsBwd, S = kStagesBwd;
+  constexpr uint32_t kWord = V * 2, kPitch = kThreadsQn * kWord, kRow = 4 * kPitch + 16 * kThreadsQn;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slot = lane / p.lanes;
+  const int at = lane - slot * p.lanes, first = slot * p.lanes;
+  const bool live = slot < p.slots;
+  const LaneAt la = lane_at<V, kAdjacent>(p, live ? at : 0);
+  const uint32_t words = ring + threadIdx.x * kWord;                      // x a, x b, dy a, dy b
+  const uint32_t notes = ring + 4 * kPitch + threadIdx.x * 16;            // y offset, row ok, position
+  const uint16_t* px = static_cast<const uint16_t*>(t.x);
+  const uint16_t* pg = static_cast<const uint16_t*>(t.dy);
+  uint16_t* py = static_cast<uint16_t*>(t.y);
+  const int stride = t.blocks * kWarpsQn;
+  Pairs<V> dwa, dwb;
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          float x, y;
-          unpack2(dwa.v[i], x, y);
-          mine[la.ea + 2 * i] = x + (sl ? mine[la.ea + 2 * i] : 0.f);
-          mine[la.ea + 2 * i + 1] = y + (sl ? mine[la.ea + 2 * i + 1] : 0.f);
-          if (!la.has_b) continue;
-          unpack2(dwb.v[i], x, y);
-          mine[la.eb + 2 * i] = x + (sl ? mine[la.eb + 2 * i] : 0.f);
-          mine[la.eb + 2 * i + 1] = y + (sl ? mine[la.eb + 2 * i + 1] : 0.f);
-        }
+  for (int i = 0; i < V / 2; ++i) dwa.v[i] = dwb.v[i] = 0;
+
+  // The loading side: run `unit`, step `part` of it.
+  int unit = block * kWarpsQn + warp, part = 0, b = 0, l = 0, head0 = 0;
+  auto load_step = [&](int stage) {
+    if (unit < t.units) {
+      if (kMany && part == 0) {
+        const int token = fast_div(unit, t.div_runs);
+        head0 = (unit - token * static_cast<int>(t.div_runs.d)) * t.run * p.slots * R + slot;
+        b = fast_div(token, t.div_length);
+        l = token - b * t.length;
       }
-      __syncwarp();
-    }
-    __syncthreads();
-    for (int d = threadIdx.x; d < p.head_dim; d += kThreadsQn) {
-      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kWarpsQn; ++i) sum += red[i * 256 + d];
-      t.partial[static_cast<long long>(block) * p.head_dim + d] = sum;
+      for (int u = 0; u < R; ++u) {
+        int head;
+        bool ok;
+        if (kMany) {
+          head = head0 + (part * R + u) * p.slots;
+          ok = live && head < t.heads;
+        } else {
+          const int row = (unit * R + u) * p.slots + slot;
+          ok = live && row < t.rows;
+          const int token = fast_div(ok ? row : 0, t.div_heads);
+          head = (ok ? row : 0) - token * t.heads;
+          b = fast_div(token, t.div_length);
+          l = token - b * t.length;
+        }
+        if (kMany && !ok) head = 0;
+        const uint16_t* x = px + (offset8(b, t.xs[0]) + offset8(l, t.xs[1]) + offset8(head, t.xs[2])) * 8;
+        const uint16_t* g = pg + (offset8(b, t.ds[0]) + offset8(l, t.ds[1]) + offset8(head, t.ds[2])) * 8;
+        const uint64_t y = (offset8(b, t.ys[0]) + offset8(l, t.ys[1]) + offset8(head, t.ys[2])) * 8;
+        const uint32_t w = words + (stage * R + u) * kRow, n = notes + (stage * R + u) * kRow;
+        const int eb = la.has_b ? la.eb : la.ea;
+        ring_load<kWord>(w, x + la.ea, ok);
+        ring_load<kWord>(w + kPitch, x + eb, ok && la.has_b);
+        ring_load<kWord>(w + 2 * kPitch, g + la.ea, ok);
+        ring_load<kWord>(w + 3 * kPitch, g + eb, ok && la.has_b);
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(n), "r"(static_cast<uint32_t>(y)),
+                     "r"(static_cast<uint32_t>(y >> 32))
+                     : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(n + 8), "r"(ok ? 1u : 0u) : "memory");
+        if (t.positions)
+          ring_load<4>(n + 12, t.positions + b * t.position_stride + l, true);
+        else
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(n + 12), "r"(l) : "memory");
+      }
+      if (!kMany || ++part == t.run) {
+        part = 0;
+        unit += stride;
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int now = unit, now_part = 0;  // the arithmetic's side
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) load_step(i);
+
+  Angles<V> an;
+  int stage = 0;
+  while (now < t.units) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+    const uint32_t w = words + stage * R * kRow, n = notes + stage * R * kRow;
+    uint16_t* y[R];
+    bool ok[R];
+    int pos[R];
+    float r[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      uint32_t lo, hi, good, at_pos;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(lo), "=r"(hi), "=r"(good), "=r"(at_pos)
+                   : "r"(n + u * kRow)
+                   : "memory");
+      y[u] = py + ((static_cast<uint64_t>(hi) << 32) | lo);
+      ok[u] = good != 0;
+      pos[u] = static_cast<int>(at_pos);
+    }
+    if (kMany && now_part == 0) load_angles<V, kAdjacent, true>(p, pos[0], la, an);
+    // (The stage read in the step before is free.)
+    load_step(stage == 0 ? S - 1 : stage - 1);
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      Loaded<V> x;
+      x.xa = ring_read<V>(w + u * kRow);
+      x.xb = ring_read<V>(w + u * kRow + kPitch);
+      r[u] = square_sum<T, V>(x);
+    }
+    row_sums<R>(r, p.lanes, at, first);
+    float dot[R];
+    Pairs<V> fa[R], fb[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      r[u] = inverse_root(fmaf(r[u], p.inv_d, p.eps));
+      if (!kMany) load_angles<V, kAdjacent, true>(p, pos[u], la, an);
+      Loaded<V> x;
+      x.xa = ring_read<V>(w + u * kRow);
+      x.xb = ring_read<V>(w + u * kRow + kPitch);
+      x.ga = ring_read<V>(w + u * kRow + 2 * kPitch);
+      x.gb = ring_read<V>(w + u * kRow + 3 * kPitch);
+      dot[u] = turn_back<T, V, kAdjacent>(x, r[u], an, weight, la, fa[u], fb[u], dwa, dwb);
+    }
+    row_sums<R>(dot, p.lanes, at, first);
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      Loaded<V> x;
+      x.xa = ring_read<V>(w + u * kRow);
+      x.xb = ring_read<V>(w + u * kRow + kPitch);
+      if (ok[u]) backward_row<T, V>(x, r[u], dot[u] * p.inv_d, fa[u], fb[u], y[u], la);
+    }
+    if (!kMany || ++now_part == t.run) {
+      now_part = 0;
+      now += stride;
+    }
+    if (++stage == S) stage = 0;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // The block's share of dw: slots of a warp, then warps, in order.
+  float* mine = red + warp * 256;
+  for (int sl = 0; sl < p.slots; ++sl) {
+    if (slot == sl) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        float x, y;
+        unpack2(dwa.v[i], x, y);
+        mine[la.ea + 2 * i] = x + (sl ? mine[la.ea + 2 * i] : 0.f);
+        mine[la.ea + 2 * i + 1] = y + (sl ? mine[la.ea + 2 * i + 1] : 0.f);
+        if (!la.has_b) continue;
+        unpack2(dwb.v[i], x, y);
+        mine[la.eb + 2 * i] = x + (sl ? mine[la.eb + 2 * i] : 0.f);
+        mine[la.eb + 2 * i + 1] = y + (sl ? mine[la.eb + 2 * i + 1] : 0.f);
+      }
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < p.head_dim; d += kThreadsQn) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarpsQn; ++i) sum += red[i * 256 + d];
+    t.partial[static_cast<long long>(block) * p.head_dim + d] = sum;
+  }
+}
+
+// Shared memory of the backward kernel: weights, the warps' shares of dw, the ring.
+template <int V>
+constexpr size_t qn_back_smem() {
+  return 1024 + kWarpsQn * 1024 +
+         static_cast<size_t>(kStagesBwd) * kRowsBwd * kThreadsQn * (4 * V * 2 + 16);
 }
 
 template <typename T, int V, bool kAdjacent, bool kBackward>
 __global__ void __launch_bounds__(kThreadsQn, kBackward ? kBlocksBwd : kBlocksFwd)
     qk_norm_rope_kernel(const __grid_constant__ QnParams p) {
-  __shared__ __align__(16) float weight[256];
-  __shared__ float red[kBackward ? kWarpsQn * 256 : 1];
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* weight = reinterpret_cast<float*>(smem);
   const bool is_k = blockIdx.x >= static_cast<unsigned>(p.t[0].blocks);
   const QnTensor& t = p.t[is_k ? 1 : 0];
   const int block = is_k ? blockIdx.x - p.t[0].blocks : blockIdx.x;
@@ -562,44 +707,43 @@ __global__ void __launch_bounds__(kThreadsQn, kBackward ? kBlocksBwd : kBlocksFw
     weight[e] = t.weight_f32 ? static_cast<const float*>(t.weight)[e]
                              : Pair<T>::load(static_cast<const uint16_t*>(t.weight)[e]).x;
   __syncthreads();
-  if (t.many)
-    norm_rows<T, V, kAdjacent, kBackward, true>(p, t, block, weight, red);
-  else
-    norm_rows<T, V, kAdjacent, kBackward, false>(p, t, block, weight, red);
+  if constexpr (kBackward) {
+    float* red = weight + 256;
+    const uint32_t ring = smem_u32(smem) + 1024 + kWarpsQn * 1024;
+    if (t.many)
+      norm_rows_back<T, V, kAdjacent, true>(p, t, block, weight, red, ring);
+    else
+      norm_rows_back<T, V, kAdjacent, false>(p, t, block, weight, red, ring);
+  } else {
+    if (t.many)
+      norm_rows<T, V, kAdjacent, true>(p, t, block, weight);
+    else
+      norm_rows<T, V, kAdjacent, false>(p, t, block, weight);
+  }
 }
 
 // dw = the blocks' shares, summed in a fixed order: one thread block per
-// tensor, kReduceRows interleaved runs of rows, then the runs.
-constexpr int kReduceRows = 8;
+// tensor and 32 elements, its warps taking every 32nd share each, so that all
+// of a lane's reads are in flight together.
 __global__ void __launch_bounds__(1024) qk_norm_rope_dw_kernel(const __grid_constant__ QnParams p) {
-  __shared__ float part[kReduceRows][256];
+  __shared__ float part[32][33];
   grid_dependency_wait();
-  const QnTensor& t = p.t[blockIdx.x];
-  if (t.blocks == 0) {
-    // A tensor without rows: the gradient of its weight is zero.
-    if (t.dweight)
-      for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) t.dweight[d] = 0.f;
-    return;
+  grid_launch_dependents();
+  const QnTensor& t = p.t[blockIdx.y];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = blockIdx.x * 32 + lane;
+  if (!t.dweight) return;
+  float sum = 0.f;
+  if (d < p.head_dim) {
+#pragma unroll 8
+    for (int i = warp; i < t.blocks; i += 32)
+      sum += t.partial[static_cast<long long>(i) * p.head_dim + d];
   }
-  const int run = threadIdx.x >> 7;
-  for (int d = threadIdx.x & 127; d < p.head_dim; d += 128) {
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-    int i = run;
-    for (; i + 3 * kReduceRows < t.blocks; i += 4 * kReduceRows) {
-      s0 += t.partial[static_cast<long long>(i) * p.head_dim + d];
-      s1 += t.partial[static_cast<long long>(i + kReduceRows) * p.head_dim + d];
-      s2 += t.partial[static_cast<long long>(i + 2 * kReduceRows) * p.head_dim + d];
-      s3 += t.partial[static_cast<long long>(i + 3 * kReduceRows) * p.head_dim + d];
-    }
-    for (; i < t.blocks; i += kReduceRows)
-      s0 += t.partial[static_cast<long long>(i) * p.head_dim + d];
-    part[run][d] = (s0 + s1) + (s2 + s3);
-  }
+  part[warp][lane] = sum;
   __syncthreads();
-  for (int d = threadIdx.x; d < p.head_dim; d += blockDim.x) {
-    float sum = 0.f;
+  if (warp == 0 && d < p.head_dim) {
+    sum = 0.f;  // (a tensor without rows: the gradient of its weight is zero)
 #pragma unroll
-    for (int i = 0; i < kReduceRows; ++i) sum += part[i][d];
+    for (int i = 0; i < 32; ++i) sum += part[i][lane];
     t.dweight[d] = sum;
   }
 }
@@ -660,12 +804,23 @@ conv_status_t take_tensor(const qk_norm_rope_args_t& a, const qk_norm_rope_tenso
   return CONV_OK;
 }
 
+template <typename T, int V, bool kAdjacent, bool kBackward>
+cudaError_t launch_qn_one(const QnParams& p, int grid, cudaStream_t stream) {
+  static std::atomic<size_t> configured[kMaxDevices];
+  const size_t smem = kBackward ? qn_back_smem<V>() : 1024;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = raise_smem(qk_norm_rope_kernel<T, V, kAdjacent, kBackward>, configured, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(qk_norm_rope_kernel<T, V, kAdjacent, kBackward>, dim3(grid), dim3(kThreadsQn),
+                    smem, stream, p);
+}
+
 template <typename T, bool kBackward>
 cudaError_t launch_qn(const QnParams& p, int v, int grid, cudaStream_t stream) {
-  const dim3 g(grid), b(kThreadsQn);
-  if (p.adjacent) return launch_pdl(qk_norm_rope_kernel<T, 8, true, kBackward>, g, b, 0, stream, p);
-  if (v == 8) return launch_pdl(qk_norm_rope_kernel<T, 8, false, kBackward>, g, b, 0, stream, p);
-  return launch_pdl(qk_norm_rope_kernel<T, 4, false, kBackward>, g, b, 0, stream, p);
+  if (p.adjacent) return launch_qn_one<T, 8, true, kBackward>(p, grid, stream);
+  if (v == 8) return launch_qn_one<T, 8, false, kBackward>(p, grid, stream);
+  return launch_qn_one<T, 4, false, kBackward>(p, grid, stream);
 }
 
 template <bool kBackward>
@@ -758,7 +913,7 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
     err = backward ? launch_qn_dtype<true>(a.dtype, v, p, grid, stream)
                    : launch_qn_dtype<false>(a.dtype, v, p, grid, stream);
   if (err == cudaSuccess && backward)
-    err = launch_pdl(qk_norm_rope_dw_kernel, dim3(2), dim3(1024), 0, stream, p);
+    err = launch_pdl(qk_norm_rope_dw_kernel, dim3((a.head_dim + 31) / 32, 2), dim3(1024), 0, stream, p);
   return err == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 
