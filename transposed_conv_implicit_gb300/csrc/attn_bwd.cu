@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
     const uint32_t idesc_acc = attn_idesc(kBf16, k_steps * 16, false, true);
-    const uint64_t desc_k = desc_mn(kv_block);
+    const uint32_t lead_k = lead_mn(kv_block);
     const uint32_t a_lo = smem_u32(smem + p.off_a) >> 4, x_lo = smem_u32(smem + p.off_x) >> 4,
                    y_lo = smem_u32(smem + p.off_y) >> 4;
     const uint32_t tile_lo = kv_tile >> 4, block_lo = kv_block >> 4;
@@ -371,9 +371,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // A (128 rows) times a key/value tile, over the head dimension.
     auto rows_by_keys = [&](uint32_t d, uint32_t a, uint32_t b, int cols) {
       const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
-      for (int k = 0; k < k_steps; ++k)
-        mma_f16_warp(d, kDescK | (a + (k >> 2) * 1024u + (k & 3) * 2u),
-                     kDescK | (b + (k >> 2) * block_lo + (k & 3) * 2u), id, k != 0);
+      mma_ss_x4(d, kLeadK | a, kLeadK | b, id, 0u, k_steps);
+      if (k_steps > 4) mma_ss_x4(d, kLeadK | (a + 1024u), kLeadK | (b + block_lo), id, 1u, k_steps - 4);
     };
     Walk<true, AttnBwdParams> w(p, start);
     bool live = w.live;
@@ -468,9 +467,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       tc_fence_after();
       const uint32_t ds = tmem + (count & 1u) * 128;
-      for (int k = 0; k < (this_cols >> 4); ++k)
-        mma_f16_ts_warp(t_acc, ds + (k >> 2) * 64 + (k & 3) * 8,
-                        desc_k | (x_lo + this_k * tile_lo + k * 128u), idesc_acc, !(first && k == 0));
+      const int steps = this_cols >> 4;
+      const uint32_t kb = lead_k | (x_lo + this_k * tile_lo);
+      mma_ts_x4(t_acc, ds, kb, idesc_acc, first ? 0u : 1u, steps);
+      if (steps > 4) mma_ts_x4(t_acc, ds + 64, kb + 512u, idesc_acc, 1u, steps - 4);
       mma_commit_warp(smem_u32(&bars.x_empty[this_k]));
       if (last) mma_commit_warp(smem_u32(&bars.acc_done));
       ++count;
@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
     const uint32_t idesc_acc = attn_idesc(kBf16, k_steps * 16, false, true);
-    const uint64_t desc_b = desc_mn(16384);
+    const uint32_t lead_b = lead_mn(16384);
     const uint32_t a_lo = smem_u32(smem + p.off_a) >> 4, x_lo = smem_u32(smem + p.off_x) >> 4,
                    y_lo = smem_u32(smem + p.off_y) >> 4;
     constexpr uint32_t kTileLo = kTile >> 4;
@@ -865,16 +865,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t xph = 0, yph = 0, aph = 0, count = 0, items = 0;
     auto keys_by_rows = [&](uint32_t d, uint32_t a, uint32_t b, int cols) {
       const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
-      for (int k = 0; k < k_steps; ++k) {
-        const uint32_t at = (k >> 2) * 1024u + (k & 3) * 2u;
-        mma_f16_warp(d, kDescK | (a + at), kDescK | (b + at), id, k != 0);
-      }
+      mma_ss_x4(d, kLeadK | a, kLeadK | b, id, 0u, k_steps);
+      if (k_steps > 4) mma_ss_x4(d, kLeadK | (a + 1024u), kLeadK | (b + 1024u), id, 1u, k_steps - 4);
     };
     // A (in TMEM, halves of 64 columns) times a query tile, over its rows.
     auto accumulate = [&](uint32_t acc, uint32_t a, uint32_t b, int cols, bool fresh) {
-      for (int k = 0; k < (cols >> 4); ++k)
-        mma_f16_ts_warp(acc, a + (k >> 2) * 64 + (k & 3) * 8, desc_b | (b + k * 128u), idesc_acc,
-                        !(fresh && k == 0));
+      const int steps = cols >> 4;
+      mma_ts_x4(acc, a, lead_b | b, idesc_acc, fresh ? 0u : 1u, steps);
+      if (steps > 4) mma_ts_x4(acc, a + 64, lead_b | (b + 512u), idesc_acc, 1u, steps - 4);
     };
     // Queries without keys are cleared: nothing they hold meets a zero of p or ds.
     auto clear = [&](uint8_t* tile, int stat_stage) {

@@ -46,6 +46,9 @@ template <typename T, int DP, int G>
 struct Layout {
   static constexpr bool kSplit = G == 1;
   static constexpr int kBlocks = DP / 64;
+  // Pairs: three warpgroups, so that the softmax groups can take the third
+  // one's registers: (208 + 208 + 80) * 128 <= 168 * 384.
+  static constexpr int kThreads = G == 2 ? 384 : 192;
   static constexpr int kMmaWarp = 4 * G, kLoadWarp = 4 * G + 1;
   static constexpr uint32_t kQTile = 128u * 128u * kBlocks;
   static constexpr uint32_t kTmemCols = G == 2 ? 512 : 256;
@@ -56,7 +59,7 @@ constexpr int kMaxStages = 8;
 struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[2][2], q_empty[2][2];  // [group][stage]
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];  // p_half: of the first 64 keys
   uint64_t drain;
   SplitStart start;
   uint32_t any[2][4][4];  // [group][warp]: keys of the tile that a row of the warp attends
@@ -65,7 +68,7 @@ struct Bars {
 };
 
 template <typename T, int DP, int G>
-__global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
+__global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     attn_fwd_kernel(const __grid_constant__ AttnFwdParams p) {
   using L = Layout<T, DP, G>;
   constexpr bool kBf16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
@@ -89,6 +92,7 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
         mbar_init(smem_u32(&bars.q_empty[g][s]), 1);
       }
       mbar_init(smem_u32(&bars.s_full[g]), 1);
+      mbar_init(smem_u32(&bars.p_half[g]), 4);
       mbar_init(smem_u32(&bars.p_full[g]), 4);
       mbar_init(smem_u32(&bars.o_done[g]), 1);
       mbar_init(smem_u32(&bars.o_free[g]), 4);
@@ -126,6 +130,7 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
 
   if (warp == L::kLoadWarp) {
     // ------------------------------------------------------------ loads
+    if (G == 2) give_registers<80>();
     const uint32_t lead = lane == 0 ? 1u : 0u;
     const uint32_t q_bytes =
         static_cast<uint32_t>(p.tile_heads * p.tile_tokens) * 128u * L::kBlocks;
@@ -204,11 +209,12 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
   } else if (warp == L::kMmaWarp) {
     // ------------------------------------------------------------ products
     // The converged warp walks the MMAs; one elected lane issues each.
+    if (G == 2) give_registers<80>();
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t n_out = static_cast<uint32_t>(k_steps) * 16u;
     const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
     const uint32_t idesc_o = attn_idesc(kBf16, n_out, false, true);
-    const uint64_t desc_v = desc_mn(kv_block);
+    const uint32_t lead_v = lead_mn(kv_block);
     const uint32_t q_lo = smem_u32(smem + p.off_q) >> 4, kv_lo = smem_u32(smem + p.off_kv) >> 4;
     const uint32_t kv_tile_lo = kv_tile >> 4, kv_block_lo = kv_block >> 4;
     bool ok = true;
@@ -225,9 +231,9 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
       const uint32_t a = q_lo + ((g * p.q_stages + q_stage) * L::kQTile >> 4);
       const uint32_t b = kv_lo + k_stage * kv_tile_lo;
       const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
-      for (int k = 0; k < k_steps; ++k)
-        mma_f16_warp(tmem + g * 128, kDescK | (a + (k >> 2) * 1024u + (k & 3) * 2u),
-                     kDescK | (b + (k >> 2) * kv_block_lo + (k & 3) * 2u), id, k != 0);
+      mma_ss_x4(tmem + g * 128, kLeadK | a, kLeadK | b, id, 0u, k_steps);
+      if (k_steps > 4)
+        mma_ss_x4(tmem + g * 128, kLeadK | (a + 1024u), kLeadK | (b + kv_block_lo), id, 1u, k_steps - 4);
       mma_commit_warp(smem_u32(&bars.s_full[g]));
     };
     Walk<L::kSplit, AttnFwdParams> w(p, start);
@@ -311,8 +317,8 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
       }
       for (int g = 0; ok && g < G; ++g) {
         if (g < here) {
-          if (!masked) ok = wait(&bars.p_full[g], tile_parity[g], kAttnMmaTimeout);
-          tile_parity[g] ^= 1u;
+          // The first 64 keys' products start before the others' P is there.
+          if (!masked) ok = wait(&bars.p_half[g], tile_parity[g], kAttnMmaTimeout);
           if (ok && first) {
             if (item_count[g] > 0)
               ok = wait(&bars.o_free[g], (item_count[g] - 1) & 1u, kAttnMmaTimeout);
@@ -322,9 +328,16 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
           tc_fence_after();
           const uint32_t o = tmem + G * 128 + g * DP;
           const uint32_t b = kv_lo + v_stage * kv_tile_lo;
-          for (int k = 0; k < (cols >> 4); ++k)
-            mma_f16_ts_warp(o, tmem + g * 128 + k * 8, desc_v | (b + k * 128u), idesc_o,
-                            !(first && k == 0));
+          const int steps = cols >> 4;
+          mma_ts_x4(o, tmem + g * 128, lead_v | b, idesc_o, first ? 0u : 1u, steps);
+          if (!masked) {
+            ok = wait(&bars.p_full[g], tile_parity[g], kAttnMmaTimeout);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tile_parity[g] ^= 1u;
+          if (steps > 4)
+            mma_ts_x4(o, tmem + g * 128 + 32, lead_v | (b + 512u), idesc_o, 1u, steps - 4);
           mma_commit_warp(smem_u32(&bars.o_done[g]));
         }
         if (more && g < w.tiles_here) {
@@ -351,8 +364,9 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
       mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 4 * G) {
     // ------------------------------------------------------------ softmax
+    if (G == 2) take_registers<208>();
     const int g = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + g * 128 + lane_field;
@@ -404,30 +418,8 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
             if (lane == 0) bars.any[g][quarter][i] = any;
           }
         }
-        if (warp_ok) {
-          uint32_t s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c * 32 < cols) tmem_ld_x32(ts + c * 32, s + c * 32);
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c * 32 < cols) {
-              tmem_wait_ld_x32(s + c * 32);
-              uint32_t on = word[c];
-              const int rest = keys - c * 32;
-              if (rest < 32) on &= rest <= 0 ? 0u : (1u << rest) - 1u;
-              if (on != 0xFFFFFFFFu) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!((on >> i) & 1u)) s[c * 32 + i] = 0xFF800000u;  // -infinity
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                top[i & 3] = fmaxf(top[i & 3], __uint_as_float(s[c * 32 + i]));
-            }
-          }
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // The row's running maximum takes in `mx`.
+        auto grow = [&](float mx) __attribute__((always_inline)) {
           if (t == w.t0) {
             m = mx;
             mc = m == -INFINITY ? 0.f : m * c2;
@@ -444,25 +436,44 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
               }
               // The product of the tile before has to be done.
               ok = wait(&bars.o_done[g], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
-              if (!ok) break;
+              if (!ok) return;
               tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < d; c += 32) {
-                uint32_t o[32];
-                tmem_ld_x32(to + c, o);
-                tmem_wait_ld_x32(o);
+              for (int c = 0; c < d; c += 16) {  // (16 columns: the scores stay in registers)
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(to + c, o);
+                tmem_wait_ld_regs(o);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st_x32(to + c, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_x16(to + c, o);
               }
               tmem_wait_st();
             }
           }
-          const uint64_t c22 = pack2(c2, c2), mc2 = pack2(-mc, -mc);
-          uint64_t sum[2] = {0, 0};
+        };
+        if (keys == 128 && !p.a.mask_bits) {
+          // A whole tile: straight-line code.
+          if (warp_ok) {
+            uint32_t s[128];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c * 32 < cols) {
+            for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + c * 32, s + c * 32);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait_ld_x32(s + c * 32);
+            float top[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[4 + i]));
+#pragma unroll
+            for (int i = 8; i < 128; i += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                top[j] = max3(top[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]));
+            grow(max3(fmaxf(top[0], top[1]), top[2], top[3]));
+            if (!ok) break;
+            const uint64_t c22 = pack2(c2, c2), mc2 = pack2(-mc, -mc);
+            uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
               uint32_t h[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -473,16 +484,83 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
                         x, y);
                 x = exp2_approx(x);
                 y = exp2_approx(y);
+                sum[i & 3] = add2(sum[i & 3], pack2(x, y));
+                h[i] = round2<T>(x, y);
+              }
+              if (c == 3) {
+                // (By now the stores of the first half have arrived.)
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.p_half[g]));
+              }
+              tmem_st_x16(ts + c * 16, h);
+            }
+            float x, y;
+            unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+            l += x + y;
+            tmem_wait_st();
+          } else if (lane == 0) {
+            mbar_arrive(smem_u32(&bars.p_half[g]));
+          }
+        } else {
+          // A part of a tile, or a mask: two passes over the scores, 32 at a
+          // time.  (P of a chunk lies over scores read before it is stored.)
+          if (warp_ok) {
+            auto chunk = [&](int c, uint32_t* s) __attribute__((always_inline)) {
+              tmem_ld_x32(ts + c * 32, s);
+              tmem_wait_ld_x32(s);
+              uint32_t on = c == 0 ? word[0] : c == 1 ? word[1] : c == 2 ? word[2] : word[3];
+              const int rest = keys - c * 32;
+              if (rest < 32) on &= rest <= 0 ? 0u : (1u << rest) - 1u;
+              if (on != 0xFFFFFFFFu) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (!((on >> i) & 1u)) s[i] = 0xFF800000u;  // -infinity
+              }
+            };
+            const int chunks = (cols + 31) >> 5;
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+              uint32_t s[32];
+              chunk(c, s);
+              float top[4] = {mx, mx, mx, mx};
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  top[j] = max3(top[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]));
+              mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+            }
+            grow(mx);
+            if (!ok) break;
+            const uint64_t c22 = pack2(c2, c2), mc2 = pack2(-mc, -mc);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+              uint32_t s[32], h[16];
+              chunk(c, s);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, mc2),
+                        x, y);
+                x = exp2_approx(x);
+                y = exp2_approx(y);
                 sum[i & 1] = add2(sum[i & 1], pack2(x, y));
                 h[i] = round2<T>(x, y);
               }
               tmem_st_x16(ts + c * 16, h);
             }
+            float x, y;
+            unpack2(add2(sum[0], sum[1]), x, y);
+            l += x + y;
+            tmem_wait_st();
           }
-          float x, y;
-          unpack2(add2(sum[0], sum[1]), x, y);
-          l += x + y;
-          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.p_half[g]));
         }
         tc_fence_before();
         __syncwarp();
@@ -569,6 +647,8 @@ __global__ void __launch_bounds__(G * 128 + 64, G == 2 ? 1 : 2)
     // Shared memory stays until the last store has read it.
     if (quarter == 0 && lane == 0) bulk_wait_read_all();
     __syncwarp();
+  } else {
+    if (G == 2) give_registers<80>();
   }
   tc_fence_before();
   __syncthreads();
@@ -673,7 +753,7 @@ cudaError_t launch_one(const AttnFwdParams& p, int grid, size_t smem, cudaStream
   static std::atomic<size_t> configured[kMaxDevices];
   const cudaError_t err = raise_smem(attn_fwd_kernel<T, DP, G>, configured, smem);
   if (err != cudaSuccess) return err;
-  return launch_pdl(attn_fwd_kernel<T, DP, G>, dim3(grid), dim3(G * 128 + 64), smem, stream, p);
+  return launch_pdl(attn_fwd_kernel<T, DP, G>, dim3(grid), dim3(Layout<T, DP, G>::kThreads), smem, stream, p);
 }
 
 template <typename T>

@@ -65,29 +65,65 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs; A holds two K elements per
-// 32-bit column.  From a converged warp (see mma_f16_warp).
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                uint32_t idesc, uint32_t accumulate) {
+// Shared-memory matrix descriptors of 128-byte-swizzled operands.  The high
+// word is the same for all: 8-row groups 1024 bytes apart (stride offset),
+// descriptor version, layout.  The low word holds the address >> 4 and the
+// leading offset >> 4: unused for operands whose 128-byte rows run along K
+// (K-major); for rows that run along M or N (64 elements, one row per K), the
+// distance of blocks of 64 M or N.
+constexpr uint32_t kDescHigh = 64u | (1u << 14) | (2u << 29);
+constexpr uint32_t kLeadK = 1u << 16;
+__device__ __forceinline__ uint32_t lead_mn(uint32_t block_bytes) { return (block_bytes >> 4) << 16; }
+
+// Up to four consecutive K-steps (16 elements each) of D[tmem] (+)= A[smem]
+// B[smem]^T, both K-major: one elected lane issues them back to back.  Every
+// lane of the warp runs this with the same operands.  (One MMA per call, with
+// its descriptors built in C++, cost about 100 cycles of issue each, twice
+// what the tensor core takes for a 128x128x16 step.)
+__device__ __forceinline__ void mma_ss_x4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate, int steps) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred e, p, t, q;\n\t.reg .b64 a, b;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
+      "setp.gt.and.s32 q, %6, 1, e;\n\t"
+      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "setp.gt.and.s32 q, %6, 2, e;\n\t"
+      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
+      "setp.gt.and.s32 q, %6, 3, e;\n\t"
+      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(steps)
       : "memory");
 }
 
-// Descriptor bits of a 128-byte-swizzled operand whose 128-byte rows run
-// along K (K-major): 8-row groups 1024 bytes apart.  Add the address >> 4.
-constexpr uint64_t kDescK = (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-
-// Descriptor bits of a 128-byte-swizzled operand whose 128-byte rows (64
-// elements) run along M or N, one row per K: groups of 8 K are 1024 bytes
-// apart (stride offset), blocks of 64 M or N `block_bytes` (leading offset).
-__device__ __forceinline__ uint64_t desc_mn(uint32_t block_bytes) {
-  return (static_cast<uint64_t>(block_bytes >> 4) << 16) | (64ull << 32) | (1ull << 46) |
-         (2ull << 61);
+// The same with A in TMEM (two K elements per 32-bit column, a step is 8
+// columns) and B's rows running along N (a step is 16 rows of 128 bytes).
+__device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate, int steps) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
+      "setp.gt.and.s32 q, %6, 1, e;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, b, 128;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t"
+      "setp.gt.and.s32 q, %6, 2, e;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, b, 128;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t"
+      "setp.gt.and.s32 q, %6, 3, e;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, b, 128;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(steps)
+      : "memory");
 }
 
 // kind::f16 instruction descriptor: fp32 accumulators, both operands of one
@@ -95,6 +131,23 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t block_bytes) {
 __host__ __device__ constexpr uint32_t attn_idesc(bool bf16, uint32_t n, bool a_mn, bool b_mn) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) |
          ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Moves registers between the warpgroups of a block: the sum over the block's
+// warpgroups stays within what it was launched with.
+template <int kRegs>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
