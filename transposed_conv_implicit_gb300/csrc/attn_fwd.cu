@@ -49,20 +49,53 @@ struct Layout {
   // Pairs: three warpgroups, so that the softmax groups can take the third
   // one's registers: (208 + 208 + 80) * 128 <= 168 * 384.
   static constexpr int kThreads = G == 2 ? 384 : 192;
-  static constexpr int kMmaWarp = 4 * G, kLoadWarp = 4 * G + 1;
+  // One warp issues each group's products: a warp's issue is in order, and
+  // the waits, descriptors and commits of two groups together take longer
+  // than their products.
+  static constexpr int kMmaWarp = 4 * G, kLoadWarp = 5 * G;
   static constexpr uint32_t kQTile = 128u * 128u * kBlocks;
   static constexpr uint32_t kTmemCols = G == 2 ? 512 : 256;
 };
 
 constexpr int kMaxStages = 8;
 
+// Keys of tile t that some row of the item's row tiles attends, by the mask
+// alone.  One warp: lanes share out the tiles' mask rows.
+template <typename W>
+__device__ uint4 tile_any(const AttnFwdParams& p, const W& w, int t, int lane) {
+  const AttnShape& a = p.a;
+  uint4 any = make_uint4(0, 0, 0, 0);
+  for (int g = 0; g < w.tiles_here; ++g) {
+    int token, head;
+    w.place(g, &token, &head);
+    const int tokens = a.mask_q ? min(p.tile_heads > 1 ? p.tile_tokens : kAttnRows, a.q_len - token) : 1;
+    const int heads = a.mask_h ? p.tile_heads : 1;
+    const uint32_t* bits =
+        a.mask_bits + (w.b * a.mask_b + head * a.mask_h + token * a.mask_q) * a.mask_words +
+        (t * p.kv_box >> 5);
+    for (int h = 0; h < heads; ++h)
+      for (int i = lane; i < tokens; i += 32) {
+        const uint4 v = *reinterpret_cast<const uint4*>(bits + (h * a.mask_h + i * a.mask_q) * a.mask_words);
+        any.x |= v.x;
+        any.y |= v.y;
+        any.z |= v.z;
+        any.w |= v.w;
+      }
+  }
+  any.x = __reduce_or_sync(0xFFFFFFFFu, any.x);
+  any.y = __reduce_or_sync(0xFFFFFFFFu, any.y);
+  any.z = __reduce_or_sync(0xFFFFFFFFu, any.z);
+  any.w = __reduce_or_sync(0xFFFFFFFFu, any.w);
+  return any;
+}
+
 struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[2][2], q_empty[2][2];  // [group][stage]
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];  // p_half: of the first 64 keys
-  uint64_t drain;
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t turn[2];  // the groups' products take turns
+  uint64_t drain[2];
   SplitStart start;
-  uint32_t any[2][4][4];  // [group][warp]: keys of the tile that a row of the warp attends
   uint32_t tmem;
   int abort_flag;
 };
@@ -84,7 +117,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(smem_u32(&bars.kv_full[s]), 1);
-      mbar_init(smem_u32(&bars.kv_empty[s]), 1);
+      mbar_init(smem_u32(&bars.kv_empty[s]), G);
     }
     for (int g = 0; g < G; ++g) {
       for (int s = 0; s < p.q_stages; ++s) {
@@ -92,12 +125,14 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         mbar_init(smem_u32(&bars.q_empty[g][s]), 1);
       }
       mbar_init(smem_u32(&bars.s_full[g]), 1);
-      mbar_init(smem_u32(&bars.p_half[g]), 4);
       mbar_init(smem_u32(&bars.p_full[g]), 4);
       mbar_init(smem_u32(&bars.o_done[g]), 1);
       mbar_init(smem_u32(&bars.o_free[g]), 4);
     }
-    mbar_init(smem_u32(&bars.drain), 1);
+    for (int g = 0; g < G; ++g) {
+      mbar_init(smem_u32(&bars.turn[g]), 1);
+      mbar_init(smem_u32(&bars.drain[g]), 1);
+    }
     bars.abort_flag = 0;
     fence_barrier_init();
   }
@@ -206,162 +241,159 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
                             static_cast<uint32_t>((q / p.q_stages) & 1), limit / 8 + 1);
     }
     __syncwarp();
-  } else if (warp == L::kMmaWarp) {
+  } else if (warp >= L::kMmaWarp && warp < L::kMmaWarp + G) {
     // ------------------------------------------------------------ products
-    // The converged warp walks the MMAs; one elected lane issues each.
+    // The converged warp walks the MMAs of its group; one elected lane issues.
     if (G == 2) give_registers<80>();
+    const int g = warp - L::kMmaWarp;
     const int k_steps = (p.a.head_dim + 15) >> 4;
-    const uint32_t n_out = static_cast<uint32_t>(k_steps) * 16u;
     const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
-    const uint32_t idesc_o = attn_idesc(kBf16, n_out, false, true);
+    const uint32_t idesc_o = attn_idesc(kBf16, static_cast<uint32_t>(k_steps) * 16u, false, true);
     const uint32_t lead_v = lead_mn(kv_block);
-    const uint32_t q_lo = smem_u32(smem + p.off_q) >> 4, kv_lo = smem_u32(smem + p.off_kv) >> 4;
+    const uint32_t q_lo = (smem_u32(smem + p.off_q) + g * p.q_stages * L::kQTile) >> 4;
+    const uint32_t kv_lo = smem_u32(smem + p.off_kv) >> 4;
     const uint32_t kv_tile_lo = kv_tile >> 4, kv_block_lo = kv_block >> 4;
+    const uint32_t ts = tmem + g * 128, to = tmem + G * 128 + g * DP;
     bool ok = true;
     int stage = 0, qs = 0;
-    uint32_t phase = 0, q_phase = 0, tile_parity[2] = {0, 0}, item_count[2] = {0, 0};
+    uint32_t phase = 0, q_phase = 0, tiles = 0, items = 0;
     auto advance = [&]() {
       if (++stage == p.stages) {
         stage = 0;
         phase ^= 1u;
       }
     };
-    // S of group g for the item and key stage given.
-    auto scores = [&](int g, int q_stage, int k_stage, int cols) {
-      const uint32_t a = q_lo + ((g * p.q_stages + q_stage) * L::kQTile >> 4);
-      const uint32_t b = kv_lo + k_stage * kv_tile_lo;
-      const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
-      mma_ss_x4(tmem + g * 128, kLeadK | a, kLeadK | b, id, 0u, k_steps);
-      if (k_steps > 4)
-        mma_ss_x4(tmem + g * 128, kLeadK | (a + 1024u), kLeadK | (b + kv_block_lo), id, 1u, k_steps - 4);
-      mma_commit_warp(smem_u32(&bars.s_full[g]));
+    auto next_q = [&]() {
+      if (++qs == p.q_stages) {
+        qs = 0;
+        q_phase ^= 1u;
+      }
+    };
+    uint32_t turns = 0;  // strictly in turn: both groups have the same steps
+    auto take_turn = [&]() {
+      return G == 1 || wait(&bars.turn[g], (turns & 1u) ^ (g == 0 ? 1u : 0u), kAttnMmaTimeout);
+    };
+    auto end_turn = [&]() {
+      if (G == 2 && lane == 0) mbar_arrive(smem_u32(&bars.turn[g ^ 1]));
+      ++turns;
     };
     Walk<L::kSplit, AttnFwdParams> w(p, start);
-    int t = w.t0;
-    bool live = w.live;
-    int cols = 0;
+    // Items without a row tile for this group: their stages are passed on.
+    auto skip_absent = [&]() {
+      while (G == 2 && ok && w.live && g >= w.tiles_here) {
+        for (int i = 2 * (w.t1 - w.t0); ok && i > 0; --i) {
+          ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+          if (ok && lane == 0) mbar_arrive(smem_u32(&bars.kv_empty[stage]));
+          advance();
+          if (i & 1) {  // a step
+            ok = ok && take_turn();
+            if (ok) end_turn();
+          }
+        }
+        mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+        next_q();
+        w.next();
+      }
+    };
+    // S of key stage `k_stage`.
+    auto scores = [&](int k_stage, int cols, bool last) {
+      const uint32_t a = kLeadK | (q_lo + qs * (L::kQTile >> 4));
+      const uint32_t b = kLeadK | (kv_lo + k_stage * kv_tile_lo);
+      const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
+      mma_ss_x4(ts, a, b, id, 0u, k_steps);
+      if (k_steps > 4) mma_ss_x4(ts, a + 1024u, b + kv_block_lo, id, 1u, k_steps - 4);
+      mma_commit_warp(smem_u32(&bars.s_full[g]));
+      mma_commit_warp(smem_u32(&bars.kv_empty[k_stage]));
+      if (last) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+    };
+    skip_absent();
+    bool live = ok && w.live;
+    int t = w.t0, cols = 0;
     if (live) {
       cols = w.tile_cols(t);
-      ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
-      for (int g = 0; ok && g < w.tiles_here; ++g) {
-        ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout);
-        if (!ok) break;
+      ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout) &&
+           wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+      if (ok) {
         tc_fence_after();
-        scores(g, qs, stage, cols);
-        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+        scores(stage, cols, t + 1 == w.t1);
+        advance();
       }
-      if (ok) mma_commit_warp(smem_u32(&bars.kv_empty[stage]));
-      advance();
     }
     while (ok && live) {
       // This step's values, then the next step's keys.
-      const int v_stage = stage;
+      const int v_stage = stage, keys = w.tile_keys(t), this_cols = cols;
       const bool first = t == w.t0;
-      const int here = w.tiles_here, keys = w.tile_keys(t);
       ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
       if (!ok) break;
       advance();
-      // Group 1 absent: its query stage is free as it stands.
-      if (t + 1 == w.t1 && here < G) mma_commit_warp(smem_u32(&bars.q_empty[1][qs]));
-      bool more = true, next_item = false;
-      int next_qs = qs;
-      uint32_t next_qphase = q_phase;
-      if (t + 1 == w.t1) {
-        w.next();
-        more = w.live;
-        next_item = true;
-        t = w.t0;
-        if (++next_qs == p.q_stages) {
-          next_qs = 0;
-          next_qphase ^= 1u;
-        }
-      } else {
-        ++t;
-      }
-      const int k_stage = stage;
-      int next_cols = 0;
-      if (more) {
-        next_cols = w.tile_cols(t);
-        ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
-        if (!ok) break;
-        advance();
-      }
       // Values that no row of the CTA takes part with are cleared, so that
       // nothing they hold meets a zero of P: keys past the request's length
       // (past the tensor's end the load has filled zeros), and masked keys.
-      const bool masked = p.a.mask_bits != nullptr;
-      if (masked)
-        for (int g = 0; ok && g < here; ++g)
-          ok = wait(&bars.p_full[g], tile_parity[g], kAttnMmaTimeout);
-      if (!ok) break;
-      if (masked || (keys < cols && p.a.kv_lengths)) {
+      // (Each group's warp clears them; both write the same zeros.)
+      if (p.a.mask_bits || (keys < this_cols && p.a.kv_lengths)) {
+        uint4 any = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
+        if (p.a.mask_bits) any = tile_any(p, w, t, lane);
+        const uint32_t word[4] = {any.x, any.y, any.z, any.w};
         uint4* row0 = reinterpret_cast<uint4*>(smem + p.off_kv + v_stage * kv_tile);
-        for (int r0 = 0; r0 < cols; r0 += 32) {
-          uint32_t used = keys - r0 >= 32 ? 0xFFFFFFFFu : keys > r0 ? (1u << (keys - r0)) - 1u : 0u;
-          if (masked) {
-            uint32_t any = 0;
-            for (int g = 0; g < here; ++g)
-              for (int i = 0; i < 4; ++i) any |= bars.any[g][i][r0 >> 5];
-            used &= any;
-          }
-          const int r = r0 + lane;
-          if (r < cols && !((used >> lane) & 1u))
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 32 + lane;
+          if (r < this_cols && (r >= keys || !((word[i] >> lane) & 1u)))
 #pragma unroll
             for (int c = 0; c < L::kBlocks; ++c)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                row0[c * (kv_block >> 4) + r * 8 + i] = make_uint4(0, 0, 0, 0);
+              for (int j = 0; j < 8; ++j)
+                row0[c * (kv_block >> 4) + r * 8 + j] = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_shared();
         __syncwarp();
       }
-      for (int g = 0; ok && g < G; ++g) {
-        if (g < here) {
-          // The first 64 keys' products start before the others' P is there.
-          if (!masked) ok = wait(&bars.p_half[g], tile_parity[g], kAttnMmaTimeout);
-          if (ok && first) {
-            if (item_count[g] > 0)
-              ok = wait(&bars.o_free[g], (item_count[g] - 1) & 1u, kAttnMmaTimeout);
-            ++item_count[g];
-          }
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t o = tmem + G * 128 + g * DP;
-          const uint32_t b = kv_lo + v_stage * kv_tile_lo;
-          const int steps = cols >> 4;
-          mma_ts_x4(o, tmem + g * 128, lead_v | b, idesc_o, first ? 0u : 1u, steps);
-          if (!masked) {
-            ok = wait(&bars.p_full[g], tile_parity[g], kAttnMmaTimeout);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          tile_parity[g] ^= 1u;
-          if (steps > 4)
-            mma_ts_x4(o, tmem + g * 128 + 32, lead_v | (b + 512u), idesc_o, 1u, steps - 4);
-          mma_commit_warp(smem_u32(&bars.o_done[g]));
-        }
-        if (more && g < w.tiles_here) {
-          if (next_item) {
-            ok = wait(&bars.q_full[g][next_qs], next_qphase, kAttnMmaTimeout);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          scores(g, next_qs, k_stage, next_cols);
-          if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][next_qs]));
-        }
+      bool more = true, next_item = false;
+      if (t + 1 == w.t1) {
+        w.next();
+        next_q();
+        skip_absent();
+        if (!ok) break;
+        more = w.live;
+        next_item = true;
+        t = w.t0;
+      } else {
+        ++t;
       }
+      if (more) {
+        cols = w.tile_cols(t);
+        if (next_item) ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout);
+        ok = ok && wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+      }
+      if (ok && first) {
+        if (items > 0) ok = wait(&bars.o_free[g], (items - 1) & 1u, kAttnMmaTimeout);
+        ++items;
+      }
+      ok = ok && wait(&bars.p_full[g], tiles & 1u, kAttnMmaTimeout);
+      // The groups take turns with whole batches (P v, then the next S):
+      // products of two batches in between one another would end together,
+      // and both groups' exponentials would leave the tensor core idle.
+      ok = ok && take_turn();
       if (!ok) break;
+      tc_fence_after();
+      const uint32_t b = lead_v | (kv_lo + v_stage * kv_tile_lo);
+      const int steps = this_cols >> 4;
+      mma_ts_x4(to, ts, b, idesc_o, first ? 0u : 1u, steps);
+      if (steps > 4) mma_ts_x4(to, ts + 32, b + 512u, idesc_o, 1u, steps - 4);
+      mma_commit_warp(smem_u32(&bars.o_done[g]));
       mma_commit_warp(smem_u32(&bars.kv_empty[v_stage]));
-      if (more) mma_commit_warp(smem_u32(&bars.kv_empty[k_stage]));
-      qs = next_qs;
-      q_phase = next_qphase;
-      cols = next_cols;
+      ++tiles;
+      if (more) {
+        scores(stage, cols, t + 1 == w.t1);
+        advance();
+      }
+      end_turn();
       live = more;
     }
     if (!ok) {
       // Every MMA already issued must finish before TMEM is released.
-      mma_commit_warp(smem_u32(&bars.drain));
-      mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
+      mma_commit_warp(smem_u32(&bars.drain[g]));
+      mbar_wait_drain(smem_u32(&bars.drain[g]), 0, limit / 8 + 1);
     }
     __syncwarp();
   } else if (warp < 4 * G) {
@@ -410,14 +442,6 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         ok = wait(&bars.s_full[g], tiles & 1u, kAttnSoftmaxTimeout);
         if (!ok) break;
         tc_fence_after();
-        if (p.a.mask_bits) {
-          // (After the wait: the products have read the tile before's by then.)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, word[i]);
-            if (lane == 0) bars.any[g][quarter][i] = any;
-          }
-        }
         // The row's running maximum takes in `mx`.
         auto grow = [&](float mx) __attribute__((always_inline)) {
           if (t == w.t0) {
@@ -455,16 +479,26 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
           // A whole tile: straight-line code.
           if (warp_ok) {
             uint32_t s[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_x32(ts + c * 32, s + c * 32);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_wait_ld_x32(s + c * 32);
+            // (The second half of the scores loads beside the first one's maximum.)
+            tmem_ld_x32(ts, s);
+            tmem_ld_x32(ts + 32, s + 32);
+            tmem_wait_ld_x32(s);
+            tmem_wait_ld_x32(s + 32);
+            tmem_ld_x32(ts + 64, s + 64);
+            tmem_ld_x32(ts + 96, s + 96);
             float top[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               top[i] = fmaxf(__uint_as_float(s[i]), __uint_as_float(s[4 + i]));
 #pragma unroll
-            for (int i = 8; i < 128; i += 8)
+            for (int i = 8; i < 64; i += 8)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                top[j] = max3(top[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]));
+            tmem_wait_ld_x32(s + 64);
+            tmem_wait_ld_x32(s + 96);
+#pragma unroll
+            for (int i = 64; i < 128; i += 8)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 top[j] = max3(top[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]));
@@ -487,21 +521,12 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
                 sum[i & 3] = add2(sum[i & 3], pack2(x, y));
                 h[i] = round2<T>(x, y);
               }
-              if (c == 3) {
-                // (By now the stores of the first half have arrived.)
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars.p_half[g]));
-              }
               tmem_st_x16(ts + c * 16, h);
             }
             float x, y;
             unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
             l += x + y;
             tmem_wait_st();
-          } else if (lane == 0) {
-            mbar_arrive(smem_u32(&bars.p_half[g]));
           }
         } else {
           // A part of a tile, or a mask: two passes over the scores, 32 at a
@@ -558,9 +583,6 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
             l += x + y;
             tmem_wait_st();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars.p_half[g]));
         }
         tc_fence_before();
         __syncwarp();
