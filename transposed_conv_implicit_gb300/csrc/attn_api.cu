@@ -42,6 +42,10 @@ conv_status_t check_sizes(const cross_attention_args_t& a) {
       a.head_dim <= 0 || a.heads % a.kv_heads != 0)
     return CONV_ERR_INVALID_VALUE;
   if (a.head_dim % 8 != 0 || a.head_dim > kMaxHeadDim) return CONV_ERR_NOT_SUPPORTED;
+  // Rows count in 31 bits (padded to whole tiles).
+  const long long rows = (static_cast<long long>(a.q_len) + kAttnRows) * a.heads;
+  const long long states = (static_cast<long long>(a.kv_len) + kAttnRows) * a.kv_heads;
+  if (a.batch > 0 && std::max(rows, states) > 0x7FFFFFFFll / a.batch) return CONV_ERR_NOT_SUPPORTED;
   return CONV_OK;
 }
 
@@ -195,6 +199,9 @@ conv_status_t run_fwd(const AttnShape& s, const FwdPlan& f, char* ws, const Layo
   p.tile_tokens = f.tile_tokens;
   p.token_tiles = f.token_tiles;
   p.row_tiles = f.row_tiles;
+  p.div_pairs = make_fast_div(static_cast<uint32_t>((f.row_tiles + 1) / 2));
+  p.div_kv_heads = make_fast_div(static_cast<uint32_t>(s.kv_heads));
+  p.div_token_tiles = make_fast_div(static_cast<uint32_t>(f.token_tiles));
   p.kv_box = f.kv_box;
   p.items = f.items;
   p.item_rows = static_cast<long long>(s.kv_heads) * f.row_tiles;
@@ -241,6 +248,7 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   p.tile_tokens = f.tile_tokens;
   p.token_tiles = f.token_tiles;
   p.row_tiles = f.row_tiles;
+  p.div_token_tiles = make_fast_div(static_cast<uint32_t>(f.token_tiles));
   p.kv_box = f.kv_box;
   p.q_tiles = g.q_tiles;
   p.q_box = std::min(kAttnRows, std::max(16, (s.q_len + 15) / 16 * 16));

@@ -10,6 +10,7 @@
 
 #include "attn_params.h"
 #include "attn_ptx.cuh"
+#include "conv_params.h"
 
 namespace convgb300 {
 
@@ -186,19 +187,20 @@ struct Walk {
     pos -= t1 - t0;
   }
   __device__ void set_pair() {
-    if constexpr (kSplit) return;
-    else live = pos < p.items;
-    if (!live) return;
-    const int pairs = (p.row_tiles + 1) >> 1;
-    const long long bh = pos / pairs;
-    row_tile = 2 * static_cast<int>(pos - bh * pairs);
-    b = static_cast<int>(bh / p.a.kv_heads);
-    hk = static_cast<int>(bh - static_cast<long long>(b) * p.a.kv_heads);
-    tiles_here = min(2, p.row_tiles - row_tile);
-    n = valid_keys(p.a, b);
-    nt = key_tiles(n, p.kv_box);
-    t0 = 0;
-    t1 = nt;
+    if constexpr (!kSplit) {
+      live = pos < p.items;
+      if (!live) return;
+      const int item = static_cast<int>(pos);
+      const int bh = fast_div(item, p.div_pairs);
+      row_tile = 2 * (item - bh * static_cast<int>(p.div_pairs.d));
+      b = fast_div(bh, p.div_kv_heads);
+      hk = bh - b * p.a.kv_heads;
+      tiles_here = min(2, p.row_tiles - row_tile);
+      n = valid_keys(p.a, b);
+      nt = key_tiles(n, p.kv_box);
+      t0 = 0;
+      t1 = nt;
+    }
   }
   __device__ void next() {
     if (kSplit) {
@@ -222,7 +224,7 @@ struct Walk {
       *token = rt * p.tile_tokens;
       *head = hk * p.a.group;
     } else {
-      const int hg = rt / p.token_tiles;
+      const int hg = fast_div(rt, p.div_token_tiles);
       *token = (rt - hg * p.token_tiles) * kAttnRows;
       *head = hk * p.a.group + hg;
     }

@@ -92,7 +92,7 @@ __device__ uint4 tile_any(const AttnFwdParams& p, const W& w, int t, int lane) {
 struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[2][2], q_empty[2][2];  // [group][stage]
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_free[2];  // p_half: of the first 64 keys
   uint64_t turn[2];  // the groups' products take turns
   uint64_t drain[2];
   SplitStart start;
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         mbar_init(smem_u32(&bars.q_empty[g][s]), 1);
       }
       mbar_init(smem_u32(&bars.s_full[g]), 1);
+      mbar_init(smem_u32(&bars.p_half[g]), 4);
       mbar_init(smem_u32(&bars.p_full[g]), 4);
       mbar_init(smem_u32(&bars.o_done[g]), 1);
       mbar_init(smem_u32(&bars.o_free[g]), 4);
@@ -295,16 +296,14 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         w.next();
       }
     };
-    // S of key stage `k_stage`.
-    auto scores = [&](int k_stage, int cols, bool last) {
+    // S of key stage `k_stage`, into the group's columns.
+    auto scores = [&](int k_stage, int cols) {
       const uint32_t a = kLeadK | (q_lo + qs * (L::kQTile >> 4));
       const uint32_t b = kLeadK | (kv_lo + k_stage * kv_tile_lo);
       const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
       mma_ss_x4(ts, a, b, id, 0u, k_steps);
       if (k_steps > 4) mma_ss_x4(ts, a + 1024u, b + kv_block_lo, id, 1u, k_steps - 4);
       mma_commit_warp(smem_u32(&bars.s_full[g]));
-      mma_commit_warp(smem_u32(&bars.kv_empty[k_stage]));
-      if (last) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
     };
     skip_absent();
     bool live = ok && w.live;
@@ -315,7 +314,9 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
            wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
       if (ok) {
         tc_fence_after();
-        scores(stage, cols, t + 1 == w.t1);
+        scores(stage, cols);
+        mma_commit_warp(smem_u32(&bars.kv_empty[stage]));
+        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
         advance();
       }
     }
@@ -369,25 +370,36 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         if (items > 0) ok = wait(&bars.o_free[g], (items - 1) & 1u, kAttnMmaTimeout);
         ++items;
       }
-      ok = ok && wait(&bars.p_full[g], tiles & 1u, kAttnMmaTimeout);
-      // The groups take turns with whole batches (P v, then the next S):
-      // products of two batches in between one another would end together,
-      // and both groups' exponentials would leave the tensor core idle.
-      ok = ok && take_turn();
+      // The first 64 keys' products start before the others' P is there.  The
+      // groups take turns with whole batches (P v, then the next S): products
+      // of two batches in between one another would end together, and both
+      // groups' exponentials would leave the tensor core idle.
+      ok = ok && wait(&bars.p_half[g], tiles & 1u, kAttnMmaTimeout) && take_turn();
       if (!ok) break;
       tc_fence_after();
       const uint32_t b = lead_v | (kv_lo + v_stage * kv_tile_lo);
       const int steps = this_cols >> 4;
       mma_ts_x4(to, ts, b, idesc_o, first ? 0u : 1u, steps);
+      ok = wait(&bars.p_full[g], tiles & 1u, kAttnMmaTimeout);
+      if (!ok) break;
+      tc_fence_after();
       if (steps > 4) mma_ts_x4(to, ts + 32, b + 512u, idesc_o, 1u, steps - 4);
-      mma_commit_warp(smem_u32(&bars.o_done[g]));
-      mma_commit_warp(smem_u32(&bars.kv_empty[v_stage]));
       ++tiles;
+      // (The row's last product is announced at once, the others after the
+      // next scores, which the softmax waits for.)
+      if (!more || next_item) mma_commit_warp(smem_u32(&bars.o_done[g]));
+      const int k_stage = stage;
       if (more) {
-        scores(stage, cols, t + 1 == w.t1);
+        scores(stage, cols);
         advance();
+        if (!next_item) mma_commit_warp(smem_u32(&bars.o_done[g]));
       }
       end_turn();
+      mma_commit_warp(smem_u32(&bars.kv_empty[v_stage]));
+      if (more) {
+        mma_commit_warp(smem_u32(&bars.kv_empty[k_stage]));
+        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+      }
       live = more;
     }
     if (!ok) {
@@ -407,22 +419,18 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     const float c2 = p.scale_log2;
     const int d = p.a.head_dim;
     uint8_t* stage_out = smem + p.off_out + g * 16384;
+    // The thread's row of every tile: (token, head) from the tile's first.
+    const int row_token = p.tile_heads > 1 ? r / p.tile_heads : r;
+    const int row_head = p.tile_heads > 1 ? r - row_token * p.tile_heads : 0;
     uint32_t tiles = 0;  // S tiles seen: barrier parity
     bool ok = true;
     for (Walk<L::kSplit, AttnFwdParams> w(p, start); ok && w.live; w.next()) {
       if (g >= w.tiles_here) continue;
       int token, head;
       w.place(g, &token, &head);
-      bool row_ok = true;
-      if (p.tile_heads > 1) {
-        const int dt = r / p.tile_heads;
-        row_ok = dt < p.tile_tokens;
-        token += dt;
-        head += r - dt * p.tile_heads;
-      } else {
-        token += r;
-      }
-      row_ok = row_ok && token < p.a.q_len;
+      token += row_token;
+      head += row_head;
+      const bool row_ok = row_token < p.tile_tokens && token < p.a.q_len;
       const bool warp_ok = __any_sync(0xFFFFFFFFu, row_ok);
       const uint32_t* bits = nullptr;
       if (p.a.mask_bits && row_ok)
@@ -521,12 +529,21 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
                 sum[i & 3] = add2(sum[i & 3], pack2(x, y));
                 h[i] = round2<T>(x, y);
               }
+              if (c == 3) {
+                // (By now the stores of the first half have arrived.)
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.p_half[g]));
+              }
               tmem_st_x16(ts + c * 16, h);
             }
             float x, y;
             unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
             l += x + y;
             tmem_wait_st();
+          } else if (lane == 0) {
+            mbar_arrive(smem_u32(&bars.p_half[g]));
           }
         } else {
           // A part of a tile, or a mask: two passes over the scores, 32 at a
@@ -583,6 +600,9 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
             l += x + y;
             tmem_wait_st();
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars.p_half[g]));
         }
         tc_fence_before();
         __syncwarp();

@@ -6,6 +6,8 @@
 
 #include <cstdint>
 
+#include "conv_params.h"
+
 namespace convgb300 {
 
 // What every cross-attention kernel knows about the call.  Strides are in
@@ -47,6 +49,7 @@ struct AttnFwdParams {  // aligned like CUtensorMap
   int tile_heads, tile_tokens;
   int token_tiles;      // tiles along the tokens
   int row_tiles;        // row tiles of one key head
+  FastDiv div_pairs, div_kv_heads, div_token_tiles;  // of pairs of row tiles, ...
   int kv_box;           // keys per tile (multiple of 16, <= 128)
   int stages;           // key/value ring
   int q_stages;
@@ -77,6 +80,7 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   AttnShape a;
   int q_mul[2], do_mul[2], k_mul[2], v_mul[2];
   int tile_heads, tile_tokens, token_tiles, row_tiles;
+  FastDiv div_token_tiles;
   int kv_box;           // keys per tile (multiple of 16, <= 128)
   int q_box;            // dk, dv: tokens per box
   int q_tiles;          // tiles of 128 tokens
