@@ -269,6 +269,10 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   const uint32_t block = wide ? 32768 : 16384;  // 128 rows
   if (queries && keys) {
     // Row statistics.
+    p.div_heads = make_fast_div(static_cast<uint32_t>(s.heads));
+    p.div_tokens = make_fast_div(static_cast<uint32_t>(g.q_tiles * kAttnRows));
+    p.div_kv_heads = make_fast_div(static_cast<uint32_t>(s.kv_heads));
+    p.div_keys = make_fast_div(static_cast<uint32_t>(s.kv_len));
     const long long rows = static_cast<long long>(s.batch) * s.heads * g.q_tiles * kAttnRows;
     p.row_blocks = static_cast<int>(std::min<long long>(kAttnNormBlocks, (rows + 63) / 64));
     const long long values = static_cast<long long>(s.batch) * s.kv_heads * s.kv_len;

@@ -83,7 +83,6 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   int width = 1;
   while (width < words) width <<= 1;
   const int at = lane & (width - 1), slot = lane / width, slots = 32 / width;
-  const long long padded = static_cast<long long>(p.q_tiles) * kAttnRows;
   float norm = 0.f;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -91,48 +90,66 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   const int block = values ? blockIdx.x - p.row_blocks : blockIdx.x;
   const int blocks = values ? gridDim.x - p.row_blocks : p.row_blocks;
   const int heads = values ? a.kv_heads : a.heads;
-  const long long length = values ? a.kv_len : padded;
-  const long long rows = length * heads * a.batch;  // tokens outermost within a batch
-  const long long step = static_cast<long long>(blocks) * 8 * slots;
-  for (long long row0 = (static_cast<long long>(block) * 8 + warp) * slots; row0 < rows;
-       row0 += step) {
-    const long long row = row0 + slot;
-    const long long bt = row / heads;
-    const int h = static_cast<int>(row - bt * heads);
-    const int b = static_cast<int>(bt / length);
-    const long long t = bt - b * length;
-    const bool in = row < rows;
-    float dot = 0.f, sq = 0.f;
-    if (values) {
-      if (in && at < words && t < valid_keys(a, b)) {
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + b * a.vs[0] +
-                                                        t * a.vs[1] + h * a.vs[2] + at * 8);
-        sq = dot8<T>(v, v);
+  const int length = values ? a.kv_len : p.q_tiles * kAttnRows;
+  const FastDiv div_heads = values ? p.div_kv_heads : p.div_heads;
+  const FastDiv div_length = values ? p.div_keys : p.div_tokens;
+  const int rows = length * heads * a.batch;  // heads innermost, then tokens
+  constexpr int kUnroll = 4;                  // rows in flight per lane
+  const int step = blocks * 8 * slots;
+  for (int row0 = (block * 8 + warp) * slots; row0 < rows; row0 += kUnroll * step) {
+    uint4 x[kUnroll], y[kUnroll];
+    int h[kUnroll], b[kUnroll], t[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      // (Counted unsigned: the rows past the end may pass 2^31.)
+      const unsigned row = static_cast<unsigned>(row0) + u * static_cast<unsigned>(step) + slot;
+      const bool in = row < static_cast<unsigned>(rows);
+      const int bt = fast_div(in ? static_cast<int>(row) : 0, div_heads);
+      h[u] = (in ? static_cast<int>(row) : 0) - bt * heads;
+      b[u] = fast_div(bt, div_length);
+      t[u] = in ? bt - b[u] * length : -1;
+      x[u] = y[u] = make_uint4(0, 0, 0, 0);
+      if (t[u] < 0 || at >= words) continue;
+      if (values) {
+        if (t[u] < valid_keys(a, b[u]))
+          x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + b[u] * a.vs[0] +
+                                                 t[u] * a.vs[1] + h[u] * a.vs[2] + at * 8);
+      } else if (t[u] < a.q_len) {
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + b[u] * a.dos[0] +
+                                               t[u] * a.dos[1] + h[u] * a.dos[2] + at * 8);
+        y[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + b[u] * a.os[0] +
+                                               t[u] * a.os[1] + h[u] * a.os[2] + at * 8);
       }
-    } else if (in && at < words && t < a.q_len) {
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + b * a.dos[0] +
-                                                      t * a.dos[1] + h * a.dos[2] + at * 8);
-      const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + b * a.os[0] +
-                                                      t * a.os[1] + h * a.os[2] + at * 8);
-      dot = dot8<T>(x, y);
-      if (p.norms) sq = dot8<T>(x, x);
     }
-    for (int o = width >> 1; o; o >>= 1) {
-      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-      sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
+    float dot[kUnroll], sq[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      dot[u] = dot8<T>(x[u], y[u]);
+      sq[u] = p.norms ? dot8<T>(x[u], x[u]) : 0.f;
     }
-    if (!values && in && at == 0) {
-      float lse2 = INFINITY;
-      if (t < a.q_len) {
-        const float lse = a.lse[(static_cast<long long>(b) * a.heads + h) * a.q_len + t];
-        if (lse != -INFINITY) lse2 = lse * kLog2e;
+    for (int o = width >> 1; o; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], o);
+        if (p.norms) sq[u] += __shfl_xor_sync(0xFFFFFFFFu, sq[u], o);
       }
-      if (lse2 == INFINITY) dot = sq = 0.f;
-      const long long tile = (static_cast<long long>(b) * a.heads + h) * p.q_tiles + (t >> 7);
-      p.stats[tile * 256 + (t & 127)] = lse2;
-      p.stats[tile * 256 + 128 + (t & 127)] = dot;
+    if (at != 0) continue;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (t[u] < 0) continue;
+      if (!values) {
+        float lse2 = INFINITY;
+        if (t[u] < a.q_len) {
+          const float lse = a.lse[(static_cast<long long>(b[u]) * a.heads + h[u]) * a.q_len + t[u]];
+          if (lse != -INFINITY) lse2 = lse * kLog2e;
+        }
+        if (lse2 == INFINITY) dot[u] = sq[u] = 0.f;
+        const long long tile = (static_cast<long long>(b[u]) * a.heads + h[u]) * p.q_tiles + (t[u] >> 7);
+        p.stats[tile * 256 + (t[u] & 127)] = lse2;
+        p.stats[tile * 256 + 128 + (t[u] & 127)] = dot[u];
+      }
+      if (sq[u] < INFINITY) norm = fmaxf(norm, sq[u]);  // (NaN compares false)
     }
-    if (in && at == 0 && sq < INFINITY) norm = fmaxf(norm, sq);  // (NaN compares false)
   }
   if (!p.norms) return;
   for (int o = 16; o; o >>= 1) norm = fmaxf(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
@@ -1147,33 +1164,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
 // ------------------------------------------------------------------ joins
 // Adds the shares of tiles that the launches before cut, in order, and clears
-// the gradients of keys past each request's length.  One block per tile: the
-// row tiles of dq first, then the key tiles of dk and dv.
+// the gradients of keys past each request's length.  Blocks of kJoinRows rows:
+// the row tiles of dq first, then the key tiles of dk and dv.
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
     attn_bwd_join_kernel(const __grid_constant__ AttnBwdParams p, int q_ctas, int kv_ctas,
                          long long q_blocks) {
-  __shared__ long long sums[2][32];
+  __shared__ JoinSlots join;
   __shared__ float factor;
   const AttnShape& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = lane * 4;
+  const int r0 = blockIdx.y * kJoinRows + warp * kJoinUnroll;
   grid_dependency_wait();
   grid_launch_dependents();
   if (warp == 0) {
     const float f = ds_scale(p, lane);
     if (lane == 0) factor = a.scale / f;
   }
-  __syncthreads();
   long long before, total;
   if (blockIdx.x < q_blocks) {
     const int b = static_cast<int>(blockIdx.x / p.item_rows);
     const int item = static_cast<int>(blockIdx.x - b * p.item_rows);
-    split_prefix(a.batch, row_steps_uniform(p), b, sums, [&](int i) { return row_steps(p, i); },
+    split_prefix(a.batch, row_steps_uniform(p), b, join.sums, [&](int i) { return row_steps(p, i); },
                  &before, &total);
     const int nt = key_tiles(valid_keys(a, b), p.kv_box);
-    const long long s0 = before + static_cast<long long>(item) * nt;
-    const int c0 = share_of(total, q_ctas, s0), c1 = share_of(total, q_ctas, s0 + nt - 1);
-    if (c0 == c1) return;
+    list_slots(join, total, q_ctas, before + static_cast<long long>(item) * nt, nt);
+    const int shares = join.count;
+    if (shares == 0) return;
     const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
     int token0, head0, rows;
     if (p.tile_heads > 1) {
@@ -1186,20 +1203,28 @@ __global__ void __launch_bounds__(256)
       head0 = hk * a.group + hg;
       rows = min(kAttnRows, a.q_len - token0);
     }
-    for (int r = warp; r < rows; r += 8) {
-      if (d0 >= a.head_dim) break;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = c0; c <= c1; ++c) {
-        if (share_begin(total, q_ctas, c) == share_begin(total, q_ctas, c + 1)) continue;
+    if (r0 >= rows || d0 >= a.head_dim) return;
+    float4 acc[kJoinUnroll];
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int c = 0; c < shares; ++c)
+#pragma unroll
+      for (int u = 0; u < kJoinUnroll; ++u) {
         const float4 v = *reinterpret_cast<const float4*>(
-            p.part_q + ((2ll * c + (c == c0 ? 1 : 0)) * kAttnRows + r) * 128 + d0);
-        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+            p.part_q + (static_cast<long long>(join.slots[c]) * kAttnRows + min(r0 + u, rows - 1)) * 128 + d0);
+        acc[u].x += v.x; acc[u].y += v.y; acc[u].z += v.z; acc[u].w += v.w;
       }
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) {
+      const int r = r0 + u;
+      if (r >= rows) break;
       const int dt = p.tile_heads > 1 ? r / p.tile_heads : r;
       const int token = token0 + dt, head = p.tile_heads > 1 ? head0 + r - dt * p.tile_heads : head0;
       *reinterpret_cast<uint2*>(static_cast<T*>(a.dq) + b * a.dqs[0] + token * a.dqs[1] +
                                 head * a.dqs[2] + d0) =
-          make_uint2(round2<T>(acc.x * factor, acc.y * factor), round2<T>(acc.z * factor, acc.w * factor));
+          make_uint2(round2<T>(acc[u].x * factor, acc[u].y * factor),
+                     round2<T>(acc[u].z * factor, acc[u].w * factor));
     }
     return;
   }
@@ -1210,30 +1235,42 @@ __global__ void __launch_bounds__(256)
   const int b = static_cast<int>(bh / a.kv_heads), hk = static_cast<int>(bh - static_cast<long long>(b) * a.kv_heads);
   const int n = p.item_steps > 0 ? valid_keys(a, b) : 0, tiles = (n + kAttnRows - 1) / kAttnRows;
   const int rows = min(kAttnRows, a.kv_len - tile * kAttnRows);
-  int c0 = 0, c1 = -1;
+  int shares = 0;
   if (tile < tiles) {
-    split_prefix(a.batch, key_steps_uniform(p), b, sums, [&](int i) { return key_steps(p, i); },
+    split_prefix(a.batch, key_steps_uniform(p), b, join.sums, [&](int i) { return key_steps(p, i); },
                  &before, &total);
-    const long long s0 = before + (static_cast<long long>(hk) * tiles + tile) * p.item_steps;
-    c0 = share_of(total, kv_ctas, s0);
-    c1 = share_of(total, kv_ctas, s0 + p.item_steps - 1);
-    if (c0 == c1) return;
+    list_slots(join, total, kv_ctas, before + (static_cast<long long>(hk) * tiles + tile) * p.item_steps,
+               p.item_steps);
+    shares = join.count;
+    if (shares == 0) return;
+  } else {
+    __syncthreads();  // (factor)
   }
-  for (int i = warp; i < 2 * rows; i += 8) {
-    if (d0 >= a.head_dim) break;
-    const int half = i & 1, r = i >> 1, j = tile * kAttnRows + r;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      if (share_begin(total, kv_ctas, c) == share_begin(total, kv_ctas, c + 1)) continue;
-      const float4 v = *reinterpret_cast<const float4*>(
-          p.part_kv + (((2ll * c + (c == c0 ? 1 : 0)) * 2 + half) * kAttnRows + r) * 128 + d0);
-      acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
-    }
+  if (r0 >= rows || d0 >= a.head_dim) return;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float4 acc[kJoinUnroll];
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int c = 0; c < shares; ++c)
+#pragma unroll
+      for (int u = 0; u < kJoinUnroll; ++u) {
+        const float4 v = *reinterpret_cast<const float4*>(
+            p.part_kv +
+            ((static_cast<long long>(join.slots[c]) * 2 + half) * kAttnRows + min(r0 + u, rows - 1)) * 128 + d0);
+        acc[u].x += v.x; acc[u].y += v.y; acc[u].z += v.z; acc[u].w += v.w;
+      }
     const float f = half ? factor : p.p_unscale;
-    T* dst = half ? static_cast<T*>(a.dk) + b * a.dks[0] + j * a.dks[1] + hk * a.dks[2]
-                  : static_cast<T*>(a.dv) + b * a.dvs[0] + j * a.dvs[1] + hk * a.dvs[2];
-    *reinterpret_cast<uint2*>(dst + d0) =
-        make_uint2(round2<T>(acc.x * f, acc.y * f), round2<T>(acc.z * f, acc.w * f));
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) {
+      if (r0 + u >= rows) break;
+      const int j = tile * kAttnRows + r0 + u;
+      T* dst = half ? static_cast<T*>(a.dk) + b * a.dks[0] + j * a.dks[1] + hk * a.dks[2]
+                    : static_cast<T*>(a.dv) + b * a.dvs[0] + j * a.dvs[1] + hk * a.dvs[2];
+      *reinterpret_cast<uint2*>(dst + d0) =
+          make_uint2(round2<T>(acc[u].x * f, acc[u].y * f), round2<T>(acc[u].z * f, acc[u].w * f));
+    }
   }
 }
 
@@ -1285,11 +1322,11 @@ cudaError_t launch_attn_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaS
 cudaError_t launch_attn_bwd_join(const AttnBwdParams& p, int q_ctas, int kv_ctas,
                                  long long q_blocks, long long kv_blocks, cudaStream_t stream) {
   if (q_blocks + kv_blocks == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>(q_blocks + kv_blocks));
-  return p.a.dtype == 0 ? launch_pdl(attn_bwd_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
-                                     p, q_ctas, kv_ctas, q_blocks)
-                        : launch_pdl(attn_bwd_join_kernel<__half>, grid, dim3(256), 0, stream, p,
-                                     q_ctas, kv_ctas, q_blocks);
+  const dim3 grid(static_cast<unsigned>(q_blocks + kv_blocks), kAttnRows / kJoinRows);
+  return p.a.dtype == 0 ? launch_pdl(attn_bwd_join_kernel<__nv_bfloat16>, grid, dim3(kJoinThreads), 0,
+                                     stream, p, q_ctas, kv_ctas, q_blocks)
+                        : launch_pdl(attn_bwd_join_kernel<__half>, grid, dim3(kJoinThreads), 0, stream,
+                                     p, q_ctas, kv_ctas, q_blocks);
 }
 
 }  // namespace convgb300

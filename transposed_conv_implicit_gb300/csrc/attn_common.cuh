@@ -234,4 +234,44 @@ struct Walk {
   __device__ int tile_cols(int t) const { return max(16, (tile_keys(t) + 15) & ~15); }
 };
 
+// Joining the shares of tiles that a launch cut: one block takes kJoinRows
+// rows of a tile, each warp kJoinUnroll at a time, and the shares' slots are
+// listed once per block, so that the rows' reads are all in flight together
+// (with the slots found row by row, in 64-bit divisions, the join of a 1021 x
+// 523 training pass took 112 us).
+constexpr int kJoinRows = 32, kJoinUnroll = 4, kJoinThreads = 256;
+constexpr int kMaxShares = 320;  // CTAs of a launch: two per SM at most
+
+struct JoinSlots {
+  long long sums[2][32];
+  int slots[kMaxShares];
+  int count;  // 0: the tile was written whole
+};
+
+// Slots of the shares of steps [s0, s0 + steps) of `total`, in order.
+__device__ __forceinline__ void list_slots(JoinSlots& j, long long total, int ctas, long long s0,
+                                           long long steps) {
+  __shared__ int range[2];
+  if (threadIdx.x == 0) {
+    range[0] = share_of(total, ctas, s0);
+    range[1] = share_of(total, ctas, s0 + steps - 1);
+    j.count = 0;
+  }
+  __syncthreads();
+  const int c0 = range[0], c1 = range[1];
+  if (c0 == c1) return;
+  if (total >= ctas) {  // every CTA has a share
+    for (int c = c0 + threadIdx.x; c <= c1; c += blockDim.x)
+      j.slots[c - c0] = 2 * c + (c == c0 ? 1 : 0);
+    if (threadIdx.x == 0) j.count = c1 - c0 + 1;
+  } else if (threadIdx.x == 0) {
+    int n = 0;
+    for (int c = c0; c <= c1; ++c)
+      if (share_begin(total, ctas, c) != share_begin(total, ctas, c + 1))
+        j.slots[n++] = 2 * c + (c == c0 ? 1 : 0);
+    j.count = n;
+  }
+  __syncthreads();
+}
+
 }  // namespace convgb300

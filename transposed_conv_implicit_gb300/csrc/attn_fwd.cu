@@ -700,12 +700,12 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
   }
 }
 
-// Joins the shares of row tiles that a split launch cut, in order: one warp
-// per row, weights 2^(m_f - max m) over the shares' maxima.
+// Joins the shares of row tiles that a split launch cut, in order, with
+// weights 2^(m_f - max m) over the shares' maxima.
 template <typename T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
     attn_join_kernel(const __grid_constant__ AttnFwdParams p, int ctas) {
-  __shared__ long long sums[2][32];
+  __shared__ JoinSlots join;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const AttnShape& a = p.a;
   const int b = static_cast<int>(blockIdx.x / p.item_rows);
@@ -713,12 +713,12 @@ __global__ void __launch_bounds__(128)
   grid_dependency_wait();
   grid_launch_dependents();
   long long before, total;
-  split_prefix(a.batch, row_steps_uniform(p), b, sums, [&](int i) { return row_steps(p, i); },
+  split_prefix(a.batch, row_steps_uniform(p), b, join.sums, [&](int i) { return row_steps(p, i); },
                &before, &total);
   const int nt = key_tiles(valid_keys(a, b), p.kv_box);
-  const long long s0 = before + static_cast<long long>(item) * nt;
-  const int c0 = share_of(total, ctas, s0), c1 = share_of(total, ctas, s0 + nt - 1);
-  if (c0 == c1) return;  // written whole
+  list_slots(join, total, ctas, before + static_cast<long long>(item) * nt, nt);
+  const int shares = join.count;
+  if (shares == 0) return;
   const int hk = item / p.row_tiles, rt = item - hk * p.row_tiles;
   int token0, head0, rows;
   if (p.tile_heads > 1) {
@@ -732,42 +732,57 @@ __global__ void __launch_bounds__(128)
     rows = min(kAttnRows, a.q_len - token0);
   }
   const int d0 = lane * 4;
-  for (int r = warp; r < rows; r += 4) {
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      if (share_begin(total, ctas, c) == share_begin(total, ctas, c + 1)) continue;  // no steps
-      const long long slot = 2ll * c + (c == c0 ? 1 : 0);
-      m = fmaxf(m, p.part_stat[(slot * kAttnRows + r) * 2]);
+  const int r0 = blockIdx.y * kJoinRows + warp * kJoinUnroll;
+  if (r0 >= rows) return;
+  // (Rows past the tile's read its last row again and write nothing.)
+  float m[kJoinUnroll], l[kJoinUnroll];
+  float4 acc[kJoinUnroll];
+#pragma unroll
+  for (int u = 0; u < kJoinUnroll; ++u) {
+    m[u] = -INFINITY;
+    l[u] = 0.f;
+    acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int c = lane; c < shares; c += 32)
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) {
+      const long long row = static_cast<long long>(join.slots[c]) * kAttnRows + min(r0 + u, rows - 1);
+      m[u] = fmaxf(m[u], p.part_stat[row * 2]);
     }
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-      if (share_begin(total, ctas, c) == share_begin(total, ctas, c + 1)) continue;
-      const long long row = (2ll * c + (c == c0 ? 1 : 0)) * kAttnRows + r;
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) m[u] = fmaxf(m[u], __shfl_xor_sync(0xFFFFFFFFu, m[u], o));
+#pragma unroll 2
+  for (int c = 0; c < shares; ++c)
+#pragma unroll
+    for (int u = 0; u < kJoinUnroll; ++u) {
+      const long long row = static_cast<long long>(join.slots[c]) * kAttnRows + min(r0 + u, rows - 1);
       const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
       // A share whose pairs are all left out holds zeros.
-      const float f = st.x == -INFINITY && st.y == 0.f ? 0.f : exp2_approx(st.x - m);
-      l = fmaf(f, st.y, l);
+      const float f = st.x == -INFINITY && st.y == 0.f ? 0.f : exp2_approx(st.x - m[u]);
+      l[u] = fmaf(f, st.y, l[u]);
       if (d0 < a.head_dim) {
         const float4 v = *reinterpret_cast<const float4*>(p.part_out + row * 128 + d0);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+        acc[u].x = fmaf(f, v.x, acc[u].x);
+        acc[u].y = fmaf(f, v.y, acc[u].y);
+        acc[u].z = fmaf(f, v.z, acc[u].z);
+        acc[u].w = fmaf(f, v.w, acc[u].w);
       }
     }
+#pragma unroll
+  for (int u = 0; u < kJoinUnroll; ++u) {
+    const int r = r0 + u;
+    if (r >= rows) break;
     const int dt = p.tile_heads > 1 ? r / p.tile_heads : r;
     const int token = token0 + dt, head = p.tile_heads > 1 ? head0 + r - dt * p.tile_heads : head0;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (d0 < a.head_dim) {
-      uint2* dst = reinterpret_cast<uint2*>(static_cast<T*>(a.out_w) + b * a.os[0] +
-                                            token * a.os[1] + head * a.os[2] + d0);
-      *dst = make_uint2(round2<T>(acc.x * inv, acc.y * inv), round2<T>(acc.z * inv, acc.w * inv));
-    }
+    const float inv = l[u] == 0.f ? 0.f : 1.f / l[u];
+    if (d0 < a.head_dim)
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out_w) + b * a.os[0] + token * a.os[1] +
+                                head * a.os[2] + d0) =
+          make_uint2(round2<T>(acc[u].x * inv, acc[u].y * inv), round2<T>(acc[u].z * inv, acc[u].w * inv));
     if (a.lse && lane == 0)
       a.lse[(static_cast<long long>(b) * a.heads + head) * a.q_len + token] =
-          l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));
+          l[u] == 0.f ? -INFINITY : fmaf(m[u], kLn2, logf(l[u]));
   }
 }
 
@@ -810,8 +825,10 @@ cudaError_t launch_type(const AttnFwdParams& p, bool split, int grid, size_t sme
              : launch_one<T, 64, 1>(p, grid, smem, stream);
   // Rows of one key tile are never cut.
   if (err != cudaSuccess || p.a.kv_len <= p.kv_box) return err;
-  return launch_pdl(attn_join_kernel<T>, dim3(static_cast<unsigned>(p.item_rows * p.a.batch)),
-                    dim3(128), 0, stream, p, grid);
+  const int rows = p.tile_heads * p.tile_tokens;
+  return launch_pdl(attn_join_kernel<T>,
+                    dim3(static_cast<unsigned>(p.item_rows * p.a.batch), (rows + kJoinRows - 1) / kJoinRows),
+                    dim3(kJoinThreads), 0, stream, p, grid);
 }
 
 }  // namespace

@@ -81,6 +81,7 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   int q_mul[2], do_mul[2], k_mul[2], v_mul[2];
   int tile_heads, tile_tokens, token_tiles, row_tiles;
   FastDiv div_token_tiles;
+  FastDiv div_heads, div_tokens, div_kv_heads, div_keys;  // (tokens: padded to whole tiles)
   int kv_box;           // keys per tile (multiple of 16, <= 128)
   int q_box;            // dk, dv: tokens per box
   int q_tiles;          // tiles of 128 tokens
