@@ -253,6 +253,7 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   p.q_tiles = g.q_tiles;
   p.q_box = std::min(kAttnRows, std::max(16, (s.q_len + 15) / 16 * 16));
   p.item_steps = g.item_steps;
+  p.last_cols = (s.q_len - std::max(0, g.q_tiles - 1) * kAttnRows + 15) / 16 * 16;
   p.item_rows = static_cast<long long>(s.kv_heads) * f.row_tiles;
   p.scale_log2 = s.scale * 1.44269504088896341f;
   p.p_shift = g.norms ? 15.f : 0.f;

@@ -69,8 +69,9 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y) {
   return s;
 }
 
-// stats[b][h][token tile][2][128]: lse in log2 units (+inf for queries without
-// keys and past the end, which makes p zero) and delta.  With norms: the
+// stats[b][h][token tile][2][128]: minus lse in log2 units, plus p_shift (-inf
+// for queries without keys and past the end, which makes p zero), and minus
+// delta: as the products' sums take them.  With norms: the
 // largest |do| row of each block, then (kNormBlocks blocks on) |v| row, both
 // squared; rows that take no part are left out.
 template <typename T>
@@ -138,15 +139,15 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     for (int u = 0; u < kUnroll; ++u) {
       if (t[u] < 0) continue;
       if (!values) {
-        float lse2 = INFINITY;
+        float lse2 = -INFINITY;
         if (t[u] < a.q_len) {
           const float lse = a.lse[(static_cast<long long>(b[u]) * a.heads + h[u]) * a.q_len + t[u]];
-          if (lse != -INFINITY) lse2 = lse * kLog2e;
+          if (lse != -INFINITY) lse2 = p.p_shift - lse * kLog2e;
         }
-        if (lse2 == INFINITY) dot[u] = sq[u] = 0.f;
+        if (lse2 == -INFINITY) dot[u] = sq[u] = 0.f;
         const long long tile = (static_cast<long long>(b[u]) * a.heads + h[u]) * p.q_tiles + (t[u] >> 7);
         p.stats[tile * 256 + (t[u] & 127)] = lse2;
-        p.stats[tile * 256 + 128 + (t[u] & 127)] = dot[u];
+        p.stats[tile * 256 + 128 + (t[u] & 127)] = -dot[u];
       }
       if (sq[u] < INFINITY) norm = fmaxf(norm, sq[u]);  // (NaN compares false)
     }
@@ -442,7 +443,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         k_stage = xs;
         rows_by_keys(tmem + ((count + 1) & 1u) * 128, a_lo, x_lo + xs * tile_lo, cols);
         mma_commit_warp(smem_u32(&bars.s_full[(count + 1) & 1u]));
-        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
         if (++xs == p.x_stages) {
           xs = 0;
           xph ^= 1u;
@@ -455,12 +455,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         rows_by_keys(t_dp, a_lo + (kATile >> 4), y_lo + ys * tile_lo, cols);
         mma_commit_warp(smem_u32(&bars.dp_full));
-        mma_commit_warp(smem_u32(&bars.y_empty[ys]));
-        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
-        if (++ys == p.y_stages) {
-          ys = 0;
-          yph ^= 1u;
-        }
       }
       ok = wait(&bars.ds_full[count & 1u], (count >> 1) & 1u, kAttnMmaTimeout);
       if (ok && first) {
@@ -488,8 +482,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint32_t kb = lead_k | (x_lo + this_k * tile_lo);
       mma_ts_x4(t_acc, ds, kb, idesc_acc, first ? 0u : 1u, steps);
       if (steps > 4) mma_ts_x4(t_acc, ds + 64, kb + 512u, idesc_acc, 1u, steps - 4);
-      mma_commit_warp(smem_u32(&bars.x_empty[this_k]));
       if (last) mma_commit_warp(smem_u32(&bars.acc_done));
+      // (Stages are handed back after the products that others wait for.)
+      mma_commit_warp(smem_u32(&bars.x_empty[this_k]));
+      if (more) {
+        mma_commit_warp(smem_u32(&bars.y_empty[ys]));
+        if (++ys == p.y_stages) {
+          ys = 0;
+          yph ^= 1u;
+        }
+        if (t + 1 == w.t1) {
+          mma_commit_warp(smem_u32(&bars.a_empty[0]));
+          mma_commit_warp(smem_u32(&bars.a_empty[1]));
+        }
+      }
       ++count;
       live = more;
     }
@@ -503,24 +509,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // Two warps share a quarter of the lanes; each takes half of the keys.
     const int half = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    const float c2 = p.scale_log2, sc = bars.ds_scale;
+    // (p is held times 2^p_shift here too; ds's scale takes it out.)
+    const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
     const int d = p.a.head_dim;
+    const int row_token = p.tile_heads > 1 ? r / p.tile_heads : r;
+    const int row_head = p.tile_heads > 1 ? r - row_token * p.tile_heads : 0;
     uint32_t count = 0, items = 0;
     bool ok = true;
     for (Walk<true, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
       int token, head;
       w.place(0, &token, &head);
-      bool row_ok = true;
-      if (p.tile_heads > 1) {
-        const int dt = r / p.tile_heads;
-        row_ok = dt < p.tile_tokens;
-        token += dt;
-        head += r - dt * p.tile_heads;
-      } else {
-        token += r;
-      }
-      row_ok = row_ok && token < p.a.q_len;
-      float lse2 = INFINITY, delta = 0.f;
+      token += row_token;
+      head += row_head;
+      const bool row_ok = row_token < p.tile_tokens && token < p.a.q_len;
+      float lse2 = -INFINITY, delta = 0.f;  // (both negated)
       const uint32_t* bits = nullptr;
       if (row_ok) {
         const float* st = p.stats +
@@ -531,8 +533,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           bits = p.a.mask_bits +
                  (w.b * p.a.mask_b + head * p.a.mask_h + token * p.a.mask_q) * p.a.mask_words;
       }
-      const uint64_t c22 = pack2(c2, c2), l2 = pack2(-lse2, -lse2), sc2 = pack2(sc, sc),
-                     dl2 = pack2(-delta * sc, -delta * sc);
+      const uint64_t c22 = pack2(c2, c2), l2 = pack2(lse2, lse2), sc2 = pack2(sc, sc),
+                     dl2 = pack2(delta * sc, delta * sc);
       for (int t = w.t0; t < w.t1; ++t) {
         const int keys = w.tile_keys(t), cols = w.tile_cols(t);
         uint32_t word[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
@@ -623,7 +625,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.nt;
       const long long slot = 2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-      const float f = p.a.scale / sc;
+      const float f = p.a.scale / bars.ds_scale;
 #pragma unroll
       for (int c = 0; c < DP / 2; c += 32) {
         const int col = half * (DP / 2) + c;
@@ -669,6 +671,7 @@ struct KeyWalk {
   long long left;  // steps after this item
   int b, hk, tile, n;
   int i0, i1;      // steps [i0, i1) of item_steps
+  int head, qt;    // query head and tile of the present step
   bool live;
   __device__ KeyWalk(const AttnBwdParams& params, const SplitStart& st) : p(params) {
     left = st.left;
@@ -686,6 +689,16 @@ struct KeyWalk {
     i0 = from;
     i1 = static_cast<int>(min(static_cast<long long>(p.item_steps), from + left));
     left -= i1 - i0;
+    const int h = from / p.q_tiles;
+    qt = from - h * p.q_tiles;
+    head = hk * p.a.group + h;
+  }
+  // The step after (within the item).
+  __device__ void step() {
+    if (++qt == p.q_tiles) {
+      qt = 0;
+      ++head;
+    }
   }
   __device__ void next() {
     live = left > 0;
@@ -700,11 +713,7 @@ struct KeyWalk {
     }
     take(0);
   }
-  __device__ int head(int i) const { return hk * p.a.group + i / p.q_tiles; }
-  __device__ int q_tile(int i) const { return i % p.q_tiles; }
-  __device__ int cols(int i) const {
-    return (min(kAttnRows, p.a.q_len - q_tile(i) * kAttnRows) + 15) & ~15;
-  }
+  __device__ int cols() const { return qt == p.q_tiles - 1 ? p.last_cols : kAttnRows; }
   __device__ int keys() const { return min(kAttnRows, n - tile * kAttnRows); }
 };
 
@@ -805,8 +814,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (i == 1) ++na;
       }
       aph ^= 1u;
-      for (int i = w.i0; ok && i < w.i1; ++i) {
-        const int h = w.head(i), qt = w.q_tile(i);
+      for (int i = w.i0; ok && i < w.i1; ++i, w.step()) {
+        const int h = w.head, qt = w.qt;
         ok = wait(&bars.x_empty[xs], xph ^ 1u, kAttnProducerTimeout);
         if (!ok) break;
         uint32_t bar = smem_u32(&bars.x_full[xs]);
@@ -895,7 +904,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     auto clear = [&](uint8_t* tile, int stat_stage) {
       const float* st = reinterpret_cast<const float*>(smem + p.off_stat + stat_stage * 1024);
       for (int r0 = 0; r0 < kAttnRows; r0 += 32) {
-        const uint32_t used = __ballot_sync(0xFFFFFFFFu, st[r0 + lane] != INFINITY);
+        const uint32_t used = __ballot_sync(0xFFFFFFFFu, st[r0 + lane] != -INFINITY);
         clear_rows(tile, 16384, kBlocks, r0, kAttnRows, used, lane);
       }
       fence_proxy_async_shared();
@@ -907,7 +916,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     bool new_item = true;
     // S^T of the step (i of w), then its dp^T.
     auto step_s = [&](uint32_t step) {
-      cols = w.cols(i);
       if (new_item) ok = wait(&bars.a_full[0], aph, kAttnMmaTimeout);
       ok = ok && wait(&bars.x_full[xs], xph, kAttnMmaTimeout);
       if (!ok) return;
@@ -920,7 +928,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       keys_by_rows(t_s, a_lo, x_lo + xs * kTileLo, cols);
       mma_commit_warp(smem_u32(&bars.s_full[0]));
-      if (i + 1 == w.i1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
       if (++xs == p.x_stages) {
         xs = 0;
         xph ^= 1u;
@@ -935,48 +942,56 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (masked) clear(smem + p.off_y + ys * kTile, step & 1u);
       keys_by_rows(t_dp, a_lo + kTileLo, y_lo + ys * kTileLo, cols);
       mma_commit_warp(smem_u32(&bars.dp_full));
-      if (i + 1 == w.i1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
+      if (i + 1 == w.i1) {
+        mma_commit_warp(smem_u32(&bars.a_empty[0]));
+        mma_commit_warp(smem_u32(&bars.a_empty[1]));
+      }
       if (++ys == p.y_stages) {
         ys = 0;
         yph ^= 1u;
       }
     };
     if (live) {
+      cols = w.cols();
       step_s(0);
       if (ok) step_dp(0);
     }
     while (ok && live) {
+      // The next step's place first: between the products below there is only
+      // what they need.
       const bool first = i == w.i0, last = i + 1 == w.i1;
       const int this_cols = cols, this_x = x_now, this_y = y_now;
-      ok = wait(&bars.p_full, count & 1u, kAttnMmaTimeout);
-      if (ok && first) {
-        if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
-        ++items;
-      }
-      if (!ok) break;
-      tc_fence_after();
-      accumulate(t_dv, t_s, y_lo + this_y * kTileLo, this_cols, first);
-      mma_commit_warp(smem_u32(&bars.y_empty[this_y]));
       bool more = true;
-      new_item = false;
+      new_item = last;
       if (last) {
         w.next();
         more = w.live;
         i = w.i0;
-        new_item = true;
         aph ^= 1u;
       } else {
+        w.step();
         ++i;
       }
+      if (more) cols = w.cols();
+      if (first) {
+        if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
+        ++items;
+      }
+      ok = ok && wait(&bars.p_full, count & 1u, kAttnMmaTimeout);
+      if (!ok) break;
+      tc_fence_after();
+      accumulate(t_dv, t_s, y_lo + this_y * kTileLo, this_cols, first);
       if (more) step_s(count + 1);
       if (!ok) break;
+      mma_commit_warp(smem_u32(&bars.y_empty[this_y]));
       ok = wait(&bars.ds_full[0], count & 1u, kAttnMmaTimeout);
       if (!ok) break;
       tc_fence_after();
       accumulate(t_dk, t_dp, x_lo + this_x * kTileLo, this_cols, first);
-      mma_commit_warp(smem_u32(&bars.x_empty[this_x]));
       if (last) mma_commit_warp(smem_u32(&bars.acc_done));
       if (more) step_dp(count + 1);
+      if (!ok) break;
+      mma_commit_warp(smem_u32(&bars.x_empty[this_x]));
       ++count;
       live = more;
     }
@@ -992,7 +1007,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
     const uint64_t c22 = pack2(c2, c2), sc2 = pack2(sc, sc);
-    const float up = p.p_shift;
     const int d = p.a.head_dim;
     const uint32_t ts = t_s + half * 64 + lane_field, td = t_dp + half * 64 + lane_field;
     uint32_t* mask_tile = reinterpret_cast<uint32_t*>(smem + p.off_mask);
@@ -1002,13 +1016,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const bool key_ok = r < w.keys();
       const bool keys_whole = w.keys() == kAttnRows;
       bool told = false;  // of a failed wait, at a barrier
-      for (int i = w.i0; i < w.i1; ++i) {
-        const int cols = w.cols(i), mine = cols - half * 64;
+      for (int i = w.i0; i < w.i1; ++i, w.step()) {
+        const int cols = w.cols(), mine = cols - half * 64;
         uint32_t on[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
         if (p.a.mask_bits) {
           // The tile's mask words, [query][4 words of 32 keys]: every warp reads
           // its word of 64 queries, one bit per lane.
-          const int h = w.head(i), t0 = w.q_tile(i) * kAttnRows;
+          const int h = w.head, t0 = w.qt * kAttnRows;
           uint32_t* buf = mask_tile + (count & 1u) * 512;
           const int row = threadIdx.x >> 1, pair = threadIdx.x & 1;
           uint2 q = make_uint2(0, 0);
@@ -1049,12 +1063,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               uint32_t h[16];
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(st + c * 32 + j);
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + c * 32 + j);
                 float x[4];
                 unpack2(fma2(pack2(__uint_as_float(s[c * 32 + j]), __uint_as_float(s[c * 32 + j + 1])),
-                             c22, pack2(up - l.x, up - l.y)), x[0], x[1]);
+                             c22, l.x), x[0], x[1]);
                 unpack2(fma2(pack2(__uint_as_float(s[c * 32 + j + 2]), __uint_as_float(s[c * 32 + j + 3])),
-                             c22, pack2(up - l.z, up - l.w)), x[2], x[3]);
+                             c22, l.y), x[2], x[3]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) s[c * 32 + j + k] = __float_as_uint(exp2_approx(x[k]));
               }
@@ -1085,15 +1099,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               tmem_wait_ld_x32(dp);
 #pragma unroll
               for (int j = 0; j < 32; j += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(st + 128 + c * 32 + j);
+                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + 128 + c * 32 + j);
+                uint64_t u = add2(pack2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1])), l.x);
+                uint64_t v = add2(pack2(__uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3])), l.y);
+                if (!kBf16) {
+                  u = mul2(u, sc2);
+                  v = mul2(v, sc2);
+                }
                 float x[4];
-                unpack2(mul2(fma2(pack2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1])), sc2,
-                                  pack2(-l.x * sc, -l.y * sc)),
-                             pack2(__uint_as_float(s[c * 32 + j]), __uint_as_float(s[c * 32 + j + 1]))),
+                unpack2(mul2(u, pack2(__uint_as_float(s[c * 32 + j]), __uint_as_float(s[c * 32 + j + 1]))),
                         x[0], x[1]);
-                unpack2(mul2(fma2(pack2(__uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3])), sc2,
-                                  pack2(-l.z * sc, -l.w * sc)),
-                             pack2(__uint_as_float(s[c * 32 + j + 2]), __uint_as_float(s[c * 32 + j + 3]))),
+                unpack2(mul2(v, pack2(__uint_as_float(s[c * 32 + j + 2]), __uint_as_float(s[c * 32 + j + 3]))),
                         x[2], x[3]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) dp[j + k] = __float_as_uint(x[k]);

@@ -86,6 +86,7 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   int q_box;            // dk, dv: tokens per box
   int q_tiles;          // tiles of 128 tokens
   int item_steps;       // dk, dv: group * q_tiles
+  int last_cols;        // queries of the last tile, to a multiple of 16
   long long item_rows;
   int x_stages, y_stages;
   uint32_t off_a, off_x, off_y, off_stat, off_mask, off_bar;
