@@ -120,6 +120,10 @@ LONG = [  # many tiles for each thread block, cut in the middle of rows
     (2, 3000, 1100, 8, 2, 40, "rows", "f16"),
     (16, 1024, 77, 8, 8, 40, "lengths", "bf16"),
     (1, 100, 9000, 4, 4, 64, "lengths", "bf16"),
+    (8, 2500, 77, 8, 4, 48, "lengths", "bf16"),      # one tile of keys
+    (3, 3001, 128, 8, 2, 64, "lengths", "bf16"),
+    (5, 2000, 90, 6, 6, 64, "none", "f16"),
+    (40, 700, 30, 4, 1, 32, "lengths", "f16"),
 ]
 
 

@@ -21,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libconvgb300.so")
 SOURCES = ["conv_api.cu", "conv_kernels.cu", "conv_kernels_gather.cu", "conv_kernels_pair.cu",
-           "conv_kernels_sk.cu", "conv_direct.cu", "conv_rowtap.cu", "attn_api.cu", "attn_mask.cu", "attn_fwd.cu",
+           "conv_kernels_sk.cu", "conv_direct.cu", "conv_rowtap.cu", "attn_api.cu", "attn_mask.cu", "attn_fwd.cu", "attn_short.cu",
            "attn_bwd.cu", "qk_norm_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

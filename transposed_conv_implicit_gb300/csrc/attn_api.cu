@@ -75,6 +75,7 @@ struct FwdPlan {
   int tile_heads, tile_tokens, token_tiles, row_tiles;
   int kv_box;
   bool split;
+  int one;               // one key tile: CTAs per SM of its kernel, or 0
   int grid;
   long long items;       // pairs: launch items
   size_t part_bytes;     // split: partial rows and their statistics
@@ -102,6 +103,14 @@ FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
   f.kv_box = std::min(kAttnRows, std::max(16, (a.kv_len + 15) / 16 * 16));
   const long long nt = std::max(1, (a.kv_len + f.kv_box - 1) / f.kv_box);
   const long long heads = static_cast<long long>(a.batch) * a.kv_heads;
+  // One tile of keys, narrow heads, no mask: the kernel made for it.  Four
+  // CTAs per SM where scores and output fit in 128 TMEM columns.
+  if (a.kv_len > 0 && a.kv_len <= kAttnRows && a.head_dim <= 64 && !a.mask) {
+    f.one = f.kv_box + (a.head_dim + 15) / 16 * 16 <= 128 ? 4 : 2;
+    f.items = heads * row_tiles;
+    f.grid = static_cast<int>(std::min<long long>(f.items, static_cast<long long>(f.one) * sms));
+    return f;
+  }
   f.items = heads * ((row_tiles + 1) / 2);
   // Pairs take whole rounds of items; split shares steps out evenly.  A
   // pair's step covers two row tiles on a whole SM.
@@ -122,6 +131,7 @@ struct BwdPlan {
   int q_tiles, item_steps, kv_tiles;
   int q_grid, kv_grid;     // CTAs of the dq and the dk, dv kernel
   bool norms;              // fp16: ds is scaled by the rows' norms
+  bool brief;              // one tile of keys, narrow heads, no mask: one kernel
   size_t stat_bytes, norm_bytes, part_q_bytes, part_kv_bytes;
 };
 
@@ -135,6 +145,8 @@ BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
   p.q_grid = static_cast<int>(std::min<long long>(heads * f.row_tiles * nt, sms));
   p.kv_grid = static_cast<int>(std::min<long long>(heads * p.kv_tiles * p.item_steps, sms));
   p.norms = a.dtype == CONV_DTYPE_F16;
+  p.brief = f.one && a.q_len > 0;
+  if (p.brief) p.kv_grid = static_cast<int>(std::min<long long>(heads * p.item_steps, sms));
   p.stat_bytes = static_cast<size_t>(a.batch) * a.heads * p.q_tiles * 256 * sizeof(float);
   p.norm_bytes = 2 * kAttnNormBlocks * sizeof(float);  // (of one size for both types)
   const size_t tile = static_cast<size_t>(kAttnRows) * 128 * sizeof(float);
@@ -199,7 +211,7 @@ conv_status_t run_fwd(const AttnShape& s, const FwdPlan& f, char* ws, const Layo
   p.tile_tokens = f.tile_tokens;
   p.token_tiles = f.token_tiles;
   p.row_tiles = f.row_tiles;
-  p.div_pairs = make_fast_div(static_cast<uint32_t>((f.row_tiles + 1) / 2));
+  p.div_pairs = make_fast_div(static_cast<uint32_t>(f.one ? f.row_tiles : (f.row_tiles + 1) / 2));
   p.div_kv_heads = make_fast_div(static_cast<uint32_t>(s.kv_heads));
   p.div_token_tiles = make_fast_div(static_cast<uint32_t>(f.token_tiles));
   p.kv_box = f.kv_box;
@@ -218,6 +230,18 @@ conv_status_t run_fwd(const AttnShape& s, const FwdPlan& f, char* ws, const Layo
   p.k_mul[1] = s.ks[0] != 0;
   p.v_mul[0] = s.vs[2] != 0;
   p.v_mul[1] = s.vs[0] != 0;
+  p.status = reinterpret_cast<unsigned int*>(ws);
+  p.timeout_cycles = wait_limit_cycles();
+  p.fault_mode = wait_fault_mode();
+  if (f.one) {
+    // Two buffers of queries (and output), keys and values, barriers.
+    p.off_q = 0;
+    p.off_kv = 2 * 16384;
+    p.off_bar = p.off_kv + 2 * f.kv_box * 128;
+    return launch_attn_one(p, f.one, f.grid, p.off_bar + attn_one_bar_bytes(), stream) == cudaSuccess
+               ? CONV_OK
+               : CONV_ERR_CUDA;
+  }
   // Shared memory: queries, the key/value ring, output staging, barriers.
   const bool wide = s.head_dim > 64;
   const uint32_t q_tile = wide ? 32768 : 16384, kv_tile = f.kv_box * (wide ? 256 : 128);
@@ -234,10 +258,26 @@ conv_status_t run_fwd(const AttnShape& s, const FwdPlan& f, char* ws, const Layo
     p.part_out = reinterpret_cast<float*>(ws + l.part_at);
     p.part_stat = p.part_out + static_cast<size_t>(2) * f.grid * kAttnRows * 128;
   }
-  p.status = reinterpret_cast<unsigned int*>(ws);
-  p.timeout_cycles = wait_limit_cycles();
-  p.fault_mode = wait_fault_mode();
   return launch_attn_fwd(p, f.split, f.grid, smem, stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+}
+
+// The maps of q, do, k and v, and where they are broadcast.
+conv_status_t encode_maps(AttnBwdParams* p, const AttnShape& s, int box_heads, int box_tokens,
+                          int kv_box) {
+  conv_status_t st = encode_map(&p->map_q, s.q, s, s.heads, s.q_len, s.qs, box_heads, box_tokens);
+  if (st == CONV_OK)
+    st = encode_map(&p->map_do, s.dout, s, s.heads, s.q_len, s.dos, box_heads, box_tokens);
+  if (st == CONV_OK) st = encode_map(&p->map_k, s.k, s, s.kv_heads, s.kv_len, s.ks, 1, kv_box);
+  if (st == CONV_OK) st = encode_map(&p->map_v, s.v, s, s.kv_heads, s.kv_len, s.vs, 1, kv_box);
+  p->q_mul[0] = s.qs[2] != 0;
+  p->q_mul[1] = s.qs[0] != 0;
+  p->do_mul[0] = s.dos[2] != 0;
+  p->do_mul[1] = s.dos[0] != 0;
+  p->k_mul[0] = s.ks[2] != 0;
+  p->k_mul[1] = s.ks[0] != 0;
+  p->v_mul[0] = s.vs[2] != 0;
+  p->v_mul[1] = s.vs[0] != 0;
+  return st;
 }
 
 conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, char* ws,
@@ -279,23 +319,32 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
     const long long values = static_cast<long long>(s.batch) * s.kv_heads * s.kv_len;
     p.value_blocks =
         g.norms ? static_cast<int>(std::min<long long>(kAttnNormBlocks, (values + 63) / 64)) : 0;
-    if (launch_attn_rows(p, stream) != cudaSuccess) return CONV_ERR_CUDA;
+    // (Short keys: delta is summed beside the scores; fp16 still wants the norms.)
+    if ((!g.brief || g.norms) && launch_attn_rows(p, stream) != cudaSuccess) return CONV_ERR_CUDA;
+    if (g.brief) {
+      conv_status_t st = encode_maps(&p, s, 1, p.q_box, f.kv_box);
+      if (st == CONV_OK) st = encode_map(&p.map_dq, s.dq, s, s.heads, s.q_len, s.dqs, 1, p.q_box);
+      if (st != CONV_OK) return st;
+      // TMEM: dv and dk (64 columns each), then buffers of scores and dp.
+      p.region = std::max(f.kv_box, (s.head_dim + 15) / 16 * 16);
+      p.bufs = 128 + 4 * p.region <= 512 ? 2 : 1;
+      // Shared memory: q and do, p and ds, dq's staging, k and v, barriers.
+      p.off_x = 0;
+      p.off_y = attn_short_stages() * 32768;
+      p.off_stat = p.off_y + 4 * 16384;
+      p.off_a = p.off_stat + 16384;
+      p.off_bar = p.off_a + 2 * f.kv_box * 128;
+      if (launch_attn_short_bwd(p, g.kv_grid, p.off_bar + attn_short_bar_bytes(), stream) != cudaSuccess)
+        return CONV_ERR_CUDA;
+      if (g.item_steps == 1) return CONV_OK;  // no item is cut
+      return launch_attn_bwd_join(p, 0, g.kv_grid, 0, static_cast<long long>(s.batch) * s.kv_heads,
+                                  stream) == cudaSuccess
+                 ? CONV_OK
+                 : CONV_ERR_CUDA;
+    }
     // dq.
-    conv_status_t st =
-        encode_map(&p.map_q, s.q, s, s.heads, s.q_len, s.qs, f.tile_heads, f.tile_tokens);
-    if (st == CONV_OK)
-      st = encode_map(&p.map_do, s.dout, s, s.heads, s.q_len, s.dos, f.tile_heads, f.tile_tokens);
-    if (st == CONV_OK) st = encode_map(&p.map_k, s.k, s, s.kv_heads, s.kv_len, s.ks, 1, f.kv_box);
-    if (st == CONV_OK) st = encode_map(&p.map_v, s.v, s, s.kv_heads, s.kv_len, s.vs, 1, f.kv_box);
+    conv_status_t st = encode_maps(&p, s, f.tile_heads, f.tile_tokens, f.kv_box);
     if (st != CONV_OK) return st;
-    p.q_mul[0] = s.qs[2] != 0;
-    p.q_mul[1] = s.qs[0] != 0;
-    p.do_mul[0] = s.dos[2] != 0;
-    p.do_mul[1] = s.dos[0] != 0;
-    p.k_mul[0] = s.ks[2] != 0;
-    p.k_mul[1] = s.ks[0] != 0;
-    p.v_mul[0] = s.vs[2] != 0;
-    p.v_mul[1] = s.vs[0] != 0;
     const uint32_t kv_tile = f.kv_box * (wide ? 256 : 128);
     p.x_stages = wide ? 3 : 4;
     p.y_stages = wide ? 2 : 4;

@@ -40,9 +40,7 @@ namespace convgb300 {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kMaxRing = 8;
-constexpr int kNormBlocks = kAttnNormBlocks;
 
 // ------------------------------------------------------------------ rows
 template <typename T>
@@ -72,7 +70,7 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y) {
 // stats[b][h][token tile][2][128]: minus lse in log2 units, plus p_shift (-inf
 // for queries without keys and past the end, which makes p zero), and minus
 // delta: as the products' sums take them.  With norms: the
-// largest |do| row of each block, then (kNormBlocks blocks on) |v| row, both
+// largest |do| row of each block, then (kAttnNormBlocks blocks on) |v| row, both
 // squared; rows that take no part are left out.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnBwdParams p) {
@@ -158,27 +156,8 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < 8; ++i) norm = fmaxf(norm, most[i]);
-    p.norms[(values ? kNormBlocks : 0) + block] = norm;
+    p.norms[(values ? kAttnNormBlocks : 0) + block] = norm;
   }
-}
-
-// The power of two that ds is scaled by: |ds| 2^k <= 2^15.  One warp.
-__device__ __forceinline__ float ds_scale(const AttnBwdParams& p, int lane) {
-  if (!p.norms) return 1.f;
-  float x = 0.f, y = 0.f;
-  for (int i = lane; i < p.row_blocks; i += 32) x = fmaxf(x, p.norms[i]);
-  for (int i = lane; i < p.value_blocks; i += 32) y = fmaxf(y, p.norms[kNormBlocks + i]);
-  for (int o = 16; o; o >>= 1) {
-    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-    y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
-  }
-  // 2 |do| |v| < 2^(1 + ceil exponents); both norms in fp16's range, so k is
-  // within +-60.
-  const float bound = 2.f * sqrtf(x) * sqrtf(y);
-  if (!(bound > 0.f)) return 1.f;
-  int e;
-  frexpf(bound, &e);  // bound < 2^e
-  return ldexpf(1.f, max(-60, min(60, 14 - e)));
 }
 
 struct Bars {
@@ -211,26 +190,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, uint32_t block_bytes, 
     for (int c = 0; c < blocks; ++c)
       for (int i = 0; i < 8; ++i) q[c * (block_bytes >> 4) + i] = make_uint4(0, 0, 0, 0);
   }
-}
-
-// Writes 32 fp32 columns of a row, scaled: rounded to T.
-template <typename T>
-__device__ __forceinline__ void store_cols(T* dst, const uint32_t* v, int n, float f) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8) {
-    if (i < n) {
-      uint32_t h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        h[j] = round2<T>(__uint_as_float(v[i + 2 * j]) * f, __uint_as_float(v[i + 2 * j + 1]) * f);
-      *reinterpret_cast<uint4*>(dst + i) = make_uint4(h[0], h[1], h[2], h[3]);
-    }
-  }
-}
-__device__ __forceinline__ void store_cols_f32(float* dst, const uint32_t* v, int n) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 4)
-    if (i < n) *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
 // ------------------------------------------------------------------ dq
@@ -663,6 +622,8 @@ __device__ __forceinline__ long long key_steps(const AttnBwdParams& p, int b) {
          p.item_steps;
 }
 __device__ __forceinline__ long long key_steps_uniform(const AttnBwdParams& p) {
+  // (Short keys: one tile for every request, also one without keys.)
+  if (p.region) return static_cast<long long>(p.a.kv_heads) * p.item_steps;
   return p.a.kv_lengths ? -1 : key_steps(p, 0);
 }
 
@@ -1249,7 +1210,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const long long bh = at / all_tiles;
   const int tile = static_cast<int>(at - bh * all_tiles);
   const int b = static_cast<int>(bh / a.kv_heads), hk = static_cast<int>(bh - static_cast<long long>(b) * a.kv_heads);
-  const int n = p.item_steps > 0 ? valid_keys(a, b) : 0, tiles = (n + kAttnRows - 1) / kAttnRows;
+  const int n = p.item_steps == 0 ? 0 : p.region ? a.kv_len : valid_keys(a, b), tiles = (n + kAttnRows - 1) / kAttnRows;
   const int rows = min(kAttnRows, a.kv_len - tile * kAttnRows);
   int shares = 0;
   if (tile < tiles) {

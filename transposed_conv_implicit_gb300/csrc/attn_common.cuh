@@ -234,6 +234,47 @@ struct Walk {
   __device__ int tile_cols(int t) const { return max(16, (tile_keys(t) + 15) & ~15); }
 };
 
+constexpr float kLog2e = 1.44269504088896341f;
+
+// The power of two that ds is scaled by: |ds| 2^k <= 2^15.  One warp.
+__device__ __forceinline__ float ds_scale(const AttnBwdParams& p, int lane) {
+  if (!p.norms) return 1.f;
+  float x = 0.f, y = 0.f;
+  for (int i = lane; i < p.row_blocks; i += 32) x = fmaxf(x, p.norms[i]);
+  for (int i = lane; i < p.value_blocks; i += 32) y = fmaxf(y, p.norms[kAttnNormBlocks + i]);
+  for (int o = 16; o; o >>= 1) {
+    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+    y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
+  }
+  // 2 |do| |v| < 2^(1 + ceil exponents); both norms in fp16's range, so k is
+  // within +-60.
+  const float bound = 2.f * sqrtf(x) * sqrtf(y);
+  if (!(bound > 0.f)) return 1.f;
+  int e;
+  frexpf(bound, &e);  // bound < 2^e
+  return ldexpf(1.f, max(-60, min(60, 14 - e)));
+}
+
+// Writes 32 fp32 columns of a row, scaled: rounded to T.
+template <typename T>
+__device__ __forceinline__ void store_cols(T* dst, const uint32_t* v, int n, float f) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8) {
+    if (i < n) {
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[j] = round2<T>(__uint_as_float(v[i + 2 * j]) * f, __uint_as_float(v[i + 2 * j + 1]) * f);
+      *reinterpret_cast<uint4*>(dst + i) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+__device__ __forceinline__ void store_cols_f32(float* dst, const uint32_t* v, int n) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+    if (i < n) *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
 // Joining the shares of tiles that a launch cut: one block takes kJoinRows
 // rows of a tile, each warp kJoinUnroll at a time, and the shares' slots are
 // listed once per block, so that the rows' reads are all in flight together

@@ -77,6 +77,7 @@ constexpr int kAttnNormBlocks = 2048;  // most blocks of each part of the rows k
 struct AttnBwdParams {  // aligned like CUtensorMap
   CUtensorMap map_q, map_do;  // {D, heads, tokens, batch}, box by kernel
   CUtensorMap map_k, map_v;   // {D, kv_heads, tokens, batch}, box {64, 1, kv_box, 1}
+  CUtensorMap map_dq;         // short keys: as map_q, boxes of 128 tokens of one head
   AttnShape a;
   int q_mul[2], do_mul[2], k_mul[2], v_mul[2];
   int tile_heads, tile_tokens, token_tiles, row_tiles;
@@ -88,6 +89,7 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   int item_steps;       // dk, dv: group * q_tiles
   int last_cols;        // queries of the last tile, to a multiple of 16
   long long item_rows;
+  int region, bufs;     // short keys: TMEM columns of S (and of dp), buffers; else 0
   int x_stages, y_stages;
   uint32_t off_a, off_x, off_y, off_stat, off_mask, off_bar;
   float scale_log2;
@@ -108,6 +110,14 @@ cudaError_t launch_attn_dq(const AttnBwdParams& p, int grid, size_t smem, cudaSt
 cudaError_t launch_attn_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream);
 cudaError_t launch_attn_bwd_join(const AttnBwdParams& p, int q_ctas, int kv_ctas,
                                  long long q_blocks, long long kv_blocks, cudaStream_t stream);
+
+// Short keys (attn_short.cu): at most 128, head_dim <= 64, no mask.
+size_t attn_one_bar_bytes();
+size_t attn_short_bar_bytes();
+int attn_short_stages();
+cudaError_t launch_attn_one(const AttnFwdParams& p, int ctas, int grid, size_t smem,
+                            cudaStream_t stream);
+cudaError_t launch_attn_short_bwd(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream);
 
 // Without keys: zeros to out (batch, q_len, heads rows) and -inf to lse.
 cudaError_t launch_attn_no_keys(const AttnShape& a, cudaStream_t stream);

@@ -25,6 +25,26 @@ __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t* v) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+        "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld_x16(uint32_t* v) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+        "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]),
+        "+r"(v[14]), "+r"(v[15])
+      :
+      : "memory");
+}
+
 // tcgen05.wait::ld naming the registers of an earlier 32-column load, so that
 // no use of them moves above the wait.
 __device__ __forceinline__ void tmem_wait_ld_x32(uint32_t* v) {
@@ -80,8 +100,11 @@ __device__ __forceinline__ uint32_t lead_mn(uint32_t block_bytes) { return (bloc
 // lane of the warp runs this with the same operands.  (One MMA per call, with
 // its descriptors built in C++, cost about 100 cycles of issue each, twice
 // what the tensor core takes for a 128x128x16 step.)
-__device__ __forceinline__ void mma_ss_x4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                          uint32_t accumulate, int steps) {
+// A step moves A by kA and B by kB units of 16 bytes: 2 along K (K-major),
+// 128 down 16 rows (rows along M or N).
+template <int kA, int kB>
+__device__ __forceinline__ void mma_x4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate, int steps) {
   asm volatile(
       "{\n\t.reg .pred e, p, t, q;\n\t.reg .b64 a, b;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -90,16 +113,20 @@ __device__ __forceinline__ void mma_ss_x4(uint32_t d, uint32_t a_lo, uint32_t b_
       "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t"
       "setp.gt.and.s32 q, %6, 1, e;\n\t"
-      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "add.s64 a, a, %7;\n\tadd.s64 b, b, %8;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
       "setp.gt.and.s32 q, %6, 2, e;\n\t"
-      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "add.s64 a, a, %7;\n\tadd.s64 b, b, %8;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t"
       "setp.gt.and.s32 q, %6, 3, e;\n\t"
-      "add.s64 a, a, 2;\n\tadd.s64 b, b, 2;\n\t"
+      "add.s64 a, a, %7;\n\tadd.s64 b, b, %8;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, t;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(steps)
+      "r"(a_lo), "r"(b_lo), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(steps), "n"(kA), "n"(kB)
       : "memory");
+}
+__device__ __forceinline__ void mma_ss_x4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                          uint32_t accumulate, int steps) {
+  mma_x4<2, 2>(d, a_lo, b_lo, idesc, accumulate, steps);
 }
 
 // The same with A in TMEM (two K elements per 32-bit column, a step is 8
