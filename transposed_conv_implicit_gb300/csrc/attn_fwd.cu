@@ -490,8 +490,8 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
             // (The second half of the scores loads beside the first one's maximum.)
             tmem_ld_x32(ts, s);
             tmem_ld_x32(ts + 32, s + 32);
-            tmem_wait_ld_x32(s);
-            tmem_wait_ld_x32(s + 32);
+            tmem_wait_ld();
+            tmem_pin<64>(s);
             tmem_ld_x32(ts + 64, s + 64);
             tmem_ld_x32(ts + 96, s + 96);
             float top[4];
@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 top[j] = max3(top[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]));
-            tmem_wait_ld_x32(s + 64);
-            tmem_wait_ld_x32(s + 96);
+            tmem_wait_ld();
+            tmem_pin<64>(s + 64);
 #pragma unroll
             for (int i = 64; i < 128; i += 8)
 #pragma unroll
@@ -659,8 +659,8 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
           uint32_t o[64];
           tmem_ld_x32(to + blk * 64, o);
           tmem_ld_x32(to + blk * 64 + 32, o + 32);
-          tmem_wait_ld_x32(o);
-          tmem_wait_ld_x32(o + 32);
+          tmem_wait_ld();
+          tmem_pin<64>(o);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             uint32_t h[4];

@@ -35,6 +35,14 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* v) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+        "=r"(v[7])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld_x16(uint32_t* v) {
   asm volatile(
       "tcgen05.wait::ld.sync.aligned;"
@@ -57,6 +65,21 @@ __device__ __forceinline__ void tmem_wait_ld_x32(uint32_t* v) {
         "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
       :
       : "memory");
+}
+
+// After a tcgen05.wait::ld: names n registers (a multiple of 8) of an earlier
+// load, so that no use of them moves above the wait.  No instruction.  (Each
+// wait costs tens of cycles even when there is nothing to wait for: loads
+// share one.)
+template <int n>
+__device__ __forceinline__ void tmem_pin(uint32_t* v) {
+#pragma unroll
+  for (int i = 0; i < n; i += 8)
+    asm volatile(""
+                 : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]),
+                   "+r"(v[i + 5]), "+r"(v[i + 6]), "+r"(v[i + 7])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* v) {

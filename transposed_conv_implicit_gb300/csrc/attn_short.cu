@@ -377,14 +377,16 @@ __global__ void __launch_bounds__(kOneThreads, kCtas)
 }
 
 // ------------------------------------------------------------------ backward
-constexpr int kShortThreads = 448;  // 8 softmax warps, 4 that write dq, products, loads
+// 8 warps for p and ds, 4 that write dq, 2 that issue products, loads.
+constexpr int kShortSoftmax = 8, kShortEpi = 8, kShortScores = 12, kShortGrads = 13, kShortLoad = 14;
+constexpr int kShortThreads = 32 * 15;
 constexpr int kShortStages = 3;     // query tiles in flight
 
 struct ShortBars {
   uint64_t kv_full, kv_empty;
   uint64_t qd_full[kShortStages], qd_empty[kShortStages];
   uint64_t s_full[2], buf_free[2], dq_full[2];  // by TMEM buffer
-  uint64_t pds_full, pds_empty, acc_done, acc_free, drain;
+  uint64_t pds_full, pds_empty, acc_done, acc_free, drain[2];
   float exchange[2][2][128];  // by step parity: a half row's share of delta
   float ds_scale;
   uint32_t tmem;
@@ -440,7 +442,6 @@ template <typename T>
 __global__ void __launch_bounds__(kShortThreads, 1)
     attn_short_bwd_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int kEpiWarp = 8, kMmaWarp = 12, kLoadWarp = 13;
   extern __shared__ __align__(1024) uint8_t smem[];
   ShortBars& bars = *reinterpret_cast<ShortBars*>(smem + p.off_bar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars.kv_full), 1);
-    mbar_init(smem_u32(&bars.kv_empty), 1);
+    mbar_init(smem_u32(&bars.kv_empty), 2);
     for (int i = 0; i < kShortStages; ++i) {
       mbar_init(smem_u32(&bars.qd_full[i]), 1);
       mbar_init(smem_u32(&bars.qd_empty[i]), 1);
@@ -467,19 +468,19 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       mbar_init(smem_u32(&bars.buf_free[i]), 4);
       mbar_init(smem_u32(&bars.dq_full[i]), 1);
     }
-    mbar_init(smem_u32(&bars.pds_full), 8);
+    mbar_init(smem_u32(&bars.pds_full), kShortSoftmax);
     mbar_init(smem_u32(&bars.pds_empty), 1);
     mbar_init(smem_u32(&bars.acc_done), 1);
-    mbar_init(smem_u32(&bars.acc_free), 8);
-    mbar_init(smem_u32(&bars.drain), 1);
+    mbar_init(smem_u32(&bars.acc_free), kShortSoftmax);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars.drain[i]), 1);
     bars.abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kShortScores) {
     tmem_alloc(smem_u32(&bars.tmem), 512);
     tmem_relinquish();
   }
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == kShortLoad && lane == 0) {
     tma_prefetch_desc(&p.map_q);
     tma_prefetch_desc(&p.map_do);
     tma_prefetch_desc(&p.map_k);
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   auto buf_of = [&](uint32_t n) { return bufs == 2 ? n & 1u : 0u; };
   auto phase_of = [&](uint32_t n) { return (bufs == 2 ? n >> 1 : n) & 1u; };
 
-  if (warp == kLoadWarp) {
+  if (warp == kShortLoad) {
     // ------------------------------------------------------------ loads
     const uint32_t lead = lane == 0 ? 1u : 0u;
     const uint32_t q_bytes = static_cast<uint32_t>(p.q_box) * 128u;
@@ -552,120 +553,105 @@ __global__ void __launch_bounds__(kShortThreads, 1)
                           static_cast<uint32_t>((q / kShortStages) & 1), limit / 8 + 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ products
+  } else if (warp == kShortScores) {
+    // ------------------------------------------------------------ S and dp
     const int k_steps = (p.a.head_dim + 15) >> 4;
-    const uint32_t n_out = static_cast<uint32_t>(k_steps) * 16u;
-    const uint32_t idesc_acc = attn_idesc(kBf16, n_out, true, true);   // p^T do, ds^T q
-    const uint32_t idesc_dq = attn_idesc(kBf16, n_out, false, true);   // ds k
-    const uint32_t q_lo = smem_u32(qd) >> 4, kv_lo = smem_u32(kv) >> 4, pds_lo = smem_u32(pds) >> 4;
-    const uint32_t mn = lead_mn(kTile);
+    const uint32_t q_lo = kLeadK | (smem_u32(qd) >> 4), kv_lo = kLeadK | (smem_u32(kv) >> 4);
     bool ok = true;
-    int s = 0, cols = 0;
+    int s = 0;
     uint32_t sph = 0, count = 0, items = 0;
-    ShortWalk w(p);
-    // Keys of a new item; those past the request's length are cleared (k meets
-    // the zeros of ds; v is only a factor of scores that are left out).
-    auto take_keys = [&]() {
+    for (ShortWalk w(p); ok && w.live; w.next()) {
       ok = wait(&bars.kv_full, items & 1u, kAttnMmaTimeout);
+      if (!ok) break;
       ++items;
-      const int keys = w.keys();
-      cols = cols_of(keys);
-      if (ok && keys < cols && p.a.kv_lengths) {
+      const int keys = w.keys(), cols = cols_of(keys);
+      if (keys < cols && p.a.kv_lengths) {
+        // Keys past the request's length are cleared (k meets the zeros of ds;
+        // v is only a factor of scores that are left out).
         uint4* k = reinterpret_cast<uint4*>(kv);
         for (int i = keys + (lane >> 3); i < cols; i += 4) k[i * 8 + (lane & 7)] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_shared();
         __syncwarp();
       }
-    };
-    // S and dp of step n from stage `s`.
-    auto scores = [&](uint32_t n) {
-      ok = ok && wait(&bars.qd_full[s], sph, kAttnMmaTimeout);
-      // (The buffer's last dq has been read.)
-      if (n >= bufs) ok = ok && wait(&bars.buf_free[buf_of(n)], phase_of(n) ^ 1u, kAttnMmaTimeout);
-      if (!ok) return;
-      tc_fence_after();
       const uint32_t id = attn_idesc(kBf16, static_cast<uint32_t>(cols), false, false);
-      const uint32_t t = t_buf + buf_of(n) * 2 * region, q = kLeadK | (q_lo + s * (2 * kTile >> 4));
-      mma_ss_x4(t, q, kLeadK | kv_lo, id, 0u, k_steps);
-      mma_ss_x4(t + region, q + (kTile >> 4), kLeadK | (kv_lo + (kv_tile >> 4)), id, 0u, k_steps);
-      mma_commit_warp(smem_u32(&bars.s_full[buf_of(n)]));
-      if (++s == kShortStages) {
-        s = 0;
-        sph ^= 1u;
+      for (int i = w.i0; i < w.i1; ++i, ++count) {
+        ok = wait(&bars.qd_full[s], sph, kAttnMmaTimeout);
+        // (The buffer's last dq has been read.)
+        if (count >= bufs)
+          ok = ok && wait(&bars.buf_free[buf_of(count)], phase_of(count) ^ 1u, kAttnMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t = t_buf + buf_of(count) * 2 * region, q = q_lo + s * (2 * kTile >> 4);
+        mma_ss_x4(t, q, kv_lo, id, 0u, k_steps);
+        mma_ss_x4(t + region, q + (kTile >> 4), kv_lo + (kv_tile >> 4), id, 0u, k_steps);
+        mma_commit_warp(smem_u32(&bars.s_full[buf_of(count)]));
+        if (++s == kShortStages) {
+          s = 0;
+          sph ^= 1u;
+        }
       }
-    };
-    bool live = w.live;
-    int i = w.i0;
-    if (live) {
-      take_keys();
-      scores(0);
+      if (ok) mma_commit_warp(smem_u32(&bars.kv_empty));
     }
-    while (ok && live) {
-      const int steps = cols >> 4, row_steps = w.rows16() >> 4;
-      const bool first = i == w.i0, last = i + 1 == w.i1;
-      const int this_s = s == 0 ? kShortStages - 1 : s - 1;
-      if (first && items > 1) {
-        ok = wait(&bars.acc_free, (items - 2) & 1u, kAttnMmaTimeout);
+    if (!ok) {
+      // Every MMA already issued must finish before TMEM is released.
+      mma_commit_warp(smem_u32(&bars.drain[0]));
+      mbar_wait_drain(smem_u32(&bars.drain[0]), 0, limit / 8 + 1);
+    }
+    __syncwarp();
+  } else if (warp == kShortGrads) {
+    // ------------------------------------------------------------ dq, dv, dk
+    const int k_steps = (p.a.head_dim + 15) >> 4;
+    const uint32_t n_out = static_cast<uint32_t>(k_steps) * 16u;
+    const uint32_t idesc_acc = attn_idesc(kBf16, n_out, true, true);   // p^T do, ds^T q
+    const uint32_t idesc_dq = attn_idesc(kBf16, n_out, false, true);   // ds k
+    const uint32_t mn = lead_mn(kTile);
+    const uint32_t q_lo = mn | (smem_u32(qd) >> 4), k_lo = lead_mn(kv_tile) | (smem_u32(kv) >> 4);
+    const uint32_t p_lo = smem_u32(pds) >> 4, ds_lo = p_lo + (2 * kTile >> 4);
+    bool ok = true;
+    int s = 0;
+    uint32_t count = 0, items = 0;
+    for (ShortWalk w(p); ok && w.live; w.next()) {
+      if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
+      ++items;
+      const int steps = cols_of(w.keys()) >> 4;
+      for (int i = w.i0; ok && i < w.i1; ++i, ++count, w.step()) {
+        const uint32_t q = q_lo + s * (2 * kTile >> 4), go_on = i == w.i0 ? 0u : 1u;
+        const uint32_t t_dq = t_buf + buf_of(count) * 2 * region;
+        const int row_steps = w.rows16() >> 4;
+        ok = wait(&bars.pds_full, count & 1u, kAttnMmaTimeout);
         if (!ok) break;
+        tc_fence_after();
+        // dq first: others wait for it.
+        mma_x4<2, 128>(t_dq, kLeadK | ds_lo, k_lo, idesc_dq, 0u, steps);
+        if (steps > 4)
+          mma_x4<2, 128>(t_dq, kLeadK | (ds_lo + (kTile >> 4)), k_lo + 512u, idesc_dq, 1u, steps - 4);
+        mma_commit_warp(smem_u32(&bars.dq_full[buf_of(count)]));
+        mma_x4<128, 128>(t_dv, mn | p_lo, q + (kTile >> 4), idesc_acc, go_on, row_steps);
+        if (row_steps > 4)
+          mma_x4<128, 128>(t_dv, mn | (p_lo + 512u), q + (kTile >> 4) + 512u, idesc_acc, 1u, row_steps - 4);
+        mma_x4<128, 128>(t_dk, mn | ds_lo, q, idesc_acc, go_on, row_steps);
+        if (row_steps > 4)
+          mma_x4<128, 128>(t_dk, mn | (ds_lo + 512u), q + 512u, idesc_acc, 1u, row_steps - 4);
+        mma_commit_warp(smem_u32(&bars.pds_empty));
+        mma_commit_warp(smem_u32(&bars.qd_empty[s]));
+        if (++s == kShortStages) s = 0;
       }
-      const bool ahead = bufs == 2 && !last;
-      if (ahead) {
-        w.step();
-        ++i;
-        scores(count + 1);
-        if (!ok) break;
-      }
-      ok = wait(&bars.pds_full, count & 1u, kAttnMmaTimeout);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t q = q_lo + this_s * (2 * kTile >> 4);
-      const uint32_t ds = pds_lo + (2 * kTile >> 4);
-      const uint32_t t_dq = t_buf + buf_of(count) * 2 * region;
-      // dq first: others wait for it.
-      mma_x4<2, 128>(t_dq, kLeadK | ds, lead_mn(kv_tile) | kv_lo, idesc_dq, 0u, steps);
-      if (steps > 4)
-        mma_x4<2, 128>(t_dq, kLeadK | (ds + (kTile >> 4)), lead_mn(kv_tile) | (kv_lo + 512u), idesc_dq,
-                       1u, steps - 4);
-      mma_commit_warp(smem_u32(&bars.dq_full[buf_of(count)]));
-      mma_x4<128, 128>(t_dv, mn | pds_lo, mn | (q + (kTile >> 4)), idesc_acc, first ? 0u : 1u, row_steps);
-      if (row_steps > 4)
-        mma_x4<128, 128>(t_dv, mn | (pds_lo + 512u), mn | (q + (kTile >> 4) + 512u), idesc_acc, 1u,
-                         row_steps - 4);
-      mma_x4<128, 128>(t_dk, mn | ds, mn | q, idesc_acc, first ? 0u : 1u, row_steps);
-      if (row_steps > 4)
-        mma_x4<128, 128>(t_dk, mn | (ds + 512u), mn | (q + 512u), idesc_acc, 1u, row_steps - 4);
-      mma_commit_warp(smem_u32(&bars.pds_empty));
-      mma_commit_warp(smem_u32(&bars.qd_empty[this_s]));
-      if (last) {
+      if (ok) {
         mma_commit_warp(smem_u32(&bars.acc_done));
         mma_commit_warp(smem_u32(&bars.kv_empty));
       }
-      ++count;
-      if (!ahead) {
-        if (last) {
-          w.next();
-          live = w.live;
-          i = w.i0;
-          if (live) take_keys();
-        } else {
-          w.step();
-          ++i;
-        }
-        if (live) scores(count);
-      }
     }
     if (!ok) {
-      mma_commit_warp(smem_u32(&bars.drain));
-      mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
+      mma_commit_warp(smem_u32(&bars.drain[1]));
+      mbar_wait_drain(smem_u32(&bars.drain[1]), 0, limit / 8 + 1);
     }
     __syncwarp();
-  } else if (warp >= kEpiWarp) {
+  } else if (warp >= kShortEpi && warp < kShortEpi + 4) {
     // ------------------------------------------------------------ dq out
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     const float f = p.a.scale / bars.ds_scale;
-    const bool leader = warp == kEpiWarp && lane == 0;
+    const bool leader = warp == kShortEpi && lane == 0;
     bool ok = true;
     uint32_t count = 0;
     for (ShortWalk w(p); ok && w.live; w.next()) {
@@ -760,7 +746,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
                 s[c * 16 + j + 1] = __float_as_uint(y);
               }
               tmem_wait_ld_x16(dp);
-              const int valid = l2 == -INFINITY ? 0 : keys - (c0 + c) * 16;
+              const int valid = keys - (c0 + c) * 16;
               if (valid < 16) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -793,7 +779,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
               uint32_t dp[16], hp[8], hd[8];
               tmem_ld_x16(ts + region + (c0 + c) * 16, dp);
               tmem_wait_ld_x16(dp);
-              const int valid = l2 == -INFINITY ? 0 : keys - (c0 + c) * 16;
+              const int valid = keys - (c0 + c) * 16;
               if (valid < 16) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -862,7 +848,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kShortScores) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
