@@ -51,8 +51,8 @@ conv_status_t check_sizes(const cross_attention_args_t& a) {
 
 // The packed mask's extents after broadcasting.
 struct MaskShape {
-  int batches, heads, queries, words;
-  size_t bytes;
+  int batches, heads, queries, words, tiles;
+  size_t bytes, any_bytes;
 };
 
 MaskShape mask_shape(const cross_attention_args_t& a) {
@@ -62,7 +62,9 @@ MaskShape mask_shape(const cross_attention_args_t& a) {
   m.heads = a.mask_stride[1] == 0 ? 1 : a.heads;
   m.queries = a.mask_stride[2] == 0 ? 1 : a.q_len;
   m.words = (a.kv_len + 127) / 128 * 4;
+  m.tiles = (m.queries + kAttnRows - 1) / kAttnRows;
   m.bytes = static_cast<size_t>(m.batches) * m.heads * m.queries * m.words * 4;
+  m.any_bytes = static_cast<size_t>(m.batches) * m.heads * m.tiles * m.words * 4;
   return m;
 }
 
@@ -157,14 +159,15 @@ BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
 
 struct Layout {
   MaskShape mask;
-  size_t mask_at, part_at, stat_at, norm_at, part_q_at, part_kv_at, total;
+  size_t mask_at, any_at, part_at, stat_at, norm_at, part_q_at, part_kv_at, total;
 };
 
 Layout layout(const cross_attention_args_t& a, bool backward, const FwdPlan& f, const BwdPlan& g) {
   Layout l{};
   l.mask = mask_shape(a);
   l.mask_at = CONV_STATUS_BYTES;
-  l.part_at = round_up(l.mask_at + l.mask.bytes, 256);
+  l.any_at = round_up(l.mask_at + l.mask.bytes, 256);
+  l.part_at = round_up(l.any_at + l.mask.any_bytes, 256);
   if (!backward) {
     l.total = round_up(l.part_at + f.part_bytes, 256);
     return l;
@@ -464,8 +467,13 @@ conv_status_t run(const cross_attention_args_t* args, bool backward, void* works
     s.mask_q = l.mask.queries > 1 ? 1 : 0;
     s.mask_h = l.mask.heads > 1 ? l.mask.queries : 0;
     s.mask_b = l.mask.batches > 1 ? static_cast<long long>(l.mask.heads) * l.mask.queries : 0;
+    uint32_t* any = reinterpret_cast<uint32_t*>(ws + l.any_at);
+    s.mask_any = any;
+    s.any_q = l.mask.queries > 1 ? 1 : 0;
+    s.any_h = l.mask.heads > 1 ? l.mask.tiles : 0;
+    s.any_b = l.mask.batches > 1 ? static_cast<long long>(l.mask.heads) * l.mask.tiles : 0;
     if (launch_mask_pack(a.mask, a.mask_stride, l.mask.batches, l.mask.heads, l.mask.queries,
-                         a.kv_len, l.mask.words, bits, stream) != cudaSuccess)
+                         a.kv_len, l.mask.words, bits, any, stream) != cudaSuccess)
       return CONV_ERR_CUDA;
   }
   if (backward) return run_bwd(s, f, g, ws, l, stream);

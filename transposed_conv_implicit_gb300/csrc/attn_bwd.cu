@@ -172,7 +172,6 @@ struct Bars {
   uint64_t drain;
   SplitStart start;
   float ds_scale;
-  uint32_t any[2][4][4];  // dq, by step parity: keys that a row of the quarter attends
   uint32_t tmem;
   int abort_flag;
 };
@@ -193,7 +192,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, uint32_t block_bytes, 
 }
 
 // ------------------------------------------------------------------ dq
-template <typename T, int DP>
+template <typename T, int DP, bool kMask>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_dq_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -272,7 +271,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int xs = 0, ys = 0;
     uint32_t xph = 0, yph = 0, aph = 0;
     long long nx = 0, ny = 0, na = 0;
-    for (Walk<true, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
+    for (Walk<true, kMask, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
       int token, head;
       w.place(0, &token, &head);
       for (int i = 0; ok && i < 2; ++i) {
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (i == 1) ++na;
       }
       aph ^= 1u;
-      for (int t = w.t0; ok && t < w.t1; ++t) {
+      for (int t = w.first(); ok && t < w.t1; t = w.after(t)) {
         ok = wait(&bars.x_empty[xs], xph ^ 1u, kAttnProducerTimeout);
         if (!ok) break;
         if (!(p.fault_mode == 1 && blockIdx.x == 0 && nx == 0)) {
@@ -351,17 +350,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mma_ss_x4(d, kLeadK | a, kLeadK | b, id, 0u, k_steps);
       if (k_steps > 4) mma_ss_x4(d, kLeadK | (a + 1024u), kLeadK | (b + block_lo), id, 1u, k_steps - 4);
     };
-    Walk<true, AttnBwdParams> w(p, start);
-    bool live = w.live;
-    int t = w.t0, cols = 0, k_stage = 0;
+    Walk<true, kMask, AttnBwdParams> w(p, start);
+    bool live = w.live, first = true;
+    int t = live ? w.first() : 0, after = 0, cols = 0, k_stage = 0;
     if (live) {
+      after = w.after(t);
       cols = w.tile_cols(t);
       ok = wait(&bars.a_full[0], 0, kAttnMmaTimeout) && wait(&bars.x_full[0], 0, kAttnMmaTimeout);
       if (ok) {
         tc_fence_after();
         rows_by_keys(tmem, a_lo, x_lo, cols);
         mma_commit_warp(smem_u32(&bars.s_full[0]));
-        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
+        if (after >= w.t1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
         if (++xs == p.x_stages) {
           xs = 0;
           xph ^= 1u;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         rows_by_keys(t_dp, a_lo + (kATile >> 4), y_lo, cols);
         mma_commit_warp(smem_u32(&bars.dp_full));
         mma_commit_warp(smem_u32(&bars.y_empty[0]));
-        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
+        if (after >= w.t1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
         if (++ys == p.y_stages) {
           ys = 0;
           yph ^= 1u;
@@ -381,17 +381,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     while (ok && live) {
-      const bool first = t == w.t0, last = t + 1 == w.t1;
+      const bool last = after >= w.t1;
       const int keys = w.tile_keys(t), this_cols = cols, this_k = k_stage;
+        uint4 any = make_uint4(0, 0, 0, 0);
+      if (kMask) any = w.any_keys(t);
       bool more = true;
       if (last) {
         w.next();
         more = w.live;
-        t = w.t0;
+        if (more) t = w.first();
         aph ^= 1u;
       } else {
-        ++t;
+        t = after;
       }
+      if (more) after = w.after(t);
       if (more) {
         // The next step's S runs beside this step's exponentials ...
         cols = w.tile_cols(t);
@@ -421,15 +424,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ++items;
       }
       if (!ok) break;
-      const bool masked = p.a.mask_bits != nullptr;
-      if (masked || (keys < this_cols && p.a.kv_lengths)) {
-        for (int r0 = 0; r0 < this_cols; r0 += 32) {
+      // Keys that no row takes part with are cleared: nothing they hold meets
+      // a zero of ds.
+      if (kMask || (keys < this_cols && p.a.kv_lengths)) {
+        const uint32_t word[4] = {any.x, any.y, any.z, any.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r0 = k * 32;
           uint32_t used = keys - r0 >= 32 ? 0xFFFFFFFFu : keys > r0 ? (1u << (keys - r0)) - 1u : 0u;
-          if (masked)
-            for (int i = 0, any = 0; i < 4; ++i) {
-              any |= bars.any[count & 1u][i][r0 >> 5];
-              if (i == 3) used &= any;
-            }
+          if (kMask) used &= word[k];
           clear_rows(smem + p.off_x + this_k * kv_tile, kv_block, kBlocks, r0, this_cols, used, lane);
         }
         fence_proxy_async_shared();
@@ -450,12 +453,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ys = 0;
           yph ^= 1u;
         }
-        if (t + 1 == w.t1) {
+        if (after >= w.t1) {
           mma_commit_warp(smem_u32(&bars.a_empty[0]));
           mma_commit_warp(smem_u32(&bars.a_empty[1]));
         }
       }
       ++count;
+      first = last;
       live = more;
     }
     if (!ok) {
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int row_head = p.tile_heads > 1 ? r - row_token * p.tile_heads : 0;
     uint32_t count = 0, items = 0;
     bool ok = true;
-    for (Walk<true, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
+    for (Walk<true, kMask, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
       int token, head;
       w.place(0, &token, &head);
       token += row_token;
@@ -488,16 +492,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                           ((static_cast<long long>(w.b) * p.a.heads + head) * p.q_tiles + (token >> 7)) * 256;
         lse2 = st[token & 127];
         delta = st[128 + (token & 127)];
-        if (p.a.mask_bits)
+        if (kMask)
           bits = p.a.mask_bits +
                  (w.b * p.a.mask_b + head * p.a.mask_h + token * p.a.mask_q) * p.a.mask_words;
       }
       const uint64_t c22 = pack2(c2, c2), l2 = pack2(lse2, lse2), sc2 = pack2(sc, sc),
                      dl2 = pack2(delta * sc, delta * sc);
-      for (int t = w.t0; t < w.t1; ++t) {
+      for (int t = w.first(); t < w.t1; t = w.after(t)) {
         const int keys = w.tile_keys(t), cols = w.tile_cols(t);
         uint32_t word[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (p.a.mask_bits) {
+        if (kMask) {
           uint2 q = make_uint2(0, 0);
           if (bits) q = *reinterpret_cast<const uint2*>(bits + (t * p.kv_box >> 5) + half * 2);
           word[0] = q.x;
@@ -561,13 +565,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_st_x16(ts + c * 16, h);
           }
         }
-        if (p.a.mask_bits) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t any = __reduce_or_sync(0xFFFFFFFFu, word[i]);
-            if (lane == 0) bars.any[buf][quarter][half * 2 + i] = any;
-          }
-        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -627,12 +624,15 @@ __device__ __forceinline__ long long key_steps_uniform(const AttnBwdParams& p) {
   return p.a.kv_lengths ? -1 : key_steps(p, 0);
 }
 
+template <bool kMask>
 struct KeyWalk {
   const AttnBwdParams& p;
   long long left;  // steps after this item
   int b, hk, tile, n;
   int i0, i1;      // steps [i0, i1) of item_steps
-  int head, qt;    // query head and tile of the present step
+  int i, head, qt;  // the present step, its query head and tile
+  uint32_t act;    // steps from act_base on that are worked on (with a mask)
+  int act_base;
   bool live;
   __device__ KeyWalk(const AttnBwdParams& params, const SplitStart& st) : p(params) {
     left = st.left;
@@ -654,12 +654,48 @@ struct KeyWalk {
     qt = from - h * p.q_tiles;
     head = hk * p.a.group + h;
   }
-  // The step after (within the item).
-  __device__ void step() {
-    if (++qt == p.q_tiles) {
-      qt = 0;
+  // The steps of [i0, i1) that are worked on, in order: all, or with a mask
+  // those whose queries attend some key of the tile (the first one if there is
+  // none).  Every lane of a warp calls these together.  `i`, `head` and `qt`
+  // are the present step's.
+  __device__ void first() {
+    act = 0;
+    act_base = i = i0;
+    if (!kMask || i1 - i0 == 1) return;
+    const int to = search(i0);
+    if (to < i1) go(to);
+  }
+  __device__ int after() {
+    if (!kMask || i1 - i0 == 1) return i + 1;
+    const int at = i - act_base;
+    const uint32_t rest = static_cast<uint32_t>(at) < 31u ? act & (0xFFFFFFFEu << at) : 0u;
+    return rest ? act_base + __ffs(rest) - 1 : search(act_base + 32);
+  }
+  __device__ void go(int to) {
+    qt += to - i;
+    i = to;
+    while (qt >= p.q_tiles) {
+      qt -= p.q_tiles;
       ++head;
     }
+  }
+  __device__ int search(int from) {
+    const AttnShape& a = p.a;
+    for (act_base = from; act_base < i1; act_base += 32) {
+      const int s = act_base + (threadIdx.x & 31);
+      bool on = false;
+      if (s < i1) {
+        const int h = s / p.q_tiles;
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            a.mask_any +
+            (b * a.any_b + (hk * a.group + h) * a.any_h + (s - h * p.q_tiles) * a.any_q) * a.mask_words +
+            tile * 4);
+        on = (v.x | v.y | v.z | v.w) != 0;
+      }
+      act = __ballot_sync(0xFFFFFFFFu, on);
+      if (act) return act_base + __ffs(act) - 1;
+    }
+    return i1;
   }
   __device__ void next() {
     live = left > 0;
@@ -678,7 +714,7 @@ struct KeyWalk {
   __device__ int keys() const { return min(kAttnRows, n - tile * kAttnRows); }
 };
 
-template <typename T, int DP>
+template <typename T, int DP, bool kMask>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_dkv_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -761,7 +797,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int xs = 0, ys = 0;
     uint32_t xph = 0, yph = 0, aph = 0;
     long long nx = 0, ny = 0, na = 0, nst = 0;
-    for (KeyWalk w(p, start); ok && w.live; w.next()) {
+    for (KeyWalk<kMask> w(p, start); ok && w.live; w.next()) {
       for (int i = 0; ok && i < 2; ++i) {
         ok = wait(&bars.a_empty[i], aph ^ 1u, kAttnProducerTimeout);
         if (!ok) break;
@@ -775,7 +811,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (i == 1) ++na;
       }
       aph ^= 1u;
-      for (int i = w.i0; ok && i < w.i1; ++i, w.step()) {
+      for (w.first(); ok && w.i < w.i1; w.go(w.after())) {
         const int h = w.head, qt = w.qt;
         ok = wait(&bars.x_empty[xs], xph ^ 1u, kAttnProducerTimeout);
         if (!ok) break;
@@ -846,7 +882,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t a_lo = smem_u32(smem + p.off_a) >> 4, x_lo = smem_u32(smem + p.off_x) >> 4,
                    y_lo = smem_u32(smem + p.off_y) >> 4;
     constexpr uint32_t kTileLo = kTile >> 4;
-    const bool masked = p.a.mask_bits != nullptr;
     bool ok = true;
     int xs = 0, ys = 0;
     uint32_t xph = 0, yph = 0, aph = 0, count = 0, items = 0;
@@ -871,18 +906,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       fence_proxy_async_shared();
       __syncwarp();
     };
-    KeyWalk w(p, start);
-    bool live = w.live;
-    int i = w.i0, cols = 0, x_now = 0, y_now = 0;
+    KeyWalk<kMask> w(p, start);
+    bool live = w.live, first = true;
+    int after = 0, cols = 0, x_now = 0, y_now = 0;
     bool new_item = true;
-    // S^T of the step (i of w), then its dp^T.
+    // S^T of the walk's step, then its dp^T.
     auto step_s = [&](uint32_t step) {
       if (new_item) ok = wait(&bars.a_full[0], aph, kAttnMmaTimeout);
       ok = ok && wait(&bars.x_full[xs], xph, kAttnMmaTimeout);
       if (!ok) return;
       tc_fence_after();
       x_now = xs;
-      if (masked) {
+      if (kMask) {
         ok = wait(&bars.st_full[step & 1u], (step >> 1) & 1u, kAttnMmaTimeout);
         if (!ok) return;
         clear(smem + p.off_x + xs * kTile, step & 1u);
@@ -900,10 +935,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) return;
       tc_fence_after();
       y_now = ys;
-      if (masked) clear(smem + p.off_y + ys * kTile, step & 1u);
+      if (kMask) clear(smem + p.off_y + ys * kTile, step & 1u);
       keys_by_rows(t_dp, a_lo + kTileLo, y_lo + ys * kTileLo, cols);
       mma_commit_warp(smem_u32(&bars.dp_full));
-      if (i + 1 == w.i1) {
+      if (after >= w.i1) {
         mma_commit_warp(smem_u32(&bars.a_empty[0]));
         mma_commit_warp(smem_u32(&bars.a_empty[1]));
       }
@@ -913,6 +948,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     };
     if (live) {
+      w.first();
+      after = w.after();
       cols = w.cols();
       step_s(0);
       if (ok) step_dp(0);
@@ -920,20 +957,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     while (ok && live) {
       // The next step's place first: between the products below there is only
       // what they need.
-      const bool first = i == w.i0, last = i + 1 == w.i1;
+      const bool last = after >= w.i1;
       const int this_cols = cols, this_x = x_now, this_y = y_now;
       bool more = true;
       new_item = last;
       if (last) {
         w.next();
         more = w.live;
-        i = w.i0;
+        if (more) w.first();
         aph ^= 1u;
       } else {
-        w.step();
-        ++i;
+        w.go(after);
       }
-      if (more) cols = w.cols();
+      if (more) {
+        after = w.after();
+        cols = w.cols();
+      }
       if (first) {
         if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
         ++items;
@@ -954,6 +993,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!ok) break;
       mma_commit_warp(smem_u32(&bars.x_empty[this_x]));
       ++count;
+      first = last;
       live = more;
     }
     if (!ok) {
@@ -973,14 +1013,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t* mask_tile = reinterpret_cast<uint32_t*>(smem + p.off_mask);
     uint32_t count = 0, items = 0;
     bool ok = true;
-    for (KeyWalk w(p, start); ok && w.live; w.next()) {
+    for (KeyWalk<kMask> w(p, start); ok && w.live; w.next()) {
       const bool key_ok = r < w.keys();
       const bool keys_whole = w.keys() == kAttnRows;
       bool told = false;  // of a failed wait, at a barrier
-      for (int i = w.i0; i < w.i1; ++i, w.step()) {
+      for (w.first(); w.i < w.i1; w.go(w.after())) {
         const int cols = w.cols(), mine = cols - half * 64;
         uint32_t on[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (p.a.mask_bits) {
+        if (kMask) {
           // The tile's mask words, [query][4 words of 32 keys]: every warp reads
           // its word of 64 queries, one bit per lane.
           const int h = w.head, t0 = w.qt * kAttnRows;
@@ -1005,11 +1045,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
         if (!key_ok) on[0] = on[1] = 0;
-        const bool select = p.a.mask_bits || !keys_whole;
+        const bool select = kMask || !keys_whole;
         const uint32_t ss = count & 1u;
         ok = wait(&bars.st_full[ss], (count >> 1) & 1u, kAttnSoftmaxTimeout) &&
              wait(&bars.s_full[0], count & 1u, kAttnSoftmaxTimeout);
-        if (!p.a.mask_bits && !ok) break;
+        if (!kMask && !ok) break;
         const float* st = reinterpret_cast<const float*>(smem + p.off_stat + ss * 1024) + half * 64;
         uint32_t s[64];
         if (ok) {
@@ -1097,9 +1137,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ++count;
         // (With a mask the warps meet at the next barrier, where a failed one
         // tells the others.)
-        if (!ok && !p.a.mask_bits) break;
+        if (!ok && !kMask) break;
       }
-      if (p.a.mask_bits && !told) ok = barrier_all(1, 256, ok);
+      if (kMask && !told) ok = barrier_all(1, 256, ok);
       if (!ok) break;
       ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
       ++items;
@@ -1251,20 +1291,33 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kMask>
 cudaError_t launch_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
   static std::atomic<size_t> configured[kMaxDevices];
-  cudaError_t e = raise_smem(attn_dq_kernel<T, DP>, configured, smem);
+  cudaError_t e = raise_smem(attn_dq_kernel<T, DP, kMask>, configured, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dq_kernel<T, DP>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+  return launch_pdl(attn_dq_kernel<T, DP, kMask>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool kMask>
 cudaError_t launch_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
   static std::atomic<size_t> configured[kMaxDevices];
-  cudaError_t e = raise_smem(attn_dkv_kernel<T, DP>, configured, smem);
+  cudaError_t e = raise_smem(attn_dkv_kernel<T, DP, kMask>, configured, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dkv_kernel<T, DP>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+  return launch_pdl(attn_dkv_kernel<T, DP, kMask>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+}
+
+// Calls f with the operands' type, whether a row is wider than 64 columns and
+// whether there is a mask.
+template <typename F>
+cudaError_t with_variant(const AttnBwdParams& p, F f) {
+  const auto by_mask = [&](auto type, auto wide) {
+    return p.a.mask_bits ? f(type, wide, std::true_type{}) : f(type, wide, std::false_type{});
+  };
+  const auto by_width = [&](auto type) {
+    return p.a.head_dim > 64 ? by_mask(type, std::true_type{}) : by_mask(type, std::false_type{});
+  };
+  return p.a.dtype == 0 ? by_width(__nv_bfloat16{}) : by_width(__half{});
 }
 
 }  // namespace
@@ -1279,21 +1332,15 @@ cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_attn_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
-  const bool wide = p.a.head_dim > 64;
-  if (p.a.dtype == 0)
-    return wide ? launch_dq<__nv_bfloat16, 128>(p, grid, smem, stream)
-                : launch_dq<__nv_bfloat16, 64>(p, grid, smem, stream);
-  return wide ? launch_dq<__half, 128>(p, grid, smem, stream)
-              : launch_dq<__half, 64>(p, grid, smem, stream);
+  return with_variant(p, [&](auto type, auto wide, auto mask) {
+    return launch_dq<decltype(type), wide() ? 128 : 64, mask()>(p, grid, smem, stream);
+  });
 }
 
 cudaError_t launch_attn_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
-  const bool wide = p.a.head_dim > 64;
-  if (p.a.dtype == 0)
-    return wide ? launch_dkv<__nv_bfloat16, 128>(p, grid, smem, stream)
-                : launch_dkv<__nv_bfloat16, 64>(p, grid, smem, stream);
-  return wide ? launch_dkv<__half, 128>(p, grid, smem, stream)
-              : launch_dkv<__half, 64>(p, grid, smem, stream);
+  return with_variant(p, [&](auto type, auto wide, auto mask) {
+    return launch_dkv<decltype(type), wide() ? 128 : 64, mask()>(p, grid, smem, stream);
+  });
 }
 
 cudaError_t launch_attn_bwd_join(const AttnBwdParams& p, int q_ctas, int kv_ctas,

@@ -151,7 +151,7 @@ __device__ SplitStart split_rows(const P& p, int lane) {
 }
 
 // Walks a CTA's work: every role walks the same sequence.
-template <bool kSplit, typename P>
+template <bool kSplit, bool kMask, typename P>
 struct Walk {
   const P& p;
   long long pos;       // pairs: item index; split: steps left after this item
@@ -159,6 +159,8 @@ struct Walk {
   int tiles_here;      // row tiles of the item
   int n;               // valid keys
   int t0, t1, nt;      // key tiles [t0, t1) of nt
+  uint32_t act;        // tiles from act_base on that are worked on (with a mask)
+  int act_base;
   bool live;
 
   __device__ Walk(const P& params, const SplitStart& st) : p(params) {
@@ -228,6 +230,58 @@ struct Walk {
       *token = (rt - hg * p.token_tiles) * kAttnRows;
       *head = hk * p.a.group + hg;
     }
+  }
+  // Keys of tile t that some row of the item's tiles may attend, by the mask
+  // (of all queries of the tiles of 128 that the rows lie in).
+  __device__ uint4 any_keys(int t) const {
+    const AttnShape& a = p.a;
+    uint4 any = make_uint4(0, 0, 0, 0);
+    for (int g = 0; g < tiles_here; ++g) {
+      int token, head;
+      place(g, &token, &head);
+      const int q0 = a.any_q ? token >> 7 : 0;
+      const int q1 = a.any_q ? (min(token + p.tile_tokens, a.q_len) - 1) >> 7 : 0;
+      const int heads = a.any_h ? p.tile_heads : 1;
+      for (int h = head; h < head + heads; ++h)
+        for (int q = q0; q <= q1; ++q) {
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              a.mask_any + (b * a.any_b + h * a.any_h + q * a.any_q) * a.mask_words + (t * p.kv_box >> 5));
+          any.x |= v.x;
+          any.y |= v.y;
+          any.z |= v.z;
+          any.w |= v.w;
+        }
+    }
+    return any;
+  }
+  // The key tiles of [t0, t1) that are worked on, in order: all, or with a
+  // mask those that some row attends (the first one if there is none).  Every
+  // lane of a warp calls these together.
+  __device__ int first() {
+    act = 0;
+    act_base = t0;
+    if (!kMask || t1 - t0 == 1) return t0;
+    const int t = search(t0);
+    return t < t1 ? t : t0;
+  }
+  __device__ int after(int t) {
+    if (!kMask || t1 - t0 == 1) return t + 1;
+    const int at = t - act_base;
+    const uint32_t rest = static_cast<uint32_t>(at) < 31u ? act & (0xFFFFFFFEu << at) : 0u;
+    return rest ? act_base + __ffs(rest) - 1 : search(act_base + 32);
+  }
+  __device__ int search(int from) {
+    for (act_base = from; act_base < t1; act_base += 32) {
+      const int t = act_base + (threadIdx.x & 31);
+      bool on = false;
+      if (t < t1) {
+        const uint4 v = any_keys(t);
+        on = (v.x | v.y | v.z | v.w) != 0;
+      }
+      act = __ballot_sync(0xFFFFFFFFu, on);
+      if (act) return act_base + __ffs(act) - 1;
+    }
+    return t1;
   }
   // Keys of tile t that are valid, and the columns multiplied for them.
   __device__ int tile_keys(int t) const { return max(0, min(p.kv_box, n - t * p.kv_box)); }

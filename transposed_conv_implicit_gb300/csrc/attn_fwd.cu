@@ -59,36 +59,6 @@ struct Layout {
 
 constexpr int kMaxStages = 8;
 
-// Keys of tile t that some row of the item's row tiles attends, by the mask
-// alone.  One warp: lanes share out the tiles' mask rows.
-template <typename W>
-__device__ uint4 tile_any(const AttnFwdParams& p, const W& w, int t, int lane) {
-  const AttnShape& a = p.a;
-  uint4 any = make_uint4(0, 0, 0, 0);
-  for (int g = 0; g < w.tiles_here; ++g) {
-    int token, head;
-    w.place(g, &token, &head);
-    const int tokens = a.mask_q ? min(p.tile_heads > 1 ? p.tile_tokens : kAttnRows, a.q_len - token) : 1;
-    const int heads = a.mask_h ? p.tile_heads : 1;
-    const uint32_t* bits =
-        a.mask_bits + (w.b * a.mask_b + head * a.mask_h + token * a.mask_q) * a.mask_words +
-        (t * p.kv_box >> 5);
-    for (int h = 0; h < heads; ++h)
-      for (int i = lane; i < tokens; i += 32) {
-        const uint4 v = *reinterpret_cast<const uint4*>(bits + (h * a.mask_h + i * a.mask_q) * a.mask_words);
-        any.x |= v.x;
-        any.y |= v.y;
-        any.z |= v.z;
-        any.w |= v.w;
-      }
-  }
-  any.x = __reduce_or_sync(0xFFFFFFFFu, any.x);
-  any.y = __reduce_or_sync(0xFFFFFFFFu, any.y);
-  any.z = __reduce_or_sync(0xFFFFFFFFu, any.z);
-  any.w = __reduce_or_sync(0xFFFFFFFFu, any.w);
-  return any;
-}
-
 struct Bars {
   uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   uint64_t q_full[2][2], q_empty[2][2];  // [group][stage]
@@ -100,7 +70,7 @@ struct Bars {
   int abort_flag;
 };
 
-template <typename T, int DP, int G>
+template <typename T, int DP, int G, bool kMask>
 __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     attn_fwd_kernel(const __grid_constant__ AttnFwdParams p) {
   using L = Layout<T, DP, G>;
@@ -175,7 +145,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     uint32_t phase = 0, q_phase = 0;
     long long issued = 0;
     long long q_issued[2] = {0, 0};
-    for (Walk<L::kSplit, AttnFwdParams> w(p, start); ok && w.live; w.next()) {
+    for (Walk<L::kSplit, kMask, AttnFwdParams> w(p, start); ok && w.live; w.next()) {
       // Both groups' stages move together.  A group without a row tile in
       // this item has its stage's phase completed for it (group 1 first, so
       // that its wait precedes everything that ends the phase).
@@ -203,7 +173,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         qs = 0;
         q_phase ^= 1u;
       }
-      for (int t = w.t0; ok && t < w.t1; ++t) {
+      for (int t = w.first(); ok && t < w.t1; t = w.after(t)) {
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (!wait(&bars.kv_empty[stage], phase ^ 1u, kAttnProducerTimeout)) {
@@ -278,18 +248,18 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       if (G == 2 && lane == 0) mbar_arrive(smem_u32(&bars.turn[g ^ 1]));
       ++turns;
     };
-    Walk<L::kSplit, AttnFwdParams> w(p, start);
+    Walk<L::kSplit, kMask, AttnFwdParams> w(p, start);
     // Items without a row tile for this group: their stages are passed on.
     auto skip_absent = [&]() {
       while (G == 2 && ok && w.live && g >= w.tiles_here) {
-        for (int i = 2 * (w.t1 - w.t0); ok && i > 0; --i) {
-          ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
-          if (ok && lane == 0) mbar_arrive(smem_u32(&bars.kv_empty[stage]));
-          advance();
-          if (i & 1) {  // a step
-            ok = ok && take_turn();
-            if (ok) end_turn();
+        for (int t = w.first(); ok && t < w.t1; t = w.after(t)) {
+          for (int i = 0; ok && i < 2; ++i) {
+            ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+            if (ok && lane == 0) mbar_arrive(smem_u32(&bars.kv_empty[stage]));
+            advance();
           }
+          ok = ok && take_turn();
+          if (ok) end_turn();
         }
         mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
         next_q();
@@ -307,8 +277,10 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     };
     skip_absent();
     bool live = ok && w.live;
-    int t = w.t0, cols = 0;
+    int t = live ? w.first() : 0, after = 0, cols = 0;
+    bool first = true;
     if (live) {
+      after = w.after(t);
       cols = w.tile_cols(t);
       ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout) &&
            wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
@@ -316,14 +288,13 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         tc_fence_after();
         scores(stage, cols);
         mma_commit_warp(smem_u32(&bars.kv_empty[stage]));
-        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+        if (after >= w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
         advance();
       }
     }
     while (ok && live) {
       // This step's values, then the next step's keys.
       const int v_stage = stage, keys = w.tile_keys(t), this_cols = cols;
-      const bool first = t == w.t0;
       ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
       if (!ok) break;
       advance();
@@ -331,9 +302,9 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       // nothing they hold meets a zero of P: keys past the request's length
       // (past the tensor's end the load has filled zeros), and masked keys.
       // (Each group's warp clears them; both write the same zeros.)
-      if (p.a.mask_bits || (keys < this_cols && p.a.kv_lengths)) {
+      if (kMask || (keys < this_cols && p.a.kv_lengths)) {
         uint4 any = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
-        if (p.a.mask_bits) any = tile_any(p, w, t, lane);
+        if (kMask) any = w.any_keys(t);
         const uint32_t word[4] = {any.x, any.y, any.z, any.w};
         uint4* row0 = reinterpret_cast<uint4*>(smem + p.off_kv + v_stage * kv_tile);
 #pragma unroll
@@ -350,18 +321,19 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         __syncwarp();
       }
       bool more = true, next_item = false;
-      if (t + 1 == w.t1) {
+      if (after >= w.t1) {
         w.next();
         next_q();
         skip_absent();
         if (!ok) break;
         more = w.live;
         next_item = true;
-        t = w.t0;
+        if (more) t = w.first();
       } else {
-        ++t;
+        t = after;
       }
       if (more) {
+        after = w.after(t);
         cols = w.tile_cols(t);
         if (next_item) ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout);
         ok = ok && wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
@@ -398,8 +370,9 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       mma_commit_warp(smem_u32(&bars.kv_empty[v_stage]));
       if (more) {
         mma_commit_warp(smem_u32(&bars.kv_empty[k_stage]));
-        if (t + 1 == w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+        if (after >= w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
       }
+      first = next_item;
       live = more;
     }
     if (!ok) {
@@ -424,7 +397,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     const int row_head = p.tile_heads > 1 ? r - row_token * p.tile_heads : 0;
     uint32_t tiles = 0;  // S tiles seen: barrier parity
     bool ok = true;
-    for (Walk<L::kSplit, AttnFwdParams> w(p, start); ok && w.live; w.next()) {
+    for (Walk<L::kSplit, kMask, AttnFwdParams> w(p, start); ok && w.live; w.next()) {
       if (g >= w.tiles_here) continue;
       int token, head;
       w.place(g, &token, &head);
@@ -433,14 +406,15 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       const bool row_ok = row_token < p.tile_tokens && token < p.a.q_len;
       const bool warp_ok = __any_sync(0xFFFFFFFFu, row_ok);
       const uint32_t* bits = nullptr;
-      if (p.a.mask_bits && row_ok)
+      if (kMask && row_ok)
         bits = p.a.mask_bits +
                (w.b * p.a.mask_b + head * p.a.mask_h + token * p.a.mask_q) * p.a.mask_words;
       float m = -INFINITY, mc = 0.f, l = 0.f;
-      for (int t = w.t0; t < w.t1; ++t) {
+      bool first = true;
+      for (int t = w.first(); t < w.t1; t = w.after(t), first = false) {
         const int keys = w.tile_keys(t), cols = w.tile_cols(t);
         uint32_t word[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (p.a.mask_bits) {
+        if (kMask) {
           // A tile of kv_box keys starts inside a row of whole 128-key words
           // only when it is the row's single tile (kv_box < 128).
           uint4 q = make_uint4(0, 0, 0, 0);
@@ -452,7 +426,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         tc_fence_after();
         // The row's running maximum takes in `mx`.
         auto grow = [&](float mx) __attribute__((always_inline)) {
-          if (t == w.t0) {
+          if (first) {
             m = mx;
             mc = m == -INFINITY ? 0.f : m * c2;
           } else {
@@ -483,7 +457,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
             }
           }
         };
-        if (keys == 128 && !p.a.mask_bits) {
+        if (keys == 128 && !kMask) {
           // A whole tile: straight-line code.
           if (warp_ok) {
             uint32_t s[128];
@@ -805,12 +779,18 @@ __global__ void __launch_bounds__(256) attn_no_keys_kernel(const AttnShape a) {
   }
 }
 
+template <typename T, int DP, int G, bool kMask>
+cudaError_t launch_masked(const AttnFwdParams& p, int grid, size_t smem, cudaStream_t stream) {
+  static std::atomic<size_t> configured[kMaxDevices];
+  const cudaError_t err = raise_smem(attn_fwd_kernel<T, DP, G, kMask>, configured, smem);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(attn_fwd_kernel<T, DP, G, kMask>, dim3(grid), dim3(Layout<T, DP, G>::kThreads), smem, stream, p);
+}
+
 template <typename T, int DP, int G>
 cudaError_t launch_one(const AttnFwdParams& p, int grid, size_t smem, cudaStream_t stream) {
-  static std::atomic<size_t> configured[kMaxDevices];
-  const cudaError_t err = raise_smem(attn_fwd_kernel<T, DP, G>, configured, smem);
-  if (err != cudaSuccess) return err;
-  return launch_pdl(attn_fwd_kernel<T, DP, G>, dim3(grid), dim3(Layout<T, DP, G>::kThreads), smem, stream, p);
+  return p.a.mask_bits ? launch_masked<T, DP, G, true>(p, grid, smem, stream)
+                       : launch_masked<T, DP, G, false>(p, grid, smem, stream);
 }
 
 template <typename T>

@@ -1,6 +1,8 @@
 // The byte mask of a cross-attention call as bits, one per key: an eighth of
-// its bytes for the kernels that read it up to three times, and in words that
-// a row's thread takes whole.
+// its bytes for the kernels that read it up to three times, in words that a
+// row's thread takes whole; and, for every 128 queries, which keys any of them
+// attends, so that the kernels skip key tiles that nobody attends and clear
+// keys that must not meet a product.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -14,49 +16,69 @@ namespace convgb300 {
 
 namespace {
 
-// One word (32 keys) per warp step: each lane reads one byte and the ballot is
-// the word.  Bound by the mask's bytes.
+// One block packs 128 queries x 128 keys: a warp takes every eighth row, each
+// lane four bytes of it, a ballot makes a word.  All of a warp's 64 reads are
+// independent; bound by the mask's bytes.
 __global__ void __launch_bounds__(256)
     mask_pack_kernel(const unsigned char* mask, long long sb, long long sh, long long sq,
-                     long long sk, int heads, int queries, int keys, int words, long long total,
-                     uint32_t* bits) {
-  const int lane = threadIdx.x & 31;
-  const long long warps = static_cast<long long>(gridDim.x) * (blockDim.x >> 5);
+                     long long sk, int heads, int queries, int keys, int words, int tiles,
+                     uint32_t* bits, uint32_t* any) {
+  __shared__ uint4 seen[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int across = words >> 2;
+  const unsigned row = blockIdx.x / across;  // of `any`
+  const int col = static_cast<int>(blockIdx.x - row * across);
+  const long long bh = row / tiles;
+  const int tile = static_cast<int>(row - bh * tiles);
+  const long long b = bh / heads, h = bh - b * heads;
+  const int i0 = tile * kAttnRows + warp;
+  const int j0 = col * 128 + lane;
+  const unsigned char* p = mask + b * sb + h * sh + i0 * sq + j0 * sk;
   grid_dependency_wait();
-  for (long long row = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-       row < total; row += warps) {
-    const long long bh = row / queries;
-    const long long i = row - bh * queries;
-    const long long b = bh / heads, h = bh - b * heads;
-    const unsigned char* p = mask + b * sb + h * sh + i * sq;
-    for (int w0 = 0; w0 < words; w0 += 4) {
-      uint32_t word[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int j = (w0 + u) * 32 + lane;
-        const bool on = j < keys && p[j * sk] != 0;
-        word[u] = __ballot_sync(0xFFFFFFFFu, on);
-      }
-      if (lane == 0)
-        *reinterpret_cast<uint4*>(bits + row * words + w0) =
-            make_uint4(word[0], word[1], word[2], word[3]);
-    }
-  }
   grid_launch_dependents();
+  uint4 all = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int u = 0; u < 16; ++u) {
+    const int i = i0 + u * 8;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool on = i < queries && j0 + k * 32 < keys && p[u * 8 * sq + k * 32 * sk] != 0;
+      w[k] = __ballot_sync(0xFFFFFFFFu, on);
+    }
+    if (lane == 0 && i < queries)
+      *reinterpret_cast<uint4*>(bits + (bh * queries + i) * words + col * 4) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    all.x |= w[0];
+    all.y |= w[1];
+    all.z |= w[2];
+    all.w |= w[3];
+  }
+  if (lane == 0) seen[warp] = all;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 8; ++k) {
+      all.x |= seen[k].x;
+      all.y |= seen[k].y;
+      all.z |= seen[k].z;
+      all.w |= seen[k].w;
+    }
+    *reinterpret_cast<uint4*>(any + static_cast<long long>(row) * words + col * 4) = all;
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_mask_pack(const unsigned char* mask, const long long stride[4], int batches,
                              int heads, int queries, int keys, int words, uint32_t* bits,
-                             cudaStream_t stream) {
-  const long long total = static_cast<long long>(batches) * heads * queries;
-  const int sms = attn_sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int grid = static_cast<int>(std::min<long long>((total + 7) / 8, sms * 8ll));
-  if (grid == 0) return cudaSuccess;
-  return launch_pdl(mask_pack_kernel, dim3(grid), dim3(256), 0, stream, mask, stride[0], stride[1],
-                    stride[2], stride[3], heads, queries, keys, words, total, bits);
+                             uint32_t* any, cudaStream_t stream) {
+  const int tiles = (queries + kAttnRows - 1) / kAttnRows;
+  const long long blocks = static_cast<long long>(batches) * heads * tiles * (words / 4);
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;  // 2^45 bytes of mask
+  return launch_pdl(mask_pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                    stream, mask, stride[0], stride[1], stride[2], stride[3], heads, queries, keys,
+                    words, tiles, bits, any);
 }
 
 }  // namespace convgb300

@@ -27,6 +27,10 @@ struct AttnShape {
   const uint32_t* mask_bits;
   int mask_words;
   long long mask_b, mask_h, mask_q;
+  // Keys that some query of a tile of 128 attends, in rows like mask_bits':
+  // row of (b, h, tile): b * any_b + h * any_h + tile * any_q.
+  const uint32_t* mask_any;
+  long long any_b, any_h, any_q;
 };
 
 constexpr int kAttnRows = 128;  // rows of one MMA: TMEM lanes
@@ -122,10 +126,10 @@ cudaError_t launch_attn_short_bwd(const AttnBwdParams& p, int grid, size_t smem,
 // Without keys: zeros to out (batch, q_len, heads rows) and -inf to lse.
 cudaError_t launch_attn_no_keys(const AttnShape& a, cudaStream_t stream);
 
-// Packs the byte mask into AttnShape::mask_bits (batches x heads x queries
+// Packs the byte mask into AttnShape::mask_bits and mask_any (batches x heads x queries
 // rows, extents after broadcasting).
 cudaError_t launch_mask_pack(const unsigned char* mask, const long long stride[4], int batches,
                              int heads, int queries, int keys, int words, uint32_t* bits,
-                             cudaStream_t stream);
+                             uint32_t* any, cudaStream_t stream);
 
 }  // namespace convgb300
