@@ -178,8 +178,9 @@ struct Bars {
 
 static_assert(sizeof(Bars) <= 1024, "shared-memory plan of the dk, dv kernel");
 
-constexpr int kBwdThreads = 320;  // 8 softmax warps, products, loads
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSoftWarps = 16;  // a quarter of the lanes and of the columns each
+constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
+constexpr int kBwdThreads = 32 * (kSoftWarps + 2);
 
 __device__ __forceinline__ void clear_rows(uint8_t* tile, uint32_t block_bytes, int blocks, int r0,
                                            int limit, uint32_t keep, int lane) {
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(smem_u32(&bars.a_full[i]), 1);
       mbar_init(smem_u32(&bars.a_empty[i]), 1);
       mbar_init(smem_u32(&bars.s_full[i]), 1);
-      mbar_init(smem_u32(&bars.ds_full[i]), 8);
+      mbar_init(smem_u32(&bars.ds_full[i]), kSoftWarps);
     }
     for (int i = 0; i < p.x_stages; ++i) {
       mbar_init(smem_u32(&bars.x_full[i]), 1);
@@ -223,9 +224,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(smem_u32(&bars.y_empty[i]), 1);
     }
     mbar_init(smem_u32(&bars.dp_full), 1);
-    mbar_init(smem_u32(&bars.dp_free), 8);
+    mbar_init(smem_u32(&bars.dp_free), kSoftWarps);
     mbar_init(smem_u32(&bars.acc_done), 1);
-    mbar_init(smem_u32(&bars.acc_free), 8);
+    mbar_init(smem_u32(&bars.acc_free), kSoftWarps);
     mbar_init(smem_u32(&bars.drain), 1);
     bars.abort_flag = 0;
     fence_barrier_init();
@@ -442,8 +443,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint32_t ds = tmem + (count & 1u) * 128;
       const int steps = this_cols >> 4;
       const uint32_t kb = lead_k | (x_lo + this_k * tile_lo);
-      mma_ts_x4(t_acc, ds, kb, idesc_acc, first ? 0u : 1u, steps);
-      if (steps > 4) mma_ts_x4(t_acc, ds + 64, kb + 512u, idesc_acc, 1u, steps - 4);
+      mma_ts_x4<32>(t_acc, ds, kb, idesc_acc, first ? 0u : 1u, steps);
+      if (steps > 4) mma_ts_x4<32>(t_acc, ds + 64, kb + 512u, idesc_acc, 1u, steps - 4);
       if (last) mma_commit_warp(smem_u32(&bars.acc_done));
       // (Stages are handed back after the products that others wait for.)
       mma_commit_warp(smem_u32(&bars.x_empty[this_k]));
@@ -469,8 +470,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ p and ds
-    // Two warps share a quarter of the lanes; each takes half of the keys.
-    const int half = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    // Four warps share a quarter of the lanes; each takes 32 of the keys.
+    const int part = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     // (p is held times 2^p_shift here too; ds's scale takes it out.)
     const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
@@ -500,70 +501,52 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                      dl2 = pack2(delta * sc, delta * sc);
       for (int t = w.first(); t < w.t1; t = w.after(t)) {
         const int keys = w.tile_keys(t), cols = w.tile_cols(t);
-        uint32_t word[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (kMask) {
-          uint2 q = make_uint2(0, 0);
-          if (bits) q = *reinterpret_cast<const uint2*>(bits + (t * p.kv_box >> 5) + half * 2);
-          word[0] = q.x;
-          word[1] = q.y;
-        }
+        const int rest = keys - part * 32;  // of this warp's columns
+        uint32_t on = rest >= 32 ? 0xFFFFFFFFu : rest <= 0 ? 0u : (1u << rest) - 1u;
+        if (kMask) on &= bits ? bits[(t * p.kv_box >> 5) + part] : 0u;
         const uint32_t buf = count & 1u;
         ok = wait(&bars.s_full[buf], (count >> 1) & 1u, kAttnSoftmaxTimeout);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ts = tmem + buf * 128 + half * 64 + lane_field;
-        const uint32_t td = t_dp + half * 64 + lane_field;
-        const int mine = cols - half * 64;  // columns of this half
-        uint32_t s[64];
+        const uint32_t ts = tmem + buf * 128 + part * 32 + lane_field;
+        const uint32_t td = t_dp + part * 32 + lane_field;
+        const bool mine = part * 32 < cols;
+        uint32_t s[32];
+        if (mine) {
+          tmem_ld_x32(ts, s);
+          tmem_wait_ld_x32(s);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (c * 32 < mine) tmem_ld_x32(ts + c * 32, s + c * 32);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c * 32 < mine) {
-            tmem_wait_ld_x32(s + c * 32);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x, y;
-              unpack2(fma2(pack2(__uint_as_float(s[c * 32 + 2 * i]),
-                                 __uint_as_float(s[c * 32 + 2 * i + 1])), c22, l2), x, y);
-              s[c * 32 + 2 * i] = __float_as_uint(exp2_approx(x));
-              s[c * 32 + 2 * i + 1] = __float_as_uint(exp2_approx(y));
-            }
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c22, l2), x, y);
+            s[2 * i] = __float_as_uint(exp2_approx(x));
+            s[2 * i + 1] = __float_as_uint(exp2_approx(y));
           }
         }
         ok = wait(&bars.dp_full, count & 1u, kAttnSoftmaxTimeout);
         if (!ok) break;
         tc_fence_after();
+        if (mine) {
+          uint32_t dp[32], h[16];
+          tmem_ld_x32(td, dp);
+          tmem_wait_ld_x32(dp);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (c * 32 < mine) {
-            uint32_t dp[32], h[16];
-            tmem_ld_x32(td + c * 32, dp);
-            tmem_wait_ld_x32(dp);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x, y;
-              unpack2(mul2(fma2(pack2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), sc2,
-                                dl2),
-                           pack2(__uint_as_float(s[c * 32 + 2 * i]),
-                                 __uint_as_float(s[c * 32 + 2 * i + 1]))), x, y);
-              dp[2 * i] = __float_as_uint(x);
-              dp[2 * i + 1] = __float_as_uint(y);
-            }
-            uint32_t on = word[c];
-            const int rest = keys - half * 64 - c * 32;
-            if (rest < 32) on &= rest <= 0 ? 0u : (1u << rest) - 1u;
-            if (on != 0xFFFFFFFFu) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((on >> i) & 1u)) dp[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              h[i] = round2<T>(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
-            tmem_st_x16(ts + c * 16, h);
+          for (int i = 0; i < 16; ++i) {
+            float x, y;
+            unpack2(mul2(fma2(pack2(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1])), sc2, dl2),
+                         pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]))), x, y);
+            dp[2 * i] = __float_as_uint(x);
+            dp[2 * i + 1] = __float_as_uint(y);
           }
+          if (on != 0xFFFFFFFFu) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((on >> i) & 1u)) dp[i] = 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            h[i] = round2<T>(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
+          tmem_st_x16(ts, h);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -582,9 +565,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const bool whole = w.t0 == 0 && w.t1 == w.nt;
       const long long slot = 2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0);
       const float f = p.a.scale / bars.ds_scale;
-#pragma unroll
-      for (int c = 0; c < DP / 2; c += 32) {
-        const int col = half * (DP / 2) + c;
+      const int col = part * 32;
+      if (col < DP) {
         uint32_t v[32];
         tmem_ld_x32(t_acc + col + lane_field, v);
         tmem_wait_ld_x32(v);
@@ -742,14 +724,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.st_full[i]), 1);
-      mbar_init(smem_u32(&bars.st_empty[i]), 8);
+      mbar_init(smem_u32(&bars.st_empty[i]), kSoftWarps);
     }
     mbar_init(smem_u32(&bars.s_full[0]), 1);
     mbar_init(smem_u32(&bars.dp_full), 1);
-    mbar_init(smem_u32(&bars.p_full), 8);
-    mbar_init(smem_u32(&bars.ds_full[0]), 8);
+    mbar_init(smem_u32(&bars.p_full), kSoftWarps);
+    mbar_init(smem_u32(&bars.ds_full[0]), kSoftWarps);
     mbar_init(smem_u32(&bars.acc_done), 1);
-    mbar_init(smem_u32(&bars.acc_free), 8);
+    mbar_init(smem_u32(&bars.acc_free), kSoftWarps);
     mbar_init(smem_u32(&bars.drain), 1);
     bars.abort_flag = 0;
     fence_barrier_init();
@@ -893,8 +875,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // A (in TMEM, halves of 64 columns) times a query tile, over its rows.
     auto accumulate = [&](uint32_t acc, uint32_t a, uint32_t b, int cols, bool fresh) {
       const int steps = cols >> 4;
-      mma_ts_x4(acc, a, lead_b | b, idesc_acc, fresh ? 0u : 1u, steps);
-      if (steps > 4) mma_ts_x4(acc, a + 64, lead_b | (b + 512u), idesc_acc, 1u, steps - 4);
+      mma_ts_x4<32>(acc, a, lead_b | b, idesc_acc, fresh ? 0u : 1u, steps);
+      if (steps > 4) mma_ts_x4<32>(acc, a + 64, lead_b | (b + 512u), idesc_acc, 1u, steps - 4);
     };
     // Queries without keys are cleared: nothing they hold meets a zero of p or ds.
     auto clear = [&](uint8_t* tile, int stat_stage) {
@@ -1003,13 +985,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ p and ds
-    // One thread per key and half of the queries.
-    const int half = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    // One thread per key and 32 of the queries.
+    const int part = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
     const uint64_t c22 = pack2(c2, c2), sc2 = pack2(sc, sc);
     const int d = p.a.head_dim;
-    const uint32_t ts = t_s + half * 64 + lane_field, td = t_dp + half * 64 + lane_field;
+    const uint32_t ts = t_s + part * 32 + lane_field, td = t_dp + part * 32 + lane_field;
     uint32_t* mask_tile = reinterpret_cast<uint32_t*>(smem + p.off_mask);
     uint32_t count = 0, items = 0;
     bool ok = true;
@@ -1018,71 +1000,58 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const bool keys_whole = w.keys() == kAttnRows;
       bool told = false;  // of a failed wait, at a barrier
       for (w.first(); w.i < w.i1; w.go(w.after())) {
-        const int cols = w.cols(), mine = cols - half * 64;
-        uint32_t on[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        const bool mine = part * 32 < w.cols();
+        uint32_t on = 0xFFFFFFFFu;
         if (kMask) {
           // The tile's mask words, [query][4 words of 32 keys]: every warp reads
-          // its word of 64 queries, one bit per lane.
+          // its word of 32 queries, one bit per lane.
           const int h = w.head, t0 = w.qt * kAttnRows;
           uint32_t* buf = mask_tile + (count & 1u) * 512;
-          const int row = threadIdx.x >> 1, pair = threadIdx.x & 1;
-          uint2 q = make_uint2(0, 0);
+          const int row = threadIdx.x >> 2, word = threadIdx.x & 3;
+          uint32_t q = 0;
           if (t0 + row < p.a.q_len)
-            q = *reinterpret_cast<const uint2*>(
-                p.a.mask_bits +
-                (w.b * p.a.mask_b + h * p.a.mask_h + (t0 + row) * p.a.mask_q) * p.a.mask_words +
-                w.tile * 4 + pair * 2);
-          *reinterpret_cast<uint2*>(buf + row * 4 + pair * 2) = q;
-          ok = barrier_all(1, 256, ok);
+            q = p.a.mask_bits[(w.b * p.a.mask_b + h * p.a.mask_h + (t0 + row) * p.a.mask_q) *
+                                  p.a.mask_words + w.tile * 4 + word];
+          buf[row * 4 + word] = q;
+          ok = barrier_all(1, 32 * kSoftWarps, ok);
           told = !ok;
           if (!ok) break;
+          on = 0;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            on[c] = 0;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              on[c] |= ((buf[(half * 64 + c * 32 + j) * 4 + quarter] >> lane) & 1u) << j;
-          }
+          for (int j = 0; j < 32; ++j) on |= ((buf[(part * 32 + j) * 4 + quarter] >> lane) & 1u) << j;
         }
-        if (!key_ok) on[0] = on[1] = 0;
+        if (!key_ok) on = 0;
         const bool select = kMask || !keys_whole;
         const uint32_t ss = count & 1u;
         ok = wait(&bars.st_full[ss], (count >> 1) & 1u, kAttnSoftmaxTimeout) &&
              wait(&bars.s_full[0], count & 1u, kAttnSoftmaxTimeout);
         if (!kMask && !ok) break;
-        const float* st = reinterpret_cast<const float*>(smem + p.off_stat + ss * 1024) + half * 64;
-        uint32_t s[64];
+        const float* st = reinterpret_cast<const float*>(smem + p.off_stat + ss * 1024) + part * 32;
+        uint32_t s[32];
         if (ok) {
           tc_fence_after();
+          if (mine) {
+            tmem_ld_x32(ts, s);
+            tmem_wait_ld_x32(s);
+            uint32_t h[16];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (c * 32 < mine) tmem_ld_x32(ts + c * 32, s + c * 32);
+            for (int j = 0; j < 32; j += 4) {
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + j);
+              float x[4];
+              unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), c22, l.x), x[0], x[1]);
+              unpack2(fma2(pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3])), c22, l.y), x[2], x[3]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c * 32 < mine) {
-              tmem_wait_ld_x32(s + c * 32);
-              uint32_t h[16];
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + c * 32 + j);
-                float x[4];
-                unpack2(fma2(pack2(__uint_as_float(s[c * 32 + j]), __uint_as_float(s[c * 32 + j + 1])),
-                             c22, l.x), x[0], x[1]);
-                unpack2(fma2(pack2(__uint_as_float(s[c * 32 + j + 2]), __uint_as_float(s[c * 32 + j + 3])),
-                             c22, l.y), x[2], x[3]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[c * 32 + j + k] = __float_as_uint(exp2_approx(x[k]));
-              }
-              if (select) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!((on[c] >> j) & 1u)) s[c * 32 + j] = 0u;
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                h[j] = round2<T>(__uint_as_float(s[c * 32 + 2 * j]), __uint_as_float(s[c * 32 + 2 * j + 1]));
-              tmem_st_x16(ts + c * 16, h);
+              for (int k = 0; k < 4; ++k) s[j + k] = __float_as_uint(exp2_approx(x[k]));
             }
+            if (select) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((on >> j) & 1u)) s[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              h[j] = round2<T>(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+            tmem_st_x16(ts, h);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -1092,39 +1061,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (ok) {
           tc_fence_after();
+          if (mine) {
+            uint32_t dp[32], h[16];
+            tmem_ld_x32(td, dp);
+            tmem_wait_ld_x32(dp);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            if (c * 32 < mine) {
-              uint32_t dp[32], h[16];
-              tmem_ld_x32(td + c * 32, dp);
-              tmem_wait_ld_x32(dp);
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + 128 + c * 32 + j);
-                uint64_t u = add2(pack2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1])), l.x);
-                uint64_t v = add2(pack2(__uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3])), l.y);
-                if (!kBf16) {
-                  u = mul2(u, sc2);
-                  v = mul2(v, sc2);
-                }
-                float x[4];
-                unpack2(mul2(u, pack2(__uint_as_float(s[c * 32 + j]), __uint_as_float(s[c * 32 + j + 1]))),
-                        x[0], x[1]);
-                unpack2(mul2(v, pack2(__uint_as_float(s[c * 32 + j + 2]), __uint_as_float(s[c * 32 + j + 3]))),
-                        x[2], x[3]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) dp[j + k] = __float_as_uint(x[k]);
+            for (int j = 0; j < 32; j += 4) {
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + 128 + j);
+              uint64_t u = add2(pack2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1])), l.x);
+              uint64_t v = add2(pack2(__uint_as_float(dp[j + 2]), __uint_as_float(dp[j + 3])), l.y);
+              if (!kBf16) {
+                u = mul2(u, sc2);
+                v = mul2(v, sc2);
               }
-              if (select) {
+              float x[4];
+              unpack2(mul2(u, pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1]))), x[0], x[1]);
+              unpack2(mul2(v, pack2(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]))), x[2], x[3]);
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!((on[c] >> j) & 1u)) dp[j] = 0u;
-              }
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                h[j] = round2<T>(__uint_as_float(dp[2 * j]), __uint_as_float(dp[2 * j + 1]));
-              tmem_st_x16(td + c * 16, h);
+              for (int k = 0; k < 4; ++k) dp[j + k] = __float_as_uint(x[k]);
             }
+            if (select) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((on >> j) & 1u)) dp[j] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              h[j] = round2<T>(__uint_as_float(dp[2 * j]), __uint_as_float(dp[2 * j + 1]));
+            tmem_st_x16(td, h);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -1139,29 +1103,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // tells the others.)
         if (!ok && !kMask) break;
       }
-      if (kMask && !told) ok = barrier_all(1, 256, ok);
+      if (kMask && !told) ok = barrier_all(1, 32 * kSoftWarps, ok);
       if (!ok) break;
       ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
       ++items;
       if (!ok) break;
       tc_fence_after();
-      // Half 0 takes dv, half 1 dk.
+      // Parts 0 and 1 take dv, 2 and 3 dk: half of the columns each.
+      const int which = part >> 1;
       const bool whole = w.i0 == 0 && w.i1 == p.item_steps;
       const long long slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
-      const float f = half ? p.a.scale / bars.ds_scale : p.p_unscale;
+      const float f = which ? p.a.scale / bars.ds_scale : p.p_unscale;
       const int j = w.tile * kAttnRows + r;
-      T* dst = half ? static_cast<T*>(p.a.dk) + w.b * p.a.dks[0] + j * p.a.dks[1] + w.hk * p.a.dks[2]
+      T* dst = which ? static_cast<T*>(p.a.dk) + w.b * p.a.dks[0] + j * p.a.dks[1] + w.hk * p.a.dks[2]
                     : static_cast<T*>(p.a.dv) + w.b * p.a.dvs[0] + j * p.a.dvs[1] + w.hk * p.a.dvs[2];
 #pragma unroll
-      for (int c = 0; c < DP; c += 32) {
+      for (int i = 0; i < DP / 2; i += 32) {
+        const int c = (part & 1) * (DP / 2) + i;
         uint32_t v[32];
-        tmem_ld_x32((half ? t_dk : t_dv) + c + lane_field, v);
+        tmem_ld_x32((which ? t_dk : t_dv) + c + lane_field, v);
         tmem_wait_ld_x32(v);
         if (c < d) {
           if (whole) {
             if (j < p.a.kv_len) store_cols(dst + c, v, d - c, f);
           } else {
-            store_cols_f32(p.part_kv + ((slot * 2 + half) * kAttnRows + r) * 128 + c, v, d - c);
+            store_cols_f32(p.part_kv + ((slot * 2 + which) * kAttnRows + r) * 128 + c, v, d - c);
           }
         }
       }

@@ -16,14 +16,16 @@ namespace convgb300 {
 
 namespace {
 
-// One block packs 128 queries x 128 keys: a warp takes every eighth row, each
-// lane four bytes of it, a ballot makes a word.  All of a warp's 64 reads are
-// independent; bound by the mask's bytes.
-__global__ void __launch_bounds__(256)
+// One block packs 128 queries x 128 keys: a warp takes four rows, each lane
+// four bytes of one, a ballot makes a word.  Bound by the latency of one read
+// of the mask, for which all of a block's reads are in flight together.
+constexpr int kWarps = 32, kRows = kAttnRows / kWarps;
+
+__global__ void __launch_bounds__(32 * kWarps)
     mask_pack_kernel(const unsigned char* mask, long long sb, long long sh, long long sq,
                      long long sk, int heads, int queries, int keys, int words, int tiles,
                      uint32_t* bits, uint32_t* any) {
-  __shared__ uint4 seen[8];
+  __shared__ uint4 seen[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int across = words >> 2;
   const unsigned row = blockIdx.x / across;  // of `any`
@@ -36,34 +38,37 @@ __global__ void __launch_bounds__(256)
   const unsigned char* p = mask + b * sb + h * sh + i0 * sq + j0 * sk;
   grid_dependency_wait();
   grid_launch_dependents();
-  uint4 all = make_uint4(0, 0, 0, 0);
-#pragma unroll 4
-  for (int u = 0; u < 16; ++u) {
-    const int i = i0 + u * 8;
-    uint32_t w[4];
+  bool on[kRows][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool on = i < queries && j0 + k * 32 < keys && p[u * 8 * sq + k * 32 * sk] != 0;
-      w[k] = __ballot_sync(0xFFFFFFFFu, on);
-    }
+  for (int u = 0; u < kRows; ++u)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      on[u][k] = i0 + u * kWarps < queries && j0 + k * 32 < keys && p[u * kWarps * sq + k * 32 * sk] != 0;
+  uint4 all = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int i = i0 + u * kWarps;
+    uint4 w;
+    w.x = __ballot_sync(0xFFFFFFFFu, on[u][0]);
+    w.y = __ballot_sync(0xFFFFFFFFu, on[u][1]);
+    w.z = __ballot_sync(0xFFFFFFFFu, on[u][2]);
+    w.w = __ballot_sync(0xFFFFFFFFu, on[u][3]);
     if (lane == 0 && i < queries)
-      *reinterpret_cast<uint4*>(bits + (bh * queries + i) * words + col * 4) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    all.x |= w[0];
-    all.y |= w[1];
-    all.z |= w[2];
-    all.w |= w[3];
+      *reinterpret_cast<uint4*>(bits + (bh * queries + i) * words + col * 4) = w;
+    all.x |= w.x;
+    all.y |= w.y;
+    all.z |= w.z;
+    all.w |= w.w;
   }
   if (lane == 0) seen[warp] = all;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < 8; ++k) {
-      all.x |= seen[k].x;
-      all.y |= seen[k].y;
-      all.z |= seen[k].z;
-      all.w |= seen[k].w;
-    }
-    *reinterpret_cast<uint4*>(any + static_cast<long long>(row) * words + col * 4) = all;
+  if (warp == 0) {
+    all = seen[lane];
+    all.x = __reduce_or_sync(0xFFFFFFFFu, all.x);
+    all.y = __reduce_or_sync(0xFFFFFFFFu, all.y);
+    all.z = __reduce_or_sync(0xFFFFFFFFu, all.z);
+    all.w = __reduce_or_sync(0xFFFFFFFFu, all.w);
+    if (lane == 0) *reinterpret_cast<uint4*>(any + static_cast<long long>(row) * words + col * 4) = all;
   }
 }
 
@@ -76,7 +81,7 @@ cudaError_t launch_mask_pack(const unsigned char* mask, const long long stride[4
   const long long blocks = static_cast<long long>(batches) * heads * tiles * (words / 4);
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;  // 2^45 bytes of mask
-  return launch_pdl(mask_pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+  return launch_pdl(mask_pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps), 0,
                     stream, mask, stride[0], stride[1], stride[2], stride[3], heads, queries, keys,
                     words, tiles, bits, any);
 }

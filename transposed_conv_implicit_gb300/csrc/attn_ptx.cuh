@@ -153,7 +153,9 @@ __device__ __forceinline__ void mma_ss_x4(uint32_t d, uint32_t a_lo, uint32_t b_
 }
 
 // The same with A in TMEM (two K elements per 32-bit column, a step is 8
-// columns) and B's rows running along N (a step is 16 rows of 128 bytes).
+// columns; the third begins kThird columns on) and B's rows running along N (a
+// step is 16 rows of 128 bytes).
+template <int kThird = 16>
 __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
                                           uint32_t accumulate, int steps) {
   asm volatile(
@@ -167,12 +169,13 @@ __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a_tmem, uint32_t 
       "add.s32 a, %1, 8;\n\tadd.s64 b, b, 128;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t"
       "setp.gt.and.s32 q, %6, 2, e;\n\t"
-      "add.s32 a, %1, 16;\n\tadd.s64 b, b, 128;\n\t"
+      "add.s32 a, %1, %7;\n\tadd.s64 b, b, 128;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t"
       "setp.gt.and.s32 q, %6, 3, e;\n\t"
-      "add.s32 a, %1, 24;\n\tadd.s64 b, b, 128;\n\t"
+      "add.s32 a, %1, %8;\n\tadd.s64 b, b, 128;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t}" ::"r"(d),
-      "r"(a_tmem), "r"(b_lo), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(steps)
+      "r"(a_tmem), "r"(b_lo), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(steps), "n"(kThird),
+      "n"(kThird + 8)
       : "memory");
 }
 
