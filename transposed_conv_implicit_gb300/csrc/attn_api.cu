@@ -118,7 +118,9 @@ FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
   // pair's step covers two row tiles on a whole SM.
   const long long rounds = (f.items + sms - 1) / sms;
   const double pairs_cost = static_cast<double>(rounds) * nt;
-  const double split_cost = static_cast<double>(heads) * row_tiles * nt / (2.0 * sms) * 1.25;
+  // The join costs what 4 steps do (8 us; 2 x 1021 x 12 heads x 80 against 523,
+  // masked: 28 us as pairs, FWDSPLIT us split and joined).
+  const double split_cost = static_cast<double>(heads) * row_tiles * nt / (2.0 * sms) * 1.25 + (nt > 1 ? 4 : 0);
   f.split = split_cost < pairs_cost;
   const long long steps = heads * row_tiles * nt;
   f.grid = static_cast<int>(f.split ? std::min<long long>(steps, 2ll * sms)
@@ -132,6 +134,7 @@ FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
 struct BwdPlan {
   int q_tiles, item_steps, kv_tiles;
   int q_grid, kv_grid;     // CTAs of the dq and the dk, dv kernel
+  bool q_whole, kv_whole;  // no item is cut between CTAs
   bool norms;              // fp16: ds is scaled by the rows' norms
   bool brief;              // one tile of keys, narrow heads, no mask: one kernel
   size_t stat_bytes, norm_bytes, part_q_bytes, part_kv_bytes;
@@ -146,14 +149,23 @@ BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
   const long long nt = std::max(1, (a.kv_len + f.kv_box - 1) / f.kv_box);
   p.q_grid = static_cast<int>(std::min<long long>(heads * f.row_tiles * nt, sms));
   p.kv_grid = static_cast<int>(std::min<long long>(heads * p.kv_tiles * p.item_steps, sms));
+  // Even shares cut items and join them, which costs about what kJoinSteps
+  // steps do; whole items leave some CTAs idle at the end.
+  constexpr double kJoinSteps = 5;
+  const auto whole = [sms](long long items, long long steps) {
+    return static_cast<double>((items + sms - 1) / sms) * steps <=
+           static_cast<double>(items) * steps / sms + (steps > 1 ? kJoinSteps : 0);
+  };
+  p.q_whole = whole(heads * f.row_tiles, nt);
+  p.kv_whole = whole(heads * p.kv_tiles, p.item_steps) && !(f.one && a.q_len > 0);
   p.norms = a.dtype == CONV_DTYPE_F16;
   p.brief = f.one && a.q_len > 0;
   if (p.brief) p.kv_grid = static_cast<int>(std::min<long long>(heads * p.item_steps, sms));
   p.stat_bytes = static_cast<size_t>(a.batch) * a.heads * p.q_tiles * 256 * sizeof(float);
   p.norm_bytes = 2 * kAttnNormBlocks * sizeof(float);  // (of one size for both types)
   const size_t tile = static_cast<size_t>(kAttnRows) * 128 * sizeof(float);
-  p.part_q_bytes = nt > 1 ? 2 * tile * p.q_grid : 0;
-  p.part_kv_bytes = p.item_steps > 1 ? 4 * tile * p.kv_grid : 0;
+  p.part_q_bytes = nt > 1 && !p.q_whole ? 2 * tile * p.q_grid : 0;
+  p.part_kv_bytes = p.item_steps > 1 && !p.kv_whole ? 4 * tile * p.kv_grid : 0;
   return p;
 }
 
@@ -314,14 +326,21 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   if (queries && keys) {
     // Row statistics.
     p.div_heads = make_fast_div(static_cast<uint32_t>(s.heads));
-    p.div_tokens = make_fast_div(static_cast<uint32_t>(g.q_tiles * kAttnRows));
+    int width = 1;  // lanes of a row
+    while (width < s.head_dim / 8) width <<= 1;
+    p.row_slots = 32 / width;
+    const int group = kAttnRowUnroll * p.row_slots;
+    const int groups = g.q_tiles * kAttnRows / group, key_groups = (s.kv_len + group - 1) / group;
+    p.div_groups = make_fast_div(static_cast<uint32_t>(groups));
     p.div_kv_heads = make_fast_div(static_cast<uint32_t>(s.kv_heads));
-    p.div_keys = make_fast_div(static_cast<uint32_t>(s.kv_len));
-    const long long rows = static_cast<long long>(s.batch) * s.heads * g.q_tiles * kAttnRows;
-    p.row_blocks = static_cast<int>(std::min<long long>(kAttnNormBlocks, (rows + 63) / 64));
-    const long long values = static_cast<long long>(s.batch) * s.kv_heads * s.kv_len;
+    p.div_key_groups = make_fast_div(static_cast<uint32_t>(key_groups));
+    const long long units = static_cast<long long>(s.batch) * s.heads * groups;
+    p.row_blocks = static_cast<int>(std::min<long long>(kAttnNormBlocks, (units + 7) / 8));
+    const long long value_units = static_cast<long long>(s.batch) * s.kv_heads * key_groups;
     p.value_blocks =
-        g.norms ? static_cast<int>(std::min<long long>(kAttnNormBlocks, (values + 63) / 64)) : 0;
+        g.norms ? static_cast<int>(std::min<long long>(kAttnNormBlocks, (value_units + 7) / 8)) : 0;
+    p.q_whole = g.q_whole;
+    p.kv_whole = g.kv_whole;
     // (Short keys: delta is summed beside the scores; fp16 still wants the norms.)
     if ((!g.brief || g.norms) && launch_attn_rows(p, stream) != cudaSuccess) return CONV_ERR_CUDA;
     if (g.brief) {
@@ -378,8 +397,8 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   }
   // Tiles that were cut between CTAs, and keys without queries.
   const long long heads = static_cast<long long>(s.batch) * s.kv_heads;
-  const long long q_blocks = queries && s.kv_len > f.kv_box ? heads * f.row_tiles : 0;
-  const bool kv_join = g.item_steps != 1 || s.kv_lengths;
+  const long long q_blocks = queries && s.kv_len > f.kv_box && !g.q_whole ? heads * f.row_tiles : 0;
+  const bool kv_join = g.item_steps == 0 || (g.item_steps > 1 && !g.kv_whole) || s.kv_lengths;
   const long long kv_blocks = kv_join ? heads * g.kv_tiles : 0;
   return launch_attn_bwd_join(p, g.q_grid, g.kv_grid, q_blocks, kv_blocks, stream) == cudaSuccess
              ? CONV_OK

@@ -77,11 +77,13 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   __shared__ float most[8];
   const AttnShape& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // Power-of-two lanes per row, 16 bytes each.
+  // Power-of-two lanes per row, 16 bytes each; a warp takes kAttnRowUnroll x slots
+  // neighbouring tokens of one head (no more than 128), so that its statistics
+  // fill whole sectors.
   const int words = a.head_dim >> 3;
-  int width = 1;
-  while (width < words) width <<= 1;
-  const int at = lane & (width - 1), slot = lane / width, slots = 32 / width;
+  const int width = 32 / p.row_slots;
+  const int at = lane & (width - 1), slot = lane / width;
+  const int group = kAttnRowUnroll * p.row_slots;
   float norm = 0.f;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -89,63 +91,56 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   const int block = values ? blockIdx.x - p.row_blocks : blockIdx.x;
   const int blocks = values ? gridDim.x - p.row_blocks : p.row_blocks;
   const int heads = values ? a.kv_heads : a.heads;
-  const int length = values ? a.kv_len : p.q_tiles * kAttnRows;
+  const int groups = values ? (a.kv_len + group - 1) / group : p.q_tiles * kAttnRows / group;
   const FastDiv div_heads = values ? p.div_kv_heads : p.div_heads;
-  const FastDiv div_length = values ? p.div_keys : p.div_tokens;
-  const int rows = length * heads * a.batch;  // heads innermost, then tokens
-  constexpr int kUnroll = 4;                  // rows in flight per lane
-  const int step = blocks * 8 * slots;
-  for (int row0 = (block * 8 + warp) * slots; row0 < rows; row0 += kUnroll * step) {
-    uint4 x[kUnroll], y[kUnroll];
-    int h[kUnroll], b[kUnroll], t[kUnroll];
+  const FastDiv div_groups = values ? p.div_key_groups : p.div_groups;
+  const int units = groups * heads * a.batch;  // heads innermost, then tokens
+  for (int unit = block * 8 + warp; unit < units; unit += blocks * 8) {
+    const int bt = fast_div(unit, div_heads), h = unit - bt * heads;
+    const int b = fast_div(bt, div_groups), t0 = (bt - b * groups) * group + slot;
+    const int length = values ? valid_keys(a, b) : a.q_len;
+    const long long row0 = (static_cast<long long>(b) * a.heads + h) * a.q_len;
+    uint4 x[kAttnRowUnroll], y[kAttnRowUnroll];
+    float lse[kAttnRowUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      // (Counted unsigned: the rows past the end may pass 2^31.)
-      const unsigned row = static_cast<unsigned>(row0) + u * static_cast<unsigned>(step) + slot;
-      const bool in = row < static_cast<unsigned>(rows);
-      const int bt = fast_div(in ? static_cast<int>(row) : 0, div_heads);
-      h[u] = (in ? static_cast<int>(row) : 0) - bt * heads;
-      b[u] = fast_div(bt, div_length);
-      t[u] = in ? bt - b[u] * length : -1;
+    for (int u = 0; u < kAttnRowUnroll; ++u) {
+      const int t = t0 + u * p.row_slots;
       x[u] = y[u] = make_uint4(0, 0, 0, 0);
-      if (t[u] < 0 || at >= words) continue;
+      lse[u] = -INFINITY;
+      if (t >= length || at >= words) continue;
       if (values) {
-        if (t[u] < valid_keys(a, b[u]))
-          x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + b[u] * a.vs[0] +
-                                                 t[u] * a.vs[1] + h[u] * a.vs[2] + at * 8);
-      } else if (t[u] < a.q_len) {
-        x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + b[u] * a.dos[0] +
-                                               t[u] * a.dos[1] + h[u] * a.dos[2] + at * 8);
-        y[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + b[u] * a.os[0] +
-                                               t[u] * a.os[1] + h[u] * a.os[2] + at * 8);
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + b * a.vs[0] + t * a.vs[1] +
+                                               h * a.vs[2] + at * 8);
+      } else {
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + b * a.dos[0] +
+                                               t * a.dos[1] + h * a.dos[2] + at * 8);
+        y[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + b * a.os[0] + t * a.os[1] +
+                                               h * a.os[2] + at * 8);
+        if (at == 0) lse[u] = a.lse[row0 + t];
       }
     }
-    float dot[kUnroll], sq[kUnroll];
+    float dot[kAttnRowUnroll], sq[kAttnRowUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < kAttnRowUnroll; ++u) {
       dot[u] = dot8<T>(x[u], y[u]);
       sq[u] = p.norms ? dot8<T>(x[u], x[u]) : 0.f;
     }
     for (int o = width >> 1; o; o >>= 1)
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < kAttnRowUnroll; ++u) {
         dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], o);
         if (p.norms) sq[u] += __shfl_xor_sync(0xFFFFFFFFu, sq[u], o);
       }
     if (at != 0) continue;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (t[u] < 0) continue;
+    for (int u = 0; u < kAttnRowUnroll; ++u) {
+      const int t = t0 + u * p.row_slots;
       if (!values) {
-        float lse2 = -INFINITY;
-        if (t[u] < a.q_len) {
-          const float lse = a.lse[(static_cast<long long>(b[u]) * a.heads + h[u]) * a.q_len + t[u]];
-          if (lse != -INFINITY) lse2 = p.p_shift - lse * kLog2e;
-        }
+        const float lse2 = lse[u] == -INFINITY ? lse[u] : p.p_shift - lse[u] * kLog2e;
         if (lse2 == -INFINITY) dot[u] = sq[u] = 0.f;
-        const long long tile = (static_cast<long long>(b[u]) * a.heads + h[u]) * p.q_tiles + (t[u] >> 7);
-        p.stats[tile * 256 + (t[u] & 127)] = lse2;
-        p.stats[tile * 256 + 128 + (t[u] & 127)] = -dot[u];
+        float* st = p.stats + ((static_cast<long long>(b) * a.heads + h) * p.q_tiles + (t >> 7)) * 256;
+        st[t & 127] = lse2;
+        st[128 + (t & 127)] = -dot[u];
       }
       if (sq[u] < INFINITY) norm = fmaxf(norm, sq[u]);  // (NaN compares false)
     }
@@ -626,11 +621,18 @@ struct KeyWalk {
     const int tiles = (n + kAttnRows - 1) / kAttnRows;
     hk = static_cast<int>(item / tiles);
     tile = static_cast<int>(item - static_cast<long long>(hk) * tiles);
-    take(static_cast<int>(st.rest - item * p.item_steps));
+    const int from = static_cast<int>(st.rest - item * p.item_steps);
+    if (p.kv_whole && from > 0) {  // an item that began in another share
+      left -= p.item_steps - from;
+      next();
+    } else {
+      take(from);
+    }
   }
   __device__ void take(int from) {
     i0 = from;
-    i1 = static_cast<int>(min(static_cast<long long>(p.item_steps), from + left));
+    i1 = p.kv_whole ? p.item_steps
+                    : static_cast<int>(min(static_cast<long long>(p.item_steps), from + left));
     left -= i1 - i0;
     const int h = from / p.q_tiles;
     qt = from - h * p.q_tiles;
@@ -1220,6 +1222,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int rows = min(kAttnRows, a.kv_len - tile * kAttnRows);
   int shares = 0;
   if (tile < tiles) {
+    if (p.kv_whole) return;
     split_prefix(a.batch, key_steps_uniform(p), b, join.sums, [&](int i) { return key_steps(p, i); },
                  &before, &total);
     list_slots(join, total, kv_ctas, before + (static_cast<long long>(hk) * tiles + tile) * p.item_steps,

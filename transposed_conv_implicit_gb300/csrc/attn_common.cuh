@@ -150,6 +150,11 @@ __device__ SplitStart split_rows(const P& p, int lane) {
   return split_start(p.a.batch, row_steps_uniform(p), lane, [&](int b) { return row_steps(p, b); });
 }
 
+// Whether a split launch cuts no item: a CTA then takes the items that begin in
+// its share.
+__device__ __forceinline__ bool whole_items(const AttnFwdParams&) { return false; }
+__device__ __forceinline__ bool whole_items(const AttnBwdParams& p) { return p.q_whole; }
+
 // Walks a CTA's work: every role walks the same sequence.
 template <bool kSplit, bool kMask, typename P>
 struct Walk {
@@ -171,7 +176,12 @@ struct Walk {
       if (live) {
         const int per = key_tiles(valid_keys(p.a, b), p.kv_box);
         const int item = static_cast<int>(st.rest / per);
-        set_split(item, static_cast<int>(st.rest - static_cast<long long>(item) * per));
+        const int tile = static_cast<int>(st.rest - static_cast<long long>(item) * per);
+        set_split(item, tile);
+        if (whole_items(p) && tile > 0) {  // an item that began in another share
+          pos = st.left - (per - tile);
+          next();
+        }
       }
     } else {
       pos = blockIdx.x;
@@ -185,7 +195,7 @@ struct Walk {
     row_tile = item - hk * p.row_tiles;
     tiles_here = 1;
     t0 = tile;
-    t1 = static_cast<int>(min(static_cast<long long>(nt), tile + pos));
+    t1 = whole_items(p) ? nt : static_cast<int>(min(static_cast<long long>(nt), tile + pos));
     pos -= t1 - t0;
   }
   __device__ void set_pair() {

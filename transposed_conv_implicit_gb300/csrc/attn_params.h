@@ -76,6 +76,7 @@ cudaError_t launch_attn_fwd(const AttnFwdParams& p, bool split, int grid, size_t
 
 // Backward launches (attn_bwd.cu).  The dq kernel's row tiles are as the
 // forward pass's; the dk, dv kernel takes tiles of 128 tokens of one head.
+constexpr int kAttnRowUnroll = 4;     // rows in flight per lane of the rows kernel
 constexpr int kAttnNormBlocks = 2048;  // most blocks of each part of the rows kernel
 
 struct AttnBwdParams {  // aligned like CUtensorMap
@@ -86,7 +87,7 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   int q_mul[2], do_mul[2], k_mul[2], v_mul[2];
   int tile_heads, tile_tokens, token_tiles, row_tiles;
   FastDiv div_token_tiles;
-  FastDiv div_heads, div_tokens, div_kv_heads, div_keys;  // (tokens: padded to whole tiles)
+  FastDiv div_heads, div_groups, div_kv_heads, div_key_groups;  // (groups of the rows kernel)
   int kv_box;           // keys per tile (multiple of 16, <= 128)
   int q_box;            // dk, dv: tokens per box
   int q_tiles;          // tiles of 128 tokens
@@ -101,6 +102,8 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   float* stats;         // [batch][heads][q_tiles][2][128]
   float* norms;         // fp16: row norms' maxima by block, else null
   int row_blocks, value_blocks;  // blocks of the rows kernel
+  int row_slots;                 // its rows side by side in a warp
+  bool q_whole, kv_whole;        // no item of the dq, of the dk, dv kernel is cut
   float* part_q;        // [2 * CTAs][128][128]
   float* part_kv;       // [2 * CTAs][2][128][128]
   unsigned int* status;
