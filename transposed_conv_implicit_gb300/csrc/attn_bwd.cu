@@ -166,7 +166,7 @@ struct Bars {
   uint64_t ds_full[2];
   uint64_t drain;
   SplitStart start;
-  float ds_scale;
+  float most[2][32];  // the norms that ds's scale is made from
   uint32_t tmem;
   int abort_flag;
 };
@@ -176,16 +176,6 @@ static_assert(sizeof(Bars) <= 1024, "shared-memory plan of the dk, dv kernel");
 constexpr int kSoftWarps = 16;  // a quarter of the lanes and of the columns each
 constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
 constexpr int kBwdThreads = 32 * (kSoftWarps + 2);
-
-__device__ __forceinline__ void clear_rows(uint8_t* tile, uint32_t block_bytes, int blocks, int r0,
-                                           int limit, uint32_t keep, int lane) {
-  const int r = r0 + lane;
-  if (r < limit && !((keep >> lane) & 1u)) {
-    uint4* q = reinterpret_cast<uint4*>(tile) + r * 8;
-    for (int c = 0; c < blocks; ++c)
-      for (int i = 0; i < 8; ++i) q[c * (block_bytes >> 4) + i] = make_uint4(0, 0, 0, 0);
-  }
-}
 
 // ------------------------------------------------------------------ dq
 template <typename T, int DP, bool kMask>
@@ -240,12 +230,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   grid_launch_dependents();
   if (warp == 0) {
     const SplitStart st = split_rows(p, lane);
-    const float f = ds_scale(p, lane);
-    if (lane == 0) {
-      bars.start = st;
-      bars.ds_scale = f;
-    }
+    if (lane == 0) bars.start = st;
   }
+  gather_norms(p, bars.most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -379,7 +366,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     while (ok && live) {
       const bool last = after >= w.t1;
       const int keys = w.tile_keys(t), this_cols = cols, this_k = k_stage;
-        uint4 any = make_uint4(0, 0, 0, 0);
+      uint4 any = make_uint4(0, 0, 0, 0);
       if (kMask) any = w.any_keys(t);
       bool more = true;
       if (last) {
@@ -423,14 +410,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // Keys that no row takes part with are cleared: nothing they hold meets
       // a zero of ds.
       if (kMask || (keys < this_cols && p.a.kv_lengths)) {
-        const uint32_t word[4] = {any.x, any.y, any.z, any.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r0 = k * 32;
-          uint32_t used = keys - r0 >= 32 ? 0xFFFFFFFFu : keys > r0 ? (1u << (keys - r0)) - 1u : 0u;
-          if (kMask) used &= word[k];
-          clear_rows(smem + p.off_x + this_k * kv_tile, kv_block, kBlocks, r0, this_cols, used, lane);
-        }
+        uint4 used = first_keys(keys);
+        if (kMask) used = make_uint4(used.x & any.x, used.y & any.y, used.z & any.z, used.w & any.w);
+        clear_rows<kBlocks>(smem + p.off_x + this_k * kv_tile, kv_block, this_cols, used, lane);
         fence_proxy_async_shared();
         __syncwarp();
       }
@@ -469,7 +451,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int part = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     // (p is held times 2^p_shift here too; ds's scale takes it out.)
-    const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
+    const float scale_ds = ds_scale(p, bars.most, lane);
+    const float c2 = p.scale_log2, sc = scale_ds * p.p_unscale;
     const int d = p.a.head_dim;
     const int row_token = p.tile_heads > 1 ? r / p.tile_heads : r;
     const int row_head = p.tile_heads > 1 ? r - row_token * p.tile_heads : 0;
@@ -559,7 +542,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after();
       const bool whole = w.t0 == 0 && w.t1 == w.nt;
       const long long slot = 2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-      const float f = p.a.scale / bars.ds_scale;
+      const float f = p.a.scale / scale_ds;
       const int col = part * 32;
       if (col < DP) {
         uint32_t v[32];
@@ -753,12 +736,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (warp == 0) {
     const SplitStart st = split_start(p.a.batch, key_steps_uniform(p), lane,
                                       [&](int b) { return key_steps(p, b); });
-    const float f = ds_scale(p, lane);
-    if (lane == 0) {
-      bars.start = st;
-      bars.ds_scale = f;
-    }
+    if (lane == 0) bars.start = st;
   }
+  gather_norms(p, bars.most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -883,10 +863,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // Queries without keys are cleared: nothing they hold meets a zero of p or ds.
     auto clear = [&](uint8_t* tile, int stat_stage) {
       const float* st = reinterpret_cast<const float*>(smem + p.off_stat + stat_stage * 1024);
-      for (int r0 = 0; r0 < kAttnRows; r0 += 32) {
-        const uint32_t used = __ballot_sync(0xFFFFFFFFu, st[r0 + lane] != -INFINITY);
-        clear_rows(tile, 16384, kBlocks, r0, kAttnRows, used, lane);
-      }
+      uint4 used;
+      used.x = __ballot_sync(0xFFFFFFFFu, st[lane] != -INFINITY);
+      used.y = __ballot_sync(0xFFFFFFFFu, st[32 + lane] != -INFINITY);
+      used.z = __ballot_sync(0xFFFFFFFFu, st[64 + lane] != -INFINITY);
+      used.w = __ballot_sync(0xFFFFFFFFu, st[96 + lane] != -INFINITY);
+      clear_rows<kBlocks>(tile, 16384, kAttnRows, used, lane);
       fence_proxy_async_shared();
       __syncwarp();
     };
@@ -990,7 +972,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // One thread per key and 32 of the queries.
     const int part = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
+    const float scale_ds = ds_scale(p, bars.most, lane);
+    const float c2 = p.scale_log2, sc = scale_ds * p.p_unscale;
     const uint64_t c22 = pack2(c2, c2), sc2 = pack2(sc, sc);
     const int d = p.a.head_dim;
     const uint32_t ts = t_s + part * 32 + lane_field, td = t_dp + part * 32 + lane_field;
@@ -1115,7 +1098,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int which = part >> 1;
       const bool whole = w.i0 == 0 && w.i1 == p.item_steps;
       const long long slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
-      const float f = which ? p.a.scale / bars.ds_scale : p.p_unscale;
+      const float f = which ? p.a.scale / scale_ds : p.p_unscale;
       const int j = w.tile * kAttnRows + r;
       T* dst = which ? static_cast<T*>(p.a.dk) + w.b * p.a.dks[0] + j * p.a.dks[1] + w.hk * p.a.dks[2]
                     : static_cast<T*>(p.a.dv) + w.b * p.a.dvs[0] + j * p.a.dvs[1] + w.hk * p.a.dvs[2];
@@ -1156,16 +1139,13 @@ __global__ void __launch_bounds__(kJoinThreads)
     attn_bwd_join_kernel(const __grid_constant__ AttnBwdParams p, int q_ctas, int kv_ctas,
                          long long q_blocks) {
   __shared__ JoinSlots join;
-  __shared__ float factor;
+  __shared__ float most[2][32];
   const AttnShape& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = lane * 4;
   const int r0 = blockIdx.y * kJoinRows + warp * kJoinUnroll;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (warp == 0) {
-    const float f = ds_scale(p, lane);
-    if (lane == 0) factor = a.scale / f;
-  }
+  gather_norms(p, most);
   long long before, total;
   if (blockIdx.x < q_blocks) {
     const int b = static_cast<int>(blockIdx.x / p.item_rows);
@@ -1188,6 +1168,7 @@ __global__ void __launch_bounds__(kJoinThreads)
       head0 = hk * a.group + hg;
       rows = min(kAttnRows, a.q_len - token0);
     }
+    const float factor = a.scale / ds_scale(p, most, lane);
     if (r0 >= rows || d0 >= a.head_dim) return;
     float4 acc[kJoinUnroll];
 #pragma unroll
@@ -1230,8 +1211,9 @@ __global__ void __launch_bounds__(kJoinThreads)
     shares = join.count;
     if (shares == 0) return;
   } else {
-    __syncthreads();  // (factor)
+    __syncthreads();  // (the norms)
   }
+  const float factor = a.scale / ds_scale(p, most, lane);
   if (r0 >= rows || d0 >= a.head_dim) return;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {

@@ -300,16 +300,30 @@ struct Walk {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// The power of two that ds is scaled by: |ds| 2^k <= 2^15.  One warp.
-__device__ __forceinline__ float ds_scale(const AttnBwdParams& p, int lane) {
-  if (!p.norms) return 1.f;
+// The largest norms of the rows kernel's blocks: a block of whole warps gathers
+// its warps' shares in `most`, which ds_scale joins after a barrier.
+__device__ __forceinline__ void gather_norms(const AttnBwdParams& p, float (*most)[32]) {
+  if (!p.norms) return;
   float x = 0.f, y = 0.f;
-  for (int i = lane; i < p.row_blocks; i += 32) x = fmaxf(x, p.norms[i]);
-  for (int i = lane; i < p.value_blocks; i += 32) y = fmaxf(y, p.norms[kAttnNormBlocks + i]);
-  for (int o = 16; o; o >>= 1) {
-    x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
-    y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, o));
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.row_blocks; i += blockDim.x) x = fmaxf(x, p.norms[i]);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < p.value_blocks; i += blockDim.x) y = fmaxf(y, p.norms[kAttnNormBlocks + i]);
+  // (Squares: as bits they are in order.)
+  x = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
+  y = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y)));
+  if ((threadIdx.x & 31) == 0) {
+    most[0][threadIdx.x >> 5] = x;
+    most[1][threadIdx.x >> 5] = y;
   }
+}
+
+// The power of two that ds is scaled by: |ds| 2^k <= 2^15.  One warp.
+__device__ __forceinline__ float ds_scale(const AttnBwdParams& p, const float (*most)[32], int lane) {
+  if (!p.norms) return 1.f;
+  const bool in = lane < static_cast<int>(blockDim.x >> 5);
+  const float x = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, in ? __float_as_uint(most[0][lane]) : 0u));
+  const float y = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, in ? __float_as_uint(most[1][lane]) : 0u));
   // 2 |do| |v| < 2^(1 + ceil exponents); both norms in fp16's range, so k is
   // within +-60.
   const float bound = 2.f * sqrtf(x) * sqrtf(y);
@@ -317,6 +331,36 @@ __device__ __forceinline__ float ds_scale(const AttnBwdParams& p, int lane) {
   int e;
   frexpf(bound, &e);  // bound < 2^e
   return ldexpf(1.f, max(-60, min(60, 14 - e)));
+}
+
+// Clears the rows of a tile (kBlocks blocks of 128-byte rows) below `limit`
+// whose bit of `keep` is not set.  One warp, four rows a store: a lane per row
+// took ten times as long, its stores meeting in the same banks.
+template <int kBlocks>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, uint32_t block_bytes, int limit, uint4 keep,
+                                           int lane) {
+  const uint32_t words[4] = {keep.x, keep.y, keep.z, keep.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (words[i] == 0xFFFFFFFFu) continue;
+    for (int r0 = lane >> 3; r0 < 32; r0 += 4) {
+      const int r = i * 32 + r0;
+      if (r < limit && !((words[i] >> r0) & 1u))
+#pragma unroll
+        for (int c = 0; c < kBlocks; ++c)
+          *reinterpret_cast<uint4*>(tile + c * block_bytes + r * 128 + (lane & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// The first n of 128 keys.
+__device__ __forceinline__ uint4 first_keys(int n) {
+  const auto word = [n](int i) {
+    const int rest = n - i * 32;
+    return rest >= 32 ? 0xFFFFFFFFu : rest <= 0 ? 0u : (1u << rest) - 1u;
+  };
+  return make_uint4(word(0), word(1), word(2), word(3));
 }
 
 // Writes 32 fp32 columns of a row, scaled: rounded to T.

@@ -303,20 +303,12 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       // (past the tensor's end the load has filled zeros), and masked keys.
       // (Each group's warp clears them; both write the same zeros.)
       if (kMask || (keys < this_cols && p.a.kv_lengths)) {
-        uint4 any = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
-        if (kMask) any = w.any_keys(t);
-        const uint32_t word[4] = {any.x, any.y, any.z, any.w};
-        uint4* row0 = reinterpret_cast<uint4*>(smem + p.off_kv + v_stage * kv_tile);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = i * 32 + lane;
-          if (r < this_cols && (r >= keys || !((word[i] >> lane) & 1u)))
-#pragma unroll
-            for (int c = 0; c < L::kBlocks; ++c)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                row0[c * (kv_block >> 4) + r * 8 + j] = make_uint4(0, 0, 0, 0);
+        uint4 used = first_keys(keys);
+        if (kMask) {
+          const uint4 any = w.any_keys(t);
+          used = make_uint4(used.x & any.x, used.y & any.y, used.z & any.z, used.w & any.w);
         }
+        clear_rows<L::kBlocks>(smem + p.off_kv + v_stage * kv_tile, kv_block, this_cols, used, lane);
         fence_proxy_async_shared();
         __syncwarp();
       }

@@ -388,7 +388,7 @@ struct ShortBars {
   uint64_t s_full[2], buf_free[2], dq_full[2];  // by TMEM buffer
   uint64_t pds_full, pds_empty, acc_done, acc_free, drain[2];
   float exchange[2][2][128];  // by step parity: a half row's share of delta
-  float ds_scale;
+  float most[2][32];  // the norms that ds's scale is made from
   uint32_t tmem;
   int abort_flag;
 };
@@ -489,10 +489,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (warp == 0) {
-    const float f = ds_scale(p, lane);
-    if (lane == 0) bars.ds_scale = f;
-  }
+  gather_norms(p, bars.most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -650,7 +647,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     // ------------------------------------------------------------ dq out
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    const float f = p.a.scale / bars.ds_scale;
+    const float f = p.a.scale / ds_scale(p, bars.most, lane);
     const bool leader = warp == kShortEpi && lane == 0;
     bool ok = true;
     uint32_t count = 0;
@@ -698,7 +695,8 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     // Two warps share a quarter of the rows: 16-key chunks [0, mid) and [mid, all).
     const int half = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    const float c2 = p.scale_log2, sc = bars.ds_scale * p.p_unscale;
+    const float scale_ds = ds_scale(p, bars.most, lane);
+    const float c2 = p.scale_log2, sc = scale_ds * p.p_unscale;
     const uint64_t c22 = pack2(c2, c2), sc2 = pack2(sc, sc);
     const int d = p.a.head_dim;
     uint32_t count = 0, items = 0;
@@ -821,7 +819,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
       // Half 0 takes dv, half 1 dk.
       const bool whole = w.i0 == 0 && w.i1 == p.item_steps;
       const long long slot = 2ll * blockIdx.x + (w.i0 == 0 ? 1 : 0);
-      const float f = half ? p.a.scale / bars.ds_scale : p.p_unscale;
+      const float f = half ? p.a.scale / scale_ds : p.p_unscale;
       T* dst = half ? static_cast<T*>(p.a.dk) + w.b * p.a.dks[0] + r * p.a.dks[1] + w.hk * p.a.dks[2]
                     : static_cast<T*>(p.a.dv) + w.b * p.a.dvs[0] + r * p.a.dvs[1] + w.hk * p.a.dvs[2];
 #pragma unroll
