@@ -23,7 +23,8 @@ extern "C" {
  *   mode 1: CTA 0's producer skips the arrive of its first k-block, so the
  *           MMA warp's wait on it can only end by running out of time (for
  *           CTA pairs: both CTAs of the first pair leave their first stage
- *           un-armed and unloaded);
+ *           un-armed and unloaded; cross attention: every CTA with work
+ *           leaves its first keys un-armed);
  *   mode 2: stream-K launches never publish their partial tiles, so the CTAs
  *           that finish split tiles wait for them until the limit runs out.
  * timeout_ns sets the per-wait limit of subsequent launches (0 = default,

@@ -243,6 +243,8 @@ def _norm_head(q, k, cos, sin, eps, adjacent_pairs):
             raise _invalid("cos and sin come together")
         rows, half, cp, sp = 0, 0, 0, 0
     else:
+        if cos.dim() != 2:
+            raise _invalid("cos must be [rows, rot_dim / 2]")
         rows, half = cos.shape
         cp = _dense(cos, "cos", (rows, half), torch.float32, device)
         sp = _dense(sin, "sin", (rows, half), torch.float32, device)

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int t = w.first(); ok && t < w.t1; t = w.after(t)) {
         ok = wait(&bars.x_empty[xs], xph ^ 1u, kAttnProducerTimeout);
         if (!ok) break;
-        if (!(p.fault_mode == 1 && blockIdx.x == 0 && nx == 0)) {
+        if (!(p.fault_mode == 1 && nx == 0)) {
           mbar_arrive_expect_tx_if(lead, smem_u32(&bars.x_full[xs]), kv_tile);
           for (int c = 0; c < kBlocks; ++c)
             tma_load_4d_if(lead, smem_u32(smem + p.off_x) + xs * kv_tile + c * kv_block, &p.map_k,
@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         ok = wait(&bars.x_empty[xs], xph ^ 1u, kAttnProducerTimeout);
         if (!ok) break;
         uint32_t bar = smem_u32(&bars.x_full[xs]);
-        if (!(p.fault_mode == 1 && blockIdx.x == 0 && nx == 0)) {
+        if (!(p.fault_mode == 1 && nx == 0)) {
           mbar_arrive_expect_tx_if(lead, bar, q_bytes);
           for (int c = 0; c < kBlocks; ++c)
             tma_load_4d_if(lead, smem_u32(smem + p.off_x) + xs * kTile + c * 16384u, &p.map_q, bar,

@@ -183,8 +183,8 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
           const uint32_t bar = smem_u32(&bars.kv_full[stage]);
           const CUtensorMap* map = kv ? &p.map_v : &p.map_k;
           const int* mul = kv ? p.v_mul : p.k_mul;
-          // (fault_mode 1, a test hook: CTA 0 leaves its first key tile un-armed.)
-          if (!(p.fault_mode == 1 && blockIdx.x == 0 && issued == 0)) {
+          // (fault_mode 1, a test hook: every CTA leaves its first key tile un-armed.)
+          if (!(p.fault_mode == 1 && issued == 0)) {
             mbar_arrive_expect_tx_if(lead, bar, kv_tile);
 #pragma unroll
             for (int c = 0; c < L::kBlocks; ++c)

@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kOneThreads, kCtas)
       if (fresh) {
         ok = wait(&bars.kv_empty, (runs & 1u) ^ 1u, kAttnProducerTimeout);
         if (!ok) break;
-        // (fault_mode 1, a test hook: CTA 0 leaves its first keys un-armed.)
-        if (!(p.fault_mode == 1 && blockIdx.x == 0 && runs == 0)) {
+        // (fault_mode 1, a test hook: every CTA leaves its first keys un-armed.)
+        if (!(p.fault_mode == 1 && runs == 0)) {
           const uint32_t bar = smem_u32(&bars.kv_full);
           mbar_arrive_expect_tx_if(lead, bar, 2 * kv_tile);
           tma_load_4d_if(lead, smem_u32(smem + p.off_kv), &p.map_k, bar, 0, w.hk * p.k_mul[0], 0,
@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     for (ShortWalk w(p); ok && w.live; w.next()) {
       ok = wait(&bars.kv_empty, (items & 1u) ^ 1u, kAttnProducerTimeout);
       if (!ok) break;
-      // (fault_mode 1, a test hook: CTA 0 leaves its first keys un-armed.)
-      if (!(p.fault_mode == 1 && blockIdx.x == 0 && items == 0)) {
+      // (fault_mode 1, a test hook: every CTA leaves its first keys un-armed.)
+      if (!(p.fault_mode == 1 && items == 0)) {
         const uint32_t bar = smem_u32(&bars.kv_full);
         mbar_arrive_expect_tx_if(lead, bar, 2 * kv_tile);
         tma_load_4d_if(lead, smem_u32(kv), &p.map_k, bar, 0, w.hk * p.k_mul[0], 0, w.b * p.k_mul[1]);

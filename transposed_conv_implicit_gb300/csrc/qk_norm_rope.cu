@@ -882,12 +882,12 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
     if (misaligned(a.cos) || misaligned(a.sin)) return CONV_ERR_MISALIGNED;
   }
   // Halves that split a 16-byte word (rot_dim an odd multiple of 8) take
-  // 8-byte words, so that a pair's members sit in whole words.
+  // 8-byte words, so that a pair's members sit in whole words (32 lanes at the
+  // most, for 256 elements).
   const int v = !a.adjacent_pairs && a.rot_dim % 16 != 0 ? 4 : 8;
   const int rot_lanes = (a.rot_dim + 2 * v - 1) / (2 * v);
   const int lanes = a.adjacent_pairs ? (a.head_dim + 15) / 16
                                      : rot_lanes + (a.head_dim - a.rot_dim + 2 * v - 1) / (2 * v);
-  if (lanes > 32) return CONV_ERR_NOT_SUPPORTED;
   QnParams p{};
   conv_status_t st = take_tensor(a, a.q, backward, &p.t[0]);
   if (st == CONV_OK) st = take_tensor(a, a.k, backward, &p.t[1]);
