@@ -160,11 +160,12 @@ struct Bars {
   uint64_t x_full[kMaxRing], x_empty[kMaxRing];   // k ring; q ring
   uint64_t y_full[kMaxRing], y_empty[kMaxRing];   // v ring; do ring
   uint64_t st_full[2], st_empty[2];               // dk, dv: the queries' statistics
-  uint64_t s_full[2], dp_full, dp_free, p_full, acc_done, acc_free;
-  // dq: by step parity.  The step after next cannot arrive before the
-  // products have waited for this one, so no wait sees a phase go by.
-  uint64_t ds_full[2];
-  uint64_t drain;
+  uint64_t s_full, p_full, acc_done, acc_free;
+  uint64_t s_free;                                // dq: the scores have been read
+  // dq: by step parity.  The step after next cannot arrive before everyone has
+  // waited for this one, so no wait sees a phase go by.
+  uint64_t dp_full[2], ds_full[2];
+  uint64_t drain[2];
   SplitStart start;
   float most[2][32];  // the norms that ds's scale is made from
   uint32_t tmem;
@@ -174,12 +175,15 @@ struct Bars {
 static_assert(sizeof(Bars) <= 1024, "shared-memory plan of the dk, dv kernel");
 
 constexpr int kSoftWarps = 16;  // a quarter of the lanes and of the columns each
-constexpr int kMmaWarp = kSoftWarps, kLoadWarp = kSoftWarps + 1;
-constexpr int kBwdThreads = 32 * (kSoftWarps + 2);
+constexpr int kMmaWarp = kSoftWarps;
+// dq: two warps issue products, so that one's waits pass beside the other's.
+constexpr int kGradWarp = kSoftWarps + 1, kLoadWarp = kSoftWarps + 2, kDqThreads = 32 * (kSoftWarps + 3);
+// dk, dv: one does.
+constexpr int kKeyLoadWarp = kSoftWarps + 1, kDkvThreads = 32 * (kSoftWarps + 2);
 
 // ------------------------------------------------------------------ dq
 template <typename T, int DP, bool kMask>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kDqThreads, 1)
     attn_dq_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kBlocks = DP / 64;
@@ -197,9 +201,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.a_full[i]), 1);
       mbar_init(smem_u32(&bars.a_empty[i]), 1);
-      mbar_init(smem_u32(&bars.s_full[i]), 1);
+      mbar_init(smem_u32(&bars.dp_full[i]), 1);
       mbar_init(smem_u32(&bars.ds_full[i]), kSoftWarps);
     }
+    mbar_init(smem_u32(&bars.s_full), 1);
+    mbar_init(smem_u32(&bars.s_free), kSoftWarps);
     for (int i = 0; i < p.x_stages; ++i) {
       mbar_init(smem_u32(&bars.x_full[i]), 1);
       mbar_init(smem_u32(&bars.x_empty[i]), 1);
@@ -208,11 +214,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(smem_u32(&bars.y_full[i]), 1);
       mbar_init(smem_u32(&bars.y_empty[i]), 1);
     }
-    mbar_init(smem_u32(&bars.dp_full), 1);
-    mbar_init(smem_u32(&bars.dp_free), kSoftWarps);
     mbar_init(smem_u32(&bars.acc_done), 1);
     mbar_init(smem_u32(&bars.acc_free), kSoftWarps);
-    mbar_init(smem_u32(&bars.drain), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&bars.drain[i]), 1);
     bars.abort_flag = 0;
     fence_barrier_init();
   }
@@ -238,12 +242,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
   const SplitStart start = bars.start;
-  // TMEM columns: S (two buffers; ds over them), dp, dq.
-  const uint32_t t_dp = tmem + 256, t_acc = tmem + 384;
+  // TMEM columns: S, dp (two buffers; ds over them), dq.
+  const uint32_t t_dp = tmem + 128, t_acc = tmem + 384;
 
   auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int code) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag, status,
                                                      code, limit));
+  };
+  auto wait_set = [&](const WaitSet& s) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(s.bar, s.parity, abort_flag, status,
+                                                     kAttnMmaTimeout, limit));
   };
 
   if (warp == kLoadWarp) {
@@ -315,8 +323,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                           limit / 8 + 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kLoadWarp && warp >= kMmaWarp) {
     // ------------------------------------------------------------ products
+    // One warp issues S and dp, the other dq.
+    const bool grads = warp == kGradWarp;
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
     const uint32_t idesc_acc = attn_idesc(kBf16, k_steps * 16, false, true);
@@ -325,124 +335,90 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                    y_lo = smem_u32(smem + p.off_y) >> 4;
     const uint32_t tile_lo = kv_tile >> 4, block_lo = kv_block >> 4;
     bool ok = true;
-    int xs = 0, ys = 0;
-    uint32_t xph = 0, yph = 0, aph = 0, count = 0, items = 0;
+    int xs = 0, ys = 0, xs_before[2] = {0, 0};  // stages; k's one and two steps before
+    uint32_t xph = 0, yph = 0, xph_before[2] = {0, 0}, count = 0, items = 0;
     // A (128 rows) times a key/value tile, over the head dimension.
     auto rows_by_keys = [&](uint32_t d, uint32_t a, uint32_t b, int cols) {
       const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
       mma_ss_x4(d, kLeadK | a, kLeadK | b, id, 0u, k_steps);
       if (k_steps > 4) mma_ss_x4(d, kLeadK | (a + 1024u), kLeadK | (b + block_lo), id, 1u, k_steps - 4);
     };
-    Walk<true, kMask, AttnBwdParams> w(p, start);
-    bool live = w.live, first = true;
-    int t = live ? w.first() : 0, after = 0, cols = 0, k_stage = 0;
-    if (live) {
-      after = w.after(t);
-      cols = w.tile_cols(t);
-      ok = wait(&bars.a_full[0], 0, kAttnMmaTimeout) && wait(&bars.x_full[0], 0, kAttnMmaTimeout);
-      if (ok) {
-        tc_fence_after();
-        rows_by_keys(tmem, a_lo, x_lo, cols);
-        mma_commit_warp(smem_u32(&bars.s_full[0]));
-        if (after >= w.t1) mma_commit_warp(smem_u32(&bars.a_empty[0]));
+    for (Walk<true, kMask, AttnBwdParams> w(p, start); ok && w.live; w.next(), ++items) {
+      bool first = true;
+      for (int t = w.first(), after; ok && t < w.t1; t = after, first = false) {
+        after = w.after(t);
+        const bool last = after >= w.t1;
+        const int cols = w.tile_cols(t);
+        const uint32_t buf = count & 1u;
+        if (!grads) {
+          // This step's S and dp run beside the step before's exponentials and
+          // ds.  (dp's buffer held the ds that dq took two steps ago.)
+          WaitSet ready(&bars.x_full[xs], xph, lane);
+          ready.also<1>(&bars.s_free, (count - 1) & 1u, count > 0);
+          ready.also<2>(&bars.a_full[0], items & 1u, first);
+          ok = wait_set(ready);
+          if (!ok) break;
+          tc_fence_after();
+          rows_by_keys(tmem, a_lo, x_lo + xs * tile_lo, cols);
+          mma_commit_warp(smem_u32(&bars.s_full));
+          WaitSet rest(&bars.y_full[ys], yph, lane);
+          rest.also<1>(&bars.x_empty[xs_before[1]], xph_before[1], count > 1);
+          rest.also<2>(&bars.a_full[1], items & 1u, first);
+          ok = wait_set(rest);
+          if (!ok) break;
+          tc_fence_after();
+          rows_by_keys(t_dp + buf * 128, a_lo + (kATile >> 4), y_lo + ys * tile_lo, cols);
+          mma_commit_warp(smem_u32(&bars.dp_full[buf]));
+          mma_commit_warp(smem_u32(&bars.y_empty[ys]));
+          if (last) {
+            mma_commit_warp(smem_u32(&bars.a_empty[0]));
+            mma_commit_warp(smem_u32(&bars.a_empty[1]));
+          }
+          if (++ys == p.y_stages) {
+            ys = 0;
+            yph ^= 1u;
+          }
+        } else {
+          const int keys = w.tile_keys(t);
+          uint4 used = first_keys(keys);
+          if (kMask) {
+            const uint4 any = w.any_keys(t);
+            used = make_uint4(used.x & any.x, used.y & any.y, used.z & any.z, used.w & any.w);
+          }
+          WaitSet ready(&bars.ds_full[buf], (count >> 1) & 1u, lane);
+          ready.also<1>(&bars.x_full[xs], xph);
+          ready.also<2>(&bars.acc_free, (items - 1) & 1u, first && items > 0);
+          ok = wait_set(ready);
+          if (!ok) break;
+          // Keys that no row takes part with are cleared: nothing they hold
+          // meets a zero of ds.
+          if (kMask || (keys < cols && p.a.kv_lengths)) {
+            clear_rows<kBlocks>(smem + p.off_x + xs * kv_tile, kv_block, cols, used, lane);
+            fence_proxy_async_shared();
+            __syncwarp();
+          }
+          tc_fence_after();
+          const int steps = cols >> 4;
+          const uint32_t kb = lead_k | (x_lo + xs * tile_lo), ds = t_dp + buf * 128;
+          mma_ts_x4<32>(t_acc, ds, kb, idesc_acc, first ? 0u : 1u, steps);
+          if (steps > 4) mma_ts_x4<32>(t_acc, ds + 64, kb + 512u, idesc_acc, 1u, steps - 4);
+          mma_commit_warp(smem_u32(&bars.x_empty[xs]));
+          if (last) mma_commit_warp(smem_u32(&bars.acc_done));
+        }
+        xs_before[1] = xs_before[0];
+        xph_before[1] = xph_before[0];
+        xs_before[0] = xs;
+        xph_before[0] = xph;
         if (++xs == p.x_stages) {
           xs = 0;
           xph ^= 1u;
         }
-        ok = wait(&bars.a_full[1], 0, kAttnMmaTimeout) && wait(&bars.y_full[0], 0, kAttnMmaTimeout);
+        ++count;
       }
-      if (ok) {
-        tc_fence_after();
-        rows_by_keys(t_dp, a_lo + (kATile >> 4), y_lo, cols);
-        mma_commit_warp(smem_u32(&bars.dp_full));
-        mma_commit_warp(smem_u32(&bars.y_empty[0]));
-        if (after >= w.t1) mma_commit_warp(smem_u32(&bars.a_empty[1]));
-        if (++ys == p.y_stages) {
-          ys = 0;
-          yph ^= 1u;
-        }
-      }
-    }
-    while (ok && live) {
-      const bool last = after >= w.t1;
-      const int keys = w.tile_keys(t), this_cols = cols, this_k = k_stage;
-      uint4 any = make_uint4(0, 0, 0, 0);
-      if (kMask) any = w.any_keys(t);
-      bool more = true;
-      if (last) {
-        w.next();
-        more = w.live;
-        if (more) t = w.first();
-        aph ^= 1u;
-      } else {
-        t = after;
-      }
-      if (more) after = w.after(t);
-      if (more) {
-        // The next step's S runs beside this step's exponentials ...
-        cols = w.tile_cols(t);
-        if (last) ok = wait(&bars.a_full[0], aph, kAttnMmaTimeout);
-        ok = ok && wait(&bars.x_full[xs], xph, kAttnMmaTimeout);
-        if (!ok) break;
-        tc_fence_after();
-        k_stage = xs;
-        rows_by_keys(tmem + ((count + 1) & 1u) * 128, a_lo, x_lo + xs * tile_lo, cols);
-        mma_commit_warp(smem_u32(&bars.s_full[(count + 1) & 1u]));
-        if (++xs == p.x_stages) {
-          xs = 0;
-          xph ^= 1u;
-        }
-        // ... and its dp as soon as this step's has been read.
-        ok = wait(&bars.dp_free, count & 1u, kAttnMmaTimeout);
-        if (ok && last) ok = wait(&bars.a_full[1], aph, kAttnMmaTimeout);
-        ok = ok && wait(&bars.y_full[ys], yph, kAttnMmaTimeout);
-        if (!ok) break;
-        tc_fence_after();
-        rows_by_keys(t_dp, a_lo + (kATile >> 4), y_lo + ys * tile_lo, cols);
-        mma_commit_warp(smem_u32(&bars.dp_full));
-      }
-      ok = wait(&bars.ds_full[count & 1u], (count >> 1) & 1u, kAttnMmaTimeout);
-      if (ok && first) {
-        if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
-        ++items;
-      }
-      if (!ok) break;
-      // Keys that no row takes part with are cleared: nothing they hold meets
-      // a zero of ds.
-      if (kMask || (keys < this_cols && p.a.kv_lengths)) {
-        uint4 used = first_keys(keys);
-        if (kMask) used = make_uint4(used.x & any.x, used.y & any.y, used.z & any.z, used.w & any.w);
-        clear_rows<kBlocks>(smem + p.off_x + this_k * kv_tile, kv_block, this_cols, used, lane);
-        fence_proxy_async_shared();
-        __syncwarp();
-      }
-      tc_fence_after();
-      const uint32_t ds = tmem + (count & 1u) * 128;
-      const int steps = this_cols >> 4;
-      const uint32_t kb = lead_k | (x_lo + this_k * tile_lo);
-      mma_ts_x4<32>(t_acc, ds, kb, idesc_acc, first ? 0u : 1u, steps);
-      if (steps > 4) mma_ts_x4<32>(t_acc, ds + 64, kb + 512u, idesc_acc, 1u, steps - 4);
-      if (last) mma_commit_warp(smem_u32(&bars.acc_done));
-      // (Stages are handed back after the products that others wait for.)
-      mma_commit_warp(smem_u32(&bars.x_empty[this_k]));
-      if (more) {
-        mma_commit_warp(smem_u32(&bars.y_empty[ys]));
-        if (++ys == p.y_stages) {
-          ys = 0;
-          yph ^= 1u;
-        }
-        if (after >= w.t1) {
-          mma_commit_warp(smem_u32(&bars.a_empty[0]));
-          mma_commit_warp(smem_u32(&bars.a_empty[1]));
-        }
-      }
-      ++count;
-      first = last;
-      live = more;
     }
     if (!ok) {
-      mma_commit_warp(smem_u32(&bars.drain));
-      mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
+      mma_commit_warp(smem_u32(&bars.drain[grads]));
+      mbar_wait_drain(smem_u32(&bars.drain[grads]), 0, limit / 8 + 1);
     }
     __syncwarp();
   } else {
@@ -482,17 +458,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int rest = keys - part * 32;  // of this warp's columns
         uint32_t on = rest >= 32 ? 0xFFFFFFFFu : rest <= 0 ? 0u : (1u << rest) - 1u;
         if (kMask) on &= bits ? bits[(t * p.kv_box >> 5) + part] : 0u;
-        const uint32_t buf = count & 1u;
-        ok = wait(&bars.s_full[buf], (count >> 1) & 1u, kAttnSoftmaxTimeout);
+        ok = wait(&bars.s_full, count & 1u, kAttnSoftmaxTimeout);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t ts = tmem + buf * 128 + part * 32 + lane_field;
-        const uint32_t td = t_dp + part * 32 + lane_field;
+        const uint32_t ts = tmem + part * 32 + lane_field;
+        const uint32_t td = t_dp + (count & 1u) * 128 + part * 32 + lane_field;
         const bool mine = part * 32 < cols;
         uint32_t s[32];
         if (mine) {
           tmem_ld_x32(ts, s);
           tmem_wait_ld_x32(s);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.s_free));
+        if (mine) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float x, y;
@@ -501,7 +481,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             s[2 * i + 1] = __float_as_uint(exp2_approx(y));
           }
         }
-        ok = wait(&bars.dp_full, count & 1u, kAttnSoftmaxTimeout);
+        ok = wait(&bars.dp_full[count & 1u], (count >> 1) & 1u, kAttnSoftmaxTimeout);
         if (!ok) break;
         tc_fence_after();
         if (mine) {
@@ -524,15 +504,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             h[i] = round2<T>(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
-          tmem_st_x16(ts, h);
+          tmem_st_x16(td, h);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&bars.dp_free));
-          mbar_arrive(smem_u32(&bars.ds_full[buf]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full[count & 1u]));
         ++count;
       }
       if (!ok) break;
@@ -682,7 +659,7 @@ struct KeyWalk {
 };
 
 template <typename T, int DP, bool kMask>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
     attn_dkv_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr int kBlocks = DP / 64;
@@ -711,13 +688,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(smem_u32(&bars.st_full[i]), 1);
       mbar_init(smem_u32(&bars.st_empty[i]), kSoftWarps);
     }
-    mbar_init(smem_u32(&bars.s_full[0]), 1);
-    mbar_init(smem_u32(&bars.dp_full), 1);
+    mbar_init(smem_u32(&bars.s_full), 1);
+    mbar_init(smem_u32(&bars.dp_full[0]), 1);
     mbar_init(smem_u32(&bars.p_full), kSoftWarps);
     mbar_init(smem_u32(&bars.ds_full[0]), kSoftWarps);
     mbar_init(smem_u32(&bars.acc_done), 1);
     mbar_init(smem_u32(&bars.acc_free), kSoftWarps);
-    mbar_init(smem_u32(&bars.drain), 1);
+    mbar_init(smem_u32(&bars.drain[0]), 1);
     bars.abort_flag = 0;
     fence_barrier_init();
   }
@@ -725,7 +702,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_alloc(smem_u32(&bars.tmem), 512);
     tmem_relinquish();
   }
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == kKeyLoadWarp && lane == 0) {
     tma_prefetch_desc(&p.map_q);
     tma_prefetch_desc(&p.map_do);
     tma_prefetch_desc(&p.map_k);
@@ -751,8 +728,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag, status,
                                                      code, limit));
   };
+  auto wait_set = [&](const WaitSet& s) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(s.bar, s.parity, abort_flag, status,
+                                                     kAttnMmaTimeout, limit));
+  };
 
-  if (warp == kLoadWarp) {
+  if (warp == kKeyLoadWarp) {
     // ------------------------------------------------------------ loads
     const uint32_t lead = lane == 0 ? 1u : 0u;
     const uint32_t kv_bytes = static_cast<uint32_t>(p.kv_box) * 128u * kBlocks;
@@ -839,6 +820,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
+    // dv of a step and S^T of the next as soon as p is there, dk and dp^T as
+    // soon as ds is: one wait for each pair.  (Two warps with a pair each ran
+    // every product at half its rate: 477 us for 375, with turns 788.)
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
     const uint32_t idesc_acc = attn_idesc(kBf16, k_steps * 16, false, true);
@@ -847,14 +831,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                    y_lo = smem_u32(smem + p.off_y) >> 4;
     constexpr uint32_t kTileLo = kTile >> 4;
     bool ok = true;
-    int xs = 0, ys = 0;
-    uint32_t xph = 0, yph = 0, aph = 0, count = 0, items = 0;
+    int xs = 0, ys = 0, x_now = 0, y_now = 0;  // stages to come, and the present step's
+    uint32_t xph = 0, yph = 0, count = 0, items = 0;
     auto keys_by_rows = [&](uint32_t d, uint32_t a, uint32_t b, int cols) {
       const uint32_t id = idesc_s | (static_cast<uint32_t>(cols >> 3) << 17);
       mma_ss_x4(d, kLeadK | a, kLeadK | b, id, 0u, k_steps);
       if (k_steps > 4) mma_ss_x4(d, kLeadK | (a + 1024u), kLeadK | (b + 1024u), id, 1u, k_steps - 4);
     };
-    // A (in TMEM, halves of 64 columns) times a query tile, over its rows.
+    // A (in TMEM, quarters of 32 columns) times a query tile, over its rows.
     auto accumulate = [&](uint32_t acc, uint32_t a, uint32_t b, int cols, bool fresh) {
       const int steps = cols >> 4;
       mma_ts_x4<32>(acc, a, lead_b | b, idesc_acc, fresh ? 0u : 1u, steps);
@@ -872,66 +856,61 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       fence_proxy_async_shared();
       __syncwarp();
     };
-    KeyWalk<kMask> w(p, start);
-    bool live = w.live, first = true;
-    int after = 0, cols = 0, x_now = 0, y_now = 0;
-    bool new_item = true;
-    // S^T of the walk's step, then its dp^T.
-    auto step_s = [&](uint32_t step) {
-      if (new_item) ok = wait(&bars.a_full[0], aph, kAttnMmaTimeout);
-      ok = ok && wait(&bars.x_full[xs], xph, kAttnMmaTimeout);
-      if (!ok) return;
-      tc_fence_after();
-      x_now = xs;
+    // S^T of step n, and its dp^T (their barriers are through).
+    auto step_s = [&](uint32_t n, int cols, bool last) {
       if (kMask) {
-        ok = wait(&bars.st_full[step & 1u], (step >> 1) & 1u, kAttnMmaTimeout);
+        ok = wait(&bars.st_full[n & 1u], (n >> 1) & 1u, kAttnMmaTimeout);
         if (!ok) return;
-        clear(smem + p.off_x + xs * kTile, step & 1u);
+        clear(smem + p.off_x + xs * kTile, n & 1u);
       }
       keys_by_rows(t_s, a_lo, x_lo + xs * kTileLo, cols);
-      mma_commit_warp(smem_u32(&bars.s_full[0]));
+      mma_commit_warp(smem_u32(&bars.s_full));
+      if (last) mma_commit_warp(smem_u32(&bars.a_empty[0]));
       if (++xs == p.x_stages) {
         xs = 0;
         xph ^= 1u;
       }
     };
-    auto step_dp = [&](uint32_t step) {
-      if (new_item) ok = wait(&bars.a_full[1], aph, kAttnMmaTimeout);
-      ok = ok && wait(&bars.y_full[ys], yph, kAttnMmaTimeout);
-      if (!ok) return;
-      tc_fence_after();
-      y_now = ys;
-      if (kMask) clear(smem + p.off_y + ys * kTile, step & 1u);
+    auto step_dp = [&](uint32_t n, int cols, bool last) {
+      if (kMask) clear(smem + p.off_y + ys * kTile, n & 1u);
       keys_by_rows(t_dp, a_lo + kTileLo, y_lo + ys * kTileLo, cols);
-      mma_commit_warp(smem_u32(&bars.dp_full));
-      if (after >= w.i1) {
-        mma_commit_warp(smem_u32(&bars.a_empty[0]));
-        mma_commit_warp(smem_u32(&bars.a_empty[1]));
-      }
+      mma_commit_warp(smem_u32(&bars.dp_full[0]));
+      if (last) mma_commit_warp(smem_u32(&bars.a_empty[1]));
       if (++ys == p.y_stages) {
         ys = 0;
         yph ^= 1u;
       }
     };
+    KeyWalk<kMask> w(p, start);
+    bool live = w.live, first = true;
+    int after = 0, cols = 0;
     if (live) {
       w.first();
       after = w.after();
       cols = w.cols();
-      step_s(0);
-      if (ok) step_dp(0);
+      WaitSet rows(&bars.x_full[0], 0, lane);
+      rows.also<1>(&bars.a_full[0], 0);
+      ok = wait_set(rows);
+      tc_fence_after();
+      if (ok) step_s(0, cols, after >= w.i1);
+      if (ok) {
+        WaitSet grads(&bars.y_full[0], 0, lane);
+        grads.also<1>(&bars.a_full[1], 0);
+        ok = wait_set(grads);
+        tc_fence_after();
+        if (ok) step_dp(0, cols, after >= w.i1);
+      }
     }
     while (ok && live) {
       // The next step's place first: between the products below there is only
       // what they need.
       const bool last = after >= w.i1;
-      const int this_cols = cols, this_x = x_now, this_y = y_now;
+      const int this_cols = cols;
       bool more = true;
-      new_item = last;
       if (last) {
         w.next();
         more = w.live;
         if (more) w.first();
-        aph ^= 1u;
       } else {
         w.go(after);
       }
@@ -939,32 +918,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         after = w.after();
         cols = w.cols();
       }
-      if (first) {
-        if (items > 0) ok = wait(&bars.acc_free, (items - 1) & 1u, kAttnMmaTimeout);
-        ++items;
-      }
-      ok = ok && wait(&bars.p_full, count & 1u, kAttnMmaTimeout);
+      const uint32_t next_item = (items + 1) & 1u;
+      WaitSet to_p(&bars.p_full, count & 1u, lane);
+      to_p.also<1>(&bars.x_full[xs], xph, more);
+      to_p.also<2>(&bars.a_full[0], next_item, more && last);
+      to_p.also<3>(&bars.acc_free, (items - 1) & 1u, first && items > 0);
+      ok = wait_set(to_p);
       if (!ok) break;
       tc_fence_after();
-      accumulate(t_dv, t_s, y_lo + this_y * kTileLo, this_cols, first);
-      if (more) step_s(count + 1);
+      accumulate(t_dv, t_s, y_lo + y_now * kTileLo, this_cols, first);
+      mma_commit_warp(smem_u32(&bars.y_empty[y_now]));
+      y_now = ys;
+      if (more) step_s(count + 1, cols, after >= w.i1);
       if (!ok) break;
-      mma_commit_warp(smem_u32(&bars.y_empty[this_y]));
-      ok = wait(&bars.ds_full[0], count & 1u, kAttnMmaTimeout);
+      WaitSet to_ds(&bars.ds_full[0], count & 1u, lane);
+      to_ds.also<1>(&bars.y_full[ys], yph, more);
+      to_ds.also<2>(&bars.a_full[1], next_item, more && last);
+      ok = wait_set(to_ds);
       if (!ok) break;
       tc_fence_after();
-      accumulate(t_dk, t_dp, x_lo + this_x * kTileLo, this_cols, first);
+      accumulate(t_dk, t_dp, x_lo + x_now * kTileLo, this_cols, first);
       if (last) mma_commit_warp(smem_u32(&bars.acc_done));
-      if (more) step_dp(count + 1);
-      if (!ok) break;
-      mma_commit_warp(smem_u32(&bars.x_empty[this_x]));
+      mma_commit_warp(smem_u32(&bars.x_empty[x_now]));
+      if (++x_now == p.x_stages) x_now = 0;
+      if (more) step_dp(count + 1, cols, after >= w.i1);
+      if (last) ++items;
       ++count;
       first = last;
       live = more;
     }
     if (!ok) {
-      mma_commit_warp(smem_u32(&bars.drain));
-      mbar_wait_drain(smem_u32(&bars.drain), 0, limit / 8 + 1);
+      mma_commit_warp(smem_u32(&bars.drain[0]));
+      mbar_wait_drain(smem_u32(&bars.drain[0]), 0, limit / 8 + 1);
     }
     __syncwarp();
   } else {
@@ -1009,7 +994,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool select = kMask || !keys_whole;
         const uint32_t ss = count & 1u;
         ok = wait(&bars.st_full[ss], (count >> 1) & 1u, kAttnSoftmaxTimeout) &&
-             wait(&bars.s_full[0], count & 1u, kAttnSoftmaxTimeout);
+             wait(&bars.s_full, count & 1u, kAttnSoftmaxTimeout);
         if (!kMask && !ok) break;
         const float* st = reinterpret_cast<const float*>(smem + p.off_stat + ss * 1024) + part * 32;
         uint32_t s[32];
@@ -1042,7 +1027,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars.p_full));
-          ok = wait(&bars.dp_full, count & 1u, kAttnSoftmaxTimeout);
+          ok = wait(&bars.dp_full[0], count & 1u, kAttnSoftmaxTimeout);
         }
         if (ok) {
           tc_fence_after();
@@ -1247,7 +1232,7 @@ cudaError_t launch_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_
   static std::atomic<size_t> configured[kMaxDevices];
   cudaError_t e = raise_smem(attn_dq_kernel<T, DP, kMask>, configured, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dq_kernel<T, DP, kMask>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+  return launch_pdl(attn_dq_kernel<T, DP, kMask>, dim3(grid), dim3(kDqThreads), smem, stream, p);
 }
 
 template <typename T, int DP, bool kMask>
@@ -1255,7 +1240,7 @@ cudaError_t launch_dkv(const AttnBwdParams& p, int grid, size_t smem, cudaStream
   static std::atomic<size_t> configured[kMaxDevices];
   cudaError_t e = raise_smem(attn_dkv_kernel<T, DP, kMask>, configured, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dkv_kernel<T, DP, kMask>, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+  return launch_pdl(attn_dkv_kernel<T, DP, kMask>, dim3(grid), dim3(kDkvThreads), smem, stream, p);
 }
 
 // Calls f with the operands' type, whether a row is wider than 64 columns and
