@@ -250,8 +250,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                                                      code, limit));
   };
   auto wait_set = [&](const WaitSet& s) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(s.bar, s.parity, abort_flag, status,
-                                                     kAttnMmaTimeout, limit));
+    return wait_set_bounded(s, abort_flag, status, kAttnMmaTimeout, limit);
   };
 
   if (warp == kLoadWarp) {
@@ -729,8 +728,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                                                      code, limit));
   };
   auto wait_set = [&](const WaitSet& s) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(s.bar, s.parity, abort_flag, status,
-                                                     kAttnMmaTimeout, limit));
+    return wait_set_bounded(s, abort_flag, status, kAttnMmaTimeout, limit);
   };
 
   if (warp == kKeyLoadWarp) {

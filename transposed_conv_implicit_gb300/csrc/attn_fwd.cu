@@ -134,6 +134,10 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
                                                      code, limit));
   };
 
+  auto wait_set = [&](const WaitSet& s) {
+    return wait_set_bounded(s, abort_flag, status, kAttnMmaTimeout, limit);
+  };
+
   if (warp == L::kLoadWarp) {
     // ------------------------------------------------------------ loads
     if (G == 2) give_registers<80>();
@@ -295,8 +299,9 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     while (ok && live) {
       // This step's values, then the next step's keys.
       const int v_stage = stage, keys = w.tile_keys(t), this_cols = cols;
-      ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
+      if (kMask || p.a.kv_lengths) ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
       if (!ok) break;
+      const uint32_t v_phase = phase;
       advance();
       // Values that no row of the CTA takes part with are cleared, so that
       // nothing they hold meets a zero of P: keys past the request's length
@@ -327,18 +332,20 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       if (more) {
         after = w.after(t);
         cols = w.tile_cols(t);
-        if (next_item) ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout);
-        ok = ok && wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
       }
-      if (ok && first) {
-        if (items > 0) ok = wait(&bars.o_free[g], (items - 1) & 1u, kAttnMmaTimeout);
-        ++items;
-      }
+      WaitSet tiles_in(&bars.kv_full[v_stage], v_phase, lane);
+      tiles_in.also<1>(&bars.kv_full[stage], phase, more);
+      tiles_in.also<2>(&bars.q_full[g][qs], q_phase, more && next_item);
+      tiles_in.also<3>(&bars.o_free[g], (items - 1) & 1u, first && items > 0);
+      ok = wait_set(tiles_in);
+      if (first) ++items;
       // The first 64 keys' products start before the others' P is there.  The
       // groups take turns with whole batches (P v, then the next S): products
       // of two batches in between one another would end together, and both
       // groups' exponentials would leave the tensor core idle.
-      ok = ok && wait(&bars.p_half[g], tiles & 1u, kAttnMmaTimeout) && take_turn();
+      WaitSet ready(&bars.p_half[g], tiles & 1u, lane);
+      ready.also<1>(&bars.turn[g], (turns & 1u) ^ (g == 0 ? 1u : 0u), G == 2);
+      ok = ok && wait_set(ready);
       if (!ok) break;
       tc_fence_after();
       const uint32_t b = lead_v | (kv_lo + v_stage * kv_tile_lo);
