@@ -819,8 +819,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ products
     // dv of a step and S^T of the next as soon as p is there, dk and dp^T as
-    // soon as ds is: one wait for each pair.  (Two warps with a pair each ran
-    // every product at half its rate: 477 us for 375, with turns 788.)
+    // soon as ds is: one wait for each pair.  (2 x 16 heads, 8192 x 2048 x
+    // 128: 350 us; two warps with a pair each 372, taking turns 358.)
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t idesc_s = attn_idesc(kBf16, 0, false, false);
     const uint32_t idesc_acc = attn_idesc(kBf16, k_steps * 16, false, true);
