@@ -132,6 +132,21 @@ def test_long(case):
     _check(case[7], *case[:7], seed=3)
 
 
+ALONE = [  # row tiles without a partner in a pair, more of them than SMs: b, lq, lk, h, hkv, d
+    (3, 100, 300, 60, 60, 128),
+    (2, 300, 300, 40, 40, 128),
+    (1, 260, 290, 90, 90, 72),
+    (4, 70, 270, 50, 50, 64),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("kind", ["none", "lengths", "rows"])
+@pytest.mark.parametrize("size", ALONE, ids=lambda s: "x".join(map(str, s)))
+def test_rows_without_a_partner(size, kind, dtype):
+    _check(dtype, *size, kind)
+
+
 TOKENS = [  # b, lq, lk, h, hkv, d: few queries over many keys
     (1, 1, 5000, 8, 8, 64),
     (3, 1, 4097, 32, 8, 128),

@@ -254,8 +254,17 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     };
     Walk<L::kSplit, kMask, AttnFwdParams> w(p, start);
     // Items without a row tile for this group: their stages are passed on.
+    // (Only once the group's own batches are issued: it would hold the last
+    // values' stage all along.  The queries' stage first, when the loads have
+    // come to it: the other group's last turn of an item waits for keys that
+    // are loaded behind the next item's queries.)
+    auto absent = [&]() { return G == 2 && w.live && g >= w.tiles_here; };
     auto skip_absent = [&]() {
-      while (G == 2 && ok && w.live && g >= w.tiles_here) {
+      while (ok && absent()) {
+        ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout);
+        if (!ok) break;
+        mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+        next_q();
         for (int t = w.first(); ok && t < w.t1; t = w.after(t)) {
           for (int i = 0; ok && i < 2; ++i) {
             ok = wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
@@ -265,8 +274,6 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
           ok = ok && take_turn();
           if (ok) end_turn();
         }
-        mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
-        next_q();
         w.next();
       }
     };
@@ -279,23 +286,27 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       if (k_steps > 4) mma_ss_x4(ts, a + 1024u, b + kv_block_lo, id, 1u, k_steps - 4);
       mma_commit_warp(smem_u32(&bars.s_full[g]));
     };
-    skip_absent();
-    bool live = ok && w.live;
-    int t = live ? w.first() : 0, after = 0, cols = 0;
+    int t = 0, after = 0, cols = 0;
     bool first = true;
-    if (live) {
+    // The next item that has a row tile for the group, and its first scores.
+    auto begin = [&]() {
+      skip_absent();
+      if (!ok || !w.live) return false;
+      t = w.first();
       after = w.after(t);
       cols = w.tile_cols(t);
+      first = true;
       ok = wait(&bars.q_full[g][qs], q_phase, kAttnMmaTimeout) &&
            wait(&bars.kv_full[stage], phase, kAttnMmaTimeout);
-      if (ok) {
-        tc_fence_after();
-        scores(stage, cols);
-        mma_commit_warp(smem_u32(&bars.kv_empty[stage]));
-        if (after >= w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
-        advance();
-      }
-    }
+      if (!ok) return false;
+      tc_fence_after();
+      scores(stage, cols);
+      mma_commit_warp(smem_u32(&bars.kv_empty[stage]));
+      if (after >= w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
+      advance();
+      return true;
+    };
+    bool live = begin();
     while (ok && live) {
       // This step's values, then the next step's keys.
       const int v_stage = stage, keys = w.tile_keys(t), this_cols = cols;
@@ -321,9 +332,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       if (after >= w.t1) {
         w.next();
         next_q();
-        skip_absent();
-        if (!ok) break;
-        more = w.live;
+        more = w.live && !absent();
         next_item = true;
         if (more) t = w.first();
       } else {
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         if (after >= w.t1) mma_commit_warp(smem_u32(&bars.q_empty[g][qs]));
       }
       first = next_item;
-      live = more;
+      live = more || begin();
     }
     if (!ok) {
       // Every MMA already issued must finish before TMEM is released.
