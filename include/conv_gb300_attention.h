@@ -42,7 +42,8 @@ extern "C" {
  * query attends is used in products with whole tiles of queries, so it has to
  * be finite for those that do not attend it, too.)
  * Backward, with dout of out:
- *   dv_j = sum_i p_ij dout_i,  delta_i = sum_d dout_i[d] out_i[d]
+ *   dv_j = sum_i p_ij dout_i,  delta_i = sum_d dout_i[d] out_i[d]  (of the
+ *   rounded out that is passed in, or summed anew where all keys are one tile)
  *   ds_ij = p_ij (dout_i . v_j - delta_i)
  *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
  * dk and dv sum over the query heads that share the key head.  Sums run in a
@@ -58,10 +59,13 @@ extern "C" {
  * [q_len].  mask is bytes (0 = left out) with any strides, 0 among them.
  *
  * Gates (CONV_ERR_NOT_SUPPORTED): dtype BF16 or F16; head_dim a multiple of 8
- * up to 128.  CONV_ERR_INVALID_VALUE: null pointers, negative sizes, heads
- * not a multiple of kv_heads, zero strides of outputs or along tokens, a
- * scale that is not finite and positive.  CONV_ERR_MISALIGNED: a pointer off 16 bytes or a stride
- * that is no multiple of 8.
+ * up to 128; batch * heads * (q_len + 128) and batch * kv_heads * (kv_len +
+ * 128) below 2^31.  CONV_ERR_INVALID_VALUE: null pointers, negative sizes,
+ * heads not a multiple of kv_heads, negative strides, zero strides of outputs
+ * or along tokens, a scale that is not finite and positive.
+ * CONV_ERR_MISALIGNED: a pointer off 16 bytes (lse and kv_lengths: 4) or a
+ * stride that is no multiple of 8.  CONV_ERR_DEVICE_TIMEOUT, by
+ * conv_check_device_status: a wait inside a kernel ran out.
  * kv_lengths values are taken as clamped to [0, kv_len].
  * ------------------------------------------------------------------------ */
 typedef struct {
@@ -116,7 +120,9 @@ conv_status_t cross_attention_bwd(const cross_attention_args_t* args, void* work
  * fp32 [table_rows][rot_dim / 2].  positions: int32 [batch][length] with
  * batch stride position_stride (0: shared by the batch), or NULL for
  * 0 .. length-1; they are clamped to [0, table_rows - 1].
- * Gates: D a multiple of 8 up to 256; rot_dim a multiple of 8 up to D, or 0.
+ * Gates: D a multiple of 8 up to 256; rot_dim a multiple of 8 up to D, or 0;
+ * batch * length * heads up to 0x7FFF0000, strides below 2^35
+ * (CONV_ERR_NOT_SUPPORTED).
  * ------------------------------------------------------------------------ */
 typedef struct {
   const void* x;

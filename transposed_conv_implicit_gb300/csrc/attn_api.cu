@@ -105,7 +105,8 @@ FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
   f.kv_box = std::min(kAttnRows, std::max(16, (a.kv_len + 15) / 16 * 16));
   const long long nt = std::max(1, (a.kv_len + f.kv_box - 1) / f.kv_box);
   const long long heads = static_cast<long long>(a.batch) * a.kv_heads;
-  // One tile of keys, narrow heads, no mask: the kernel made for it.  Four
+  // One tile of keys, narrow heads, no mask: the kernel made for it (16 x 4096
+  // x 8 heads x 40 against 77 keys: 31 us, 47 in pairs).  Four
   // CTAs per SM where scores and output fit in 128 TMEM columns.
   if (a.kv_len > 0 && a.kv_len <= kAttnRows && a.head_dim <= 64 && !a.mask) {
     f.one = f.kv_box + (a.head_dim + 15) / 16 * 16 <= 128 ? 4 : 2;
@@ -118,8 +119,10 @@ FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
   // pair's step covers two row tiles on a whole SM.
   const long long rounds = (f.items + sms - 1) / sms;
   const double pairs_cost = static_cast<double>(rounds) * nt;
-  // The join costs what 4 steps do (8 us; 2 x 1021 x 12 heads x 80 against 523,
-  // masked: 28 us as pairs, FWDSPLIT us split and joined).
+  // The join costs what 4 steps do.  Both sides, whole calls: one token of 64
+  // requests x 32 heads x 128 against up to 4096 keys, 171 us as pairs and 141
+  // split; 3 x 1021 x 12 heads x 80 against 1531, masked, 42 and 59; 2 x 16 heads,
+  // 16384 x 4096 x 128, 774 and 963.
   const double split_cost = static_cast<double>(heads) * row_tiles * nt / (2.0 * sms) * 1.25 + (nt > 1 ? 4 : 0);
   f.split = split_cost < pairs_cost;
   const long long steps = heads * row_tiles * nt;
@@ -150,7 +153,9 @@ BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
   p.q_grid = static_cast<int>(std::min<long long>(heads * f.row_tiles * nt, sms));
   p.kv_grid = static_cast<int>(std::min<long long>(heads * p.kv_tiles * p.item_steps, sms));
   // Even shares cut items and join them, which costs about what kJoinSteps
-  // steps do; whole items leave some CTAs idle at the end.
+  // steps do; whole items leave some CTAs idle at the end.  (2 x 1021 x 12
+  // heads x 80 against 523, masked, the training pass: 107 us with dq's items
+  // cut, 99 whole.)
   constexpr double kJoinSteps = 5;
   const auto whole = [sms](long long items, long long steps) {
     return static_cast<double>((items + sms - 1) / sms) * steps <=

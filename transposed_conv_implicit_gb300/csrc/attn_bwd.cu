@@ -7,8 +7,10 @@
 // Three kernels, none with atomics, so that every sum has a fixed order:
 //  - rows: delta and the statistics of every query (bound by reading do, o);
 //  - dq: a row tile of 128 (token, head) rows stays, key tiles stream by.
-//    S = q k^T and dp = do v^T (lanes = queries) land in TMEM, ds replaces S
-//    there and is the A operand of dq += ds k: three products per tile;
+//    S = q k^T and dp = do v^T (lanes = queries) land in TMEM, ds replaces dp
+//    there and is the A operand of dq += ds k: three products per tile.  S is
+//    free once it is read and dp has two buffers, so that both are ready when
+//    the exponentials come to them;
 //  - dk, dv: 128 keys stay, query tiles stream by, over all query heads that
 //    share the key head.  S^T = k q^T and dp^T = v do^T (lanes = keys), so
 //    that p^T and ds^T are A operands in TMEM where they are made: dv += p^T
@@ -17,7 +19,15 @@
 // price of dq and dk, dv each summing in registers of their own CTA, without
 // adding fp32 partial sums of dq through L2 once per key tile.
 //
-// Each kernel's (tile, step) sequence is cut into equal shares, one per SM;
+// 2 x 16 heads, 8192 x 2048 x 128 (bound by the products): rows 28 us (4.9
+// TB/s), dq 254 (1.62 PFLOP/s), dk and dv 350 (1.57 PFLOP/s), joins 31.  What
+// held the products back were waits: products of 128 x 128 from shared memory
+// take all of its bandwidth, and an mbarrier that is looked at beside them
+// answers after some 300 cycles.  16 softmax warps (a quarter of the columns
+// each) take 3 % less than 8.
+//
+// Each kernel's (tile, step) sequence is cut into equal shares, one per SM,
+// unless whole tiles even out;
 // the tiles that a share boundary cuts go through fp32 partial sums, which a
 // last kernel adds in order.  Rows that take no part are cleared in shared
 // memory before a product sums over them.
@@ -67,6 +77,9 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y) {
   return s;
 }
 
+// delta is taken from the rounded output, which leaves ds an error of the
+// output's rounding (gradients up to 1.8 times as far from 64 bits as with an
+// fp32 output), for a pass over the keys that is saved.
 // stats[b][h][token tile][2][128]: minus lse in log2 units, plus p_shift (-inf
 // for queries without keys and past the end, which makes p zero), and minus
 // delta: as the products' sums take them.  With norms: the

@@ -46,7 +46,7 @@ __device__ __forceinline__ bool barrier_all(uint32_t id, uint32_t count, bool v)
 // the barrier is through or not (the products take all of the bandwidth), and
 // one set takes no more.  The lanes poll in step: where they left the loop one
 // by one, the warp's products afterwards issued at half their rate (the forward
-// pass at 2 x 16 heads, 16384 x 4096 x 128: 1819 us, in step FWDSET).
+// pass at 2 x 16 heads, 16384 x 4096 x 128: 1819 us, in step 768).
 struct WaitSet {
   uint32_t bar, parity, lane;
   __device__ WaitSet(uint64_t* b, uint32_t q, int at) : bar(smem_u32(b)), parity(q), lane(at & 7) {}

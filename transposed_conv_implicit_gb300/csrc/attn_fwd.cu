@@ -25,6 +25,17 @@
 //
 // P is rounded to the inputs' type (the product's operand type), the sum is
 // taken of the unrounded fp32 values; O is rounded once.
+//
+// A group's products (P v, then the next S) are one batch that its own warp
+// issues; the groups' batches take turns.  With a mask, key tiles that none of
+// the rows' tiles of 128 queries attends are skipped.
+//
+// Bound by the products and, beside them, the exponentials: 2 x 16 heads, 16384
+// x 4096 x 128 takes 771 us, 1.43 PFLOP/s (567 us at the rate of a large matrix
+// product).  Split, by reading the keys: one token of 64 requests x 32 heads
+// against up to 4096 keys, 141 us, 5.8 TB/s.  Masked (each query sees its own
+// segment), 3 x 1021 x 12 heads x 80 against 1531: 41 us, of which the mask's
+// packing takes 6; 104 without the skipping.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -9,12 +9,20 @@
 // the queries' shared-memory buffer; keys and values stay while consecutive
 // tiles share them.
 //
+// 16 x 4096 x 8 heads x 40 against 77 keys: 32 us, 2.6 TB/s; the floor is 12.5
+// us of memory traffic.  A row tile passes loads, scores, exponentials,
+// products and stores one after another (5300 cycles, 37 % of the issue slots
+// with four CTAs per SM, whose scores and outputs fill TMEM).
+//
 // Backward, one pass over q and do for all three gradients: a row's scores
 // and dp = do v^T are whole in TMEM, so delta = sum_j p_j dp_j is summed right
 // there (no read of out).  p and ds go to shared memory as the queries' rows;
 // the same bytes are the A operand of dv += p^T do and dk += ds^T q (rows along
 // M) and of dq = ds k (rows along K).  dk and dv stay in TMEM over a CTA's
 // share of a key head's query tiles and are joined through the workspace.
+// The same call: 54 us and 9 for the join (the floor is 19): shared memory
+// carries p and ds three times and the 128-row operands of five products, some
+// 2000 cycles a step of 2700.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
