@@ -31,13 +31,15 @@ _NORM_HEAD = struct.Struct("@6if4x2Q")
 _NO_TENSOR = bytes(_NORM_TENSOR.size)
 _NO_STRIDES = (0, 0, 0)
 
-_codes = None         # torch dtype -> conv_dtype_t, filled on first use
+_torch = None         # with the next two, filled on first use
+_codes = None         # torch dtype -> conv_dtype_t
 _raw_stream = None
 
 
 def _fill_codes():
-    global _codes, _raw_stream
+    global _torch, _codes, _raw_stream
     import torch
+    _torch = torch
     # The current stream as a plain number, without building a Stream object.
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -59,14 +61,24 @@ def _check(status, where):
         raise _error(status, where)
 
 
+# The calls below run before every launch, single tokens' among them: devices are
+# compared as numbers and shapes as they come (a torch.device or a tuple for each
+# tensor made a call of one token half as long again).
 def _stream(stream, device):
     if stream is None:
-        return _raw_stream(device.index)
+        return _raw_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _workspace(workspace, device):
+    """Address and bytes of the caller's workspace."""
+    if workspace.get_device() != device:
+        raise _invalid("workspace must be on cuda:%d" % device)
+    return workspace.data_ptr(), workspace.nbytes
+
+
 def _common(x, name):
-    """The dtype code and device of the leading tensor."""
+    """The dtype code and the device's number of the leading tensor."""
     codes = _codes or _fill_codes()
     if x.dim() != 4:
         raise _invalid("%s must be [batch, length, heads, head_dim]" % name)
@@ -75,32 +87,31 @@ def _common(x, name):
         raise _error(CONV_ERR_NOT_SUPPORTED, "dtype %s" % x.dtype)
     if not x.is_cuda:
         raise _invalid("%s must be a CUDA tensor" % name)
-    return code, x.device
+    return code, x.get_device()
 
 
 def _strides(t, name, shape, dtype, device):
     """{batch, token, head} strides of a tensor of this shape, type and device."""
     if t.shape != shape:
         raise _invalid("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype or t.device != device:
-        raise _invalid("%s must be %s on %s" % (name, dtype, device))
-    s = t.stride()
-    if s[3] != 1 and shape[3] > 1:
+    if t.dtype is not dtype or t.get_device() != device:
+        raise _invalid("%s must be %s on cuda:%d" % (name, dtype, device))
+    b, l, h, d = t.stride()
+    if d != 1 and shape[3] > 1:
         raise _invalid("%s: the innermost dimension must be contiguous" % name)
-    return s[:3]
+    return b, l, h
 
 
 def _dense(t, name, shape, dtype, device):
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise _invalid("%s must be a contiguous %s tensor of shape %s on %s"
-                       % (name, dtype, shape, device))
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise _invalid("%s must be a contiguous %s tensor of shape %s on cuda:%d"
+                       % (name, dtype, tuple(shape), device))
     return t.data_ptr()
 
 
 def _attention(backward, q, k, v, output, lse, kv_lengths, mask, scale, grads, workspace, stream):
-    import torch
     code, device = _common(q, "q")
-    dtype, shape = q.dtype, q.shape
+    torch, dtype, shape = _torch, q.dtype, q.shape
     b, lq, h, d = shape
     if k.dim() != 4 or k.shape[0] != b or k.shape[3] != d:
         raise _invalid("k must be [batch, kv_len, kv_heads, head_dim] of q's batch and head_dim")
@@ -117,8 +128,9 @@ def _attention(backward, q, k, v, output, lse, kv_lengths, mask, scale, grads, w
         kv_lengths = _dense(kv_lengths, "kv_lengths", (b,), torch.int32, device)
     mask_ptr, mask_strides = 0, (0, 0, 0, 0)
     if mask is not None:
-        if mask.dim() != 4 or mask.dtype not in (torch.bool, torch.uint8) or mask.device != device:
-            raise _invalid("mask must be a bool or uint8 tensor of 4 dimensions on %s" % device)
+        if (mask.dim() != 4 or mask.dtype not in (torch.bool, torch.uint8)
+                or mask.get_device() != device):
+            raise _invalid("mask must be a bool or uint8 tensor of 4 dimensions on cuda:%d" % device)
         for have, want in zip(mask.shape, (b, h, lq, lk)):
             if have != want and have != 1:
                 raise _invalid("mask has shape %s, not broadcast to %s"
@@ -142,12 +154,9 @@ def _attention(backward, q, k, v, output, lse, kv_lengths, mask, scale, grads, w
     lib = _lib.lib()
     if workspace is None:
         from . import new_workspace
-        workspace = new_workspace(lib.cross_attention_workspace_size(args, int(backward)), device)
-    elif workspace.device != device:
-        raise _invalid("workspace must be on %s" % device)
+        workspace = new_workspace(lib.cross_attention_workspace_size(args, int(backward)), q.device)
     call = lib.cross_attention_bwd if backward else lib.cross_attention_fwd
-    status = call(args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                  _stream(stream, device))
+    status = call(args, *_workspace(workspace, device), _stream(stream, device))
     if status != CONV_OK:
         raise _error(status, "cross_attention_bwd" if backward else "cross_attention_fwd")
 
@@ -189,28 +198,27 @@ def cross_attention_bwd(dout, q, k, v, output, lse, dq, dk, dv, *, kv_lengths=No
 
 
 def _norm_tensor(name, x, weight, positions, y, dy, dx, dweight, batch, d, dtype, device):
-    import torch
     if x is None:
         return _NO_TENSOR
-    shape = x.shape
+    torch, shape = _torch, x.shape
     if shape[0] != batch or shape[3] != d:
         raise _invalid("%s differs from the other tensor in batch or head_dim" % name)
     if weight is None:
         raise _invalid("%s needs its weight" % name)
-    if weight.shape != (d,) or weight.device != device or not weight.is_contiguous() or (
-            weight.dtype != dtype and weight.dtype != torch.float32):
+    if weight.shape != (d,) or weight.get_device() != device or not weight.is_contiguous() or (
+            weight.dtype is not dtype and weight.dtype is not torch.float32):
         raise _invalid("%s_weight must be a contiguous [%d] tensor of %s or float32" % (name, d, dtype))
     pos, pos_stride = 0, 0
     if positions is not None:
         if positions.dim() == 1 and positions.shape[0] == shape[1]:
             stride = (0, positions.stride(0))
-        elif tuple(positions.shape) == (batch, shape[1]):
+        elif positions.shape == (batch, shape[1]):
             stride = positions.stride()
         else:
             raise _invalid("%s_positions must be [length] or [batch, length]" % name)
-        if positions.dtype != torch.int32 or positions.device != device or (
+        if positions.dtype is not torch.int32 or positions.get_device() != device or (
                 stride[1] != 1 and shape[1] > 1):
-            raise _invalid("%s_positions must be int32 on %s, contiguous along the length"
+            raise _invalid("%s_positions must be int32 on cuda:%d, contiguous along the length"
                            % (name, device))
         pos, pos_stride = positions.data_ptr(), stride[0]
     xs = _strides(x, name, shape, dtype, device)
@@ -227,11 +235,10 @@ def _norm_tensor(name, x, weight, positions, y, dy, dx, dweight, batch, d, dtype
         strides = (*xs, 0, 0, 0, *_strides(dy, "d%s_out" % name, shape, dtype, device),
                    *_strides(dx, "d" + name, shape, dtype, device))
     return _NORM_TENSOR.pack(x.data_ptr(), weight.data_ptr(), pos, out, *rest, shape[1], shape[2],
-                             int(weight.dtype != dtype), pos_stride, *strides)
+                             weight.dtype is not dtype, pos_stride, *strides)
 
 
 def _norm_head(q, k, cos, sin, eps, adjacent_pairs):
-    import torch
     lead = q if q is not None else k
     if lead is None:
         raise _invalid("q and k are both missing")
@@ -245,9 +252,10 @@ def _norm_head(q, k, cos, sin, eps, adjacent_pairs):
     else:
         if cos.dim() != 2:
             raise _invalid("cos must be [rows, rot_dim / 2]")
-        rows, half = cos.shape
-        cp = _dense(cos, "cos", (rows, half), torch.float32, device)
-        sp = _dense(sin, "sin", (rows, half), torch.float32, device)
+        shape = cos.shape
+        rows, half = shape
+        cp = _dense(cos, "cos", shape, _torch.float32, device)
+        sp = _dense(sin, "sin", shape, _torch.float32, device)
     head = _NORM_HEAD.pack(code, lead.shape[0], lead.shape[3], 2 * half, rows,
                            1 if adjacent_pairs else 0, eps, cp, sp)
     return head, lead, device
@@ -292,10 +300,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, dq, dk, dq_weight
                            device))
     if workspace is None:
         from . import new_workspace
-        workspace = new_workspace(qk_norm_rope_workspace_size(d), device)
-    elif workspace.device != device:
-        raise _invalid("workspace must be on %s" % device)
-    _check(_lib.lib().qk_norm_rope_bwd(args, workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(),
-                                       _stream(stream, device)), "qk_norm_rope_bwd")
+        workspace = new_workspace(qk_norm_rope_workspace_size(d), lead.device)
+    _check(_lib.lib().qk_norm_rope_bwd(args, *_workspace(workspace, device), _stream(stream, device)),
+           "qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
