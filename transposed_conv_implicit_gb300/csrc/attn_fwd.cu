@@ -376,14 +376,13 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       tc_fence_after();
       if (steps > 4) mma_ts_x4(to, ts + 32, b + 512u, idesc_o, 1u, steps - 4);
       ++tiles;
-      // (The row's last product is announced at once, the others after the
-      // next scores, which the softmax waits for.)
-      if (!more || next_item) mma_commit_warp(smem_u32(&bars.o_done[g]));
+      // (Announced before the next scores are: who has seen those can tell this
+      // product's phase from the one before.)
+      mma_commit_warp(smem_u32(&bars.o_done[g]));
       const int k_stage = stage;
       if (more) {
         scores(stage, cols);
         advance();
-        if (!next_item) mma_commit_warp(smem_u32(&bars.o_done[g]));
       }
       end_turn();
       mma_commit_warp(smem_u32(&bars.kv_empty[v_stage]));
