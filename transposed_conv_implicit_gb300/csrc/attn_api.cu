@@ -373,10 +373,13 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
     conv_status_t st = encode_maps(&p, s, f.tile_heads, f.tile_tokens, f.kv_box);
     if (st != CONV_OK) return st;
     const uint32_t kv_tile = f.kv_box * (wide ? 256 : 128);
-    p.x_stages = wide ? 3 : 4;
+    // (One key tile: two of its stages do, and leave room for the sums of delta.)
+    const bool one = s.kv_len <= f.kv_box;
+    p.x_stages = one ? 2 : wide ? 3 : 4;
     p.y_stages = wide ? 2 : 4;
     p.off_a = 0;
-    p.off_x = 2 * block;
+    p.off_stat = 2 * block;
+    p.off_x = p.off_stat + (one ? 2048 : 0);
     p.off_y = p.off_x + p.x_stages * kv_tile;
     p.off_bar = p.off_y + p.y_stages * kv_tile;
     if (launch_attn_dq(p, g.q_grid, p.off_bar + attn_bwd_bar_bytes(), stream) != cudaSuccess)
@@ -387,6 +390,7 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
     if (st != CONV_OK) return st;
     p.x_stages = wide && s.mask_bits ? 2 : 3;
     p.y_stages = 2;
+    p.off_x = 2 * block;
     p.off_y = p.off_x + p.x_stages * block;
     p.off_stat = p.off_y + p.y_stages * block;
     p.off_mask = p.off_stat + 2048;

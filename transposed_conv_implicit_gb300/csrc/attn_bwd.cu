@@ -77,9 +77,9 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y) {
   return s;
 }
 
-// delta is taken from the rounded output, which leaves ds an error of the
-// output's rounding (gradients up to 1.8 times as far from 64 bits as with an
-// fp32 output), for a pass over the keys that is saved.
+// With more than one tile of keys, delta is taken from the rounded output, which
+// leaves ds an error of the output's rounding, for a pass over the keys that is
+// saved (one tile: the dq kernel sums it and puts it in).
 // stats[b][h][token tile][2][128]: minus lse in log2 units, plus p_shift (-inf
 // for queries without keys and past the end, which makes p zero), and minus
 // delta: as the products' sums take them.  With norms: the
@@ -127,8 +127,9 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
       } else {
         x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.dout) + b * a.dos[0] +
                                                t * a.dos[1] + h * a.dos[2] + at * 8);
-        y[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + b * a.os[0] + t * a.os[1] +
-                                               h * a.os[2] + at * 8);
+        if (a.kv_len > p.kv_box)
+          y[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.out) + b * a.os[0] +
+                                                 t * a.os[1] + h * a.os[2] + at * 8);
         if (at == 0) lse[u] = a.lse[row0 + t];
       }
     }
@@ -195,7 +196,11 @@ constexpr int kGradWarp = kSoftWarps + 1, kLoadWarp = kSoftWarps + 2, kDqThreads
 constexpr int kKeyLoadWarp = kSoftWarps + 1, kDkvThreads = 32 * (kSoftWarps + 2);
 
 // ------------------------------------------------------------------ dq
-template <typename T, int DP, bool kMask>
+// kOne: all keys are one tile, and each row's delta is summed here, from p and
+// dp in fp32 (with few keys ds is a small difference, which the rounding of the
+// output that delta is else taken from would swamp: against 3 keys the
+// gradients were 1.8 times as far off); the dk, dv kernel then takes it too.
+template <typename T, int DP, bool kMask, bool kOne>
 __global__ void __launch_bounds__(kDqThreads, 1)
     attn_dq_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -454,28 +459,29 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const bool row_ok = row_token < p.tile_tokens && token < p.a.q_len;
       float lse2 = -INFINITY, delta = 0.f;  // (both negated)
       const uint32_t* bits = nullptr;
+      float* st = nullptr;
       if (row_ok) {
-        const float* st = p.stats +
+        st = p.stats +
                           ((static_cast<long long>(w.b) * p.a.heads + head) * p.q_tiles + (token >> 7)) * 256;
         lse2 = st[token & 127];
-        delta = st[128 + (token & 127)];
+        if (!kOne) delta = st[128 + (token & 127)];
         if (kMask)
           bits = p.a.mask_bits +
                  (w.b * p.a.mask_b + head * p.a.mask_h + token * p.a.mask_q) * p.a.mask_words;
       }
-      const uint64_t c22 = pack2(c2, c2), l2 = pack2(lse2, lse2), sc2 = pack2(sc, sc),
-                     dl2 = pack2(delta * sc, delta * sc);
+      const uint64_t c22 = pack2(c2, c2), l2 = pack2(lse2, lse2), sc2 = pack2(sc, sc);
       for (int t = w.first(); t < w.t1; t = w.after(t)) {
         const int keys = w.tile_keys(t), cols = w.tile_cols(t);
         const int rest = keys - part * 32;  // of this warp's columns
         uint32_t on = rest >= 32 ? 0xFFFFFFFFu : rest <= 0 ? 0u : (1u << rest) - 1u;
         if (kMask) on &= bits ? bits[(t * p.kv_box >> 5) + part] : 0u;
+        // (kOne: the warps of a row meet below, where a failed one tells the others.)
         ok = wait(&bars.s_full, count & 1u, kAttnSoftmaxTimeout);
-        if (!ok) break;
+        if (!kOne && !ok) break;
         tc_fence_after();
         const uint32_t ts = tmem + part * 32 + lane_field;
         const uint32_t td = t_dp + (count & 1u) * 128 + part * 32 + lane_field;
-        const bool mine = part * 32 < cols;
+        const bool mine = part * 32 < cols && (!kOne || ok);
         uint32_t s[32];
         if (mine) {
           tmem_ld_x32(ts, s);
@@ -493,9 +499,27 @@ __global__ void __launch_bounds__(kDqThreads, 1)
             s[2 * i + 1] = __float_as_uint(exp2_approx(y));
           }
         }
-        ok = wait(&bars.dp_full[count & 1u], (count >> 1) & 1u, kAttnSoftmaxTimeout);
-        if (!ok) break;
+        ok = ok && wait(&bars.dp_full[count & 1u], (count >> 1) & 1u, kAttnSoftmaxTimeout);
+        if (!kOne && !ok) break;
         tc_fence_after();
+        if constexpr (kOne) {
+          float sum = 0.f;
+          if (mine && ok) {
+            uint32_t dp[32];
+            tmem_ld_x32(td, dp);
+            tmem_wait_ld_x32(dp);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((on >> i) & 1u) sum = fmaf(__uint_as_float(s[i]), __uint_as_float(dp[i]), sum);
+          }
+          float* parts = reinterpret_cast<float*>(smem + p.off_stat);
+          parts[part * 128 + r] = sum;
+          ok = barrier_all(1 + quarter, 128, ok);
+          if (!ok) break;
+          delta = -p.p_unscale * ((parts[r] + parts[128 + r]) + (parts[256 + r] + parts[384 + r]));
+          if (part == 0 && st) st[128 + (token & 127)] = delta;
+        }
+        const uint64_t dl2 = pack2(delta * sc, delta * sc);
         if (mine) {
           uint32_t dp[32], h[16];
           tmem_ld_x32(td, dp);
@@ -526,6 +550,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       }
       if (!ok) break;
       ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      if (kOne) ok = barrier_all(1 + quarter, 128, ok);  // (the sums' parts have been read, too)
       ++items;
       if (!ok) break;
       tc_fence_after();
@@ -1238,12 +1263,12 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
 }
 
-template <typename T, int DP, bool kMask>
+template <typename T, int DP, bool kMask, bool kOne>
 cudaError_t launch_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
   static std::atomic<size_t> configured[kMaxDevices];
-  cudaError_t e = raise_smem(attn_dq_kernel<T, DP, kMask>, configured, smem);
+  cudaError_t e = raise_smem(attn_dq_kernel<T, DP, kMask, kOne>, configured, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dq_kernel<T, DP, kMask>, dim3(grid), dim3(kDqThreads), smem, stream, p);
+  return launch_pdl(attn_dq_kernel<T, DP, kMask, kOne>, dim3(grid), dim3(kDqThreads), smem, stream, p);
 }
 
 template <typename T, int DP, bool kMask>
@@ -1280,7 +1305,9 @@ cudaError_t launch_attn_rows(const AttnBwdParams& p, cudaStream_t stream) {
 
 cudaError_t launch_attn_dq(const AttnBwdParams& p, int grid, size_t smem, cudaStream_t stream) {
   return with_variant(p, [&](auto type, auto wide, auto mask) {
-    return launch_dq<decltype(type), wide() ? 128 : 64, mask()>(p, grid, smem, stream);
+    constexpr int kDp = wide() ? 128 : 64;
+    return p.a.kv_len <= p.kv_box ? launch_dq<decltype(type), kDp, mask(), true>(p, grid, smem, stream)
+                                  : launch_dq<decltype(type), kDp, mask(), false>(p, grid, smem, stream);
   });
 }
 
