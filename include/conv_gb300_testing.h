@@ -12,6 +12,7 @@
 #include <stddef.h>
 
 #include "conv_gb300.h"
+#include "conv_gb300_attention.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -66,6 +67,12 @@ conv_status_t conv_testing_fwd_plan(int n, int h, int w, int c_in, conv_dtype_t 
                                     int s, int c_out, const int stride[2],
                                     const int symmetric_padding[2], int has_residual, int num_sms,
                                     size_t workspace_bytes, int out[14]);
+
+/* Thread blocks that a qk_norm_rope call gives its two tensors on num_sms SMs
+ * (out[0] of q, out[1] of k), and the rows of partial sums that the backward
+ * pass's workspace holds for them, one for each block (out[2]).  Host-only. */
+conv_status_t conv_testing_qk_norm_rope_blocks(const qk_norm_rope_args_t* args, int backward,
+                                               int num_sms, int out[3]);
 
 /* Read the CONV_* tuning overrides from the environment again (the library
  * reads them once, on first use) and invalidate every cached prepared call.

@@ -26,6 +26,7 @@
 #include <cstdint>
 
 #include "../../include/conv_gb300_attention.h"
+#include "../../include/conv_gb300_testing.h"
 #include "attn_internal.h"
 #include "conv_params.h"
 #include "attn_ptx.cuh"
@@ -871,10 +872,31 @@ cudaError_t launch_qn_dtype(int dtype, int v, const QnParams& p, int grid, cudaS
                                   : launch_qn<__half, kBackward>(p, v, grid, stream);
 }
 
-conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, void* workspace,
-                               size_t workspace_bytes, cudaStream_t stream) {
-  if (!args) return CONV_ERR_INVALID_VALUE;
-  const qk_norm_rope_args_t& a = *args;
+// Thread blocks of the two tensors: a warp for every unit where those fit the
+// SMs once, else a share of the blocks in proportion to the units.  They add up
+// to no more than `most`, for which the workspace holds rows of partial sums.
+// (The choice goes by the sum of both tensors' whole blocks: each rounds up by
+// itself, so units that fit may still need a block more than there are.)
+void share_blocks(QnTensor (&t)[2], int most) {
+  long long units = 0, want[2];
+  for (int i = 0; i < 2; ++i) {
+    units += t[i].units;
+    want[i] = (t[i].units + kWarpsQn - 1) / kWarpsQn;
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (t[i].units == 0) continue;
+    const long long share = want[0] + want[1] <= most
+                                ? want[i]
+                                : std::max(1ll, (most - 1ll) * t[i].units / units);
+    t[i].blocks = static_cast<int>(std::min(want[i], share));
+  }
+}
+
+// Rows of partial sums that the backward pass's workspace holds.
+int partial_rows(int sms) { return sms * kBlocksBwd; }
+
+// Checks a call and takes its arguments over; `v`: the elements of a lane's word.
+conv_status_t plan_qk_norm_rope(const qk_norm_rope_args_t& a, bool backward, QnParams* out, int* v) {
   if (a.dtype != CONV_DTYPE_BF16 && a.dtype != CONV_DTYPE_F16) return CONV_ERR_NOT_SUPPORTED;
   if (a.batch < 0 || a.head_dim <= 0 || a.rot_dim < 0 || a.rot_dim > a.head_dim || !(a.eps >= 0.f) ||
       !std::isfinite(a.eps))
@@ -887,22 +909,15 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
   // Halves that split a 16-byte word (rot_dim an odd multiple of 8) take
   // 8-byte words, so that a pair's members sit in whole words (32 lanes at the
   // most, for 256 elements).
-  const int v = !a.adjacent_pairs && a.rot_dim % 16 != 0 ? 4 : 8;
-  const int rot_lanes = (a.rot_dim + 2 * v - 1) / (2 * v);
+  *v = !a.adjacent_pairs && a.rot_dim % 16 != 0 ? 4 : 8;
+  const int rot_lanes = (a.rot_dim + 2 * *v - 1) / (2 * *v);
   const int lanes = a.adjacent_pairs ? (a.head_dim + 15) / 16
-                                     : rot_lanes + (a.head_dim - a.rot_dim + 2 * v - 1) / (2 * v);
-  QnParams p{};
+                                     : rot_lanes + (a.head_dim - a.rot_dim + 2 * *v - 1) / (2 * *v);
+  QnParams& p = *out;
+  p = QnParams{};
   conv_status_t st = take_tensor(a, a.q, backward, &p.t[0]);
   if (st == CONV_OK) st = take_tensor(a, a.k, backward, &p.t[1]);
   if (st != CONV_OK) return st;
-  if (backward) {
-    if (!workspace) return CONV_ERR_INVALID_VALUE;
-    if (misaligned(workspace)) return CONV_ERR_MISALIGNED;
-    if (workspace_bytes < qk_norm_rope_workspace_size(a.head_dim))
-      return CONV_ERR_WORKSPACE_TOO_SMALL;
-  }
-  const int sms = attn_sm_count();
-  if (sms <= 0) return CONV_ERR_CUDA;
   p.cos = a.cos;
   p.sin = a.sin;
   p.head_dim = a.head_dim;
@@ -914,7 +929,11 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
   p.adjacent = a.adjacent_pairs != 0;
   p.eps = a.eps;
   p.inv_d = 1.0f / static_cast<float>(a.head_dim);
-  long long units = 0;
+  return CONV_OK;
+}
+
+// Units and thread blocks of both tensors on `sms` SMs; returns the grid.
+int share_qk_norm_rope(QnParams& p, bool backward, int sms) {
   for (QnTensor& t : p.t) {
     if (!t.x || t.rows == 0) continue;
     // Lanes keep their token where there are tokens for every warp and heads
@@ -931,20 +950,29 @@ conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, v
                      : (t.rows + p.slots * rows_step - 1) / (p.slots * rows_step);
     t.div_heads = make_fast_div(static_cast<uint32_t>(t.heads));
     t.div_length = make_fast_div(static_cast<uint32_t>(t.length));
-    units += t.units;
   }
-  // The grid fills the SMs once; the two tensors share the blocks in
-  // proportion to their units.
-  const long long most = static_cast<long long>(sms) * (backward ? kBlocksBwd : kBlocksFwd);
-  int grid = 0;
-  for (QnTensor& t : p.t) {
-    if (t.units == 0) continue;
-    const long long want = (t.units + kWarpsQn - 1) / kWarpsQn;
-    const long long share =
-        units <= most * kWarpsQn ? want : std::max(1ll, (most - 1) * t.units / units);
-    t.blocks = static_cast<int>(std::min(want, share));
-    grid += t.blocks;
+  // The grid fills the SMs once.
+  share_blocks(p.t, backward ? partial_rows(sms) : sms * kBlocksFwd);
+  return p.t[0].blocks + p.t[1].blocks;
+}
+
+conv_status_t run_qk_norm_rope(const qk_norm_rope_args_t* args, bool backward, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+  if (!args) return CONV_ERR_INVALID_VALUE;
+  const qk_norm_rope_args_t& a = *args;
+  QnParams p;
+  int v = 0;
+  const conv_status_t st = plan_qk_norm_rope(a, backward, &p, &v);
+  if (st != CONV_OK) return st;
+  if (backward) {
+    if (!workspace) return CONV_ERR_INVALID_VALUE;
+    if (misaligned(workspace)) return CONV_ERR_MISALIGNED;
+    if (workspace_bytes < qk_norm_rope_workspace_size(a.head_dim))
+      return CONV_ERR_WORKSPACE_TOO_SMALL;
   }
+  const int sms = attn_sm_count();
+  if (sms <= 0) return CONV_ERR_CUDA;
+  const int grid = share_qk_norm_rope(p, backward, sms);
   if (backward) {
     float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + CONV_STATUS_BYTES);
     p.t[0].partial = part;
@@ -970,7 +998,7 @@ size_t qk_norm_rope_workspace_size(int head_dim) {
   if (head_dim <= 0 || sms <= 0) return 0;
   // One row of partial sums per thread block.
   return CONV_STATUS_BYTES +
-         static_cast<size_t>(sms) * convgb300::kBlocksBwd * head_dim * sizeof(float);
+         static_cast<size_t>(convgb300::partial_rows(sms)) * head_dim * sizeof(float);
 }
 
 conv_status_t qk_norm_rope_fwd(const qk_norm_rope_args_t* args, void* stream) {
@@ -981,6 +1009,20 @@ conv_status_t qk_norm_rope_bwd(const qk_norm_rope_args_t* args, void* workspace,
                                size_t workspace_bytes, void* stream) {
   return convgb300::run_qk_norm_rope(args, true, workspace, workspace_bytes,
                                      static_cast<cudaStream_t>(stream));
+}
+
+conv_status_t conv_testing_qk_norm_rope_blocks(const qk_norm_rope_args_t* args, int backward,
+                                               int num_sms, int out[3]) {
+  using namespace convgb300;
+  QnParams p;
+  int v = 0;
+  const conv_status_t st = plan_qk_norm_rope(*args, backward != 0, &p, &v);
+  if (st != CONV_OK) return st;
+  share_qk_norm_rope(p, backward != 0, num_sms);
+  out[0] = p.t[0].blocks;
+  out[1] = p.t[1].blocks;
+  out[2] = partial_rows(num_sms);
+  return CONV_OK;
 }
 
 }  // extern "C"
