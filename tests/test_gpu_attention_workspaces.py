@@ -44,3 +44,85 @@ def test_norm_backward_keeps_to_its_workspace(size):
         ref = A.NormReference(x[n], w[n], cos, sin, None, 1e-6, False, u, dy[n])
         A.assert_within("d" + n, dx[n], ref.dx, ref.dx_tol)
         A.assert_within("d%s_weight" % n, dw[n], ref.dw, ref.dw_tol)
+
+
+# A stream-K convolution keeps flags and partial tiles in its workspace; what other calls leave
+# there must not be taken for them.
+DEEP = dict(n=2, hw=8, c=1024, f=256)
+
+
+def _deep_conv(ws):
+    """A convolution that the planner runs in stream-K, as (call, output, exact result)."""
+    n, hw, c, f = DEEP["n"], DEEP["hw"], DEEP["c"], DEEP["f"]
+    g = _gen(21)
+    # Small whole numbers: every sum is exact.
+    x = torch.randint(-2, 3, (n, hw, hw, c), generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randint(-1, 2, (3, 3, c, f), generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.empty((n, hw // 2, hw // 2, f), dtype=torch.bfloat16, device=DEV)
+    packed = cg.conv2d_pack_filter(w, filter_is_fcrs=False)
+    want = torch.nn.functional.conv2d(x.double().permute(0, 3, 1, 2), w.double().permute(3, 2, 0, 1),
+                                      stride=2, padding=1).permute(0, 2, 3, 1).to(torch.bfloat16)
+
+    def call():
+        out.fill_(float("nan"))
+        cg.conv2d_fwd_packed(x, packed, out, r=3, s=3, stride=(2, 2), symmetric_padding=(1, 1),
+                             workspace=ws)
+    return call, out, want
+
+
+def _streamk_workspace():
+    return cg.new_workspace(cg.CONV_STATUS_BYTES + cg.conv_streamk_workspace_size(), DEV)
+
+
+@pytest.mark.parametrize("left", [0, 1, 7, 0x7F800000, -1])
+def test_streamk_does_not_take_what_lies_in_its_workspace_for_flags(left):
+    ws = _streamk_workspace()
+    call, out, want = _deep_conv(ws)
+    words = ws.view(torch.int32)
+    for i in range(4):
+        words[cg.CONV_STATUS_BYTES // 4:] = left if i else torch.arange(
+            1, words.numel() - cg.CONV_STATUS_BYTES // 4 + 1, dtype=torch.int32, device=DEV)
+        call()
+        assert cg.conv_check_device_status(ws) == (0, 0)
+        assert torch.equal(out, want)
+
+
+def test_streamk_beside_masked_attention_and_the_norm_in_one_workspace():
+    ws = _streamk_workspace()
+    call, out, want = _deep_conv(ws)
+    g = _gen(22)
+    q, dout = (_normal(g, (1, 100, 2, 64), torch.bfloat16) for _ in range(2))
+    k, v = (_normal(g, (1, 100, 2, 64), torch.bfloat16) for _ in range(2))
+    mask = torch.ones((1, 1, 100, 100), dtype=torch.bool, device=DEV).tril()
+    attended, dq, dk, dv = (torch.empty_like(q) for _ in range(4))
+    lse = torch.empty((1, 2, 100), device=DEV)
+    w, dw = torch.ones(64, dtype=torch.bfloat16, device=DEV), torch.empty(64, device=DEV)
+    ref = A.Reference(q, k, v, mask=mask, dout=dout, u=A.UNIT["bf16"])
+    for _ in range(40):
+        cg.cross_attention_fwd(q, k, v, attended, lse=lse, mask=mask, workspace=ws)
+        call()
+        assert torch.equal(out, want)
+        cg.cross_attention_bwd(dout, q, k, v, attended, lse, dq, dk, dv, mask=mask, workspace=ws)
+        call()
+        assert torch.equal(out, want)
+        cg.qk_norm_rope_bwd(dq, None, q, None, w, None, torch.empty_like(q), None, dw, None, workspace=ws)
+        call()
+        assert torch.equal(out, want)
+    assert cg.conv_check_device_status(ws) == (0, 0)
+    A.assert_within("dq", dq, ref.dq, ref.dq_tol)
+
+
+def test_streamk_in_a_graph_that_is_replayed():
+    ws = _streamk_workspace()
+    call, out, want = _deep_conv(ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(5):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert cg.conv_check_device_status(ws) == (0, 0)

@@ -22,7 +22,9 @@
 
 #include "../../include/conv_gb300.h"
 #include "../../include/conv_gb300_testing.h"
+#include "attn_internal.h"
 #include "conv_internal.h"
+#include "ptx.cuh"
 
 using namespace convgb300;
 
@@ -1710,17 +1712,14 @@ conv_status_t run_pack(const Prepared& pr, cudaStream_t stream) {
   return CONV_OK;
 }
 
-// Stream-K flags hold the value of the launch that raised them: every launch
-// takes a new value (never 0, the value of a fresh workspace), so flags left
-// by an earlier launch -- finished or stopped by a timeout -- never match.
-std::atomic<uint32_t> g_sk_epoch{0};
-
-uint32_t next_sk_epoch() {
-  uint32_t e;
-  do {
-    e = g_sk_epoch.fetch_add(1, std::memory_order_relaxed) + 1;
-  } while (e == 0);
-  return e;
+// Clears a stream-K launch's flags.  Whatever used the workspace before (an
+// earlier launch, another call's packed filter, mask bits or partial sums, a
+// replay of the same graph) may have left any value there, so no value of a
+// flag could tell this launch's partial tiles from what was there.
+__global__ void __launch_bounds__(512) sk_clear_kernel(uint4* flags, int n) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) flags[i] = make_uint4(0, 0, 0, 0);
 }
 
 conv_status_t launch_prepared(const Prepared& pr, cudaStream_t stream) {
@@ -1733,16 +1732,12 @@ conv_status_t launch_prepared(const Prepared& pr, cudaStream_t stream) {
     return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
   }
   for (int i = 0; i < pr.n_plans; ++i) {
-    if (pr.pl[i].kp.streamk) {
-      // The prepared plan is shared and immutable: the launch's flag value
-      // goes into a copy.
-      thread_local Plan sk_plan;
-      sk_plan = pr.pl[i];
-      sk_plan.kp.sk_epoch = next_sk_epoch();
-      st = launch_plan(sk_plan, stream);
-    } else {
-      st = launch_plan(pr.pl[i], stream);
-    }
+    const ConvKernelParams& kp = pr.pl[i].kp;
+    if (kp.streamk && kp.total_tiles > 0 &&
+        launch_pdl(sk_clear_kernel, dim3(1), dim3(512), 0, stream, reinterpret_cast<uint4*>(kp.sk_flags),
+                   static_cast<int>(sk_flag_bytes(pr.pl[i].grid) / sizeof(uint4))) != cudaSuccess)
+      return CONV_ERR_CUDA;
+    st = launch_plan(pr.pl[i], stream);
     if (st != CONV_OK) return st;
   }
   return CONV_OK;

@@ -197,7 +197,7 @@ __device__ __forceinline__ bool sk_wait_partials(const ConvKernelParams& p, cons
   for (long long pos = first + w.kb1; pos < end;) {
     const int c = sk_owner(p, pos, nctas);
     const unsigned int* flag = p.sk_flags + static_cast<size_t>(c) * kEpilogueWarps + ew;
-    while (ld_acquire_gpu(flag) != p.sk_epoch) {
+    while (ld_acquire_gpu(flag) == 0u) {
       if (*abort_flag) return false;
       if (cycle_count() - t0 > limit) {
         *abort_flag = 1;
@@ -273,12 +273,12 @@ __device__ __forceinline__ void tmem_add_groups(uint32_t taddr, int ngroups,
   }
 }
 
-// Contributor: after the warp's partial stores, publish them (flag = epoch).
+// Contributor: after the warp's partial stores, publish them.
 __device__ __forceinline__ void sk_publish(const ConvKernelParams& p, int cta, int ew, int lane) {
   __threadfence();
   __syncwarp();
   if (lane == 0 && p.fault_mode != 2)  // (fault_mode 2, a test hook: never publish)
-    st_release_gpu(p.sk_flags + static_cast<size_t>(cta) * kEpilogueWarps + ew, p.sk_epoch);
+    st_release_gpu(p.sk_flags + static_cast<size_t>(cta) * kEpilogueWarps + ew, 1u);
 }
 
 // Image and first output row of row-window tile t.

@@ -172,15 +172,14 @@ struct ConvKernelParams {  // aligned like CUtensorMap (64 B or more)
   // contiguous shares, one per CTA, and each share into work items at tile
   // boundaries.  A CTA whose share starts inside a tile writes that item's
   // fp32 accumulators to its partial slot and raises its epilogue warps'
-  // flags to sk_epoch; the CTA holding the tile's first k-block adds every
+  // flags; the CTA holding the tile's first k-block adds every
   // such partial and runs the epilogue.
   int streamk;
   long long sk_iters;                    // iterations in all (< 2^31)
   long long sk_iter_start[kMaxPhases + 1];  // first iteration of each phase
   int sk_kpt[kMaxPhases];                // k-blocks per tile of each phase (> 0)
   FastDiv sk_div_kpt[kMaxPhases];
-  uint32_t sk_epoch;                     // this launch's flag value (never 0)
-  unsigned int* sk_flags;                // [CTA][epilogue warp]
+  unsigned int* sk_flags;                // [CTA][epilogue warp]: 0, then 1
   float* sk_partials;                    // [CTA][m_halves * bn / 16][128 rows][16]
   uint32_t sk_slot_floats;               // floats per CTA slot
 
