@@ -1,0 +1,87 @@
+"""float16 gradients where rows of dout differ by large factors.  Scaling a row of dout by a power of
+two scales its dq by the same (nothing is lost as long as both stay within the type's normal numbers),
+and one request's or key head's gradients do not depend on another's size."""
+import pytest
+import torch
+
+from tests import _attention as A
+from tests.test_gpu_attention import DEV, _compare, _gen, _make_mask, _normal, _run
+
+pytestmark = pytest.mark.gpu
+DT = torch.float16
+STEP = 2.0 ** -24        # of float16's subnormal numbers
+
+CASES = [  # b, lq, lk, h, hkv, d, mask
+    (1, 200, 2048, 4, 2, 128, "none"),
+    (2, 300, 700, 2, 2, 64, "lengths"),
+    (1, 333, 900, 6, 2, 80, "rows"),
+    (2, 130, 100, 3, 3, 96, "none"),       # one tile of keys
+    (2, 150, 128, 4, 2, 40, "heads"),
+    (2, 400, 77, 4, 4, 40, "none"),        # one tile of keys, narrow heads, no mask
+    (3, 300, 128, 8, 2, 64, "lengths"),
+]
+
+
+def _tensors(case, seed):
+    b, lq, lk, h, hkv, d, kind = case
+    g = _gen(seed)
+    # Keys four times as large and queries a quarter: larger dq for the same scores.
+    q, k = _normal(g, (b, lq, h, d), DT, 0.25), _normal(g, (b, lk, hkv, d), DT, 4.0)
+    v = _normal(g, (b, lk, hkv, d), DT)
+    # Multiples of 2^-6, so that small powers of two scale them exactly.
+    dout = (torch.randint(-128, 129, (b, lq, h, d), generator=g, device=DEV) / 64).to(DT)
+    n, m = _make_mask(kind, g, b, h, lq, lk)
+    return g, q, k, v, dout, dict(kv_lengths=n, mask=m)
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c)))
+def test_a_row_of_dout_scales_its_dq(case):
+    g, q, k, v, dout, kw = _tensors(case, 31)
+    b, lq, _, h, _, _, _ = case
+    power = torch.randint(-8, -5, (b, lq, h, 1), generator=g, device=DEV)
+    power[:, 7::50] = 8
+    power[:, 5::60, ::2] = 3
+    scale = torch.exp2(power.float())
+    scaled = (dout.float() * scale).to(DT)
+    assert torch.equal(scaled.float(), dout.float() * scale)
+    base = _run(q, k, v, dout, **kw)[2].float()
+    got = _run(q, k, v, scaled, **kw)[2].float()
+    off = (got - base * scale).abs()
+    # Subnormal results are rounded by steps of 2^-24, twice.
+    assert (off <= torch.where((base * scale).abs() < 2.0 ** -14, STEP, 0.0)).all(), float(
+        (off / (base * scale).abs().clamp(min=STEP)).max())
+
+
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** -6])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c)))
+def test_gradients_do_not_depend_on_other_requests_and_key_heads(case, size):
+    b, lq, lk, h, hkv, d, kind = case
+    g, q, k, v, dout, kw = _tensors(case, 32)
+    group = h // hkv
+    factor = torch.ones((b, 1, hkv, 1), device=DEV)
+    factor[:, :, 1::2] = size
+    factor[1:] = size
+    factor = factor * torch.ones((b, 1, hkv, 1), device=DEV)
+    scaled = (dout.float() * factor.repeat_interleave(group, dim=2)).to(DT)
+    base, got = _run(q, k, v, dout, **kw), _run(q, k, v, scaled, **kw)
+    same_k = (factor == 1).expand(b, lk, hkv, d)
+    same_q = (factor == 1).repeat_interleave(group, dim=2).expand(b, lq, h, d)
+    assert torch.equal(base[2][same_q], got[2][same_q])
+    assert torch.equal(base[3][same_k], got[3][same_k])
+    assert torch.equal(base[4][same_k], got[4][same_k])
+    # Values' sizes do not matter to other key heads either.
+    big = torch.where(factor == 1, v.float(), v.float() * 2.0 ** 8).to(DT)
+    base, got = _run(q, k, v, dout, **kw), _run(q, k, big, dout, **kw)
+    assert torch.equal(base[2][same_q], got[2][same_q])
+    assert torch.equal(base[3][same_k], got[3][same_k])
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, c)))
+def test_rows_of_very_different_size_within_bounds(case):
+    g, q, k, v, dout, kw = _tensors(case, 33)
+    b, lq, lk, h, hkv, d, kind = case
+    power = torch.randint(-9, -5, (b, lq, h, 1), generator=g, device=DEV)
+    power[:, 3::40] = 7
+    dout = (dout.float() * torch.exp2(power.float())).to(DT)
+    got = _run(q, k, v, dout, **kw)
+    _compare(got, A.Reference(q, k, v, dout=dout, u=A.UNIT["f16"], **kw))

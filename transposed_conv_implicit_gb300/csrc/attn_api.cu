@@ -134,13 +134,21 @@ FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
 }
 
 // ------------------------------------------------------------------ backward plan
+// Rows that a warp of the rows kernel reads side by side: 16 bytes a lane, a power
+// of two of lanes a row.
+int row_slots(int head_dim) {
+  int width = 1;
+  while (width < head_dim / 8) width <<= 1;
+  return 32 / width;
+}
+
 struct BwdPlan {
   int q_tiles, item_steps, kv_tiles;
   int q_grid, kv_grid;     // CTAs of the dq and the dk, dv kernel
   bool q_whole, kv_whole;  // no item is cut between CTAs
-  bool norms;              // fp16: ds is scaled by the rows' norms
+  int per_tile, key_groups;  // neighbouring rows whose norms are joined: of a tile of queries, of the keys
   bool brief;              // one tile of keys, narrow heads, no mask: one kernel
-  size_t stat_bytes, norm_bytes, part_q_bytes, part_kv_bytes;
+  size_t stat_bytes, row_norm_bytes, value_norm_bytes, part_q_bytes, part_kv_bytes;
 };
 
 BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
@@ -163,11 +171,15 @@ BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
   };
   p.q_whole = whole(heads * f.row_tiles, nt);
   p.kv_whole = whole(heads * p.kv_tiles, p.item_steps) && !(f.one && a.q_len > 0);
-  p.norms = a.dtype == CONV_DTYPE_F16;
   p.brief = f.one && a.q_len > 0;
   if (p.brief) p.kv_grid = static_cast<int>(std::min<long long>(heads * p.item_steps, sms));
-  p.stat_bytes = static_cast<size_t>(a.batch) * a.heads * p.q_tiles * 256 * sizeof(float);
-  p.norm_bytes = 2 * kAttnNormBlocks * sizeof(float);  // (of one size for both types)
+  const int group = kAttnRowUnroll * row_slots(a.head_dim);
+  p.per_tile = kAttnRows / group;
+  p.key_groups = (a.kv_len + group - 1) / group;
+  // (Of one size for both types; bf16 has no use for the norms.)
+  p.stat_bytes = static_cast<size_t>(a.batch) * a.heads * p.q_tiles * 384 * sizeof(float);
+  p.row_norm_bytes = static_cast<size_t>(a.batch) * a.heads * p.q_tiles * p.per_tile * sizeof(float);
+  p.value_norm_bytes = static_cast<size_t>(heads) * p.key_groups * sizeof(float);
   const size_t tile = static_cast<size_t>(kAttnRows) * 128 * sizeof(float);
   p.part_q_bytes = nt > 1 && !p.q_whole ? 2 * tile * p.q_grid : 0;
   p.part_kv_bytes = p.item_steps > 1 && !p.kv_whole ? 4 * tile * p.kv_grid : 0;
@@ -176,7 +188,7 @@ BwdPlan plan_bwd(const cross_attention_args_t& a, const FwdPlan& f, int sms) {
 
 struct Layout {
   MaskShape mask;
-  size_t mask_at, any_at, part_at, stat_at, norm_at, part_q_at, part_kv_at, total;
+  size_t mask_at, any_at, part_at, stat_at, row_norm_at, value_norm_at, part_q_at, part_kv_at, total;
 };
 
 Layout layout(const cross_attention_args_t& a, bool backward, const FwdPlan& f, const BwdPlan& g) {
@@ -190,8 +202,9 @@ Layout layout(const cross_attention_args_t& a, bool backward, const FwdPlan& f, 
     return l;
   }
   l.stat_at = l.part_at;
-  l.norm_at = round_up(l.stat_at + g.stat_bytes, 256);
-  l.part_q_at = round_up(l.norm_at + g.norm_bytes, 256);
+  l.row_norm_at = round_up(l.stat_at + g.stat_bytes, 256);
+  l.value_norm_at = round_up(l.row_norm_at + g.row_norm_bytes, 256);
+  l.part_q_at = round_up(l.value_norm_at + g.value_norm_bytes, 256);
   l.part_kv_at = round_up(l.part_q_at + g.part_q_bytes, 256);
   l.total = round_up(l.part_kv_at + g.part_kv_bytes, 256);
   return l;
@@ -316,10 +329,14 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   p.last_cols = (s.q_len - std::max(0, g.q_tiles - 1) * kAttnRows + 15) / 16 * 16;
   p.item_rows = static_cast<long long>(s.kv_heads) * f.row_tiles;
   p.scale_log2 = s.scale * 1.44269504088896341f;
-  p.p_shift = g.norms ? 15.f : 0.f;
-  p.p_unscale = g.norms ? 1.f / 32768.f : 1.f;
+  const bool half = s.dtype == CONV_DTYPE_F16;
+  p.p_shift = half ? 15.f : 0.f;
+  p.p_unscale = half ? 1.f / 32768.f : 1.f;
   p.stats = reinterpret_cast<float*>(ws + l.stat_at);
-  p.norms = g.norms ? reinterpret_cast<float*>(ws + l.norm_at) : nullptr;
+  p.stat_pitch = half ? 384 : 256;
+  p.row_norms = reinterpret_cast<float*>(ws + l.row_norm_at);
+  p.value_norms = reinterpret_cast<float*>(ws + l.value_norm_at);
+  p.key_groups = g.key_groups;
   p.part_q = reinterpret_cast<float*>(ws + l.part_q_at);
   p.part_kv = reinterpret_cast<float*>(ws + l.part_kv_at);
   p.status = reinterpret_cast<unsigned int*>(ws);
@@ -331,23 +348,20 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   if (queries && keys) {
     // Row statistics.
     p.div_heads = make_fast_div(static_cast<uint32_t>(s.heads));
-    int width = 1;  // lanes of a row
-    while (width < s.head_dim / 8) width <<= 1;
-    p.row_slots = 32 / width;
-    const int group = kAttnRowUnroll * p.row_slots;
-    const int groups = g.q_tiles * kAttnRows / group, key_groups = (s.kv_len + group - 1) / group;
+    p.row_slots = row_slots(s.head_dim);
+    const int groups = g.q_tiles * g.per_tile;
     p.div_groups = make_fast_div(static_cast<uint32_t>(groups));
     p.div_kv_heads = make_fast_div(static_cast<uint32_t>(s.kv_heads));
-    p.div_key_groups = make_fast_div(static_cast<uint32_t>(key_groups));
+    p.div_key_groups = make_fast_div(static_cast<uint32_t>(g.key_groups));
     const long long units = static_cast<long long>(s.batch) * s.heads * groups;
-    p.row_blocks = static_cast<int>(std::min<long long>(kAttnNormBlocks, (units + 7) / 8));
-    const long long value_units = static_cast<long long>(s.batch) * s.kv_heads * key_groups;
+    p.row_blocks = static_cast<int>(std::min<long long>(kAttnRowBlocks, (units + 7) / 8));
+    const long long value_units = static_cast<long long>(s.batch) * s.kv_heads * g.key_groups;
     p.value_blocks =
-        g.norms ? static_cast<int>(std::min<long long>(kAttnNormBlocks, (value_units + 7) / 8)) : 0;
+        half ? static_cast<int>(std::min<long long>(kAttnRowBlocks, (value_units + 7) / 8)) : 0;
     p.q_whole = g.q_whole;
     p.kv_whole = g.kv_whole;
     // (Short keys: delta is summed beside the scores; fp16 still wants the norms.)
-    if ((!g.brief || g.norms) && launch_attn_rows(p, stream) != cudaSuccess) return CONV_ERR_CUDA;
+    if ((!g.brief || half) && launch_attn_rows(p, stream) != cudaSuccess) return CONV_ERR_CUDA;
     if (g.brief) {
       conv_status_t st = encode_maps(&p, s, 1, p.q_box, f.kv_box);
       if (st == CONV_OK) st = encode_map(&p.map_dq, s.dq, s, s.heads, s.q_len, s.dqs, 1, p.q_box);

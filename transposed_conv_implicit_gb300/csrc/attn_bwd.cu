@@ -33,9 +33,11 @@
 // memory before a product sums over them.
 //
 // p and ds are rounded to the inputs' type.  In fp16 both are scaled by
-// powers of two first: p <= 1 by 2^15, and ds by the largest power that
-// |ds| <= 2 max|do| max|v| allows, so that neither leaves fp16's range; the
-// results are scaled back in fp32.
+// powers of two first: p <= 1 by 2^15, and ds by what the norms of do and v
+// allow, for dq row by row and for dk by shares of a key head's queries
+// (attn_common.cuh); the results are scaled back in fp32.  (With one scale for
+// the whole call, rows of do 2^16 smaller than the largest lost 0.4 % of dq at
+// 2048 keys.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -82,12 +84,12 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y) {
 // saved (one tile: the dq kernel sums it and puts it in).
 // stats[b][h][token tile][2][128]: minus lse in log2 units, plus p_shift (-inf
 // for queries without keys and past the end, which makes p zero), and minus
-// delta: as the products' sums take them.  With norms: the
-// largest |do| row of each block, then (kAttnNormBlocks blocks on) |v| row, both
-// squared; rows that take no part are left out.
+// delta: as the products' sums take them.  In fp16 also |do|^2, and the largest
+// ones of every warp's rows of do and of v.  Rows of do without keys count as
+// zeros, and so do rows that are not finite: their gradients are not, either.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnBwdParams p) {
-  __shared__ float most[8];
+  constexpr bool kNorms = std::is_same<T, __half>::value;
   const AttnShape& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // Power-of-two lanes per row, 16 bytes each; a warp takes kAttnRowUnroll x slots
@@ -97,20 +99,19 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
   const int width = 32 / p.row_slots;
   const int at = lane & (width - 1), slot = lane / width;
   const int group = kAttnRowUnroll * p.row_slots;
-  float norm = 0.f;
   grid_dependency_wait();
   grid_launch_dependents();
   const bool values = blockIdx.x >= static_cast<unsigned>(p.row_blocks);
   const int block = values ? blockIdx.x - p.row_blocks : blockIdx.x;
   const int blocks = values ? gridDim.x - p.row_blocks : p.row_blocks;
   const int heads = values ? a.kv_heads : a.heads;
-  const int groups = values ? (a.kv_len + group - 1) / group : p.q_tiles * kAttnRows / group;
+  const int groups = values ? p.key_groups : p.q_tiles * kAttnRows / group;
   const FastDiv div_heads = values ? p.div_kv_heads : p.div_heads;
   const FastDiv div_groups = values ? p.div_key_groups : p.div_groups;
   const int units = groups * heads * a.batch;  // heads innermost, then tokens
   for (int unit = block * 8 + warp; unit < units; unit += blocks * 8) {
     const int bt = fast_div(unit, div_heads), h = unit - bt * heads;
-    const int b = fast_div(bt, div_groups), t0 = (bt - b * groups) * group + slot;
+    const int b = fast_div(bt, div_groups), part = bt - b * groups, t0 = part * group + slot;
     const int length = values ? valid_keys(a, b) : a.q_len;
     const long long row0 = (static_cast<long long>(b) * a.heads + h) * a.q_len;
     uint4 x[kAttnRowUnroll], y[kAttnRowUnroll];
@@ -137,35 +138,34 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
 #pragma unroll
     for (int u = 0; u < kAttnRowUnroll; ++u) {
       dot[u] = dot8<T>(x[u], y[u]);
-      sq[u] = p.norms ? dot8<T>(x[u], x[u]) : 0.f;
+      sq[u] = kNorms ? dot8<T>(x[u], x[u]) : 0.f;
     }
     for (int o = width >> 1; o; o >>= 1)
 #pragma unroll
       for (int u = 0; u < kAttnRowUnroll; ++u) {
         dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], o);
-        if (p.norms) sq[u] += __shfl_xor_sync(0xFFFFFFFFu, sq[u], o);
+        if (kNorms) sq[u] += __shfl_xor_sync(0xFFFFFFFFu, sq[u], o);
       }
-    if (at != 0) continue;
+    float norm = 0.f;
 #pragma unroll
     for (int u = 0; u < kAttnRowUnroll; ++u) {
       const int t = t0 + u * p.row_slots;
-      if (!values) {
+      if (!(sq[u] < INFINITY)) sq[u] = 0.f;  // (NaN compares false)
+      if (at == 0 && !values) {
         const float lse2 = lse[u] == -INFINITY ? lse[u] : p.p_shift - lse[u] * kLog2e;
         if (lse2 == -INFINITY) dot[u] = sq[u] = 0.f;
-        float* st = p.stats + ((static_cast<long long>(b) * a.heads + h) * p.q_tiles + (t >> 7)) * 256;
+        float* st = p.stats + ((static_cast<long long>(b) * a.heads + h) * p.q_tiles + (t >> 7)) * p.stat_pitch;
         st[t & 127] = lse2;
         st[128 + (t & 127)] = -dot[u];
+        if (kNorms) st[256 + (t & 127)] = sq[u];
       }
-      if (sq[u] < INFINITY) norm = fmaxf(norm, sq[u]);  // (NaN compares false)
+      if (at == 0) norm = fmaxf(norm, sq[u]);
     }
-  }
-  if (!p.norms) return;
-  for (int o = 16; o; o >>= 1) norm = fmaxf(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
-  if (lane == 0) most[warp] = norm;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < 8; ++i) norm = fmaxf(norm, most[i]);
-    p.norms[(values ? kAttnNormBlocks : 0) + block] = norm;
+    if (kNorms) {
+      norm = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(norm)));
+      if (lane == 0)
+        (values ? p.value_norms : p.row_norms)[(static_cast<long long>(b) * heads + h) * groups + part] = norm;
+    }
   }
 }
 
@@ -181,7 +181,6 @@ struct Bars {
   uint64_t dp_full[2], ds_full[2];
   uint64_t drain[2];
   SplitStart start;
-  float most[2][32];  // the norms that ds's scale is made from
   uint32_t tmem;
   int abort_flag;
 };
@@ -254,7 +253,6 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const SplitStart st = split_rows(p, lane);
     if (lane == 0) bars.start = st;
   }
-  gather_norms(p, bars.most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -443,32 +441,39 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     // Four warps share a quarter of the lanes; each takes 32 of the keys.
     const int part = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    // (p is held times 2^p_shift here too; ds's scale takes it out.)
-    const float scale_ds = ds_scale(p, bars.most, lane);
-    const float c2 = p.scale_log2, sc = scale_ds * p.p_unscale;
+    const float c2 = p.scale_log2;
     const int d = p.a.head_dim;
     const int row_token = p.tile_heads > 1 ? r / p.tile_heads : r;
     const int row_head = p.tile_heads > 1 ? r - row_token * p.tile_heads : 0;
     uint32_t count = 0, items = 0;
     bool ok = true;
+    float values = 0.f;  // fp16: the largest |v|^2 of the key head of (of_b, of_hk)
+    int of_b = -1, of_hk = -1;
     for (Walk<true, kMask, AttnBwdParams> w(p, start); ok && w.live; w.next()) {
+      if (!kBf16 && (w.b != of_b || w.hk != of_hk)) {
+        of_b = w.b;
+        of_hk = w.hk;
+        values = largest_value(p, of_b, of_hk, lane);
+      }
       int token, head;
       w.place(0, &token, &head);
       token += row_token;
       head += row_head;
       const bool row_ok = row_token < p.tile_tokens && token < p.a.q_len;
-      float lse2 = -INFINITY, delta = 0.f;  // (both negated)
+      float lse2 = -INFINITY, delta = 0.f, norm = 0.f;  // (the first two negated)
       const uint32_t* bits = nullptr;
       float* st = nullptr;
       if (row_ok) {
-        st = p.stats +
-                          ((static_cast<long long>(w.b) * p.a.heads + head) * p.q_tiles + (token >> 7)) * 256;
+        st = p.stats + ((static_cast<long long>(w.b) * p.a.heads + head) * p.q_tiles + (token >> 7)) * p.stat_pitch;
         lse2 = st[token & 127];
         if (!kOne) delta = st[128 + (token & 127)];
+        if (!kBf16) norm = st[256 + (token & 127)];
         if (kMask)
           bits = p.a.mask_bits +
                  (w.b * p.a.mask_b + head * p.a.mask_h + token * p.a.mask_q) * p.a.mask_words;
       }
+      // (p is held times 2^p_shift here too; ds's scale takes it out.)
+      const float scale_ds = kBf16 ? 1.f : ds_scale(norm, values), sc = scale_ds * p.p_unscale;
       const uint64_t c22 = pack2(c2, c2), l2 = pack2(lse2, lse2), sc2 = pack2(sc, sc);
       for (int t = w.first(); t < w.t1; t = w.after(t)) {
         const int keys = w.tile_keys(t), cols = w.tile_cols(t);
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                            head * p.a.dqs[2] + col,
                        v, d - col, f);
           else
-            store_cols_f32(p.part_q + (slot * kAttnRows + r) * 128 + col, v, d - col);
+            store_cols_f32(p.part_q + (slot * kAttnRows + r) * 128 + col, v, d - col, 1.f / scale_ds);
         }
       }
       tc_fence_before();
@@ -752,7 +757,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                                       [&](int b) { return key_steps(p, b); });
     if (lane == 0) bars.start = st;
   }
-  gather_norms(p, bars.most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -810,7 +814,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           mbar_arrive_expect_tx_if(lead, sbar, 1024u);
           if (lead)
             bulk_load(smem_u32(smem + p.off_stat) + ss * 1024u,
-                      p.stats + ((static_cast<long long>(w.b) * p.a.heads + h) * p.q_tiles + qt) * 256,
+                      p.stats + ((static_cast<long long>(w.b) * p.a.heads + h) * p.q_tiles + qt) * p.stat_pitch,
                       1024u, sbar);
           __syncwarp();
           ++nst;
@@ -993,9 +997,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     // One thread per key and 32 of the queries.
     const int part = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    const float scale_ds = ds_scale(p, bars.most, lane);
-    const float c2 = p.scale_log2, sc = scale_ds * p.p_unscale;
-    const uint64_t c22 = pack2(c2, c2), sc2 = pack2(sc, sc);
+    const float c2 = p.scale_log2;
+    const uint64_t c22 = pack2(c2, c2);
     const int d = p.a.head_dim;
     const uint32_t ts = t_s + part * 32 + lane_field, td = t_dp + part * 32 + lane_field;
     uint32_t* mask_tile = reinterpret_cast<uint32_t*>(smem + p.off_mask);
@@ -1005,6 +1008,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       const bool key_ok = r < w.keys();
       const bool keys_whole = w.keys() == kAttnRows;
       bool told = false;  // of a failed wait, at a barrier
+      const float scale_ds = kBf16 ? 1.f
+                                   : ds_scale(largest_row(p, w.b, w.hk, w.i0, w.i1, lane),
+                                              largest_value(p, w.b, w.hk, lane));
+      const float sc = scale_ds * p.p_unscale;
+      const uint64_t sc2 = pack2(sc, sc);
       for (w.first(); w.i < w.i1; w.go(w.after())) {
         const bool mine = part * 32 < w.cols();
         uint32_t on = 0xFFFFFFFFu;
@@ -1133,7 +1141,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           if (whole) {
             if (j < p.a.kv_len) store_cols(dst + c, v, d - c, f);
           } else {
-            store_cols_f32(p.part_kv + ((slot * 2 + which) * kAttnRows + r) * 128 + c, v, d - c);
+            store_cols_f32(p.part_kv + ((slot * 2 + which) * kAttnRows + r) * 128 + c, v, d - c,
+                           which ? 1.f / scale_ds : p.p_unscale);
           }
         }
       }
@@ -1160,13 +1169,11 @@ __global__ void __launch_bounds__(kJoinThreads)
     attn_bwd_join_kernel(const __grid_constant__ AttnBwdParams p, int q_ctas, int kv_ctas,
                          long long q_blocks) {
   __shared__ JoinSlots join;
-  __shared__ float most[2][32];
   const AttnShape& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = lane * 4;
   const int r0 = blockIdx.y * kJoinRows + warp * kJoinUnroll;
   grid_dependency_wait();
   grid_launch_dependents();
-  gather_norms(p, most);
   long long before, total;
   if (blockIdx.x < q_blocks) {
     const int b = static_cast<int>(blockIdx.x / p.item_rows);
@@ -1189,7 +1196,6 @@ __global__ void __launch_bounds__(kJoinThreads)
       head0 = hk * a.group + hg;
       rows = min(kAttnRows, a.q_len - token0);
     }
-    const float factor = a.scale / ds_scale(p, most, lane);
     if (r0 >= rows || d0 >= a.head_dim) return;
     float4 acc[kJoinUnroll];
 #pragma unroll
@@ -1210,8 +1216,8 @@ __global__ void __launch_bounds__(kJoinThreads)
       const int token = token0 + dt, head = p.tile_heads > 1 ? head0 + r - dt * p.tile_heads : head0;
       *reinterpret_cast<uint2*>(static_cast<T*>(a.dq) + b * a.dqs[0] + token * a.dqs[1] +
                                 head * a.dqs[2] + d0) =
-          make_uint2(round2<T>(acc[u].x * factor, acc[u].y * factor),
-                     round2<T>(acc[u].z * factor, acc[u].w * factor));
+          make_uint2(round2<T>(acc[u].x * a.scale, acc[u].y * a.scale),
+                     round2<T>(acc[u].z * a.scale, acc[u].w * a.scale));
     }
     return;
   }
@@ -1231,10 +1237,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                p.item_steps);
     shares = join.count;
     if (shares == 0) return;
-  } else {
-    __syncthreads();  // (the norms)
   }
-  const float factor = a.scale / ds_scale(p, most, lane);
   if (r0 >= rows || d0 >= a.head_dim) return;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -1250,7 +1253,7 @@ __global__ void __launch_bounds__(kJoinThreads)
             ((static_cast<long long>(join.slots[c]) * 2 + half) * kAttnRows + min(r0 + u, rows - 1)) * 128 + d0);
         acc[u].x += v.x; acc[u].y += v.y; acc[u].z += v.z; acc[u].w += v.w;
       }
-    const float f = half ? factor : p.p_unscale;
+    const float f = half ? a.scale : 1.f;
 #pragma unroll
     for (int u = 0; u < kJoinUnroll; ++u) {
       if (r0 + u >= rows) break;

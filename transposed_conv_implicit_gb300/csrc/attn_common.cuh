@@ -340,36 +340,37 @@ struct Walk {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
-// The largest norms of the rows kernel's blocks: a block of whole warps gathers
-// its warps' shares in `most`, which ds_scale joins after a barrier.
-__device__ __forceinline__ void gather_norms(const AttnBwdParams& p, float (*most)[32]) {
-  if (!p.norms) return;
-  float x = 0.f, y = 0.f;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < p.row_blocks; i += blockDim.x) x = fmaxf(x, p.norms[i]);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < p.value_blocks; i += blockDim.x) y = fmaxf(y, p.norms[kAttnNormBlocks + i]);
-  // (Squares: as bits they are in order.)
-  x = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));
-  y = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y)));
-  if ((threadIdx.x & 31) == 0) {
-    most[0][threadIdx.x >> 5] = x;
-    most[1][threadIdx.x >> 5] = y;
-  }
+// fp16: ds is rounded after a scaling by a power of two, so that it does not
+// leave the type's range on either side.  |ds_ij| <= 2 |do_i| max |v|, over the
+// values of the request's key head.  dq_i sums over the keys only: every query
+// has a scale of its own.  dk sums over the queries: one scale for a thread
+// block's share of a key head's queries, taken out again before the shares meet.
+//
+// The largest of n squares, 0 without any.  One warp.
+__device__ __forceinline__ float largest(const float* v, int n, int lane) {
+  float x = 0.f;
+#pragma unroll 8
+  for (int i = lane; i < n; i += 32) x = fmaxf(x, v[i]);
+  return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(x)));  // (as bits they are in order)
 }
-
-// The power of two that ds is scaled by: |ds| 2^k <= 2^15.  One warp.
-__device__ __forceinline__ float ds_scale(const AttnBwdParams& p, const float (*most)[32], int lane) {
-  if (!p.norms) return 1.f;
-  const bool in = lane < static_cast<int>(blockDim.x >> 5);
-  const float x = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, in ? __float_as_uint(most[0][lane]) : 0u));
-  const float y = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, in ? __float_as_uint(most[1][lane]) : 0u));
-  // 2 |do| |v| < 2^(1 + ceil exponents); both norms in fp16's range, so k is
-  // within +-60.
+// The largest |v|^2 of a request's key head, and |do|^2 of its queries' steps
+// [i0, i1) (tiles of 128 tokens, over the query heads that share it).
+__device__ __forceinline__ float largest_value(const AttnBwdParams& p, int b, int hk, int lane) {
+  return largest(p.value_norms + (static_cast<long long>(b) * p.a.kv_heads + hk) * p.key_groups,
+                 p.key_groups, lane);
+}
+__device__ __forceinline__ float largest_row(const AttnBwdParams& p, int b, int hk, int i0, int i1, int lane) {
+  const int per = kAttnRows / (kAttnRowUnroll * p.row_slots);  // entries of a tile
+  return largest(p.row_norms + ((static_cast<long long>(b) * p.a.heads + hk * p.a.group) * p.q_tiles + i0) * per,
+                 (i1 - i0) * per, lane);
+}
+// The power of two for |do|^2 <= x and |v|^2 <= y: |ds| 2^k <= 2^15.
+__device__ __forceinline__ float ds_scale(float x, float y) {
+  // 2 |do| |v| < 2^e; both norms in fp16's range, so k is within +-60.
   const float bound = 2.f * sqrtf(x) * sqrtf(y);
   if (!(bound > 0.f)) return 1.f;
   int e;
-  frexpf(bound, &e);  // bound < 2^e
+  frexpf(bound, &e);
   return ldexpf(1.f, max(-60, min(60, 14 - e)));
 }
 
@@ -417,10 +418,13 @@ __device__ __forceinline__ void store_cols(T* dst, const uint32_t* v, int n, flo
     }
   }
 }
-__device__ __forceinline__ void store_cols_f32(float* dst, const uint32_t* v, int n) {
+__device__ __forceinline__ void store_cols_f32(float* dst, const uint32_t* v, int n, float f) {
 #pragma unroll
   for (int i = 0; i < 32; i += 4)
-    if (i < n) *reinterpret_cast<uint4*>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    if (i < n)
+      *reinterpret_cast<float4*>(dst + i) =
+          make_float4(__uint_as_float(v[i]) * f, __uint_as_float(v[i + 1]) * f,
+                      __uint_as_float(v[i + 2]) * f, __uint_as_float(v[i + 3]) * f);
 }
 
 // Joining the shares of tiles that a launch cut: one block takes kJoinRows

@@ -77,7 +77,7 @@ cudaError_t launch_attn_fwd(const AttnFwdParams& p, bool split, int grid, size_t
 // Backward launches (attn_bwd.cu).  The dq kernel's row tiles are as the
 // forward pass's; the dk, dv kernel takes tiles of 128 tokens of one head.
 constexpr int kAttnRowUnroll = 4;     // rows in flight per lane of the rows kernel
-constexpr int kAttnNormBlocks = 2048;  // most blocks of each part of the rows kernel
+constexpr int kAttnRowBlocks = 2048;  // most blocks of each part of the rows kernel
 
 struct AttnBwdParams {  // aligned like CUtensorMap
   CUtensorMap map_q, map_do;  // {D, heads, tokens, batch}, box by kernel
@@ -99,8 +99,13 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   uint32_t off_a, off_x, off_y, off_stat, off_mask, off_bar;
   float scale_log2;
   float p_shift, p_unscale;  // fp16: p is held times 2^p_shift; 2^-p_shift
-  float* stats;         // [batch][heads][q_tiles][2][128]
-  float* norms;         // fp16: row norms' maxima by block, else null
+  float* stats;         // [batch][heads][q_tiles][2, in fp16 3][128]
+  int stat_pitch;       // floats of a tile: 256, in fp16 384
+  // fp16: the largest squares of the norms of neighbouring rows (as many as a warp
+  // of the rows kernel takes), of do [batch][heads][q_tiles][...] and of v
+  // [batch][kv_heads][key_groups].
+  float *row_norms, *value_norms;
+  int key_groups;
   int row_blocks, value_blocks;  // blocks of the rows kernel
   int row_slots;                 // its rows side by side in a warp
   bool q_whole, kv_whole;        // no item of the dq, of the dk, dv kernel is cut

@@ -82,6 +82,13 @@ __device__ __forceinline__ void tmem_pin(uint32_t* v) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -152,10 +159,10 @@ __device__ __forceinline__ void mma_ss_x4(uint32_t d, uint32_t a_lo, uint32_t b_
   mma_x4<2, 2>(d, a_lo, b_lo, idesc, accumulate, steps);
 }
 
-// The same with A in TMEM (two K elements per 32-bit column, a step is 8
-// columns; the third begins kThird columns on) and B's rows running along N (a
-// step is 16 rows of 128 bytes).
-template <int kThird = 16>
+// The same with A in TMEM (two K elements per 32-bit column, 8 columns a step;
+// the second step begins kSecond columns on, the third kThird) and B's rows
+// running along N (a step is 16 rows of 128 bytes).
+template <int kThird = 16, int kSecond = 8>
 __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
                                           uint32_t accumulate, int steps) {
   asm volatile(
@@ -166,7 +173,7 @@ __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a_tmem, uint32_t 
       "mov.b64 b, {%2, %3};\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
       "setp.gt.and.s32 q, %6, 1, e;\n\t"
-      "add.s32 a, %1, 8;\n\tadd.s64 b, b, 128;\n\t"
+      "add.s32 a, %1, %9;\n\tadd.s64 b, b, 128;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t"
       "setp.gt.and.s32 q, %6, 2, e;\n\t"
       "add.s32 a, %1, %7;\n\tadd.s64 b, b, 128;\n\t"
@@ -175,7 +182,7 @@ __device__ __forceinline__ void mma_ts_x4(uint32_t d, uint32_t a_tmem, uint32_t 
       "add.s32 a, %1, %8;\n\tadd.s64 b, b, 128;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t}" ::"r"(d),
       "r"(a_tmem), "r"(b_lo), "r"(kDescHigh), "r"(idesc), "r"(accumulate), "r"(steps), "n"(kThird),
-      "n"(kThird + 8)
+      "n"(kThird + kSecond), "n"(kSecond)
       : "memory");
 }
 

@@ -16,9 +16,10 @@
 //
 // Backward, one pass over q and do for all three gradients: a row's scores
 // and dp = do v^T are whole in TMEM, so delta = sum_j p_j dp_j is summed right
-// there (no read of out).  p and ds go to shared memory as the queries' rows;
-// the same bytes are the A operand of dv += p^T do and dk += ds^T q (rows along
-// M) and of dq = ds k (rows along K).  dk and dv stay in TMEM over a CTA's
+// there (no read of out).  p and ds go to shared memory as the queries' rows,
+// the A operands of dv += p^T do and dk += ds^T q (rows along M), and ds to TMEM,
+// over dp, the A operand of dq = ds k (in fp16 with the queries' own scales,
+// which a sum over the queries cannot have).  dk and dv stay in TMEM over a CTA's
 // share of a key head's query tiles and are joined through the workspace.
 // The same call: 54 us and 9 for the join (the floor is 19): shared memory
 // carries p and ds three times and the 128-row operands of five products, some
@@ -396,7 +397,6 @@ struct ShortBars {
   uint64_t s_full[2], buf_free[2], dq_full[2];  // by TMEM buffer
   uint64_t pds_full, pds_empty, acc_done, acc_free, drain[2];
   float exchange[2][2][128];  // by step parity: a half row's share of delta
-  float most[2][32];  // the norms that ds's scale is made from
   uint32_t tmem;
   int abort_flag;
 };
@@ -445,6 +445,11 @@ struct ShortWalk {
   __device__ int keys() const { return min(valid_keys(p.a, b), p.kv_box); }
   __device__ int rows16() const { return qt == p.q_tiles - 1 ? p.last_cols : kAttnRows; }
 };
+
+// fp16: |do|^2 of row r of the walk's tile, as the rows kernel left it.
+__device__ __forceinline__ float row_norm(const AttnBwdParams& p, const ShortWalk& w, int r) {
+  return p.stats[((static_cast<long long>(w.b) * p.a.heads + w.head) * p.q_tiles + w.qt) * p.stat_pitch + 256 + r];
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kShortThreads, 1)
@@ -497,12 +502,11 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  gather_norms(p, bars.most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
-  // TMEM columns: dv, dk, then buffers of S (dq over it) and dp.
+  // TMEM columns: dv, dk, then buffers of S (dq over it) and dp (ds over it).
   const uint32_t t_dv = tmem, t_dk = tmem + 64, t_buf = tmem + 128;
   const uint32_t region = static_cast<uint32_t>(p.region), bufs = static_cast<uint32_t>(p.bufs);
 
@@ -608,7 +612,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t n_out = static_cast<uint32_t>(k_steps) * 16u;
     const uint32_t idesc_acc = attn_idesc(kBf16, n_out, true, true);   // p^T do, ds^T q
-    const uint32_t idesc_dq = attn_idesc(kBf16, n_out, false, true);   // ds k
+    const uint32_t idesc_dq = attn_idesc(kBf16, n_out, false, true);   // ds k (ds in TMEM)
     const uint32_t mn = lead_mn(kTile);
     const uint32_t q_lo = mn | (smem_u32(qd) >> 4), k_lo = lead_mn(kv_tile) | (smem_u32(kv) >> 4);
     const uint32_t p_lo = smem_u32(pds) >> 4, ds_lo = p_lo + (2 * kTile >> 4);
@@ -626,10 +630,9 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         ok = wait(&bars.pds_full, count & 1u, kAttnMmaTimeout);
         if (!ok) break;
         tc_fence_after();
-        // dq first: others wait for it.
-        mma_x4<2, 128>(t_dq, kLeadK | ds_lo, k_lo, idesc_dq, 0u, steps);
-        if (steps > 4)
-          mma_x4<2, 128>(t_dq, kLeadK | (ds_lo + (kTile >> 4)), k_lo + 512u, idesc_dq, 1u, steps - 4);
+        // dq first: others wait for it.  (A chunk of ds lies over its own dp.)
+        mma_ts_x4<32, 16>(t_dq, t_dq + region, k_lo, idesc_dq, 0u, steps);
+        if (steps > 4) mma_ts_x4<32, 16>(t_dq, t_dq + region + 64, k_lo + 512u, idesc_dq, 1u, steps - 4);
         mma_commit_warp(smem_u32(&bars.dq_full[buf_of(count)]));
         mma_x4<128, 128>(t_dv, mn | p_lo, q + (kTile >> 4), idesc_acc, go_on, row_steps);
         if (row_steps > 4)
@@ -655,12 +658,13 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     // ------------------------------------------------------------ dq out
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    const float f = p.a.scale / ds_scale(p, bars.most, lane);
     const bool leader = warp == kShortEpi && lane == 0;
     bool ok = true;
     uint32_t count = 0;
     for (ShortWalk w(p); ok && w.live; w.next()) {
+      const float values = kBf16 ? 0.f : largest_value(p, w.b, w.hk, lane);
       for (int i = w.i0; i < w.i1; ++i, ++count, w.step()) {
+        const float f = kBf16 ? p.a.scale : p.a.scale / ds_scale(row_norm(p, w, r), values);
         ok = wait(&bars.dq_full[buf_of(count)], phase_of(count), kAttnSoftmaxTimeout);
         if (leader) bulk_wait_read_all();
         ok = barrier_all(5, 128, ok);  // (the staging buffer is free)
@@ -703,28 +707,38 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     // Two warps share a quarter of the rows: 16-key chunks [0, mid) and [mid, all).
     const int half = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-    const float scale_ds = ds_scale(p, bars.most, lane);
-    const float c2 = p.scale_log2, sc = scale_ds * p.p_unscale;
-    const uint64_t c22 = pack2(c2, c2), sc2 = pack2(sc, sc);
+    const float c2 = p.scale_log2;
+    const uint64_t c22 = pack2(c2, c2);
     const int d = p.a.head_dim;
     uint32_t count = 0, items = 0;
     bool ok = true;
     for (ShortWalk w(p); ok && w.live; w.next()) {
       const int keys = w.keys(), all = cols_of(keys) >> 4, mid = (all + 1) >> 1;
       const int c0 = half ? mid : 0, c1 = half ? all : mid;
-      float lse = -INFINITY;
-      auto load_lse = [&]() {
+      // ds's scales: of this share of the key head's queries, for dk, and of a row.
+      float values = 0.f, scale_ds = 1.f;
+      if (!kBf16) {
+        values = largest_value(p, w.b, w.hk, lane);
+        scale_ds = ds_scale(largest_row(p, w.b, w.hk, w.i0, w.i1, lane), values);
+      }
+      const float sc = scale_ds * p.p_unscale;
+      const uint64_t sc2 = pack2(sc, sc);
+      float lse = -INFINITY, norm = 0.f;
+      auto load_row = [&]() {
         const int token = w.qt * kAttnRows + r;
         lse = token < p.a.q_len
                   ? p.a.lse[(static_cast<long long>(w.b) * p.a.heads + w.head) * p.a.q_len + token]
                   : -INFINITY;
+        if (!kBf16) norm = row_norm(p, w, r);
       };
-      load_lse();
+      load_row();
       for (int i = w.i0; i < w.i1; ++i, ++count) {
         // Minus lse in log2 units; a row without keys or past the end: p = 0.
         const float l2 = lse == -INFINITY ? -INFINITY : p.p_shift - lse * kLog2e;
+        const float row_sc = kBf16 ? 1.f : ds_scale(norm, values) * p.p_unscale;
+        const uint64_t row_sc2 = pack2(row_sc, row_sc);
         w.step();
-        if (i + 1 < w.i1) load_lse();  // (for the step after)
+        if (i + 1 < w.i1) load_row();  // (for the step after)
         ok = ok && wait(&bars.s_full[buf_of(count)], phase_of(count), kAttnSoftmaxTimeout);
         const uint32_t ts = t_buf + buf_of(count) * 2 * region + lane_field;
         uint32_t s[64];
@@ -782,7 +796,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           for (int c = 0; c < 4; ++c) {
             if (c0 + c < c1) {
               // (dp is read again: held beside p, it would not fit the registers.)
-              uint32_t dp[16], hp[8], hd[8];
+              uint32_t dp[16], hp[8], hd[8], hr[8];  // (hr: ds by its row's scale)
               tmem_ld_x16(ts + region + (c0 + c) * 16, dp);
               tmem_wait_ld_x16(dp);
               const int valid = keys - (c0 + c) * 16;
@@ -795,7 +809,11 @@ __global__ void __launch_bounds__(kShortThreads, 1)
               for (int j = 0; j < 8; ++j) {
                 const uint64_t pp = pack2(__uint_as_float(s[c * 16 + 2 * j]), __uint_as_float(s[c * 16 + 2 * j + 1]));
                 uint64_t u = add2(pack2(__uint_as_float(dp[2 * j]), __uint_as_float(dp[2 * j + 1])), dl);
-                if (!kBf16) u = mul2(u, sc2);
+                if (!kBf16) {
+                  unpack2(mul2(mul2(u, row_sc2), pp), x, y);
+                  hr[j] = round2<T>(x, y);
+                  u = mul2(u, sc2);
+                }
                 unpack2(mul2(u, pp), x, y);
                 hd[j] = round2<T>(x, y);
                 unpack2(pp, x, y);
@@ -803,6 +821,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
               }
               // Two 16-byte words of the row's block of 64 keys, swizzled.
               const int chunk = c0 + c, word = (chunk & 3) * 2;
+              tmem_st_x8(ts + region + chunk * 16, kBf16 ? hd : hr);
               uint8_t* row = pds + (chunk >> 2) * kTile + r * 128;
               const int w0 = (word ^ (r & 7)) << 4, w1 = ((word + 1) ^ (r & 7)) << 4;
               *reinterpret_cast<uint4*>(row + w0) = make_uint4(hp[0], hp[1], hp[2], hp[3]);
@@ -812,6 +831,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
               *reinterpret_cast<uint4*>(row + w1) = make_uint4(hd[4], hd[5], hd[6], hd[7]);
             }
           }
+          tmem_wait_st();
           tc_fence_before();
           fence_proxy_async_shared();
           __syncwarp();
@@ -843,7 +863,8 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           if (whole)
             store_cols(dst + c, v, d - c, f);
           else
-            store_cols_f32(p.part_kv + ((slot * 2 + half) * kAttnRows + r) * 128 + c, v, d - c);
+            store_cols_f32(p.part_kv + ((slot * 2 + half) * kAttnRows + r) * 128 + c, v, d - c,
+                           half ? 1.f / scale_ds : p.p_unscale);
         }
       }
       tc_fence_before();
