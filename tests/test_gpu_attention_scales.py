@@ -85,3 +85,28 @@ def test_rows_of_very_different_size_within_bounds(case):
     dout = (dout.float() * torch.exp2(power.float())).to(DT)
     got = _run(q, k, v, dout, **kw)
     _compare(got, A.Reference(q, k, v, dout=dout, u=A.UNIT["f16"], **kw))
+
+
+@pytest.mark.parametrize("case", [
+    (2, 200, 700, 4, 2, 64, "keys"), (1, 300, 1500, 2, 2, 128, "tail"), (2, 150, 400, 4, 2, 80, "rows"),
+    (2, 200, 100, 4, 1, 40, "keys"), (1, 260, 600, 6, 2, 24, "heads"), (3, 100, 500, 3, 3, 8, "tail"),
+    (2, 300, 640, 2, 1, 48, "lengths")], ids=lambda c: "x".join(map(str, c)))
+def test_large_values_that_no_query_attends_change_nothing(case):
+    """Masked padding that holds large finite numbers: the same bits as with zeros there."""
+    b, lq, lk, h, hkv, d, kind = case
+    g, q, k, v, dout, kw = _tensors(case, 34)
+    if kind in ("rows", "heads"):
+        kw["mask"][..., lk // 3:lk // 2] = 0
+    keep = A.pairs(b, h, lq, lk, **kw)
+    live = keep.any(2).reshape(b, hkv, h // hkv, lk).any(2).transpose(1, 2)
+    dout = (dout.float() / 256).to(DT)
+    runs = []
+    for fill in (0.0, 6e4):
+        k2, v2 = k.clone(), v.clone()
+        k2[~live] = fill
+        v2[~live] = fill
+        runs.append(_run(q, k2, v2, dout, **kw))
+    assert not live.all()
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
+    _compare(runs[1], A.Reference(q, k, v, dout=dout, u=A.UNIT["f16"], **kw))

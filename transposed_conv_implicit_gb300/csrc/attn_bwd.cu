@@ -85,8 +85,9 @@ __device__ __forceinline__ float dot8(uint4 x, uint4 y) {
 // stats[b][h][token tile][2][128]: minus lse in log2 units, plus p_shift (-inf
 // for queries without keys and past the end, which makes p zero), and minus
 // delta: as the products' sums take them.  In fp16 also |do|^2, and the largest
-// ones of every warp's rows of do and of v.  Rows of do without keys count as
-// zeros, and so do rows that are not finite: their gradients are not, either.
+// ones of every warp's rows of do and of v.  Rows of do without keys and of v
+// without queries count as zeros, and so do rows that are not finite: their
+// gradients are not, either.
 template <typename T>
 __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ AttnBwdParams p) {
   constexpr bool kNorms = std::is_same<T, __half>::value;
@@ -114,6 +115,25 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
     const int b = fast_div(bt, div_groups), part = bt - b * groups, t0 = part * group + slot;
     const int length = values ? valid_keys(a, b) : a.q_len;
     const long long row0 = (static_cast<long long>(b) * a.heads + h) * a.q_len;
+    // Keys of the tile of 128 around t0 that some query of the key head attends.
+    uint4 used = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (kNorms && values && a.mask_bits) {
+      const int rows = (a.any_h ? a.group : 1) * (a.any_q ? p.q_tiles : 1);
+      used = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = lane; i < rows; i += 32) {
+        const int hg = a.any_q ? i / p.q_tiles : i, qt = a.any_q ? i - hg * p.q_tiles : 0;
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            a.mask_any + (b * a.any_b + (h * a.group + hg) * a.any_h + qt * a.any_q) * a.mask_words + (t0 >> 7) * 4);
+        used.x |= v.x;
+        used.y |= v.y;
+        used.z |= v.z;
+        used.w |= v.w;
+      }
+      used.x = __reduce_or_sync(0xFFFFFFFFu, used.x);
+      used.y = __reduce_or_sync(0xFFFFFFFFu, used.y);
+      used.z = __reduce_or_sync(0xFFFFFFFFu, used.z);
+      used.w = __reduce_or_sync(0xFFFFFFFFu, used.w);
+    }
     uint4 x[kAttnRowUnroll], y[kAttnRowUnroll];
     float lse[kAttnRowUnroll];
 #pragma unroll
@@ -150,7 +170,11 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
 #pragma unroll
     for (int u = 0; u < kAttnRowUnroll; ++u) {
       const int t = t0 + u * p.row_slots;
-      if (!(sq[u] < INFINITY)) sq[u] = 0.f;  // (NaN compares false)
+      if (kNorms) {
+        const int bit = t & 127;
+        const uint32_t word = bit < 32 ? used.x : bit < 64 ? used.y : bit < 96 ? used.z : used.w;
+        if (!(sq[u] < INFINITY) || !((word >> (bit & 31)) & 1u)) sq[u] = 0.f;  // (NaN compares false)
+      }
       if (at == 0 && !values) {
         const float lse2 = lse[u] == -INFINITY ? lse[u] : p.p_shift - lse[u] * kLog2e;
         if (lse2 == -INFINITY) dot[u] = sq[u] = 0.f;
