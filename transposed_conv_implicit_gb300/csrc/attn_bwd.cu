@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                            head * p.a.dqs[2] + col,
                        v, d - col, f);
           else
-            store_cols_f32(p.part_q + (slot * kAttnRows + r) * 128 + col, v, d - col, 1.f / scale_ds);
+            store_cols_f32(p.part_q + (slot * kAttnRows + r) * 128 + col, v, d - col,
+                           kBf16 ? 1.f : 1.f / scale_ds);
         }
       }
       tc_fence_before();
@@ -1166,7 +1167,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             if (j < p.a.kv_len) store_cols(dst + c, v, d - c, f);
           } else {
             store_cols_f32(p.part_kv + ((slot * 2 + which) * kAttnRows + r) * 128 + c, v, d - c,
-                           which ? 1.f / scale_ds : p.p_unscale);
+                           kBf16 ? 1.f : which ? 1.f / scale_ds : p.p_unscale);
           }
         }
       }

@@ -364,14 +364,13 @@ __device__ __forceinline__ float largest_row(const AttnBwdParams& p, int b, int 
   return largest(p.row_norms + ((static_cast<long long>(b) * p.a.heads + hk * p.a.group) * p.q_tiles + i0) * per,
                  (i1 - i0) * per, lane);
 }
-// The power of two for |do|^2 <= x and |v|^2 <= y: |ds| 2^k <= 2^15.
+// The power of two for |do|^2 <= x and |v|^2 <= y: |ds| 2^k <= 2^15.  By the
+// exponents alone: x y < 2^e, so 2 |do| |v| < 2^(1 + ceil(e / 2)).  (Squares of
+// fp16 numbers and their sums are normal, and k is within +-61.)
 __device__ __forceinline__ float ds_scale(float x, float y) {
-  // 2 |do| |v| < 2^e; both norms in fp16's range, so k is within +-60.
-  const float bound = 2.f * sqrtf(x) * sqrtf(y);
-  if (!(bound > 0.f)) return 1.f;
-  int e;
-  frexpf(bound, &e);
-  return ldexpf(1.f, max(-60, min(60, 14 - e)));
+  if (x == 0.f || y == 0.f) return 1.f;
+  const int e = (__float_as_int(x) >> 23) + (__float_as_int(y) >> 23) - 2 * 126;
+  return __int_as_float((127 + 14 - ((e + 1) >> 1)) << 23);
 }
 
 // Clears the rows of a tile (kBlocks blocks of 128-byte rows) below `limit`

@@ -16,11 +16,13 @@
 //
 // Backward, one pass over q and do for all three gradients: a row's scores
 // and dp = do v^T are whole in TMEM, so delta = sum_j p_j dp_j is summed right
-// there (no read of out).  p and ds go to shared memory as the queries' rows,
-// the A operands of dv += p^T do and dk += ds^T q (rows along M), and ds to TMEM,
-// over dp, the A operand of dq = ds k (in fp16 with the queries' own scales,
-// which a sum over the queries cannot have).  dk and dv stay in TMEM over a CTA's
-// share of a key head's query tiles and are joined through the workspace.
+// there (no read of out).  p and ds go to shared memory as the queries' rows;
+// the same bytes are the A operand of dv += p^T do and dk += ds^T q (rows along
+// M) and, in bf16, of dq = ds k (rows along K).  In fp16 dq's ds has the queries'
+// own scales, which a sum over the queries cannot have: it lies in TMEM, over dp
+// (the same call in fp16, with the norms' kernel and the join: 99 us, 95 with one
+// scale for both).  dk and dv stay in TMEM over a CTA's share of a key head's
+// query tiles and are joined through the workspace.
 // The same call: 54 us and 9 for the join (the floor is 19): shared memory
 // carries p and ds three times and the 128-row operands of five products, some
 // 2000 cycles a step of 2700.
@@ -442,13 +444,28 @@ struct ShortWalk {
     }
     take(0);
   }
+  // Where the present step's statistics begin.
+  __device__ long long stats_at(int pitch) const {
+    return ((static_cast<long long>(b) * p.a.heads + head) * p.q_tiles + qt) * pitch;
+  }
   __device__ int keys() const { return min(valid_keys(p.a, b), p.kv_box); }
   __device__ int rows16() const { return qt == p.q_tiles - 1 ? p.last_cols : kAttnRows; }
 };
 
-// fp16: |do|^2 of row r of the walk's tile, as the rows kernel left it.
-__device__ __forceinline__ float row_norm(const AttnBwdParams& p, const ShortWalk& w, int r) {
-  return p.stats[((static_cast<long long>(w.b) * p.a.heads + w.head) * p.q_tiles + w.qt) * p.stat_pitch + 256 + r];
+// fp16: a row's scale of ds is the share's times 2^down.  At most 2^24, the
+// largest that a factor of fp16 takes back: rows still smaller beside the share's
+// largest have less room above fp16's smallest numbers.
+__device__ __forceinline__ int row_down(float norm, float values, float share) {
+  const int own = __float_as_int(ds_scale(norm, values)) >> 23, all = __float_as_int(share) >> 23;
+  return norm == 0.f ? 0 : min(24, own - all);
+}
+__device__ __forceinline__ float power(int e) { return __int_as_float((127 + e) << 23); }
+__device__ __forceinline__ __half2 half_down(int e) {  // 2^-e, e in [0, 24]
+  return __half2half2(__ushort_as_half(static_cast<unsigned short>(e <= 14 ? (15 - e) << 10 : 1 << (24 - e))));
+}
+__device__ __forceinline__ uint32_t times(uint32_t pair, __half2 f) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&pair), f);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 template <typename T>
@@ -506,7 +523,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
-  // TMEM columns: dv, dk, then buffers of S (dq over it) and dp (ds over it).
+  // TMEM columns: dv, dk, then buffers of S (dq over it) and dp (in fp16 ds over it).
   const uint32_t t_dv = tmem, t_dk = tmem + 64, t_buf = tmem + 128;
   const uint32_t region = static_cast<uint32_t>(p.region), bufs = static_cast<uint32_t>(p.bufs);
 
@@ -612,7 +629,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     const int k_steps = (p.a.head_dim + 15) >> 4;
     const uint32_t n_out = static_cast<uint32_t>(k_steps) * 16u;
     const uint32_t idesc_acc = attn_idesc(kBf16, n_out, true, true);   // p^T do, ds^T q
-    const uint32_t idesc_dq = attn_idesc(kBf16, n_out, false, true);   // ds k (ds in TMEM)
+    const uint32_t idesc_dq = attn_idesc(kBf16, n_out, false, true);   // ds k
     const uint32_t mn = lead_mn(kTile);
     const uint32_t q_lo = mn | (smem_u32(qd) >> 4), k_lo = lead_mn(kv_tile) | (smem_u32(kv) >> 4);
     const uint32_t p_lo = smem_u32(pds) >> 4, ds_lo = p_lo + (2 * kTile >> 4);
@@ -630,9 +647,16 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         ok = wait(&bars.pds_full, count & 1u, kAttnMmaTimeout);
         if (!ok) break;
         tc_fence_after();
-        // dq first: others wait for it.  (A chunk of ds lies over its own dp.)
-        mma_ts_x4<32, 16>(t_dq, t_dq + region, k_lo, idesc_dq, 0u, steps);
-        if (steps > 4) mma_ts_x4<32, 16>(t_dq, t_dq + region + 64, k_lo + 512u, idesc_dq, 1u, steps - 4);
+        // dq first: others wait for it.
+        if (kBf16) {
+          mma_x4<2, 128>(t_dq, kLeadK | ds_lo, k_lo, idesc_dq, 0u, steps);
+          if (steps > 4)
+            mma_x4<2, 128>(t_dq, kLeadK | (ds_lo + (kTile >> 4)), k_lo + 512u, idesc_dq, 1u, steps - 4);
+        } else {  // (a chunk of 16 keys lies over its own dp)
+          mma_ts_x4<32, 16>(t_dq, t_dq + region, k_lo, idesc_dq, 0u, steps);
+          if (steps > 4)
+            mma_ts_x4<32, 16>(t_dq, t_dq + region + 64, k_lo + 512u, idesc_dq, 1u, steps - 4);
+        }
         mma_commit_warp(smem_u32(&bars.dq_full[buf_of(count)]));
         mma_x4<128, 128>(t_dv, mn | p_lo, q + (kTile >> 4), idesc_acc, go_on, row_steps);
         if (row_steps > 4)
@@ -663,8 +687,13 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     uint32_t count = 0;
     for (ShortWalk w(p); ok && w.live; w.next()) {
       const float values = kBf16 ? 0.f : largest_value(p, w.b, w.hk, lane);
+      const float scale_ds = kBf16 ? 1.f : ds_scale(largest_row(p, w.b, w.hk, w.i0, w.i1, lane), values);
+      const float* st = p.stats + w.stats_at(p.stat_pitch) + 256 + r;
+      float norm = kBf16 ? 0.f : *st;
       for (int i = w.i0; i < w.i1; ++i, ++count, w.step()) {
-        const float f = kBf16 ? p.a.scale : p.a.scale / ds_scale(row_norm(p, w, r), values);
+        const float f = kBf16 ? p.a.scale : p.a.scale / (power(row_down(norm, values, scale_ds)) * scale_ds);
+        st += 384;
+        if (!kBf16 && i + 1 < w.i1) norm = *st;  // (for the step after)
         ok = wait(&bars.dq_full[buf_of(count)], phase_of(count), kAttnSoftmaxTimeout);
         if (leader) bulk_wait_read_all();
         ok = barrier_all(5, 128, ok);  // (the staging buffer is free)
@@ -721,23 +750,29 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         values = largest_value(p, w.b, w.hk, lane);
         scale_ds = ds_scale(largest_row(p, w.b, w.hk, w.i0, w.i1, lane), values);
       }
-      const float sc = scale_ds * p.p_unscale;
-      const uint64_t sc2 = pack2(sc, sc);
       float lse = -INFINITY, norm = 0.f;
+      const float* st = p.stats + w.stats_at(p.stat_pitch) + r;
       auto load_row = [&]() {
-        const int token = w.qt * kAttnRows + r;
-        lse = token < p.a.q_len
-                  ? p.a.lse[(static_cast<long long>(w.b) * p.a.heads + w.head) * p.a.q_len + token]
-                  : -INFINITY;
-        if (!kBf16) norm = row_norm(p, w, r);
+        if constexpr (kBf16) {
+          const int token = w.qt * kAttnRows + r;
+          lse = token < p.a.q_len
+                    ? p.a.lse[(static_cast<long long>(w.b) * p.a.heads + w.head) * p.a.q_len + token]
+                    : -INFINITY;
+        } else {  // (as the rows kernel left them: lse is l2 already)
+          lse = st[0];
+          norm = st[256];
+          st += 384;
+        }
       };
       load_row();
       for (int i = w.i0; i < w.i1; ++i, ++count) {
         // Minus lse in log2 units; a row without keys or past the end: p = 0.
-        const float l2 = lse == -INFINITY ? -INFINITY : p.p_shift - lse * kLog2e;
-        const float row_sc = kBf16 ? 1.f : ds_scale(norm, values) * p.p_unscale;
-        const uint64_t row_sc2 = pack2(row_sc, row_sc);
-        w.step();
+        const float l2 = !kBf16 || lse == -INFINITY ? lse : -lse * kLog2e;
+        const int down = kBf16 ? 0 : row_down(norm, values, scale_ds);
+        const float sc = power(down) * scale_ds * p.p_unscale;
+        const uint64_t sc2 = pack2(sc, sc);
+        const __half2 to_share = half_down(down);
+        if (kBf16) w.step();
         if (i + 1 < w.i1) load_row();  // (for the step after)
         ok = ok && wait(&bars.s_full[buf_of(count)], phase_of(count), kAttnSoftmaxTimeout);
         const uint32_t ts = t_buf + buf_of(count) * 2 * region + lane_field;
@@ -809,19 +844,18 @@ __global__ void __launch_bounds__(kShortThreads, 1)
               for (int j = 0; j < 8; ++j) {
                 const uint64_t pp = pack2(__uint_as_float(s[c * 16 + 2 * j]), __uint_as_float(s[c * 16 + 2 * j + 1]));
                 uint64_t u = add2(pack2(__uint_as_float(dp[2 * j]), __uint_as_float(dp[2 * j + 1])), dl);
-                if (!kBf16) {
-                  unpack2(mul2(mul2(u, row_sc2), pp), x, y);
-                  hr[j] = round2<T>(x, y);
-                  u = mul2(u, sc2);
-                }
-                unpack2(mul2(u, pp), x, y);
+                unpack2(mul2(kBf16 ? u : mul2(u, sc2), pp), x, y);
                 hd[j] = round2<T>(x, y);
+                if (!kBf16) {
+                  hr[j] = hd[j];
+                  hd[j] = times(hd[j], to_share);
+                }
                 unpack2(pp, x, y);
                 hp[j] = round2<T>(x, y);
               }
               // Two 16-byte words of the row's block of 64 keys, swizzled.
               const int chunk = c0 + c, word = (chunk & 3) * 2;
-              tmem_st_x8(ts + region + chunk * 16, kBf16 ? hd : hr);
+              if (!kBf16) tmem_st_x8(ts + region + chunk * 16, hr);
               uint8_t* row = pds + (chunk >> 2) * kTile + r * 128;
               const int w0 = (word ^ (r & 7)) << 4, w1 = ((word + 1) ^ (r & 7)) << 4;
               *reinterpret_cast<uint4*>(row + w0) = make_uint4(hp[0], hp[1], hp[2], hp[3]);
@@ -831,7 +865,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
               *reinterpret_cast<uint4*>(row + w1) = make_uint4(hd[4], hd[5], hd[6], hd[7]);
             }
           }
-          tmem_wait_st();
+          if (!kBf16) tmem_wait_st();
           tc_fence_before();
           fence_proxy_async_shared();
           __syncwarp();
@@ -864,7 +898,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
             store_cols(dst + c, v, d - c, f);
           else
             store_cols_f32(p.part_kv + ((slot * 2 + half) * kAttnRows + r) * 128 + c, v, d - c,
-                           half ? 1.f / scale_ds : p.p_unscale);
+                           kBf16 ? 1.f : half ? 1.f / scale_ds : p.p_unscale);
         }
       }
       tc_fence_before();
