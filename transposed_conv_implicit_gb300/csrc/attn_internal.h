@@ -5,9 +5,10 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
+
+#include "smem_limit.h"
 
 namespace convgb300 {
 
@@ -39,24 +40,6 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
   cfg.numAttrs = 1;
   cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
   return err != cudaSuccess ? err : cudaGetLastError();
-}
-
-// Raises a kernel's dynamic shared-memory limit, once per device, to the
-// largest size asked for so far (`configured`: one entry per device).
-constexpr int kMaxDevices = 64;
-template <typename K>
-cudaError_t raise_smem(K kernel, std::atomic<size_t>* configured, size_t smem) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (configured[dev].load(std::memory_order_relaxed) < smem) {
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem));
-    if (err != cudaSuccess) return err;
-    configured[dev].store(smem, std::memory_order_relaxed);
-  }
-  return cudaSuccess;
 }
 
 }  // namespace convgb300

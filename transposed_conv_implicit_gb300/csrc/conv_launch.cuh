@@ -6,28 +6,17 @@
 
 #include "conv_internal.h"
 #include "conv_kernel.cuh"
+#include "smem_limit.h"
 
 namespace convgb300 {
-
-constexpr int kMaxDevices = 64;
 
 template <int kKind, typename OutT, bool kGather, bool kPair = false, bool kStreamK = false>
 cudaError_t launch_instance(const ConvKernelParams& p, int grid, size_t smem_bytes,
                             cudaStream_t stream) {
-  // The dynamic shared-memory limit is a per-device function attribute: raise
-  // it once per device to the largest size requested so far.
   static std::atomic<size_t> configured[kMaxDevices];
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  cudaError_t err =
+      raise_smem(conv_igemm_kernel<kKind, OutT, kGather, kPair, kStreamK>, configured, smem_bytes);
   if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (configured[dev].load(std::memory_order_relaxed) < smem_bytes) {
-    err = cudaFuncSetAttribute(conv_igemm_kernel<kKind, OutT, kGather, kPair, kStreamK>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem_bytes));
-    if (err != cudaSuccess) return err;
-    configured[dev].store(smem_bytes, std::memory_order_relaxed);
-  }
   // Programmatic stream serialization: the kernel may be scheduled while the
   // previous kernel of the stream drains; it waits (griddepcontrol.wait)
   // before touching global memory, so stream order is preserved.

@@ -33,6 +33,7 @@
 #include "conv_internal.h"
 #include "ptx.cuh"
 #include "segment_copy.cuh"
+#include "smem_limit.h"
 
 namespace convgb300 {
 
@@ -424,18 +425,9 @@ __global__ void __launch_bounds__(kRtThreads, 1)
 template <int kKind, typename OutT>
 cudaError_t launch_rowtap(const RowTapParams& p, int grid, size_t smem_bytes,
                           cudaStream_t stream) {
-  static std::atomic<size_t> configured[64];
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  static std::atomic<size_t> configured[kMaxDevices];
+  const cudaError_t err = raise_smem(conv_rowtap_kernel<kKind, OutT>, configured, smem_bytes);
   if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (configured[dev].load(std::memory_order_relaxed) < smem_bytes) {
-    err = cudaFuncSetAttribute(conv_rowtap_kernel<kKind, OutT>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem_bytes));
-    if (err != cudaSuccess) return err;
-    configured[dev].store(smem_bytes, std::memory_order_relaxed);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kRtThreads);
