@@ -272,7 +272,6 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     tma_prefetch_desc(&p.map_v);
   }
   grid_dependency_wait();
-  grid_launch_dependents();
   if (warp == 0) {
     const SplitStart st = split_rows(p, lane);
     if (lane == 0) bars.start = st;
@@ -280,6 +279,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_launch_dependents();  // (TMEM is held: what starts now cannot take it first)
   const uint32_t tmem = bars.tmem;
   const SplitStart start = bars.start;
   // TMEM columns: S, dp (two buffers; ds over them), dq.
@@ -776,7 +776,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     tma_prefetch_desc(&p.map_v);
   }
   grid_dependency_wait();
-  grid_launch_dependents();
   if (warp == 0) {
     const SplitStart st = split_start(p.a.batch, key_steps_uniform(p), lane,
                                       [&](int b) { return key_steps(p, b); });
@@ -785,6 +784,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_launch_dependents();  // (TMEM is held: what starts now cannot take it first)
   const uint32_t tmem = bars.tmem;
   const SplitStart start = bars.start;
   // TMEM columns: S^T (p^T over it), dp^T (ds^T over it), dv, dk.

@@ -129,7 +129,6 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
     tma_prefetch_desc(&p.map_out);
   }
   grid_dependency_wait();
-  grid_launch_dependents();
   if (L::kSplit && warp == 0) {
     const SplitStart st = split_rows(p, lane);
     if (lane == 0) bars.start = st;
@@ -137,6 +136,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_launch_dependents();  // (TMEM is held: what starts now cannot take it first)
   const uint32_t tmem = bars.tmem;
   const SplitStart start = L::kSplit ? bars.start : SplitStart{};
 

@@ -518,10 +518,10 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     tma_prefetch_desc(&p.map_dq);
   }
   grid_dependency_wait();
-  grid_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_launch_dependents();  // (TMEM is held: what starts now cannot take it first)
   const uint32_t tmem = bars.tmem;
   // TMEM columns: dv, dk, then buffers of S (dq over it) and dp (in fp16 ds over it).
   const uint32_t t_dv = tmem, t_dk = tmem + 64, t_buf = tmem + 128;
