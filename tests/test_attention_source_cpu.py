@@ -36,3 +36,21 @@ def test_dependents_are_released_once_tensor_memory_is_held(kernel):
     body = kernel[2]
     alloc, release = body.index("tmem_alloc("), body.index("grid_launch_dependents()")
     assert "__syncthreads()" in body[alloc:release]
+
+
+MEET = [("attn_short_bwd_kernel", "barrier_all(1 + quarter, 64, ok)"),
+        ("attn_dkv_kernel", "if (kMask) ok = barrier_all(1, 32 * kSoftWarps, ok)"),
+        ("attn_dq_kernel", "if (kOne) ok = barrier_all(1 + quarter, 128, ok)")]
+
+
+@pytest.mark.parametrize("name,barrier", MEET, ids=[m[0] for m in MEET])
+def test_warps_that_meet_at_barriers_leave_an_item_together(name, barrier):
+    """A wait that runs out in one warp alone must not leave others at a named barrier, which has no
+    limit: after the wait that ends an item, and before anything can leave it, they agree."""
+    body = next(b for _, n, b in TMEM if n == name)
+    wait = "ok = ok && wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);"
+    after = body[body.index(wait) + len(wait):]
+    assert after.lstrip().startswith(barrier) or after.lstrip().startswith("ok = " + barrier)
+    # From the item's last step to that wait nothing leaves the item but what all warps do together.
+    loop = body[:body.index(wait)]
+    assert not loop.rstrip().endswith("break;")

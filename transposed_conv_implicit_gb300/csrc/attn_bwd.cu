@@ -577,8 +577,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bars.ds_full[count & 1u]));
         ++count;
       }
-      if (!ok) break;
-      ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      ok = ok && wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
       if (kOne) ok = barrier_all(1 + quarter, 128, ok);  // (the sums' parts have been read, too)
       ++items;
       if (!ok) break;
@@ -1032,7 +1031,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     for (KeyWalk<kMask> w(p, start); ok && w.live; w.next()) {
       const bool key_ok = r < w.keys();
       const bool keys_whole = w.keys() == kAttnRows;
-      bool told = false;  // of a failed wait, at a barrier
       const float scale_ds = kBf16 ? 1.f
                                    : ds_scale(largest_row(p, w.b, w.hk, w.i0, w.i1, lane),
                                               largest_value(p, w.b, w.hk, lane));
@@ -1053,7 +1051,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
                                   p.a.mask_words + w.tile * 4 + word];
           buf[row * 4 + word] = q;
           ok = barrier_all(1, 32 * kSoftWarps, ok);
-          told = !ok;
           if (!ok) break;
           on = 0;
 #pragma unroll
@@ -1142,9 +1139,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         // tells the others.)
         if (!ok && !kMask) break;
       }
-      if (kMask && !told) ok = barrier_all(1, 32 * kSoftWarps, ok);
-      if (!ok) break;
-      ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      // (With a mask all warps leave the item together: one that gave up alone
+      // would be missed at the next item's barriers.)
+      ok = ok && wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      if (kMask) ok = barrier_all(1, 32 * kSoftWarps, ok);
       ++items;
       if (!ok) break;
       tc_fence_after();

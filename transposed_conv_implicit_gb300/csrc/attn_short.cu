@@ -872,9 +872,10 @@ __global__ void __launch_bounds__(kShortThreads, 1)
           if (lane == 0) mbar_arrive(smem_u32(&bars.pds_full));
         }
       }
-      // Both halves leave the item together (ok or not).
-      if (!ok) break;
-      ok = wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      // Both halves leave the item together, ok or not: one that gave up alone would
+      // be missed at the next item's barriers.
+      ok = ok && wait(&bars.acc_done, items & 1u, kAttnSoftmaxTimeout);
+      ok = barrier_all(1 + quarter, 64, ok);
       ++items;
       if (!ok) break;
       tc_fence_after();
