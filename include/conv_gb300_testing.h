@@ -74,6 +74,13 @@ conv_status_t conv_testing_fwd_plan(int n, int h, int w, int c_in, conv_dtype_t 
 conv_status_t conv_testing_qk_norm_rope_blocks(const qk_norm_rope_args_t* args, int backward,
                                                int num_sms, int out[3]);
 
+/* How a cross_attention_fwd call (of queries that are not broadcast) would run
+ * on num_sms SMs: out[0] = schedule (0 pairs of row tiles, 1 shares of the keys,
+ * 2 one tile of keys), out[1] = CTAs, out[2] = with one tile of keys, shared
+ * memory bytes of a CTA.  Host-only. */
+conv_status_t conv_testing_cross_attention_plan(const cross_attention_args_t* args, int num_sms,
+                                                int out[3]);
+
 /* Read the CONV_* tuning overrides from the environment again (the library
  * reads them once, on first use) and invalidate every cached prepared call.
  * For tests that change an override between calls; not to be called while

@@ -3,7 +3,7 @@ import ctypes
 
 import pytest
 
-from tests.test_attention_abi_cpu import _norm
+from tests.test_attention_abi_cpu import _attn, _norm
 from transposed_conv_implicit_gb300 import _lib, build
 
 SMS = 152
@@ -56,3 +56,24 @@ def test_small_calls_of_the_norm_get_a_warp_for_each_unit(lib):
     a, b, _ = _blocks(lib, False, 8, (1, 32), (1, 8), 128, 128)
     rows = 4 * 4
     assert a == -(-(-(-8 * 32 // rows)) // 4) and b == -(-(-(-8 * 8 // rows)) // 4)
+
+
+@pytest.mark.parametrize("kv_len", [1, 16, 40, 64, 77, 80, 96, 100, 112, 128])
+@pytest.mark.parametrize("head_dim", [8, 16, 24, 32, 40, 48, 64])
+def test_one_tile_of_keys_runs_in_one_round(lib, head_dim, kv_len):
+    """Persistent thread blocks with equal shares of the row tiles: no more than an SM holds at once
+    (228 KB of shared memory, 1 KB of it taken for each block; 512 columns of tensor memory)."""
+    out = (ctypes.c_int * 3)()
+    args = _attn(batch=16, heads=8, kv_heads=8, q_len=4096, kv_len=kv_len, head_dim=head_dim, mask=0)
+    assert lib.conv_testing_cross_attention_plan(args, SMS, out) == 0
+    schedule, grid, smem = out
+    columns = 128 if -(-kv_len // 16) * 16 + -(-head_dim // 16) * 16 <= 128 else 256
+    assert schedule == 2 and grid % SMS == 0
+    assert grid == SMS * min(512 // columns, 228 * 1024 // (smem + 1024))
+
+
+def test_few_rows_take_a_block_each(lib):
+    out = (ctypes.c_int * 3)()
+    args = _attn(batch=2, heads=3, kv_heads=3, q_len=200, kv_len=77, head_dim=64, mask=0)
+    assert lib.conv_testing_cross_attention_plan(args, SMS, out) == 0
+    assert list(out)[:2] == [2, 2 * 3 * 2]

@@ -43,7 +43,7 @@ EXPORTS = (
     "conv_transposed_pack_filter_dilated",
     "cross_attention_workspace_size", "cross_attention_fwd", "cross_attention_bwd",
     "qk_norm_rope_fwd", "qk_norm_rope_workspace_size", "qk_norm_rope_bwd",
-    "conv_testing_qk_norm_rope_blocks",
+    "conv_testing_qk_norm_rope_blocks", "conv_testing_cross_attention_plan",
 )
 
 
@@ -117,6 +117,8 @@ def _declare(lib):
     lib.qk_norm_rope_bwd.restype = I
     lib.conv_testing_qk_norm_rope_blocks.argtypes = [B, I, I, IP]
     lib.conv_testing_qk_norm_rope_blocks.restype = I
+    lib.conv_testing_cross_attention_plan.argtypes = [B, I, IP]
+    lib.conv_testing_cross_attention_plan.restype = I
     return lib
 
 

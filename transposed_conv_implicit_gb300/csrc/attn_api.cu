@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "../../include/conv_gb300_attention.h"
+#include "../../include/conv_gb300_testing.h"
 #include "attn_internal.h"
 #include "attn_params.h"
 
@@ -83,6 +84,11 @@ struct FwdPlan {
   size_t part_bytes;     // split: partial rows and their statistics
 };
 
+// Shared memory of the kernel for one tile of keys: two buffers of queries (and
+// output), keys and values, barriers.
+uint32_t one_bar_offset(int kv_box) { return 2 * 16384 + 2 * kv_box * 128; }
+size_t one_smem(int kv_box) { return one_bar_offset(kv_box) + attn_one_bar_bytes(); }
+
 FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
   FwdPlan f{};
   const int group = a.heads / a.kv_heads;
@@ -107,11 +113,15 @@ FwdPlan plan_fwd(const cross_attention_args_t& a, int sms, bool may_pack) {
   const long long heads = static_cast<long long>(a.batch) * a.kv_heads;
   // One tile of keys, narrow heads, no mask: the kernel made for it (16 x 4096
   // x 8 heads x 40 against 77 keys: 31 us, 47 in pairs).  Four
-  // CTAs per SM where scores and output fit in 128 TMEM columns.
+  // CTAs per SM where scores and output fit in 128 TMEM columns, three of them
+  // where shared memory (228 KB, 1 KB a CTA taken) has no room for a fourth: with
+  // equal shares for more CTAs than run at once, some begin when others end (96
+  // keys x 32: 24.5 us, with shares for four 34.9; 112 x 16: 28.8 and 38.6).
   if (a.kv_len > 0 && a.kv_len <= kAttnRows && a.head_dim <= 64 && !a.mask) {
     f.one = f.kv_box + (a.head_dim + 15) / 16 * 16 <= 128 ? 4 : 2;
     f.items = heads * row_tiles;
-    f.grid = static_cast<int>(std::min<long long>(f.items, static_cast<long long>(f.one) * sms));
+    const long long fit = std::min<long long>(f.one, 228 * 1024 / (one_smem(f.kv_box) + 1024));
+    f.grid = static_cast<int>(std::min(f.items, fit * sms));
     return f;
   }
   f.items = heads * ((row_tiles + 1) / 2);
@@ -267,11 +277,10 @@ conv_status_t run_fwd(const AttnShape& s, const FwdPlan& f, char* ws, const Layo
   p.timeout_cycles = wait_limit_cycles();
   p.fault_mode = wait_fault_mode();
   if (f.one) {
-    // Two buffers of queries (and output), keys and values, barriers.
     p.off_q = 0;
     p.off_kv = 2 * 16384;
-    p.off_bar = p.off_kv + 2 * f.kv_box * 128;
-    return launch_attn_one(p, f.one, f.grid, p.off_bar + attn_one_bar_bytes(), stream) == cudaSuccess
+    p.off_bar = one_bar_offset(f.kv_box);
+    return launch_attn_one(p, f.one, f.grid, one_smem(f.kv_box), stream) == cudaSuccess
                ? CONV_OK
                : CONV_ERR_CUDA;
   }
@@ -553,6 +562,18 @@ conv_status_t cross_attention_fwd(const cross_attention_args_t* args, void* work
 conv_status_t cross_attention_bwd(const cross_attention_args_t* args, void* workspace,
                                   size_t workspace_bytes, void* stream) {
   return convgb300::run(args, true, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+conv_status_t conv_testing_cross_attention_plan(const cross_attention_args_t* args, int num_sms,
+                                                int out[3]) {
+  using namespace convgb300;
+  const conv_status_t st = check_sizes(*args);
+  if (st != CONV_OK) return st;
+  const FwdPlan f = plan_fwd(*args, num_sms, true);
+  out[0] = f.one ? 2 : f.split ? 1 : 0;
+  out[1] = f.grid;
+  out[2] = f.one ? static_cast<int>(one_smem(f.kv_box)) : 0;
+  return CONV_OK;
 }
 
 }  // extern "C"
