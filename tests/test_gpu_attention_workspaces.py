@@ -4,7 +4,7 @@ import torch
 
 import transposed_conv_implicit_gb300 as cg
 from tests import _attention as A
-from tests.test_gpu_attention import DEV, _gen, _normal, _tables
+from tests.test_gpu_attention import DEV, _gen, _make_mask, _normal, _tables
 
 pytestmark = pytest.mark.gpu
 GUARD = 0xA5
@@ -126,3 +126,43 @@ def test_streamk_in_a_graph_that_is_replayed():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert cg.conv_check_device_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("by_number", [False, True])
+def test_default_workspaces_belong_to_the_stream_of_the_call(by_number):
+    """A call on another stream without a workspace of its own: memory freed by the call is not handed
+    to the current stream while the call still waits there."""
+    g, dt = _gen(41), torch.bfloat16
+    q, dout = _normal(g, (1, 300, 4, 64), dt), _normal(g, (1, 300, 4, 64), dt)
+    k, v = _normal(g, (1, 700, 2, 64), dt), _normal(g, (1, 700, 2, 64), dt)
+    mask = torch.rand((1, 1, 300, 700), generator=g, device=DEV) < 0.5
+    out, dq, dk, dv = (torch.empty_like(t) for t in (q, q, k, v))
+    lse = torch.empty((1, 4, 300), device=DEV)
+    w, normed, dw = torch.ones(64, dtype=dt, device=DEV), torch.empty_like(q), torch.empty(64, device=DEV)
+    busy = _normal(g, (4096, 4096), dt)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if by_number else side
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(50):
+            busy = busy @ busy * 1e-2
+    cg.cross_attention_fwd(q, k, v, out, lse=lse, mask=mask, stream=stream)
+    cg.cross_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, mask=mask, stream=stream)
+    cg.qk_norm_rope_bwd(dout, None, q, None, w, None, normed, None, dw, None, stream=stream)
+    held = [torch.full((1 << n,), 0xFF, dtype=torch.uint8, device=DEV) for n in range(9, 25) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all((h == 0xFF).all() for h in held)
+    ref = A.Reference(q, k, v, mask=mask, dout=dout, u=A.UNIT["bf16"])
+    for name, x in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        A.assert_within(name, x, getattr(ref, name), getattr(ref, name + "_tol"))
+    norm = A.NormReference(q, w, None, None, None, 1e-6, False, A.UNIT["bf16"], dout)
+    A.assert_within("dw", dw, norm.dw, norm.dw_tol)
+
+
+def test_a_new_workspace_is_cleared_on_its_stream():
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0, torch.cuda.default_stream().cuda_stream):
+        ws = cg.new_workspace(1000, DEV, stream)
+        torch.cuda.synchronize()
+        assert ws.numel() == 1000 and not ws.any()
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()

@@ -82,10 +82,17 @@ def _need_dense(*ts):
             raise ConvError(CONV_ERR_INVALID_VALUE, "tensors must be dense (contiguous)")
 
 
-def new_workspace(nbytes: int, device):
-    """A zeroed uint8 device buffer (the status region must start at zero)."""
+def new_workspace(nbytes: int, device, stream=None):
+    """A zeroed uint8 device buffer (the status region must start at zero), cleared on `stream`
+    (default: the current one) and, once dropped, free for what follows there."""
     import torch
-    return torch.zeros(max(int(nbytes), CONV_STATUS_BYTES), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.zeros(max(int(nbytes), CONV_STATUS_BYTES), dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return new_workspace(nbytes, device)
 
 
 def conv2d_packed_filter_bytes(r, s, c_in, c_out, dtype: str) -> int:
@@ -144,7 +151,7 @@ def conv2d_fwd(input, filter, output, *, stride=(1, 1), dilation=(1, 1), symmetr
         raise ConvError(CONV_ERR_INVALID_VALUE, "filter shape does not match input/output/groups")
     if workspace is None:
         workspace = new_workspace(conv2d_workspace_size(r, s, c_in, c_out, dtype_name(input)),
-                                  input.device)
+                                  input.device, stream)
     _check(_lib.lib().conv2d_fwd(
         _ptr(input), n, h, w, c_in, _code(input), _ptr(filter), r, s, c_out, int(bool(filter_is_fcrs)),
         _ptr(output), ho, wo, _code(output), st, dl, pd, int(num_groups), int(bool(has_residual)),
@@ -165,7 +172,7 @@ def conv2d_fwd_packed(input, packed_filter, output, *, r, s, stride=(1, 1), dila
             != conv2d_packed_filter_bytes(r, s, c_in // groups, c_out, dtype_name(input))):
         raise ConvError(CONV_ERR_INVALID_VALUE, "packed filter size does not match")
     if workspace is None:
-        workspace = new_workspace(CONV_STATUS_BYTES, input.device)
+        workspace = new_workspace(CONV_STATUS_BYTES, input.device, stream)
     _check(_lib.lib().conv2d_fwd_packed(
         _ptr(input), n, h, w, c_in, _code(input), _ptr(packed_filter), r, s, c_out, _ptr(output), ho,
         wo, _code(output), st, dl, pd, int(num_groups), int(bool(has_residual)), _ptr(source),
@@ -225,7 +232,7 @@ def conv_transposed(input, filter_rsfc, output, *, stride=(1, 1), dilation=(1, 1
     if workspace is None:
         workspace = new_workspace(conv_transposed_workspace_size(r, s, c_in, c_out, stride, padding,
                                                                  dtype_name(input), dilation),
-                                  input.device)
+                                  input.device, stream)
     _check(_lib.lib().conv_transposed(
         _ptr(input), n, h, w, c_in, _code(input), _ptr(filter_rsfc), r, s, c_out, _ptr(output), ho, wo,
         _code(output), st, dl, pd, int(bool(has_residual)), _ptr(source), float(beta),
@@ -242,7 +249,7 @@ def conv_transposed_packed(input, packed_filter, output, *, r, s, stride=(1, 1),
                                                              source)
     _need_dense(packed_filter)
     if workspace is None:
-        workspace = new_workspace(CONV_STATUS_BYTES, input.device)
+        workspace = new_workspace(CONV_STATUS_BYTES, input.device, stream)
     _check(_lib.lib().conv_transposed_packed(
         _ptr(input), n, h, w, c_in, _code(input), _ptr(packed_filter), r, s, c_out, _ptr(output), ho,
         wo, _code(output), st, dl, pd, int(bool(has_residual)), _ptr(source), float(beta),
@@ -280,7 +287,7 @@ def bind_conv2d_fwd_packed(input, packed_filter, output, *, r, s, stride=(1, 1),
     n, h, w, c_in, ho, wo, c_out, st, dl, pd = _fwd_common(input, output, stride, dilation,
                                                              symmetric_padding, source)
     if workspace is None:
-        workspace = new_workspace(CONV_STATUS_BYTES, input.device)
+        workspace = new_workspace(CONV_STATUS_BYTES, input.device, stream)
     args = (_ptr(input), n, h, w, c_in, _code(input), _ptr(packed_filter), r, s, c_out, _ptr(output),
             ho, wo, _code(output), st, dl, pd, int(num_groups), int(bool(has_residual)), _ptr(source),
             float(beta), _lib.EPILOGUE_CODES[epilogue], _ptr(workspace),
@@ -296,7 +303,7 @@ def bind_conv_transposed_packed(input, packed_filter, output, *, r, s, stride=(1
     n, h, w, c_in, ho, wo, c_out, st, dl, pd = _fwd_common(input, output, stride, dilation, padding,
                                                              source)
     if workspace is None:
-        workspace = new_workspace(CONV_STATUS_BYTES, input.device)
+        workspace = new_workspace(CONV_STATUS_BYTES, input.device, stream)
     args = (_ptr(input), n, h, w, c_in, _code(input), _ptr(packed_filter), r, s, c_out, _ptr(output),
             ho, wo, _code(output), st, dl, pd, int(bool(has_residual)), _ptr(source), float(beta),
             _lib.EPILOGUE_CODES[epilogue], _ptr(workspace),

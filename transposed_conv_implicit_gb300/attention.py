@@ -154,7 +154,8 @@ def _attention(backward, q, k, v, output, lse, kv_lengths, mask, scale, grads, w
     lib = _lib.lib()
     if workspace is None:
         from . import new_workspace
-        workspace = new_workspace(lib.cross_attention_workspace_size(args, int(backward)), q.device)
+        workspace = new_workspace(lib.cross_attention_workspace_size(args, int(backward)), q.device,
+                                  stream)
     call = lib.cross_attention_bwd if backward else lib.cross_attention_fwd
     status = call(args, *_workspace(workspace, device), _stream(stream, device))
     if status != CONV_OK:
@@ -300,7 +301,7 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, dq, dk, dq_weight
                            device))
     if workspace is None:
         from . import new_workspace
-        workspace = new_workspace(qk_norm_rope_workspace_size(d), lead.device)
+        workspace = new_workspace(qk_norm_rope_workspace_size(d), lead.device, stream)
     _check(_lib.lib().qk_norm_rope_bwd(args, *_workspace(workspace, device), _stream(stream, device)),
            "qk_norm_rope_bwd")
     return dq, dk, dq_weight, dk_weight
