@@ -166,3 +166,34 @@ def test_a_new_workspace_is_cleared_on_its_stream():
         torch.cuda.synchronize()
         assert ws.numel() == 1000 and not ws.any()
         assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+ATTENTION = [  # b, lq, lk, h, hkv, d, mask: exact workspaces of each schedule
+    (2, 300, 77, 4, 4, 40, "lengths"), (1, 260, 290, 90, 90, 72, "none"), (4, 1, 3000, 8, 2, 128, "lengths"),
+    (2, 333, 700, 6, 2, 80, "rows"), (1, 500, 100, 4, 2, 96, "heads"), (3, 130, 260, 4, 1, 8, "keys"),
+    (2, 1021, 523, 12, 4, 80, "rows"), (1, 129, 2000, 2, 2, 24, "tail"),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("case", ATTENTION, ids=lambda c: "x".join(map(str, c)))
+def test_attention_keeps_to_its_workspace(case, dtype):
+    b, lq, lk, h, hkv, d, kind = case
+    g, dt = _gen(sum(case[:6])), A.TYPES[dtype]
+    q, dout = _normal(g, (b, lq, h, d), dt), _normal(g, (b, lq, h, d), dt)
+    k, v = _normal(g, (b, lk, hkv, d), dt), _normal(g, (b, lk, hkv, d), dt)
+    n, m = _make_mask(kind, g, b, h, lq, lk)
+    out, dq, dk, dv = (torch.empty_like(t) for t in (q, q, k, v))
+    lse = torch.empty((b, h, lq), device=DEV)
+    kw = dict(kv_lengths=n, mask=m)
+    masked = dict(masked=m is not None, mask_heads=1 if m is None else m.shape[1])
+    for backward in (False, True):
+        ws, behind = guarded(cg.cross_attention_workspace_size(b, h, hkv, lq, lk, d, backward=backward, **masked))
+        cg.cross_attention_fwd(q, k, v, out, lse=lse, workspace=ws, **kw)
+        if backward:
+            cg.cross_attention_bwd(dout, q, k, v, out, lse, dq, dk, dv, workspace=ws, **kw)
+        assert cg.conv_check_device_status(ws) == (0, 0)
+        assert (behind == GUARD).all()
+    ref = A.Reference(q, k, v, dout=dout, u=A.UNIT[dtype], **kw)
+    for name, x in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        A.assert_within(name, x, getattr(ref, name), getattr(ref, name + "_tol"))
