@@ -61,6 +61,14 @@ def _check(status, where):
         raise _error(status, where)
 
 
+def _pack(layout, *values):
+    """The values as a C struct; numbers that its fields cannot hold are refused."""
+    try:
+        return layout.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise _invalid("a size, a stride or a factor is out of range (%s)" % e) from None
+
+
 # The calls below run before every launch, single tokens' among them: devices are
 # compared as numbers and shapes as they come (a torch.device or a tuple for each
 # tensor made a call of one token half as long again).
@@ -147,10 +155,10 @@ def _attention(backward, q, k, v, output, lse, kv_lengths, mask, scale, grads, w
                     + _strides(dv, "dv", kshape, dtype, device))
         ptrs = (dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr())
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    args = _ATTN.pack(code, b, h, hkv, lq, lk, d, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                      output.data_ptr(), lse or 0, kv_lengths or 0, mask_ptr, *ptrs, *strides,
-                      *gstrides, *mask_strides)
+        scale = 1.0 / math.sqrt(d) if d else 1.0
+    args = _pack(_ATTN, code, b, h, hkv, lq, lk, d, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                 output.data_ptr(), lse or 0, kv_lengths or 0, mask_ptr, *ptrs, *strides, *gstrides,
+                 *mask_strides)
     lib = _lib.lib()
     if workspace is None:
         from . import new_workspace
@@ -166,9 +174,8 @@ def cross_attention_workspace_size(batch, heads, kv_heads, q_len, kv_len, head_d
                                    mask_heads=1, backward=False, dtype="bf16") -> int:
     """Workspace bytes for calls of these sizes.  `masked`: a mask with its own rows for every
     batch and query (for `mask_heads` heads) is given; narrower masks need no more."""
-    args = _ATTN.pack(_lib.DTYPE_CODES[dtype], batch, heads, kv_heads, q_len, kv_len, head_dim, 1.0,
-                      0, 0, 0, 0, 0, 0, int(masked), 0, 0, 0, 0, *(_NO_STRIDES * 8),
-                      1, int(mask_heads > 1), 1, 1)
+    args = _pack(_ATTN, _lib.DTYPE_CODES[dtype], batch, heads, kv_heads, q_len, kv_len, head_dim, 1.0,
+                 0, 0, 0, 0, 0, 0, int(masked), 0, 0, 0, 0, *(_NO_STRIDES * 8), 1, int(mask_heads > 1), 1, 1)
     size = _lib.lib().cross_attention_workspace_size(args, int(backward))
     if size == 0:
         raise _error(CONV_ERR_NOT_SUPPORTED, "cross_attention_workspace_size")
@@ -235,8 +242,8 @@ def _norm_tensor(name, x, weight, positions, y, dy, dx, dweight, batch, d, dtype
                         _dense(dweight, "d%s_weight" % name, (d,), torch.float32, device))
         strides = (*xs, 0, 0, 0, *_strides(dy, "d%s_out" % name, shape, dtype, device),
                    *_strides(dx, "d" + name, shape, dtype, device))
-    return _NORM_TENSOR.pack(x.data_ptr(), weight.data_ptr(), pos, out, *rest, shape[1], shape[2],
-                             weight.dtype is not dtype, pos_stride, *strides)
+    return _pack(_NORM_TENSOR, x.data_ptr(), weight.data_ptr(), pos, out, *rest, shape[1], shape[2],
+                 weight.dtype is not dtype, pos_stride, *strides)
 
 
 def _norm_head(q, k, cos, sin, eps, adjacent_pairs):
@@ -257,8 +264,8 @@ def _norm_head(q, k, cos, sin, eps, adjacent_pairs):
         rows, half = shape
         cp = _dense(cos, "cos", shape, _torch.float32, device)
         sp = _dense(sin, "sin", shape, _torch.float32, device)
-    head = _NORM_HEAD.pack(code, lead.shape[0], lead.shape[3], 2 * half, rows,
-                           1 if adjacent_pairs else 0, eps, cp, sp)
+    head = _pack(_NORM_HEAD, code, lead.shape[0], lead.shape[3], 2 * half, rows,
+                 1 if adjacent_pairs else 0, eps, cp, sp)
     return head, lead, device
 
 
