@@ -110,3 +110,41 @@ def test_large_values_that_no_query_attends_change_nothing(case):
     for x, y in zip(*runs):
         assert torch.equal(x, y)
     _compare(runs[1], A.Reference(q, k, v, dout=dout, u=A.UNIT["f16"], **kw))
+
+
+SMALL = [  # b, lq, lk, h, hkv, d: one tile of keys, shares of the keys, pairs
+    (2, 300, 120, 4, 4, 40), (3, 1, 3000, 8, 2, 128), (1, 5, 4000, 2, 2, 64), (2, 1500, 2000, 16, 16, 64),
+    (2, 200, 100, 2, 2, 128),
+]
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("size", SMALL, ids=lambda s: "x".join(map(str, s)))
+def test_many_small_probabilities_beside_a_large_one(size, masked):
+    """One key takes nearly all of every row and holds zeros; the output is what the others add, whose
+    probabilities lie between 2^-20 and 2^-28 of its own.  Their roundings are half a step of float16's
+    subnormals at most, of P times 2^7: 2^-32 each."""
+    b, lq, lk, h, hkv, d = size
+    g = _gen(sum(size))
+    q = torch.full((b, lq, h, d), 1.0, dtype=DT, device=DEV)
+    k = _normal(g, (b, lk, hkv, d), DT, 0.01)
+    # scale * q.k = ln 2 * (0 for the first key, -20 .. -28 for the others)
+    drop = 20 + 8 * torch.rand((b, lk, hkv, 1), generator=g, device=DEV)
+    drop[:, 0] = 0
+    k[..., :1] -= (drop * 0.6931 / 0.25 / 8).to(DT)
+    for i in range(1, 8):
+        k[..., i:i + 1] -= (drop * 0.6931 / 0.25 / 8).to(DT)
+    v = (torch.rand((b, lk, hkv, d), generator=g, device=DEV) * 200 + 100).to(DT)
+    v[:, 0] = 0
+    mask = None
+    if masked:
+        mask = torch.rand((b, 1, lq, lk), generator=g, device=DEV) < 0.7
+        mask[..., 0] = True
+    out, lse = _run(q, k, v, mask=mask, scale=0.25)
+    ref = A.Reference(q, k, v, mask=mask, scale=0.25, u=A.UNIT["f16"])
+    keep = A.pairs(b, h, lq, lk, None, mask).double()
+    total = (keep @ v.double().transpose(1, 2).repeat_interleave(h // hkv, dim=1)).transpose(1, 2)
+    bound = ref.out_tol - (2.0 ** -24 - 2.0 ** -31) * total     # (the general bound allows 2^-24 each)
+    assert (ref.out > 4 * bound).all()
+    A.assert_within("out", out, ref.out, bound)
+    A.assert_within("lse", lse, ref.lse, ref.lse_tol)

@@ -339,6 +339,15 @@ struct Walk {
 };
 
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+// The forward pass holds P times 2^shift (the running maximum in log2 units,
+// `mc`, is less by shift), and its sums with it.  In fp16 the shift takes P up to
+// 2^15, so that probabilities far below a row's largest are not rounded among the
+// type's subnormal numbers.
+__device__ __forceinline__ float row_lse(float mc, float l, float shift) {
+  return fmaf(mc + shift, kLn2, logf(l * exp2f(-shift)));
+}
 
 // fp16: ds is rounded after a scaling by a power of two, so that it does not
 // leave the type's range on either side.  |ds_ij| <= 2 |do_i| max |v|, over the

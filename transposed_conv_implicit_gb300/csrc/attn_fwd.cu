@@ -23,8 +23,9 @@
 //    a second kernel joins in order.  Query heads that share a key head sit
 //    side by side in a row tile when that makes fewer tiles.
 //
-// P is rounded to the inputs' type (the product's operand type), the sum is
-// taken of the unrounded fp32 values; O is rounded once.
+// P is rounded to the inputs' type (the product's operand type; in fp16 times 2^7,
+// with which it stays within 2^15), the sum is taken of the unrounded fp32 values;
+// O is rounded once.
 //
 // A group's products (P v, then the next S) are one batch that its own warp
 // issues; the groups' batches take turns.  With a mask, key tiles that none of
@@ -50,8 +51,9 @@ namespace convgb300 {
 
 namespace {
 
-constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleLog2 = 8.f;
+template <typename T>
+constexpr float kShift = std::is_same<T, __half>::value ? 15.f - kRescaleLog2 : 0.f;  // (row_lse)
 
 template <typename T, int DP, int G>
 struct Layout {
@@ -446,13 +448,13 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
         auto grow = [&](float mx) __attribute__((always_inline)) {
           if (first) {
             m = mx;
-            mc = m == -INFINITY ? 0.f : m * c2;
+            mc = m == -INFINITY ? 0.f : fmaf(m, c2, -kShift<T>);
           } else {
             const bool grown = (mx - m) * c2 > kRescaleLog2;  // (false for -inf - -inf = NaN)
             if (__any_sync(0xFFFFFFFFu, grown)) {
               float f = 1.f;
               if (grown) {
-                const float next = mx * c2;
+                const float next = fmaf(mx, c2, -kShift<T>);
                 f = m == -INFINITY ? 0.f : exp2_approx(mc - next);
                 m = mx;
                 mc = next;
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (p.a.lse && row_ok)
         p.a.lse[(static_cast<long long>(w.b) * p.a.heads + head) * p.a.q_len + token] =
-            l == 0.f ? -INFINITY : fmaf(mc, kLn2, logf(l));
+            l == 0.f ? -INFINITY : row_lse(mc, l, kShift<T>);
       int token0, head0;
       w.place(g, &token0, &head0);
 #pragma unroll 1
@@ -774,7 +776,7 @@ __global__ void __launch_bounds__(kJoinThreads)
           make_uint2(round2<T>(acc[u].x * inv, acc[u].y * inv), round2<T>(acc[u].z * inv, acc[u].w * inv));
     if (a.lse && lane == 0)
       a.lse[(static_cast<long long>(b) * a.heads + head) * a.q_len + token] =
-          l[u] == 0.f ? -INFINITY : fmaf(m[u], kLn2, logf(l[u]));
+          l[u] == 0.f ? -INFINITY : row_lse(m[u], l[u], kShift<T>);
   }
 }
 
