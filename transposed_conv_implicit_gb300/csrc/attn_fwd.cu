@@ -467,8 +467,8 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
 #pragma unroll 1
               for (int c = 0; c < d; c += 16) {  // (16 columns: the scores stay in registers)
                 uint32_t o[16];
-                tmem_ld_32x32b_x16(to + c, o);
-                tmem_wait_ld_regs(o);
+                tmem_ld_x16(to + c, o);
+                tmem_wait_ld_x16(o);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                 tmem_st_x16(to + c, o);

@@ -67,7 +67,7 @@ struct AttnFwdParams {  // aligned like CUtensorMap
   float* part_stat;     // split: [2 * grid][128][2]: maximum (log2 units), sum
   unsigned int* status;
   long long timeout_cycles;
-  int fault_mode;       // test hook: 1 = CTA 0 leaves its first key tile un-armed
+  int fault_mode;       // test hook: 1 = every CTA with work leaves its first keys un-armed
 };
 
 size_t attn_fwd_bar_bytes();
