@@ -341,12 +341,17 @@ struct Walk {
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 
-// The forward pass holds P times 2^shift (the running maximum in log2 units,
-// `mc`, is less by shift), and its sums with it.  In fp16 the shift takes P up to
-// 2^15, so that probabilities far below a row's largest are not rounded among the
-// type's subnormal numbers.
-__device__ __forceinline__ float row_lse(float mc, float l, float shift) {
-  return fmaf(mc + shift, kLn2, logf(l * exp2f(-shift)));
+// The forward pass holds P times 2^kShift (the running maximum in log2 units,
+// `mc`, is less by it), and its sums with it.  In fp16 P then reaches 2^15 (the
+// maximum may lag by 2^8), so that probabilities far below a row's largest are not
+// rounded among the type's subnormal numbers.  (No more: the exponent's argument
+// is rounded at the shift's size, 1.7e-7 of P here.)
+template <typename T>
+constexpr float kShift = std::is_same<T, __half>::value ? 7.f : 0.f;
+
+template <typename T>
+__device__ __forceinline__ float row_lse(float mc, float l) {
+  return fmaf(mc + kShift<T>, kLn2, logf(l * exp2f(-kShift<T>)));
 }
 
 // fp16: ds is rounded after a scaling by a power of two, so that it does not

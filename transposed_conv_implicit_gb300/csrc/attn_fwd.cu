@@ -52,8 +52,6 @@ namespace convgb300 {
 namespace {
 
 constexpr float kRescaleLog2 = 8.f;
-template <typename T>
-constexpr float kShift = std::is_same<T, __half>::value ? 15.f - kRescaleLog2 : 0.f;  // (row_lse)
 
 template <typename T, int DP, int G>
 struct Layout {
@@ -639,7 +637,7 @@ __global__ void __launch_bounds__(Layout<T, DP, G>::kThreads, G == 2 ? 1 : 2)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (p.a.lse && row_ok)
         p.a.lse[(static_cast<long long>(w.b) * p.a.heads + head) * p.a.q_len + token] =
-            l == 0.f ? -INFINITY : row_lse(mc, l, kShift<T>);
+            l == 0.f ? -INFINITY : row_lse<T>(mc, l);
       int token0, head0;
       w.place(g, &token0, &head0);
 #pragma unroll 1
@@ -776,7 +774,7 @@ __global__ void __launch_bounds__(kJoinThreads)
           make_uint2(round2<T>(acc[u].x * inv, acc[u].y * inv), round2<T>(acc[u].z * inv, acc[u].w * inv));
     if (a.lse && lane == 0)
       a.lse[(static_cast<long long>(b) * a.heads + head) * a.q_len + token] =
-          l[u] == 0.f ? -INFINITY : row_lse(m[u], l[u], kShift<T>);
+          l[u] == 0.f ? -INFINITY : row_lse<T>(m[u], l[u]);
   }
 }
 

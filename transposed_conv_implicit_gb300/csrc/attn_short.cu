@@ -107,7 +107,6 @@ __global__ void __launch_bounds__(kOneThreads, kCtas)
     attn_one_kernel(const __grid_constant__ AttnFwdParams p) {
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
   constexpr uint32_t kCols = kCtas == 4 ? 128 : 256;
-  constexpr float kShift = kBf16 ? 0.f : 15.f;
   extern __shared__ __align__(1024) uint8_t smem[];
   OneBars& bars = *reinterpret_cast<OneBars*>(smem + p.off_bar);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(kOneThreads, kCtas)
                 top[j] = max3(top[j], __uint_as_float(s[i + j]), __uint_as_float(s[i + 4 + j]));
             mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
           }
-          mc = mx == -INFINITY ? 0.f : fmaf(mx, c2, -kShift);  // (row_lse; P is no more than 1)
+          mc = mx == -INFINITY ? 0.f : fmaf(mx, c2, -kShift<T>);
           const uint64_t c22 = pack2(c2, c2), mc2 = pack2(-mc, -mc);
           uint64_t sum[2] = {0, 0};
 #pragma unroll 1
@@ -343,7 +342,7 @@ __global__ void __launch_bounds__(kOneThreads, kCtas)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (p.a.lse && row_ok)
           p.a.lse[(static_cast<long long>(b) * p.a.heads + head0 + row_head) * p.a.q_len + token] =
-              l == 0.f ? -INFINITY : row_lse(mc, l, kShift);
+              l == 0.f ? -INFINITY : row_lse<T>(mc, l);
         if (warp_ok) {
 #pragma unroll 1
           for (int c = 0; c < p.a.head_dim; c += 16) {  // (16 columns: no further than they are ours)
