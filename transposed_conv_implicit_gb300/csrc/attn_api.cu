@@ -342,7 +342,6 @@ conv_status_t run_bwd(const AttnShape& s, const FwdPlan& f, const BwdPlan& g, ch
   p.p_shift = half ? 15.f : 0.f;
   p.p_unscale = half ? 1.f / 32768.f : 1.f;
   p.stats = reinterpret_cast<float*>(ws + l.stat_at);
-  p.stat_pitch = half ? 384 : 256;
   p.row_norms = reinterpret_cast<float*>(ws + l.row_norm_at);
   p.value_norms = reinterpret_cast<float*>(ws + l.value_norm_at);
   p.key_groups = g.key_groups;

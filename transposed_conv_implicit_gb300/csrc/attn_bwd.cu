@@ -19,7 +19,7 @@
 // price of dq and dk, dv each summing in registers of their own CTA, without
 // adding fp32 partial sums of dq through L2 once per key tile.
 //
-// 2 x 16 heads, 8192 x 2048 x 128 (bound by the products): rows 28 us (4.9
+// 2 x 16 heads, 8192 x 2048 x 128 (bound by the products): rows 27 us (5.0
 // TB/s), dq 254 (1.62 PFLOP/s), dk and dv 350 (1.57 PFLOP/s), joins 31.  What
 // held the products back were waits: products of 128 x 128 from shared memory
 // take all of its bandwidth, and an mbarrier that is looked at beside them
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
         dot[u] += __shfl_xor_sync(0xFFFFFFFFu, dot[u], o);
         if (kNorms) sq[u] += __shfl_xor_sync(0xFFFFFFFFu, sq[u], o);
       }
+    if (!kNorms && at != 0) continue;
     float norm = 0.f;
 #pragma unroll
     for (int u = 0; u < kAttnRowUnroll; ++u) {
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(const __grid_constant__ 
       if (at == 0 && !values) {
         const float lse2 = lse[u] == -INFINITY ? lse[u] : p.p_shift - lse[u] * kLog2e;
         if (lse2 == -INFINITY) dot[u] = sq[u] = 0.f;
-        float* st = p.stats + ((static_cast<long long>(b) * a.heads + h) * p.q_tiles + (t >> 7)) * p.stat_pitch;
+        float* st = p.stats + ((static_cast<long long>(b) * a.heads + h) * p.q_tiles + (t >> 7)) * kStatPitch<T>;
         st[t & 127] = lse2;
         st[128 + (t & 127)] = -dot[u];
         if (kNorms) st[256 + (t & 127)] = sq[u];
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       const uint32_t* bits = nullptr;
       float* st = nullptr;
       if (row_ok) {
-        st = p.stats + ((static_cast<long long>(w.b) * p.a.heads + head) * p.q_tiles + (token >> 7)) * p.stat_pitch;
+        st = p.stats + ((static_cast<long long>(w.b) * p.a.heads + head) * p.q_tiles + (token >> 7)) * kStatPitch<T>;
         lse2 = st[token & 127];
         if (!kOne) delta = st[128 + (token & 127)];
         if (!kBf16) norm = st[256 + (token & 127)];
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           mbar_arrive_expect_tx_if(lead, sbar, 1024u);
           if (lead)
             bulk_load(smem_u32(smem + p.off_stat) + ss * 1024u,
-                      p.stats + ((static_cast<long long>(w.b) * p.a.heads + h) * p.q_tiles + qt) * p.stat_pitch,
+                      p.stats + ((static_cast<long long>(w.b) * p.a.heads + h) * p.q_tiles + qt) * kStatPitch<T>,
                       1024u, sbar);
           __syncwarp();
           ++nst;

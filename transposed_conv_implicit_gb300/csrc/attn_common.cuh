@@ -354,6 +354,11 @@ __device__ __forceinline__ float row_lse(float mc, float l) {
   return fmaf(mc + kShift<T>, kLn2, logf(l * exp2f(-kShift<T>)));
 }
 
+// Floats of a tile of 128 queries in the statistics: minus lse, minus delta, and in
+// fp16 |do|^2.
+template <typename T>
+constexpr int kStatPitch = std::is_same<T, __half>::value ? 384 : 256;
+
 // fp16: ds is rounded after a scaling by a power of two, so that it does not
 // leave the type's range on either side.  |ds_ij| <= 2 |do_i| max |v|, over the
 // values of the request's key head.  dq_i sums over the keys only: every query

@@ -100,7 +100,6 @@ struct AttnBwdParams {  // aligned like CUtensorMap
   float scale_log2;
   float p_shift, p_unscale;  // fp16: p is held times 2^p_shift; 2^-p_shift
   float* stats;         // [batch][heads][q_tiles][2, in fp16 3][128]
-  int stat_pitch;       // floats of a tile: 256, in fp16 384
   // fp16: the largest squares of the norms of neighbouring rows (as many as a warp
   // of the rows kernel takes), of do [batch][heads][q_tiles][...] and of v
   // [batch][kv_heads][key_groups].

@@ -23,7 +23,7 @@
 // (the same call in fp16, with the norms' kernel and the join: 99 us, 95 with one
 // scale for both).  dk and dv stay in TMEM over a CTA's share of a key head's
 // query tiles and are joined through the workspace.
-// The same call: 54 us and 9 for the join (the floor is 19): shared memory
+// The same call: 57 us and 10 for the join (the floor is 19): shared memory
 // carries p and ds three times and the 128-row operands of five products, some
 // 2000 cycles a step of 2700.
 #include <cuda_bf16.h>
@@ -443,9 +443,9 @@ struct ShortWalk {
     }
     take(0);
   }
-  // Where the present step's statistics begin.
-  __device__ long long stats_at(int pitch) const {
-    return ((static_cast<long long>(b) * p.a.heads + head) * p.q_tiles + qt) * pitch;
+  // The present step's place in the statistics, in tiles.
+  __device__ long long stats_at() const {
+    return (static_cast<long long>(b) * p.a.heads + head) * p.q_tiles + qt;
   }
   __device__ int keys() const { return min(valid_keys(p.a, b), p.kv_box); }
   __device__ int rows16() const { return qt == p.q_tiles - 1 ? p.last_cols : kAttnRows; }
@@ -687,11 +687,11 @@ __global__ void __launch_bounds__(kShortThreads, 1)
     for (ShortWalk w(p); ok && w.live; w.next()) {
       const float values = kBf16 ? 0.f : largest_value(p, w.b, w.hk, lane);
       const float scale_ds = kBf16 ? 1.f : ds_scale(largest_row(p, w.b, w.hk, w.i0, w.i1, lane), values);
-      const float* st = p.stats + w.stats_at(p.stat_pitch) + 256 + r;
+      const float* st = p.stats + w.stats_at() * kStatPitch<T> + 256 + r;
       float norm = kBf16 ? 0.f : *st;
       for (int i = w.i0; i < w.i1; ++i, ++count, w.step()) {
         const float f = kBf16 ? p.a.scale : p.a.scale / (power(row_down(norm, values, scale_ds)) * scale_ds);
-        st += 384;
+        st += kStatPitch<T>;
         if (!kBf16 && i + 1 < w.i1) norm = *st;  // (for the step after)
         ok = wait(&bars.dq_full[buf_of(count)], phase_of(count), kAttnSoftmaxTimeout);
         if (leader) bulk_wait_read_all();
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         scale_ds = ds_scale(largest_row(p, w.b, w.hk, w.i0, w.i1, lane), values);
       }
       float lse = -INFINITY, norm = 0.f;
-      const float* st = p.stats + w.stats_at(p.stat_pitch) + r;
+      const float* st = p.stats + w.stats_at() * kStatPitch<T> + r;
       auto load_row = [&]() {
         if constexpr (kBf16) {
           const int token = w.qt * kAttnRows + r;
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kShortThreads, 1)
         } else {  // (as the rows kernel left them: lse is l2 already)
           lse = st[0];
           norm = st[256];
-          st += 384;
+          st += kStatPitch<T>;
         }
       };
       load_row();
