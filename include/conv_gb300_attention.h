@@ -15,7 +15,8 @@
  * failures return before any launch and write nothing; workspaces start with
  * the CONV_STATUS_BYTES status region, zeroed once by the caller and read by
  * conv_check_device_status.  Calls that may overlap on the GPU need separate
- * workspaces.  Lengths and the batch may be zero here.
+ * workspaces; calls that follow one another, the convolutions' among them, may
+ * share one.  Lengths and the batch may be zero here.
  */
 #ifndef CONV_GB300_ATTENTION_H
 #define CONV_GB300_ATTENTION_H
@@ -50,7 +51,11 @@ extern "C" {
  * fixed order: equal calls give equal bits.
  *
  * Scores, sums and statistics are fp32; probabilities and ds are rounded to
- * `dtype` for the products that take them; results are rounded once.
+ * `dtype` for the products that take them; results are rounded once.  F16:
+ * probabilities are rounded after a scaling by 2^7 (backward 2^15), ds after one
+ * by a power of two from the norms of dout and v: for dq each query's own, for
+ * dk one for a part of a request's and key head's queries, where what is below
+ * 2^-29 of the largest 2 |dout| |v| is rounded in steps of 2^-40 of it.
  *
  * Layouts: [batch][length][heads][head_dim] with any strides (in elements,
  * {batch, token, head}; the innermost stride is 1).  Strides are multiples of
