@@ -21,6 +21,8 @@ from ._lib import (CONV_ERR_CUDA, CONV_ERR_DEVICE_TIMEOUT, CONV_ERR_INVALID_VALU
                    CONV_OK, CONV_STATUS_BYTES, ExtensionMissing)
 from .attention import (cross_attention_bwd, cross_attention_fwd, cross_attention_workspace_size,
                         qk_norm_rope_bwd, qk_norm_rope_fwd, qk_norm_rope_workspace_size)
+from .decoder import (kv_cache_read, kv_cache_write, layer_norm_bwd, layer_norm_fwd,
+                      layer_norm_workspace_size, tree_attention_fwd, tree_attention_workspace_size)
 
 __all__ = [
     "conv2d_fwd", "conv2d_fwd_packed", "conv2d_pack_filter", "conv2d_packed_filter_bytes",
@@ -31,6 +33,8 @@ __all__ = [
     "ConvError", "ExtensionMissing", "new_workspace", "dtype_name", "library_path",
     "cross_attention_fwd", "cross_attention_bwd", "cross_attention_workspace_size",
     "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_workspace_size",
+    "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_size", "kv_cache_write", "kv_cache_read",
+    "tree_attention_fwd", "tree_attention_workspace_size",
 ]
 
 

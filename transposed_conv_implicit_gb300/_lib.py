@@ -44,6 +44,8 @@ EXPORTS = (
     "cross_attention_workspace_size", "cross_attention_fwd", "cross_attention_bwd",
     "qk_norm_rope_fwd", "qk_norm_rope_workspace_size", "qk_norm_rope_bwd",
     "conv_testing_qk_norm_rope_blocks", "conv_testing_cross_attention_plan",
+    "layer_norm_fwd", "layer_norm_workspace_size", "layer_norm_bwd", "kv_cache_write", "kv_cache_read",
+    "tree_attention_workspace_size", "tree_attention_fwd",
 )
 
 
@@ -101,7 +103,7 @@ def _declare(lib):
     lib.conv_testing_reload_tuning.restype = None
     lib.conv_testing_cache_stats.argtypes = [ctypes.POINTER(U64), ctypes.POINTER(U64)]
     lib.conv_testing_cache_stats.restype = None
-    # The attention entry points take their argument structs as packed bytes.
+    # The attention's and the decoder's entry points take their argument structs as packed bytes.
     B = ctypes.c_char_p
     lib.cross_attention_workspace_size.argtypes = [B, I]
     lib.cross_attention_workspace_size.restype = Z
@@ -119,6 +121,20 @@ def _declare(lib):
     lib.conv_testing_qk_norm_rope_blocks.restype = I
     lib.conv_testing_cross_attention_plan.argtypes = [B, I, IP]
     lib.conv_testing_cross_attention_plan.restype = I
+    lib.layer_norm_fwd.argtypes = [B, P]
+    lib.layer_norm_fwd.restype = I
+    lib.layer_norm_workspace_size.argtypes = [I]
+    lib.layer_norm_workspace_size.restype = Z
+    lib.layer_norm_bwd.argtypes = [B, P, Z, P]
+    lib.layer_norm_bwd.restype = I
+    lib.kv_cache_write.argtypes = [B, P]
+    lib.kv_cache_write.restype = I
+    lib.kv_cache_read.argtypes = [B, P]
+    lib.kv_cache_read.restype = I
+    lib.tree_attention_workspace_size.argtypes = [B]
+    lib.tree_attention_workspace_size.restype = Z
+    lib.tree_attention_fwd.argtypes = [B, P, Z, P]
+    lib.tree_attention_fwd.restype = I
     return lib
 
 

@@ -1,0 +1,316 @@
+// Writing the paged 8-bit cache and reading it back, and their C entry points.
+//
+// A row of D elements becomes D e4m3 codes and one byte, the exponent of a
+// power-of-two scale.  e4m3 has a mantissa of its own for every element, so a
+// finer scale would not make the rounding finer (2^-4 of an element either
+// way); with a power of two the scaling is exact, the codes are the same
+// whatever width it is computed in, and attention can add exponents where it
+// would multiply.
+//
+// Bound by memory: 2 D bytes in and D + 1 out for each row, or the other way.
+// A lane takes 16 elements (two 16-byte words in, one out), the lanes of a row
+// (a power of two, D / 16 of them at work) find its largest element with
+// shuffles, and the key and the value of a token and head go together, so that
+// their exponents leave in one store.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "cache_common.cuh"
+
+namespace convgb300 {
+
+namespace {
+
+constexpr int kCacheThreads = 256;
+
+struct CacheParams {
+  CacheView c;
+  uint16_t *k, *v;
+  const int *starts, *lengths;
+  long long ks[3], vs[3];  // of k and v: batch, token, head
+  int length, rows, lanes;  // rows: batch * length * kv_heads
+  FastDiv div_length, div_heads;
+};
+
+__device__ __forceinline__ float magnitude(float x) {
+  x = fabsf(x);
+  return x < INFINITY ? x : 0.f;  // (not for infinities and NaN)
+}
+
+__device__ __forceinline__ float2 both(uint32_t v, __nv_bfloat16) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 both(uint32_t v, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+__device__ __forceinline__ uint32_t joined(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t joined(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The byte of a row whose largest element is `top`: top = m 2^k, 1 <= m < 2,
+// fits 448 = 1.75 2^8 with the exponent k - 8, or k - 7 where m > 1.75.
+__device__ __forceinline__ uint32_t scale_byte(float top) {
+  const uint32_t u = __float_as_uint(top);
+  const int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return top == 0.f ? 127u : static_cast<uint32_t>(max(e, 1));
+}
+
+// Where a row's token goes: page and offset, or page -1.
+struct Place {
+  int b, i, head, page, offset;
+};
+__device__ __forceinline__ Place place_of(const CacheParams& p, int row, bool* taken) {
+  Place o;
+  const int token = fast_div(row, p.div_heads);
+  o.head = row - token * static_cast<int>(p.div_heads.d);
+  o.b = fast_div(token, p.div_length);
+  o.i = token - o.b * static_cast<int>(p.div_length.d);
+  *taken = !p.lengths || o.i < p.lengths[o.b];
+  o.page = -1;
+  o.offset = 0;
+  const long long at = (p.starts ? static_cast<long long>(p.starts[o.b]) : 0ll) + o.i;
+  if (*taken && at >= 0 && at < static_cast<long long>(p.c.table_width) * p.c.page_size) {
+    const int index = fast_div(static_cast<int>(at), p.c.div_page);
+    o.offset = static_cast<int>(at) - index * p.c.page_size;
+    o.page = page_of(p.c, o.b, index);
+  }
+  return o;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 quantise(const uint4 (&raw)[2], uint32_t byte) {
+  const float f = __uint_as_float((254u - byte) << 23);  // 2^(127 - byte)
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 r = raw[i >> 1];
+    const float2 a = both((i & 1) ? r.z : r.x, T()), b = both((i & 1) ? r.w : r.y, T());
+    w[i] = round_codes(a.x * f, a.y * f) | (static_cast<uint32_t>(round_codes(b.x * f, b.y * f)) << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ float largest_of(const uint4 (&raw)[2]) {
+  const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 a = both(u[i], T());
+    top = fmaxf(top, fmaxf(magnitude(a.x), magnitude(a.y)));
+  }
+  return top;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kCacheThreads)
+    kv_cache_write_kernel(const __grid_constant__ CacheParams p) {
+  const int at = threadIdx.x & (p.lanes - 1);
+  const int groups = kCacheThreads / p.lanes;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (long long row0 = static_cast<long long>(blockIdx.x) * groups; row0 < p.rows;
+       row0 += static_cast<long long>(gridDim.x) * groups) {
+    const long long row = row0 + threadIdx.x / p.lanes;
+    bool taken = false;
+    Place o{};
+    o.page = -1;
+    if (row < p.rows) o = place_of(p, static_cast<int>(row), &taken);
+    const bool on = o.page >= 0 && at * 16 < p.c.head_dim;
+    uint4 k[2] = {}, v[2] = {};
+    if (on) {
+      const uint4* kp = reinterpret_cast<const uint4*>(p.k + o.b * p.ks[0] + o.i * p.ks[1] + o.head * p.ks[2]) + 2 * at;
+      const uint4* vp = reinterpret_cast<const uint4*>(p.v + o.b * p.vs[0] + o.i * p.vs[1] + o.head * p.vs[2]) + 2 * at;
+      k[0] = kp[0];
+      k[1] = kp[1];
+      v[0] = vp[0];
+      v[1] = vp[1];
+    }
+    float kt = largest_of<T>(k), vt = largest_of<T>(v);
+    for (int step = p.lanes >> 1; step > 0; step >>= 1) {
+      kt = fmaxf(kt, __shfl_xor_sync(0xFFFFFFFFu, kt, step));
+      vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, step));
+    }
+    if (!on) continue;
+    const uint32_t kb = scale_byte(kt), vb = scale_byte(vt);
+    *reinterpret_cast<uint4*>(p.c.k + o.page * p.c.ks[0] + o.offset * p.c.ks[1] + o.head * p.c.ks[2] +
+                              at * 16) = quantise<T>(k, kb);
+    *reinterpret_cast<uint4*>(p.c.v + o.page * p.c.vs[0] + o.offset * p.c.vs[1] + o.head * p.c.vs[2] +
+                              at * 16) = quantise<T>(v, vb);
+    if (at == 0)
+      *reinterpret_cast<uint16_t*>(p.c.scales + scale_at(p.c, o.page, o.head, o.offset)) =
+          static_cast<uint16_t>(kb | (vb << 8));
+  }
+}
+
+// Sixteen codes times 2^(byte - 127), rounded to T and limited to its numbers.
+template <typename T>
+__device__ __forceinline__ void restore(uint4 codes, uint32_t byte, uint4* out) {
+  const float f = __uint_as_float(byte << 23);  // (0 for rows that were never written)
+  const uint32_t u[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[2];
+    widen_codes4(u[i], h[0], h[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+      // (Rounding up to a power of two can pass either type's largest number.  NaN stays.)
+      constexpr float kMost = std::is_same<T, __half>::value ? 65504.f : 0x1.FEp127f;
+      const float x = a.x * f, y = a.y * f;
+      w[2 * i + j] = joined(x > kMost ? kMost : x < -kMost ? -kMost : x,
+                            y > kMost ? kMost : y < -kMost ? -kMost : y, T());
+    }
+  }
+  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kCacheThreads)
+    kv_cache_read_kernel(const __grid_constant__ CacheParams p) {
+  const int at = threadIdx.x & (p.lanes - 1);
+  const int groups = kCacheThreads / p.lanes;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (at * 16 >= p.c.head_dim) return;
+  for (long long row = static_cast<long long>(blockIdx.x) * groups + threadIdx.x / p.lanes; row < p.rows;
+       row += static_cast<long long>(gridDim.x) * groups) {
+    bool taken;
+    const Place o = place_of(p, static_cast<int>(row), &taken);
+    if (!taken) continue;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    uint32_t bytes = 0;
+    if (o.page >= 0) {
+      k = *reinterpret_cast<const uint4*>(p.c.k + o.page * p.c.ks[0] + o.offset * p.c.ks[1] +
+                                          o.head * p.c.ks[2] + at * 16);
+      v = *reinterpret_cast<const uint4*>(p.c.v + o.page * p.c.vs[0] + o.offset * p.c.vs[1] +
+                                          o.head * p.c.vs[2] + at * 16);
+      bytes = *reinterpret_cast<const uint16_t*>(p.c.scales + scale_at(p.c, o.page, o.head, o.offset));
+    }
+    if ((bytes & 0xFFu) == 0) {  // nothing was written there
+      k = v = make_uint4(0, 0, 0, 0);
+      bytes = 0;
+    }
+    restore<T>(k, bytes & 0xFFu,
+               reinterpret_cast<uint4*>(p.k + o.b * p.ks[0] + o.i * p.ks[1] + o.head * p.ks[2]) + 2 * at);
+    restore<T>(v, bytes >> 8,
+               reinterpret_cast<uint4*>(p.v + o.b * p.vs[0] + o.i * p.vs[1] + o.head * p.vs[2]) + 2 * at);
+  }
+}
+
+bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+conv_status_t cache_run(const kv_cache_args_t* args, bool write, cudaStream_t stream) {
+  if (!args) return CONV_ERR_INVALID_VALUE;
+  const kv_cache_args_t& a = *args;
+  if (a.dtype != CONV_DTYPE_BF16 && a.dtype != CONV_DTYPE_F16) return CONV_ERR_NOT_SUPPORTED;
+  if (a.batch < 0 || a.length < 0) return CONV_ERR_INVALID_VALUE;
+  const bool rows = a.batch > 0 && a.length > 0;
+  CacheParams p{};
+  conv_status_t st = take_cache(a.batch, a.kv_heads, a.head_dim, a.pages, a.page_size, a.table_width,
+                                a.table_stride, a.k_cache, a.v_cache, a.scales, a.block_table,
+                                a.k_cache_stride, a.v_cache_stride, write, rows, &p.c);
+  if (st != CONV_OK) return st;
+  if (rows && (!a.k || !a.v)) return CONV_ERR_INVALID_VALUE;
+  if (off(a.k, 16) || off(a.v, 16) || off(a.starts, 4) || off(a.lengths, 4)) return CONV_ERR_MISALIGNED;
+  st = take_row_strides(a.k_stride, a.batch, a.length, a.kv_heads, !write, p.ks);
+  if (st == CONV_OK) st = take_row_strides(a.v_stride, a.batch, a.length, a.kv_heads, !write, p.vs);
+  if (st != CONV_OK) return st;
+  if (!rows) return CONV_OK;
+  if (static_cast<long long>(a.batch) * a.length > kMaxCacheRows / a.kv_heads) return CONV_ERR_NOT_SUPPORTED;
+  p.k = static_cast<uint16_t*>(a.k);
+  p.v = static_cast<uint16_t*>(a.v);
+  p.starts = a.starts;
+  p.lengths = a.lengths;
+  p.length = a.length;
+  p.rows = a.batch * a.length * a.kv_heads;
+  p.lanes = 1;
+  while (p.lanes * 16 < a.head_dim) p.lanes <<= 1;
+  p.div_length = make_fast_div(static_cast<uint32_t>(a.length));
+  p.div_heads = make_fast_div(static_cast<uint32_t>(a.kv_heads));
+  const int sms = attn_sm_count();
+  if (sms <= 0) return CONV_ERR_CUDA;
+  const long long groups = kCacheThreads / p.lanes;
+  const dim3 grid(static_cast<unsigned>(std::min<long long>((p.rows + groups - 1) / groups, 8ll * sms)));
+  const auto kernel = a.dtype == CONV_DTYPE_BF16
+                          ? (write ? kv_cache_write_kernel<__nv_bfloat16> : kv_cache_read_kernel<__nv_bfloat16>)
+                          : (write ? kv_cache_write_kernel<__half> : kv_cache_read_kernel<__half>);
+  return launch_pdl(kernel, grid, dim3(kCacheThreads), 0, stream, p) == cudaSuccess ? CONV_OK
+                                                                                   : CONV_ERR_CUDA;
+}
+
+}  // namespace
+
+conv_status_t take_row_strides(const long long in[3], int batch, int length, int heads, bool output,
+                               long long out[3]) {
+  const int extent[3] = {batch, length, heads};
+  for (int i = 0; i < 3; ++i) {
+    out[i] = extent[i] > 1 ? in[i] : 0;
+    if (extent[i] > 1 && (in[i] < 0 || (in[i] == 0 && output))) return CONV_ERR_INVALID_VALUE;
+    if (out[i] % 8 != 0) return CONV_ERR_MISALIGNED;
+    if (out[i] >= 1ll << 40) return CONV_ERR_NOT_SUPPORTED;
+  }
+  return CONV_OK;
+}
+
+conv_status_t take_cache(int batch, int kv_heads, int head_dim, int pages, int page_size,
+                         int table_width, long long table_stride, const void* k, const void* v,
+                         const void* scales, const int* table, const long long ks[3],
+                         const long long vs[3], bool written, bool needed, CacheView* out) {
+  if (kv_heads <= 0 || head_dim <= 0 || pages < 0 || page_size <= 0 || table_width < 0)
+    return CONV_ERR_INVALID_VALUE;
+  if (head_dim % 16 != 0 || head_dim > 128 || page_size % 16 != 0) return CONV_ERR_NOT_SUPPORTED;
+  if (static_cast<long long>(table_width) * page_size > kMaxCacheRows) return CONV_ERR_NOT_SUPPORTED;
+  if (needed && ((pages > 0 && (!k || !v || !scales)) || (table_width > 0 && !table)))
+    return CONV_ERR_INVALID_VALUE;
+  if (batch > 1 && table_stride < 0) return CONV_ERR_INVALID_VALUE;
+  if (off(k, 16) || off(v, 16) || off(scales, 16) || off(table, 4)) return CONV_ERR_MISALIGNED;
+  const int extent[3] = {pages, page_size, kv_heads};
+  for (int i = 0; i < 3; ++i) {
+    const long long s[2] = {extent[i] > 1 ? ks[i] : 0, extent[i] > 1 ? vs[i] : 0};
+    for (const long long x : s) {
+      if (extent[i] > 1 && (x < 0 || (x == 0 && written))) return CONV_ERR_INVALID_VALUE;
+      if (x % 16 != 0) return CONV_ERR_MISALIGNED;
+      if (x >= 1ll << 40) return CONV_ERR_NOT_SUPPORTED;
+    }
+    out->ks[i] = s[0];
+    out->vs[i] = s[1];
+  }
+  out->k = static_cast<uint8_t*>(const_cast<void*>(k));
+  out->v = static_cast<uint8_t*>(const_cast<void*>(v));
+  out->scales = static_cast<uint8_t*>(const_cast<void*>(scales));
+  out->table = table;
+  out->table_stride = batch > 1 ? table_stride : 0;
+  out->pages = pages;
+  out->page_size = page_size;
+  out->table_width = table_width;
+  out->kv_heads = kv_heads;
+  out->head_dim = head_dim;
+  out->div_page = make_fast_div(static_cast<uint32_t>(page_size));
+  return CONV_OK;
+}
+
+}  // namespace convgb300
+
+extern "C" {
+
+conv_status_t kv_cache_write(const kv_cache_args_t* args, void* stream) {
+  return convgb300::cache_run(args, true, static_cast<cudaStream_t>(stream));
+}
+
+conv_status_t kv_cache_read(const kv_cache_args_t* args, void* stream) {
+  return convgb300::cache_run(args, false, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,587 @@
+// Layer norm, forward and backward, and its C entry points.
+//
+//   y = (x - m) r w + b,  m = mean x,  r = 1 / sqrt(mean (x - m)^2 + eps)
+//   dx = r (g - mean g - h mean(g h)),  g = dy w,  h = (x - m) r
+//   dw = sum_rows dy h,  db = sum_rows dy
+//
+// Bound by memory: x in, y out; x and dy in, dx out.  A row lies in the
+// registers of `lanes` lanes (a power of two up to a warp, or a whole block),
+// up to kWords words of kVec elements each, so it is read once: the mean, the
+// deviations from it and the result come from the same registers.  Lanes take
+// words that are neighbours, and rows go around the groups of the grid.
+//
+// Backward, a lane keeps the same columns in every row, so dw and db add up in
+// its registers over all rows of its group; groups of a block meet in shared
+// memory and blocks in the workspace, in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/conv_gb300_decoder.h"
+#include "attn_internal.h"
+#include "attn_ptx.cuh"
+#include "conv_params.h"
+
+namespace convgb300 {
+
+namespace {
+
+constexpr int kMaxChannels = 16384;
+constexpr long long kMaxLnRows = 0x7F000000ll;  // (a step of the grid beyond still counts in 31 bits)
+constexpr int kLnBwdBlocksPerSm = 2;  // rows of partial sums in the workspace
+
+struct LnParams {
+  const void *x, *weight, *bias, *dy;
+  void* y;  // y or dx
+  float *mean, *rstd;
+  float* partial;  // backward: [blocks][2][C]
+  float *dweight, *dbias;
+  int channels, words, lanes;  // words of kVec elements, lanes of a row
+  int rows, blocks;
+  float eps, inv_c;
+  FastDiv div_length;
+  long long xs[2], ds[2], ys[2];  // batch, token
+};
+
+template <typename T>
+__device__ __forceinline__ float to_float(T v);
+template <>
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_float(float v) { return v; }
+template <typename T>
+__device__ __forceinline__ T from_float(float v);
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ float2 halves(uint32_t v, __nv_bfloat16) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 halves(uint32_t v, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+__device__ __forceinline__ uint32_t joined(float a, float b, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t joined(float a, float b, __half) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A word of kVec elements as loaded: 16 bytes, or one element.
+template <int kVec>
+struct Word;
+template <>
+struct Word<8> {
+  uint4 v;
+};
+template <>
+struct Word<1> {
+  uint16_t v;
+};
+
+template <int kVec>
+__device__ __forceinline__ Word<kVec> load_word(const uint16_t* p) {
+  Word<kVec> w;
+  if constexpr (kVec == 8)
+    w.v = *reinterpret_cast<const uint4*>(p);
+  else
+    w.v = *p;
+  return w;
+}
+template <int kVec>
+__device__ __forceinline__ Word<kVec> no_word() {
+  Word<kVec> w;
+  if constexpr (kVec == 8)
+    w.v = make_uint4(0, 0, 0, 0);
+  else
+    w.v = 0;
+  return w;
+}
+template <typename T, int kVec>
+__device__ __forceinline__ void widen(const Word<kVec>& w, float* f) {
+  if constexpr (kVec == 8) {
+    const uint32_t u[4] = {w.v.x, w.v.y, w.v.z, w.v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = halves(u[i], T());
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+  } else {
+    f[0] = to_float(*reinterpret_cast<const T*>(&w.v));
+  }
+}
+template <typename T, int kVec>
+__device__ __forceinline__ void store_word(uint16_t* p, const float* f) {
+  if constexpr (kVec == 8) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(joined(f[0], f[1], T()), joined(f[2], f[3], T()),
+                                              joined(f[4], f[5], T()), joined(f[6], f[7], T()));
+  } else {
+    *reinterpret_cast<T*>(p) = from_float<T>(f[0]);
+  }
+}
+// Elements [at, at + kVec) of weight or bias; `fill` without one.
+template <typename W, int kVec>
+__device__ __forceinline__ void load_weight(const void* w, int at, float fill, float* f) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = fill;
+    return;
+  }
+  if constexpr (kVec == 8 && sizeof(W) == 4) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else if constexpr (kVec == 8) {
+    Word<8> v;
+    v.v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + at));
+    widen<W, 8>(v, f);
+  } else {
+    f[0] = to_float(static_cast<const W*>(w)[at]);
+  }
+}
+
+// Sums over the lanes of a row, given to all of them.  kBlock: the row is the
+// whole block's; `turn` alternates between two sets of slots, so that one
+// barrier a sum does.
+template <bool kBlock, int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float (*slots)[N][32], int& turn) {
+  for (int step = kBlock ? 16 : lanes >> 1; step > 0; step >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], step);
+  if constexpr (kBlock) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) slots[turn][i][warp] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.f;
+      for (int w = 0; w < warps; ++w) v[i] += slots[turn][i][w];
+    }
+    turn ^= 1;
+  }
+}
+
+// 1/sqrt(x): the hardware's approximation and one Newton step.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  return r * fmaf(-0.5f * x * r, r, 1.5f);
+}
+
+__device__ __forceinline__ long long row_at(const LnParams& p, int row, const long long s[2]) {
+  const int b = fast_div(row, p.div_length);
+  return b * s[0] + (row - b * static_cast<int>(p.div_length.d)) * s[1];
+}
+
+template <typename T, typename W, int kVec, int kWords, bool kBlock>
+__global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256)
+    layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
+  __shared__ float slots[2][1][32];
+  const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
+  const int at = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (lanes - 1);
+  const int groups = kBlock ? 1 : static_cast<int>(blockDim.x) / lanes;
+  const int group = kBlock ? 0 : static_cast<int>(threadIdx.x) / lanes;
+  int turn = 0;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // (Every lane goes through every step: groups without a row left load nothing.)
+  for (int row0 = blockIdx.x * groups; row0 < p.rows; row0 += gridDim.x * groups) {
+    const int row = row0 + group;
+    const bool live = row < p.rows;
+    const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
+    Word<kVec> raw[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = at + i * lanes;
+      raw[i] = live && w < p.words ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
+    }
+    float f[kWords * kVec], sum[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      widen<T, kVec>(raw[i], f + i * kVec);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) sum[0] += f[i * kVec + j];
+    }
+    row_sum<kBlock, 1>(sum, lanes, slots, turn);
+    const float mean = sum[0] * p.inv_c;
+    sum[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if (at + i * lanes < p.words)
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+          f[i * kVec + j] -= mean;
+          sum[0] = fmaf(f[i * kVec + j], f[i * kVec + j], sum[0]);
+        }
+    }
+    row_sum<kBlock, 1>(sum, lanes, slots, turn);
+    const float rstd = inverse_root(fmaf(sum[0], p.inv_c, p.eps));
+    if (!live) continue;
+    if (at == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+    uint16_t* y = static_cast<uint16_t*>(p.y) + row_at(p, row, p.ys);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = at + i * lanes;
+      if (w >= p.words) break;
+      float wt[kVec], bs[kVec];
+      load_weight<W, kVec>(p.weight, w * kVec, 1.f, wt);
+      load_weight<W, kVec>(p.bias, w * kVec, 0.f, bs);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) wt[j] = fmaf(f[i * kVec + j] * rstd, wt[j], bs[j]);
+      store_word<T, kVec>(y + w * kVec, wt);
+    }
+  }
+}
+
+template <typename T, typename W, int kVec, int kWords, bool kBlock>
+__global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
+    layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
+  __shared__ float slots[2][2][32];
+  extern __shared__ float sums[];  // [2][C] where a block has several groups
+  const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
+  const int at = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (lanes - 1);
+  const int groups = kBlock ? 1 : static_cast<int>(blockDim.x) / lanes;
+  const int group = kBlock ? 0 : static_cast<int>(threadIdx.x) / lanes;
+  int turn = 0;
+  float dw[kWords * kVec], db[kWords * kVec];
+#pragma unroll
+  for (int i = 0; i < kWords * kVec; ++i) dw[i] = db[i] = 0.f;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int row0 = blockIdx.x * groups; row0 < p.rows; row0 += gridDim.x * groups) {
+    const int row = row0 + group;
+    const bool live = row < p.rows;
+    const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
+    const uint16_t* dy = static_cast<const uint16_t*>(p.dy) + (live ? row_at(p, row, p.ds) : 0);
+    Word<kVec> rx[kWords], rd[kWords];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = at + i * lanes;
+      const bool on = live && w < p.words;
+      rx[i] = on ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
+      rd[i] = on ? load_word<kVec>(dy + w * kVec) : no_word<kVec>();
+    }
+    const float mean = live ? p.mean[row] : 0.f, rstd = live ? p.rstd[row] : 0.f;
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = at + i * lanes;
+      if (w >= p.words) break;
+      float h[kVec], g[kVec], wt[kVec];
+      widen<T, kVec>(rx[i], h);
+      widen<T, kVec>(rd[i], g);
+      load_weight<W, kVec>(p.weight, w * kVec, 1.f, wt);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        h[j] = (h[j] - mean) * rstd;
+        dw[i * kVec + j] = fmaf(g[j], h[j], dw[i * kVec + j]);  // (rows left out hold zeros of dy)
+        db[i * kVec + j] += g[j];
+        g[j] *= wt[j];
+        sum[0] += g[j];
+        sum[1] = fmaf(g[j], h[j], sum[1]);
+      }
+    }
+    row_sum<kBlock, 2>(sum, lanes, slots, turn);
+    if (!live) continue;
+    const float mg = sum[0] * p.inv_c, mgh = sum[1] * p.inv_c;
+    uint16_t* dx = static_cast<uint16_t*>(p.y) + row_at(p, row, p.ys);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = at + i * lanes;
+      if (w >= p.words) break;
+      float h[kVec], g[kVec], wt[kVec];
+      widen<T, kVec>(rx[i], h);
+      widen<T, kVec>(rd[i], g);
+      load_weight<W, kVec>(p.weight, w * kVec, 1.f, wt);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        h[j] = (h[j] - mean) * rstd;
+        g[j] = rstd * (fmaf(g[j], wt[j], -mg) - h[j] * mgh);
+      }
+      store_word<T, kVec>(dx + w * kVec, g);
+    }
+  }
+  if (!p.partial) return;
+  float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.channels;
+  if constexpr (kBlock) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const int w = at + i * lanes;
+      if (w >= p.words) break;
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        out[w * kVec + j] = dw[i * kVec + j];
+        out[p.channels + w * kVec + j] = db[i * kVec + j];
+      }
+    }
+  } else {
+    // The groups of a warp, then the warps one after the other.
+    for (int step = lanes; step < 32; step <<= 1)
+#pragma unroll
+      for (int i = 0; i < kWords * kVec; ++i) {
+        dw[i] += __shfl_xor_sync(0xFFFFFFFFu, dw[i], step);
+        db[i] += __shfl_xor_sync(0xFFFFFFFFu, db[i], step);
+      }
+    const int warps = static_cast<int>(blockDim.x) >> 5, warp = threadIdx.x >> 5;
+    for (int turn_of = 0; turn_of < warps; ++turn_of) {
+      if (warp == turn_of && (threadIdx.x & 31) < lanes)
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const int w = at + i * lanes;
+          if (w >= p.words) break;
+#pragma unroll
+          for (int j = 0; j < kVec; ++j) {
+            float* s = sums + w * kVec + j;
+            const float a = dw[i * kVec + j], b = db[i * kVec + j];
+            s[0] = turn_of ? s[0] + a : a;
+            s[p.channels] = turn_of ? s[p.channels] + b : b;
+          }
+        }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < 2 * p.channels; i += blockDim.x) out[i] = sums[i];
+  }
+}
+
+// Sums the blocks' shares: a block takes 32 columns, its warps every eighth
+// share each, in order.
+constexpr int kSumWarps = 8;
+__global__ void __launch_bounds__(32 * kSumWarps)
+    layer_norm_sum_kernel(const __grid_constant__ LnParams p) {
+  __shared__ float part[kSumWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;  // of [2][C]
+  grid_dependency_wait();
+  grid_launch_dependents();
+  float s = 0.f;
+  if (col < 2 * p.channels) {
+    const float* from = p.partial + col;
+#pragma unroll 8
+    for (int b = warp; b < p.blocks; b += kSumWarps) s += from[static_cast<long long>(b) * 2 * p.channels];
+  }
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && col < 2 * p.channels) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSumWarps; ++w) s += part[w][lane];
+    if (col < p.channels) {
+      if (p.dweight) p.dweight[col] = s;
+    } else if (p.dbias) {
+      p.dbias[col - p.channels] = s;
+    }
+  }
+}
+
+// How a row's words lie on lanes.
+struct LnShape {
+  int vec, words, lanes, per_lane, threads;
+  bool block;
+};
+
+// Words of a lane: as few idle ones as possible, then more rows side by side.
+LnShape ln_shape(int channels, bool vectors, bool backward) {
+  LnShape s{};
+  s.vec = vectors ? 8 : 1;
+  s.words = channels / s.vec;
+  const int most = !vectors ? 8 : backward ? 5 : 8;
+  long long best = -1;
+  for (int lanes = 32; lanes >= 1; lanes >>= 1) {
+    const int per = (s.words + lanes - 1) / lanes;
+    if (per > most) continue;
+    const long long idle = static_cast<long long>(lanes) * per - s.words;
+    const long long cost = idle * 32 / lanes + (lanes > 8 ? 0 : 1);
+    if (best < 0 || cost < best) {
+      best = cost;
+      s.lanes = lanes;
+      s.per_lane = per;
+    }
+  }
+  s.threads = backward ? 128 : 256;
+  if (best >= 0) return s;
+  s.block = true;
+  const int target = !vectors ? 16 : 4;
+  s.threads = 64;
+  while (s.threads < 1024 && (s.words + s.threads - 1) / s.threads > target) s.threads <<= 1;
+  s.lanes = s.threads;
+  s.per_lane = (s.words + s.threads - 1) / s.threads;
+  return s;
+}
+
+int ln_bwd_grid(const LnShape& s, int rows, int sms) {
+  const int groups = s.block ? 1 : s.threads / s.lanes;
+  const long long need = (static_cast<long long>(rows) + groups - 1) / groups;
+  return static_cast<int>(std::min<long long>(need, static_cast<long long>(kLnBwdBlocksPerSm) * sms));
+}
+
+template <typename T, typename W, int kVec, int kWords, bool kBlock>
+cudaError_t ln_launch(const LnParams& p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
+  if (!backward) {
+    const int groups = s.block ? 1 : s.threads / s.lanes;
+    const long long need = (static_cast<long long>(p.rows) + groups - 1) / groups;
+    const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(sms) * (2048 / s.threads)));
+    return launch_pdl(layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock>, dim3(grid), dim3(s.threads), 0,
+                      stream, p);
+  }
+  const size_t smem = s.block ? 0 : static_cast<size_t>(2) * p.channels * sizeof(float);
+  cudaError_t err = launch_pdl(layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock>, dim3(p.blocks),
+                               dim3(s.threads), smem, stream, p);
+  if (err != cudaSuccess || !p.partial) return err;
+  return launch_pdl(layer_norm_sum_kernel, dim3((2 * p.channels + 31) / 32), dim3(32 * kSumWarps), 0,
+                    stream, p);
+}
+
+template <typename T, typename W>
+cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, int sms,
+                            cudaStream_t stream) {
+  const auto pick = [&](auto words) {
+    constexpr int kWords = decltype(words)::value;
+    return s.vec == 8 ? (s.block ? ln_launch<T, W, 8, (kWords > 4 ? 4 : kWords), true>(p, s, backward, sms, stream)
+                                 : ln_launch<T, W, 8, kWords, false>(p, s, backward, sms, stream))
+                      : (s.block ? ln_launch<T, W, 1, 2 * kWords, true>(p, s, backward, sms, stream)
+                                 : ln_launch<T, W, 1, kWords, false>(p, s, backward, sms, stream));
+  };
+  const int n = s.vec == 1 && s.block ? (s.per_lane + 1) / 2 : s.per_lane;
+  if (n <= 1) return pick(std::integral_constant<int, 1>());
+  if (n <= 2) return pick(std::integral_constant<int, 2>());
+  if (n <= 3) return pick(std::integral_constant<int, 3>());
+  if (n <= 4) return pick(std::integral_constant<int, 4>());
+  if (n <= 5) return pick(std::integral_constant<int, 5>());
+  return pick(std::integral_constant<int, 8>());
+}
+
+bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+conv_status_t ln_strides(const long long in[2], int batch, int length, bool output, long long out[2]) {
+  const int extent[2] = {batch, length};
+  for (int i = 0; i < 2; ++i) {
+    out[i] = extent[i] > 1 ? in[i] : 0;
+    if (extent[i] > 1 && (in[i] < 0 || (in[i] == 0 && output))) return CONV_ERR_INVALID_VALUE;
+    if (out[i] >= 1ll << 40) return CONV_ERR_NOT_SUPPORTED;
+  }
+  return CONV_OK;
+}
+
+conv_status_t ln_check(const layer_norm_args_t& a, bool backward, LnParams* p) {
+  if (a.dtype != CONV_DTYPE_BF16 && a.dtype != CONV_DTYPE_F16) return CONV_ERR_NOT_SUPPORTED;
+  if (a.batch < 0 || a.length < 0 || a.channels <= 0) return CONV_ERR_INVALID_VALUE;
+  if (a.channels > kMaxChannels || static_cast<long long>(a.batch) * a.length > kMaxLnRows)
+    return CONV_ERR_NOT_SUPPORTED;
+  if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return CONV_ERR_INVALID_VALUE;
+  const bool rows = a.batch > 0 && a.length > 0;
+  if (rows && (!a.x || (backward ? !a.dy || !a.dx || !a.mean || !a.rstd : !a.y)))
+    return CONV_ERR_INVALID_VALUE;
+  const uintptr_t weight_size = a.weight_f32 ? 4 : 2;
+  if (off(a.x, 2) || off(a.weight, weight_size) || off(a.mean, 4) || off(a.rstd, 4))
+    return CONV_ERR_MISALIGNED;
+  if (backward ? off(a.dy, 2) || off(a.dx, 2) || off(a.dweight, 4) || off(a.dbias, 4)
+               : off(a.y, 2) || off(a.bias, weight_size))
+    return CONV_ERR_MISALIGNED;
+  conv_status_t st = ln_strides(a.x_stride, a.batch, a.length, false, p->xs);
+  if (st == CONV_OK && backward) st = ln_strides(a.dy_stride, a.batch, a.length, false, p->ds);
+  if (st == CONV_OK)
+    st = ln_strides(backward ? a.dx_stride : a.y_stride, a.batch, a.length, true, p->ys);
+  return st;
+}
+
+conv_status_t ln_run(const layer_norm_args_t* args, bool backward, void* workspace,
+                     size_t workspace_bytes, cudaStream_t stream) {
+  if (!args) return CONV_ERR_INVALID_VALUE;
+  const layer_norm_args_t& a = *args;
+  LnParams p{};
+  conv_status_t st = ln_check(a, backward, &p);
+  if (st != CONV_OK) return st;
+  const bool sums = backward && (a.dweight || a.dbias);
+  if (backward) {
+    if (!workspace) return CONV_ERR_INVALID_VALUE;
+    if (off(workspace, 16)) return CONV_ERR_MISALIGNED;
+    const size_t need = layer_norm_workspace_size(a.channels);
+    if (need == 0) return CONV_ERR_CUDA;
+    if (workspace_bytes < need) return CONV_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const int sms = attn_sm_count();
+  if (sms <= 0) return CONV_ERR_CUDA;
+  p.rows = a.batch * a.length;
+  if (p.rows == 0 && !sums) return CONV_OK;
+  p.x = a.x;
+  p.weight = a.weight;
+  p.bias = a.bias;
+  p.dy = a.dy;
+  p.y = backward ? a.dx : a.y;
+  p.mean = a.mean;
+  p.rstd = a.rstd;
+  p.dweight = a.dweight;
+  p.dbias = a.dbias;
+  p.channels = a.channels;
+  p.eps = a.eps;
+  p.inv_c = 1.f / static_cast<float>(a.channels);
+  p.div_length = make_fast_div(static_cast<uint32_t>(std::max(1, a.length)));
+  bool vectors = a.channels % 8 == 0;
+  const void* ptrs[] = {a.x, p.y, backward ? a.dy : nullptr};
+  for (const void* q : ptrs) vectors = vectors && !off(q, 16);
+  vectors = vectors && !off(a.weight, 16) && (backward || !off(a.bias, 16));
+  for (int i = 0; i < 2; ++i)
+    vectors = vectors && p.xs[i] % 8 == 0 && p.ys[i] % 8 == 0 && p.ds[i] % 8 == 0;
+  const LnShape s = ln_shape(a.channels, vectors, backward);
+  p.words = s.words;
+  p.lanes = s.lanes;
+  if (backward) {
+    p.blocks = ln_bwd_grid(s, p.rows, sms);
+    if (sums) p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + CONV_STATUS_BYTES);
+    if (p.rows == 0)  // sums over nothing
+      return launch_pdl(layer_norm_sum_kernel, dim3((2 * p.channels + 31) / 32), dim3(32 * kSumWarps),
+                        0, stream, p) == cudaSuccess
+                 ? CONV_OK
+                 : CONV_ERR_CUDA;
+  }
+  cudaError_t err;
+  if (a.dtype == CONV_DTYPE_BF16)
+    err = a.weight_f32 ? ln_launch_shape<__nv_bfloat16, float>(p, s, backward, sms, stream)
+                       : ln_launch_shape<__nv_bfloat16, __nv_bfloat16>(p, s, backward, sms, stream);
+  else
+    err = a.weight_f32 ? ln_launch_shape<__half, float>(p, s, backward, sms, stream)
+                       : ln_launch_shape<__half, __half>(p, s, backward, sms, stream);
+  return err == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace convgb300
+
+extern "C" {
+
+size_t layer_norm_workspace_size(int channels) {
+  using namespace convgb300;
+  if (channels <= 0 || channels > kMaxChannels) return 0;
+  const int sms = attn_sm_count();
+  if (sms <= 0) return 0;
+  return CONV_STATUS_BYTES +
+         static_cast<size_t>(kLnBwdBlocksPerSm) * sms * 2 * channels * sizeof(float);
+}
+
+conv_status_t layer_norm_fwd(const layer_norm_args_t* args, void* stream) {
+  return convgb300::ln_run(args, false, nullptr, 0, static_cast<cudaStream_t>(stream));
+}
+
+conv_status_t layer_norm_bwd(const layer_norm_args_t* args, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  return convgb300::ln_run(args, true, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
