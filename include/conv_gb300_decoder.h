@@ -92,7 +92,7 @@ conv_status_t layer_norm_bwd(const layer_norm_args_t* args, void* workspace,
  * kv_cache_write quantises rows of k and v, [batch][length][kv_heads][D] of
  * `dtype` (BF16 or F16; strides {batch, token, head} in elements, multiples
  * of 8), as tokens starts[b] .. of request b.  The exponent is the smallest
- * (-126 at least) with which the row's largest finite element is at most 448,
+ * (-64 at least) with which the row's largest finite element is at most 448,
  * 0 for rows of zeros; elements are rounded to nearest, ties to even, after
  * that exact scaling; infinities become +-448, NaN stays NaN.  With lengths
  * (int32 [batch]) only the first lengths[b] tokens are taken.  Tokens in front
@@ -153,8 +153,11 @@ conv_status_t kv_cache_read(const kv_cache_args_t* args, void* stream);
  * meet in the products as fp16: codes are exact there, a query's row is held
  * times a power of two (elements below 2^-28 of the row's largest are rounded
  * in steps of 2^-39 of it), and probabilities times 2^7 and their value's
- * scale relative to the largest of these.  Results are rounded once.  Sums run
- * in a fixed order: equal calls give equal bits.
+ * scale relative to the largest of these.  With more than 32 rows (drafts
+ * times query heads of a key head) codes are held relative to the largest
+ * scale of 16 neighbouring tokens: elements of keys are rounded in steps of
+ * 2^-24, of values in steps of 2^-31, of that.  Results are rounded once.  Sums
+ * run in a fixed order: equal calls give equal bits.
  *
  * q and out: [batch][q_len][heads][D] of `dtype`, strides {batch, token,
  * head} in elements, multiples of 8; lse: dense fp32 [batch][heads][q_len], or

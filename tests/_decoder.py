@@ -61,7 +61,7 @@ def quantised(x):
     size = torch.where(x.isfinite(), x.abs(), torch.zeros_like(x))
     top = size.amax(-1, keepdim=True)
     m, e = torch.frexp(top / 448.0)                     # (0.5 only where top is 448 times a power of two)
-    e = (e - (m == 0.5).to(e.dtype)).clamp(min=-126)
+    e = (e - (m == 0.5).to(e.dtype)).clamp(min=-64)
     e = torch.where(top == 0, torch.zeros_like(e), e)
     z = x * pow2(-e)
     step = pow2(torch.frexp(z.abs().clamp(2.0 ** -6, 448.0))[1] - 4)

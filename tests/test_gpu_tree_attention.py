@@ -7,6 +7,7 @@ import torch
 import transposed_conv_implicit_gb300 as cg
 from tests import _decoder as D
 from tests._attention import TYPES, UNIT, assert_within
+from transposed_conv_implicit_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -269,6 +270,29 @@ def test_guard_bytes_behind_an_exact_workspace(t, h, hkv, d):
     cg.tree_attention_fwd(q, *cache.args(), torch.tensor(keys, dtype=torch.int32, device=DEV), torch.empty_like(q),
                           workspace=ws[:size])
     assert (ws[size:] == 0x5A).all() and not ws[:cg.CONV_STATUS_BYTES].any()
+
+
+@pytest.mark.parametrize("t", [20, 64, 100])
+def test_a_wait_that_runs_out_is_reported(t):
+    """Many rows: the widened keys are not announced, every wait for them ends, and the next call is
+    right again."""
+    g, keys = _gen(23), [700, 300]
+    cache = _filled(g, "bf16", keys, 2, 128, 64)
+    q = torch.randn((2, t, 8, 128), generator=g, device=DEV).bfloat16()
+    out, n = torch.empty_like(q), torch.tensor(keys, dtype=torch.int32, device=DEV)
+    ws = cg.new_workspace(cg.tree_attention_workspace_size(2, 8, 2, t, cache.block_table.shape[1] * 64, 128), DEV)
+    lib = _lib.lib()
+    try:
+        lib.conv_testing_set_wait_fault(1, 5_000_000)
+        cg.tree_attention_fwd(q, *cache.args(), n, out, workspace=ws)
+        status, bits = cg.conv_check_device_status(ws)
+    finally:
+        lib.conv_testing_set_wait_fault(0, 0)
+    assert status == cg.CONV_ERR_DEVICE_TIMEOUT and bits != 0 and bits & ~7 == 0, (status, bits)
+    cg.tree_attention_fwd(q, *cache.args(), n, out, workspace=ws)
+    assert cg.conv_check_device_status(ws) == (0, 0)
+    ref = D.TreeReference(q, cache, keys, u=UNIT["bf16"])
+    assert_within("out", out, ref.out, ref.out_tol)
 
 
 def test_offsets_past_32_bits():

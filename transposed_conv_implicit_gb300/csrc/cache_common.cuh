@@ -5,10 +5,11 @@
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/conv_gb300_decoder.h"
+#include "attn_common.cuh"
 #include "attn_internal.h"
-#include "attn_ptx.cuh"
 #include "conv_params.h"
 
 namespace convgb300 {
@@ -51,6 +52,43 @@ __device__ __forceinline__ uint16_t round_codes(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
+}
+
+// Sixteen codes times 2^(byte - 127) (0 for rows that were never written),
+// rounded to T and limited to its numbers.
+template <typename T>
+__device__ __forceinline__ void restore(uint4 codes, uint32_t byte, uint4& first, uint4& second) {
+  constexpr bool kHalf = std::is_same<T, __half>::value;
+  const float f = __uint_as_float(byte << 23);
+  const uint64_t ff = pack2(f, f);
+  const uint32_t u[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t w[8];
+  auto each = [&](auto rounded) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[2];
+      widen_codes4(u[i], h[0], h[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        float x, y;
+        unpack2(mul2(pack2(a.x, a.y), ff), x, y);
+        w[2 * i + j] = rounded(x, y);
+      }
+    }
+  };
+  // Codes up to 448 can pass the largest number from these scales on (bfloat16's, by a row that
+  // was rounded up).  NaN stays.
+  if (byte < (kHalf ? 127u + 8u : 127u + 120u)) {
+    each([](float x, float y) { return round2<T>(x, y); });
+  } else {
+    each([](float x, float y) {
+      constexpr float kMost = kHalf ? 65504.f : 0x1.FEp127f;
+      return round2<T>(x > kMost ? kMost : x < -kMost ? -kMost : x, y > kMost ? kMost : y < -kMost ? -kMost : y);
+    });
+  }
+  first = make_uint4(w[0], w[1], w[2], w[3]);
+  second = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // Sizes, pages and strides that writing, reading and attention check alike;

@@ -16,7 +16,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <type_traits>
 
 #include "cache_common.cuh"
 
@@ -47,21 +46,13 @@ __device__ __forceinline__ float2 both(uint32_t v, __half) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
-__device__ __forceinline__ uint32_t joined(float a, float b, __nv_bfloat16) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t joined(float a, float b, __half) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // The byte of a row whose largest element is `top`: top = m 2^k, 1 <= m < 2,
-// fits 448 = 1.75 2^8 with the exponent k - 8, or k - 7 where m > 1.75.
+// fits 448 = 1.75 2^8 with the exponent k - 8, or k - 7 where m > 1.75.  (No less
+// than -64: attention divides its sums of probabilities by values' scales.)
 __device__ __forceinline__ uint32_t scale_byte(float top) {
   const uint32_t u = __float_as_uint(top);
   const int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return top == 0.f ? 127u : static_cast<uint32_t>(max(e, 1));
+  return top == 0.f ? 127u : static_cast<uint32_t>(max(e, 127 - 64));
 }
 
 // Where a row's token goes: page and offset, or page -1.
@@ -152,30 +143,6 @@ __global__ void __launch_bounds__(kCacheThreads)
   }
 }
 
-// Sixteen codes times 2^(byte - 127), rounded to T and limited to its numbers.
-template <typename T>
-__device__ __forceinline__ void restore(uint4 codes, uint32_t byte, uint4* out) {
-  const float f = __uint_as_float(byte << 23);  // (0 for rows that were never written)
-  const uint32_t u[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h[2];
-    widen_codes4(u[i], h[0], h[1]);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-      // (Rounding up to a power of two can pass either type's largest number.  NaN stays.)
-      constexpr float kMost = std::is_same<T, __half>::value ? 65504.f : 0x1.FEp127f;
-      const float x = a.x * f, y = a.y * f;
-      w[2 * i + j] = joined(x > kMost ? kMost : x < -kMost ? -kMost : x,
-                            y > kMost ? kMost : y < -kMost ? -kMost : y, T());
-    }
-  }
-  out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  out[1] = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kCacheThreads)
     kv_cache_read_kernel(const __grid_constant__ CacheParams p) {
@@ -202,10 +169,10 @@ __global__ void __launch_bounds__(kCacheThreads)
       k = v = make_uint4(0, 0, 0, 0);
       bytes = 0;
     }
-    restore<T>(k, bytes & 0xFFu,
-               reinterpret_cast<uint4*>(p.k + o.b * p.ks[0] + o.i * p.ks[1] + o.head * p.ks[2]) + 2 * at);
-    restore<T>(v, bytes >> 8,
-               reinterpret_cast<uint4*>(p.v + o.b * p.vs[0] + o.i * p.vs[1] + o.head * p.vs[2]) + 2 * at);
+    uint4* ko = reinterpret_cast<uint4*>(p.k + o.b * p.ks[0] + o.i * p.ks[1] + o.head * p.ks[2]) + 2 * at;
+    uint4* vo = reinterpret_cast<uint4*>(p.v + o.b * p.vs[0] + o.i * p.vs[1] + o.head * p.vs[2]) + 2 * at;
+    restore<T>(k, bytes & 0xFFu, ko[0], ko[1]);
+    restore<T>(v, bytes >> 8, vo[0], vo[1]);
   }
 }
 

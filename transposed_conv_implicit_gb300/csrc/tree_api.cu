@@ -12,7 +12,11 @@ namespace convgb300 {
 
 namespace {
 
+// Rows of a key head from which on the tensor cores' kernel is the faster one.
+constexpr int kFewRows = 32;
+
 struct TreePlan {
+  bool many;
   int tile_rows, max_tiles, grid;
   size_t part_bytes;
 };
@@ -32,15 +36,16 @@ conv_status_t check_sizes(const tree_attention_args_t& a) {
 TreePlan plan(const tree_attention_args_t& a, int sms) {
   TreePlan f{};
   const int rows = a.q_len * (a.heads / a.kv_heads);
-  f.tile_rows = rows <= 16 ? 16 : 32;
+  f.many = rows > kFewRows;
+  f.tile_rows = f.many ? kTreeManyRows : rows <= 16 ? 16 : 32;
   f.max_tiles = std::max(1, (rows + f.tile_rows - 1) / f.tile_rows);
   const long long key_tiles =
       (static_cast<long long>(a.table_width) * a.page_size + kTreeKeys - 1) / kTreeKeys;
   const long long items = static_cast<long long>(a.batch) * a.kv_heads * f.max_tiles;
-  const long long most = static_cast<long long>(tree_few_ctas(a.head_dim, f.tile_rows)) * sms;
+  const long long most = static_cast<long long>(f.many ? 1 : tree_few_ctas(f.tile_rows)) * sms;
   // (More items than CTAs by far: their steps are as many at least.)
   f.grid = static_cast<int>(items >= most ? most : std::min(most, items * std::max(1ll, key_tiles)));
-  if (key_tiles > 1)
+  if (key_tiles > 1 || f.many)
     f.part_bytes = static_cast<size_t>(2) * f.grid * f.tile_rows * (128 + 2) * sizeof(float);
   return f;
 }
@@ -96,7 +101,13 @@ conv_status_t run(const tree_attention_args_t* args, void* workspace, size_t wor
   p.div_slices = make_fast_div(static_cast<uint32_t>(a.page_size / 16));
   p.part_out = reinterpret_cast<float*>(static_cast<char*>(workspace) + CONV_STATUS_BYTES);
   p.part_stat = p.part_out + static_cast<size_t>(2) * f.grid * f.tile_rows * 128;
-  if (launch_tree_few(p, a.dtype, f.grid, stream) != cudaSuccess) return CONV_ERR_CUDA;
+  p.many = f.many;
+  p.status = static_cast<unsigned int*>(workspace);
+  p.timeout_cycles = wait_limit_cycles();
+  p.fault_mode = wait_fault_mode();
+  const cudaError_t err = f.many ? launch_tree_many(p, a.dtype, f.grid, stream)
+                                 : launch_tree_few(p, a.dtype, f.grid, stream);
+  if (err != cudaSuccess) return CONV_ERR_CUDA;
   if (f.part_bytes && launch_tree_join(p, a.dtype, f.grid, stream) != cudaSuccess) return CONV_ERR_CUDA;
   return CONV_OK;
 }

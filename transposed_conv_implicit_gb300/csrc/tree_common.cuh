@@ -113,6 +113,14 @@ __device__ __forceinline__ float row_factor(float top, float* back) {
   return __int_as_float((127 + f) << 23);
 }
 
+// Two bf16 numbers: the larger magnitude, and both times `up` as fp16.
+__device__ __forceinline__ float larger_of(uint32_t v) {
+  return fmaxf(fabsf(__uint_as_float(v << 16)), fabsf(__uint_as_float(v & 0xFFFF0000u)));
+}
+__device__ __forceinline__ uint32_t to_half(uint32_t v, float up) {
+  return round2<__half>(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+}
+
 // y = (score in log2 units) + (exponent of the value's scale): probabilities
 // are held as 2^(y - maximum + kTreeShift), see tree_few.cu.  The maximum may
 // lag by kTreeLag, so they stay within 2^15.

@@ -96,19 +96,6 @@ __device__ __forceinline__ void product(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-template <typename T>
-__device__ __forceinline__ float2 wide(uint32_t v) {
-  if constexpr (std::is_same<T, __half>::value)
-    return __half22float2(*reinterpret_cast<const __half2*>(&v));
-  else
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-}
-
 template <typename T>
 __device__ __forceinline__ void store4(uint16_t* dst, float a, float b, float c, float d) {
   *reinterpret_cast<uint2*>(dst) = make_uint2(round2<T>(a, b), round2<T>(c, d));
@@ -232,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint4 u = raw[i][j >> 2];
-            const float2 f = wide<T>((j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w);
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            if constexpr (!std::is_same<T, __half>::value)
+              top = fmaxf(top, larger_of((j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w));
           }
         }
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -248,12 +235,7 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
             const uint4 u = raw[i][j >> 2];
             const uint32_t v = (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
             // Elements 2 j, 2 j + 1: inner step 4 i + j / 2, its first or second pair.
-            if constexpr (std::is_same<T, __half>::value) {
-              qa[m][4 * i + j / 2][h + 2 * (j & 1)] = v;
-            } else {
-              const float2 f = wide<T>(v);
-              qa[m][4 * i + j / 2][h + 2 * (j & 1)] = pack_half(f.x * up, f.y * up);
-            }
+            qa[m][4 * i + j / 2][h + 2 * (j & 1)] = std::is_same<T, __half>::value ? v : to_half(v, up);
           }
       }
 
@@ -379,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
           for (int n = 0; n < 2; ++n) {
             const float x = exp2_approx(s[m][n][2 * h] - base), y = exp2_approx(s[m][n][2 * h + 1] - base);
             sum[m][h] = fmaf(x, value_back[2 * n], fmaf(y, value_back[2 * n + 1], sum[m][h]));
-            pa[m][h + 2 * n] = pack_half(x, y);
+            pa[m][h + 2 * n] = round2<__half>(x, y);
           }
         }
       // The values: bytes of two keys side by side are the operands of two output tiles.
@@ -457,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
           float l = 0.f;
 #pragma unroll
           for (int i = 0; i < kWarps; ++i)
-            l += stat[i][r][0] == -INFINITY ? 0.f : stat[i][r][1] * exp2_approx(stat[i][r][0] - all);
+            // (Without keys a warp's sum is 0, or NaN of the row's own.)
+            l = fmaf(stat[i][r][1], stat[i][r][0] == -INFINITY ? 0.f : exp2_approx(stat[i][r][0] - all), l);
           row_stat[r][0] = all;
           row_stat[r][1] = l;
         }
@@ -506,36 +489,45 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
   grid_launch_dependents();
   const TreeSize size = tree_size(p, b);
   const int row_tiles = tree_row_tiles(p, size), nt = tree_key_tiles(size);
-  if (at >= p.kv_heads * row_tiles || nt == 1) return;  // (one tile is never cut)
+  if (at >= p.kv_heads * row_tiles) return;
   long long before, total;
   split_prefix(p.batch, -1, b, sums, [&](int i) { return tree_steps(p, i); }, &before, &total);
   const long long first = before + static_cast<long long>(at) * nt;
-  const int c0 = share_of(total, ctas, first), c1 = share_of(total, ctas, first + nt - 1);
-  if (c0 == c1) return;  // written whole
   const int hk = at / row_tiles, row0 = (at - hk * row_tiles) * p.tile_rows;
   const int rows = min(p.tile_rows, size.drafts * p.group - row0);
-  // (With fewer steps than CTAs some shares are empty.)
+  // Of an item of up to half a tile, many rows' CTAs leave two shares (their groups').
+  const int halves = p.many && rows <= p.tile_rows / 2 ? 2 : 1;
+  const int c0 = share_of(total, ctas, first), c1 = share_of(total, ctas, first + nt - 1);
+  if (c0 == c1 && halves == 1) return;  // written whole
+  // (With fewer steps than CTAs some CTAs' shares are empty.)
   const bool gaps = total < ctas;
-  auto empty = [&](int c) {
-    return gaps && share_begin(total, ctas, c) == share_begin(total, ctas, c + 1);
+  // Share i's row of the workspace, or -1.
+  auto share_row = [&](int i, int r) -> long long {
+    const int c = c0 + (halves == 2 ? i >> 1 : i);
+    if (gaps && share_begin(total, ctas, c) == share_begin(total, ctas, c + 1)) return -1;
+    return (2ll * c + (c == c0 ? 1 : 0)) * p.tile_rows + (halves == 2 && (i & 1) ? p.tile_rows / 2 : 0) + r;
   };
+  const int shares = (c1 - c0 + 1) * halves;
   const int words = p.c.head_dim / 4;
   for (int i = blockIdx.y * kTreeJoinThreads + threadIdx.x; i < rows * words;
        i += gridDim.y * kTreeJoinThreads) {
     const int r = i / words, d = (i - r * words) * 4;
     float m = -INFINITY;
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c)
-      if (!empty(c)) m = fmaxf(m, p.part_stat[((2ll * c + (c == c0 ? 1 : 0)) * p.tile_rows + r) * 2]);
+    for (int c = 0; c < shares; ++c) {
+      const long long row = share_row(c, r);
+      if (row >= 0) m = fmaxf(m, p.part_stat[row * 2]);
+    }
     float l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      if (empty(c)) continue;
-      const long long row = (2ll * c + (c == c0 ? 1 : 0)) * p.tile_rows + r;
+    for (int c = 0; c < shares; ++c) {
+      const long long row = share_row(c, r);
+      if (row < 0) continue;
       const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
+      if (st.x == -INFINITY && st.y == 0.f) continue;  // no keys: its rows may not even be written
       const float4 v = *reinterpret_cast<const float4*>(p.part_out + row * 128 + d);
-      const float f = st.x == -INFINITY ? 0.f : exp2_approx(st.x - m);  // (zeros, or NaN of the row's own)
+      const float f = st.x == -INFINITY ? 0.f : exp2_approx(st.x - m);  // (without keys, NaN of the row's own)
       l = fmaf(f, st.y, l);
       a.x = fmaf(f, v.x, a.x);
       a.y = fmaf(f, v.y, a.y);
@@ -571,11 +563,7 @@ cudaError_t few_launch_type(const TreeParams& p, int grid, cudaStream_t stream) 
 
 }  // namespace
 
-int tree_few_ctas(int, int tile_rows) { return tile_rows == 16 ? 3 : 2; }
-
-size_t tree_few_smem(int head_dim, int tile_rows) {
-  return head_dim <= 64 ? few_smem<64>(tile_rows) : few_smem<128>(tile_rows);
-}
+int tree_few_ctas(int tile_rows) { return tile_rows == 16 ? 3 : 2; }
 
 cudaError_t launch_tree_few(const TreeParams& p, int dtype, int grid, cudaStream_t stream) {
   return dtype == CONV_DTYPE_BF16 ? few_launch_type<__nv_bfloat16>(p, grid, stream)

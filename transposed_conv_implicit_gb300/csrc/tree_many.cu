@@ -1,0 +1,679 @@
+// Attention of drafted tokens to the paged 8-bit cache, many rows to a key
+// head, on the tensor cores.
+//
+//   s = scale q K^T,  p = exp(s - max),  out = (p V) / sum p
+//
+// The forward attention's scheme: a softmax group of four warps owns a row
+// tile of 128 (draft, head) rows, one thread per row; S (fp32, TMEM) comes from
+// one tcgen05.mma over the head dimension, the thread writes P (fp16) over it,
+// and the second tcgen05.mma takes P from TMEM against V; the output stays in
+// TMEM and is rescaled only when a row's maximum grows by more than 2^8.
+//
+// The keys come as 8-bit codes from pages of any strides, and the products
+// want 16-bit operands in shared memory: four warps copy codes with cp.async
+// (each lane what it will read itself, two tiles ahead), widen them and store
+// them where TMA would have put 128-byte rows with the 128-byte swizzle.  That
+// is work for each key tile, so a CTA has two softmax groups that share the
+// widened tiles:
+//  - an item of more than 128 rows: the groups are two row tiles;
+//  - an item of up to 128 rows: both groups hold the same rows, and take the
+//    key tiles in turn; each leaves a share of its own for the join.
+// The sequence of all items' key tiles is cut evenly between the CTAs (one per
+// SM), as for few rows.
+//
+// Numbers, as for few rows, but that scales are common to 16 keys: codes become
+// fp16 times their row's scale relative to the largest of the slice of 16 that
+// the row lies in (a key's by 2^-24 at least, a value's by 2^-31: rows further
+// below become 0), whose exponents go to the slice's scores (keys: E) and with
+// the probabilities (values: F): w = 2^(y - M), y = s log2(e) + F, M the running
+// maximum of y less kTreeShift; the sum of probabilities adds 2^-F w.  (With
+// every row's scale applied in fp32 and rounded to the queries' type the
+// widening took 60 instructions for 16 codes, 28 now, and the whole pass 213 us
+// at 16 x 64 drafts x 32 heads against 8192 keys.)
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <type_traits>
+
+#include "tree_common.cuh"
+
+namespace convgb300 {
+
+namespace {
+
+constexpr int kRowsMany = 128;               // of a group
+constexpr int kWordStages = 3;               // widened tiles of keys or values
+constexpr int kCodeStages = 3;               // tiles of codes in flight
+constexpr int kSlotsMany = 4;                // tiles whose validity and scales are kept
+// Two softmax groups, a group of which two warps issue the products, and the
+// widening's group.  Registers of a thread: (176 + 176 + 72 + 88) * 128 = 128 * 512.
+constexpr int kWidenWarps = 4;
+constexpr int kThreadsMany = 32 * (12 + kWidenWarps);
+constexpr int kSlices = kTreeKeys / 16;      // of a tile
+constexpr uint32_t kBlockBytes = 128 * 128;  // 128 keys (or rows) x 64 elements
+
+template <int DP>
+struct Many {
+  static constexpr int kBlocks = DP / 64;
+  static constexpr uint32_t kTile = kBlockBytes * kBlocks;       // a widened tile; a row tile
+  static constexpr int kPieces = 4 * kBlocks;                    // 16-byte words a lane takes of a tile
+  static constexpr uint32_t kCodeWarp = kPieces * 512 + 4 * 128; // a warp's codes and scales of a tile
+  static constexpr uint32_t kOffWords = 2 * kTile;
+  static constexpr uint32_t kOffCodes = kOffWords + kWordStages * kTile;
+  static constexpr uint32_t kOffShared = kOffCodes + kCodeStages * kWidenWarps * kCodeWarp;
+};
+
+struct ManyShared {
+  uint64_t kv_full[kWordStages], kv_empty[kWordStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+  uint64_t drain[2];
+  SplitStart start;
+  uint32_t tmem;
+  int abort_flag;
+  uint32_t valid[kSlotsMany][kWidenWarps];  // keys of a tile that are there
+  // Of a slice: 2^E, F, 2^-F (see above).
+  float4 slice[kSlotsMany][kSlices];
+  int parents[2][kMaxDrafts];
+  uint32_t bits[2][kTreeWords][kRowsMany];  // drafts that a row attends
+};
+
+// 2^-below as fp16, twice; 0 below 2^-24.
+__device__ __forceinline__ uint32_t half_power(int below) {
+  const uint32_t h = below <= 14 ? static_cast<uint32_t>(15 - below) << 10 : below <= 24 ? 1u << (24 - below) : 0u;
+  return h | (h << 16);
+}
+constexpr int kValueLift = 7;  // values stay below 448 2^7 < 65504
+
+// Sixteen codes as fp16 times `factor`.
+__device__ __forceinline__ void widen16(uint4 codes, uint32_t factor, uint4& first, uint4& second) {
+  const uint32_t u[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    widen_codes4(u[i], w[2 * i], w[2 * i + 1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(w[2 * i + j]) : "r"(factor));
+  }
+  first = make_uint4(w[0], w[1], w[2], w[3]);
+  second = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int DP>
+constexpr size_t many_smem() {
+  return Many<DP>::kOffShared + sizeof(ManyShared);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreadsMany, 1)
+    tree_many_kernel(const __grid_constant__ TreeParams p) {
+  using L = Many<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  ManyShared& sh = *reinterpret_cast<ManyShared*>(smem + L::kOffShared);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sh.abort_flag;
+  unsigned int* status = p.status;
+  const long long limit = p.timeout_cycles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kWordStages; ++s) {
+      mbar_init(smem_u32(&sh.kv_full[s]), kWidenWarps);
+      mbar_init(smem_u32(&sh.kv_empty[s]), 2);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(smem_u32(&sh.q_full[g]), 4);
+      mbar_init(smem_u32(&sh.q_empty[g]), 1);
+      mbar_init(smem_u32(&sh.s_full[g]), 1);
+      mbar_init(smem_u32(&sh.p_half[g]), 4);
+      mbar_init(smem_u32(&sh.p_full[g]), 4);
+      mbar_init(smem_u32(&sh.o_done[g]), 1);
+      mbar_init(smem_u32(&sh.drain[g]), 1);
+    }
+    sh.abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&sh.tmem), 512);
+    tmem_relinquish();
+  }
+  grid_dependency_wait();
+  if (warp == 0) {
+    const SplitStart st = split_start(p.batch, -1, lane, [&](int b) { return tree_steps(p, b); });
+    if (lane == 0) sh.start = st;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_launch_dependents();  // (TMEM is held: what starts now cannot take it first)
+  const uint32_t tmem = sh.tmem;
+  const SplitStart start = sh.start;
+  auto wait = [&](uint64_t* bar, uint32_t parity, unsigned int code) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(bar), parity, abort_flag, status, code, limit));
+  };
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------ codes to operands
+    give_registers<88>();
+    const int w4 = warp - 12;
+    const uint32_t codes = smem_u32(smem + L::kOffCodes) + w4 * L::kCodeWarp;
+    // A lane's rows of the warp's two slices (which lie in a page each): row8 and row8 + 8; its 16
+    // codes of each 64: col.  (Two rows of four lanes together store to all banks.)
+    const int row8 = lane >> 2, col = lane & 3;
+    const long long lane_at[2] = {row8 * p.c.ks[1] + col * 16, row8 * p.c.vs[1] + col * 16};
+    TreeWalk lw(p, start);
+    int lt = lw.live ? lw.t0 : 0, lkv = 0;
+    auto page_at = [&](int t, int h) {
+      const int slice = t * kSlices + w4 * 2 + h;
+      return lw.live && slice * 16 < lw.size.keys ? page_of(p.c, lw.b, fast_div(slice, p.div_slices)) : -1;
+    };
+    int page[2] = {page_at(lt, 0), page_at(lt, 1)}, next_page[2] = {-1, -1};
+    auto load = [&](int stage) {
+      if (lw.live) {
+        const uint32_t to = codes + stage * (kWidenWarps * L::kCodeWarp);
+        // (Numbers are chosen, not pointers to them: parameters read through a pointer are slow.)
+        const long long token = lkv ? p.c.vs[1] : p.c.ks[1];
+        const long long step = lkv ? p.c.vs[0] : p.c.ks[0];
+        const uint8_t* head = (lkv ? p.c.v + lane_at[1] : p.c.k + lane_at[0]) +
+                              lw.hk * (lkv ? p.c.vs[2] : p.c.ks[2]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int slice = lt * kSlices + w4 * 2 + h;
+          const int offset = (slice - fast_div(slice, p.div_slices) * static_cast<int>(p.div_slices.d)) * 16;
+          const int keys = page[h] < 0 ? 0 : lw.size.keys - slice * 16;  // of the slice, that are there
+          const int from = page[h] < 0 ? 0 : page[h];
+          const uint8_t* rows = head + from * step + offset * token;
+          const uint8_t* sc = p.c.scales + scale_at(p.c, from, lw.hk, page[h] < 0 ? 0 : offset) + 2 * (row8 & ~1);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool on = 8 * k + row8 < keys;
+#pragma unroll
+            for (int c = 0; c < L::kBlocks; ++c) {
+              const bool ok = on && (c * 4 + col) * 16 < p.c.head_dim;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               to + (((2 * h + k) * L::kBlocks + c) * 32 + lane) * 16),
+                           "l"(rows + k * 8 * token + c * 64), "r"(ok ? 16 : 0)
+                           : "memory");
+            }
+            // The scales of two keys, of which those that are there.
+            const int there = keys - 8 * k - (row8 & ~1);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                             to + L::kPieces * 512 + ((2 * h + k) * 32 + lane) * 4),
+                         "l"(sc + 16 * k), "r"(there >= 2 ? 4 : there == 1 ? 2 : 0)
+                         : "memory");
+          }
+        }
+        // The next tile's pages arrive while this one's values are copied (an item's first ones
+        // are waited for).
+        if (lkv == 0) {
+          if (lt + 1 < lw.t1) {
+            next_page[0] = page_at(lt + 1, 0);
+            next_page[1] = page_at(lt + 1, 1);
+          }
+        } else if (++lt < lw.t1) {
+          page[0] = next_page[0];
+          page[1] = next_page[1];
+        } else {
+          lw.next();
+          lt = lw.live ? lw.t0 : 0;
+          page[0] = page_at(lt, 0);
+          page[1] = page_at(lt, 1);
+        }
+        lkv ^= 1;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kCodeStages - 1; ++i) load(i);
+    bool ok = true;
+    int code_stage = 0, stage = 0;
+    uint32_t phase = 0, tiles = 0;
+    for (TreeWalk w(p, start); ok && w.live; w.next()) {
+      for (int t = w.t0; ok && t < w.t1; ++t, ++tiles) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          load(code_stage == 0 ? kCodeStages - 1 : code_stage - 1);
+          asm volatile("cp.async.wait_group %0;" ::"n"(kCodeStages - 1) : "memory");
+          const uint32_t from = codes + code_stage * (kWidenWarps * L::kCodeWarp);
+          // The rows' bytes (keys', values'; 0 where nothing was written), and the slices' largest.
+          int key_byte[4], value_byte[4], key_most[2], value_most[2];
+          uint32_t there = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t two = lds32(from + L::kPieces * 512 + (k * 32 + lane) * 4) >> (16 * (row8 & 1));
+            key_byte[k] = two & 0xFFu;
+            value_byte[k] = key_byte[k] ? (two >> 8) & 0xFFu : 0;
+            if (key_byte[k]) there |= 1u << (8 * k + row8);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            key_most[h] = __reduce_max_sync(0xFFFFFFFFu, max(key_byte[2 * h], key_byte[2 * h + 1]));
+            value_most[h] = __reduce_max_sync(0xFFFFFFFFu, max(value_byte[2 * h], value_byte[2 * h + 1]));
+          }
+          ok = wait(&sh.kv_empty[stage], phase ^ 1u, kAttnProducerTimeout);
+          if (!ok) break;
+          uint8_t* to = smem + L::kOffWords + stage * L::kTile + (w4 * 32 + row8) * 128;
+#pragma unroll
+          for (int k2 = 0; k2 < 4; k2 += 2) {  // (a slice's words are read together)
+            uint4 u[2][L::kBlocks];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int c = 0; c < L::kBlocks; ++c) {
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(u[k][c].x), "=r"(u[k][c].y), "=r"(u[k][c].z), "=r"(u[k][c].w)
+                             : "r"(from + (((k2 + k) * L::kBlocks + c) * 32 + lane) * 16));
+                // (Rows that were never written may hold NaN.)
+                if (!((there >> (8 * (k2 + k) + row8)) & 1u)) u[k][c] = make_uint4(0, 0, 0, 0);
+              }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t factor = kv ? half_power(value_most[k2 >> 1] - value_byte[k2 + k] - kValueLift)
+                                         : half_power(key_most[k2 >> 1] - key_byte[k2 + k]);
+#pragma unroll
+              for (int c = 0; c < L::kBlocks; ++c) {
+                uint4 a, b;
+                widen16(u[k][c], factor, a, b);
+                uint8_t* row = to + c * kBlockBytes + (k2 + k) * 1024;
+                *reinterpret_cast<uint4*>(row + (((2 * col) ^ row8) << 4)) = a;
+                *reinterpret_cast<uint4*>(row + (((2 * col + 1) ^ row8) << 4)) = b;
+              }
+            }
+          }
+          if (kv == 0) {
+            there = __reduce_or_sync(0xFFFFFFFFu, there);
+            if (lane == 0) sh.valid[tiles % kSlotsMany][w4] = there;
+            if (lane < 2) {
+              const int f = (lane ? value_most[1] : value_most[0]) - 127 - kValueLift;
+              sh.slice[tiles % kSlotsMany][w4 * 2 + lane] =
+                  make_float4(__uint_as_float(static_cast<uint32_t>(lane ? key_most[1] : key_most[0]) << 23), static_cast<float>(f),
+                              __uint_as_float(static_cast<uint32_t>(min(254, 127 - f)) << 23), 0.f);
+            }
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          // (fault_mode 1, a test hook: every CTA leaves its first keys un-announced.)
+          if (lane == 0 && !(p.fault_mode == 1 && tiles == 0 && kv == 0)) mbar_arrive(smem_u32(&sh.kv_full[stage]));
+          code_stage = code_stage == kCodeStages - 1 ? 0 : code_stage + 1;
+          if (++stage == kWordStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else if (warp == 8 || warp == 9) {
+    // ------------------------------------------------------------ products
+    give_registers<72>();
+    const int g = warp - 8;
+    const int k_steps = p.c.head_dim >> 4;
+    const uint32_t idesc_s = attn_idesc(false, kTreeKeys, false, false);
+    const uint32_t idesc_o = attn_idesc(false, static_cast<uint32_t>(p.c.head_dim), false, true);
+    const uint32_t q_lo = kLeadK | ((smem_u32(smem) + g * L::kTile) >> 4);
+    const uint32_t word_lo = smem_u32(smem + L::kOffWords) >> 4;
+    const uint32_t ts = tmem + g * 128, to = tmem + 256 + g * DP;
+    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0, tiles = 0, items = 0;
+    auto advance = [&]() {
+      if (++stage == kWordStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    // A tile's keys, or values, that the other group alone uses.
+    auto pass = [&]() {
+      ok = ok && wait(&sh.kv_full[stage], phase, kAttnMmaTimeout);
+      if (ok && lane == 0) mbar_arrive(smem_u32(&sh.kv_empty[stage]));
+      advance();
+    };
+    for (TreeWalk w(p, start); ok && w.live; w.next()) {
+      const bool single = w.size.drafts * p.group - w.row_tile * p.tile_rows <= kRowsMany;
+      ok = wait(&sh.q_full[g], items & 1u, kAttnMmaTimeout);
+      ++items;
+      // Its own tiles: t, t + step, ...; the others pass.
+      const int step = single ? 2 : 1;
+      int t = w.t0 + (single ? g : 0);
+      auto scores = [&]() {  // of the stage that comes next
+        ok = ok && wait(&sh.kv_full[stage], phase, kAttnMmaTimeout);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t b = kLeadK | (word_lo + stage * (L::kTile >> 4));
+        mma_ss_x4(ts, q_lo, b, idesc_s, 0u, k_steps);
+        if (k_steps > 4) mma_ss_x4(ts, q_lo + (kBlockBytes >> 4), b + (kBlockBytes >> 4), idesc_s, 1u, k_steps - 4);
+        mma_commit_warp(smem_u32(&sh.s_full[g]));
+        mma_commit_warp(smem_u32(&sh.kv_empty[stage]));
+        advance();
+      };
+      if (single && g == 1) {
+        pass();
+        pass();
+      }
+      if (t < w.t1) scores();
+      for (bool first = true; ok && t < w.t1; first = false) {
+        // This tile's values, then the next tile's scores.
+        ok = wait(&sh.kv_full[stage], phase, kAttnMmaTimeout) && wait(&sh.p_half[g], tiles & 1u, kAttnMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t b = lead_mn(kBlockBytes) | (word_lo + stage * (L::kTile >> 4));
+        mma_ts_x4(to, ts, b, idesc_o, first ? 0u : 1u, 4);
+        ok = wait(&sh.p_full[g], tiles & 1u, kAttnMmaTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        mma_ts_x4(to, ts + 32, b + 512u, idesc_o, 1u, 4);
+        ++tiles;
+        mma_commit_warp(smem_u32(&sh.o_done[g]));
+        mma_commit_warp(smem_u32(&sh.kv_empty[stage]));
+        advance();
+        if (single && t + 1 < w.t1) {
+          pass();
+          pass();
+        }
+        t += step;
+        if (t < w.t1) scores();
+      }
+      // (The queries' place is free once these have been read.)
+      mma_commit_warp(smem_u32(&sh.q_empty[g]));
+    }
+    if (!ok) {
+      // Every MMA already issued must finish before TMEM is released.
+      mma_commit_warp(smem_u32(&sh.drain[g]));
+      mbar_wait_drain(smem_u32(&sh.drain[g]), 0, limit / 8 + 1);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    take_registers<176>();
+    const int g = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = tmem + g * 128 + lane_field, to = tmem + 256 + g * DP + lane_field;
+    const uint32_t bar_id = 1 + g;
+    const int d = p.c.head_dim;
+    uint32_t tiles = 0, items = 0, seen = 0;  // own tiles: barrier parity; all tiles: validity's slot
+    bool ok = true;
+    for (TreeWalk w(p, start); ok && w.live; w.next()) {
+      const int left = w.size.drafts * p.group - w.row_tile * p.tile_rows;
+      const bool single = left <= kRowsMany;
+      const int row = w.row_tile * p.tile_rows + (single ? r : g * kRowsMany + r);
+      const bool row_ok = row < w.size.drafts * p.group;
+      const bool warp_ok = __any_sync(0xFFFFFFFFu, row_ok);
+      const int draft = row_ok ? fast_div(row, p.div_group) : 0;
+      const int head = w.hk * p.group + (row_ok ? row - draft * p.group : 0);
+      const int prefix = w.size.keys - w.size.drafts;
+      ok = wait(&sh.q_empty[g], (items & 1u) ^ 1u, kAttnSoftmaxTimeout);
+      ok = barrier_all(bar_id, 128, ok);
+      if (!ok) break;
+      ++items;
+      float rf;  // of the row's scores: scale, and the query's power of two
+      {  // the row's query as fp16, as TMA would place it
+        const uint16_t* q = p.q + w.b * p.qs[0] + draft * p.qs[1] + head * p.qs[2];
+        uint8_t* dst = smem + g * L::kTile + r * 128;
+        uint4 v[8 * L::kBlocks];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8 * L::kBlocks; ++i)
+          v[i] = row_ok && i * 8 < d ? *reinterpret_cast<const uint4*>(q + i * 8) : make_uint4(0, 0, 0, 0);
+        if constexpr (!std::is_same<T, __half>::value)
+#pragma unroll
+          for (int i = 0; i < 8 * L::kBlocks; ++i) {
+            top = fmaxf(top, larger_of(v[i].x));
+            top = fmaxf(top, larger_of(v[i].y));
+            top = fmaxf(top, larger_of(v[i].z));
+            top = fmaxf(top, larger_of(v[i].w));
+          }
+        float back;
+        const float up = row_factor<T>(top, &back);
+        rf = p.scale_log2 * back;
+#pragma unroll
+        for (int i = 0; i < 8 * L::kBlocks; ++i) {
+          if constexpr (!std::is_same<T, __half>::value)
+            v[i] = make_uint4(to_half(v[i].x, up), to_half(v[i].y, up), to_half(v[i].z, up), to_half(v[i].w, up));
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlockBytes + (((i & 7) ^ (r & 7)) << 4)) = v[i];
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[g]));
+      }
+      if (w.t1 * kTreeKeys > prefix) {  // this share comes to the drafts
+        if (p.parents)
+          for (int i = r; i < w.size.drafts; i += 128) sh.parents[g][i] = p.parents[w.b * p.parent_stride + i];
+        named_barrier(bar_id, 128);
+        uint32_t mine[kTreeWords];
+        draft_bits(p.parents ? sh.parents[g] : nullptr, draft, mine);
+#pragma unroll
+        for (int i = 0; i < kTreeWords; ++i) sh.bits[g][i][r] = mine[i];
+      }
+      float mc = -INFINITY, l = 0.f;  // the running maximum less kTreeShift, the sum
+      bool first = true;
+      const int step = single ? 2 : 1;
+      for (int t = w.t0 + (single ? g : 0); t < w.t1; t += step, first = false) {
+        ok = wait(&sh.s_full[g], tiles & 1u, kAttnSoftmaxTimeout);
+        if (!ok) break;
+        tc_fence_after();
+        const int slot = static_cast<int>((seen + t - w.t0) % kSlotsMany);
+        const float4* slices = sh.slice[slot];
+        uint32_t word[4];
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          word[i] = sh.valid[slot][i];
+          all = all && word[i] == 0xFFFFFFFFu;
+        }
+        if ((t + 1) * kTreeKeys > prefix) {
+          all = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // Bits from d0 on: in front of 0 all, behind the row's words none.
+            const int d0 = t * kTreeKeys + 32 * i - prefix, at = d0 >> 5;
+            const uint32_t lo = at < 0 ? 0xFFFFFFFFu : at < kTreeWords ? sh.bits[g][at][r] : 0u;
+            const uint32_t hi = at + 1 < 0 ? 0xFFFFFFFFu : at + 1 < kTreeWords ? sh.bits[g][at + 1][r] : 0u;
+            word[i] &= __funnelshift_r(lo, hi, d0 & 31);
+          }
+        }
+        // The row's running maximum takes in `mx`.
+        auto grow = [&](float mx) __attribute__((always_inline)) {
+          mx -= kTreeShift;
+          if (first) {
+            mc = mx;
+            return;
+          }
+          const bool grown = mx - mc > kTreeLag;  // (false for -inf - -inf = NaN)
+          if (__any_sync(0xFFFFFFFFu, grown)) {
+            float f = 1.f;
+            if (grown) {
+              f = exp2_approx(mc - mx);  // (0 from -inf)
+              mc = mx;
+              l *= f;
+            }
+            // The product of the tile before has to be done.
+            ok = wait(&sh.o_done[g], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < d; c += 16) {  // (16 columns: the scores stay in registers)
+              uint32_t o[16];
+              tmem_ld_x16(to + c, o);
+              tmem_wait_ld_x16(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_x16(to + c, o);
+            }
+            tmem_wait_st();
+          }
+        };
+        // (Not 0, for the sake of scores that are left out: -infinity times it.)
+        auto score_factor = [&](float4 sl) { return fmaxf(sl.x * rf, 1.17549435e-38f); };
+        // A slice's 16 scores from s on: the largest y.
+        auto slice_most = [&](const uint32_t* s, float4 sl) __attribute__((always_inline)) {
+          float x = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+          float y = max3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
+#pragma unroll
+          for (int i = 6; i < 16; i += 4) {
+            x = max3(x, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            if (i + 3 < 16) y = max3(y, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+          }
+          return fmaf(fmaxf(x, y), score_factor(sl), sl.y);
+        };
+        // A slice's probabilities as eight pairs, their sum into l.
+        auto slice_exp = [&](const uint32_t* s, float4 sl, uint32_t* h) __attribute__((always_inline)) {
+          const float f = score_factor(sl), e = sl.y - (mc == -INFINITY ? 0.f : mc);
+          const uint64_t ff = pack2(f, f), ee = pack2(e, e);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, ee), x, y);
+            x = exp2_approx(x);
+            y = exp2_approx(y);
+            sum[i & 1] = add2(sum[i & 1], pack2(x, y));
+            h[i] = round2<__half>(x, y);
+          }
+          float x, y;
+          unpack2(add2(sum[0], sum[1]), x, y);
+          l = fmaf(x + y, sl.z, l);
+        };
+        if (all) {
+          // Straight-line code.  (`all` is the same for the whole warp.)
+          if (warp_ok) {
+            uint32_t s[128];
+            // (The second half of the scores loads beside the first one's maximum.)
+            tmem_ld_x32(ts, s);
+            tmem_ld_x32(ts + 32, s + 32);
+            tmem_wait_ld();
+            tmem_pin<64>(s);
+            tmem_ld_x32(ts + 64, s + 64);
+            tmem_ld_x32(ts + 96, s + 96);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i & 1] = fmaxf(top[i & 1], slice_most(s + 16 * i, slices[i]));
+            tmem_wait_ld();
+            tmem_pin<64>(s + 64);
+#pragma unroll
+            for (int i = 4; i < 8; ++i) top[i & 1] = fmaxf(top[i & 1], slice_most(s + 16 * i, slices[i]));
+            grow(fmaxf(top[0], top[1]));
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t h[16];
+              slice_exp(s + 32 * c, slices[2 * c], h);
+              slice_exp(s + 32 * c + 16, slices[2 * c + 1], h + 8);
+              if (c == 3) {
+                // (By now the stores of the first half have arrived.)
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.p_half[g]));
+              }
+              tmem_st_x16(ts + c * 16, h);
+            }
+            tmem_wait_st();
+          } else if (lane == 0) {
+            mbar_arrive(smem_u32(&sh.p_half[g]));
+          }
+        } else {
+          // Two passes over the scores, 32 at a time.  (P of a chunk lies over scores read before
+          // it is stored.)
+          if (warp_ok) {
+            auto chunk = [&](int c, uint32_t* s) __attribute__((always_inline)) {
+              tmem_ld_x32(ts + c * 32, s);
+              tmem_wait_ld_x32(s);
+              const uint32_t on = c == 0 ? word[0] : c == 1 ? word[1] : c == 2 ? word[2] : word[3];
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((on >> i) & 1u)) s[i] = 0xFF800000u;  // -infinity
+            };
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              chunk(c, s);
+              mx = fmaxf(mx, fmaxf(slice_most(s, slices[2 * c]), slice_most(s + 16, slices[2 * c + 1])));
+            }
+            grow(mx);
+            if (!ok) break;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32], h[16];
+              chunk(c, s);
+              slice_exp(s, slices[2 * c], h);
+              slice_exp(s + 16, slices[2 * c + 1], h + 8);
+              tmem_st_x16(ts + c * 16, h);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_half[g]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[g]));
+        ++tiles;
+      }
+      seen += w.t1 - w.t0;
+      if (ok && !first) ok = wait(&sh.o_done[g], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
+      ok = barrier_all(bar_id, 128, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = !single && w.whole();
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // A share: unnormalised, with its maximum and sum.  (Both groups' shares of one row tile
+      // lie behind one another; one without a tile leaves no rows.)
+      const long long at = (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * (2 * kRowsMany) + g * kRowsMany + r;
+      if (warp_ok && (!first || whole)) {
+        uint16_t* dst = p.out + w.b * p.os[0] + draft * p.os[1] + head * p.os[2];
+#pragma unroll 1
+        for (int c = 0; c < d; c += 32) {
+          uint32_t o[32];
+          tmem_ld_x32(to + c, o);
+          tmem_wait_ld_x32(o);
+          if (row_ok) {
+            if (whole)
+              store_cols(reinterpret_cast<T*>(dst) + c, o, d - c, inv);
+            else
+              store_cols_f32(p.part_out + at * 128 + c, o, d - c, 1.f);
+          }
+        }
+      }
+      if (row_ok) {
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_stat + at * 2) = make_float2(mc, l);
+        else if (p.lse)
+          p.lse[(static_cast<long long>(w.b) * p.heads + head) * p.q_len + draft] =
+              l == 0.f ? -INFINITY : fmaf(mc, kLn2, logf(l));
+      }
+      tc_fence_before();
+    }
+  } else {
+    give_registers<72>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int DP>
+cudaError_t many_launch(const TreeParams& p, int grid, cudaStream_t stream) {
+  static std::atomic<size_t> configured[kMaxDevices];
+  const cudaError_t err = raise_smem(tree_many_kernel<T, DP>, configured, many_smem<DP>());
+  if (err != cudaSuccess) return err;
+  return launch_pdl(tree_many_kernel<T, DP>, dim3(grid), dim3(kThreadsMany), many_smem<DP>(), stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_many(const TreeParams& p, int dtype, int grid, cudaStream_t stream) {
+  if (dtype == CONV_DTYPE_BF16)
+    return p.c.head_dim <= 64 ? many_launch<__nv_bfloat16, 64>(p, grid, stream)
+                              : many_launch<__nv_bfloat16, 128>(p, grid, stream);
+  return p.c.head_dim <= 64 ? many_launch<__half, 64>(p, grid, stream)
+                            : many_launch<__half, 128>(p, grid, stream);
+}
+
+}  // namespace convgb300

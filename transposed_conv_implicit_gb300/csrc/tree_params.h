@@ -36,13 +36,19 @@ struct TreeParams {
   float* part_out;
   float* part_stat;
   int max_tiles;           // most row tiles of a key head
+  bool many;               // tree_many.cu: two shares of items of up to half a tile
+  unsigned int* status;
+  long long timeout_cycles;
+  int fault_mode;          // test hook: 1 = every CTA with work leaves its first keys un-announced
 };
 
 // Few rows (tree_few.cu).
 constexpr int kTreeFewWarps = 4;
-int tree_few_ctas(int head_dim, int tile_rows);  // a SM
-size_t tree_few_smem(int head_dim, int tile_rows);
+int tree_few_ctas(int tile_rows);  // a SM
 cudaError_t launch_tree_few(const TreeParams& p, int dtype, int grid, cudaStream_t stream);
+// Many rows (tree_many.cu): one CTA a SM, row tiles of twice 128 rows.
+constexpr int kTreeManyRows = 256;
+cudaError_t launch_tree_many(const TreeParams& p, int dtype, int grid, cudaStream_t stream);
 // Joins the shares of `ctas` CTAs.
 cudaError_t launch_tree_join(const TreeParams& p, int dtype, int ctas, cudaStream_t stream);
 
