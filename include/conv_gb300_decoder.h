@@ -152,7 +152,7 @@ conv_status_t kv_cache_read(const kv_cache_args_t* args, void* stream);
  * Scores, sums and statistics are fp32.  Codes, queries and probabilities
  * meet in the products as fp16: codes are exact there, a query's row is held
  * times a power of two (elements below 2^-28 of the row's largest are rounded
- * in steps of 2^-39 of it), and probabilities times 2^7 and their value's
+ * in steps of 2^-39 of it), and probabilities times 2^4 and their value's
  * scale relative to the largest of these.  With more than 32 rows (drafts
  * times query heads of a key head) codes are held relative to the largest
  * scale of 16 neighbouring tokens: elements of keys are rounded in steps of

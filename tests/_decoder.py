@@ -162,9 +162,10 @@ class TreeReference:
                 off = F32 * ((d + 2) * s_abs + 4 * (s_abs + base.abs() + 4) + 2 * (ev.abs() + 16)) + low
                 off = torch.where(keep, off, torch.zeros_like(off)).amax(2, keepdim=True)
                 share = 2.0 ** -11 + 2 * off + 2.0 ** -21 + n * F32
-                # Probabilities times their value's scale, below fp16's normal numbers.
+                # Probabilities times their value's scale, below fp16's normal numbers: off by 2^-25 where the
+                # largest is 2^4 at least.
                 weight = torch.where(keep, p * pow2(ev), torch.zeros_like(p))
-                tiny = 2.0 ** -32 * weight.amax(2, keepdim=True) * (
+                tiny = 2.0 ** -29 * weight.amax(2, keepdim=True) * (
                     keep.double() @ (vg * pow2(-ev)[:, None]).abs())
                 tol = u * o.abs() + (1 + u) * share * (p @ vg.abs()) + tiny + grain(u)
                 rows = slice(g * group, (g + 1) * group)

@@ -123,7 +123,9 @@ __device__ __forceinline__ uint32_t to_half(uint32_t v, float up) {
 
 // y = (score in log2 units) + (exponent of the value's scale): probabilities
 // are held as 2^(y - maximum + kTreeShift), see tree_few.cu.  The maximum may
-// lag by kTreeLag, so they stay within 2^15.
-constexpr float kTreeShift = 7.f, kTreeLag = 8.f;
+// lag by kTreeLag, so they stay within 2^15; small ones are rounded in steps of
+// 2^-28 of the largest at worst.  (Rescaling costs a row's whole output: scores
+// of cached keys that differ in size grow by 2^8 now and then, hardly by 2^11.)
+constexpr float kTreeShift = 4.f, kTreeLag = 11.f;
 
 }  // namespace convgb300

@@ -10,7 +10,7 @@
 // TMEM and is rescaled only when a row's maximum grows by more than 2^8.
 //
 // The keys come as 8-bit codes from pages of any strides, and the products
-// want 16-bit operands in shared memory: four warps copy codes with cp.async
+// want 16-bit operands in shared memory: eight warps copy codes with cp.async
 // (each lane what it will read itself, two tiles ahead), widen them and store
 // them where TMA would have put 128-byte rows with the 128-byte swizzle.  That
 // is work for each key tile, so a CTA has two softmax groups that share the
@@ -48,19 +48,19 @@ constexpr int kWordStages = 3;               // widened tiles of keys or values
 constexpr int kCodeStages = 3;               // tiles of codes in flight
 constexpr int kSlotsMany = 4;                // tiles whose validity and scales are kept
 // Two softmax groups, a group of which two warps issue the products, and the
-// widening's group.  Registers of a thread: (176 + 176 + 72 + 88) * 128 = 128 * 512.
-constexpr int kWidenWarps = 4;
+// widening's warps, which take a slice of 16 keys each.  Registers of a thread:
+// (136 + 136 + 64 + 72 + 72) * 128 = 96 * 640.
+constexpr int kWidenWarps = 8;
 constexpr int kThreadsMany = 32 * (12 + kWidenWarps);
-constexpr int kSlices = kTreeKeys / 16;      // of a tile
 constexpr uint32_t kBlockBytes = 128 * 128;  // 128 keys (or rows) x 64 elements
 
 template <int DP>
 struct Many {
   static constexpr int kBlocks = DP / 64;
   static constexpr uint32_t kTile = kBlockBytes * kBlocks;       // a widened tile; a row tile
-  static constexpr int kPieces = 4 * kBlocks;                    // 16-byte words a lane takes of a tile
-  static constexpr uint32_t kCodeWarp = kPieces * 512 + 4 * 128; // a warp's codes and scales of a tile
   static constexpr uint32_t kOffWords = 2 * kTile;
+  static constexpr int kPieces = 2 * kBlocks;                    // 16-byte words a lane takes of a tile
+  static constexpr uint32_t kCodeWarp = kPieces * 512 + 2 * 128; // a warp's codes and scales of a tile
   static constexpr uint32_t kOffCodes = kOffWords + kWordStages * kTile;
   static constexpr uint32_t kOffShared = kOffCodes + kCodeStages * kWidenWarps * kCodeWarp;
 };
@@ -73,9 +73,8 @@ struct ManyShared {
   SplitStart start;
   uint32_t tmem;
   int abort_flag;
-  uint32_t valid[kSlotsMany][kWidenWarps];  // keys of a tile that are there
-  // Of a slice: 2^E, F, 2^-F (see above).
-  float4 slice[kSlotsMany][kSlices];
+  alignas(16) uint16_t valid[kSlotsMany][kWidenWarps];  // keys of a tile that are there
+  alignas(16) float scale[kSlotsMany][3][kWidenWarps];  // of a slice: 2^E, F, 2^-F (see above)
   int parents[2][kMaxDrafts];
   uint32_t bits[2][kTreeWords][kRowsMany];  // drafts that a row attends
 };
@@ -156,70 +155,64 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
 
   if (warp >= 12) {
     // ------------------------------------------------------------ codes to operands
-    give_registers<88>();
-    const int w4 = warp - 12;
-    const uint32_t codes = smem_u32(smem + L::kOffCodes) + w4 * L::kCodeWarp;
-    // A lane's rows of the warp's two slices (which lie in a page each): row8 and row8 + 8; its 16
+    give_registers<72>();
+    const int w8 = warp - 12;
+    const uint32_t codes = smem_u32(smem + L::kOffCodes) + w8 * L::kCodeWarp;
+    // A lane's rows of the warp's slice of 16 (which lies in one page): row8 and row8 + 8; its 16
     // codes of each 64: col.  (Two rows of four lanes together store to all banks.)
     const int row8 = lane >> 2, col = lane & 3;
     const long long lane_at[2] = {row8 * p.c.ks[1] + col * 16, row8 * p.c.vs[1] + col * 16};
     TreeWalk lw(p, start);
     int lt = lw.live ? lw.t0 : 0, lkv = 0;
-    auto page_at = [&](int t, int h) {
-      const int slice = t * kSlices + w4 * 2 + h;
-      return lw.live && slice * 16 < lw.size.keys ? page_of(p.c, lw.b, fast_div(slice, p.div_slices)) : -1;
+    // (As the table has it, so that nothing waits for it before its tile.)
+    auto page_at = [&](int t) {
+      const int slice = t * kWidenWarps + w8;
+      return lw.live && slice * 16 < lw.size.keys
+                 ? p.c.table[lw.b * p.c.table_stride + fast_div(slice, p.div_slices)]
+                 : -1;
     };
-    int page[2] = {page_at(lt, 0), page_at(lt, 1)}, next_page[2] = {-1, -1};
+    int page = page_at(lt), next_page = -1;
     auto load = [&](int stage) {
       if (lw.live) {
-        const uint32_t to = codes + stage * (kWidenWarps * L::kCodeWarp);
+        const int slice = lt * kWidenWarps + w8;
+        const int offset = (slice - fast_div(slice, p.div_slices) * static_cast<int>(p.div_slices.d)) * 16;
+        const bool real = static_cast<unsigned int>(page) < static_cast<unsigned int>(p.c.pages);
+        const int from = real ? page : 0, keys = real ? lw.size.keys - slice * 16 : 0;  // that are there
         // (Numbers are chosen, not pointers to them: parameters read through a pointer are slow.)
         const long long token = lkv ? p.c.vs[1] : p.c.ks[1];
-        const long long step = lkv ? p.c.vs[0] : p.c.ks[0];
-        const uint8_t* head = (lkv ? p.c.v + lane_at[1] : p.c.k + lane_at[0]) +
+        const uint8_t* rows = (lkv ? p.c.v + lane_at[1] : p.c.k + lane_at[0]) +
+                              from * (lkv ? p.c.vs[0] : p.c.ks[0]) + offset * token +
                               lw.hk * (lkv ? p.c.vs[2] : p.c.ks[2]);
+        const uint8_t* sc = p.c.scales + scale_at(p.c, from, lw.hk, real ? offset : 0) + 2 * (row8 & ~1);
+        const uint32_t to = codes + stage * (kWidenWarps * L::kCodeWarp);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int slice = lt * kSlices + w4 * 2 + h;
-          const int offset = (slice - fast_div(slice, p.div_slices) * static_cast<int>(p.div_slices.d)) * 16;
-          const int keys = page[h] < 0 ? 0 : lw.size.keys - slice * 16;  // of the slice, that are there
-          const int from = page[h] < 0 ? 0 : page[h];
-          const uint8_t* rows = head + from * step + offset * token;
-          const uint8_t* sc = p.c.scales + scale_at(p.c, from, lw.hk, page[h] < 0 ? 0 : offset) + 2 * (row8 & ~1);
+        for (int k = 0; k < 2; ++k) {
+          const bool on = 8 * k + row8 < keys;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const bool on = 8 * k + row8 < keys;
-#pragma unroll
-            for (int c = 0; c < L::kBlocks; ++c) {
-              const bool ok = on && (c * 4 + col) * 16 < p.c.head_dim;
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                               to + (((2 * h + k) * L::kBlocks + c) * 32 + lane) * 16),
-                           "l"(rows + k * 8 * token + c * 64), "r"(ok ? 16 : 0)
-                           : "memory");
-            }
-            // The scales of two keys, of which those that are there.
-            const int there = keys - 8 * k - (row8 & ~1);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                             to + L::kPieces * 512 + ((2 * h + k) * 32 + lane) * 4),
-                         "l"(sc + 16 * k), "r"(there >= 2 ? 4 : there == 1 ? 2 : 0)
+          for (int c = 0; c < L::kBlocks; ++c) {
+            const bool ok = on && (c * 4 + col) * 16 < p.c.head_dim;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             to + ((k * L::kBlocks + c) * 32 + lane) * 16),
+                         "l"(rows + k * 8 * token + c * 64), "r"(ok ? 16 : 0)
                          : "memory");
           }
+          // The scales of two keys, of which those that are there.
+          const int there = keys - 8 * k - (row8 & ~1);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                           to + L::kPieces * 512 + (k * 32 + lane) * 4),
+                       "l"(sc + 16 * k), "r"(there >= 2 ? 4 : there == 1 ? 2 : 0)
+                       : "memory");
         }
-        // The next tile's pages arrive while this one's values are copied (an item's first ones
-        // are waited for).
+        // The next tile's page arrives while this one's values are copied (an item's first one
+        // is waited for).
         if (lkv == 0) {
-          if (lt + 1 < lw.t1) {
-            next_page[0] = page_at(lt + 1, 0);
-            next_page[1] = page_at(lt + 1, 1);
-          }
+          if (lt + 1 < lw.t1) next_page = page_at(lt + 1);
         } else if (++lt < lw.t1) {
-          page[0] = next_page[0];
-          page[1] = next_page[1];
+          page = next_page;
         } else {
           lw.next();
           lt = lw.live ? lw.t0 : 0;
-          page[0] = page_at(lt, 0);
-          page[1] = page_at(lt, 1);
+          page = page_at(lt);
         }
         lkv ^= 1;
       }
@@ -237,59 +230,58 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
           load(code_stage == 0 ? kCodeStages - 1 : code_stage - 1);
           asm volatile("cp.async.wait_group %0;" ::"n"(kCodeStages - 1) : "memory");
           const uint32_t from = codes + code_stage * (kWidenWarps * L::kCodeWarp);
-          // The rows' bytes (keys', values'; 0 where nothing was written), and the slices' largest.
-          int key_byte[4], value_byte[4], key_most[2], value_most[2];
-          uint32_t there = 0;
+          uint4 u[2][L::kBlocks];
+          uint32_t two[2];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t two = lds32(from + L::kPieces * 512 + (k * 32 + lane) * 4) >> (16 * (row8 & 1));
-            key_byte[k] = two & 0xFFu;
-            value_byte[k] = key_byte[k] ? (two >> 8) & 0xFFu : 0;
-            if (key_byte[k]) there |= 1u << (8 * k + row8);
-          }
+          for (int k = 0; k < 2; ++k) {
+            two[k] = lds32(from + L::kPieces * 512 + (k * 32 + lane) * 4) >> (16 * (row8 & 1)) & 0xFFFFu;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            key_most[h] = __reduce_max_sync(0xFFFFFFFFu, max(key_byte[2 * h], key_byte[2 * h + 1]));
-            value_most[h] = __reduce_max_sync(0xFFFFFFFFu, max(value_byte[2 * h], value_byte[2 * h + 1]));
+            for (int c = 0; c < L::kBlocks; ++c)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(u[k][c].x), "=r"(u[k][c].y), "=r"(u[k][c].z), "=r"(u[k][c].w)
+                           : "r"(from + ((k * L::kBlocks + c) * 32 + lane) * 16));
           }
           ok = wait(&sh.kv_empty[stage], phase ^ 1u, kAttnProducerTimeout);
           if (!ok) break;
-          uint8_t* to = smem + L::kOffWords + stage * L::kTile + (w4 * 32 + row8) * 128;
+          // The rows' bytes (0 where nothing was written: there may be NaN), and the slice's largest.
+          int key_most = 0, value_most = 0;
+          uint32_t there = 0;
 #pragma unroll
-          for (int k2 = 0; k2 < 4; k2 += 2) {  // (a slice's words are read together)
-            uint4 u[2][L::kBlocks];
+          for (int k = 0; k < 2; ++k) {
+            if (two[k] & 0xFFu) {
+              there |= 1u << (8 * k + row8);
+            } else {
+              two[k] = 0;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int c = 0; c < L::kBlocks; ++c) {
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(u[k][c].x), "=r"(u[k][c].y), "=r"(u[k][c].z), "=r"(u[k][c].w)
-                             : "r"(from + (((k2 + k) * L::kBlocks + c) * 32 + lane) * 16));
-                // (Rows that were never written may hold NaN.)
-                if (!((there >> (8 * (k2 + k) + row8)) & 1u)) u[k][c] = make_uint4(0, 0, 0, 0);
-              }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t factor = kv ? half_power(value_most[k2 >> 1] - value_byte[k2 + k] - kValueLift)
-                                         : half_power(key_most[k2 >> 1] - key_byte[k2 + k]);
-#pragma unroll
-              for (int c = 0; c < L::kBlocks; ++c) {
-                uint4 a, b;
-                widen16(u[k][c], factor, a, b);
-                uint8_t* row = to + c * kBlockBytes + (k2 + k) * 1024;
-                *reinterpret_cast<uint4*>(row + (((2 * col) ^ row8) << 4)) = a;
-                *reinterpret_cast<uint4*>(row + (((2 * col + 1) ^ row8) << 4)) = b;
-              }
+              for (int c = 0; c < L::kBlocks; ++c) u[k][c] = make_uint4(0, 0, 0, 0);
             }
+            key_most = max(key_most, static_cast<int>(two[k] & 0xFFu));
+            value_most = max(value_most, static_cast<int>(two[k] >> 8));
           }
+          key_most = __reduce_max_sync(0xFFFFFFFFu, key_most);
+          value_most = __reduce_max_sync(0xFFFFFFFFu, value_most);
           if (kv == 0) {
             there = __reduce_or_sync(0xFFFFFFFFu, there);
-            if (lane == 0) sh.valid[tiles % kSlotsMany][w4] = there;
-            if (lane < 2) {
-              const int f = (lane ? value_most[1] : value_most[0]) - 127 - kValueLift;
-              sh.slice[tiles % kSlotsMany][w4 * 2 + lane] =
-                  make_float4(__uint_as_float(static_cast<uint32_t>(lane ? key_most[1] : key_most[0]) << 23), static_cast<float>(f),
-                              __uint_as_float(static_cast<uint32_t>(min(254, 127 - f)) << 23), 0.f);
+            if (lane == 0) {
+              const int f = value_most - 127 - kValueLift, slot = tiles % kSlotsMany;
+              sh.valid[slot][w8] = static_cast<uint16_t>(there);
+              sh.scale[slot][0][w8] = __uint_as_float(static_cast<uint32_t>(key_most) << 23);
+              sh.scale[slot][1][w8] = static_cast<float>(f);
+              sh.scale[slot][2][w8] = __uint_as_float(static_cast<uint32_t>(min(254, 127 - f)) << 23);
+            }
+          }
+          uint8_t* to = smem + L::kOffWords + stage * L::kTile + (w8 * 16 + row8) * 128;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t factor = half_power(kv ? value_most - static_cast<int>(two[k] >> 8) - kValueLift
+                                                  : key_most - static_cast<int>(two[k] & 0xFFu));
+#pragma unroll
+            for (int c = 0; c < L::kBlocks; ++c) {
+              uint4 a, b;
+              widen16(u[k][c], factor, a, b);
+              uint8_t* row = to + c * kBlockBytes + k * 1024;
+              *reinterpret_cast<uint4*>(row + (((2 * col) ^ row8) << 4)) = a;
+              *reinterpret_cast<uint4*>(row + (((2 * col + 1) ^ row8) << 4)) = b;
             }
           }
           fence_proxy_async_shared();
@@ -307,7 +299,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   } else if (warp == 8 || warp == 9) {
     // ------------------------------------------------------------ products
-    give_registers<72>();
+    give_registers<64>();
     const int g = warp - 8;
     const int k_steps = p.c.head_dim >> 4;
     const uint32_t idesc_s = attn_idesc(false, kTreeKeys, false, false);
@@ -386,7 +378,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    take_registers<176>();
+    take_registers<136>();
     const int g = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + g * 128 + lane_field, to = tmem + 256 + g * DP + lane_field;
@@ -454,14 +446,22 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
         if (!ok) break;
         tc_fence_after();
         const int slot = static_cast<int>((seen + t - w.t0) % kSlotsMany);
-        const float4* slices = sh.slice[slot];
-        uint32_t word[4];
-        bool all = true;
+        // Of the slices: the factor of their scores (not 0, for the sake of scores that are left
+        // out: -infinity times it), and what goes to their exponents.
+        float factor[8], lift[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          word[i] = sh.valid[slot][i];
-          all = all && word[i] == 0xFFFFFFFFu;
+        for (int i = 0; i < 8; i += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(sh.scale[slot][0] + i);
+          const float4 b = *reinterpret_cast<const float4*>(sh.scale[slot][1] + i);
+          factor[i] = fmaxf(a.x * rf, 1.17549435e-38f);
+          factor[i + 1] = fmaxf(a.y * rf, 1.17549435e-38f);
+          factor[i + 2] = fmaxf(a.z * rf, 1.17549435e-38f);
+          factor[i + 3] = fmaxf(a.w * rf, 1.17549435e-38f);
+          lift[i] = b.x; lift[i + 1] = b.y; lift[i + 2] = b.z; lift[i + 3] = b.w;
         }
+        const uint4 valid4 = *reinterpret_cast<const uint4*>(sh.valid[slot]);
+        uint32_t word[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
+        bool all = (valid4.x & valid4.y & valid4.z & valid4.w) == 0xFFFFFFFFu;
         if ((t + 1) * kTreeKeys > prefix) {
           all = false;
 #pragma unroll
@@ -504,109 +504,84 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
             tmem_wait_st();
           }
         };
-        // (Not 0, for the sake of scores that are left out: -infinity times it.)
-        auto score_factor = [&](float4 sl) { return fmaxf(sl.x * rf, 1.17549435e-38f); };
-        // A slice's 16 scores from s on: the largest y.
-        auto slice_most = [&](const uint32_t* s, float4 sl) __attribute__((always_inline)) {
-          float x = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
-          float y = max3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
+        // Two passes over the scores, 32 columns at a time: the maximum, then P.  (Held in
+        // registers in between they would take those of the widening's warps; a second read of
+        // TMEM costs less.  `all` is the same for the whole warp.)
+        if (warp_ok) {
+          uint32_t s0[32], s1[32];
+          auto left_out = [&](uint32_t on, uint32_t* s) __attribute__((always_inline)) {
 #pragma unroll
-          for (int i = 6; i < 16; i += 4) {
-            x = max3(x, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-            if (i + 3 < 16) y = max3(y, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-          }
-          return fmaf(fmaxf(x, y), score_factor(sl), sl.y);
-        };
-        // A slice's probabilities as eight pairs, their sum into l.
-        auto slice_exp = [&](const uint32_t* s, float4 sl, uint32_t* h) __attribute__((always_inline)) {
-          const float f = score_factor(sl), e = sl.y - (mc == -INFINITY ? 0.f : mc);
-          const uint64_t ff = pack2(f, f), ee = pack2(e, e);
-          uint64_t sum[2] = {0, 0};
+            for (int i = 0; i < 32; ++i)
+              if (!((on >> i) & 1u)) s[i] = 0xFF800000u;  // -infinity
+          };
+          // The largest y of the slice of 16 scores from s on.
+          auto slice_most = [&](const uint32_t* s, int i) __attribute__((always_inline)) {
+            float x = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+            float y = max3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
+            x = max3(x, __uint_as_float(s[6]), __uint_as_float(s[7]));
+            y = max3(y, __uint_as_float(s[8]), __uint_as_float(s[9]));
+            x = max3(x, __uint_as_float(s[10]), __uint_as_float(s[11]));
+            y = max3(y, __uint_as_float(s[12]), __uint_as_float(s[13]));
+            x = max3(x, __uint_as_float(s[14]), __uint_as_float(s[15]));
+            return fmaf(fmaxf(x, y), factor[i], lift[i]);
+          };
+          float top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, ee), x, y);
-            x = exp2_approx(x);
-            y = exp2_approx(y);
-            sum[i & 1] = add2(sum[i & 1], pack2(x, y));
-            h[i] = round2<__half>(x, y);
-          }
-          float x, y;
-          unpack2(add2(sum[0], sum[1]), x, y);
-          l = fmaf(x + y, sl.z, l);
-        };
-        if (all) {
-          // Straight-line code.  (`all` is the same for the whole warp.)
-          if (warp_ok) {
-            uint32_t s[128];
-            // (The second half of the scores loads beside the first one's maximum.)
-            tmem_ld_x32(ts, s);
-            tmem_ld_x32(ts + 32, s + 32);
+          for (int c = 0; c < 4; c += 2) {
+            tmem_ld_x32(ts + c * 32, s0);
+            tmem_ld_x32(ts + c * 32 + 32, s1);
             tmem_wait_ld();
-            tmem_pin<64>(s);
-            tmem_ld_x32(ts + 64, s + 64);
-            tmem_ld_x32(ts + 96, s + 96);
-            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top[i & 1] = fmaxf(top[i & 1], slice_most(s + 16 * i, slices[i]));
+            tmem_pin<32>(s0);
+            tmem_pin<32>(s1);
+            if (!all) {
+              left_out(word[c], s0);
+              left_out(word[c + 1], s1);
+            }
+            top = max3(top, slice_most(s0, 2 * c), slice_most(s0 + 16, 2 * c + 1));
+            top = max3(top, slice_most(s1, 2 * c + 2), slice_most(s1 + 16, 2 * c + 3));
+          }
+          grow(top);
+          if (!ok) break;
+          tmem_ld_x32(ts, s0);
+          const float base = mc == -INFINITY ? 0.f : mc;
+          // P of a chunk lies over scores that were read before it is stored.
+          auto exponentials = [&](int c, uint32_t* s, uint32_t* next) __attribute__((always_inline)) {
             tmem_wait_ld();
-            tmem_pin<64>(s + 64);
+            tmem_pin<32>(s);
+            if (next) tmem_ld_x32(ts + c * 32 + 32, next);
+            if (!all) left_out(word[c], s);
+            uint32_t h[16];
 #pragma unroll
-            for (int i = 4; i < 8; ++i) top[i & 1] = fmaxf(top[i & 1], slice_most(s + 16 * i, slices[i]));
-            grow(fmaxf(top[0], top[1]));
-            if (!ok) break;
+            for (int half = 0; half < 2; ++half) {
+              const float f = factor[2 * c + half], e = lift[2 * c + half] - base;
+              const uint64_t ff = pack2(f, f), ee = pack2(e, e);
+              uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t h[16];
-              slice_exp(s + 32 * c, slices[2 * c], h);
-              slice_exp(s + 32 * c + 16, slices[2 * c + 1], h + 8);
-              if (c == 3) {
-                // (By now the stores of the first half have arrived.)
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.p_half[g]));
+              for (int i = 8 * half; i < 8 * half + 8; ++i) {
+                float x, y;
+                unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, ee), x, y);
+                x = exp2_approx(x);
+                y = exp2_approx(y);
+                sum[i & 1] = add2(sum[i & 1], pack2(x, y));
+                h[i] = round2<__half>(x, y);
               }
-              tmem_st_x16(ts + c * 16, h);
+              float x, y;
+              unpack2(add2(sum[0], sum[1]), x, y);
+              l = fmaf(x + y, sh.scale[slot][2][2 * c + half], l);
             }
-            tmem_wait_st();
-          } else if (lane == 0) {
-            mbar_arrive(smem_u32(&sh.p_half[g]));
-          }
-        } else {
-          // Two passes over the scores, 32 at a time.  (P of a chunk lies over scores read before
-          // it is stored.)
-          if (warp_ok) {
-            auto chunk = [&](int c, uint32_t* s) __attribute__((always_inline)) {
-              tmem_ld_x32(ts + c * 32, s);
-              tmem_wait_ld_x32(s);
-              const uint32_t on = c == 0 ? word[0] : c == 1 ? word[1] : c == 2 ? word[2] : word[3];
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((on >> i) & 1u)) s[i] = 0xFF800000u;  // -infinity
-            };
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              chunk(c, s);
-              mx = fmaxf(mx, fmaxf(slice_most(s, slices[2 * c]), slice_most(s + 16, slices[2 * c + 1])));
-            }
-            grow(mx);
-            if (!ok) break;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32], h[16];
-              chunk(c, s);
-              slice_exp(s, slices[2 * c], h);
-              slice_exp(s + 16, slices[2 * c + 1], h + 8);
-              tmem_st_x16(ts + c * 16, h);
-            }
-            tmem_wait_st();
-          }
+            tmem_st_x16(ts + c * 16, h);
+          };
+          exponentials(0, s0, s1);
+          exponentials(1, s1, s0);
+          exponentials(2, s0, s1);
+          tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.p_half[g]));
+          exponentials(3, s1, nullptr);
+          tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(smem_u32(&sh.p_half[g]));
         }
         tc_fence_before();
         __syncwarp();
@@ -648,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       tc_fence_before();
     }
   } else {
-    give_registers<72>();
+    give_registers<64>();
   }
   tc_fence_before();
   __syncthreads();
