@@ -24,6 +24,7 @@ namespace convgb300 {
 namespace {
 
 constexpr int kCacheThreads = 256;
+constexpr int kCacheRows = 2;  // in flight for each lane
 
 struct CacheParams {
   CacheView c;
@@ -55,26 +56,28 @@ __device__ __forceinline__ uint32_t scale_byte(float top) {
   return top == 0.f ? 127u : static_cast<uint32_t>(max(e, 127 - 64));
 }
 
-// Where a row's token goes: page and offset, or page -1.
-struct Place {
-  int b, i, head, page, offset;
+// A row: request, token, head, and whether it is taken at all.
+struct Row {
+  int b, i, head;
+  bool taken;
 };
-__device__ __forceinline__ Place place_of(const CacheParams& p, int row, bool* taken) {
-  Place o;
-  const int token = fast_div(row, p.div_heads);
-  o.head = row - token * static_cast<int>(p.div_heads.d);
+__device__ __forceinline__ Row row_of(const CacheParams& p, long long row) {
+  Row o{0, 0, 0, false};
+  if (row >= p.rows) return o;
+  const int token = fast_div(static_cast<int>(row), p.div_heads);
+  o.head = static_cast<int>(row) - token * static_cast<int>(p.div_heads.d);
   o.b = fast_div(token, p.div_length);
   o.i = token - o.b * static_cast<int>(p.div_length.d);
-  *taken = !p.lengths || o.i < p.lengths[o.b];
-  o.page = -1;
-  o.offset = 0;
-  const long long at = (p.starts ? static_cast<long long>(p.starts[o.b]) : 0ll) + o.i;
-  if (*taken && at >= 0 && at < static_cast<long long>(p.c.table_width) * p.c.page_size) {
-    const int index = fast_div(static_cast<int>(at), p.c.div_page);
-    o.offset = static_cast<int>(at) - index * p.c.page_size;
-    o.page = page_of(p.c, o.b, index);
-  }
+  o.taken = !p.lengths || o.i < p.lengths[o.b];
   return o;
+}
+// Where the token goes: page and offset, or page -1.
+__device__ __forceinline__ int2 place_of(const CacheParams& p, const Row& o) {
+  const long long at = (p.starts ? static_cast<long long>(p.starts[o.b]) : 0ll) + o.i;
+  if (!o.taken || at < 0 || at >= static_cast<long long>(p.c.table_width) * p.c.page_size)
+    return make_int2(-1, 0);
+  const int index = fast_div(static_cast<int>(at), p.c.div_page);
+  return make_int2(page_of(p.c, o.b, index), static_cast<int>(at) - index * p.c.page_size);
 }
 
 template <typename T>
@@ -109,37 +112,48 @@ __global__ void __launch_bounds__(kCacheThreads)
   const int groups = kCacheThreads / p.lanes;
   grid_dependency_wait();
   grid_launch_dependents();
-  for (long long row0 = static_cast<long long>(blockIdx.x) * groups; row0 < p.rows;
-       row0 += static_cast<long long>(gridDim.x) * groups) {
-    const long long row = row0 + threadIdx.x / p.lanes;
-    bool taken = false;
-    Place o{};
-    o.page = -1;
-    if (row < p.rows) o = place_of(p, static_cast<int>(row), &taken);
-    const bool on = o.page >= 0 && at * 16 < p.c.head_dim;
-    uint4 k[2] = {}, v[2] = {};
-    if (on) {
-      const uint4* kp = reinterpret_cast<const uint4*>(p.k + o.b * p.ks[0] + o.i * p.ks[1] + o.head * p.ks[2]) + 2 * at;
-      const uint4* vp = reinterpret_cast<const uint4*>(p.v + o.b * p.vs[0] + o.i * p.vs[1] + o.head * p.vs[2]) + 2 * at;
-      k[0] = kp[0];
-      k[1] = kp[1];
-      v[0] = vp[0];
-      v[1] = vp[1];
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  const bool lane_on = at * 16 < p.c.head_dim;
+  for (long long row0 = static_cast<long long>(blockIdx.x) * groups; row0 < p.rows; row0 += kCacheRows * step) {
+    // (The elements are asked for before the page, which takes two loads that depend on one another.)
+    Row o[kCacheRows];
+    uint4 k[kCacheRows][2], v[kCacheRows][2];
+    int2 place[kCacheRows];
+#pragma unroll
+    for (int u = 0; u < kCacheRows; ++u) {
+      o[u] = row_of(p, row0 + u * step + threadIdx.x / p.lanes);
+      k[u][0] = k[u][1] = v[u][0] = v[u][1] = make_uint4(0, 0, 0, 0);
+      if (o[u].taken && lane_on) {
+        const uint4* kp =
+            reinterpret_cast<const uint4*>(p.k + o[u].b * p.ks[0] + o[u].i * p.ks[1] + o[u].head * p.ks[2]) + 2 * at;
+        const uint4* vp =
+            reinterpret_cast<const uint4*>(p.v + o[u].b * p.vs[0] + o[u].i * p.vs[1] + o[u].head * p.vs[2]) + 2 * at;
+        k[u][0] = kp[0];
+        k[u][1] = kp[1];
+        v[u][0] = vp[0];
+        v[u][1] = vp[1];
+      }
     }
-    float kt = largest_of<T>(k), vt = largest_of<T>(v);
-    for (int step = p.lanes >> 1; step > 0; step >>= 1) {
-      kt = fmaxf(kt, __shfl_xor_sync(0xFFFFFFFFu, kt, step));
-      vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, step));
+#pragma unroll
+    for (int u = 0; u < kCacheRows; ++u) place[u] = place_of(p, o[u]);
+#pragma unroll
+    for (int u = 0; u < kCacheRows; ++u) {
+      float kt = largest_of<T>(k[u]), vt = largest_of<T>(v[u]);
+      for (int s = p.lanes >> 1; s > 0; s >>= 1) {
+        kt = fmaxf(kt, __shfl_xor_sync(0xFFFFFFFFu, kt, s));
+        vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, s));
+      }
+      const int page = place[u].x, offset = place[u].y;
+      if (page < 0 || !lane_on) continue;
+      const uint32_t kb = scale_byte(kt), vb = scale_byte(vt);
+      *reinterpret_cast<uint4*>(p.c.k + page * p.c.ks[0] + offset * p.c.ks[1] + o[u].head * p.c.ks[2] + at * 16) =
+          quantise<T>(k[u], kb);
+      *reinterpret_cast<uint4*>(p.c.v + page * p.c.vs[0] + offset * p.c.vs[1] + o[u].head * p.c.vs[2] + at * 16) =
+          quantise<T>(v[u], vb);
+      if (at == 0)
+        *reinterpret_cast<uint16_t*>(p.c.scales + scale_at(p.c, page, o[u].head, offset)) =
+            static_cast<uint16_t>(kb | (vb << 8));
     }
-    if (!on) continue;
-    const uint32_t kb = scale_byte(kt), vb = scale_byte(vt);
-    *reinterpret_cast<uint4*>(p.c.k + o.page * p.c.ks[0] + o.offset * p.c.ks[1] + o.head * p.c.ks[2] +
-                              at * 16) = quantise<T>(k, kb);
-    *reinterpret_cast<uint4*>(p.c.v + o.page * p.c.vs[0] + o.offset * p.c.vs[1] + o.head * p.c.vs[2] +
-                              at * 16) = quantise<T>(v, vb);
-    if (at == 0)
-      *reinterpret_cast<uint16_t*>(p.c.scales + scale_at(p.c, o.page, o.head, o.offset)) =
-          static_cast<uint16_t>(kb | (vb << 8));
   }
 }
 
@@ -151,28 +165,42 @@ __global__ void __launch_bounds__(kCacheThreads)
   grid_dependency_wait();
   grid_launch_dependents();
   if (at * 16 >= p.c.head_dim) return;
-  for (long long row = static_cast<long long>(blockIdx.x) * groups + threadIdx.x / p.lanes; row < p.rows;
-       row += static_cast<long long>(gridDim.x) * groups) {
-    bool taken;
-    const Place o = place_of(p, static_cast<int>(row), &taken);
-    if (!taken) continue;
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
-    uint32_t bytes = 0;
-    if (o.page >= 0) {
-      k = *reinterpret_cast<const uint4*>(p.c.k + o.page * p.c.ks[0] + o.offset * p.c.ks[1] +
-                                          o.head * p.c.ks[2] + at * 16);
-      v = *reinterpret_cast<const uint4*>(p.c.v + o.page * p.c.vs[0] + o.offset * p.c.vs[1] +
-                                          o.head * p.c.vs[2] + at * 16);
-      bytes = *reinterpret_cast<const uint16_t*>(p.c.scales + scale_at(p.c, o.page, o.head, o.offset));
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  for (long long row0 = static_cast<long long>(blockIdx.x) * groups; row0 < p.rows; row0 += kCacheRows * step) {
+    Row o[kCacheRows];
+    int2 place[kCacheRows];
+    uint4 k[kCacheRows], v[kCacheRows];
+    uint32_t bytes[kCacheRows];
+#pragma unroll
+    for (int u = 0; u < kCacheRows; ++u) {
+      o[u] = row_of(p, row0 + u * step + threadIdx.x / p.lanes);
+      place[u] = place_of(p, o[u]);
     }
-    if ((bytes & 0xFFu) == 0) {  // nothing was written there
-      k = v = make_uint4(0, 0, 0, 0);
-      bytes = 0;
+#pragma unroll
+    for (int u = 0; u < kCacheRows; ++u) {
+      const int page = place[u].x, offset = place[u].y;
+      k[u] = v[u] = make_uint4(0, 0, 0, 0);
+      bytes[u] = 0;
+      if (page >= 0) {
+        k[u] = *reinterpret_cast<const uint4*>(p.c.k + page * p.c.ks[0] + offset * p.c.ks[1] +
+                                               o[u].head * p.c.ks[2] + at * 16);
+        v[u] = *reinterpret_cast<const uint4*>(p.c.v + page * p.c.vs[0] + offset * p.c.vs[1] +
+                                               o[u].head * p.c.vs[2] + at * 16);
+        bytes[u] = *reinterpret_cast<const uint16_t*>(p.c.scales + scale_at(p.c, page, o[u].head, offset));
+      }
     }
-    uint4* ko = reinterpret_cast<uint4*>(p.k + o.b * p.ks[0] + o.i * p.ks[1] + o.head * p.ks[2]) + 2 * at;
-    uint4* vo = reinterpret_cast<uint4*>(p.v + o.b * p.vs[0] + o.i * p.vs[1] + o.head * p.vs[2]) + 2 * at;
-    restore<T>(k, bytes & 0xFFu, ko[0], ko[1]);
-    restore<T>(v, bytes >> 8, vo[0], vo[1]);
+#pragma unroll
+    for (int u = 0; u < kCacheRows; ++u) {
+      if (!o[u].taken) continue;
+      if ((bytes[u] & 0xFFu) == 0) {  // nothing was written there
+        k[u] = v[u] = make_uint4(0, 0, 0, 0);
+        bytes[u] = 0;
+      }
+      uint4* ko = reinterpret_cast<uint4*>(p.k + o[u].b * p.ks[0] + o[u].i * p.ks[1] + o[u].head * p.ks[2]) + 2 * at;
+      uint4* vo = reinterpret_cast<uint4*>(p.v + o[u].b * p.vs[0] + o[u].i * p.vs[1] + o[u].head * p.vs[2]) + 2 * at;
+      restore<T>(k[u], bytes[u] & 0xFFu, ko[0], ko[1]);
+      restore<T>(v[u], bytes[u] >> 8, vo[0], vo[1]);
+    }
   }
 }
 
@@ -209,7 +237,7 @@ conv_status_t cache_run(const kv_cache_args_t* args, bool write, cudaStream_t st
   const int sms = attn_sm_count();
   if (sms <= 0) return CONV_ERR_CUDA;
   const long long groups = kCacheThreads / p.lanes;
-  const dim3 grid(static_cast<unsigned>(std::min<long long>((p.rows + groups - 1) / groups, 8ll * sms)));
+  const dim3 grid(static_cast<unsigned>(std::min<long long>((p.rows + groups - 1) / groups, 16ll * sms)));
   const auto kernel = a.dtype == CONV_DTYPE_BF16
                           ? (write ? kv_cache_write_kernel<__nv_bfloat16> : kv_cache_read_kernel<__nv_bfloat16>)
                           : (write ? kv_cache_write_kernel<__half> : kv_cache_read_kernel<__half>);

@@ -10,7 +10,9 @@
 // deviations from it and the result come from the same registers.  Lanes take
 // words that are neighbours, and rows go around the groups of the grid.
 //
-// Backward, a lane keeps the same columns in every row, so dw and db add up in
+// Backward, rows come through a ring in shared memory (each lane copies what it
+// will read itself, so nothing waits but for its own copies), two ahead, and
+// a lane keeps the same columns in every row, so dw and db add up in
 // its registers over all rows of its group; groups of a block meet in shared
 // memory and blocks in the workspace, in a fixed order.
 #include <cuda_bf16.h>
@@ -18,8 +20,10 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/conv_gb300_decoder.h"
 #include "attn_internal.h"
@@ -32,7 +36,8 @@ namespace {
 
 constexpr int kMaxChannels = 16384;
 constexpr long long kMaxLnRows = 0x7F000000ll;  // (a step of the grid beyond still counts in 31 bits)
-constexpr int kLnBwdBlocksPerSm = 2;  // rows of partial sums in the workspace
+constexpr int kLnBwdBlocksPerSm = 4;  // rows of partial sums in the workspace
+constexpr int kLnStages = 3;          // rows of a lane in the backward pass's ring
 
 struct LnParams {
   const void *x, *weight, *bias, *dy;
@@ -187,7 +192,7 @@ __device__ __forceinline__ long long row_at(const LnParams& p, int row, const lo
 }
 
 template <typename T, typename W, int kVec, int kWords, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256)
+__global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBlock ? 1 : 3)
     layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
   __shared__ float slots[2][1][32];
   const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
@@ -249,11 +254,27 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256)
   }
 }
 
+__device__ __forceinline__ void ring_copy(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ring_word(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
+}
+
 template <typename T, typename W, int kVec, int kWords, bool kBlock>
 __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
     layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
+  constexpr bool kRing = kVec == 8;
   __shared__ float slots[2][2][32];
-  extern __shared__ float sums[];  // [2][C] where a block has several groups
+  // [kLnStages][2 * kWords][threads] words; then, where a block has several groups, [2][C].
+  extern __shared__ __align__(16) uint8_t shared[];
+  float* sums = reinterpret_cast<float*>(shared);
   const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
   const int at = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (lanes - 1);
   const int groups = kBlock ? 1 : static_cast<int>(blockDim.x) / lanes;
@@ -264,20 +285,65 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
   for (int i = 0; i < kWords * kVec; ++i) dw[i] = db[i] = 0.f;
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int row0 = blockIdx.x * groups; row0 < p.rows; row0 += gridDim.x * groups) {
+  const int step = gridDim.x * groups;
+  const uint32_t ring = smem_u32(shared) + threadIdx.x * 16, pitch = blockDim.x * 16;
+  float stat[2] = {0.f, 0.f}, next_stat[2] = {0.f, 0.f};  // mean and rstd of the next rows, as they are copied
+  auto copy = [&](int row0, int stage) {
     const int row = row0 + group;
-    const bool live = row < p.rows;
+    const bool live = row < p.rows && row0 < p.rows;
     const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
     const uint16_t* dy = static_cast<const uint16_t*>(p.dy) + (live ? row_at(p, row, p.ds) : 0);
-    Word<kVec> rx[kWords], rd[kWords];
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
       const bool on = live && w < p.words;
-      rx[i] = on ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
-      rd[i] = on ? load_word<kVec>(dy + w * kVec) : no_word<kVec>();
+      const uint32_t to = ring + (stage * 2 * kWords + i) * pitch;
+      ring_copy(to, x + (on ? w * kVec : 0), on);
+      ring_copy(to + kWords * pitch, dy + (on ? w * kVec : 0), on);
     }
-    const float mean = live ? p.mean[row] : 0.f, rstd = live ? p.rstd[row] : 0.f;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int stage = 0;
+  if constexpr (kRing) {
+    copy(blockIdx.x * groups, 0);
+    copy(blockIdx.x * groups + step, 1);
+  }
+  if (static_cast<int>(blockIdx.x) * groups + group < p.rows) {
+    next_stat[0] = p.mean[blockIdx.x * groups + group];
+    next_stat[1] = p.rstd[blockIdx.x * groups + group];
+  }
+  for (int row0 = blockIdx.x * groups; row0 < p.rows; row0 += step) {
+    const int row = row0 + group;
+    const bool live = row < p.rows;
+    Word<kVec> rx[kWords], rd[kWords];
+    stat[0] = next_stat[0];
+    stat[1] = next_stat[1];
+    if (row + step < p.rows) {
+      next_stat[0] = p.mean[row + step];
+      next_stat[1] = p.rstd[row + step];
+    }
+    if constexpr (kRing) {
+      copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t from = ring + (stage * 2 * kWords + i) * pitch;
+        rx[i].v = ring_word(from);
+        rd[i].v = ring_word(from + kWords * pitch);
+      }
+      stage = stage == kLnStages - 1 ? 0 : stage + 1;
+    } else {
+      const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
+      const uint16_t* dy = static_cast<const uint16_t*>(p.dy) + (live ? row_at(p, row, p.ds) : 0);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int w = at + i * lanes;
+        const bool on = live && w < p.words;
+        rx[i] = on ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
+        rd[i] = on ? load_word<kVec>(dy + w * kVec) : no_word<kVec>();
+      }
+    }
+    const float mean = stat[0], rstd = stat[1];
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
@@ -317,7 +383,9 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
       store_word<T, kVec>(dx + w * kVec, g);
     }
   }
+  if constexpr (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!p.partial) return;
+  __syncthreads();  // (the sums lie over the ring)
   float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.channels;
   if constexpr (kBlock) {
 #pragma unroll
@@ -359,9 +427,9 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
   }
 }
 
-// Sums the blocks' shares: a block takes 32 columns, its warps every eighth
-// share each, in order.
-constexpr int kSumWarps = 8;
+// Sums the blocks' shares: a block takes 32 columns, its warps every 32nd share
+// each, in order.
+constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps)
     layer_norm_sum_kernel(const __grid_constant__ LnParams p) {
   __shared__ float part[kSumWarps][32];
@@ -400,7 +468,7 @@ LnShape ln_shape(int channels, bool vectors, bool backward) {
   LnShape s{};
   s.vec = vectors ? 8 : 1;
   s.words = channels / s.vec;
-  const int most = !vectors ? 8 : backward ? 5 : 8;
+  const int most = !vectors ? 8 : 5;
   long long best = -1;
   for (int lanes = 32; lanes >= 1; lanes >>= 1) {
     const int per = (s.words + lanes - 1) / lanes;
@@ -424,24 +492,30 @@ LnShape ln_shape(int channels, bool vectors, bool backward) {
   return s;
 }
 
-int ln_bwd_grid(const LnShape& s, int rows, int sms) {
-  const int groups = s.block ? 1 : s.threads / s.lanes;
-  const long long need = (static_cast<long long>(rows) + groups - 1) / groups;
-  return static_cast<int>(std::min<long long>(need, static_cast<long long>(kLnBwdBlocksPerSm) * sms));
-}
+int ln_groups(const LnShape& s) { return s.block ? 1 : s.threads / s.lanes; }
 
 template <typename T, typename W, int kVec, int kWords, bool kBlock>
-cudaError_t ln_launch(const LnParams& p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
+cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
+  const long long need = (static_cast<long long>(p.rows) + ln_groups(s) - 1) / ln_groups(s);
   if (!backward) {
-    const int groups = s.block ? 1 : s.threads / s.lanes;
-    const long long need = (static_cast<long long>(p.rows) + groups - 1) / groups;
-    const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(sms) * (2048 / s.threads)));
+    // (Nothing is kept from row to row: as many blocks as there are rows for.)
+    const int grid = static_cast<int>(std::min<long long>(need, 1 << 20));
     return launch_pdl(layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock>, dim3(grid), dim3(s.threads), 0,
                       stream, p);
   }
-  const size_t smem = s.block ? 0 : static_cast<size_t>(2) * p.channels * sizeof(float);
-  cudaError_t err = launch_pdl(layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock>, dim3(p.blocks),
-                               dim3(s.threads), smem, stream, p);
+  const auto kernel = layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock>;
+  const size_t ring = kVec == 8 ? static_cast<size_t>(kLnStages) * 2 * kWords * s.threads * 16 : 0;
+  const size_t smem = std::max(ring, s.block ? size_t{0} : static_cast<size_t>(2) * p.channels * sizeof(float));
+  static std::atomic<size_t> configured[kMaxDevices];
+  cudaError_t err = raise_smem(kernel, configured, smem);
+  if (err != cudaSuccess) return err;
+  // As many blocks as run at once: each keeps its columns' sums over all of its rows.
+  int fit = 0;
+  err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, s.threads, smem);
+  if (err != cudaSuccess) return err;
+  p.blocks = static_cast<int>(std::min<long long>(
+      need, static_cast<long long>(std::max(1, std::min(fit, kLnBwdBlocksPerSm))) * sms));
+  err = launch_pdl(kernel, dim3(p.blocks), dim3(s.threads), smem, stream, p);
   if (err != cudaSuccess || !p.partial) return err;
   return launch_pdl(layer_norm_sum_kernel, dim3((2 * p.channels + 31) / 32), dim3(32 * kSumWarps), 0,
                     stream, p);
@@ -450,20 +524,27 @@ cudaError_t ln_launch(const LnParams& p, const LnShape& s, bool backward, int sm
 template <typename T, typename W>
 cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, int sms,
                             cudaStream_t stream) {
-  const auto pick = [&](auto words) {
-    constexpr int kWords = decltype(words)::value;
-    return s.vec == 8 ? (s.block ? ln_launch<T, W, 8, (kWords > 4 ? 4 : kWords), true>(p, s, backward, sms, stream)
-                                 : ln_launch<T, W, 8, kWords, false>(p, s, backward, sms, stream))
-                      : (s.block ? ln_launch<T, W, 1, 2 * kWords, true>(p, s, backward, sms, stream)
-                                 : ln_launch<T, W, 1, kWords, false>(p, s, backward, sms, stream));
+  const auto part = [&](auto vec, auto words) {  // rows on a warp's lanes
+    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, false>(p, s, backward, sms, stream);
   };
-  const int n = s.vec == 1 && s.block ? (s.per_lane + 1) / 2 : s.per_lane;
-  if (n <= 1) return pick(std::integral_constant<int, 1>());
-  if (n <= 2) return pick(std::integral_constant<int, 2>());
-  if (n <= 3) return pick(std::integral_constant<int, 3>());
-  if (n <= 4) return pick(std::integral_constant<int, 4>());
-  if (n <= 5) return pick(std::integral_constant<int, 5>());
-  return pick(std::integral_constant<int, 8>());
+  const auto whole = [&](auto vec, auto words) {  // rows on a block
+    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, true>(p, s, backward, sms, stream);
+  };
+  using N1 = std::integral_constant<int, 1>;
+  using N2 = std::integral_constant<int, 2>;
+  using N3 = std::integral_constant<int, 3>;
+  using N4 = std::integral_constant<int, 4>;
+  using N5 = std::integral_constant<int, 5>;
+  using N8 = std::integral_constant<int, 8>;
+  using N16 = std::integral_constant<int, 16>;
+  const int n = s.per_lane;
+  if (s.vec == 8) {
+    if (s.block) return n <= 3 ? whole(N8(), N3()) : whole(N8(), N4());
+    return n == 1 ? part(N8(), N1()) : n == 2 ? part(N8(), N2()) : n == 3 ? part(N8(), N3())
+         : n == 4 ? part(N8(), N4()) : part(N8(), N5());
+  }
+  if (s.block) return n <= 12 ? whole(N1(), std::integral_constant<int, 12>()) : whole(N1(), N16());
+  return n <= 2 ? part(N1(), N2()) : n <= 4 ? part(N1(), N4()) : part(N1(), N8());
 }
 
 bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -542,7 +623,6 @@ conv_status_t ln_run(const layer_norm_args_t* args, bool backward, void* workspa
   p.words = s.words;
   p.lanes = s.lanes;
   if (backward) {
-    p.blocks = ln_bwd_grid(s, p.rows, sms);
     if (sums) p.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + CONV_STATUS_BYTES);
     if (p.rows == 0)  // sums over nothing
       return launch_pdl(layer_norm_sum_kernel, dim3((2 * p.channels + 31) / 32), dim3(32 * kSumWarps),

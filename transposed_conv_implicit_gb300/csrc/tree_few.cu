@@ -477,72 +477,82 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
 }
 
 // Joins the shares of items that the launch cut, in order, with weights
-// 2^(m_c - max m).  A block takes an item.
-constexpr int kTreeJoinThreads = 128;
+// 2^(m_c - max m).  A block takes eight rows of an item, a warp each, whose lanes
+// hold four columns; the shares' slots are listed once per block, so that a
+// row's reads are in flight together (found share by share, with 64-bit
+// divisions, the join of 5 requests x 29 drafts took 45 us).
+constexpr int kTreeJoinRows = 8, kTreeJoinThreads = 32 * kTreeJoinRows;
+constexpr int kTreeMaxShares = 1024;  // of an item: two for each CTA at most
 template <typename T>
 __global__ void __launch_bounds__(kTreeJoinThreads)
     tree_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
   __shared__ long long sums[2][32];
+  __shared__ int slots[kTreeMaxShares];  // rows of the workspace, or -1
+  __shared__ int range[2];
   const int items = p.kv_heads * p.max_tiles;
   const int b = static_cast<int>(blockIdx.x / items), at = static_cast<int>(blockIdx.x - b * items);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
   const TreeSize size = tree_size(p, b);
   const int row_tiles = tree_row_tiles(p, size), nt = tree_key_tiles(size);
   if (at >= p.kv_heads * row_tiles) return;
-  long long before, total;
-  split_prefix(p.batch, -1, b, sums, [&](int i) { return tree_steps(p, i); }, &before, &total);
-  const long long first = before + static_cast<long long>(at) * nt;
   const int hk = at / row_tiles, row0 = (at - hk * row_tiles) * p.tile_rows;
   const int rows = min(p.tile_rows, size.drafts * p.group - row0);
+  if (static_cast<int>(blockIdx.y) * kTreeJoinRows >= rows) return;
   // Of an item of up to half a tile, many rows' CTAs leave two shares (their groups').
   const int halves = p.many && rows <= p.tile_rows / 2 ? 2 : 1;
-  const int c0 = share_of(total, ctas, first), c1 = share_of(total, ctas, first + nt - 1);
-  if (c0 == c1 && halves == 1) return;  // written whole
-  // (With fewer steps than CTAs some CTAs' shares are empty.)
-  const bool gaps = total < ctas;
-  // Share i's row of the workspace, or -1.
-  auto share_row = [&](int i, int r) -> long long {
+  if (nt == 1 && halves == 1) return;  // written whole
+  long long before, total;
+  split_prefix(p.batch, -1, b, sums, [&](int i) { return tree_steps(p, i); }, &before, &total);
+  if (threadIdx.x < 2) {
+    const long long first = before + static_cast<long long>(at) * nt;
+    range[threadIdx.x] = share_of(total, ctas, threadIdx.x ? first + nt - 1 : first);
+  }
+  __syncthreads();
+  const int c0 = range[0], shares = (range[1] - c0 + 1) * halves;
+  if (shares == 1) return;  // written whole
+  for (int i = threadIdx.x; i < shares; i += kTreeJoinThreads) {
     const int c = c0 + (halves == 2 ? i >> 1 : i);
-    if (gaps && share_begin(total, ctas, c) == share_begin(total, ctas, c + 1)) return -1;
-    return (2ll * c + (c == c0 ? 1 : 0)) * p.tile_rows + (halves == 2 && (i & 1) ? p.tile_rows / 2 : 0) + r;
-  };
-  const int shares = (c1 - c0 + 1) * halves;
-  const int words = p.c.head_dim / 4;
-  for (int i = blockIdx.y * kTreeJoinThreads + threadIdx.x; i < rows * words;
-       i += gridDim.y * kTreeJoinThreads) {
-    const int r = i / words, d = (i - r * words) * 4;
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int c = 0; c < shares; ++c) {
-      const long long row = share_row(c, r);
-      if (row >= 0) m = fmaxf(m, p.part_stat[row * 2]);
-    }
-    float l = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = 0; c < shares; ++c) {
-      const long long row = share_row(c, r);
-      if (row < 0) continue;
-      const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
-      if (st.x == -INFINITY && st.y == 0.f) continue;  // no keys: its rows may not even be written
-      const float4 v = *reinterpret_cast<const float4*>(p.part_out + row * 128 + d);
-      const float f = st.x == -INFINITY ? 0.f : exp2_approx(st.x - m);  // (without keys, NaN of the row's own)
-      l = fmaf(f, st.y, l);
-      a.x = fmaf(f, v.x, a.x);
-      a.y = fmaf(f, v.y, a.y);
-      a.z = fmaf(f, v.z, a.z);
-      a.w = fmaf(f, v.w, a.w);
-    }
-    const int draft = fast_div(row0 + r, p.div_group);
-    const int head = hk * p.group + row0 + r - draft * p.group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    // (With fewer steps than CTAs some CTAs' shares are empty.)
+    const bool none = total < ctas && share_begin(total, ctas, c) == share_begin(total, ctas, c + 1);
+    slots[i] = none ? -1 : (2 * c + (c == c0 ? 1 : 0)) * p.tile_rows +
+                               (halves == 2 && (i & 1) ? p.tile_rows / 2 : 0);
+  }
+  __syncthreads();
+  const int r = blockIdx.y * kTreeJoinRows + warp, d = lane * 4;
+  if (r >= rows) return;
+  float m = -INFINITY;
+  for (int c = lane; c < shares; c += 32)
+    if (slots[c] >= 0) m = fmaxf(m, p.part_stat[(static_cast<long long>(slots[c]) + r) * 2]);
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  float l = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool on = d < p.c.head_dim;
+#pragma unroll 8
+  for (int c = 0; c < shares; ++c) {
+    const long long row = max(slots[c], 0) + r;
+    const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
+    const float4 v = on ? *reinterpret_cast<const float4*>(p.part_out + row * 128 + d) : a;
+    // A share without keys leaves no rows, what lies there is not used; one whose maximum is
+    // -infinity all the same holds NaN of the row's own.
+    const bool used = slots[c] >= 0 && !(st.x == -INFINITY && st.y == 0.f);
+    const float f = st.x == -INFINITY ? 0.f : exp2_approx(st.x - m);
+    l = used ? fmaf(f, st.y, l) : l;
+    a.x = used ? fmaf(f, v.x, a.x) : a.x;
+    a.y = used ? fmaf(f, v.y, a.y) : a.y;
+    a.z = used ? fmaf(f, v.z, a.z) : a.z;
+    a.w = used ? fmaf(f, v.w, a.w) : a.w;
+  }
+  const int draft = fast_div(row0 + r, p.div_group);
+  const int head = hk * p.group + row0 + r - draft * p.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (on)
     store4<T>(p.out + b * p.os[0] + draft * p.os[1] + head * p.os[2] + d, a.x * inv, a.y * inv, a.z * inv,
               a.w * inv);
-    if (d == 0 && p.lse)
-      p.lse[(static_cast<long long>(b) * p.heads + head) * p.q_len + draft] =
-          l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));
-  }
+  if (lane == 0 && p.lse)
+    p.lse[(static_cast<long long>(b) * p.heads + head) * p.q_len + draft] =
+        l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));
 }
 
 template <typename T, int DP, int kGroups>
@@ -571,8 +581,9 @@ cudaError_t launch_tree_few(const TreeParams& p, int dtype, int grid, cudaStream
 }
 
 cudaError_t launch_tree_join(const TreeParams& p, int dtype, int ctas, cudaStream_t stream) {
-  const int blocks_y = (p.tile_rows * (p.c.head_dim / 4) + 4 * kTreeJoinThreads - 1) / (4 * kTreeJoinThreads);
-  const dim3 grid(static_cast<unsigned>(p.batch) * p.kv_heads * p.max_tiles, blocks_y);
+  const int rows = std::min(p.tile_rows, p.q_len * p.group);
+  const dim3 grid(static_cast<unsigned>(p.batch) * p.kv_heads * p.max_tiles,
+                  (rows + kTreeJoinRows - 1) / kTreeJoinRows);
   return dtype == CONV_DTYPE_BF16
              ? launch_pdl(tree_join_kernel<__nv_bfloat16>, grid, dim3(kTreeJoinThreads), 0, stream, p, ctas)
              : launch_pdl(tree_join_kernel<__half>, grid, dim3(kTreeJoinThreads), 0, stream, p, ctas);
