@@ -83,18 +83,46 @@ __device__ __forceinline__ int2 place_of(const CacheParams& p, const Row& o) {
 template <typename T>
 __device__ __forceinline__ uint4 quantise(const uint4 (&raw)[2], uint32_t byte) {
   const float f = __uint_as_float((254u - byte) << 23);  // 2^(127 - byte)
+  const uint64_t ff = pack2(f, f);
+  const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint4 r = raw[i >> 1];
-    const float2 a = both((i & 1) ? r.z : r.x, T()), b = both((i & 1) ? r.w : r.y, T());
-    w[i] = round_codes(a.x * f, a.y * f) | (static_cast<uint32_t>(round_codes(b.x * f, b.y * f)) << 16);
+    uint16_t code[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float2 a = both(u[2 * i + j], T());
+      float x, y;
+      unpack2(mul2(pack2(a.x, a.y), ff), x, y);
+      code[j] = round_codes(x, y);
+    }
+    w[i] = code[0] | (static_cast<uint32_t>(code[1]) << 16);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The larger magnitudes of two pairs of numbers; NaN only where both are.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  return r;
+}
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, __half) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  return r;
+}
+// The largest element of a lane's sixteen: among them infinities, or the finite ones.
 template <typename T>
 __device__ __forceinline__ float largest_of(const uint4 (&raw)[2]) {
+  const T t{};
+  const uint32_t a = larger(larger(raw[0].x, raw[0].y, t), larger(raw[0].z, raw[0].w, t), t);
+  const uint32_t b = larger(larger(raw[1].x, raw[1].y, t), larger(raw[1].z, raw[1].w, t), t);
+  const float2 f = both(larger(a, b, t), t);
+  return fmaxf(fmaxf(f.x, f.y), 0.f);  // (0 for NaN)
+}
+template <typename T>
+__device__ __forceinline__ float largest_finite_of(const uint4 (&raw)[2]) {
   const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
   float top = 0.f;
 #pragma unroll
@@ -139,6 +167,10 @@ __global__ void __launch_bounds__(kCacheThreads)
 #pragma unroll
     for (int u = 0; u < kCacheRows; ++u) {
       float kt = largest_of<T>(k[u]), vt = largest_of<T>(v[u]);
+      if (__any_sync(0xFFFFFFFFu, fmaxf(kt, vt) == INFINITY)) {
+        kt = largest_finite_of<T>(k[u]);
+        vt = largest_finite_of<T>(v[u]);
+      }
       for (int s = p.lanes >> 1; s > 0; s >>= 1) {
         kt = fmaxf(kt, __shfl_xor_sync(0xFFFFFFFFu, kt, s));
         vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, s));

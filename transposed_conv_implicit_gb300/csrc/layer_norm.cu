@@ -112,49 +112,71 @@ __device__ __forceinline__ Word<kVec> no_word() {
     w.v = 0;
   return w;
 }
+// Elements as fp32 pairs, so that arithmetic goes two at a time (a single
+// element's pair has a 0).
+template <int kVec>
+struct Pairs {
+  static constexpr int kCount = kVec == 8 ? 4 : 1;
+  uint64_t v[kCount];
+};
 template <typename T, int kVec>
-__device__ __forceinline__ void widen(const Word<kVec>& w, float* f) {
+__device__ __forceinline__ Pairs<kVec> widen(const Word<kVec>& w) {
+  Pairs<kVec> o;
   if constexpr (kVec == 8) {
     const uint32_t u[4] = {w.v.x, w.v.y, w.v.z, w.v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 h = halves(u[i], T());
-      f[2 * i] = h.x;
-      f[2 * i + 1] = h.y;
+      o.v[i] = pack2(h.x, h.y);
     }
   } else {
-    f[0] = to_float(*reinterpret_cast<const T*>(&w.v));
+    o.v[0] = pack2(to_float(*reinterpret_cast<const T*>(&w.v)), 0.f);
   }
+  return o;
 }
 template <typename T, int kVec>
-__device__ __forceinline__ void store_word(uint16_t* p, const float* f) {
-  if constexpr (kVec == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(joined(f[0], f[1], T()), joined(f[2], f[3], T()),
-                                              joined(f[4], f[5], T()), joined(f[6], f[7], T()));
-  } else {
-    *reinterpret_cast<T*>(p) = from_float<T>(f[0]);
+__device__ __forceinline__ void store_word(uint16_t* p, const Pairs<kVec>& o) {
+  uint32_t u[Pairs<kVec>::kCount];
+#pragma unroll
+  for (int i = 0; i < Pairs<kVec>::kCount; ++i) {
+    float a, b;
+    unpack2(o.v[i], a, b);
+    if constexpr (kVec == 8)
+      u[i] = joined(a, b, T());
+    else
+      *reinterpret_cast<T*>(p) = from_float<T>(a);
   }
+  if constexpr (kVec == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 // Elements [at, at + kVec) of weight or bias; `fill` without one.
 template <typename W, int kVec>
-__device__ __forceinline__ void load_weight(const void* w, int at, float fill, float* f) {
+__device__ __forceinline__ Pairs<kVec> load_weight(const void* w, int at, float fill) {
+  Pairs<kVec> o;
   if (!w) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) f[i] = fill;
-    return;
+    for (int i = 0; i < Pairs<kVec>::kCount; ++i) o.v[i] = pack2(fill, fill);
+    return o;
   }
   if constexpr (kVec == 8 && sizeof(W) == 4) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
     const float4 a = __ldg(p), b = __ldg(p + 1);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    o.v[0] = pack2(a.x, a.y);
+    o.v[1] = pack2(a.z, a.w);
+    o.v[2] = pack2(b.x, b.y);
+    o.v[3] = pack2(b.z, b.w);
   } else if constexpr (kVec == 8) {
     Word<8> v;
     v.v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + at));
-    widen<W, 8>(v, f);
+    o = widen<W, 8>(v);
   } else {
-    f[0] = to_float(static_cast<const W*>(w)[at]);
+    o.v[0] = pack2(to_float(static_cast<const W*>(w)[at]), 0.f);
   }
+  return o;
+}
+__device__ __forceinline__ float both_of(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return a + b;
 }
 
 // Sums over the lanes of a row, given to all of them.  kBlock: the row is the
@@ -213,25 +235,30 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
       const int w = at + i * lanes;
       raw[i] = live && w < p.words ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
     }
-    float f[kWords * kVec], sum[1] = {0.f};
+    constexpr int kPairs = Pairs<kVec>::kCount;
+    Pairs<kVec> f[kWords];
+    uint64_t total = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      widen<T, kVec>(raw[i], f + i * kVec);
+      f[i] = widen<T, kVec>(raw[i]);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) sum[0] += f[i * kVec + j];
+      for (int j = 0; j < kPairs; ++j) total = add2(total, f[i].v[j]);
     }
+    float sum[1] = {both_of(total)};
     row_sum<kBlock, 1>(sum, lanes, slots, turn);
     const float mean = sum[0] * p.inv_c;
-    sum[0] = 0.f;
+    const uint64_t minus = pack2(-mean, kVec == 8 ? -mean : 0.f);
+    total = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       if (at + i * lanes < p.words)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          f[i * kVec + j] -= mean;
-          sum[0] = fmaf(f[i * kVec + j], f[i * kVec + j], sum[0]);
+        for (int j = 0; j < kPairs; ++j) {
+          f[i].v[j] = add2(f[i].v[j], minus);
+          total = fma2(f[i].v[j], f[i].v[j], total);
         }
     }
+    sum[0] = both_of(total);
     row_sum<kBlock, 1>(sum, lanes, slots, turn);
     const float rstd = inverse_root(fmaf(sum[0], p.inv_c, p.eps));
     if (!live) continue;
@@ -240,16 +267,16 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
       if (p.rstd) p.rstd[row] = rstd;
     }
     uint16_t* y = static_cast<uint16_t*>(p.y) + row_at(p, row, p.ys);
+    const uint64_t rr = pack2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
       if (w >= p.words) break;
-      float wt[kVec], bs[kVec];
-      load_weight<W, kVec>(p.weight, w * kVec, 1.f, wt);
-      load_weight<W, kVec>(p.bias, w * kVec, 0.f, bs);
+      const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
+      const Pairs<kVec> bs = load_weight<W, kVec>(p.bias, w * kVec, 0.f);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) wt[j] = fmaf(f[i * kVec + j] * rstd, wt[j], bs[j]);
-      store_word<T, kVec>(y + w * kVec, wt);
+      for (int j = 0; j < kPairs; ++j) f[i].v[j] = fma2(mul2(f[i].v[j], rr), wt.v[j], bs.v[j]);
+      store_word<T, kVec>(y + w * kVec, f[i]);
     }
   }
 }
@@ -280,9 +307,10 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
   const int groups = kBlock ? 1 : static_cast<int>(blockDim.x) / lanes;
   const int group = kBlock ? 0 : static_cast<int>(threadIdx.x) / lanes;
   int turn = 0;
-  float dw[kWords * kVec], db[kWords * kVec];
+  constexpr int kPairs = Pairs<kVec>::kCount;
+  uint64_t dw[kWords * kPairs], db[kWords * kPairs];
 #pragma unroll
-  for (int i = 0; i < kWords * kVec; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < kWords * kPairs; ++i) dw[i] = db[i] = 0;
   grid_dependency_wait();
   grid_launch_dependents();
   const int step = gridDim.x * groups;
@@ -344,82 +372,84 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
       }
     }
     const float mean = stat[0], rstd = stat[1];
-    float sum[2] = {0.f, 0.f};
+    // h = x rstd - mean rstd
+    const uint64_t rr = pack2(rstd, rstd), shift = pack2(-mean * rstd, -mean * rstd);
+    uint64_t sum_g = 0, sum_gh = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
       if (w >= p.words) break;
-      float h[kVec], g[kVec], wt[kVec];
-      widen<T, kVec>(rx[i], h);
-      widen<T, kVec>(rd[i], g);
-      load_weight<W, kVec>(p.weight, w * kVec, 1.f, wt);
+      const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
+      const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        h[j] = (h[j] - mean) * rstd;
-        dw[i * kVec + j] = fmaf(g[j], h[j], dw[i * kVec + j]);  // (rows left out hold zeros of dy)
-        db[i * kVec + j] += g[j];
-        g[j] *= wt[j];
-        sum[0] += g[j];
-        sum[1] = fmaf(g[j], h[j], sum[1]);
+      for (int j = 0; j < kPairs; ++j) {
+        const uint64_t h = fma2(x.v[j], rr, shift), f = mul2(g.v[j], wt.v[j]);
+        // (Rows left out hold zeros of dy; so does a single element's other half.)
+        dw[i * kPairs + j] = fma2(g.v[j], h, dw[i * kPairs + j]);
+        db[i * kPairs + j] = add2(db[i * kPairs + j], g.v[j]);
+        sum_g = add2(sum_g, f);
+        sum_gh = fma2(f, h, sum_gh);
       }
     }
+    float sum[2] = {both_of(sum_g), both_of(sum_gh)};
     row_sum<kBlock, 2>(sum, lanes, slots, turn);
     if (!live) continue;
-    const float mg = sum[0] * p.inv_c, mgh = sum[1] * p.inv_c;
+    const float c0 = -rstd * (sum[0] * p.inv_c), c1 = -rstd * (sum[1] * p.inv_c);
+    const uint64_t cc0 = pack2(c0, c0), cc1 = pack2(c1, c1);
     uint16_t* dx = static_cast<uint16_t*>(p.y) + row_at(p, row, p.ys);
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
       if (w >= p.words) break;
-      float h[kVec], g[kVec], wt[kVec];
-      widen<T, kVec>(rx[i], h);
-      widen<T, kVec>(rd[i], g);
-      load_weight<W, kVec>(p.weight, w * kVec, 1.f, wt);
+      const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
+      const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
+      Pairs<kVec> o;
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        h[j] = (h[j] - mean) * rstd;
-        g[j] = rstd * (fmaf(g[j], wt[j], -mg) - h[j] * mgh);
-      }
-      store_word<T, kVec>(dx + w * kVec, g);
+      for (int j = 0; j < kPairs; ++j)
+        o.v[j] = fma2(mul2(g.v[j], wt.v[j]), rr, fma2(fma2(x.v[j], rr, shift), cc1, cc0));
+      store_word<T, kVec>(dx + w * kVec, o);
     }
   }
   if constexpr (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!p.partial) return;
   __syncthreads();  // (the sums lie over the ring)
   float* out = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.channels;
+  // Element w * kVec + e of a lane's sums.
+  auto put = [&](float* to, int w, const uint64_t* v, bool more) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      float a, b;
+      unpack2(v[j], a, b);
+      float* t = to + w * kVec + 2 * j;
+      t[0] = more ? t[0] + a : a;
+      if (kVec == 8) t[1] = more ? t[1] + b : b;
+    }
+  };
   if constexpr (kBlock) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
       if (w >= p.words) break;
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        out[w * kVec + j] = dw[i * kVec + j];
-        out[p.channels + w * kVec + j] = db[i * kVec + j];
-      }
+      put(out, w, dw + i * kPairs, false);
+      put(out + p.channels, w, db + i * kPairs, false);
     }
   } else {
     // The groups of a warp, then the warps one after the other.
-    for (int step = lanes; step < 32; step <<= 1)
+    for (int step_lanes = lanes; step_lanes < 32; step_lanes <<= 1)
 #pragma unroll
-      for (int i = 0; i < kWords * kVec; ++i) {
-        dw[i] += __shfl_xor_sync(0xFFFFFFFFu, dw[i], step);
-        db[i] += __shfl_xor_sync(0xFFFFFFFFu, db[i], step);
+      for (int i = 0; i < kWords * kPairs; ++i) {
+        dw[i] = add2(dw[i], __shfl_xor_sync(0xFFFFFFFFu, dw[i], step_lanes));
+        db[i] = add2(db[i], __shfl_xor_sync(0xFFFFFFFFu, db[i], step_lanes));
       }
     const int warps = static_cast<int>(blockDim.x) >> 5, warp = threadIdx.x >> 5;
-    for (int turn_of = 0; turn_of < warps; ++turn_of) {
-      if (warp == turn_of && (threadIdx.x & 31) < lanes)
+    for (int next = 0; next < warps; ++next) {
+      if (warp == next && (threadIdx.x & 31) < lanes)
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
           const int w = at + i * lanes;
           if (w >= p.words) break;
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) {
-            float* s = sums + w * kVec + j;
-            const float a = dw[i * kVec + j], b = db[i * kVec + j];
-            s[0] = turn_of ? s[0] + a : a;
-            s[p.channels] = turn_of ? s[p.channels] + b : b;
-          }
+          put(sums, w, dw + i * kPairs, next > 0);
+          put(sums + p.channels, w, db + i * kPairs, next > 0);
         }
       __syncthreads();
     }
@@ -484,7 +514,7 @@ LnShape ln_shape(int channels, bool vectors, bool backward) {
   s.threads = backward ? 128 : 256;
   if (best >= 0) return s;
   s.block = true;
-  const int target = !vectors ? 16 : 4;
+  const int target = !vectors ? 8 : 4;
   s.threads = 64;
   while (s.threads < 1024 && (s.words + s.threads - 1) / s.threads > target) s.threads <<= 1;
   s.lanes = s.threads;
@@ -543,7 +573,7 @@ cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, 
     return n == 1 ? part(N8(), N1()) : n == 2 ? part(N8(), N2()) : n == 3 ? part(N8(), N3())
          : n == 4 ? part(N8(), N4()) : part(N8(), N5());
   }
-  if (s.block) return n <= 12 ? whole(N1(), std::integral_constant<int, 12>()) : whole(N1(), N16());
+  if (s.block) return n <= 8 ? whole(N1(), N8()) : whole(N1(), N16());
   return n <= 2 ? part(N1(), N2()) : n <= 4 ? part(N1(), N4()) : part(N1(), N8());
 }
 
