@@ -294,10 +294,15 @@ __device__ __forceinline__ uint4 ring_word(uint32_t src) {
   return v;
 }
 
-template <typename T, typename W, int kVec, int kWords, bool kBlock>
-__global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
+// kWide: rows of blocks of more than 256 threads, which leave a lane no
+// registers to keep its weights and the products of the first pass.  (With
+// them kept, a row of 4096 takes 360 instructions of a warp, 880 without;
+// twice the lanes with two words each: 188 us for both passes over 16381 rows,
+// 153 with four.)
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide>
+__global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512 : 256)
     layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
-  constexpr bool kRing = kVec == 8;
+  constexpr bool kRing = kVec == 8, kKeep = kVec == 8 && !kWide;
   __shared__ float slots[2][2][32];
   // [kLnStages][2 * kWords][threads] words; then, where a block has several groups, [2][C].
   extern __shared__ __align__(16) uint8_t shared[];
@@ -313,6 +318,11 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
   for (int i = 0; i < kWords * kPairs; ++i) dw[i] = db[i] = 0;
   grid_dependency_wait();
   grid_launch_dependents();
+  Pairs<kVec> weight[kKeep ? kWords : 1];
+  if constexpr (kKeep)
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      weight[i] = load_weight<W, kVec>(at + i * lanes < p.words ? p.weight : nullptr, (at + i * lanes) * kVec, 1.f);
   const int step = gridDim.x * groups;
   const uint32_t ring = smem_u32(shared) + threadIdx.x * 16, pitch = blockDim.x * 16;
   float stat[2] = {0.f, 0.f}, next_stat[2] = {0.f, 0.f};  // mean and rstd of the next rows, as they are copied
@@ -375,12 +385,15 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
     // h = x rstd - mean rstd
     const uint64_t rr = pack2(rstd, rstd), shift = pack2(-mean * rstd, -mean * rstd);
     uint64_t sum_g = 0, sum_gh = 0;
+    Pairs<kVec> hs[kKeep ? kWords : 1], fs[kKeep ? kWords : 1];  // h, and dy w
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
       if (w >= p.words) break;
       const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
-      const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
+      Pairs<kVec> wt;
+      if constexpr (kKeep) wt = weight[i];
+      else wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
         const uint64_t h = fma2(x.v[j], rr, shift), f = mul2(g.v[j], wt.v[j]);
@@ -389,6 +402,10 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
         db[i * kPairs + j] = add2(db[i * kPairs + j], g.v[j]);
         sum_g = add2(sum_g, f);
         sum_gh = fma2(f, h, sum_gh);
+        if constexpr (kKeep) {
+          hs[i].v[j] = h;
+          fs[i].v[j] = f;
+        }
       }
     }
     float sum[2] = {both_of(sum_g), both_of(sum_gh)};
@@ -401,12 +418,17 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 128)
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
       if (w >= p.words) break;
-      const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
-      const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
       Pairs<kVec> o;
+      if constexpr (kKeep) {
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j)
-        o.v[j] = fma2(mul2(g.v[j], wt.v[j]), rr, fma2(fma2(x.v[j], rr, shift), cc1, cc0));
+        for (int j = 0; j < kPairs; ++j) o.v[j] = fma2(fs[i].v[j], rr, fma2(hs[i].v[j], cc1, cc0));
+      } else {
+        const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
+        const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j)
+          o.v[j] = fma2(mul2(g.v[j], wt.v[j]), rr, fma2(fma2(x.v[j], rr, shift), cc1, cc0));
+      }
       store_word<T, kVec>(dx + w * kVec, o);
     }
   }
@@ -498,7 +520,7 @@ LnShape ln_shape(int channels, bool vectors, bool backward) {
   LnShape s{};
   s.vec = vectors ? 8 : 1;
   s.words = channels / s.vec;
-  const int most = !vectors ? 8 : 5;
+  const int most = !vectors ? 8 : backward ? 4 : 5;
   long long best = -1;
   for (int lanes = 32; lanes >= 1; lanes >>= 1) {
     const int per = (s.words + lanes - 1) / lanes;
@@ -524,16 +546,9 @@ LnShape ln_shape(int channels, bool vectors, bool backward) {
 
 int ln_groups(const LnShape& s) { return s.block ? 1 : s.threads / s.lanes; }
 
-template <typename T, typename W, int kVec, int kWords, bool kBlock>
-cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
-  const long long need = (static_cast<long long>(p.rows) + ln_groups(s) - 1) / ln_groups(s);
-  if (!backward) {
-    // (Nothing is kept from row to row: as many blocks as there are rows for.)
-    const int grid = static_cast<int>(std::min<long long>(need, 1 << 20));
-    return launch_pdl(layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock>, dim3(grid), dim3(s.threads), 0,
-                      stream, p);
-  }
-  const auto kernel = layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock>;
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide>
+cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms, cudaStream_t stream) {
+  const auto kernel = layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock, kWide>;
   const size_t ring = kVec == 8 ? static_cast<size_t>(kLnStages) * 2 * kWords * s.threads * 16 : 0;
   const size_t smem = std::max(ring, s.block ? size_t{0} : static_cast<size_t>(2) * p.channels * sizeof(float));
   static std::atomic<size_t> configured[kMaxDevices];
@@ -551,14 +566,28 @@ cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cuda
                     stream, p);
 }
 
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide>
+cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
+  const long long need = (static_cast<long long>(p.rows) + ln_groups(s) - 1) / ln_groups(s);
+  if (!backward) {
+    // (Nothing is kept from row to row: as many blocks as there are rows for.)
+    const int grid = static_cast<int>(std::min<long long>(need, 1 << 20));
+    return launch_pdl(layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock>, dim3(grid), dim3(s.threads), 0,
+                      stream, p);
+  }
+  // (Five words a lane are for the forward pass alone: see ln_shape.)
+  if constexpr (kVec == 8 && kWords == 5) return cudaErrorInvalidValue;
+  else return ln_launch_bwd<T, W, kVec, kWords, kBlock, kWide>(p, s, need, sms, stream);
+}
 template <typename T, typename W>
 cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, int sms,
                             cudaStream_t stream) {
   const auto part = [&](auto vec, auto words) {  // rows on a warp's lanes
-    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, false>(p, s, backward, sms, stream);
+    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, false, false>(p, s, backward, sms, stream);
   };
-  const auto whole = [&](auto vec, auto words) {  // rows on a block
-    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, true>(p, s, backward, sms, stream);
+  const auto whole = [&](auto vec, auto words, auto wide) {  // rows on a block
+    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, true, decltype(wide)::value>(
+        p, s, backward, sms, stream);
   };
   using N1 = std::integral_constant<int, 1>;
   using N2 = std::integral_constant<int, 2>;
@@ -569,11 +598,13 @@ cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, 
   using N16 = std::integral_constant<int, 16>;
   const int n = s.per_lane;
   if (s.vec == 8) {
-    if (s.block) return n <= 3 ? whole(N8(), N3()) : whole(N8(), N4());
+    if (s.block && s.threads > 256) return whole(N8(), N4(), std::true_type());
+    if (s.block)
+      return n <= 3 ? whole(N8(), N3(), std::false_type()) : whole(N8(), N4(), std::false_type());
     return n == 1 ? part(N8(), N1()) : n == 2 ? part(N8(), N2()) : n == 3 ? part(N8(), N3())
          : n == 4 ? part(N8(), N4()) : part(N8(), N5());
   }
-  if (s.block) return n <= 8 ? whole(N1(), N8()) : whole(N1(), N16());
+  if (s.block) return n <= 8 ? whole(N1(), N8(), std::false_type()) : whole(N1(), N16(), std::false_type());
   return n <= 2 ? part(N1(), N2()) : n <= 4 ? part(N1(), N4()) : part(N1(), N8());
 }
 
