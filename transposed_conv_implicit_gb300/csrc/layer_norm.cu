@@ -10,9 +10,9 @@
 // deviations from it and the result come from the same registers.  Lanes take
 // words that are neighbours, and rows go around the groups of the grid.
 //
-// Backward, rows come through a ring in shared memory (each lane copies what it
-// will read itself, so nothing waits but for its own copies), two ahead, and
-// a lane keeps the same columns in every row, so dw and db add up in
+// Rows come through a ring in shared memory, two ahead (each lane copies what it
+// will read itself, so nothing waits but for its own copies).  Backward, a lane
+// keeps the same columns in every row, so dw and db add up in
 // its registers over all rows of its group; groups of a block meet in shared
 // memory and blocks in the workspace, in a fixed order.
 #include <cuda_bf16.h>
@@ -37,7 +37,7 @@ namespace {
 constexpr int kMaxChannels = 16384;
 constexpr long long kMaxLnRows = 0x7F000000ll;  // (a step of the grid beyond still counts in 31 bits)
 constexpr int kLnBwdBlocksPerSm = 4;  // rows of partial sums in the workspace
-constexpr int kLnStages = 3;          // rows of a lane in the backward pass's ring
+constexpr int kLnStages = 3;          // rows of a lane in the ring
 
 struct LnParams {
   const void *x, *weight, *bias, *dy;
@@ -213,10 +213,25 @@ __device__ __forceinline__ long long row_at(const LnParams& p, int row, const lo
   return b * s[0] + (row - b * static_cast<int>(p.div_length.d)) * s[1];
 }
 
+__device__ __forceinline__ void ring_copy(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ring_word(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(src)
+               : "memory");
+  return v;
+}
+
 template <typename T, typename W, int kVec, int kWords, bool kBlock>
 __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBlock ? 1 : 3)
     layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
+  constexpr bool kRing = kVec == 8;
   __shared__ float slots[2][1][32];
+  extern __shared__ __align__(16) uint8_t shared[];  // [kLnStages][kWords][threads] words
   const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
   const int at = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (lanes - 1);
   const int groups = kBlock ? 1 : static_cast<int>(blockDim.x) / lanes;
@@ -224,16 +239,43 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
   int turn = 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  // (Every lane goes through every step: groups without a row left load nothing.)
-  for (int row0 = blockIdx.x * groups; row0 < p.rows; row0 += gridDim.x * groups) {
+  const int step = gridDim.x * groups;
+  const uint32_t ring = smem_u32(shared) + threadIdx.x * 16, pitch = blockDim.x * 16;
+  auto copy = [&](int row0, int stage) {
     const int row = row0 + group;
-    const bool live = row < p.rows;
+    const bool live = row0 < p.rows && row < p.rows;
     const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
-    Word<kVec> raw[kWords];
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      raw[i] = live && w < p.words ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
+      const bool on = live && w < p.words;
+      ring_copy(ring + (stage * kWords + i) * pitch, x + (on ? w * kVec : 0), on);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int stage = 0;
+  if constexpr (kRing) {
+    copy(blockIdx.x * groups, 0);
+    copy(blockIdx.x * groups + step, 1);
+  }
+  // (Every lane goes through every step: groups without a row left load nothing.)
+  for (int row0 = blockIdx.x * groups; row0 < p.rows; row0 += step) {
+    const int row = row0 + group;
+    const bool live = row < p.rows;
+    Word<kVec> raw[kWords];
+    if constexpr (kRing) {
+      copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) raw[i].v = ring_word(ring + (stage * kWords + i) * pitch);
+      stage = stage == kLnStages - 1 ? 0 : stage + 1;
+    } else {
+      const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int w = at + i * lanes;
+        raw[i] = live && w < p.words ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
+      }
     }
     constexpr int kPairs = Pairs<kVec>::kCount;
     Pairs<kVec> f[kWords];
@@ -279,19 +321,6 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
       store_word<T, kVec>(y + w * kVec, f[i]);
     }
   }
-}
-
-__device__ __forceinline__ void ring_copy(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ uint4 ring_word(uint32_t src) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(src)
-               : "memory");
-  return v;
 }
 
 // kWide: rows of blocks of more than 256 threads, which leave a lane no
@@ -570,10 +599,16 @@ template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide>
 cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
   const long long need = (static_cast<long long>(p.rows) + ln_groups(s) - 1) / ln_groups(s);
   if (!backward) {
-    // (Nothing is kept from row to row: as many blocks as there are rows for.)
-    const int grid = static_cast<int>(std::min<long long>(need, 1 << 20));
-    return launch_pdl(layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock>, dim3(grid), dim3(s.threads), 0,
-                      stream, p);
+    const auto kernel = layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock>;
+    const size_t smem = kVec == 8 ? static_cast<size_t>(kLnStages) * kWords * s.threads * 16 : 0;
+    static std::atomic<size_t> configured[kMaxDevices];
+    cudaError_t err = raise_smem(kernel, configured, smem);
+    if (err != cudaSuccess) return err;
+    int fit = 0;
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, s.threads, smem);
+    if (err != cudaSuccess) return err;
+    const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(std::max(1, fit)) * sms));
+    return launch_pdl(kernel, dim3(grid), dim3(s.threads), smem, stream, p);
   }
   // (Five words a lane are for the forward pass alone: see ln_shape.)
   if constexpr (kVec == 8 && kWords == 5) return cudaErrorInvalidValue;
