@@ -99,6 +99,9 @@ conv_status_t run(const tree_attention_args_t* args, void* workspace, size_t wor
   p.scale_log2 = a.scale * 1.44269504088896341f;
   p.div_group = make_fast_div(static_cast<uint32_t>(p.group));
   p.div_slices = make_fast_div(static_cast<uint32_t>(a.page_size / 16));
+  p.ks8 = 8 * p.c.ks[1];
+  p.vs8 = 8 * p.c.vs[1];
+  p.scale_page = 2ll * a.kv_heads * a.page_size;
   p.part_out = reinterpret_cast<float*>(static_cast<char*>(workspace) + CONV_STATUS_BYTES);
   p.part_stat = p.part_out + static_cast<size_t>(2) * f.grid * f.tile_rows * 128;
   p.many = f.many;

@@ -59,15 +59,16 @@ constexpr size_t few_smem(int rows) {
   return std::max<size_t>(Few<DP>::kRing, static_cast<size_t>(kWarps) * rows * Few<DP>::kPitch * 4);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
-               : "memory");
-}
+// Copies kBytes, of which `bytes` come from src and the rest is cleared.
 template <int kBytes>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
-               "r"(ok ? kBytes : 0)
-               : "memory");
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, int bytes) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes),
+                 "r"(bytes)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
@@ -130,49 +131,55 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
     // Slices of 16 keys, this warp's every fourth.
     const int end = min(w.t1 * (kTreeKeys / kSlice), (w.size.keys + kSlice - 1) / kSlice);
     int load_at = w.t0 * (kTreeKeys / kSlice) + warp;
-    const uint8_t* k_head = p.c.k + w.hk * p.c.ks[2];
-    const uint8_t* v_head = p.c.v + w.hk * p.c.vs[2];
-    // (The next slice's page is read a slice ahead.)
-    auto page_at = [&](int slice) { return slice < end ? page_of(p.c, w.b, fast_div(slice, p.div_slices)) : -1; };
+    // The lane's part of a slice: rows g and g + 8 of the keys, 2 c4, 2 c4 + 1 and 8 further of the
+    // values, the scales of the latter.
+    const uint8_t* k_lane = p.c.k + w.hk * p.c.ks[2] + g * p.c.ks[1] + c4 * 16;
+    const uint8_t* v_lane = p.c.v + w.hk * p.c.vs[2] + 2 * c4 * p.c.vs[1] + g * L::kValueBytes;
+    const uint8_t* s_lane = p.c.scales + static_cast<long long>(w.hk) * p.c.page_size * 2 + 4 * c4;
+    // Bytes that the lane copies of a row: none behind its end.
+    const int k_bytes[2] = {c4 * 16 < p.c.head_dim ? 16 : 0, (c4 + 4) * 16 < p.c.head_dim ? 16 : 0};
+    const int v_bytes = g * L::kValueBytes < p.c.head_dim ? L::kValueBytes : 0;
+    // (The next slice's page is read a slice ahead, as the table has it, so that nothing waits for it.)
+    const int* table = p.c.table + w.b * p.c.table_stride;
+    auto page_at = [&](int slice) { return slice < end ? table[fast_div(slice, p.div_slices)] : -1; };
     int load_page = page_at(load_at);
     auto load = [&](int stage) {
       if (load_at < end) {
-        const int page = load_page;
+        const bool real = static_cast<unsigned int>(load_page) < static_cast<unsigned int>(p.c.pages);
+        const int page = real ? load_page : 0;
         const int offset = (load_at - fast_div(load_at, p.div_slices) * static_cast<int>(p.div_slices.d)) * kSlice;
-        const int keys = page < 0 ? 0 : w.size.keys - load_at * kSlice;  // of the slice, that are there
+        const int keys = real ? w.size.keys - load_at * kSlice : 0;  // of the slice, that are there
         load_page = page_at(load_at + kWarps);
-        const long long from = page < 0 ? 0 : page;
-        const uint8_t* k = k_head + from * p.c.ks[0] + offset * p.c.ks[1];
-        const uint8_t* v = v_head + from * p.c.vs[0] + offset * p.c.vs[1];
-        const uint32_t dst = ring + stage * L::kStageBytes;
+        const uint8_t* k = k_lane + (page * p.c.ks[0] + offset * p.c.ks[1]);
+        const uint8_t* v = v_lane + (page * p.c.vs[0] + offset * p.c.vs[1]);
+        const uint8_t* sc = s_lane + (page * p.scale_page + offset * 2);
+        const uint32_t dst = ring + stage * L::kStageBytes + lane * 16;
+        const uint32_t dst_v = ring + stage * L::kStageBytes + L::kKeyBytes + lane * L::kValueBytes;
+        const uint32_t dst_s = ring + stage * L::kStageBytes + L::kKeyBytes + 4 * 32 * L::kValueBytes + lane * 8;
+        auto copy = [&](auto whole) __attribute__((always_inline)) {
+          constexpr bool kWhole = decltype(whole)::value;  // all 16 keys are there
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int i = 0; i < L::kKeyWords; ++i) {
-            const int at = (c4 + 4 * i) * 16;
-            copy16(dst + (n * L::kKeyWords + i) * 512 + lane * 16, k + (8 * n + g) * p.c.ks[1] + at,
-                   8 * n + g < keys && at < p.c.head_dim);
+            for (int i = 0; i < L::kKeyWords; ++i)
+              copy_bytes<16>(dst + (n * L::kKeyWords + i) * 512, k + (n ? p.ks8 : 0) + i * 64,
+                             kWhole || 8 * n + g < keys ? k_bytes[i] : 0);
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            copy_bytes<L::kValueBytes>(dst_v + n * 32 * L::kValueBytes,
+                                       v + ((n & 1) ? p.c.vs[1] : 0) + ((n >> 1) ? p.vs8 : 0),
+                                       kWhole || 2 * c4 + (n & 1) + 8 * (n >> 1) < keys ? v_bytes : 0);
+          // (Where a key is not there its byte arrives as 0, which says so.)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int there = keys - (2 * c4 + 8 * n);  // of two keys
+            copy_bytes<4>(dst_s + n * 4, sc + 16 * n, kWhole || there >= 2 ? 4 : there == 1 ? 2 : 0);
           }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int key = 2 * c4 + (n & 1) + 8 * (n >> 1), at = g * L::kValueBytes;
-          const bool on = key < keys && at < p.c.head_dim;
-          const uint32_t to = dst + L::kKeyBytes + (n * 32 + lane) * L::kValueBytes;
-          if constexpr (L::kValueBytes == 16)
-            copy16(to, v + key * p.c.vs[1] + at, on);
-          else
-            copy_small<8>(to, v + key * p.c.vs[1] + at, on);
-        }
-        // (Where a key is not there its byte arrives as 0, which says so.)
-        const uint8_t* s = p.c.scales + scale_at(p.c, page < 0 ? 0 : page, w.hk, offset) + 4 * c4;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int there = keys - (2 * c4 + 8 * n);  // of two keys
-          const uint32_t to = dst + L::kKeyBytes + 4 * 32 * L::kValueBytes + lane * 8 + n * 4;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(s + 16 * n),
-                       "r"(there >= 2 ? 4 : there == 1 ? 2 : 0)
-                       : "memory");
-        }
+        };
+        if (keys >= kSlice)
+          copy(std::true_type());
+        else
+          copy(std::false_type());
       }
       load_at += kWarps;
       copy_commit();
@@ -258,13 +265,14 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
       copy_wait<L::kStages - 2>();
       const uint32_t src = ring + stage * L::kStageBytes;
       // Scores of the slice's keys 2 c4, 2 c4 + 1 (n = 0) and 8 further (n = 1).
-      float s[kGroups][2][4];
+      // (Two chains of products for each, which wait for one another's sums.)
+      float s[kGroups][2][4], odd[kGroups][2][4];
 #pragma unroll
       for (int m = 0; m < kGroups; ++m)
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[m][n][i] = 0.f;
+          for (int i = 0; i < 4; ++i) s[m][n][i] = odd[m][n][i] = 0.f;
 #pragma unroll
       for (int i = 0; i < L::kKeyWords; ++i) {
         uint32_t u[2][4];
@@ -280,9 +288,15 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
             uint32_t b0, b1;
             widen_codes4(u[n][t], b0, b1);
 #pragma unroll
-            for (int m = 0; m < kGroups; ++m) product(s[m][n], qa[m][4 * i + t], b0, b1);
+            for (int m = 0; m < kGroups; ++m)
+              product((t & 1) && kGroups == 1 ? odd[m][n] : s[m][n], qa[m][4 * i + t], b0, b1);
           }
       }
+      if constexpr (kGroups == 1)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[0][n][i] += odd[0][n][i];
       const uint2 bytes = read8(src + L::kKeyBytes + 4 * 32 * L::kValueBytes + lane * 8);
       float key_scale[4], value_exp[4], value_back[4];
       uint32_t there = 0;

@@ -30,6 +30,8 @@ struct TreeParams {
   float scale_log2;        // scale * log2(e)
   FastDiv div_group;
   FastDiv div_slices;      // by slices of 16 keys of a page
+  long long ks8, vs8;      // eight tokens on in the cache
+  long long scale_page;    // bytes of a page's scales
   // Rows whose keys are shared out: [2 * CTAs][tile_rows][128] unnormalised,
   // and their maximum (log2 units) and sum.  A share that begins in the middle
   // of an item leaves its rows in slot 2 c, one that begins with it in 2 c + 1.
