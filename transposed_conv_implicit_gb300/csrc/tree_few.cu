@@ -491,13 +491,14 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
 }
 
 // Joins the shares of items that the launch cut, in order, with weights
-// 2^(m_c - max m).  A block takes eight rows of an item, a warp each, whose lanes
-// hold four columns; the shares' slots are listed once per block, so that a
-// row's reads are in flight together (found share by share, with 64-bit
-// divisions, the join of 5 requests x 29 drafts took 45 us).
-constexpr int kTreeJoinRows = 8, kTreeJoinThreads = 32 * kTreeJoinRows;
+// 2^(m_c - max m).  A warp takes kPer neighbouring rows of an item, whose lanes
+// hold four columns; the shares' slots are listed once per block, before the
+// launch that wrote them has ended, and a row's reads are in flight together.
+// (Found share by share, with 64-bit divisions, the join of 5 requests x 29
+// drafts took 45 us; with a row a warp that of 16 x 64 drafts 25.)
+constexpr int kTreeJoinWarps = 8, kTreeJoinThreads = 32 * kTreeJoinWarps;
 constexpr int kTreeMaxShares = 1024;  // of an item: two for each CTA at most
-template <typename T>
+template <typename T, int kPer>
 __global__ void __launch_bounds__(kTreeJoinThreads)
     tree_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
   __shared__ long long sums[2][32];
@@ -506,67 +507,88 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
   const int items = p.kv_heads * p.max_tiles;
   const int b = static_cast<int>(blockIdx.x / items), at = static_cast<int>(blockIdx.x - b * items);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dependency_wait();
-  grid_launch_dependents();
+  // (The launch before has waited for those in front of it before this one could start: the
+  // lengths are there.)
   const TreeSize size = tree_size(p, b);
   const int row_tiles = tree_row_tiles(p, size), nt = tree_key_tiles(size);
-  if (at >= p.kv_heads * row_tiles) return;
-  const int hk = at / row_tiles, row0 = (at - hk * row_tiles) * p.tile_rows;
+  const int hk = row_tiles > 0 ? at / row_tiles : 0, row0 = (at - hk * row_tiles) * p.tile_rows;
   const int rows = min(p.tile_rows, size.drafts * p.group - row0);
-  if (static_cast<int>(blockIdx.y) * kTreeJoinRows >= rows) return;
+  const int r0 = static_cast<int>(blockIdx.y * kTreeJoinWarps) * kPer;
   // Of an item of up to half a tile, many rows' CTAs leave two shares (their groups').
   const int halves = p.many && rows <= p.tile_rows / 2 ? 2 : 1;
-  if (nt == 1 && halves == 1) return;  // written whole
-  long long before, total;
-  split_prefix(p.batch, -1, b, sums, [&](int i) { return tree_steps(p, i); }, &before, &total);
-  if (threadIdx.x < 2) {
-    const long long first = before + static_cast<long long>(at) * nt;
-    range[threadIdx.x] = share_of(total, ctas, threadIdx.x ? first + nt - 1 : first);
+  int shares = 0;
+  if (at < p.kv_heads * row_tiles && r0 < rows && (nt > 1 || halves > 1)) {
+    long long before, total;
+    split_prefix(p.batch, -1, b, sums, [&](int i) { return tree_steps(p, i); }, &before, &total);
+    if (threadIdx.x < 2) {
+      const long long first = before + static_cast<long long>(at) * nt;
+      range[threadIdx.x] = share_of(total, ctas, threadIdx.x ? first + nt - 1 : first);
+    }
+    __syncthreads();
+    const int c0 = range[0];
+    shares = (range[1] - c0 + 1) * halves;
+    for (int i = threadIdx.x; i < shares; i += kTreeJoinThreads) {
+      const int c = c0 + (halves == 2 ? i >> 1 : i);
+      // (With fewer steps than CTAs some CTAs' shares are empty.)
+      const bool none = total < ctas && share_begin(total, ctas, c) == share_begin(total, ctas, c + 1);
+      slots[i] = none ? -1 : (2 * c + (c == c0 ? 1 : 0)) * p.tile_rows +
+                                 (halves == 2 && (i & 1) ? p.tile_rows / 2 : 0);
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  const int c0 = range[0], shares = (range[1] - c0 + 1) * halves;
-  if (shares == 1) return;  // written whole
-  for (int i = threadIdx.x; i < shares; i += kTreeJoinThreads) {
-    const int c = c0 + (halves == 2 ? i >> 1 : i);
-    // (With fewer steps than CTAs some CTAs' shares are empty.)
-    const bool none = total < ctas && share_begin(total, ctas, c) == share_begin(total, ctas, c + 1);
-    slots[i] = none ? -1 : (2 * c + (c == c0 ? 1 : 0)) * p.tile_rows +
-                               (halves == 2 && (i & 1) ? p.tile_rows / 2 : 0);
-  }
-  __syncthreads();
-  const int r = blockIdx.y * kTreeJoinRows + warp, d = lane * 4;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (shares <= 1) return;  // nothing here, or written whole
+  const int r = r0 + warp * kPer, d = lane * 4;
   if (r >= rows) return;
-  float m = -INFINITY;
-  for (int c = lane; c < shares; c += 32)
-    if (slots[c] >= 0) m = fmaxf(m, p.part_stat[(static_cast<long long>(slots[c]) + r) * 2]);
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float l = 0.f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool on = d < p.c.head_dim;
-#pragma unroll 8
-  for (int c = 0; c < shares; ++c) {
-    const long long row = max(slots[c], 0) + r;
-    const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
-    const float4 v = on ? *reinterpret_cast<const float4*>(p.part_out + row * 128 + d) : a;
-    // A share without keys leaves no rows, what lies there is not used; one whose maximum is
-    // -infinity all the same holds NaN of the row's own.
-    const bool used = slots[c] >= 0 && !(st.x == -INFINITY && st.y == 0.f);
-    const float f = st.x == -INFINITY ? 0.f : exp2_approx(st.x - m);
-    l = used ? fmaf(f, st.y, l) : l;
-    a.x = used ? fmaf(f, v.x, a.x) : a.x;
-    a.y = used ? fmaf(f, v.y, a.y) : a.y;
-    a.z = used ? fmaf(f, v.z, a.z) : a.z;
-    a.w = used ? fmaf(f, v.w, a.w) : a.w;
+  // (Rows past the item's read its last one again and write nothing.)
+  float m[kPer], l[kPer];
+  float4 a[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    m[k] = -INFINITY;
+    l[k] = 0.f;
+    a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const int draft = fast_div(row0 + r, p.div_group);
-  const int head = hk * p.group + row0 + r - draft * p.group;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (on)
-    store4<T>(p.out + b * p.os[0] + draft * p.os[1] + head * p.os[2] + d, a.x * inv, a.y * inv, a.z * inv,
-              a.w * inv);
-  if (lane == 0 && p.lse)
-    p.lse[(static_cast<long long>(b) * p.heads + head) * p.q_len + draft] =
-        l == 0.f ? -INFINITY : fmaf(m, kLn2, logf(l));
+  for (int c = lane; c < shares; c += 32)
+    if (slots[c] >= 0)
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        m[k] = fmaxf(m[k], p.part_stat[(static_cast<long long>(slots[c]) + min(r + k, rows - 1)) * 2]);
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) m[k] = fmaxf(m[k], __shfl_xor_sync(0xFFFFFFFFu, m[k], o));
+#pragma unroll(kPer == 1 ? 8 : 2)
+  for (int c = 0; c < shares; ++c)
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const long long row = max(slots[c], 0) + min(r + k, rows - 1);
+      const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
+      const float4 v = on ? *reinterpret_cast<const float4*>(p.part_out + row * 128 + d) : a[k];
+      // A share without keys leaves no rows, what lies there is not used; one whose maximum is
+      // -infinity all the same holds NaN of the row's own.
+      const bool used = slots[c] >= 0 && !(st.x == -INFINITY && st.y == 0.f);
+      const float f = st.x == -INFINITY ? 0.f : exp2_approx(st.x - m[k]);
+      l[k] = used ? fmaf(f, st.y, l[k]) : l[k];
+      a[k].x = used ? fmaf(f, v.x, a[k].x) : a[k].x;
+      a[k].y = used ? fmaf(f, v.y, a[k].y) : a[k].y;
+      a[k].z = used ? fmaf(f, v.z, a[k].z) : a[k].z;
+      a[k].w = used ? fmaf(f, v.w, a[k].w) : a[k].w;
+    }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    if (r + k >= rows) break;
+    const int draft = fast_div(row0 + r + k, p.div_group);
+    const int head = hk * p.group + row0 + r + k - draft * p.group;
+    const float inv = l[k] == 0.f ? 0.f : 1.f / l[k];
+    if (on)
+      store4<T>(p.out + b * p.os[0] + draft * p.os[1] + head * p.os[2] + d, a[k].x * inv, a[k].y * inv,
+                a[k].z * inv, a[k].w * inv);
+    if (lane == 0 && p.lse)
+      p.lse[(static_cast<long long>(b) * p.heads + head) * p.q_len + draft] =
+          l[k] == 0.f ? -INFINITY : fmaf(m[k], kLn2, logf(l[k]));
+  }
 }
 
 template <typename T, int DP, int kGroups>
@@ -594,13 +616,22 @@ cudaError_t launch_tree_few(const TreeParams& p, int dtype, int grid, cudaStream
                                   : few_launch_type<__half>(p, grid, stream);
 }
 
+template <typename T, int kPer>
+cudaError_t join_launch(const TreeParams& p, int ctas, cudaStream_t stream) {
+  const int rows = std::min(p.tile_rows, p.q_len * p.group), of_block = kTreeJoinWarps * kPer;
+  return launch_pdl(tree_join_kernel<T, kPer>,
+                    dim3(static_cast<unsigned>(p.batch) * p.kv_heads * p.max_tiles, (rows + of_block - 1) / of_block),
+                    dim3(kTreeJoinThreads), 0, stream, p, ctas);
+}
+
 cudaError_t launch_tree_join(const TreeParams& p, int dtype, int ctas, cudaStream_t stream) {
-  const int rows = std::min(p.tile_rows, p.q_len * p.group);
-  const dim3 grid(static_cast<unsigned>(p.batch) * p.kv_heads * p.max_tiles,
-                  (rows + kTreeJoinRows - 1) / kTreeJoinRows);
-  return dtype == CONV_DTYPE_BF16
-             ? launch_pdl(tree_join_kernel<__nv_bfloat16>, grid, dim3(kTreeJoinThreads), 0, stream, p, ctas)
-             : launch_pdl(tree_join_kernel<__half>, grid, dim3(kTreeJoinThreads), 0, stream, p, ctas);
+  // Four rows a warp where there are more rows than warps that run at once: 128 items of 256 rows
+  // 25 us with one, 18 with four; 20 items of 87 rows (18 shares each) 5 and 28.
+  const long long rows = static_cast<long long>(p.batch) * p.q_len * p.heads;
+  const bool four = rows > 64ll * attn_sm_count();
+  if (dtype == CONV_DTYPE_BF16)
+    return four ? join_launch<__nv_bfloat16, 4>(p, ctas, stream) : join_launch<__nv_bfloat16, 1>(p, ctas, stream);
+  return four ? join_launch<__half, 4>(p, ctas, stream) : join_launch<__half, 1>(p, ctas, stream);
 }
 
 }  // namespace convgb300
