@@ -7,7 +7,11 @@
 // tile of 128 (draft, head) rows, one thread per row; S (fp32, TMEM) comes from
 // one tcgen05.mma over the head dimension, the thread writes P (fp16) over it,
 // and the second tcgen05.mma takes P from TMEM against V; the output stays in
-// TMEM and is rescaled only when a row's maximum grows by more than 2^8.
+// TMEM and is rescaled only when a row's maximum grows by more than 2^kTreeLag.
+// A tile of 128 keys goes by halves of 64: while a group's threads turn one
+// half's scores into P, the tensor core multiplies the other's.  (By whole
+// tiles, with the scores read twice, 196 us at 16 x 64 drafts x 32 heads against
+// 8192 keys.)
 //
 // The keys come as 8-bit codes from pages of any strides, and the products
 // want 16-bit operands in shared memory: eight warps copy codes with cp.async
@@ -46,6 +50,7 @@ namespace {
 constexpr int kRowsMany = 128;               // of a group
 constexpr int kWordStages = 3;               // widened tiles of keys or values
 constexpr int kCodeStages = 3;               // tiles of codes in flight
+constexpr int kHalfKeys = 64;                // of a tile: scores and probabilities go by halves
 constexpr int kSlotsMany = 4;                // tiles whose validity and scales are kept
 // Two softmax groups, a group of which two warps issue the products, and the
 // widening's warps, which take a slice of 16 keys each.  Registers of a thread:
@@ -68,7 +73,7 @@ struct Many {
 struct ManyShared {
   uint64_t kv_full[kWordStages], kv_empty[kWordStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+  uint64_t s_full[2][2], p_full[2][2], o_done[2];  // [group][half of a tile]
   uint64_t drain[2];
   SplitStart start;
   uint32_t tmem;
@@ -125,9 +130,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     for (int g = 0; g < 2; ++g) {
       mbar_init(smem_u32(&sh.q_full[g]), 4);
       mbar_init(smem_u32(&sh.q_empty[g]), 1);
-      mbar_init(smem_u32(&sh.s_full[g]), 1);
-      mbar_init(smem_u32(&sh.p_half[g]), 4);
-      mbar_init(smem_u32(&sh.p_full[g]), 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_u32(&sh.s_full[g][h]), 1);
+        mbar_init(smem_u32(&sh.p_full[g][h]), 4);
+      }
       mbar_init(smem_u32(&sh.o_done[g]), 1);
       mbar_init(smem_u32(&sh.drain[g]), 1);
     }
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     give_registers<64>();
     const int g = warp - 8;
     const int k_steps = p.c.head_dim >> 4;
-    const uint32_t idesc_s = attn_idesc(false, kTreeKeys, false, false);
+    const uint32_t idesc_s = attn_idesc(false, kHalfKeys, false, false);
     const uint32_t idesc_o = attn_idesc(false, static_cast<uint32_t>(p.c.head_dim), false, true);
     const uint32_t q_lo = kLeadK | ((smem_u32(smem) + g * L::kTile) >> 4);
     const uint32_t word_lo = smem_u32(smem + L::kOffWords) >> 4;
@@ -322,6 +328,14 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       if (ok && lane == 0) mbar_arrive(smem_u32(&sh.kv_empty[stage]));
       advance();
     };
+    // Scores of a half of the tile whose keys are in stage `at`.
+    auto scores = [&](int at, int half) {
+      const uint32_t b = kLeadK | (word_lo + at * (L::kTile >> 4) + half * (kHalfKeys * 128 >> 4));
+      mma_ss_x4(ts + half * kHalfKeys, q_lo, b, idesc_s, 0u, k_steps);
+      if (k_steps > 4)
+        mma_ss_x4(ts + half * kHalfKeys, q_lo + (kBlockBytes >> 4), b + (kBlockBytes >> 4), idesc_s, 1u, k_steps - 4);
+      mma_commit_warp(smem_u32(&sh.s_full[g][half]));
+    };
     for (TreeWalk w(p, start); ok && w.live; w.next()) {
       const bool single = w.size.drafts * p.group - w.row_tile * p.tile_rows <= kRowsMany;
       ok = wait(&sh.q_full[g], items & 1u, kAttnMmaTimeout);
@@ -329,14 +343,12 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       // Its own tiles: t, t + step, ...; the others pass.
       const int step = single ? 2 : 1;
       int t = w.t0 + (single ? g : 0);
-      auto scores = [&]() {  // of the stage that comes next
+      auto both_scores = [&]() {  // of the stage that comes next
         ok = ok && wait(&sh.kv_full[stage], phase, kAttnMmaTimeout);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t b = kLeadK | (word_lo + stage * (L::kTile >> 4));
-        mma_ss_x4(ts, q_lo, b, idesc_s, 0u, k_steps);
-        if (k_steps > 4) mma_ss_x4(ts, q_lo + (kBlockBytes >> 4), b + (kBlockBytes >> 4), idesc_s, 1u, k_steps - 4);
-        mma_commit_warp(smem_u32(&sh.s_full[g]));
+        scores(stage, 0);
+        scores(stage, 1);
         mma_commit_warp(smem_u32(&sh.kv_empty[stage]));
         advance();
       };
@@ -344,28 +356,41 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
         pass();
         pass();
       }
-      if (t < w.t1) scores();
+      if (t < w.t1) both_scores();
       for (bool first = true; ok && t < w.t1; first = false) {
-        // This tile's values, then the next tile's scores.
-        ok = wait(&sh.kv_full[stage], phase, kAttnMmaTimeout) && wait(&sh.p_half[g], tiles & 1u, kAttnMmaTimeout);
+        // Half of the values, then the next tile's scores in that half's place (softmax has the
+        // other half's scores meanwhile).  Where tiles are taken in turn, the next tile's keys come
+        // when these values have left.
+        const int v_stage = stage;
+        ok = wait(&sh.kv_full[v_stage], phase, kAttnMmaTimeout);
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t b = lead_mn(kBlockBytes) | (word_lo + stage * (L::kTile >> 4));
-        mma_ts_x4(to, ts, b, idesc_o, first ? 0u : 1u, 4);
-        ok = wait(&sh.p_full[g], tiles & 1u, kAttnMmaTimeout);
-        if (!ok) break;
-        tc_fence_after();
-        mma_ts_x4(to, ts + 32, b + 512u, idesc_o, 1u, 4);
-        ++tiles;
-        mma_commit_warp(smem_u32(&sh.o_done[g]));
-        mma_commit_warp(smem_u32(&sh.kv_empty[stage]));
         advance();
+        const bool more = !single && t + 1 < w.t1;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ok = wait(&sh.p_full[g][half], tiles & 1u, kAttnMmaTimeout);
+          if (ok && more && half == 0) ok = wait(&sh.kv_full[stage], phase, kAttnMmaTimeout);
+          if (!ok) break;
+          tc_fence_after();
+          mma_ts_x4(to, ts + half * kHalfKeys,
+                    lead_mn(kBlockBytes) | (word_lo + v_stage * (L::kTile >> 4) + half * (kHalfKeys * 128 >> 4)),
+                    idesc_o, first && half == 0 ? 0u : 1u, 4);
+          mma_commit_warp(smem_u32(&sh.o_done[g]));
+          if (half == 1) mma_commit_warp(smem_u32(&sh.kv_empty[v_stage]));
+          if (more) scores(stage, half);
+        }
+        if (!ok) break;
+        ++tiles;
+        if (more) {
+          mma_commit_warp(smem_u32(&sh.kv_empty[stage]));
+          advance();
+        }
         if (single && t + 1 < w.t1) {
           pass();
           pass();
         }
         t += step;
-        if (t < w.t1) scores();
+        if (single && t < w.t1) both_scores();
       }
       // (The queries' place is free once these have been read.)
       mma_commit_warp(smem_u32(&sh.q_empty[g]));
@@ -385,6 +410,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     const uint32_t bar_id = 1 + g;
     const int d = p.c.head_dim;
     uint32_t tiles = 0, items = 0, seen = 0;  // own tiles: barrier parity; all tiles: validity's slot
+    uint32_t halves = 0;                      // own halves of tiles
     bool ok = true;
     for (TreeWalk w(p, start); ok && w.live; w.next()) {
       const int left = w.size.drafts * p.group - w.row_tile * p.tile_rows;
@@ -441,155 +467,131 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       float mc = -INFINITY, l = 0.f;  // the running maximum less kTreeShift, the sum
       bool first = true;
       const int step = single ? 2 : 1;
-      for (int t = w.t0 + (single ? g : 0); t < w.t1; t += step, first = false) {
-        ok = wait(&sh.s_full[g], tiles & 1u, kAttnSoftmaxTimeout);
-        if (!ok) break;
-        tc_fence_after();
+      for (int t = w.t0 + (single ? g : 0); ok && t < w.t1; t += step) {
         const int slot = static_cast<int>((seen + t - w.t0) % kSlotsMany);
-        // Of the slices: the factor of their scores (not 0, for the sake of scores that are left
-        // out: -infinity times it), and what goes to their exponents.
-        float factor[8], lift[8];
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 a = *reinterpret_cast<const float4*>(sh.scale[slot][0] + i);
-          const float4 b = *reinterpret_cast<const float4*>(sh.scale[slot][1] + i);
-          factor[i] = fmaxf(a.x * rf, 1.17549435e-38f);
-          factor[i + 1] = fmaxf(a.y * rf, 1.17549435e-38f);
-          factor[i + 2] = fmaxf(a.z * rf, 1.17549435e-38f);
-          factor[i + 3] = fmaxf(a.w * rf, 1.17549435e-38f);
-          lift[i] = b.x; lift[i + 1] = b.y; lift[i + 2] = b.z; lift[i + 3] = b.w;
-        }
-        const uint4 valid4 = *reinterpret_cast<const uint4*>(sh.valid[slot]);
-        uint32_t word[4] = {valid4.x, valid4.y, valid4.z, valid4.w};
-        bool all = (valid4.x & valid4.y & valid4.z & valid4.w) == 0xFFFFFFFFu;
-        if ((t + 1) * kTreeKeys > prefix) {
-          all = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // Bits from d0 on: in front of 0 all, behind the row's words none.
-            const int d0 = t * kTreeKeys + 32 * i - prefix, at = d0 >> 5;
-            const uint32_t lo = at < 0 ? 0xFFFFFFFFu : at < kTreeWords ? sh.bits[g][at][r] : 0u;
-            const uint32_t hi = at + 1 < 0 ? 0xFFFFFFFFu : at + 1 < kTreeWords ? sh.bits[g][at + 1][r] : 0u;
-            word[i] &= __funnelshift_r(lo, hi, d0 & 31);
-          }
-        }
-        // The row's running maximum takes in `mx`.
-        auto grow = [&](float mx) __attribute__((always_inline)) {
-          mx -= kTreeShift;
-          if (first) {
-            mc = mx;
-            return;
-          }
-          const bool grown = mx - mc > kTreeLag;  // (false for -inf - -inf = NaN)
-          if (__any_sync(0xFFFFFFFFu, grown)) {
-            float f = 1.f;
-            if (grown) {
-              f = exp2_approx(mc - mx);  // (0 from -inf)
-              mc = mx;
-              l *= f;
-            }
-            // The product of the tile before has to be done.
-            ok = wait(&sh.o_done[g], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
-            if (!ok) return;
-            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < d; c += 16) {  // (16 columns: the scores stay in registers)
-              uint32_t o[16];
-              tmem_ld_x16(to + c, o);
-              tmem_wait_ld_x16(o);
+        for (int half = 0; half < 2; ++half, first = false) {
+          ok = wait(&sh.s_full[g][half], tiles & 1u, kAttnSoftmaxTimeout);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ts_half = ts + half * kHalfKeys;
+          uint32_t s[64];
+          if (warp_ok) {
+            tmem_ld_x32(ts_half, s);
+            tmem_ld_x32(ts_half + 32, s + 32);
+          }
+          // Of the half's slices: the factor of their scores (not 0, for the sake of scores that are
+          // left out: -infinity times it), what goes to their exponents and to their sums.
+          const float4 scale4 = *reinterpret_cast<const float4*>(sh.scale[slot][0] + 4 * half);
+          const float4 lift4 = *reinterpret_cast<const float4*>(sh.scale[slot][1] + 4 * half);
+          const float4 back4 = *reinterpret_cast<const float4*>(sh.scale[slot][2] + 4 * half);
+          const uint2 valid2 = *reinterpret_cast<const uint2*>(sh.valid[slot] + 4 * half);
+          constexpr float kLeast = 1.17549435e-38f;
+          const float factor[4] = {fmaxf(scale4.x * rf, kLeast), fmaxf(scale4.y * rf, kLeast),
+                                   fmaxf(scale4.z * rf, kLeast), fmaxf(scale4.w * rf, kLeast)};
+          const float lift[4] = {lift4.x, lift4.y, lift4.z, lift4.w};
+          const float back[4] = {back4.x, back4.y, back4.z, back4.w};
+          uint32_t word[2] = {valid2.x, valid2.y};
+          bool all = (valid2.x & valid2.y) == 0xFFFFFFFFu;
+          if (t * kTreeKeys + (half + 1) * kHalfKeys > prefix) {
+            all = false;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st_x16(to + c, o);
+            for (int i = 0; i < 2; ++i) {
+              // Bits from d0 on: in front of 0 all, behind the row's words none.
+              const int d0 = t * kTreeKeys + half * kHalfKeys + 32 * i - prefix, at = d0 >> 5;
+              const uint32_t lo = at < 0 ? 0xFFFFFFFFu : at < kTreeWords ? sh.bits[g][at][r] : 0u;
+              const uint32_t hi = at + 1 < 0 ? 0xFFFFFFFFu : at + 1 < kTreeWords ? sh.bits[g][at + 1][r] : 0u;
+              word[i] &= __funnelshift_r(lo, hi, d0 & 31);
+            }
+          }
+          if (warp_ok) {
+            tmem_wait_ld();
+            tmem_pin<64>(s);
+            if (!all) {  // (the same for the whole warp)
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (!((word[i >> 5] >> (i & 31)) & 1u)) s[i] = 0xFF800000u;  // -infinity
+            }
+            // The running maximum takes in the half's largest y.
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* v = s + 16 * i;
+              float x = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+              float y = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+              x = max3(x, __uint_as_float(v[6]), __uint_as_float(v[7]));
+              y = max3(y, __uint_as_float(v[8]), __uint_as_float(v[9]));
+              x = max3(x, __uint_as_float(v[10]), __uint_as_float(v[11]));
+              y = max3(y, __uint_as_float(v[12]), __uint_as_float(v[13]));
+              x = max3(x, __uint_as_float(v[14]), __uint_as_float(v[15]));
+              mx = fmaxf(mx, fmaf(fmaxf(x, y), factor[i], lift[i]));
+            }
+            mx -= kTreeShift;
+            if (first) {
+              mc = mx;
+            } else {
+              const bool grown = mx - mc > kTreeLag;  // (false for -inf - -inf = NaN)
+              if (__any_sync(0xFFFFFFFFu, grown)) {
+                float f = 1.f;
+                if (grown) {
+                  f = exp2_approx(mc - mx);  // (0 from -inf)
+                  mc = mx;
+                  l *= f;
+                }
+                // The product of the half before has to be done.
+                ok = wait(&sh.o_done[g], (halves - 1) & 1u, kAttnSoftmaxTimeout);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < d; c += 16) {  // (16 columns: the scores stay in registers)
+                  uint32_t o[16];
+                  tmem_ld_x16(to + c, o);
+                  tmem_wait_ld_x16(o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st_x16(to + c, o);
+                }
+                tmem_wait_st();
+              }
+            }
+            // P lies over the scores.
+            const float base = mc == -INFINITY ? 0.f : mc;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t h[16];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float f = factor[2 * c + q], e = lift[2 * c + q] - base;
+                const uint64_t ff = pack2(f, f), ee = pack2(e, e);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int i = 8 * q; i < 8 * q + 8; ++i) {
+                  float x, y;
+                  unpack2(fma2(pack2(__uint_as_float(s[32 * c + 2 * i]), __uint_as_float(s[32 * c + 2 * i + 1])),
+                               ff, ee),
+                          x, y);
+                  x = exp2_approx(x);
+                  y = exp2_approx(y);
+                  sum[i & 1] = add2(sum[i & 1], pack2(x, y));
+                  h[i] = round2<__half>(x, y);
+                }
+                float x, y;
+                unpack2(add2(sum[0], sum[1]), x, y);
+                l = fmaf(x + y, back[2 * c + q], l);
+              }
+              tmem_st_x16(ts_half + c * 16, h);
             }
             tmem_wait_st();
           }
-        };
-        // Two passes over the scores, 32 columns at a time: the maximum, then P.  (Held in
-        // registers in between they would take those of the widening's warps; a second read of
-        // TMEM costs less.  `all` is the same for the whole warp.)
-        if (warp_ok) {
-          uint32_t s0[32], s1[32];
-          auto left_out = [&](uint32_t on, uint32_t* s) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((on >> i) & 1u)) s[i] = 0xFF800000u;  // -infinity
-          };
-          // The largest y of the slice of 16 scores from s on.
-          auto slice_most = [&](const uint32_t* s, int i) __attribute__((always_inline)) {
-            float x = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
-            float y = max3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
-            x = max3(x, __uint_as_float(s[6]), __uint_as_float(s[7]));
-            y = max3(y, __uint_as_float(s[8]), __uint_as_float(s[9]));
-            x = max3(x, __uint_as_float(s[10]), __uint_as_float(s[11]));
-            y = max3(y, __uint_as_float(s[12]), __uint_as_float(s[13]));
-            x = max3(x, __uint_as_float(s[14]), __uint_as_float(s[15]));
-            return fmaf(fmaxf(x, y), factor[i], lift[i]);
-          };
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            tmem_ld_x32(ts + c * 32, s0);
-            tmem_ld_x32(ts + c * 32 + 32, s1);
-            tmem_wait_ld();
-            tmem_pin<32>(s0);
-            tmem_pin<32>(s1);
-            if (!all) {
-              left_out(word[c], s0);
-              left_out(word[c + 1], s1);
-            }
-            top = max3(top, slice_most(s0, 2 * c), slice_most(s0 + 16, 2 * c + 1));
-            top = max3(top, slice_most(s1, 2 * c + 2), slice_most(s1 + 16, 2 * c + 3));
-          }
-          grow(top);
-          if (!ok) break;
-          tmem_ld_x32(ts, s0);
-          const float base = mc == -INFINITY ? 0.f : mc;
-          // P of a chunk lies over scores that were read before it is stored.
-          auto exponentials = [&](int c, uint32_t* s, uint32_t* next) __attribute__((always_inline)) {
-            tmem_wait_ld();
-            tmem_pin<32>(s);
-            if (next) tmem_ld_x32(ts + c * 32 + 32, next);
-            if (!all) left_out(word[c], s);
-            uint32_t h[16];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float f = factor[2 * c + half], e = lift[2 * c + half] - base;
-              const uint64_t ff = pack2(f, f), ee = pack2(e, e);
-              uint64_t sum[2] = {0, 0};
-#pragma unroll
-              for (int i = 8 * half; i < 8 * half + 8; ++i) {
-                float x, y;
-                unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), ff, ee), x, y);
-                x = exp2_approx(x);
-                y = exp2_approx(y);
-                sum[i & 1] = add2(sum[i & 1], pack2(x, y));
-                h[i] = round2<__half>(x, y);
-              }
-              float x, y;
-              unpack2(add2(sum[0], sum[1]), x, y);
-              l = fmaf(x + y, sh.scale[slot][2][2 * c + half], l);
-            }
-            tmem_st_x16(ts + c * 16, h);
-          };
-          exponentials(0, s0, s1);
-          exponentials(1, s1, s0);
-          exponentials(2, s0, s1);
-          tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.p_half[g]));
-          exponentials(3, s1, nullptr);
-          tmem_wait_st();
-        } else if (lane == 0) {
-          mbar_arrive(smem_u32(&sh.p_half[g]));
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[g][half]));
+          ++halves;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[g]));
         ++tiles;
       }
       seen += w.t1 - w.t0;
-      if (ok && !first) ok = wait(&sh.o_done[g], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
+      if (ok && !first) ok = wait(&sh.o_done[g], (halves - 1) & 1u, kAttnSoftmaxTimeout);
       ok = barrier_all(bar_id, 128, ok);
       if (!ok) break;
       tc_fence_after();
