@@ -425,31 +425,46 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       ok = barrier_all(bar_id, 128, ok);
       if (!ok) break;
       ++items;
-      float rf;  // of the row's scores: scale, and the query's power of two
-      {  // the row's query as fp16, as TMA would place it
-        const uint16_t* q = p.q + w.b * p.qs[0] + draft * p.qs[1] + head * p.qs[2];
-        uint8_t* dst = smem + g * L::kTile + r * 128;
-        uint4 v[8 * L::kBlocks];
-        float top = 0.f;
+      float rf = 0.f;  // of the row's scores: scale, and the query's power of two
+      {
+        // The queries as fp16, as TMA would place them: copied there as they are, kAtOnce of the
+        // warp's rows side by side, then (bfloat16) each word by the lane that copied it.  Short
+        // loops: a row a lane, or eight words in registers, took 24000 cycles an item for code that
+        // runs once and is fetched every time.
+        constexpr int kLanes = DP / 8, kAtOnce = 32 / kLanes;
+        const int col = lane % kLanes;
+        const int first_row = w.row_tile * p.tile_rows + (single ? 0 : g * kRowsMany) + quarter * 32;
+        uint8_t* place = smem + g * L::kTile + (col >> 3) * kBlockBytes + quarter * 32 * 128;
+#pragma unroll 2
+        for (int i = 0; i < 32; i += kAtOnce) {
+          const int at = i + lane / kLanes;  // of the warp's rows
+          const bool on = first_row + at < w.size.drafts * p.group && col * 8 < d;
+          const int at_draft = on ? fast_div(first_row + at, p.div_group) : 0;
+          const int at_head = w.hk * p.group + (on ? first_row + at - at_draft * p.group : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_u32(place + at * 128 + (((col & 7) ^ (at & 7)) << 4))),
+                       "l"(p.q + w.b * p.qs[0] + at_draft * p.qs[1] + at_head * p.qs[2] + (on ? col * 8 : 0)),
+                       "r"(on ? 16 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        if constexpr (std::is_same<T, __half>::value) {
+          rf = p.scale_log2;
+        } else {
+#pragma unroll 2
+          for (int i = 0; i < 32; i += kAtOnce) {
+            const int at = i + lane / kLanes;
+            uint4* word = reinterpret_cast<uint4*>(place + at * 128 + (((col & 7) ^ (at & 7)) << 4));
+            const uint4 v = *word;
+            float top = fmaxf(fmaxf(larger_of(v.x), larger_of(v.y)), fmaxf(larger_of(v.z), larger_of(v.w)));
 #pragma unroll
-        for (int i = 0; i < 8 * L::kBlocks; ++i)
-          v[i] = row_ok && i * 8 < d ? *reinterpret_cast<const uint4*>(q + i * 8) : make_uint4(0, 0, 0, 0);
-        if constexpr (!std::is_same<T, __half>::value)
-#pragma unroll
-          for (int i = 0; i < 8 * L::kBlocks; ++i) {
-            top = fmaxf(top, larger_of(v[i].x));
-            top = fmaxf(top, larger_of(v[i].y));
-            top = fmaxf(top, larger_of(v[i].z));
-            top = fmaxf(top, larger_of(v[i].w));
+            for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            float back;
+            const float up = row_factor<T>(top, &back);
+            *word = make_uint4(to_half(v.x, up), to_half(v.y, up), to_half(v.z, up), to_half(v.w, up));
+            const float mine = __shfl_sync(0xFFFFFFFFu, back, (lane % kAtOnce) * kLanes);
+            if (lane - lane % kAtOnce == i) rf = p.scale_log2 * mine;
           }
-        float back;
-        const float up = row_factor<T>(top, &back);
-        rf = p.scale_log2 * back;
-#pragma unroll
-        for (int i = 0; i < 8 * L::kBlocks; ++i) {
-          if constexpr (!std::is_same<T, __half>::value)
-            v[i] = make_uint4(to_half(v[i].x, up), to_half(v[i].y, up), to_half(v[i].z, up), to_half(v[i].w, up));
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * kBlockBytes + (((i & 7) ^ (r & 7)) << 4)) = v[i];
         }
         fence_proxy_async_shared();
         __syncwarp();
@@ -601,19 +616,63 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       // lie behind one another; one without a tile leaves no rows.)
       const long long at = (2ll * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * (2 * kRowsMany) + g * kRowsMany + r;
       if (warp_ok && (!first || whole)) {
-        uint16_t* dst = p.out + w.b * p.os[0] + draft * p.os[1] + head * p.os[2];
+        // Through the warp's part of the queries' place (whose products have ended), so that rows
+        // leave side by side.  (A row a lane, 16 bytes at a time, took 9 us an item.)
+        uint8_t* staged = smem + g * L::kTile + quarter * (L::kTile / 4);
+        const int row_first = row - lane;
+        if (whole) {
+          constexpr int kChunks = DP / 8, kAtOnce = 32 / kChunks;  // 16-byte words of a row
 #pragma unroll 1
-        for (int c = 0; c < d; c += 32) {
-          uint32_t o[32];
-          tmem_ld_x32(to + c, o);
-          tmem_wait_ld_x32(o);
-          if (row_ok) {
-            if (whole)
-              store_cols(reinterpret_cast<T*>(dst) + c, o, d - c, inv);
-            else
-              store_cols_f32(p.part_out + at * 128 + c, o, d - c, 1.f);
+          for (int c = 0; c < d; c += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(to + c, o);
+            tmem_wait_ld_x32(o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                h[j] = round2<T>(__uint_as_float(o[8 * i + 2 * j]) * inv, __uint_as_float(o[8 * i + 2 * j + 1]) * inv);
+              *reinterpret_cast<uint4*>(staged + lane * (DP * 2) + ((((c >> 3) + i) ^ (lane % kChunks)) << 4)) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+          __syncwarp();
+          const int col = lane % kChunks;
+#pragma unroll 4
+          for (int i = 0; i < 32; i += kAtOnce) {
+            const int at = i + lane / kChunks, at_row = row_first + at;
+            if (at_row < w.size.drafts * p.group && col * 8 < d) {
+              const int at_draft = fast_div(at_row, p.div_group);
+              const int at_head = w.hk * p.group + at_row - at_draft * p.group;
+              *reinterpret_cast<uint4*>(p.out + w.b * p.os[0] + at_draft * p.os[1] + at_head * p.os[2] + col * 8) =
+                  *reinterpret_cast<const uint4*>(staged + at * (DP * 2) + ((col ^ (at % kChunks)) << 4));
+            }
+          }
+        } else {
+          float* part = p.part_out + (at - lane) * 128;
+#pragma unroll 1
+          for (int c = 0; c < d; c += 32) {  // 32 columns: eight words of a row
+            uint32_t o[32];
+            tmem_ld_x32(to + c, o);
+            tmem_wait_ld_x32(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(staged + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                  make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            __syncwarp();
+            const int col = lane & 7;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const int from = i + (lane >> 3);
+              if (row_first + from < w.size.drafts * p.group && c + col * 4 < d)
+                *reinterpret_cast<uint4*>(part + from * 128 + c + col * 4) =
+                    *reinterpret_cast<const uint4*>(staged + from * 128 + ((col ^ (from & 7)) << 4));
+            }
+            __syncwarp();
           }
         }
+        __syncwarp();
       }
       if (row_ok) {
         if (!whole)
