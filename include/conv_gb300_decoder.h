@@ -152,12 +152,13 @@ conv_status_t kv_cache_read(const kv_cache_args_t* args, void* stream);
  * Scores, sums and statistics are fp32.  Codes, queries and probabilities
  * meet in the products as fp16: codes are exact there, a query's row is held
  * times a power of two (elements below 2^-28 of the row's largest are rounded
- * in steps of 2^-39 of it), and probabilities times 2^4 and their value's
- * scale relative to the largest of these.  With more than 32 rows (drafts
- * times query heads of a key head) codes are held relative to the largest
- * scale of 16 neighbouring tokens: elements of keys are rounded in steps of
- * 2^-24, of values in steps of 2^-31, of that.  Results are rounded once.  Sums
- * run in a fixed order: equal calls give equal bits.
+ * in steps of 2^-39 of it), and probabilities times their value's scale and a
+ * power of two that holds the row's largest of these at 2^4 at least (small
+ * ones are rounded in steps of 2^-28 of it).  With more than 64 rows (drafts
+ * times query heads of a key head) that scale is the largest of 16 neighbouring
+ * tokens, and codes are held relative to it: elements of keys are rounded in
+ * steps of 2^-24, of values in steps of 2^-31, of it.  Results are rounded once.
+ * Sums run in a fixed order: equal calls give equal bits.
  *
  * q and out: [batch][q_len][heads][D] of `dtype`, strides {batch, token,
  * head} in elements, multiples of 8; lse: dense fp32 [batch][heads][q_len], or

@@ -162,11 +162,18 @@ class TreeReference:
                 off = F32 * ((d + 2) * s_abs + 4 * (s_abs + base.abs() + 4) + 2 * (ev.abs() + 16)) + low
                 off = torch.where(keep, off, torch.zeros_like(off)).amax(2, keepdim=True)
                 share = 2.0 ** -11 + 2 * off + 2.0 ** -21 + n * F32
-                # Probabilities times their value's scale, below fp16's normal numbers: off by 2^-25 where the
-                # largest is 2^4 at least.
-                weight = torch.where(keep, p * pow2(ev), torch.zeros_like(p))
+                # A probability is held as w = p 2^f, with f its value's exponent, or (more than 64 rows) the
+                # largest of the 16 tokens it lies among.  The largest w of a row is held at 2^4 at least,
+                # and those below fp16's normal numbers are off by 2^-25: by 2^-29 of the largest.  The
+                # value that w meets is v 2^-f.
+                f = ev
+                if t * group > 64:
+                    fill = torch.where(live[:, g], ev, torch.full_like(ev, -1000.0))
+                    fill = torch.nn.functional.pad(fill, (0, -n % 16), value=-1000.0)
+                    f = fill.view(-1, 16).amax(1).repeat_interleave(16)[:n].clamp(min=-64)
+                weight = torch.where(keep, p * pow2(f), torch.zeros_like(p))
                 tiny = 2.0 ** -29 * weight.amax(2, keepdim=True) * (
-                    keep.double() @ (vg * pow2(-ev)[:, None]).abs())
+                    keep.double() @ (vg * pow2(-f)[:, None]).abs())
                 tol = u * o.abs() + (1 + u) * share * (p @ vg.abs()) + tiny + grain(u)
                 rows = slice(g * group, (g + 1) * group)
                 self.out[i, :drafts, rows], self.out_tol[i, :drafts, rows] = o.transpose(0, 1), tol.transpose(0, 1)

@@ -12,8 +12,10 @@ namespace convgb300 {
 
 namespace {
 
-// Rows of a key head from which on the tensor cores' kernel is the faster one.
-constexpr int kFewRows = 32;
+// Rows of a key head up to which the kernel for few rows takes them (in tiles of 32, which read
+// the keys once each).  Its time and the other kernel's: 48 rows, 2 requests x 8192 keys 38 and 45
+// us, 32 x 4096 160 and 155; 64 rows, 32 x 2048 101 and 108; 96 rows, 16 x 4096 131 and 95.
+constexpr int kFewRows = 64;
 
 struct TreePlan {
   bool many;
