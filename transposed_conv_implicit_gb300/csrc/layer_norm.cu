@@ -226,7 +226,8 @@ __device__ __forceinline__ uint4 ring_word(uint32_t src) {
   return v;
 }
 
-template <typename T, typename W, int kVec, int kWords, bool kBlock>
+// kFull: a row's words are as many as its lanes take (320 channels on 8 lanes of 5).
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kFull>
 __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBlock ? 1 : 3)
     layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
   constexpr bool kRing = kVec == 8;
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      const bool on = live && w < p.words;
+      const bool on = live && (kFull || w < p.words);
       ring_copy(ring + (stage * kWords + i) * pitch, x + (on ? w * kVec : 0), on);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int w = at + i * lanes;
-        raw[i] = live && w < p.words ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
+        raw[i] = live && (kFull || w < p.words) ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
       }
     }
     constexpr int kPairs = Pairs<kVec>::kCount;
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
     total = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      if (at + i * lanes < p.words)
+      if (kFull || at + i * lanes < p.words)
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           f[i].v[j] = add2(f[i].v[j], minus);
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (w >= p.words) break;
+      if (!kFull && w >= p.words) break;
       const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
       const Pairs<kVec> bs = load_weight<W, kVec>(p.bias, w * kVec, 0.f);
 #pragma unroll
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 // them kept, a row of 4096 takes 360 instructions of a warp, 880 without;
 // twice the lanes with two words each: 188 us for both passes over 16381 rows,
 // 153 with four.)
-template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide>
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull>
 __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512 : 256)
     layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
   constexpr bool kRing = kVec == 8, kKeep = kVec == 8 && !kWide;
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
   if constexpr (kKeep)
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-      weight[i] = load_weight<W, kVec>(at + i * lanes < p.words ? p.weight : nullptr, (at + i * lanes) * kVec, 1.f);
+      weight[i] = load_weight<W, kVec>(kFull || at + i * lanes < p.words ? p.weight : nullptr, (at + i * lanes) * kVec, 1.f);
   const int step = gridDim.x * groups;
   const uint32_t ring = smem_u32(shared) + threadIdx.x * 16, pitch = blockDim.x * 16;
   float stat[2] = {0.f, 0.f}, next_stat[2] = {0.f, 0.f};  // mean and rstd of the next rows, as they are copied
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      const bool on = live && w < p.words;
+      const bool on = live && (kFull || w < p.words);
       const uint32_t to = ring + (stage * 2 * kWords + i) * pitch;
       ring_copy(to, x + (on ? w * kVec : 0), on);
       ring_copy(to + kWords * pitch, dy + (on ? w * kVec : 0), on);
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         const int w = at + i * lanes;
-        const bool on = live && w < p.words;
+        const bool on = live && (kFull || w < p.words);
         rx[i] = on ? load_word<kVec>(x + w * kVec) : no_word<kVec>();
         rd[i] = on ? load_word<kVec>(dy + w * kVec) : no_word<kVec>();
       }
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (w >= p.words) break;
+      if (!kFull && w >= p.words) break;
       const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
       Pairs<kVec> wt;
       if constexpr (kKeep) wt = weight[i];
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (w >= p.words) break;
+      if (!kFull && w >= p.words) break;
       Pairs<kVec> o;
       if constexpr (kKeep) {
 #pragma unroll
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (w >= p.words) break;
+      if (!kFull && w >= p.words) break;
       put(out, w, dw + i * kPairs, false);
       put(out + p.channels, w, db + i * kPairs, false);
     }
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
           const int w = at + i * lanes;
-          if (w >= p.words) break;
+          if (!kFull && w >= p.words) break;
           put(sums, w, dw + i * kPairs, next > 0);
           put(sums + p.channels, w, db + i * kPairs, next > 0);
         }
@@ -573,11 +574,29 @@ LnShape ln_shape(int channels, bool vectors, bool backward) {
   return s;
 }
 
+// Blocks of a kernel that an SM runs at once, asked for once for each device and
+// number of threads (a power of two; the shared memory goes by that).
+template <typename Kernel>
+cudaError_t blocks_per_sm(Kernel kernel, std::atomic<int> (*known)[16], int threads, size_t smem, int* fit) {
+  int dev = 0, at = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  while ((1 << at) < threads) ++at;
+  *fit = known[dev][at].load(std::memory_order_relaxed);
+  if (*fit > 0) return cudaSuccess;
+  err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, kernel, threads, smem);
+  if (err != cudaSuccess) return err;
+  *fit = std::max(1, *fit);
+  known[dev][at].store(*fit, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 int ln_groups(const LnShape& s) { return s.block ? 1 : s.threads / s.lanes; }
 
-template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide>
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull>
 cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms, cudaStream_t stream) {
-  const auto kernel = layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock, kWide>;
+  const auto kernel = layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock, kWide, kFull>;
   const size_t ring = kVec == 8 ? static_cast<size_t>(kLnStages) * 2 * kWords * s.threads * 16 : 0;
   const size_t smem = std::max(ring, s.block ? size_t{0} : static_cast<size_t>(2) * p.channels * sizeof(float));
   static std::atomic<size_t> configured[kMaxDevices];
@@ -585,44 +604,54 @@ cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms,
   if (err != cudaSuccess) return err;
   // As many blocks as run at once: each keeps its columns' sums over all of its rows.
   int fit = 0;
-  err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, s.threads, smem);
+  static std::atomic<int> known[kMaxDevices][16];
+  err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
   if (err != cudaSuccess) return err;
-  p.blocks = static_cast<int>(std::min<long long>(
-      need, static_cast<long long>(std::max(1, std::min(fit, kLnBwdBlocksPerSm))) * sms));
+  p.blocks = static_cast<int>(
+      std::min<long long>(need, static_cast<long long>(std::min(fit, kLnBwdBlocksPerSm)) * sms));
   err = launch_pdl(kernel, dim3(p.blocks), dim3(s.threads), smem, stream, p);
   if (err != cudaSuccess || !p.partial) return err;
   return launch_pdl(layer_norm_sum_kernel, dim3((2 * p.channels + 31) / 32), dim3(32 * kSumWarps), 0,
                     stream, p);
 }
 
-template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide>
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull>
 cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
   const long long need = (static_cast<long long>(p.rows) + ln_groups(s) - 1) / ln_groups(s);
   if (!backward) {
-    const auto kernel = layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock>;
+    const auto kernel = layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock, kFull>;
     const size_t smem = kVec == 8 ? static_cast<size_t>(kLnStages) * kWords * s.threads * 16 : 0;
     static std::atomic<size_t> configured[kMaxDevices];
     cudaError_t err = raise_smem(kernel, configured, smem);
     if (err != cudaSuccess) return err;
     int fit = 0;
-    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, s.threads, smem);
+    static std::atomic<int> known[kMaxDevices][16];
+    err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
     if (err != cudaSuccess) return err;
-    const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(std::max(1, fit)) * sms));
+    const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(fit) * sms));
     return launch_pdl(kernel, dim3(grid), dim3(s.threads), smem, stream, p);
   }
   // (Five words a lane are for the forward pass alone: see ln_shape.)
   if constexpr (kVec == 8 && kWords == 5) return cudaErrorInvalidValue;
-  else return ln_launch_bwd<T, W, kVec, kWords, kBlock, kWide>(p, s, need, sms, stream);
+  else return ln_launch_bwd<T, W, kVec, kWords, kBlock, kWide, kFull>(p, s, need, sms, stream);
 }
 template <typename T, typename W>
 cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, int sms,
                             cudaStream_t stream) {
   const auto part = [&](auto vec, auto words) {  // rows on a warp's lanes
-    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, false, false>(p, s, backward, sms, stream);
+    constexpr int kVec = decltype(vec)::value, kWords = decltype(words)::value;
+    if constexpr (kVec == 8)
+      if (s.lanes * kWords == s.words)
+        return ln_launch<T, W, kVec, kWords, false, false, true>(p, s, backward, sms, stream);
+    return ln_launch<T, W, kVec, kWords, false, false, false>(p, s, backward, sms, stream);
   };
   const auto whole = [&](auto vec, auto words, auto wide) {  // rows on a block
-    return ln_launch<T, W, decltype(vec)::value, decltype(words)::value, true, decltype(wide)::value>(
-        p, s, backward, sms, stream);
+    constexpr int kVec = decltype(vec)::value, kWords = decltype(words)::value;
+    constexpr bool kWide = decltype(wide)::value;
+    if constexpr (kVec == 8)
+      if (s.lanes * kWords == s.words)
+        return ln_launch<T, W, kVec, kWords, true, kWide, true>(p, s, backward, sms, stream);
+    return ln_launch<T, W, kVec, kWords, true, kWide, false>(p, s, backward, sms, stream);
   };
   using N1 = std::integral_constant<int, 1>;
   using N2 = std::integral_constant<int, 2>;

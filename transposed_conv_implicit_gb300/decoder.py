@@ -28,13 +28,19 @@ _CACHE = struct.Struct("@8i8Q13q")     # kv_cache_args_t
 _TREE = struct.Struct("@9if10Q14q")    # tree_attention_args_t
 
 
+_current_device = None    # filled on first use
+
+
 def _call(fn, name, device, *args):
     """Calls with the tensors' device current: the library launches on the current one."""
-    torch = _a._torch
-    if torch.cuda.current_device() == device:
+    global _current_device
+    if _current_device is None:
+        torch = _a._torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    if _current_device() == device:
         status = fn(*args)
     else:
-        with torch.cuda.device(device):
+        with _a._torch.cuda.device(device):
             status = fn(*args)
     if status != CONV_OK:
         raise _error(status, name)
@@ -47,13 +53,18 @@ def _sized(fn, device, *args):
 
 
 # ------------------------------------------------------------------ layer norm
-def _rows(t, name, shape, dtype, device):
-    """(batch, length) and their strides of [..., C] with at most two leading dimensions that do
-    not run into one another (a feature map's pixels, a slice of a fused projection)."""
-    if t.shape != shape:
-        raise _invalid("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype is not dtype or t.get_device() != device:
-        raise _invalid("%s must be %s on cuda:%d" % (name, dtype, device))
+def _like(t, name, x):
+    if t.shape != x.shape:
+        raise _invalid("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(x.shape)))
+    if t.dtype is not x.dtype or t.get_device() != x.get_device():
+        raise _invalid("%s must be %s on cuda:%d" % (name, x.dtype, x.get_device()))
+
+
+def _rows(t, name, x):
+    """(extent, stride) of [..., C]'s leading dimensions, those that run into one another joined (a
+    feature map's pixels, a slice of a fused projection)."""
+    _like(t, name, x)
+    shape = x.shape
     if shape[-1] > 1 and t.stride(-1) != 1:
         raise _invalid("%s: the innermost dimension must be contiguous" % name)
     dims = []
@@ -72,10 +83,10 @@ def _two(all_dims, names):
     cut = None    # a size of the inner dimension that every tensor can be cut at
     for dims in all_dims:
         if len(dims) > 2:
-            raise _invalid("%s: the rows have more than two strides" % names)
+            raise _invalid("%s: the rows have more than two strides" % " or ".join(names))
         if len(dims) == 2:
             if cut is not None and cut != dims[1][0]:
-                raise _invalid("%s: the tensors' rows are strided differently" % names)
+                raise _invalid("%s: the rows are strided differently" % " and ".join(names))
             cut = dims[1][0]
     rows = 1
     for n, _ in all_dims[0]:
@@ -114,10 +125,20 @@ def _norm_weight(w, name, c, dtype, device):
     return w.data_ptr(), w.dtype
 
 
-def _norm_size(x, eps, all_dims, names):
-    if x.numel() == 0:
-        return 0, 0, [(0, 0)] * len(all_dims)
-    return _two(all_dims, names)
+def _norm_size(x, others, names):
+    """(batch, length, strides of x and of the others), which are (tensor, name)."""
+    rows = x.numel() // x.shape[-1]
+    if x.is_contiguous():     # (without the walk over the dimensions: a call of few tokens is its launch)
+        for t, name in others:
+            if not t.is_contiguous():
+                break
+            _like(t, name, x)
+        else:
+            return 1, rows, [(0, x.shape[-1])] * (1 + len(others))
+    dims = [_rows(x, names[0], x)] + [_rows(t, name, x) for t, name in others]
+    if rows == 0:
+        return 0, 0, [(0, 0)] * len(dims)
+    return _two(dims, names)
 
 
 def layer_norm_fwd(x, weight, bias, y, *, mean=None, rstd=None, eps=1e-5, stream=None):
@@ -135,8 +156,7 @@ def layer_norm_fwd(x, weight, bias, y, *, mean=None, rstd=None, eps=1e-5, stream
         raise _invalid("weight and bias must be of one type")
     m = 0 if mean is None else _dense(mean, "mean", shape[:-1], torch.float32, device)
     r = 0 if rstd is None else _dense(rstd, "rstd", shape[:-1], torch.float32, device)
-    batch, length, (xs, ys) = _norm_size(x, eps, [_rows(x, "x", shape, dtype, device),
-                                                  _rows(y, "y", shape, dtype, device)], "x and y")
+    batch, length, (xs, ys) = _norm_size(x, ((y, "y"),), ("x", "y"))
     args = _pack(_NORM, code, batch, length, c, torch.float32 in (wt, bt), eps, x.data_ptr(), w, b,
                  y.data_ptr(), m, r, 0, 0, 0, 0, *xs, *ys, 0, 0, 0, 0)
     _call(_lib.lib().layer_norm_fwd, "layer_norm_fwd", device, args, _stream(stream, device))
@@ -165,9 +185,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, *, workspace=N
     r = _dense(rstd, "rstd", shape[:-1], torch.float32, device)
     dw = 0 if dweight is None else _dense(dweight, "dweight", (c,), torch.float32, device)
     db = 0 if dbias is None else _dense(dbias, "dbias", (c,), torch.float32, device)
-    batch, length, (xs, ds, dxs) = _norm_size(x, 0.0, [
-        _rows(x, "x", shape, dtype, device), _rows(dy, "dy", shape, dtype, device),
-        _rows(dx, "dx", shape, dtype, device)], "x, dy and dx")
+    batch, length, (xs, ds, dxs) = _norm_size(x, ((dy, "dy"), (dx, "dx")), ("x", "dy", "dx"))
     args = _pack(_NORM, code, batch, length, c, wt is torch.float32, 0.0, x.data_ptr(), w, 0, 0, m, r,
                  dy.data_ptr(), dx.data_ptr(), dw, db, *xs, 0, 0, *ds, *dxs)
     lib = _lib.lib()
