@@ -106,8 +106,9 @@ conv_status_t layer_norm_bwd(const layer_norm_args_t* args, void* workspace,
  *
  * Gates (CONV_ERR_NOT_SUPPORTED): other dtypes; D no multiple of 16 or above
  * 128; page_size no multiple of 16; table_width * page_size or batch * length
- * * kv_heads above 0x7FFF0000.  CONV_ERR_INVALID_VALUE: missing tensors,
- * negative sizes or strides, strides of 0 of what is written.
+ * * kv_heads above 0x7FFF0000.  CONV_ERR_INVALID_VALUE: missing tensors, a
+ * cache without pages, negative sizes or strides, strides of 0 of what is
+ * written.
  * CONV_ERR_MISALIGNED: pointers off 16 bytes (int32: 4), other strides.
  * ------------------------------------------------------------------------ */
 typedef struct {

@@ -92,7 +92,7 @@ def test_norm_refuses_its_workspace(lib):
 PAGES = [
     (dict(dtype=2), NOTSUP), (dict(batch=-1), INVALID), (dict(kv_heads=0), INVALID), (dict(head_dim=0), INVALID),
     (dict(head_dim=72), NOTSUP), (dict(head_dim=144), NOTSUP), (dict(page_size=0), INVALID),
-    (dict(page_size=24), NOTSUP), (dict(pages=-1), INVALID), (dict(table_width=-1), INVALID),
+    (dict(page_size=24), NOTSUP), (dict(pages=-1), INVALID), (dict(pages=0), INVALID), (dict(table_width=-1), INVALID),
     (dict(table_width=1 << 27), NOTSUP), (dict(k_cache=0), INVALID), (dict(v_cache=0), INVALID),
     (dict(scales=0), INVALID), (dict(block_table=0), INVALID), (dict(k_cache=0x30008), MISALIGNED),
     (dict(scales=0x50002), MISALIGNED), (dict(block_table=0x60002), MISALIGNED), (dict(table_stride=-4), INVALID),

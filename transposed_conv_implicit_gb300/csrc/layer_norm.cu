@@ -4,8 +4,10 @@
 //   dx = r (g - mean g - h mean(g h)),  g = dy w,  h = (x - m) r
 //   dw = sum_rows dy h,  db = sum_rows dy
 //
-// Bound by memory: x in, y out; x and dy in, dx out.  A row lies in the
-// registers of `lanes` lanes (a power of two up to a warp, or a whole block),
+// Bound by memory: x in, y out; x and dy in, dx out.  Measured: 65536 x 320
+// forward 17.8 us (4.7 TB/s), backward 24 us (5.2); 16381 x 4096 forward 48 us
+// (5.6 TB/s), backward 80 us (5.0); the weights' sums another 4.  A row lies in
+// the registers of `lanes` lanes (a power of two up to a warp, or a whole block),
 // up to kWords words of kVec elements each, so it is read once: the mean, the
 // deviations from it and the result come from the same registers.  Lanes take
 // words that are neighbours, and rows go around the groups of the grid.
@@ -545,7 +547,9 @@ struct LnShape {
   bool block;
 };
 
-// Words of a lane: as few idle ones as possible, then more rows side by side.
+// How a row lies on lanes: as few idle words as possible, then few words a lane.
+// Forward up to five a lane (320 channels on 8 lanes of 5: 19.8 us, on 16 of 3
+// 24.1); backward four, with what it keeps of a row.  Longer rows take a block.
 LnShape ln_shape(int channels, bool vectors, bool backward) {
   LnShape s{};
   s.vec = vectors ? 8 : 1;

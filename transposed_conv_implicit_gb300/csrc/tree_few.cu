@@ -17,6 +17,12 @@
 // four inner steps' operands) and of a value's row (as a column of each of the
 // 16 output tiles).
 //
+// Measured: one token of 64 requests x 32/8 heads x 128 against up to 4096 keys
+// 94.5 us, its join with it (4.3 TB/s; 5.4 for each further key); 7 drafts of 32
+// requests against up to 8192 keys 123 us.  (Turned over, with the rows along N,
+// single tokens need half the products and 128 registers, and take 99.7 us: the
+// copies alone take 89 to 95.)
+//
 // Numbers: e4m3 codes are exact in fp16, and stay unscaled.  A key's scale goes
 // to its scores.  A value's scale 2^e goes to its probability: p 2^e is held as
 // w = 2^(y - M), y = s log2(e) + e, with M the running maximum of y, which
