@@ -198,37 +198,46 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, *, workspace=N
 
 
 # ------------------------------------------------------------------ the cache
+# (The calls below run before every launch, single tokens' among them: a tensor's shape and strides
+# are asked for once, which takes longer than anything that is done with them.)
 def _cache(k_cache, v_cache, scales, block_table, batch, kv_heads, d, device):
-    """(pages, page_size, table_width), the pointers, the table's stride and the cache's strides."""
+    """(pages, page_size, table_width), the pointers, the table's stride and the cache's strides.
+    kv_heads None: as k_cache has them."""
     torch = _a._torch
-    if k_cache.dim() != 4 or k_cache.shape[2] != kv_heads or k_cache.shape[3] != d:
-        raise _invalid("k_cache must be [pages, page_size, %d, %d]" % (kv_heads, d))
     shape = k_cache.shape
-    pages, page_size = shape[0], shape[1]
+    if len(shape) != 4 or shape[3] != d or (shape[2] != kv_heads if kv_heads else shape[2] < 1):
+        raise _invalid("k_cache must be [pages, page_size, %s, %d]" % (kv_heads or "kv_heads", d))
+    pages, page_size, kv_heads, _ = shape
     ks = _strides(k_cache, "k_cache", shape, torch.float8_e4m3fn, device)
     vs = _strides(v_cache, "v_cache", shape, torch.float8_e4m3fn, device)
     s = _dense(scales, "scales", (pages, kv_heads, page_size, 2), torch.uint8, device)
-    if (block_table.dim() != 2 or block_table.shape[0] != batch or block_table.dtype is not torch.int32
-            or block_table.get_device() != device
-            or (block_table.stride(1) != 1 and block_table.shape[1] > 1)):
+    table, stride = block_table.shape, block_table.stride()
+    if (len(table) != 2 or table[0] != batch or block_table.dtype is not torch.int32
+            or block_table.get_device() != device or (stride[1] != 1 and table[1] > 1)):
         raise _invalid("block_table must be int32 [%d, pages of a request] on cuda:%d, contiguous "
                        "along the pages" % (batch, device))
-    return ((pages, page_size, block_table.shape[1]),
-            (k_cache.data_ptr(), v_cache.data_ptr(), s, block_table.data_ptr()), block_table.stride(0),
-            ks + vs)
+    return ((pages, page_size, table[1]), kv_heads,
+            (k_cache.data_ptr(), v_cache.data_ptr(), s, block_table.data_ptr()), stride[0], ks + vs)
 
 
 def _per_request(t, name, batch, device):
     return 0 if t is None else _dense(t, name, (batch,), _a._torch.int32, device)
 
 
+def _leading(x, name):
+    """The dtype's code, the device's number, the dtype and the shape of [batch, length, heads, D]."""
+    code, device = _common(x, name)
+    return code, device, x.dtype, x.shape
+
+
 def _move(name, k, v, k_cache, v_cache, scales, block_table, starts, lengths, stream):
-    code, device = _common(k, "k")
-    shape = k.shape
+    code, device, dtype, shape = _leading(k, "k")
     b, length, heads, d = shape
-    strides = _strides(k, "k", shape, k.dtype, device) + _strides(v, "v", shape, k.dtype, device)
-    sizes, ptrs, table_stride, cache_strides = _cache(k_cache, v_cache, scales, block_table, b, heads, d,
-                                                      device)
+    strides = _strides(k, "k", shape, dtype, device) + _strides(v, "v", shape, dtype, device)
+    if heads < 1:
+        raise _invalid("k must have heads")
+    sizes, _, ptrs, table_stride, cache_strides = _cache(k_cache, v_cache, scales, block_table, b, heads, d,
+                                                         device)
     args = _pack(_CACHE, code, b, length, heads, d, *sizes, k.data_ptr(), v.data_ptr(), *ptrs,
                  _per_request(starts, "starts", b, device), _per_request(lengths, "lengths", b, device),
                  table_stride, *strides, *cache_strides)
@@ -283,22 +292,20 @@ def tree_attention_fwd(q, k_cache, v_cache, scales, block_table, kv_lengths, out
     all drafts up to i.  Rows of output (and lse, float32 [B, H, T], optional) from draft_lengths[b]
     on keep what they hold.  scale defaults to 1 / sqrt(D).  Calls that may overlap on the GPU need
     workspaces of their own."""
-    code, device = _common(q, "q")
-    torch, shape = _a._torch, q.shape
+    code, device, dtype, shape = _leading(q, "q")
+    torch = _a._torch
     b, t, h, d = shape
-    if k_cache.dim() != 4 or k_cache.shape[2] < 1:
-        raise _invalid("k_cache must be [pages, page_size, kv_heads, %d]" % d)
-    strides = (_strides(q, "q", shape, q.dtype, device) + _strides(output, "output", shape, q.dtype, device))
-    hkv = k_cache.shape[2]
-    sizes, ptrs, table_stride, cache_strides = _cache(k_cache, v_cache, scales, block_table, b, hkv, d, device)
+    strides = _strides(q, "q", shape, dtype, device) + _strides(output, "output", shape, dtype, device)
+    sizes, hkv, ptrs, table_stride, cache_strides = _cache(k_cache, v_cache, scales, block_table, b, None, d,
+                                                           device)
     up, up_stride = 0, 0
     if parents is not None:
+        tree, steps = parents.shape, parents.stride()
         if (parents.dtype is not torch.int32 or parents.get_device() != device
-                or (parents.shape != (b, t) and parents.shape != (t,))
-                or (parents.stride(-1) != 1 and t > 1)):
+                or (tree != (b, t) and tree != (t,)) or (steps[-1] != 1 and t > 1)):
             raise _invalid("parents must be int32 [%d, %d] or [%d] on cuda:%d, contiguous along the drafts"
                            % (b, t, t, device))
-        up, up_stride = parents.data_ptr(), parents.stride(0) if parents.dim() == 2 else 0
+        up, up_stride = parents.data_ptr(), steps[0] if len(tree) == 2 else 0
     if kv_lengths is None:
         raise _invalid("kv_lengths is missing")
     if lse is not None:
