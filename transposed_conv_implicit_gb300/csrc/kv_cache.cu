@@ -27,7 +27,7 @@ namespace convgb300 {
 namespace {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 2;  // in flight for each lane
+constexpr int kCacheRows = 2;  // in flight for each lane (four: 19 us to read back what two do in 14)
 
 struct CacheParams {
   CacheView c;

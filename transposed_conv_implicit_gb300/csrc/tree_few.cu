@@ -548,7 +548,9 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
   const int r = r0 + warp * kPer, d = lane * 4;
   if (r >= rows) return;
   const bool on = d < p.c.head_dim;
+  // A few shares at a time, their statistics and rows in flight together, with the running maximum.
   // (Rows past the item's read its last one again and write nothing.)
+  constexpr int kAtOnce = kPer == 1 ? 8 : 3;
   float m[kPer], l[kPer];
   float4 a[kPer];
 #pragma unroll
@@ -557,31 +559,49 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
     l[k] = 0.f;
     a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  for (int c = lane; c < shares; c += 32)
-    if (slots[c] >= 0)
+  for (int c0 = 0; c0 < shares; c0 += kAtOnce) {
+    float2 st[kAtOnce][kPer];
+    float4 v[kAtOnce][kPer];
 #pragma unroll
-      for (int k = 0; k < kPer; ++k)
-        m[k] = fmaxf(m[k], p.part_stat[(static_cast<long long>(slots[c]) + min(r + k, rows - 1)) * 2]);
-  for (int o = 16; o; o >>= 1)
+    for (int c = 0; c < kAtOnce; ++c) {
+      const int slot = c0 + c < shares ? slots[c0 + c] : -1;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) m[k] = fmaxf(m[k], __shfl_xor_sync(0xFFFFFFFFu, m[k], o));
-#pragma unroll(kPer == 1 ? 8 : 2)
-  for (int c = 0; c < shares; ++c)
+      for (int k = 0; k < kPer; ++k) {
+        const long long row = max(slot, 0) + min(r + k, rows - 1);
+        st[c][k] = make_float2(-INFINITY, 0.f);
+        v[c][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (slot >= 0) {
+          st[c][k] = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
+          if (on) v[c][k] = *reinterpret_cast<const float4*>(p.part_out + row * 128 + d);
+        }
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const long long row = max(slots[c], 0) + min(r + k, rows - 1);
-      const float2 st = *reinterpret_cast<const float2*>(p.part_stat + row * 2);
-      const float4 v = on ? *reinterpret_cast<const float4*>(p.part_out + row * 128 + d) : a[k];
-      // A share without keys leaves no rows, what lies there is not used; one whose maximum is
-      // -infinity all the same holds NaN of the row's own.
-      const bool used = slots[c] >= 0 && !(st.x == -INFINITY && st.y == 0.f);
-      const float f = st.x == -INFINITY ? 0.f : exp2_approx(st.x - m[k]);
-      l[k] = used ? fmaf(f, st.y, l[k]) : l[k];
-      a[k].x = used ? fmaf(f, v.x, a[k].x) : a[k].x;
-      a[k].y = used ? fmaf(f, v.y, a[k].y) : a[k].y;
-      a[k].z = used ? fmaf(f, v.z, a[k].z) : a[k].z;
-      a[k].w = used ? fmaf(f, v.w, a[k].w) : a[k].w;
+      float top = m[k];
+#pragma unroll
+      for (int c = 0; c < kAtOnce; ++c) top = fmaxf(top, st[c][k].x);
+      const float down = m[k] == -INFINITY ? 0.f : exp2_approx(m[k] - top);
+      m[k] = top;
+      l[k] *= down;
+      a[k].x *= down;
+      a[k].y *= down;
+      a[k].z *= down;
+      a[k].w *= down;
+#pragma unroll
+      for (int c = 0; c < kAtOnce; ++c) {
+        // A share without keys leaves no rows, what lies there is not used; one whose maximum is
+        // -infinity all the same holds NaN of the row's own.
+        if (st[c][k].x == -INFINITY && st[c][k].y == 0.f) continue;
+        const float f = st[c][k].x == -INFINITY ? 0.f : exp2_approx(st[c][k].x - top);
+        l[k] = fmaf(f, st[c][k].y, l[k]);
+        a[k].x = fmaf(f, v[c][k].x, a[k].x);
+        a[k].y = fmaf(f, v[c][k].y, a[k].y);
+        a[k].z = fmaf(f, v[c][k].z, a[k].z);
+        a[k].w = fmaf(f, v[c][k].w, a[k].w);
+      }
     }
+  }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
     if (r + k >= rows) break;
