@@ -171,110 +171,128 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     // A lane's rows of the warp's slice of 16 (which lies in one page): row8 and row8 + 8; its 16
     // codes of each 64: col.  (Two rows of four lanes together store to all banks.)
     const int row8 = lane >> 2, col = lane & 3;
-    const long long lane_at[2] = {row8 * p.c.ks[1] + col * 16, row8 * p.c.vs[1] + col * 16};
+    // Bytes that the lane copies of a row's 64 codes: none behind its end.
+    const int whole_bytes[2] = {col * 16 < p.c.head_dim ? 16 : 0, (4 + col) * 16 < p.c.head_dim ? 16 : 0};
+    // What is copied next: tile lt of item lw, where the warp's slice of it lies (`page` as the table
+    // has it, read a tile ahead so that nothing waits for it; an item's first one is waited for).
     TreeWalk lw(p, start);
-    int lt = lw.live ? lw.t0 : 0, lkv = 0;
-    // (As the table has it, so that nothing waits for it before its tile.)
+    int lt = 0, page = -1, next_page = -1, from = 0, offset = 0, keys = 0;
+    const uint8_t *k_lane = nullptr, *v_lane = nullptr, *s_lane = nullptr;
     auto page_at = [&](int t) {
       const int slice = t * kWidenWarps + w8;
-      return lw.live && slice * 16 < lw.size.keys
-                 ? p.c.table[lw.b * p.c.table_stride + fast_div(slice, p.div_slices)]
-                 : -1;
+      return slice * 16 < lw.size.keys ? p.c.table[lw.b * p.c.table_stride + fast_div(slice, p.div_slices)] : -1;
     };
-    int page = page_at(lt), next_page = -1;
-    auto load = [&](int stage) {
+    auto begin_item = [&]() {
+      if (!lw.live) return;
+      lt = lw.t0;
+      page = page_at(lt);
+      k_lane = p.c.k + lw.hk * p.c.ks[2] + row8 * p.c.ks[1] + col * 16;
+      v_lane = p.c.v + lw.hk * p.c.vs[2] + row8 * p.c.vs[1] + col * 16;
+      s_lane = p.c.scales + static_cast<long long>(lw.hk) * p.c.page_size * 2 + 2 * (row8 & ~1);
+    };
+    begin_item();
+    auto copy_rows = [&](const uint8_t* rows, long long eight, uint32_t to) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < L::kBlocks; ++c)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           to + ((k * L::kBlocks + c) * 32 + lane) * 16),
+                       "l"(rows + (k ? eight : 0) + c * 64), "r"(8 * k + row8 < keys ? whole_bytes[c] : 0)
+                       : "memory");
+    };
+    auto load_keys = [&](int stage) {
       if (lw.live) {
         const int slice = lt * kWidenWarps + w8;
-        const int offset = (slice - fast_div(slice, p.div_slices) * static_cast<int>(p.div_slices.d)) * 16;
         const bool real = static_cast<unsigned int>(page) < static_cast<unsigned int>(p.c.pages);
-        const int from = real ? page : 0, keys = real ? lw.size.keys - slice * 16 : 0;  // that are there
-        // (Numbers are chosen, not pointers to them: parameters read through a pointer are slow.)
-        const long long token = lkv ? p.c.vs[1] : p.c.ks[1];
-        const uint8_t* rows = (lkv ? p.c.v + lane_at[1] : p.c.k + lane_at[0]) +
-                              from * (lkv ? p.c.vs[0] : p.c.ks[0]) + offset * token +
-                              lw.hk * (lkv ? p.c.vs[2] : p.c.ks[2]);
-        const uint8_t* sc = p.c.scales + scale_at(p.c, from, lw.hk, real ? offset : 0) + 2 * (row8 & ~1);
+        from = real ? page : 0;
+        offset = (slice - fast_div(slice, p.div_slices) * static_cast<int>(p.div_slices.d)) * 16;
+        keys = real ? lw.size.keys - slice * 16 : 0;  // that are there
+        if (lt + 1 < lw.t1) next_page = page_at(lt + 1);
         const uint32_t to = codes + stage * (kWidenWarps * L::kCodeWarp);
+        copy_rows(k_lane + (from * p.c.ks[0] + offset * p.c.ks[1]), p.ks8, to);
+        // The scales of two keys each, of which those that are there.
+        const uint8_t* sc = s_lane + (from * p.scale_page + offset * 2);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const bool on = 8 * k + row8 < keys;
-#pragma unroll
-          for (int c = 0; c < L::kBlocks; ++c) {
-            const bool ok = on && (c * 4 + col) * 16 < p.c.head_dim;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             to + ((k * L::kBlocks + c) * 32 + lane) * 16),
-                         "l"(rows + k * 8 * token + c * 64), "r"(ok ? 16 : 0)
-                         : "memory");
-          }
-          // The scales of two keys, of which those that are there.
           const int there = keys - 8 * k - (row8 & ~1);
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
                            to + L::kPieces * 512 + (k * 32 + lane) * 4),
                        "l"(sc + 16 * k), "r"(there >= 2 ? 4 : there == 1 ? 2 : 0)
                        : "memory");
         }
-        // The next tile's page arrives while this one's values are copied (an item's first one
-        // is waited for).
-        if (lkv == 0) {
-          if (lt + 1 < lw.t1) next_page = page_at(lt + 1);
-        } else if (++lt < lw.t1) {
-          page = next_page;
-        } else {
-          lw.next();
-          lt = lw.live ? lw.t0 : 0;
-          page = page_at(lt);
-        }
-        lkv ^= 1;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
-    for (int i = 0; i < kCodeStages - 1; ++i) load(i);
+    auto load_values = [&](int stage) {
+      if (lw.live) {
+        copy_rows(v_lane + (from * p.c.vs[0] + offset * p.c.vs[1]), p.vs8,
+                  codes + stage * (kWidenWarps * L::kCodeWarp));
+        if (++lt < lw.t1) {
+          page = next_page;
+        } else {
+          lw.next();
+          begin_item();
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    static_assert(kCodeStages == 3, "a tile's keys, and its values, are copied a tile ahead");
+    load_keys(0);
+    load_values(1);
     bool ok = true;
     int code_stage = 0, stage = 0;
     uint32_t phase = 0, tiles = 0;
     for (TreeWalk w(p, start); ok && w.live; w.next()) {
       for (int t = w.t0; ok && t < w.t1; ++t, ++tiles) {
-#pragma unroll 1
+        uint32_t factor[2][2];  // of the rows' codes: keys', values'
+        bool there[2];
+#pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          load(code_stage == 0 ? kCodeStages - 1 : code_stage - 1);
+          const int ahead = code_stage == 0 ? kCodeStages - 1 : code_stage - 1;
+          if (kv == 0)
+            load_keys(ahead);
+          else
+            load_values(ahead);
           asm volatile("cp.async.wait_group %0;" ::"n"(kCodeStages - 1) : "memory");
-          const uint32_t from = codes + code_stage * (kWidenWarps * L::kCodeWarp);
+          const uint32_t from_codes = codes + code_stage * (kWidenWarps * L::kCodeWarp);
           uint4 u[2][L::kBlocks];
-          uint32_t two[2];
+          uint32_t two[2] = {0, 0};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            two[k] = lds32(from + L::kPieces * 512 + (k * 32 + lane) * 4) >> (16 * (row8 & 1)) & 0xFFFFu;
+            if (kv == 0)
+              two[k] = lds32(from_codes + L::kPieces * 512 + (k * 32 + lane) * 4) >> (16 * (row8 & 1)) & 0xFFFFu;
 #pragma unroll
             for (int c = 0; c < L::kBlocks; ++c)
               asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(u[k][c].x), "=r"(u[k][c].y), "=r"(u[k][c].z), "=r"(u[k][c].w)
-                           : "r"(from + ((k * L::kBlocks + c) * 32 + lane) * 16));
+                           : "r"(from_codes + ((k * L::kBlocks + c) * 32 + lane) * 16));
           }
-          ok = wait(&sh.kv_empty[stage], phase ^ 1u, kAttnProducerTimeout);
+          ok = ok && wait(&sh.kv_empty[stage], phase ^ 1u, kAttnProducerTimeout);
           if (!ok) break;
-          // The rows' bytes (0 where nothing was written: there may be NaN), and the slice's largest.
-          int key_most = 0, value_most = 0;
-          uint32_t there = 0;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (two[k] & 0xFFu) {
-              there |= 1u << (8 * k + row8);
-            } else {
-              two[k] = 0;
-#pragma unroll
-              for (int c = 0; c < L::kBlocks; ++c) u[k][c] = make_uint4(0, 0, 0, 0);
-            }
-            key_most = max(key_most, static_cast<int>(two[k] & 0xFFu));
-            value_most = max(value_most, static_cast<int>(two[k] >> 8));
-          }
-          key_most = __reduce_max_sync(0xFFFFFFFFu, key_most);
-          value_most = __reduce_max_sync(0xFFFFFFFFu, value_most);
           if (kv == 0) {
-            there = __reduce_or_sync(0xFFFFFFFFu, there);
+            // The rows' bytes, and the slice's largest.
+            uint32_t mine = 0;
+            int key_most = 0, value_most = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              there[k] = (two[k] & 0xFFu) != 0;
+              if (there[k]) mine |= 1u << (8 * k + row8);
+              if (!there[k]) two[k] = 0;
+              key_most = max(key_most, static_cast<int>(two[k] & 0xFFu));
+              value_most = max(value_most, static_cast<int>(two[k] >> 8));
+            }
+            key_most = __reduce_max_sync(0xFFFFFFFFu, key_most);
+            value_most = __reduce_max_sync(0xFFFFFFFFu, value_most);
+            mine = __reduce_or_sync(0xFFFFFFFFu, mine);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              factor[0][k] = half_power(key_most - static_cast<int>(two[k] & 0xFFu));
+              factor[1][k] = half_power(value_most - static_cast<int>(two[k] >> 8) - kValueLift);
+            }
             if (lane == 0) {
               const int f = value_most - 127 - kValueLift, slot = tiles % kSlotsMany;
-              sh.valid[slot][w8] = static_cast<uint16_t>(there);
+              sh.valid[slot][w8] = static_cast<uint16_t>(mine);
               sh.scale[slot][0][w8] = __uint_as_float(static_cast<uint32_t>(key_most) << 23);
               sh.scale[slot][1][w8] = static_cast<float>(f);
               sh.scale[slot][2][w8] = __uint_as_float(static_cast<uint32_t>(min(254, 127 - f)) << 23);
@@ -282,18 +300,16 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
           }
           uint8_t* to = smem + L::kOffWords + stage * L::kTile + (w8 * 16 + row8) * 128;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t factor = half_power(kv ? value_most - static_cast<int>(two[k] >> 8) - kValueLift
-                                                  : key_most - static_cast<int>(two[k] & 0xFFu));
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int c = 0; c < L::kBlocks; ++c) {
               uint4 a, b;
-              widen16(u[k][c], factor, a, b);
+              // (Where nothing was written there may be NaN.)
+              widen16(there[k] ? u[k][c] : make_uint4(0, 0, 0, 0), factor[kv][k], a, b);
               uint8_t* row = to + c * kBlockBytes + k * 1024;
               *reinterpret_cast<uint4*>(row + (((2 * col) ^ row8) << 4)) = a;
               *reinterpret_cast<uint4*>(row + (((2 * col + 1) ^ row8) << 4)) = b;
             }
-          }
           fence_proxy_async_shared();
           __syncwarp();
           // (fault_mode 1, a test hook: every CTA leaves its first keys un-announced.)
