@@ -7,7 +7,7 @@ import torch
 import transposed_conv_implicit_gb300 as cg
 from tests import _decoder as D
 from tests._attention import TYPES, UNIT, assert_within
-from transposed_conv_implicit_gb300 import _lib
+from transposed_conv_implicit_gb300 import _lib, decoder
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -127,6 +127,31 @@ def test_strides_and_scale():
     other = torch.empty_like(heads)
     cg.tree_attention_fwd(heads, *cache.args(), n, other, scale=0.05)
     assert torch.equal(other, out)
+
+
+def test_tables_and_trees_as_parts_of_larger_ones(monkeypatch):
+    """Rows of the block table and of the parents further apart than they are long; the tensors' device
+    not the current one, as far as one device can show."""
+    g, keys, t = _gen(24), [333, 90], 30
+    cache = _filled(g, "bf16", keys, 2, 64, 32)
+    q = torch.randn((2, t, 6, 64), generator=g, device=DEV).bfloat16()
+    up = _tree(g, 2, t, "random")
+    n = torch.tensor(keys, dtype=torch.int32, device=DEV)
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    cg.tree_attention_fwd(q, *cache.args(), n, want, parents=up)
+    width = cache.block_table.shape[1]
+    wide = torch.full((2, width + 3), 1 << 20, dtype=torch.int32, device=DEV)
+    wide[:, :width] = cache.block_table
+    more = torch.full((2, t + 5), 7, dtype=torch.int32, device=DEV)
+    more[:, :t] = up
+    monkeypatch.setattr(decoder, "_current_device", lambda: -1)
+    cg.tree_attention_fwd(q, cache.k, cache.v, cache.scales, wide[:, :width], n, got, parents=more[:, :t])
+    assert torch.equal(want, got)
+    back = [torch.empty((2, 333, 2, 64), dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    cg.kv_cache_read(*cache.args(), None, *back[:2], lengths=n)
+    cg.kv_cache_read(cache.k, cache.v, cache.scales, wide[:, :width], None, *back[2:], lengths=n)
+    for i, k in enumerate(keys):
+        assert torch.equal(back[0][i, :k], back[2][i, :k]) and torch.equal(back[1][i, :k], back[3][i, :k])
 
 
 def test_one_query_for_all():
