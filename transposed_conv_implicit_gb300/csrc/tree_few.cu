@@ -18,7 +18,7 @@
 // 16 output tiles).
 //
 // Measured: one token of 64 requests x 32/8 heads x 128 against up to 4096 keys
-// 94.5 us, its join with it (4.3 TB/s; 5.4 for each further key); 7 drafts of 32
+// 94 us, its join with it (4.3 TB/s; 5.4 for each further key); 7 drafts of 32
 // requests against up to 8192 keys 123 us.  (Turned over, with the rows along N,
 // single tokens need half the products and 128 registers, and take 99.7 us: the
 // copies alone take 89 to 95.)
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
 // hold four columns; the shares' slots are listed once per block, before the
 // launch that wrote them has ended, and a row's reads are in flight together.
 // (Found share by share, with 64-bit divisions, the join of 5 requests x 29
-// drafts took 45 us; with a row a warp that of 16 x 64 drafts 25.)
+// drafts took 45 us; with a row a warp that of 16 x 64 drafts 25, now 20.)
 constexpr int kTreeJoinWarps = 8, kTreeJoinThreads = 32 * kTreeJoinWarps;
 constexpr int kTreeMaxShares = 1024;  // of an item: two for each CTA at most
 template <typename T, int kPer>

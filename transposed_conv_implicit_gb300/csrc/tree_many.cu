@@ -27,7 +27,7 @@
 //
 // Bound by issue slots (58 %: exponentials and widening) beside the products (46
 // % of their pipe): 64 drafts of 16 requests x 32/8 heads x 128 against 8192 keys
-// 172 us, its join with it (0.79 PFLOP/s; 0.99 for each further key).
+// 168 us, its join with it (0.81 PFLOP/s; 0.99 for each further key).
 //
 // Numbers, as for few rows, but that scales are common to 16 keys: codes become
 // fp16 times their row's scale relative to the largest of the slice of 16 that
