@@ -92,6 +92,39 @@ def test_strides(c):
     assert torch.equal(dy2, dx)
 
 
+@pytest.mark.parametrize("c", [1, 5, 7, 9, 15, 63, 64, 65, 130, 321, 333, 643, 1281, 1288, 2047, 4099, 8185, 8186])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rows_that_begin_inside_a_word(c, dtype):
+    """Every place of a 16-byte word, another one in each tensor: what lies around a row stays, and a
+    row's bits do not depend on where it lies."""
+    g, dt, rows = _gen(c), TYPES[dtype], 21 if c < 2000 else 6
+    x, dy = _rows(g, rows, c, dt), torch.randn((rows, c), generator=g, device=DEV).to(dt)
+    w = (1 + 0.2 * torch.randn(c, generator=g, device=DEV)).to(torch.float32 if c % 4 == 1 else dt)
+    b = torch.randn(c, generator=g, device=DEV).to(w.dtype)
+    first = None
+    for turn in range(4):
+        views, flats = [], []
+        for n in range(4):                                  # x, dy, y, dx
+            at, apart = (2 * turn + 3 * n) % 8 if turn else 0, c + (turn + n) * (turn > 1)
+            flat = torch.full((at + rows * apart + 8,), MARK, dtype=dt, device=DEV)
+            views.append(flat[at:].as_strided((rows, c), (apart, 1), flat.storage_offset() + at))
+            flats.append(flat)
+        views[0].copy_(x)
+        views[1].copy_(dy)
+        mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+        dw, db = torch.empty(c, device=DEV), torch.empty(c, device=DEV)
+        cg.layer_norm_fwd(views[0], w, b, views[2], mean=mean, rstd=rstd)
+        cg.layer_norm_bwd(views[1], views[0], w, mean, rstd, views[3], dw, db)
+        got = [views[2].clone(), views[3].clone(), mean, rstd, dw, db]
+        _check(x, w, b, got[0], mean, rstd, dy, got[1], dw, db, 1e-5, UNIT[dtype])
+        for flat, view in list(zip(flats, views))[2:]:
+            view.fill_(MARK)
+            assert (flat == MARK).all()
+        if c % 8 and c < 8186:
+            first = first or got
+            assert all(torch.equal(p, q) for p, q in zip(got, first))
+
+
 def test_a_map_and_an_unaligned_view():
     g, dt = _gen(3), torch.float16
     x = _rows(g, 2 * 5 * 7, 48, dt).view(2, 5, 7, 48)

@@ -49,6 +49,7 @@ struct LnParams {
   float *dweight, *dbias;
   int channels, words, lanes;  // words of kVec elements, lanes of a row
   int rows, blocks;
+  bool weight_f32;  // of kShift alone: the others are built for a type
   float eps, inv_c;
   FastDiv div_length;
   long long xs[2], ds[2], ys[2];  // batch, token
@@ -215,8 +216,9 @@ __device__ __forceinline__ long long row_at(const LnParams& p, int row, const lo
   return b * s[0] + (row - b * static_cast<int>(p.div_length.d)) * s[1];
 }
 
-__device__ __forceinline__ void ring_copy(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+// 16 bytes, of which the first `bytes` are read and the others become zeros.
+__device__ __forceinline__ void ring_copy(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ uint4 ring_word(uint32_t src) {
@@ -228,13 +230,116 @@ __device__ __forceinline__ uint4 ring_word(uint32_t src) {
   return v;
 }
 
+__device__ __forceinline__ void ring_put(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// kShift: rows that begin inside a 16-byte word, as those of an odd number of
+// channels do.  A row that begins k elements into a word comes as the words that it
+// touches; what a lane computes with is elements [8 w, 8 w + 8) all the same, put
+// together from two words of the ring, its own and its neighbour's, so that a row's
+// result does not depend on where the row lies.  The results go back through the
+// ring in the same way, and to memory as whole words but for a row's two ends.
+// (Element by element, without a ring: 65536 x 321 at 0.98 TB/s forward.)
+__device__ __forceinline__ int place(const uint16_t* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7;
+}
+// Elements [k, k + 8) of the words at `a` and `b`; zeros in place of a word that the
+// ring does not have.
+__device__ __forceinline__ uint4 shifted(uint32_t a, uint32_t b, bool has_b, int k) {
+  const uint4 lo = ring_word(a);
+  uint4 hi = make_uint4(0, 0, 0, 0);
+  if (has_b) hi = ring_word(b);
+  uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int j = 0; j < 6; ++j) u[j] = k & 4 ? u[j + 2] : u[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) u[j] = k & 2 ? u[j + 1] : u[j];
+  const int odd = k & 1 ? 16 : 0;
+  return make_uint4(__funnelshift_r(u[0], u[1], odd), __funnelshift_r(u[1], u[2], odd),
+                    __funnelshift_r(u[2], u[3], odd), __funnelshift_r(u[3], u[4], odd));
+}
+// Copies word w of a row of `channels` that begins at `row`, in a tensor that begins
+// at `base` (nothing before it is read).
+__device__ __forceinline__ void shift_copy(uint32_t dst, const uint16_t* row, const uint16_t* base, int w,
+                                           int channels, bool live) {
+  const int k = place(row), left = channels + k - 8 * w;
+  if (live && w == 0 && row - base < k) {
+    uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j >= k && j < left) u[j >> 1] |= static_cast<uint32_t>(row[j - k]) << (16 * (j & 1));
+    ring_put(dst, make_uint4(u[0], u[1], u[2], u[3]));
+    return;
+  }
+  const bool on = live && left > 0;
+  const uintptr_t word = reinterpret_cast<uintptr_t>(row) & ~uintptr_t{15};  // (not read unless `on`)
+  ring_copy(dst, reinterpret_cast<const void*>(word + (on ? 16 * w : 0)), on ? min(16, 2 * left) : 0);
+}
+// Stores word w of such a row.
+__device__ __forceinline__ void shift_store(uint16_t* row, const uint4& v, int w, int k, int channels) {
+  const int first = 8 * w - k;
+  uint16_t* p = row + first;
+  if (first >= 0 && first + 8 <= channels) {
+    *reinterpret_cast<uint4*>(p) = v;
+    return;
+  }
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (first + j >= 0 && first + j < channels) p[j] = static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1)));
+}
+// An element of weight or bias, whose type is a choice of the run here: they are
+// read once a block.
+template <typename T>
+__device__ __forceinline__ float weight_at(const LnParams& p, const void* w, int at, float none) {
+  if (at >= p.channels) return 0.f;
+  if (!w) return none;
+  return p.weight_f32 ? static_cast<const float*>(w)[at] : to_float(static_cast<const T*>(w)[at]);
+}
+template <bool kBlock>
+__device__ __forceinline__ void row_sync() {
+  if constexpr (kBlock) __syncthreads();
+  else __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ uint4 joined8(const Pairs<8>& o) {
+  uint32_t u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    unpack2(o.v[j], a, b);
+    u[j] = joined(a, b, T());
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Stores a row whose words lie at `held`.
+template <int kWords>
+__device__ __forceinline__ void store_shifted(uint16_t* row, uint32_t held, uint32_t pitch, int before, int at,
+                                              int lanes, int channels) {
+  const int k = place(row), words = channels > 0 ? (channels + k + 7) >> 3 : 0;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    const int w = at + i * lanes;
+    if (w >= words) break;
+    // Elements [8 w - k, 8 w - k + 8): the last k of the word before, the first of this.
+    // (In front of the first lie elements that are not stored.)
+    const uint32_t own = held + i * pitch, left = i > 0 || at > 0 ? own + before : own;
+    shift_store(row, k == 0 ? ring_word(own) : shifted(left, own, true, 8 - k), w, k, channels);
+  }
+}
+
 // kFull: a row's words are as many as its lanes take (320 channels on 8 lanes of 5).
-template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kFull>
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kFull, bool kShift>
 __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBlock ? 1 : 3)
     layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
   constexpr bool kRing = kVec == 8;
   __shared__ float slots[2][1][32];
-  extern __shared__ __align__(16) uint8_t shared[];  // [kLnStages][kWords][threads] words
+  // [kLnStages][kWords][threads] words; kShift: then weight and bias in fp32, each
+  // word's first half [words] and its second half [words].
+  extern __shared__ __align__(16) uint8_t shared[];
   const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
   const int at = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (lanes - 1);
   const int groups = kBlock ? 1 : static_cast<int>(blockDim.x) / lanes;
@@ -251,8 +356,13 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      const bool on = live && (kFull || w < p.words);
-      ring_copy(ring + (stage * kWords + i) * pitch, x + (on ? w * kVec : 0), on);
+      const uint32_t to = ring + (stage * kWords + i) * pitch;
+      if constexpr (kShift) {
+        shift_copy(to, x, static_cast<const uint16_t*>(p.x), w, p.channels, live);
+      } else {
+        const bool on = live && (kFull || w < p.words);
+        ring_copy(to, x + (on ? w * kVec : 0), on ? 16 : 0);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -261,16 +371,43 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
     copy(blockIdx.x * groups, 0);
     copy(blockIdx.x * groups + step, 1);
   }
+  const float4* affine = reinterpret_cast<const float4*>(shared + kLnStages * kWords * blockDim.x * 16);
+  const int words = kShift ? (p.channels + 7) >> 3 : p.words;
+  // The words before and after a lane's own, in the ring.
+  const int before = at > 0 ? -16 : 16 * (lanes - 1) - static_cast<int>(pitch);
+  const int after = at + 1 < lanes ? 16 : static_cast<int>(pitch) - 16 * at;
+  if constexpr (kShift) {
+    float* to = reinterpret_cast<float*>(shared + kLnStages * kWords * blockDim.x * 16);
+    for (int e = threadIdx.x; e < 8 * words; e += blockDim.x) {
+      float* t = to + (e & 4) * words + (e >> 3) * 4 + (e & 3);
+      t[0] = weight_at<T>(p, p.weight, e, 1.f);
+      t[8 * words] = weight_at<T>(p, p.bias, e, 0.f);
+    }
+    __syncthreads();
+  }
   // (Every lane goes through every step: groups without a row left load nothing.)
   for (int row0 = blockIdx.x * groups; row0 < p.rows; row0 += step) {
     const int row = row0 + group;
     const bool live = row < p.rows;
     Word<kVec> raw[kWords];
+    const uint32_t held = ring + stage * kWords * pitch;
     if constexpr (kRing) {
+      if constexpr (kShift) row_sync<kBlock>();  // (the last row's results have left the ring)
       copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
+      if constexpr (kShift) {
+        row_sync<kBlock>();
+        const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
+        const int k = place(x);
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) raw[i].v = ring_word(ring + (stage * kWords + i) * pitch);
+        for (int i = 0; i < kWords; ++i) {
+          const uint32_t own = held + i * pitch;
+          raw[i].v = shifted(own, own + after, i + 1 < kWords || at + 1 < lanes, k);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) raw[i].v = ring_word(held + i * pitch);
+      }
       stage = stage == kLnStages - 1 ? 0 : stage + 1;
     } else {
       const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
@@ -296,32 +433,55 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
     total = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      if (kFull || at + i * lanes < p.words)
+      const int w = at + i * lanes;
+      if (kFull || w < words) {
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          f[i].v[j] = add2(f[i].v[j], minus);
-          total = fma2(f[i].v[j], f[i].v[j], total);
-        }
+        for (int j = 0; j < kPairs; ++j) f[i].v[j] = add2(f[i].v[j], minus);
+        if constexpr (kShift)
+          if (w == words - 1) {  // zeros behind the row
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+              float a, b;
+              unpack2(f[i].v[j], a, b);
+              f[i].v[j] = pack2(8 * w + 2 * j < p.channels ? a : 0.f, 8 * w + 2 * j + 1 < p.channels ? b : 0.f);
+            }
+          }
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) total = fma2(f[i].v[j], f[i].v[j], total);
+      }
     }
     sum[0] = both_of(total);
     row_sum<kBlock, 1>(sum, lanes, slots, turn);
     const float rstd = inverse_root(fmaf(sum[0], p.inv_c, p.eps));
-    if (!live) continue;
-    if (at == 0) {
+    if (!kShift && !live) continue;
+    if (live && at == 0) {
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
     }
-    uint16_t* y = static_cast<uint16_t*>(p.y) + row_at(p, row, p.ys);
+    uint16_t* y = static_cast<uint16_t*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
     const uint64_t rr = pack2(rstd, rstd);
+    if constexpr (kShift) row_sync<kBlock>();  // (all lanes have read the row)
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (!kFull && w >= p.words) break;
-      const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
-      const Pairs<kVec> bs = load_weight<W, kVec>(p.bias, w * kVec, 0.f);
+      if (!kFull && w >= words) break;
+      Pairs<kVec> wt, bs;
+      if constexpr (kShift) {
+        const float4 a = affine[w], b = affine[words + w], c = affine[2 * words + w], d = affine[3 * words + w];
+        wt.v[0] = pack2(a.x, a.y), wt.v[1] = pack2(a.z, a.w), wt.v[2] = pack2(b.x, b.y), wt.v[3] = pack2(b.z, b.w);
+        bs.v[0] = pack2(c.x, c.y), bs.v[1] = pack2(c.z, c.w), bs.v[2] = pack2(d.x, d.y), bs.v[3] = pack2(d.z, d.w);
+      } else {
+        wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
+        bs = load_weight<W, kVec>(p.bias, w * kVec, 0.f);
+      }
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) f[i].v[j] = fma2(mul2(f[i].v[j], rr), wt.v[j], bs.v[j]);
-      store_word<T, kVec>(y + w * kVec, f[i]);
+      if constexpr (kShift) ring_put(held + i * pitch, joined8<T>(f[i]));
+      else store_word<T, kVec>(y + w * kVec, f[i]);
+    }
+    if constexpr (kShift) {
+      row_sync<kBlock>();
+      store_shifted<kWords>(y, held, pitch, before, at, lanes, live ? p.channels : 0);
     }
   }
 }
@@ -331,7 +491,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 // them kept, a row of 4096 takes 360 instructions of a warp, 880 without;
 // twice the lanes with two words each: 188 us for both passes over 16381 rows,
 // 153 with four.)
-template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull>
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull, bool kShift>
 __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512 : 256)
     layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
   constexpr bool kRing = kVec == 8, kKeep = kVec == 8 && !kWide;
@@ -350,13 +510,24 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
   for (int i = 0; i < kWords * kPairs; ++i) dw[i] = db[i] = 0;
   grid_dependency_wait();
   grid_launch_dependents();
+  const int words = kShift ? (p.channels + 7) >> 3 : p.words;
   Pairs<kVec> weight[kKeep ? kWords : 1];
-  if constexpr (kKeep)
+  if constexpr (kShift)
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const int e = 8 * (at + i * lanes) + 2 * j;
+        weight[i].v[j] = pack2(weight_at<T>(p, p.weight, e, 1.f), weight_at<T>(p, p.weight, e + 1, 1.f));
+      }
+  else if constexpr (kKeep)
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
       weight[i] = load_weight<W, kVec>(kFull || at + i * lanes < p.words ? p.weight : nullptr, (at + i * lanes) * kVec, 1.f);
   const int step = gridDim.x * groups;
   const uint32_t ring = smem_u32(shared) + threadIdx.x * 16, pitch = blockDim.x * 16;
+  const int before = at > 0 ? -16 : 16 * (lanes - 1) - static_cast<int>(pitch);
+  const int after = at + 1 < lanes ? 16 : static_cast<int>(pitch) - 16 * at;
   float stat[2] = {0.f, 0.f}, next_stat[2] = {0.f, 0.f};  // mean and rstd of the next rows, as they are copied
   auto copy = [&](int row0, int stage) {
     const int row = row0 + group;
@@ -366,10 +537,15 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      const bool on = live && (kFull || w < p.words);
       const uint32_t to = ring + (stage * 2 * kWords + i) * pitch;
-      ring_copy(to, x + (on ? w * kVec : 0), on);
-      ring_copy(to + kWords * pitch, dy + (on ? w * kVec : 0), on);
+      if constexpr (kShift) {
+        shift_copy(to, x, static_cast<const uint16_t*>(p.x), w, p.channels, live);
+        shift_copy(to + kWords * pitch, dy, static_cast<const uint16_t*>(p.dy), w, p.channels, live);
+      } else {
+        const bool on = live && (kFull || w < p.words);
+        ring_copy(to, x + (on ? w * kVec : 0), on ? 16 : 0);
+        ring_copy(to + kWords * pitch, dy + (on ? w * kVec : 0), on ? 16 : 0);
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -392,14 +568,30 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
       next_stat[0] = p.mean[row + step];
       next_stat[1] = p.rstd[row + step];
     }
+    const uint32_t held = ring + stage * 2 * kWords * pitch;
     if constexpr (kRing) {
+      if constexpr (kShift) row_sync<kBlock>();  // (the last row's results have left the ring)
       copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
+      if constexpr (kShift) {
+        row_sync<kBlock>();
+        const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
+        const uint16_t* dy = static_cast<const uint16_t*>(p.dy) + (live ? row_at(p, row, p.ds) : 0);
+        const int kx = place(x), kd = place(dy);
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        const uint32_t from = ring + (stage * 2 * kWords + i) * pitch;
-        rx[i].v = ring_word(from);
-        rd[i].v = ring_word(from + kWords * pitch);
+        for (int i = 0; i < kWords; ++i) {
+          const bool next = i + 1 < kWords || at + 1 < lanes;
+          const uint32_t own = held + i * pitch, own_d = own + kWords * pitch;
+          rx[i].v = shifted(own, own + after, next, kx);
+          rd[i].v = shifted(own_d, own_d + after, next, kd);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          const uint32_t from = held + i * pitch;
+          rx[i].v = ring_word(from);
+          rd[i].v = ring_word(from + kWords * pitch);
+        }
       }
       stage = stage == kLnStages - 1 ? 0 : stage + 1;
     } else {
@@ -421,7 +613,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (!kFull && w >= p.words) break;
+      if (!kFull && w >= words) break;
       const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
       Pairs<kVec> wt;
       if constexpr (kKeep) wt = weight[i];
@@ -442,14 +634,15 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
     }
     float sum[2] = {both_of(sum_g), both_of(sum_gh)};
     row_sum<kBlock, 2>(sum, lanes, slots, turn);
-    if (!live) continue;
+    if (!kShift && !live) continue;
     const float c0 = -rstd * (sum[0] * p.inv_c), c1 = -rstd * (sum[1] * p.inv_c);
     const uint64_t cc0 = pack2(c0, c0), cc1 = pack2(c1, c1);
-    uint16_t* dx = static_cast<uint16_t*>(p.y) + row_at(p, row, p.ys);
+    uint16_t* dx = static_cast<uint16_t*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
+    if constexpr (kShift) row_sync<kBlock>();  // (all lanes have read the row)
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (!kFull && w >= p.words) break;
+      if (!kFull && w >= words) break;
       Pairs<kVec> o;
       if constexpr (kKeep) {
 #pragma unroll
@@ -461,7 +654,12 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
         for (int j = 0; j < kPairs; ++j)
           o.v[j] = fma2(mul2(g.v[j], wt.v[j]), rr, fma2(fma2(x.v[j], rr, shift), cc1, cc0));
       }
-      store_word<T, kVec>(dx + w * kVec, o);
+      if constexpr (kShift) ring_put(held + i * pitch, joined8<T>(o));
+      else store_word<T, kVec>(dx + w * kVec, o);
+    }
+    if constexpr (kShift) {
+      row_sync<kBlock>();
+      store_shifted<kWords>(dx, held, pitch, before, at, lanes, live ? p.channels : 0);
     }
   }
   if constexpr (kRing) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -474,16 +672,17 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
     for (int j = 0; j < kPairs; ++j) {
       float a, b;
       unpack2(v[j], a, b);
-      float* t = to + w * kVec + 2 * j;
-      t[0] = more ? t[0] + a : a;
-      if (kVec == 8) t[1] = more ? t[1] + b : b;
+      const int c = w * kVec + 2 * j;
+      float* t = to + c;
+      if (!kShift || c < p.channels) t[0] = more ? t[0] + a : a;
+      if (kVec == 8 && (!kShift || c + 1 < p.channels)) t[1] = more ? t[1] + b : b;
     }
   };
   if constexpr (kBlock) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
-      if (!kFull && w >= p.words) break;
+      if (!kFull && w >= words) break;
       put(out, w, dw + i * kPairs, false);
       put(out + p.channels, w, db + i * kPairs, false);
     }
@@ -501,7 +700,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
 #pragma unroll
         for (int i = 0; i < kWords; ++i) {
           const int w = at + i * lanes;
-          if (!kFull && w >= p.words) break;
+          if (!kFull && w >= words) break;
           put(sums, w, dw + i * kPairs, next > 0);
           put(sums + p.channels, w, db + i * kPairs, next > 0);
         }
@@ -544,19 +743,23 @@ __global__ void __launch_bounds__(32 * kSumWarps)
 // How a row's words lie on lanes.
 struct LnShape {
   int vec, words, lanes, per_lane, threads;
-  bool block;
+  bool block, shift;
 };
+
+// Words that a row touches at most, wherever in one it begins.
+int ln_shift_words(int channels) { return (channels + 14) / 8; }
 
 // How a row lies on lanes: as few idle words as possible, then few words a lane.
 // Forward up to five a lane (320 channels on 8 lanes of 5: 19.8 us, on 16 of 3
 // 24.1); backward four, with what it keeps of a row.  Longer rows take a block.
-LnShape ln_shape(int channels, bool vectors, bool backward) {
+LnShape ln_shape(int channels, bool vectors, bool shift, bool backward) {
   LnShape s{};
   s.vec = vectors ? 8 : 1;
-  s.words = channels / s.vec;
-  const int most = !vectors ? 8 : backward ? 4 : 5;
+  s.shift = shift;
+  s.words = shift ? ln_shift_words(channels) : channels / s.vec;
+  const int most = backward ? 4 : 5;
   long long best = -1;
-  for (int lanes = 32; lanes >= 1; lanes >>= 1) {
+  for (int lanes = vectors ? 32 : 0; lanes >= 1; lanes >>= 1) {
     const int per = (s.words + lanes - 1) / lanes;
     if (per > most) continue;
     const long long idle = static_cast<long long>(lanes) * per - s.words;
@@ -598,9 +801,9 @@ cudaError_t blocks_per_sm(Kernel kernel, std::atomic<int> (*known)[16], int thre
 
 int ln_groups(const LnShape& s) { return s.block ? 1 : s.threads / s.lanes; }
 
-template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull>
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull, bool kShift>
 cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms, cudaStream_t stream) {
-  const auto kernel = layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock, kWide, kFull>;
+  const auto kernel = layer_norm_bwd_kernel<T, W, kVec, kWords, kBlock, kWide, kFull, kShift>;
   const size_t ring = kVec == 8 ? static_cast<size_t>(kLnStages) * 2 * kWords * s.threads * 16 : 0;
   const size_t smem = std::max(ring, s.block ? size_t{0} : static_cast<size_t>(2) * p.channels * sizeof(float));
   static std::atomic<size_t> configured[kMaxDevices];
@@ -619,12 +822,13 @@ cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms,
                     stream, p);
 }
 
-template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull>
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull, bool kShift>
 cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
   const long long need = (static_cast<long long>(p.rows) + ln_groups(s) - 1) / ln_groups(s);
   if (!backward) {
-    const auto kernel = layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock, kFull>;
-    const size_t smem = kVec == 8 ? static_cast<size_t>(kLnStages) * kWords * s.threads * 16 : 0;
+    const auto kernel = layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock, kFull, kShift>;
+    size_t smem = kVec == 8 ? static_cast<size_t>(kLnStages) * kWords * s.threads * 16 : 0;
+    if (kShift) smem += static_cast<size_t>(s.words) * 16 * sizeof(float);
     static std::atomic<size_t> configured[kMaxDevices];
     cudaError_t err = raise_smem(kernel, configured, smem);
     if (err != cudaSuccess) return err;
@@ -637,25 +841,27 @@ cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cuda
   }
   // (Five words a lane are for the forward pass alone: see ln_shape.)
   if constexpr (kVec == 8 && kWords == 5) return cudaErrorInvalidValue;
-  else return ln_launch_bwd<T, W, kVec, kWords, kBlock, kWide, kFull>(p, s, need, sms, stream);
+  else return ln_launch_bwd<T, W, kVec, kWords, kBlock, kWide, kFull, kShift>(p, s, need, sms, stream);
 }
 template <typename T, typename W>
 cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, int sms,
                             cudaStream_t stream) {
   const auto part = [&](auto vec, auto words) {  // rows on a warp's lanes
     constexpr int kVec = decltype(vec)::value, kWords = decltype(words)::value;
-    if constexpr (kVec == 8)
-      if (s.lanes * kWords == s.words)
-        return ln_launch<T, W, kVec, kWords, false, false, true>(p, s, backward, sms, stream);
-    return ln_launch<T, W, kVec, kWords, false, false, false>(p, s, backward, sms, stream);
+    if (s.shift) return ln_launch<T, T, kVec, kWords, false, false, false, true>(p, s, backward, sms, stream);
+    if (s.lanes * kWords == s.words)
+      return ln_launch<T, W, kVec, kWords, false, false, true, false>(p, s, backward, sms, stream);
+    return ln_launch<T, W, kVec, kWords, false, false, false, false>(p, s, backward, sms, stream);
   };
   const auto whole = [&](auto vec, auto words, auto wide) {  // rows on a block
     constexpr int kVec = decltype(vec)::value, kWords = decltype(words)::value;
     constexpr bool kWide = decltype(wide)::value;
+    if constexpr (kVec == 8 && !kWide)
+      if (s.shift) return ln_launch<T, T, kVec, kWords, true, false, false, true>(p, s, backward, sms, stream);
     if constexpr (kVec == 8)
       if (s.lanes * kWords == s.words)
-        return ln_launch<T, W, kVec, kWords, true, kWide, true>(p, s, backward, sms, stream);
-    return ln_launch<T, W, kVec, kWords, true, kWide, false>(p, s, backward, sms, stream);
+        return ln_launch<T, W, kVec, kWords, true, kWide, true, false>(p, s, backward, sms, stream);
+    return ln_launch<T, W, kVec, kWords, true, kWide, false, false>(p, s, backward, sms, stream);
   };
   using N1 = std::integral_constant<int, 1>;
   using N2 = std::integral_constant<int, 2>;
@@ -672,8 +878,7 @@ cudaError_t ln_launch_shape(const LnParams& p, const LnShape& s, bool backward, 
     return n == 1 ? part(N8(), N1()) : n == 2 ? part(N8(), N2()) : n == 3 ? part(N8(), N3())
          : n == 4 ? part(N8(), N4()) : part(N8(), N5());
   }
-  if (s.block) return n <= 8 ? whole(N1(), N8(), std::false_type()) : whole(N1(), N16(), std::false_type());
-  return n <= 2 ? part(N1(), N2()) : n <= 4 ? part(N1(), N4()) : part(N1(), N8());
+  return n <= 8 ? whole(N1(), N8(), std::false_type()) : whole(N1(), N16(), std::false_type());
 }
 
 bool off(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -748,7 +953,10 @@ conv_status_t ln_run(const layer_norm_args_t* args, bool backward, void* workspa
   vectors = vectors && !off(a.weight, 16) && (backward || !off(a.bias, 16));
   for (int i = 0; i < 2; ++i)
     vectors = vectors && p.xs[i] % 8 == 0 && p.ys[i] % 8 == 0 && p.ds[i] % 8 == 0;
-  const LnShape s = ln_shape(a.channels, vectors, backward);
+  // (Up to 1024 words, which a block of 256 threads takes.)
+  const bool shift = !vectors && ln_shift_words(a.channels) <= 1024;
+  p.weight_f32 = a.weight_f32 != 0;
+  const LnShape s = ln_shape(a.channels, vectors || shift, shift, backward);
   p.words = s.words;
   p.lanes = s.lanes;
   if (backward) {
