@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
   constexpr bool kRing = kVec == 8;
   __shared__ float slots[2][1][32];
   // [kLnStages][kWords][threads] words; kShift: then weight and bias in fp32, each
-  // word's first half [words] and its second half [words].
+  // word's first half [words] and its second half [words] (from memory in every row:
+  // 65536 x 321 in 41 us, so 33).
   extern __shared__ __align__(16) uint8_t shared[];
   const int lanes = kBlock ? static_cast<int>(blockDim.x) : p.lanes;
   const int at = kBlock ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (lanes - 1);
@@ -392,11 +393,14 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
     Word<kVec> raw[kWords];
     const uint32_t held = ring + stage * kWords * pitch;
     if constexpr (kRing) {
-      if constexpr (kShift) row_sync<kBlock>();  // (the last row's results have left the ring)
-      copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
       if constexpr (kShift) {
+        // The others' copies have come, and the last row's results have left the ring.
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 2) : "memory");
         row_sync<kBlock>();
+      }
+      copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
+      if constexpr (!kShift) asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
+      if constexpr (kShift) {
         const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
         const int k = place(x);
 #pragma unroll
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
     }
     uint16_t* y = static_cast<uint16_t*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
     const uint64_t rr = pack2(rstd, rstd);
-    if constexpr (kShift) row_sync<kBlock>();  // (all lanes have read the row)
+    if constexpr (kShift && !kBlock) __syncwarp();  // (all lanes have read the row; a block's, before its sums)
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
@@ -570,11 +574,14 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
     }
     const uint32_t held = ring + stage * 2 * kWords * pitch;
     if constexpr (kRing) {
-      if constexpr (kShift) row_sync<kBlock>();  // (the last row's results have left the ring)
-      copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
       if constexpr (kShift) {
+        // The others' copies have come, and the last row's results have left the ring.
+        asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 2) : "memory");
         row_sync<kBlock>();
+      }
+      copy(row0 + 2 * step, stage == 0 ? 2 : stage - 1);
+      if constexpr (!kShift) asm volatile("cp.async.wait_group %0;" ::"n"(kLnStages - 1) : "memory");
+      if constexpr (kShift) {
         const uint16_t* x = static_cast<const uint16_t*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
         const uint16_t* dy = static_cast<const uint16_t*>(p.dy) + (live ? row_at(p, row, p.ds) : 0);
         const int kx = place(x), kd = place(dy);
@@ -638,7 +645,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
     const float c0 = -rstd * (sum[0] * p.inv_c), c1 = -rstd * (sum[1] * p.inv_c);
     const uint64_t cc0 = pack2(c0, c0), cc1 = pack2(c1, c1);
     uint16_t* dx = static_cast<uint16_t*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
-    if constexpr (kShift) row_sync<kBlock>();  // (all lanes have read the row)
+    if constexpr (kShift && !kBlock) __syncwarp();  // (all lanes have read the row; a block's, before its sums)
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
@@ -773,23 +780,24 @@ LnShape ln_shape(int channels, bool vectors, bool shift, bool backward) {
   s.threads = backward ? 128 : 256;
   if (best >= 0) return s;
   s.block = true;
-  const int target = !vectors ? 8 : 4;
-  s.threads = 64;
-  while (s.threads < 1024 && (s.words + s.threads - 1) / s.threads > target) s.threads <<= 1;
+  // Three or four words a lane, whichever leaves fewer lanes idle.
+  const auto warps = [&](int per) { return (s.words + 32 * per - 1) / (32 * per) * 32; };
+  const int four = std::max(64, warps(4)), three = std::max(64, warps(3));
+  s.threads = !vectors ? 1024 : three <= 256 && three * 3 < four * 4 ? three : four;
   s.lanes = s.threads;
   s.per_lane = (s.words + s.threads - 1) / s.threads;
   return s;
 }
 
 // Blocks of a kernel that an SM runs at once, asked for once for each device and
-// number of threads (a power of two; the shared memory goes by that).
+// number of warps (the shared memory goes by that).
 template <typename Kernel>
-cudaError_t blocks_per_sm(Kernel kernel, std::atomic<int> (*known)[16], int threads, size_t smem, int* fit) {
-  int dev = 0, at = 0;
+cudaError_t blocks_per_sm(Kernel kernel, std::atomic<int> (*known)[33], int threads, size_t smem, int* fit) {
+  int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  while ((1 << at) < threads) ++at;
+  const int at = threads / 32;
   *fit = known[dev][at].load(std::memory_order_relaxed);
   if (*fit > 0) return cudaSuccess;
   err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, kernel, threads, smem);
@@ -811,7 +819,7 @@ cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms,
   if (err != cudaSuccess) return err;
   // As many blocks as run at once: each keeps its columns' sums over all of its rows.
   int fit = 0;
-  static std::atomic<int> known[kMaxDevices][16];
+  static std::atomic<int> known[kMaxDevices][33];
   err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
   if (err != cudaSuccess) return err;
   p.blocks = static_cast<int>(
@@ -833,7 +841,7 @@ cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cuda
     cudaError_t err = raise_smem(kernel, configured, smem);
     if (err != cudaSuccess) return err;
     int fit = 0;
-    static std::atomic<int> known[kMaxDevices][16];
+    static std::atomic<int> known[kMaxDevices][33];
     err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
     if (err != cudaSuccess) return err;
     const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(fit) * sms));
