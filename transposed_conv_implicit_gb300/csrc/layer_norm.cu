@@ -496,9 +496,9 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 // twice the lanes with two words each: 188 us for both passes over 16381 rows,
 // 153 with four.)
 template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull, bool kShift>
-__global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512 : 256)
+__global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512 : 256, !kShift ? 1 : kBlock ? 2 : 3)
     layer_norm_bwd_kernel(const __grid_constant__ LnParams p) {
-  constexpr bool kRing = kVec == 8, kKeep = kVec == 8 && !kWide;
+  constexpr bool kRing = kVec == 8, kKeep = kVec == 8 && !kWide, kKeepRow = kKeep && !kShift;
   __shared__ float slots[2][2][32];
   // [kLnStages][2 * kWords][threads] words; then, where a block has several groups, [2][C].
   extern __shared__ __align__(16) uint8_t shared[];
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
     // h = x rstd - mean rstd
     const uint64_t rr = pack2(rstd, rstd), shift = pack2(-mean * rstd, -mean * rstd);
     uint64_t sum_g = 0, sum_gh = 0;
-    Pairs<kVec> hs[kKeep ? kWords : 1], fs[kKeep ? kWords : 1];  // h, and dy w
+    Pairs<kVec> hs[kKeepRow ? kWords : 1], fs[kKeepRow ? kWords : 1];  // h, and dy w
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
         db[i * kPairs + j] = add2(db[i * kPairs + j], g.v[j]);
         sum_g = add2(sum_g, f);
         sum_gh = fma2(f, h, sum_gh);
-        if constexpr (kKeep) {
+        if constexpr (kKeepRow) {
           hs[i].v[j] = h;
           fs[i].v[j] = f;
         }
@@ -651,12 +651,14 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
       const int w = at + i * lanes;
       if (!kFull && w >= words) break;
       Pairs<kVec> o;
-      if constexpr (kKeep) {
+      if constexpr (kKeepRow) {
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) o.v[j] = fma2(fs[i].v[j], rr, fma2(hs[i].v[j], cc1, cc0));
       } else {
         const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
-        const Pairs<kVec> wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
+        Pairs<kVec> wt;
+        if constexpr (kKeep) wt = weight[i];
+        else wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j)
           o.v[j] = fma2(mul2(g.v[j], wt.v[j]), rr, fma2(fma2(x.v[j], rr, shift), cc1, cc0));
