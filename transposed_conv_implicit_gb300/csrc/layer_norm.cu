@@ -286,9 +286,21 @@ __device__ __forceinline__ void shift_store(uint16_t* row, const uint4& v, int w
     return;
   }
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  if (first + 8 <= channels) {  // from element k on: one, two and four of them
+    const int even = k + (k & 1);
+    if (k & 1) p[k] = static_cast<uint16_t>((k & 4 ? k & 2 ? u[3] : u[2] : k & 2 ? u[1] : u[0]) >> 16);
+    if (even & 2) *reinterpret_cast<uint32_t*>(p + even) = even & 4 ? u[3] : u[1];
+    if (even <= 4) *reinterpret_cast<uint2*>(p + 4) = make_uint2(u[2], u[3]);
+  } else if (first >= 0) {  // up to the row's end: four, two and one
+    const int n = channels - first;
+    if (n & 4) *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    if (n & 2) *reinterpret_cast<uint32_t*>(p + (n & 4)) = n & 4 ? u[2] : u[0];
+    if (n & 1) p[n - 1] = static_cast<uint16_t>(n & 4 ? n & 2 ? u[3] : u[2] : n & 2 ? u[1] : u[0]);
+  } else {  // a row within one word
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (first + j >= 0 && first + j < channels) p[j] = static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1)));
+    for (int j = 0; j < 8; ++j)
+      if (first + j >= 0 && first + j < channels) p[j] = static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1)));
+  }
 }
 // An element of weight or bias, whose type is a choice of the run here: they are
 // read once a block.
