@@ -45,8 +45,9 @@ extern "C" {
  * above 0x7F000000; strides from 2^40 on.  CONV_ERR_INVALID_VALUE: negative
  * sizes or strides, eps negative or not finite, outputs with strides of 0,
  * missing tensors.  CONV_ERR_MISALIGNED: a pointer off its element's size.
- * (Rows of 8 k elements on 16-byte boundaries are read 16 bytes at a time,
- * any others element by element.)
+ * (Rows are read 16 bytes at a time: fastest with C and strides multiples of 8
+ * and tensors on 16-byte boundaries, then with any others up to C = 8185; beyond,
+ * those go element by element.)
  * ------------------------------------------------------------------------ */
 typedef struct {
   int dtype; /* conv_dtype_t */

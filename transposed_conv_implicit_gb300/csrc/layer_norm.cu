@@ -6,7 +6,8 @@
 //
 // Bound by memory: x in, y out; x and dy in, dx out.  Measured: 65536 x 320
 // forward 17.8 us (4.7 TB/s), backward 24 us (5.2); 16381 x 4096 forward 48 us
-// (5.6 TB/s), backward 80 us (5.0); the weights' sums another 4.  A row lies in
+// (5.6 TB/s), backward 80 us (5.0); the weights' sums another 4; with 321 and 4099
+// channels 32 and 103 us forward, 89 and 252 for both passes.  A row lies in
 // the registers of `lanes` lanes (a power of two up to a warp, or a whole block),
 // up to kWords words of kVec elements each, so it is read once: the mean, the
 // deviations from it and the result come from the same registers.  Lanes take
@@ -241,7 +242,8 @@ __device__ __forceinline__ void ring_put(uint32_t dst, uint4 v) {
 // together from two words of the ring, its own and its neighbour's, so that a row's
 // result does not depend on where the row lies.  The results go back through the
 // ring in the same way, and to memory as whole words but for a row's two ends.
-// (Element by element, without a ring: 65536 x 321 at 0.98 TB/s forward.)
+// (65536 x 321 forward 32 us at 61 % of the issue slots, element by element without
+// a ring 86.)
 __device__ __forceinline__ int place(const uint16_t* p) {
   return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7;
 }
@@ -263,9 +265,9 @@ __device__ __forceinline__ uint4 shifted(uint32_t a, uint32_t b, bool has_b, int
 // Copies word w of a row of `channels` that begins at `row`, in a tensor that begins
 // at `base` (nothing before it is read).
 __device__ __forceinline__ void shift_copy(uint32_t dst, const uint16_t* row, const uint16_t* base, int w,
-                                           int channels, bool live) {
+                                           bool first, int channels, bool live) {
   const int k = place(row), left = channels + k - 8 * w;
-  if (live && w == 0 && row - base < k) {
+  if (first && live && row - base < k) {
     uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
       const int w = at + i * lanes;
       const uint32_t to = ring + (stage * kWords + i) * pitch;
       if constexpr (kShift) {
-        shift_copy(to, x, static_cast<const uint16_t*>(p.x), w, p.channels, live);
+        shift_copy(to, x, static_cast<const uint16_t*>(p.x), w, i == 0 && at == 0, p.channels, live);
       } else {
         const bool on = live && (kFull || w < p.words);
         ring_copy(to, x + (on ? w * kVec : 0), on ? 16 : 0);
@@ -555,8 +557,8 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
       const int w = at + i * lanes;
       const uint32_t to = ring + (stage * 2 * kWords + i) * pitch;
       if constexpr (kShift) {
-        shift_copy(to, x, static_cast<const uint16_t*>(p.x), w, p.channels, live);
-        shift_copy(to + kWords * pitch, dy, static_cast<const uint16_t*>(p.dy), w, p.channels, live);
+        shift_copy(to, x, static_cast<const uint16_t*>(p.x), w, i == 0 && at == 0, p.channels, live);
+        shift_copy(to + kWords * pitch, dy, static_cast<const uint16_t*>(p.dy), w, i == 0 && at == 0, p.channels, live);
       } else {
         const bool on = live && (kFull || w < p.words);
         ring_copy(to, x + (on ? w * kVec : 0), on ? 16 : 0);
