@@ -77,7 +77,7 @@ struct Many {
 struct ManyShared {
   uint64_t kv_full[kWordStages], kv_empty[kWordStages];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2][2], p_full[2][2], o_done[2];  // [group][half of a tile]
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [group][half of a tile]
   uint64_t drain[2];
   SplitStart start;
   uint32_t tmem;
@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       for (int h = 0; h < 2; ++h) {
         mbar_init(smem_u32(&sh.s_full[g][h]), 1);
         mbar_init(smem_u32(&sh.p_full[g][h]), 4);
+        mbar_init(smem_u32(&sh.o_done[g][h]), 1);
       }
-      mbar_init(smem_u32(&sh.o_done[g]), 1);
       mbar_init(smem_u32(&sh.drain[g]), 1);
     }
     sh.abort_flag = 0;
@@ -395,7 +395,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
           mma_ts_x4(to, ts + half * kHalfKeys,
                     lead_mn(kBlockBytes) | (word_lo + v_stage * (L::kTile >> 4) + half * (kHalfKeys * 128 >> 4)),
                     idesc_o, first && half == 0 ? 0u : 1u, 4);
-          mma_commit_warp(smem_u32(&sh.o_done[g]));
+          // (A barrier for each half: who has seen the scores of a half knows the products of the
+          // tile before to be done, so a wait for this half's cannot take the phase before for it.
+          // With one barrier for both the two halves' phases could be taken for one another.)
+          mma_commit_warp(smem_u32(&sh.o_done[g][half]));
           if (half == 1) mma_commit_warp(smem_u32(&sh.kv_empty[v_stage]));
           if (more) scores(stage, half);
         }
@@ -430,7 +433,6 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     const uint32_t bar_id = 1 + g;
     const int d = p.c.head_dim;
     uint32_t tiles = 0, items = 0, seen = 0;  // own tiles: barrier parity; all tiles: validity's slot
-    uint32_t halves = 0;                      // own halves of tiles
     bool ok = true;
     for (TreeWalk w(p, start); ok && w.live; w.next()) {
       const int left = w.size.drafts * p.group - w.row_tile * p.tile_rows;
@@ -574,7 +576,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
                   l *= f;
                 }
                 // The product of the half before has to be done.
-                ok = wait(&sh.o_done[g], (halves - 1) & 1u, kAttnSoftmaxTimeout);
+                ok = wait(&sh.o_done[g][half ^ 1], (tiles - (half ^ 1)) & 1u, kAttnSoftmaxTimeout);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -621,12 +623,13 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[g][half]));
-          ++halves;
         }
         ++tiles;
       }
       seen += w.t1 - w.t0;
-      if (ok && !first) ok = wait(&sh.o_done[g], (halves - 1) & 1u, kAttnSoftmaxTimeout);
+      if (ok && !first)  // the last tile's products, each half's
+        ok = wait(&sh.o_done[g][0], (tiles - 1) & 1u, kAttnSoftmaxTimeout) &&
+             wait(&sh.o_done[g][1], (tiles - 1) & 1u, kAttnSoftmaxTimeout);
       ok = barrier_all(bar_id, 128, ok);
       if (!ok) break;
       tc_fence_after();
