@@ -154,3 +154,60 @@ def test_the_walk_sees_what_is_missing():
     nothing completes, the standstill."""
     assert _walk((2,), False, set(), [])[0]
     assert _walk((2,), False, set(), END + [("0", "tiles & 1")])[1]
+
+
+def _meet(pairs, read_wait):
+    """Two softmax groups over items of which pairs[i] are held by both and written here: what each does,
+    over every interleaving.  Returns (whether one reads the other's statistics or output of another item,
+    whether anything can wait for ever)."""
+    steps = []
+    for i, pair in enumerate(pairs):
+        if i and pairs[i - 1] and read_wait:
+            steps.append(("wait", 1))
+        steps.append(("products", i))            # writes the group's output
+        if pair:
+            steps += [("stat", i), ("arrive",), ("wait", 0), ("read", i), ("arrive",)]
+    early = stuck = False
+    seen, todo = set(), [(0, 0)]
+    while todo:
+        state = todo.pop()
+        if state in seen:
+            continue
+        seen.add(state)
+        done = [steps[:at] for at in state]
+        phase = sum(s[0] == "arrive" for d in done for s in d) // 2
+        # (An arrival counts for the phase that is incomplete: nobody may be two ahead.)
+        counts = [sum(s[0] == "arrive" for s in d) for d in done]
+        assert abs(counts[0] - counts[1]) <= 1 or not read_wait
+        nexts = []
+        for g in range(2):
+            if state[g] == len(steps):
+                continue
+            s = steps[state[g]]
+            if s[0] == "read":
+                other = done[1 - g]
+                last = lambda kind: max([x[1] for x in other if x[0] == kind], default=-1)
+                early |= last("stat") != s[1] or last("products") != s[1]
+            if s[0] != "wait" or (phase & 1) != s[1]:
+                nexts.append((state[0] + (g == 0), state[1] + (g == 1)))
+        stuck |= not nexts and state != (len(steps), len(steps))
+        todo += nexts
+    return early, stuck
+
+
+@pytest.mark.parametrize("pairs", [(1,), (1, 1), (1, 0, 1), (0, 1, 1, 0), (1, 1, 1, 1), (1, 0, 0, 1, 1)], ids=str)
+def test_groups_read_one_anothers_output_of_their_item(pairs):
+    assert "ok = (!met || wait(&sh.meet, 1u, kAttnSoftmaxTimeout)) &&" in SOURCE
+    assert "ok = wait(&sh.meet, 0u, kAttnSoftmaxTimeout);" in SOURCE
+    assert SOURCE.count("mbar_arrive(smem_u32(&sh.meet))") == 2
+    assert _meet(pairs, True) == (False, False)
+    if len(pairs) > 1 and pairs[0]:
+        assert _meet(pairs, False)[0]
+
+
+def test_groups_that_meet_leave_an_item_together():
+    """Behind the wait for the other group, whose end each warp sees for itself, the group's warps agree."""
+    for wait in ("ok = wait(&sh.meet, 0u, kAttnSoftmaxTimeout);",
+                 "wait(&sh.q_empty[g], (items & 1u) ^ 1u, kAttnSoftmaxTimeout);"):
+        after = SOURCE[SOURCE.index(wait) + len(wait):]
+        assert after.lstrip().startswith("ok = barrier_all(bar_id, 128, ok);")

@@ -47,7 +47,7 @@ TreePlan plan(const tree_attention_args_t& a, int sms) {
   const long long most = static_cast<long long>(f.many ? 1 : tree_few_ctas(f.tile_rows)) * sms;
   // (More items than CTAs by far: their steps are as many at least.)
   f.grid = static_cast<int>(items >= most ? most : std::min(most, items * std::max(1ll, key_tiles)));
-  if (key_tiles > 1 || f.many)
+  if (key_tiles > 1)
     f.part_bytes = static_cast<size_t>(2) * f.grid * f.tile_rows * (128 + 2) * sizeof(float);
   return f;
 }

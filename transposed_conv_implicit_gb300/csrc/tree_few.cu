@@ -520,10 +520,11 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
   const int hk = row_tiles > 0 ? at / row_tiles : 0, row0 = (at - hk * row_tiles) * p.tile_rows;
   const int rows = min(p.tile_rows, size.drafts * p.group - row0);
   const int r0 = static_cast<int>(blockIdx.y * kTreeJoinWarps) * kPer;
-  // Of an item of up to half a tile, many rows' CTAs leave two shares (their groups').
+  // Of an item of up to half a tile, many rows' CTAs leave two shares (their groups') where they
+  // have a part of it.
   const int halves = p.many && rows <= p.tile_rows / 2 ? 2 : 1;
   int shares = 0;
-  if (at < p.kv_heads * row_tiles && r0 < rows && (nt > 1 || halves > 1)) {
+  if (at < p.kv_heads * row_tiles && r0 < rows && nt > 1) {
     long long before, total;
     split_prefix(p.batch, -1, b, sums, [&](int i) { return tree_steps(p, i); }, &before, &total);
     if (threadIdx.x < 2) {
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(kTreeJoinThreads)
     }
     __syncthreads();
     const int c0 = range[0];
-    shares = (range[1] - c0 + 1) * halves;
+    shares = range[1] == c0 ? 1 : (range[1] - c0 + 1) * halves;
     for (int i = threadIdx.x; i < shares; i += kTreeJoinThreads) {
       const int c = c0 + (halves == 2 ? i >> 1 : i);
       // (With fewer steps than CTAs some CTAs' shares are empty.)

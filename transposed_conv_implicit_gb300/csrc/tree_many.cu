@@ -21,9 +21,13 @@
 // widened tiles:
 //  - an item of more than 128 rows: the groups are two row tiles;
 //  - an item of up to 128 rows: both groups hold the same rows, and take the
-//    key tiles in turn; each leaves a share of its own for the join.
+//    key tiles in turn.  A row is the same lane of tensor memory in both, so
+//    where the CTA has all of the item each group reads the other's output
+//    there and writes half of the columns; else each leaves a share of its own
+//    for the join.
 // The sequence of all items' key tiles is cut evenly between the CTAs (one per
-// SM), as for few rows.
+// SM), as for few rows.  A CTA leaves at most two items' shares: of one that
+// began in front of its part, and of one that ends behind it.
 //
 // Bound by issue slots (58 %: exponentials and widening) beside the products (46
 // % of their pipe): 64 drafts of 16 requests x 32/8 heads x 128 against 8192 keys
@@ -79,6 +83,7 @@ struct ManyShared {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [group][half of a tile]
   uint64_t drain[2];
+  uint64_t meet;  // the groups, over an item whose rows both hold: statistics are there, outputs have been read
   SplitStart start;
   uint32_t tmem;
   int abort_flag;
@@ -86,6 +91,7 @@ struct ManyShared {
   alignas(16) float scale[kSlotsMany][3][kWidenWarps];  // of a slice: 2^E, F, 2^-F (see above)
   int parents[2][kMaxDrafts];
   uint32_t bits[2][kTreeWords][kRowsMany];  // drafts that a row attends
+  float2 stat[2][kRowsMany];                // a group's maximum and sum, for the other group
 };
 
 // 2^-below as fp16, twice; 0 below 2^-24.
@@ -112,6 +118,7 @@ __device__ __forceinline__ void widen16(uint4 codes, uint32_t factor, uint4& fir
 
 template <int DP>
 constexpr size_t many_smem() {
+  static_assert(Many<DP>::kOffShared + sizeof(ManyShared) <= 227 * 1024, "a block's shared memory");
   return Many<DP>::kOffShared + sizeof(ManyShared);
 }
 
@@ -141,6 +148,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       }
       mbar_init(smem_u32(&sh.drain[g]), 1);
     }
+    mbar_init(smem_u32(&sh.meet), 8);
     sh.abort_flag = 0;
     fence_barrier_init();
   }
@@ -430,22 +438,26 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
     const int g = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t ts = tmem + g * 128 + lane_field, to = tmem + 256 + g * DP + lane_field;
+    const uint32_t to_other = tmem + 256 + (g ^ 1) * DP + lane_field;
     const uint32_t bar_id = 1 + g;
     const int d = p.c.head_dim;
     uint32_t tiles = 0, items = 0, seen = 0;  // own tiles: barrier parity; all tiles: validity's slot
-    bool ok = true;
+    bool ok = true, met = false;  // met: the other group may still be reading this one's last output
     for (TreeWalk w(p, start); ok && w.live; w.next()) {
       const int left = w.size.drafts * p.group - w.row_tile * p.tile_rows;
       const bool single = left <= kRowsMany;
+      const bool whole = w.whole(), pair = single && whole;
       const int row = w.row_tile * p.tile_rows + (single ? r : g * kRowsMany + r);
       const bool row_ok = row < w.size.drafts * p.group;
       const bool warp_ok = __any_sync(0xFFFFFFFFu, row_ok);
       const int draft = row_ok ? fast_div(row, p.div_group) : 0;
       const int head = w.hk * p.group + (row_ok ? row - draft * p.group : 0);
       const int prefix = w.size.keys - w.size.drafts;
-      ok = wait(&sh.q_empty[g], (items & 1u) ^ 1u, kAttnSoftmaxTimeout);
+      ok = (!met || wait(&sh.meet, 1u, kAttnSoftmaxTimeout)) &&
+           wait(&sh.q_empty[g], (items & 1u) ^ 1u, kAttnSoftmaxTimeout);
       ok = barrier_all(bar_id, 128, ok);
       if (!ok) break;
+      met = pair;
       ++items;
       float rf = 0.f;  // of the row's scores: scale, and the query's power of two
       {
@@ -633,7 +645,32 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       ok = barrier_all(bar_id, 128, ok);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = !single && w.whole();
+      // Both groups' parts of a row: their weights, as the join has them.  (A part without keys is
+      // left out, whatever its output holds; one whose maximum is -infinity all the same holds NaN of
+      // the row's own.)
+      float weight = 1.f, weight_other = 0.f;
+      bool on = true, on_other = false;
+      if (pair) {
+        sh.stat[g][r] = make_float2(mc, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.meet));
+        ok = wait(&sh.meet, 0u, kAttnSoftmaxTimeout);
+        ok = barrier_all(bar_id, 128, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float2 a = sh.stat[0][r], b = sh.stat[1][r];
+        const float top = fmaxf(a.x, b.x);
+        const bool on_a = a.x != -INFINITY || a.y != 0.f, on_b = b.x != -INFINITY || b.y != 0.f;
+        const float fa = a.x == -INFINITY ? 0.f : exp2_approx(a.x - top);
+        const float fb = b.x == -INFINITY ? 0.f : exp2_approx(b.x - top);
+        mc = top;
+        l = fmaf(fb, b.y, fa * a.y);
+        weight = g ? fb : fa;
+        weight_other = g ? fa : fb;
+        on = g ? on_b : on_a;
+        on_other = g ? on_a : on_b;
+      }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       // A share: unnormalised, with its maximum and sum.  (Both groups' shares of one row tile
       // lie behind one another; one without a tile leaves no rows.)
@@ -646,10 +683,23 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
         if (whole) {
           constexpr int kChunks = DP / 8, kAtOnce = 32 / kChunks;  // 16-byte words of a row
 #pragma unroll 1
-          for (int c = 0; c < d; c += 32) {
+          for (int c = pair ? 32 * g : 0; c < d; c += pair ? 64 : 32) {
             uint32_t o[32];
             tmem_ld_x32(to + c, o);
             tmem_wait_ld_x32(o);
+            if (pair) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 16) {
+                uint32_t v[16];
+                tmem_ld_x16(to_other + c + j, v);
+                tmem_wait_ld_x16(v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float mine = on ? weight * __uint_as_float(o[j + i]) : 0.f;
+                  o[j + i] = __float_as_uint(on_other ? fmaf(weight_other, __uint_as_float(v[i]), mine) : mine);
+                }
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t h[4];
@@ -665,7 +715,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
 #pragma unroll 4
           for (int i = 0; i < 32; i += kAtOnce) {
             const int at = i + lane / kChunks, at_row = row_first + at;
-            if (at_row < w.size.drafts * p.group && col * 8 < d) {
+            if (at_row < w.size.drafts * p.group && col * 8 < d && (!pair || ((col >> 2) & 1) == g)) {
               const int at_draft = fast_div(at_row, p.div_group);
               const int at_head = w.hk * p.group + at_row - at_draft * p.group;
               *reinterpret_cast<uint4*>(p.out + w.b * p.os[0] + at_draft * p.os[1] + at_head * p.os[2] + col * 8) =
@@ -700,11 +750,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1)
       if (row_ok) {
         if (!whole)
           *reinterpret_cast<float2*>(p.part_stat + at * 2) = make_float2(mc, l);
-        else if (p.lse)
+        else if (p.lse && (!pair || g == 0))
           p.lse[(static_cast<long long>(w.b) * p.heads + head) * p.q_len + draft] =
               l == 0.f ? -INFINITY : fmaf(mc, kLn2, logf(l));
       }
       tc_fence_before();
+      if (pair) {  // (before the next item this group waits for the other's arrival here)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.meet));
+      }
     }
   } else {
     give_registers<64>();

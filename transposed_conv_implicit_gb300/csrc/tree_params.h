@@ -34,11 +34,13 @@ struct TreeParams {
   long long scale_page;    // bytes of a page's scales
   // Rows whose keys are shared out: [2 * CTAs][tile_rows][128] unnormalised,
   // and their maximum (log2 units) and sum.  A share that begins in the middle
-  // of an item leaves its rows in slot 2 c, one that begins with it in 2 c + 1.
+  // of an item leaves its rows in slot 2 c, one that begins with it in 2 c + 1:
+  // there is one of either at most, since items that a CTA has whole are
+  // written by it.
   float* part_out;
   float* part_stat;
   int max_tiles;           // most row tiles of a key head
-  bool many;               // tree_many.cu: two shares of items of up to half a tile
+  bool many;               // tree_many.cu: two shares, behind one another, of items of up to half a tile
   unsigned int* status;
   long long timeout_cycles;
   int fault_mode;          // test hook: 1 = every CTA with work leaves its first keys un-announced
