@@ -318,6 +318,9 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
       const bool drafts = (slice + 1) * kSlice > prefix;
       if (drafts || __any_sync(0xFFFFFFFFu, there != 15u)) {
 #pragma unroll
+        for (int j = 0; j < 4; ++j)  // (a value's byte of 255 would make the probability of 0 NaN)
+          if (!((there >> j) & 1u)) value_back[j] = 0.f;
+#pragma unroll
         for (int m = 0; m < kGroups; ++m)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
