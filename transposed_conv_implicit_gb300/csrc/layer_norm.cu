@@ -4,6 +4,14 @@
 //   dx = r (g - mean g - h mean(g h)),  g = dy w,  h = (x - m) r
 //   dw = sum_rows dy h,  db = sum_rows dy
 //
+// Deviations are taken from c, the first sum's mean rounded to the rows' type:
+//   m = c + d,  d = mean (x - c),  mean (x - m)^2 = mean (x - c)^2 - d^2
+// A row of one value has c equal to it, so its deviations are 0 whatever the sum's
+// rounding (from the mean in fp32 they were the last bit of it, times r: y = 0.8
+// for 60000 in 1000 channels).  The difference loses a bit at most: elements lie on
+// the type's grid, so where d is some half of its step the deviations are that large
+// too.
+//
 // Bound by memory: x in, y out; x and dy in, dx out.  Measured: 65536 x 320
 // forward 17.8 us (4.7 TB/s), backward 24 us (5.2); 16381 x 4096 forward 48 us
 // (5.6 TB/s), backward 80 us (5.0); the weights' sums another 4; with 321 and 4099
@@ -187,7 +195,7 @@ __device__ __forceinline__ float both_of(uint64_t v) {
 // whole block's; `turn` alternates between two sets of slots, so that one
 // barrier a sum does.
 template <bool kBlock, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float (*slots)[N][32], int& turn) {
+__device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float (*slots)[2][32], int& turn) {
   for (int step = kBlock ? 16 : lanes >> 1; step > 0; step >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], step);
@@ -350,7 +358,7 @@ template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kFull,
 __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBlock ? 1 : 3)
     layer_norm_fwd_kernel(const __grid_constant__ LnParams p) {
   constexpr bool kRing = kVec == 8;
-  __shared__ float slots[2][1][32];
+  __shared__ float slots[2][2][32];
   // [kLnStages][kWords][threads] words; kShift: then weight and bias in fp32, each
   // word's first half [words] and its second half [words] (from memory in every row:
   // 65536 x 321 in 41 us, so 33).
@@ -444,11 +452,12 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) total = add2(total, f[i].v[j]);
     }
-    float sum[1] = {both_of(total)};
-    row_sum<kBlock, 1>(sum, lanes, slots, turn);
-    const float mean = sum[0] * p.inv_c;
-    const uint64_t minus = pack2(-mean, kVec == 8 ? -mean : 0.f);
+    float first[1] = {both_of(total)};
+    row_sum<kBlock, 1>(first, lanes, slots, turn);
+    const float near = to_float(from_float<T>(first[0] * p.inv_c));
+    const uint64_t minus = pack2(-near, kVec == 8 ? -near : 0.f);
     total = 0;
+    uint64_t squares = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const int w = at + i * lanes;
@@ -465,19 +474,23 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
             }
           }
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) total = fma2(f[i].v[j], f[i].v[j], total);
+        for (int j = 0; j < kPairs; ++j) {
+          total = add2(total, f[i].v[j]);
+          squares = fma2(f[i].v[j], f[i].v[j], squares);
+        }
       }
     }
-    sum[0] = both_of(total);
-    row_sum<kBlock, 1>(sum, lanes, slots, turn);
-    const float rstd = inverse_root(fmaf(sum[0], p.inv_c, p.eps));
+    float sum[2] = {both_of(total), both_of(squares)};
+    row_sum<kBlock, 2>(sum, lanes, slots, turn);
+    const float off = sum[0] * p.inv_c, var = fmaf(-off, off, sum[1] * p.inv_c);
+    const float rstd = inverse_root((var < 0.f ? 0.f : var) + p.eps);
     if (!kShift && !live) continue;
     if (live && at == 0) {
-      if (p.mean) p.mean[row] = mean;
+      if (p.mean) p.mean[row] = near + off;
       if (p.rstd) p.rstd[row] = rstd;
     }
     uint16_t* y = static_cast<uint16_t*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
-    const uint64_t rr = pack2(rstd, rstd);
+    const uint64_t rr = pack2(rstd, rstd), shift = pack2(-off * rstd, -off * rstd);
     if constexpr (kShift && !kBlock) __syncwarp();  // (all lanes have read the row; a block's, before its sums)
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
@@ -493,7 +506,7 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
         bs = load_weight<W, kVec>(p.bias, w * kVec, 0.f);
       }
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) f[i].v[j] = fma2(mul2(f[i].v[j], rr), wt.v[j], bs.v[j]);
+      for (int j = 0; j < kPairs; ++j) f[i].v[j] = fma2(fma2(f[i].v[j], rr, shift), wt.v[j], bs.v[j]);
       if constexpr (kShift) ring_put(held + i * pitch, joined8<T>(f[i]));
       else store_word<T, kVec>(y + w * kVec, f[i]);
     }
@@ -627,8 +640,8 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
       }
     }
     const float mean = stat[0], rstd = stat[1];
-    // h = x rstd - mean rstd
-    const uint64_t rr = pack2(rstd, rstd), shift = pack2(-mean * rstd, -mean * rstd);
+    // (The mean goes off first: of x rstd - mean rstd little is left where a row is nearly of one value.)
+    const uint64_t rr = pack2(rstd, rstd), minus = pack2(-mean, kVec == 8 ? -mean : 0.f);
     uint64_t sum_g = 0, sum_gh = 0;
     Pairs<kVec> hs[kKeepRow ? kWords : 1], fs[kKeepRow ? kWords : 1];  // h, and dy w
 #pragma unroll
@@ -641,7 +654,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
       else wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        const uint64_t h = fma2(x.v[j], rr, shift), f = mul2(g.v[j], wt.v[j]);
+        const uint64_t h = mul2(add2(x.v[j], minus), rr), f = mul2(g.v[j], wt.v[j]);
         // (Rows left out hold zeros of dy; so does a single element's other half.)
         dw[i * kPairs + j] = fma2(g.v[j], h, dw[i * kPairs + j]);
         db[i * kPairs + j] = add2(db[i * kPairs + j], g.v[j]);
@@ -675,7 +688,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
         else wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j)
-          o.v[j] = fma2(mul2(g.v[j], wt.v[j]), rr, fma2(fma2(x.v[j], rr, shift), cc1, cc0));
+          o.v[j] = fma2(mul2(g.v[j], wt.v[j]), rr, fma2(mul2(add2(x.v[j], minus), rr), cc1, cc0));
       }
       if constexpr (kShift) ring_put(held + i * pitch, joined8<T>(o));
       else store_word<T, kVec>(dx + w * kVec, o);
