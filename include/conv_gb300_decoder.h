@@ -31,7 +31,9 @@ extern "C" {
  *   dx = rstd * (g - sum g / C - xhat * sum(g xhat) / C)
  *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
  * Sums are fp32, the forward pass's deviations are taken from the row's own
- * mean, and every sum runs in a fixed order: equal calls give equal bits.
+ * mean, and every sum runs in a fixed order: equal calls give equal bits.  A
+ * finite row's squares and sum may pass fp32's range.  With eps = 0 a row of one
+ * value has rstd = infinity (and y, as in the formula, is not a number).
  *
  * x, y, dy, dx: [batch][length][C] of `dtype` (BF16 or F16), strides {batch,
  * token} in elements (ignored for extents of 1; inputs may repeat a row with

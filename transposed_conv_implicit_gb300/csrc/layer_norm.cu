@@ -214,10 +214,11 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int lanes, float (*slots)
   }
 }
 
-// 1/sqrt(x): the hardware's approximation and one Newton step.
+// 1/sqrt(x): the hardware's approximation and one Newton step (which would make
+// NaN of the infinity that belongs to 0).
 __device__ __forceinline__ float inverse_root(float x) {
   const float r = rsqrtf(x);
-  return r * fmaf(-0.5f * x * r, r, 1.5f);
+  return r < INFINITY ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;
 }
 
 __device__ __forceinline__ long long row_at(const LnParams& p, int row, const long long s[2]) {
@@ -353,6 +354,42 @@ __device__ __forceinline__ void store_shifted(uint16_t* row, uint32_t held, uint
   }
 }
 
+// A row whose squares, or whose sum, pass fp32's range, as bfloat16's from some 2^60
+// on do: from the elements times 2^-80, whose squares stay below 2^96, element by
+// element from memory (such rows are few, and nothing is held for them).  All lanes
+// of a warp, or a block, come here; rows of `past` are written.
+template <typename T, bool kBlock>
+__device__ __noinline__ void layer_norm_far_row(const LnParams& p, int row, bool live, bool past, int at, int lanes,
+                                                float (*slots)[2][32], int turn) {
+  constexpr float kDown = 0x1p-80f, kUp = 0x1p80f;
+  const T* x = static_cast<const T*>(p.x) + (live ? row_at(p, row, p.xs) : 0);
+  T* y = static_cast<T*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
+  const int end = live ? p.channels : 0;
+  float first[1] = {0.f}, sum[2] = {0.f, 0.f};
+  for (int e = at; e < end; e += lanes) first[0] += to_float(x[e]) * kDown;
+  row_sum<kBlock, 1>(first, lanes, slots, turn);
+  const float near = to_float(from_float<T>(first[0] * p.inv_c));
+  for (int e = at; e < end; e += lanes) {
+    const float d = to_float(x[e]) * kDown - near;
+    sum[0] += d;
+    sum[1] = fmaf(d, d, sum[1]);
+  }
+  row_sum<kBlock, 2>(sum, lanes, slots, turn);
+  if (!past || !live) return;
+  const float off = sum[0] * p.inv_c, difference = fmaf(-off, off, sum[1] * p.inv_c);
+  const float var = difference < 0.f ? 0.f : difference, var_up = var * kUp * kUp;
+  // (eps is nothing beside a variance that passes fp32, and all of it in a row of one value.)
+  const float scale = var_up < INFINITY ? inverse_root(var_up + p.eps) * kUp : inverse_root(var);
+  if (at == 0) {
+    if (p.mean) p.mean[row] = (near + off) * kUp;
+    if (p.rstd) p.rstd[row] = scale * kDown;
+  }
+  for (int e = at; e < end; e += lanes) {
+    const float h = fmaf(to_float(x[e]) * kDown - near, scale, -off * scale);
+    y[e] = from_float<T>(fmaf(h, weight_at<T>(p, p.weight, e, 1.f), weight_at<T>(p, p.bias, e, 0.f)));
+  }
+}
+
 // kFull: a row's words are as many as its lanes take (320 channels on 8 lanes of 5).
 template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kFull, bool kShift>
 __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBlock ? 1 : 3)
@@ -482,38 +519,44 @@ __global__ void __launch_bounds__(kBlock ? (kVec == 8 ? 512 : 1024) : 256, kBloc
     }
     float sum[2] = {both_of(total), both_of(squares)};
     row_sum<kBlock, 2>(sum, lanes, slots, turn);
+    const bool far = !std::is_same<T, __half>::value && !(sum[1] < INFINITY);  // (fp16's stay within fp32)
     const float off = sum[0] * p.inv_c, var = fmaf(-off, off, sum[1] * p.inv_c);
     const float rstd = inverse_root((var < 0.f ? 0.f : var) + p.eps);
-    if (!kShift && !live) continue;
-    if (live && at == 0) {
-      if (p.mean) p.mean[row] = near + off;
-      if (p.rstd) p.rstd[row] = rstd;
-    }
-    uint16_t* y = static_cast<uint16_t*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
-    const uint64_t rr = pack2(rstd, rstd), shift = pack2(-off * rstd, -off * rstd);
-    if constexpr (kShift && !kBlock) __syncwarp();  // (all lanes have read the row; a block's, before its sums)
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const int w = at + i * lanes;
-      if (!kFull && w >= words) break;
-      Pairs<kVec> wt, bs;
-      if constexpr (kShift) {
-        const float4 a = affine[w], b = affine[words + w], c = affine[2 * words + w], d = affine[3 * words + w];
-        wt.v[0] = pack2(a.x, a.y), wt.v[1] = pack2(a.z, a.w), wt.v[2] = pack2(b.x, b.y), wt.v[3] = pack2(b.z, b.w);
-        bs.v[0] = pack2(c.x, c.y), bs.v[1] = pack2(c.z, c.w), bs.v[2] = pack2(d.x, d.y), bs.v[3] = pack2(d.z, d.w);
-      } else {
-        wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
-        bs = load_weight<W, kVec>(p.bias, w * kVec, 0.f);
+    const bool here = live && !far;  // written here
+    if (kShift || here) {
+      if (here && at == 0) {
+        if (p.mean) p.mean[row] = near + off;
+        if (p.rstd) p.rstd[row] = rstd;
       }
+      uint16_t* y = static_cast<uint16_t*>(p.y) + (live ? row_at(p, row, p.ys) : 0);
+      const uint64_t rr = pack2(rstd, rstd), shift = pack2(-off * rstd, -off * rstd);
+      if constexpr (kShift && !kBlock) __syncwarp();  // (all lanes have read the row; a block's, before its sums)
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) f[i].v[j] = fma2(fma2(f[i].v[j], rr, shift), wt.v[j], bs.v[j]);
-      if constexpr (kShift) ring_put(held + i * pitch, joined8<T>(f[i]));
-      else store_word<T, kVec>(y + w * kVec, f[i]);
+      for (int i = 0; i < kWords; ++i) {
+        const int w = at + i * lanes;
+        if (!kFull && w >= words) break;
+        Pairs<kVec> wt, bs;
+        if constexpr (kShift) {
+          const float4 a = affine[w], b = affine[words + w], c = affine[2 * words + w], d = affine[3 * words + w];
+          wt.v[0] = pack2(a.x, a.y), wt.v[1] = pack2(a.z, a.w), wt.v[2] = pack2(b.x, b.y), wt.v[3] = pack2(b.z, b.w);
+          bs.v[0] = pack2(c.x, c.y), bs.v[1] = pack2(c.z, c.w), bs.v[2] = pack2(d.x, d.y), bs.v[3] = pack2(d.z, d.w);
+        } else {
+          wt = load_weight<W, kVec>(p.weight, w * kVec, 1.f);
+          bs = load_weight<W, kVec>(p.bias, w * kVec, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) f[i].v[j] = fma2(fma2(f[i].v[j], rr, shift), wt.v[j], bs.v[j]);
+        if constexpr (kShift) ring_put(held + i * pitch, joined8<T>(f[i]));
+        else store_word<T, kVec>(y + w * kVec, f[i]);
+      }
+      if constexpr (kShift) {
+        row_sync<kBlock>();
+        store_shifted<kWords>(y, held, pitch, before, at, lanes, here ? p.channels : 0);
+      }
     }
-    if constexpr (kShift) {
-      row_sync<kBlock>();
-      store_shifted<kWords>(y, held, pitch, before, at, lanes, live ? p.channels : 0);
-    }
+    if constexpr (!std::is_same<T, __half>::value)
+      if (kBlock ? far : __any_sync(0xFFFFFFFFu, far))
+        layer_norm_far_row<T, kBlock>(p, row, live, far, at, lanes, slots, turn);
   }
 }
 
@@ -639,7 +682,7 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
         rd[i] = on ? load_word<kVec>(dy + w * kVec) : no_word<kVec>();
       }
     }
-    const float mean = stat[0], rstd = stat[1];
+    const float mean = live ? stat[0] : 0.f, rstd = live ? stat[1] : 0.f;
     // (The mean goes off first: of x rstd - mean rstd little is left where a row is nearly of one value.)
     const uint64_t rr = pack2(rstd, rstd), minus = pack2(-mean, kVec == 8 ? -mean : 0.f);
     uint64_t sum_g = 0, sum_gh = 0;
@@ -667,6 +710,21 @@ __global__ void __launch_bounds__(!kBlock ? 128 : kVec == 1 ? 1024 : kWide ? 512
       }
     }
     float sum[2] = {both_of(sum_g), both_of(sum_gh)};
+    if (kShift && !(fabsf(mean * rstd) < INFINITY)) {  // the zeros behind a row, less its mean, are no numbers
+      sum[1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const Pairs<kVec> x = widen<T, kVec>(rx[i]), g = widen<T, kVec>(rd[i]);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const int e = 8 * (at + i * lanes) + 2 * j;
+          float a, b, c, d;
+          unpack2(mul2(add2(x.v[j], minus), rr), a, b);
+          unpack2(mul2(g.v[j], weight[i].v[j]), c, d);
+          sum[1] += (e < p.channels ? a * c : 0.f) + (e + 1 < p.channels ? b * d : 0.f);
+        }
+      }
+    }
     row_sum<kBlock, 2>(sum, lanes, slots, turn);
     if (!kShift && !live) continue;
     const float c0 = -rstd * (sum[0] * p.inv_c), c1 = -rstd * (sum[1] * p.inv_c);
