@@ -876,24 +876,6 @@ LnShape ln_shape(int channels, bool vectors, bool shift, bool backward) {
   return s;
 }
 
-// Blocks of a kernel that an SM runs at once, asked for once for each device and
-// number of warps (the shared memory goes by that).
-template <typename Kernel>
-cudaError_t blocks_per_sm(Kernel kernel, std::atomic<int> (*known)[33], int threads, size_t smem, int* fit) {
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  const int at = threads / 32;
-  *fit = known[dev][at].load(std::memory_order_relaxed);
-  if (*fit > 0) return cudaSuccess;
-  err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, kernel, threads, smem);
-  if (err != cudaSuccess) return err;
-  *fit = std::max(1, *fit);
-  known[dev][at].store(*fit, std::memory_order_relaxed);
-  return cudaSuccess;
-}
-
 int ln_groups(const LnShape& s) { return s.block ? 1 : s.threads / s.lanes; }
 
 template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull, bool kShift>
@@ -906,7 +888,7 @@ cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms,
   if (err != cudaSuccess) return err;
   // As many blocks as run at once: each keeps its columns' sums over all of its rows.
   int fit = 0;
-  static std::atomic<int> known[kMaxDevices][33];
+  static BlocksPerSm known[kMaxDevices][kWarpCounts];
   err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
   if (err != cudaSuccess) return err;
   p.blocks = static_cast<int>(
@@ -928,7 +910,7 @@ cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cuda
     cudaError_t err = raise_smem(kernel, configured, smem);
     if (err != cudaSuccess) return err;
     int fit = 0;
-    static std::atomic<int> known[kMaxDevices][33];
+    static BlocksPerSm known[kMaxDevices][kWarpCounts];
     err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
     if (err != cudaSuccess) return err;
     const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(fit) * sms));
