@@ -71,7 +71,8 @@ typedef struct {
 
 conv_status_t layer_norm_fwd(const layer_norm_args_t* args, void* stream);
 
-/* Workspace bytes of the backward pass on the current device. */
+/* Workspace bytes of the backward pass on the current device (with neither
+ * dweight nor dbias the status region's CONV_STATUS_BYTES do). */
 size_t layer_norm_workspace_size(int channels);
 
 conv_status_t layer_norm_bwd(const layer_norm_args_t* args, void* workspace,

@@ -1003,7 +1003,8 @@ conv_status_t ln_run(const layer_norm_args_t* args, bool backward, void* workspa
   if (backward) {
     if (!workspace) return CONV_ERR_INVALID_VALUE;
     if (off(workspace, 16)) return CONV_ERR_MISALIGNED;
-    const size_t need = layer_norm_workspace_size(a.channels);
+    // (Partial sums are of dweight and dbias alone.)
+    const size_t need = sums ? layer_norm_workspace_size(a.channels) : CONV_STATUS_BYTES;
     if (need == 0) return CONV_ERR_CUDA;
     if (workspace_bytes < need) return CONV_ERR_WORKSPACE_TOO_SMALL;
   }

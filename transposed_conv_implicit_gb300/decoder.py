@@ -17,7 +17,7 @@ import struct
 
 from . import _lib
 from . import attention as _a
-from ._lib import CONV_ERR_NOT_SUPPORTED, CONV_OK
+from ._lib import CONV_ERR_NOT_SUPPORTED, CONV_OK, CONV_STATUS_BYTES
 from .attention import _common, _dense, _error, _invalid, _pack, _stream, _strides, _workspace
 
 __all__ = ["layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_size", "kv_cache_write",
@@ -164,7 +164,7 @@ def layer_norm_fwd(x, weight, bias, y, *, mean=None, rstd=None, eps=1e-5, stream
 
 
 def layer_norm_workspace_size(channels) -> int:
-    """Workspace bytes of layer_norm_bwd."""
+    """Workspace bytes of layer_norm_bwd (CONV_STATUS_BYTES do where neither dweight nor dbias is wanted)."""
     size = _lib.lib().layer_norm_workspace_size(int(channels))
     if size == 0:
         raise _error(CONV_ERR_NOT_SUPPORTED, "layer_norm_workspace_size")
@@ -191,7 +191,8 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, *, workspace=N
     lib = _lib.lib()
     if workspace is None:
         from . import new_workspace
-        workspace = new_workspace(_sized(lib.layer_norm_workspace_size, device, c), x.device, stream)
+        size = _sized(lib.layer_norm_workspace_size, device, c) if dw or db else CONV_STATUS_BYTES
+        workspace = new_workspace(size, x.device, stream)
     _call(lib.layer_norm_bwd, "layer_norm_bwd", device, args, *_workspace(workspace, device),
           _stream(stream, device))
     return dx, dweight, dbias
