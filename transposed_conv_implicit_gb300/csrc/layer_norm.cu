@@ -899,23 +899,27 @@ cudaError_t ln_launch_bwd(LnParams p, const LnShape& s, long long need, int sms,
                     stream, p);
 }
 
+// (A launcher's parameters are its kernel's, as what it remembers is of one kernel.)
+template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kFull, bool kShift>
+cudaError_t ln_launch_fwd(const LnParams& p, const LnShape& s, long long need, int sms, cudaStream_t stream) {
+  const auto kernel = layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock, kFull, kShift>;
+  size_t smem = kVec == 8 ? static_cast<size_t>(kLnStages) * kWords * s.threads * 16 : 0;
+  if (kShift) smem += static_cast<size_t>(s.words) * 16 * sizeof(float);
+  static std::atomic<size_t> configured[kMaxDevices];
+  cudaError_t err = raise_smem(kernel, configured, smem);
+  if (err != cudaSuccess) return err;
+  int fit = 0;
+  static BlocksPerSm known[kMaxDevices][kWarpCounts];
+  err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
+  if (err != cudaSuccess) return err;
+  const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(fit) * sms));
+  return launch_pdl(kernel, dim3(grid), dim3(s.threads), smem, stream, p);
+}
+
 template <typename T, typename W, int kVec, int kWords, bool kBlock, bool kWide, bool kFull, bool kShift>
-cudaError_t ln_launch(LnParams p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
+cudaError_t ln_launch(const LnParams& p, const LnShape& s, bool backward, int sms, cudaStream_t stream) {
   const long long need = (static_cast<long long>(p.rows) + ln_groups(s) - 1) / ln_groups(s);
-  if (!backward) {
-    const auto kernel = layer_norm_fwd_kernel<T, W, kVec, kWords, kBlock, kFull, kShift>;
-    size_t smem = kVec == 8 ? static_cast<size_t>(kLnStages) * kWords * s.threads * 16 : 0;
-    if (kShift) smem += static_cast<size_t>(s.words) * 16 * sizeof(float);
-    static std::atomic<size_t> configured[kMaxDevices];
-    cudaError_t err = raise_smem(kernel, configured, smem);
-    if (err != cudaSuccess) return err;
-    int fit = 0;
-    static BlocksPerSm known[kMaxDevices][kWarpCounts];
-    err = blocks_per_sm(kernel, known, s.threads, smem, &fit);
-    if (err != cudaSuccess) return err;
-    const int grid = static_cast<int>(std::min<long long>(need, static_cast<long long>(fit) * sms));
-    return launch_pdl(kernel, dim3(grid), dim3(s.threads), smem, stream, p);
-  }
+  if (!backward) return ln_launch_fwd<T, W, kVec, kWords, kBlock, kFull, kShift>(p, s, need, sms, stream);
   // (Five words a lane are for the forward pass alone: see ln_shape.)
   if constexpr (kVec == 8 && kWords == 5) return cudaErrorInvalidValue;
   else return ln_launch_bwd<T, W, kVec, kWords, kBlock, kWide, kFull, kShift>(p, s, need, sms, stream);
