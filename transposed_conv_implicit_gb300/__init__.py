@@ -86,17 +86,23 @@ def _need_dense(*ts):
             raise ConvError(CONV_ERR_INVALID_VALUE, "tensors must be dense (contiguous)")
 
 
-def new_workspace(nbytes: int, device, stream=None):
+def new_workspace(nbytes: int, device, stream=None, *, status_only: bool = False):
     """A zeroed uint8 device buffer (the status region must start at zero), cleared on `stream`
-    (default: the current one) and, once dropped, free for what follows there."""
+    (default: the current one) and, once dropped, free for what follows there.  status_only: only the
+    status region is cleared, which is all that the decoder's operators need."""
     import torch
     if stream is None:
-        return torch.zeros(max(int(nbytes), CONV_STATUS_BYTES), dtype=torch.uint8, device=device)
+        size = max(int(nbytes), CONV_STATUS_BYTES)
+        if not status_only:
+            return torch.zeros(size, dtype=torch.uint8, device=device)
+        out = torch.empty(size, dtype=torch.uint8, device=device)
+        out[:CONV_STATUS_BYTES].zero_()
+        return out
     if not hasattr(stream, "cuda_stream"):
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
                   else torch.cuda.default_stream(device))
     with torch.cuda.stream(stream):
-        return new_workspace(nbytes, device)
+        return new_workspace(nbytes, device, status_only=status_only)
 
 
 def conv2d_packed_filter_bytes(r, s, c_in, c_out, dtype: str) -> int:

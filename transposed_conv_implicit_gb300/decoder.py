@@ -192,7 +192,7 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight, dbias, *, workspace=N
     if workspace is None:
         from . import new_workspace
         size = _sized(lib.layer_norm_workspace_size, device, c) if dw or db else CONV_STATUS_BYTES
-        workspace = new_workspace(size, x.device, stream)
+        workspace = new_workspace(size, x.device, stream, status_only=True)
     _call(lib.layer_norm_bwd, "layer_norm_bwd", device, args, *_workspace(workspace, device),
           _stream(stream, device))
     return dx, dweight, dbias
@@ -320,7 +320,8 @@ def tree_attention_fwd(q, k_cache, v_cache, scales, block_table, kv_lengths, out
     lib = _lib.lib()
     if workspace is None:
         from . import new_workspace
-        workspace = new_workspace(_sized(lib.tree_attention_workspace_size, device, args), q.device, stream)
+        workspace = new_workspace(_sized(lib.tree_attention_workspace_size, device, args), q.device, stream,
+                                  status_only=True)
     _call(lib.tree_attention_fwd, "tree_attention_fwd", device, args, *_workspace(workspace, device),
           _stream(stream, device))
     return output
