@@ -86,8 +86,9 @@ conv_status_t layer_norm_bwd(const layer_norm_args_t* args, void* workspace,
  * tokens.  scales: dense bytes [pages][kv_heads][page_size][2], for each row
  * the exponents, plus 127, of its key (first) and of its value:
  *   row = code * 2^(byte - 127)
- * A key's byte of 0 says that nothing was written there: attention leaves
- * such a token out (a cache whose scales start at zero is empty).
+ * A key's byte of 0 says that nothing was written there, whatever the value's
+ * byte is: attention leaves such a token out (a cache whose scales start at zero
+ * is empty).  Other bytes lie in [63, 247], as kv_cache_write gives them.
  * block_table: int32 [batch][table_width] with rows table_stride apart: token
  * p of request b is token p % page_size of page block_table[b][p / page_size].
  * Page numbers outside [0, pages) stand for no page: nothing is written

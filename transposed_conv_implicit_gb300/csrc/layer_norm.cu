@@ -13,9 +13,10 @@
 // too.
 //
 // Bound by memory: x in, y out; x and dy in, dx out.  Measured: 65536 x 320
-// forward 17.8 us (4.7 TB/s), backward 24 us (5.2); 16381 x 4096 forward 48 us
-// (5.6 TB/s), backward 80 us (5.0); the weights' sums another 4; with 321 and 4099
-// channels 32 and 103 us forward, 89 and 252 for both passes.  A row lies in
+// forward 18 us (4.7 TB/s; 6.7 for each further row), backward 24 us (5.3), 30 with
+// the weights' sums; 16381 x 4096 forward 52 us (5.1 TB/s), backward 70 us (5.8),
+// 82 with the weights' sums; with 321 and 4099 channels 32 and 114 us forward, 91
+// and 266 for both passes.  A row lies in
 // the registers of `lanes` lanes (a power of two up to a warp, or a whole block),
 // up to kWords words of kVec elements each, so it is read once: the mean, the
 // deviations from it and the result come from the same registers.  Lanes take

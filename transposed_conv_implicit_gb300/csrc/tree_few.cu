@@ -19,7 +19,7 @@
 //
 // Measured: one token of 64 requests x 32/8 heads x 128 against up to 4096 keys
 // 94 us, its join with it (4.3 TB/s; 5.4 for each further key); 7 drafts of 32
-// requests against up to 8192 keys 123 us.  (Turned over, with the rows along N,
+// requests against up to 8192 keys 124 us.  (Turned over, with the rows along N,
 // single tokens need half the products and 128 registers, and take 99.7 us: the
 // copies alone take 89 to 95.)
 //
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, kGroups == 1 ? 3 : 2)
 // hold four columns; the shares' slots are listed once per block, before the
 // launch that wrote them has ended, and a row's reads are in flight together.
 // (Found share by share, with 64-bit divisions, the join of 5 requests x 29
-// drafts took 45 us; with a row a warp that of 16 x 64 drafts 25, now 20.)
+// drafts took 45 us; that of 16 x 64 drafts takes 20 under the profiler.)
 constexpr int kTreeJoinWarps = 8, kTreeJoinThreads = 32 * kTreeJoinWarps;
 constexpr int kTreeMaxShares = 1024;  // of an item: two for each CTA at most
 template <typename T, int kPer>
@@ -655,8 +655,8 @@ cudaError_t join_launch(const TreeParams& p, int ctas, cudaStream_t stream) {
 }
 
 cudaError_t launch_tree_join(const TreeParams& p, int dtype, int ctas, cudaStream_t stream) {
-  // Four rows a warp where there are more rows than warps that run at once: 128 items of 256 rows
-  // 25 us with one, 18 with four; 20 items of 87 rows (18 shares each) 5 and 28.
+  // Four rows a warp where there are more rows than warps that run at once: attention of 128 items
+  // of 256 rows takes 178 us with one, 168 with four; of 20 items of 87 rows (18 shares each) 25 and 32.
   const long long rows = static_cast<long long>(p.batch) * p.q_len * p.heads;
   const bool four = rows > 64ll * attn_sm_count();
   if (dtype == CONV_DTYPE_BF16)

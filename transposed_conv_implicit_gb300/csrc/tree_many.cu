@@ -29,8 +29,8 @@
 // SM), as for few rows.  A CTA leaves at most two items' shares: of one that
 // began in front of its part, and of one that ends behind it.
 //
-// Bound by issue slots (58 %: exponentials and widening) beside the products (46
-// % of their pipe): 64 drafts of 16 requests x 32/8 heads x 128 against 8192 keys
+// Bound by the order of exponentials, widening (issue slots 53 %) and products (47
+// % of their pipe), of which neither is full: 64 drafts of 16 requests x 32/8 heads x 128 against 8192 keys
 // 168 us, its join with it (0.81 PFLOP/s; 0.99 for each further key).
 //
 // Numbers, as for few rows, but that scales are common to 16 keys: codes become

@@ -250,9 +250,9 @@ def kv_cache_write(k, v, k_cache, v_cache, scales, block_table, starts, *, lengt
     their exponents into scales; returns (k_cache, v_cache, scales).
 
     starts and lengths: int32 [B]; starts may be None (0), lengths[b] tokens of request b are taken
-    (default: all).  A row's scale is the smallest power of two that brings its largest finite
-    element to 448 or below; codes are rounded to nearest; infinities become the largest code, NaN
-    stays.  Tokens outside the table, or on pages that it gives no number of, are left out.  No two
+    (default: all).  A row's scale is the smallest power of two, 2^-64 at least, that brings its
+    largest finite element to 448 or below (1 for rows of zeros); codes are rounded to nearest;
+    infinities become the largest code, NaN stays.  Tokens outside the table, or on pages that it gives no number of, are left out.  No two
     tokens of a call may go to the same place."""
     _move("kv_cache_write", k, v, k_cache, v_cache, scales, block_table, starts, lengths, stream)
     return k_cache, v_cache, scales
