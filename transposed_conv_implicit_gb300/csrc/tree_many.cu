@@ -30,8 +30,9 @@
 // began in front of its part, and of one that ends behind it.
 //
 // Bound by the order of exponentials, widening (issue slots 53 %) and products (47
-// % of their pipe), of which neither is full: 64 drafts of 16 requests x 32/8 heads x 128 against 8192 keys
-// 168 us, its join with it (0.81 PFLOP/s; 0.99 for each further key).
+// % of their pipe), of which neither is full: 64 drafts of 16 requests x 32/8 heads
+// x 128 against 8192 keys 168 us, its join with it (0.81 PFLOP/s; 0.99 for each
+// further key).
 //
 // Numbers, as for few rows, but that scales are common to 16 keys: codes become
 // fp16 times their row's scale relative to the largest of the slice of 16 that
